@@ -46,6 +46,7 @@ extern "C" {
 #define RNN_ENOSPC 3      /* workspace smaller than rnn_workspace_size() */
 #define RNN_ETIMEOUT 4    /* a device-side wait gave up (reported by rnn_check_status) */
 #define RNN_ECUDA 5       /* a CUDA runtime call or launch failed */
+#define RNN_ERANGE 6      /* a token or slot index out of range (reported by rnn_check_status) */
 
 /* ---- enumerations ---------------------------------------------------------- */
 typedef enum { RNN_LSTM = 0, RNN_GRU = 1, RNN_ELMAN = 2, RNN_SLSTM = 3, RNN_SLSTM_LOGSIG = 4 } rnn_function_t;
@@ -171,7 +172,8 @@ int rnn_bwd_noalloc(const rnn_dims_t *dims, const void *Wx, const void *R, const
 int rnn_bwd_noalloc_status(void *stream);
 
 /* Synchronises `stream`, reads and clears the device status word that kernels
- * running on `workspace` recorded. Returns RNN_OK, RNN_ETIMEOUT or RNN_ECUDA.
+ * running on `workspace` recorded. Returns RNN_OK, RNN_ETIMEOUT, RNN_ERANGE or
+ * RNN_ECUDA.
  * (The pages have no device-side error path; the status-code convention --
  * validation errors returned before any work, the empty-batch error, T = 0 as
  * a copy of the initial state -- follows the precedent of ruDNN 0.2.1,
@@ -307,6 +309,112 @@ int rnn_input_proj_fwd(int BT, int I, int C, const void *x, const void *W, const
  * NULL when not wanted. Same conventions and errors as the forward. */
 int rnn_input_proj_bwd(int BT, int I, int C, const void *x, const void *W, const void *dWx, void *dx, void *dW,
                        void *dbias, void *workspace, size_t ws_bytes, void *stream);
+
+/* ---- gated linear scan -------------------------------------------------------- */
+/*
+ * The scan without R: the gates come from Wx and b alone, so the recurrence is
+ * linear in the carried state c and the time axis can be split over the GPU.
+ * (The pages name only the recurrences with R; layout, gate positions and
+ * conventions are those of the scan above.) With a = Wx + b per step:
+ *   RNN_LINEAR (G = 4, gates i, f, g, o):  c_t = s(a_f) c_{t-1} + s(a_i) a_g,
+ *                                          h_t = s(a_o) c_t
+ *   RNN_LINEAR_COUPLED (G = 2, gates f, g): h_t = c_t = s(a_f) c_{t-1} + (1 - s(a_f)) a_g
+ * (s = sigmoid). reset[b,t] != 0 takes c_{t-1} as zero at step t (the start of
+ * another document). Steps t >= lengths[b] do not exist: their inputs are not
+ * looked at (they may hold anything), h is 0 there, the state is kept, their
+ * gradients are 0. lengths outside 0 .. T count as 0 or T.
+ * The carried state is fp32 for either dtype.
+ */
+typedef enum { RNN_LINEAR = 0, RNN_LINEAR_COUPLED = 1 } rnn_gated_function_t;
+/* What a training forward keeps for the backward beside Wx: with
+ * RNN_CKPT_NONE the carried state before every RNN_GATED_CHUNK-th step; with
+ * RNN_CKPT_INT8 also Wx in 8 bits (the format of rnn_act_pack, a block being
+ * RNN_ACT_BLOCK steps of one channel and gate; steps past a length count as
+ * zeros), so that the caller may drop Wx. The gradient is then taken at the
+ * 8-bit values, from the exact states at the chunks' starts. */
+typedef enum { RNN_CKPT_NONE = 0, RNN_CKPT_INT8 = 1 } rnn_checkpoint_t;
+#define RNN_GATED_CHUNK 128
+#define RNN_ACT_BLOCK 32
+
+typedef struct {
+  int B, T, N, D;
+  int function;   /* rnn_gated_function_t */
+  int dtype;      /* rnn_dtype_t, of Wx, b, h, dh, dWx, db */
+  int checkpoint; /* rnn_checkpoint_t */
+} rnn_gated_dims_t;
+
+int rnn_gated_num_gates(int function); /* G, or -1 for an unknown function */
+/* Bytes of the tape / of the workspace (kind: RNN_WS_FWD or RNN_WS_BWD); 0 for
+ * invalid dims. */
+size_t rnn_gated_tape_size(const rnn_gated_dims_t *dims);
+size_t rnn_gated_workspace_size(const rnn_gated_dims_t *dims, int kind);
+
+/* Forward.
+ *   Wx      [B,T,G,N,D]                                                 (in)
+ *   b       [G,N,D], or NULL = zeros                                     (in)
+ *   state0  [B,1,N,D] fp32, or NULL = zeros                              (in)
+ *   reset   [B,T] bytes, or NULL = none                                  (in)
+ *   lengths [B] int32, or NULL = all T                                   (in)
+ *   h       [B,T,N,D]                                                   (out)
+ *   last    [B,1,N,D] fp32, the state after the last step, or NULL       (out)
+ *   tape    rnn_gated_tape_size() bytes, or NULL (no backward to come)   (out)
+ * Errors: RNN_EINVAL, RNN_ENOSPC, RNN_ECUDA; RNN_ETIMEOUT by rnn_check_status. */
+int rnn_gated_fwd(const rnn_gated_dims_t *dims, const void *Wx, const void *b, const void *state0,
+                  const unsigned char *reset, const int *lengths, void *h, void *last, void *tape,
+                  void *workspace, size_t ws_bytes, void *stream);
+
+/* Backward: the gradient of sum(h*dh) + sum(last*dlast).
+ *   Wx may be NULL with RNN_CKPT_INT8; b, reset, lengths and tape as in / from
+ *   the forward; dh [B,T,N,D] and dlast [B,1,N,D] fp32 may be NULL (zero);
+ *   outputs dWx [B,T,G,N,D], db [G,N,D], dstate0 [B,1,N,D] fp32, each may be
+ *   NULL. Sums over time and batch run in a fixed order.
+ * Errors: as rnn_gated_fwd. */
+int rnn_gated_bwd(const rnn_gated_dims_t *dims, const void *Wx, const void *b, const unsigned char *reset,
+                  const int *lengths, const void *tape, const void *dh, const void *dlast, void *dWx, void *db,
+                  void *dstate0, void *workspace, size_t ws_bytes, void *stream);
+
+/* One step of `rows` sequences whose states live in a pool (serving).
+ *   Wx [rows,G,N,D], b [G,N,D] or NULL, h [rows,N,D]
+ *   slot [rows] int32: the row's place in the pool, or NULL = the row's number
+ *     (rows <= slots). A negative slot marks an unused row: h = 0, no state is
+ *     touched. No slot may appear twice. A slot >= slots counts as unused and
+ *     sets RNN_ERANGE in `status`.
+ *   pool [slots,N,D] fp32: read; pool_out: the new states are written here (pool
+ *     itself, or another pool that keeps the old states valid)
+ *   status: a device word (4-byte aligned) that rnn_check_status reads, not
+ *     cleared by this call, or NULL
+ * Errors: RNN_EINVAL, RNN_ECUDA. */
+int rnn_gated_step(int rows, int slots, int N, int D, int function, int dtype, const void *Wx, const void *b,
+                   const int *slot, const void *pool, void *pool_out, void *h, void *status, void *stream);
+
+/* ---- 8-bit activation checkpoints ----------------------------------------------- */
+/* Packs x [rows][cols] (dtype) into int8 q [rows][cols] and one scale byte per
+ * RNN_ACT_BLOCK rows of a column, scales [ceil(rows/32)][cols]
+ * (rnn_act_scale_bytes). The scale is 2^e (byte e + 127) with the smallest
+ * e >= -126 for which 127 * 2^e holds the block's largest magnitude; q is
+ * x / 2^e rounded to nearest even. e is at most 121: magnitudes past 127 * 2^121
+ * (3.38e38) saturate there instead of unpacking to an infinity. A block with an infinity or a NaN gets the
+ * byte 255 and unpacks to NaN. Unpacking gives q * 2^e, exact in bf16 too.
+ * Errors: RNN_EINVAL, RNN_ECUDA. */
+size_t rnn_act_scale_bytes(long long rows, int cols);
+int rnn_act_pack(long long rows, int cols, int dtype, const void *x, void *q, void *scales, void *stream);
+int rnn_act_unpack(long long rows, int cols, int dtype, const void *q, const void *scales, void *x, void *stream);
+
+/* ---- token embedding --------------------------------------------------------------- */
+/* out[i] = scale * W[ids[i]] for n < 2^31 tokens; W [V][E], out [n][E], ids int32
+ * (id_bytes 4) or int64 (8). A token outside 0 .. V-1 gives a zero row and sets
+ * RNN_ERANGE in `status` (a device word that rnn_check_status reads, not
+ * cleared by this call, or NULL).
+ * The backward writes the whole of dW [V][E]: scale * the sum of dout's rows
+ * over each id's tokens, fp32 sums in a fixed order (of the token order), zero
+ * rows for ids without tokens and for padding_idx (-1: none). Tokens out of
+ * range are left out and set RNN_ERANGE in the workspace's status word.
+ * Errors: RNN_EINVAL, RNN_ENOSPC, RNN_ECUDA. */
+size_t rnn_embed_bwd_workspace_size(long long n, int V, int E); /* 0 for invalid sizes */
+int rnn_embed_fwd(long long n, int V, int E, int dtype, int id_bytes, const void *ids, const void *W, float scale,
+                  void *out, void *status, void *stream);
+int rnn_embed_bwd(long long n, int V, int E, int dtype, int id_bytes, const void *ids, long long padding_idx,
+                  const void *dout, float scale, void *dW, void *workspace, size_t ws_bytes, void *stream);
 
 /* Latency floor of the cluster exchange (a measurement aid). Runs a kernel
  * whose steps hold only the h exchange of the forward cluster kernel: every

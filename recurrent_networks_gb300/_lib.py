@@ -12,16 +12,22 @@ import torch
 
 from . import build as _build
 
-RNN_OK, RNN_EINVAL, RNN_EUNSUPPORTED, RNN_ENOSPC, RNN_ETIMEOUT, RNN_ECUDA = range(6)
+RNN_OK, RNN_EINVAL, RNN_EUNSUPPORTED, RNN_ENOSPC, RNN_ETIMEOUT, RNN_ECUDA, RNN_ERANGE = range(7)
 FUNCTIONS = {"lstm": 0, "gru": 1, "elman": 2, "slstm": 3, "slstm_logsig": 4}
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 PATHS = {"auto": 0, "fused": 1, "alternating": 2, "simt": 3, "grid": 4}
 WS_FWD, WS_BWD, WS_BWD_RECOMPUTE = 0, 1, 2
+GATED_FUNCTIONS = {"linear": 0, "linear_coupled": 1}
+CHECKPOINTS = {None: 0, "int8": 1}
+ACT_BLOCK = 32  # rows that share a scale in an 8-bit checkpoint
 
 EXPORTS = ["rnn_num_gates", "rnn_num_states", "rnn_tape_size", "rnn_workspace_size", "rnn_fwd",
            "rnn_bwd", "rnn_check_status", "rnn_plan_describe", "rnn_strerror", "rnn_kernel_launches",
            "rnn_profile_events", "rnn_bwd_noalloc", "rnn_bwd_noalloc_status", "rnn_trace",
-           "rnn_debug_inject_wait", "rnn_plan_set_limits", "rnn_die_layout", "rnn_die_plan_for"]
+           "rnn_debug_inject_wait", "rnn_plan_set_limits", "rnn_die_layout", "rnn_die_plan_for",
+           "rnn_gated_num_gates", "rnn_gated_tape_size", "rnn_gated_workspace_size", "rnn_gated_fwd",
+           "rnn_gated_bwd", "rnn_gated_step", "rnn_act_scale_bytes", "rnn_act_pack", "rnn_act_unpack",
+           "rnn_embed_bwd_workspace_size", "rnn_embed_fwd", "rnn_embed_bwd"]
 
 
 class RnnError(RuntimeError):
@@ -33,6 +39,11 @@ class RnnError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("N", ctypes.c_int), ("D", ctypes.c_int),
                 ("function", ctypes.c_int), ("dtype", ctypes.c_int), ("path", ctypes.c_int)]
+
+
+class GatedDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("N", ctypes.c_int), ("D", ctypes.c_int),
+                ("function", ctypes.c_int), ("dtype", ctypes.c_int), ("checkpoint", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -76,6 +87,23 @@ def load(path: str | None = None):
             lib.rnn_input_proj_workspace_size.restype = sz
             lib.rnn_input_proj_fwd.argtypes = [i, i, i] + [vp] * 5 + [sz, vp]
             lib.rnn_input_proj_bwd.argtypes = [i, i, i] + [vp] * 7 + [sz, vp]
+            gp, ll, f = ctypes.POINTER(GatedDims), ctypes.c_longlong, ctypes.c_float
+            lib.rnn_gated_num_gates.argtypes = [i]
+            lib.rnn_gated_tape_size.argtypes = [gp]
+            lib.rnn_gated_tape_size.restype = sz
+            lib.rnn_gated_workspace_size.argtypes = [gp, i]
+            lib.rnn_gated_workspace_size.restype = sz
+            lib.rnn_gated_fwd.argtypes = [gp] + [vp] * 9 + [sz, vp]
+            lib.rnn_gated_bwd.argtypes = [gp] + [vp] * 11 + [sz, vp]
+            lib.rnn_gated_step.argtypes = [i] * 6 + [vp] * 8
+            lib.rnn_act_scale_bytes.argtypes = [ll, i]
+            lib.rnn_act_scale_bytes.restype = sz
+            lib.rnn_act_pack.argtypes = [ll, i, i] + [vp] * 4
+            lib.rnn_act_unpack.argtypes = [ll, i, i] + [vp] * 4
+            lib.rnn_embed_bwd_workspace_size.argtypes = [ll, i, i]
+            lib.rnn_embed_bwd_workspace_size.restype = sz
+            lib.rnn_embed_fwd.argtypes = [ll, i, i, i, i, vp, vp, f, vp, vp, vp]
+            lib.rnn_embed_bwd.argtypes = [ll, i, i, i, i, vp, ll, vp, f, vp, vp, sz, vp]
             _lib = lib
     return _lib
 
@@ -261,3 +289,79 @@ def rnn_input_proj_bwd(BT: int, I: int, C: int, x, W, dWx, dx, dW, dbias, worksp
     rc = load().rnn_input_proj_bwd(int(BT), int(I), int(C), _p(x), _p(W), _p(dWx), _p(dx), _p(dW), _p(dbias),
                                    _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     return _check(rc, "rnn_input_proj_bwd")
+
+
+# ---- gated linear scan ------------------------------------------------------------
+def make_gated_dims(B, T, N, D, function="linear", dtype=torch.bfloat16, checkpoint=None) -> GatedDims:
+    fn = GATED_FUNCTIONS[function] if isinstance(function, str) else int(function)
+    dt = DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    ck = checkpoint if isinstance(checkpoint, int) else CHECKPOINTS[checkpoint]
+    return GatedDims(int(B), int(T), int(N), int(D), fn, dt, ck)
+
+
+def rnn_gated_num_gates(function) -> int:
+    return load().rnn_gated_num_gates(GATED_FUNCTIONS.get(function, -1) if isinstance(function, str) else function)
+
+
+def rnn_gated_tape_size(dims: GatedDims) -> int:
+    return load().rnn_gated_tape_size(ctypes.byref(dims))
+
+
+def rnn_gated_workspace_size(dims: GatedDims, kind: int = WS_FWD) -> int:
+    return load().rnn_gated_workspace_size(ctypes.byref(dims), kind)
+
+
+def rnn_gated_fwd(dims: GatedDims, Wx, b, state0, reset, lengths, h, last, tape, workspace, stream=None) -> int:
+    rc = load().rnn_gated_fwd(ctypes.byref(dims), _p(Wx), _p(b), _p(state0), _p(reset), _p(lengths), _p(h), _p(last),
+                              _p(tape), _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    return _check(rc, "rnn_gated_fwd")
+
+
+def rnn_gated_bwd(dims: GatedDims, Wx, b, reset, lengths, tape, dh, dlast, dWx, db, dstate0, workspace,
+                  stream=None) -> int:
+    rc = load().rnn_gated_bwd(ctypes.byref(dims), _p(Wx), _p(b), _p(reset), _p(lengths), _p(tape), _p(dh), _p(dlast),
+                              _p(dWx), _p(db), _p(dstate0), _p(workspace),
+                              workspace.numel() * workspace.element_size(), _stream(stream))
+    return _check(rc, "rnn_gated_bwd")
+
+
+def rnn_gated_step(rows, slots, N, D, function, dtype, Wx, b, slot, pool, pool_out, h, status=None, stream=None) -> int:
+    fn = GATED_FUNCTIONS[function] if isinstance(function, str) else int(function)
+    rc = load().rnn_gated_step(int(rows), int(slots), int(N), int(D), fn, DTYPES[dtype], _p(Wx), _p(b), _p(slot),
+                               _p(pool), _p(pool_out), _p(h), _p(status), _stream(stream))
+    return _check(rc, "rnn_gated_step")
+
+
+# ---- 8-bit activation checkpoints ------------------------------------------------------
+def rnn_act_scale_bytes(rows: int, cols: int) -> int:
+    return int(load().rnn_act_scale_bytes(int(rows), int(cols)))
+
+
+def rnn_act_pack(rows: int, cols: int, x, q, scales, stream=None) -> int:
+    return _check(load().rnn_act_pack(int(rows), int(cols), DTYPES[x.dtype], _p(x), _p(q), _p(scales),
+                                      _stream(stream)), "rnn_act_pack")
+
+
+def rnn_act_unpack(rows: int, cols: int, q, scales, x, stream=None) -> int:
+    return _check(load().rnn_act_unpack(int(rows), int(cols), DTYPES[x.dtype], _p(q), _p(scales), _p(x),
+                                        _stream(stream)), "rnn_act_unpack")
+
+
+# ---- token embedding -----------------------------------------------------------------------
+def rnn_embed_bwd_workspace_size(n: int, V: int, E: int) -> int:
+    return int(load().rnn_embed_bwd_workspace_size(int(n), int(V), int(E)))
+
+
+def rnn_embed_fwd(n: int, V: int, E: int, ids, W, scale: float, out, status=None, stream=None) -> int:
+    rc = load().rnn_embed_fwd(int(n), int(V), int(E), DTYPES[W.dtype], ids.element_size(), _p(ids), _p(W),
+                              float(scale), _p(out), _p(status), _stream(stream))
+    return _check(rc, "rnn_embed_fwd")
+
+
+def rnn_embed_bwd(n: int, V: int, E: int, ids, padding_idx: int, dout, scale: float, dW, workspace,
+                  stream=None) -> int:
+    """dW [V][E] from dout [n][E] (see include/rnn.h); padding_idx -1 = none."""
+    rc = load().rnn_embed_bwd(int(n), int(V), int(E), DTYPES[dW.dtype], ids.element_size(), _p(ids), int(padding_idx),
+                              _p(dout), float(scale), _p(dW), _p(workspace),
+                              workspace.numel() * workspace.element_size(), _stream(stream))
+    return _check(rc, "rnn_embed_bwd")

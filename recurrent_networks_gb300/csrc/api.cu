@@ -631,7 +631,7 @@ int rnn_check_status(void* workspace, void* stream) {
     e = cudaMemsetAsync(workspace, 0, sizeof(h), st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_status(e);
-    return RNN_ETIMEOUT;
+    return (h & STATUS_TIMEOUT) ? RNN_ETIMEOUT : RNN_ERANGE;
   }
   return RNN_OK;
 }
@@ -725,6 +725,7 @@ const char* rnn_strerror(int status) {
     case RNN_ENOSPC: return "workspace too small";
     case RNN_ETIMEOUT: return "a device-side wait timed out";
     case RNN_ECUDA: return "CUDA runtime error";
+    case RNN_ERANGE: return "a token or slot index is out of range";
   }
   return "unknown status";
 }

@@ -8,6 +8,7 @@ the backward through time run in librnn_gb300.so's kernels via the C ABI.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -77,7 +78,7 @@ def flashrnn(Wx, R, b, states=None, function: str = "lstm", backend: str = "auto
 
 class _ProjFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, W, bias):
+    def forward(ctx, x, W, bias, checkpoint=None):
         BT, I = x.shape
         C = W.shape[0]
         x, W = x.contiguous(), W.contiguous()
@@ -86,12 +87,22 @@ class _ProjFn(torch.autograd.Function):
         ws = torch.empty(_lib.rnn_input_proj_workspace_size(BT, I, C), dtype=torch.uint8, device=x.device)
         _lib.rnn_input_proj_fwd(BT, I, C, x, W, bias, Wx, ws)
         ctx.has_bias = bias is not None
-        ctx.save_for_backward(x, W)
+        ctx.packed = checkpoint == "int8"
+        if ctx.packed:  # x is needed for dW alone
+            ctx.save_for_backward(W, *(_pack(x) if ctx.needs_input_grad[1] else ()))
+        else:
+            ctx.save_for_backward(x, W)
         return Wx
 
     @staticmethod
     def backward(ctx, dWx):
-        x, W = ctx.saved_tensors
+        if ctx.packed:
+            W, *kept = ctx.saved_tensors
+            x = torch.empty((dWx.shape[0], W.shape[1]), dtype=W.dtype, device=W.device)
+            if kept:
+                _lib.rnn_act_unpack(x.shape[0], x.shape[1], kept[0], kept[1], x)
+        else:
+            x, W = ctx.saved_tensors
         BT, I = x.shape
         C = W.shape[0]
         dWx = dWx.contiguous()
@@ -100,16 +111,21 @@ class _ProjFn(torch.autograd.Function):
         db = torch.empty((C,), dtype=x.dtype, device=x.device) if (ctx.has_bias and ctx.needs_input_grad[2]) else None
         ws = torch.empty(_lib.rnn_input_proj_workspace_size(BT, I, C), dtype=torch.uint8, device=x.device)
         _lib.rnn_input_proj_bwd(BT, I, C, x, W, dWx, dx, dW, db, ws)
-        return dx, dW, db
+        return dx, dW, db, None
 
 
-def input_projection(x, W, bias=None):
+def input_projection(x, W, bias=None, checkpoint=None):
     """Wx = x W^T (+ bias) on the tensor cores: x [..., I], W [C, I] (the
-    weight_ih layout), bias [C] or None; returns [..., C]. bf16, CUDA only."""
+    weight_ih layout), bias [C] or None; returns [..., C]. bf16, CUDA only.
+    checkpoint="int8" keeps x for the backward in 8 bits (checkpoint_pack over
+    the flattened rows) instead of x itself: dW is then taken at the unpacked
+    values; the result, dx and dbias are unchanged."""
     if not x.is_cuda:
         raise RuntimeError("input_projection runs on CUDA tensors only (there is no CPU path)")
+    if checkpoint not in _lib.CHECKPOINTS:
+        raise ValueError(f"checkpoint must be one of {list(_lib.CHECKPOINTS)}, got {checkpoint!r}")
     lead = x.shape[:-1]
-    y = _ProjFn.apply(x.reshape(-1, x.shape[-1]), W, bias)
+    y = _ProjFn.apply(x.reshape(-1, x.shape[-1]), W, bias, checkpoint)
     return y.reshape(*lead, W.shape[0])
 
 
@@ -132,3 +148,217 @@ def flashrnn_stack(x, layers, function: str = "lstm", backend: str = "auto"):
         outs.append((states, last))
         h = states[0].reshape(B, T, N * D)
     return h, outs
+
+
+# ---- gated linear scan ------------------------------------------------------------
+def _need(ok, text, kind=ValueError):
+    if not ok:
+        raise kind(text)
+
+
+def _dense(t):
+    """t (or None) as the library takes it: contiguous and 16-byte aligned."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+class _GatedFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, Wx, b, state, function, reset, lengths, checkpoint):
+        B, T, _, N, D = Wx.shape
+        Wx, b, state = _dense(Wx), _dense(b), _dense(state)
+        dims = _lib.make_gated_dims(B, T, N, D, function, Wx.dtype, checkpoint)
+        h = torch.empty((B, T, N, D), dtype=Wx.dtype, device=Wx.device)
+        last = torch.empty((B, 1, N, D), dtype=torch.float32, device=Wx.device)
+        tape = None
+        if any(ctx.needs_input_grad[:3]):
+            tape = torch.empty(_lib.rnn_gated_tape_size(dims), dtype=torch.uint8, device=Wx.device)
+        ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_FWD), dtype=torch.uint8, device=Wx.device)
+        _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, ws)
+        ctx.dims, ctx.wx_shape = dims, Wx.shape
+        ctx.has_state = state is not None
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(Wx if checkpoint is None else None, b, reset, lengths, tape)
+        return h, last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh, dlast):
+        Wx, b, reset, lengths, tape = ctx.saved_tensors
+        dims, dev = ctx.dims, tape.device
+        dt = torch.bfloat16 if dims.dtype == _lib.DTYPES[torch.bfloat16] else torch.float32
+        B, _, G, N, D = ctx.wx_shape
+        need = ctx.needs_input_grad
+        dWx = torch.empty(ctx.wx_shape, dtype=dt, device=dev) if need[0] else None
+        db = torch.empty((G, N, D), dtype=dt, device=dev) if b is not None and need[1] else None
+        ds = torch.empty((B, 1, N, D), dtype=torch.float32, device=dev) if ctx.has_state and need[2] else None
+        ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_BWD), dtype=torch.uint8, device=dev)
+        _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, ws)
+        return dWx, db, ds, None, None, None, None
+
+
+def _gated_shapes(Wx, b, function, lead):
+    _need(function in _lib.GATED_FUNCTIONS, f"function must be one of {list(_lib.GATED_FUNCTIONS)}, got {function!r}")
+    _need(Wx.dtype in _lib.DTYPES, f"unsupported dtype {Wx.dtype}", TypeError)
+    _need(Wx.dim() == lead + 3, f"Wx must have {lead + 3} dimensions, got shape {tuple(Wx.shape)}")
+    G, N, D = Wx.shape[lead:]
+    want = 4 if function == "linear" else 2
+    _need(G == want, f"{function} needs G={want} gates, Wx has {G}")
+    if b is not None:
+        _need(tuple(b.shape) == (G, N, D), f"b must be [G,N,D]={(G, N, D)}, got {tuple(b.shape)}")
+        _need(b.dtype == Wx.dtype, f"b is {b.dtype}, Wx is {Wx.dtype}", TypeError)
+        _need(b.device == Wx.device, "b must be on Wx's device")
+    return N, D
+
+
+def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, lengths=None, checkpoint=None):
+    """Gated linear scan: the recurrence without R, linear in its state.
+
+    Wx [B,T,G,N,D] (bf16 or fp32), b [G,N,D] or None, state [B,1,N,D] or None
+    (zeros). function "linear" (gates i, f, g, o): c_t = s(f) c_{t-1} + s(i) g,
+    h_t = s(o) c_t; "linear_coupled" (gates f, g): h_t = c_t = s(f) c_{t-1} +
+    (1 - s(f)) g, s the sigmoid of the biased pre-activation. reset [B,T] (bool
+    or uint8): c_{t-1} counts as zero at the marked steps (packed documents).
+    lengths [B]: row b has lengths[b] steps; past them h is zero and the state
+    is kept. Returns (h [B,T,N,D], last [B,1,N,D]: the state after the last
+    step, fp32). Differentiable in Wx, b and state; the backward recomputes the
+    states from those kept every 128 steps. checkpoint="int8" keeps Wx for the
+    backward in 8 bits (a power-of-two scale per 32 steps of a channel and
+    gate) instead of Wx itself; the gradient is then taken at those values."""
+    if not Wx.is_cuda:
+        raise RuntimeError("gated_scan runs on CUDA tensors only (there is no CPU path)")
+    N, D = _gated_shapes(Wx, b, function, 2)
+    B, T = Wx.shape[:2]
+    _need(checkpoint in _lib.CHECKPOINTS, f"checkpoint must be one of {list(_lib.CHECKPOINTS)}, got {checkpoint!r}")
+    if state is not None:
+        _need(tuple(state.shape) == (B, 1, N, D), f"state must be [B,1,N,D]={(B, 1, N, D)}, got {tuple(state.shape)}")
+        _need(state.device == Wx.device, "state must be on Wx's device")
+        state = state.float()
+    if reset is not None:
+        _need(tuple(reset.shape) == (B, T), f"reset must be [B,T]={(B, T)}, got {tuple(reset.shape)}")
+        _need(reset.dtype in (torch.bool, torch.uint8), f"reset must be bool or uint8, got {reset.dtype}", TypeError)
+        _need(reset.device == Wx.device, "reset must be on Wx's device")
+        reset = reset.contiguous()
+    if lengths is not None:
+        _need(tuple(lengths.shape) == (B,), f"lengths must be [B]={(B,)}, got {tuple(lengths.shape)}")
+        _need(lengths.dtype in (torch.int32, torch.int64), f"lengths must be integers, got {lengths.dtype}", TypeError)
+        _need(lengths.device == Wx.device, "lengths must be on Wx's device")
+        lengths = lengths.clamp(0, T).to(torch.int32).contiguous() if lengths.dtype == torch.int64 else lengths.contiguous()
+    if not torch.is_grad_enabled():  # nothing is kept for a backward
+        Wx, b, state = (v if v is None else v.detach() for v in (Wx, b, state))
+    return _GatedFn.apply(Wx, b, state, function, reset, lengths, checkpoint)
+
+
+def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=None, status=None):
+    """One step of running sequences whose states live in a pool (serving; not
+    differentiable). Wx [M,G,N,D], b [G,N,D] or None, pool [P,N,D] fp32, slots
+    [M] int32: each row's place in the pool, or None for the row's number; no
+    slot twice; a negative slot marks an unused row (h = 0, no state touched).
+    The new states go to pool_out, by default the pool itself. Returns h
+    [M,N,D]. status: an int32 CUDA tensor of one element, zeroed by the caller,
+    in which a slot past the pool is recorded (such a row counts as unused);
+    _lib.rnn_check_status(status) raises for it."""
+    if not Wx.is_cuda:
+        raise RuntimeError("gated_scan_step runs on CUDA tensors only (there is no CPU path)")
+    N, D = _gated_shapes(Wx, b, function, 1)
+    M = Wx.shape[0]
+    pool_out = pool if pool_out is None else pool_out
+    for p in (pool, pool_out):
+        _need(p.dtype == torch.float32, f"the pool must be float32, got {p.dtype}", TypeError)
+        _need(p.dim() == 3 and tuple(p.shape[1:]) == (N, D) and p.shape == pool.shape,
+              f"the pool must be [P,N,D]=[P,{N},{D}], got {tuple(p.shape)}")
+        _need(p.is_contiguous() and p.data_ptr() % 16 == 0 and p.device == Wx.device,
+              "the pool must be contiguous, 16-byte aligned and on Wx's device")
+    if slots is None:
+        _need(M <= pool.shape[0], f"{M} rows need as many slots, the pool has {pool.shape[0]}")
+    else:
+        _need(tuple(slots.shape) == (M,) and slots.dtype == torch.int32 and slots.device == Wx.device,
+              f"slots must be [M]=[{M}] int32 on Wx's device")
+        slots = slots.contiguous()
+    h = torch.empty((M, N, D), dtype=Wx.dtype, device=Wx.device)
+    _lib.rnn_gated_step(M, pool.shape[0], N, D, function, Wx.dtype, _dense(Wx), _dense(b), slots, pool, pool_out, h,
+                        status)
+    return h
+
+
+# ---- 8-bit activation checkpoints -----------------------------------------------------
+def _pack(x):
+    rows, cols = x.shape
+    q = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    scales = torch.empty((-(-rows // _lib.ACT_BLOCK), cols), dtype=torch.uint8, device=x.device)
+    _lib.rnn_act_pack(rows, cols, x, q, scales)
+    return q, scales
+
+
+def checkpoint_pack(x):
+    """x [..., cols] (bf16 or fp32) in 8 bits: q (int8, x's shape) and scales
+    (uint8, [ceil(rows / 32), cols], rows being the flattened leading axes): one
+    power of two per 32 rows of a column, the smallest whose 127-fold holds the
+    block's largest magnitude. Blocks with an infinity or a NaN unpack to NaN."""
+    if not x.is_cuda:
+        raise RuntimeError("checkpoint_pack runs on CUDA tensors only (there is no CPU path)")
+    _need(x.dtype in _lib.DTYPES, f"unsupported dtype {x.dtype}", TypeError)
+    _need(x.dim() >= 1 and x.shape[-1] >= 1, f"x must have a last axis, got shape {tuple(x.shape)}")
+    q, scales = _pack(_dense(x.detach().reshape(-1, x.shape[-1])))
+    return q.reshape(x.shape), scales
+
+
+def checkpoint_unpack(q, scales, dtype=torch.bfloat16):
+    """The values (exact in either dtype) that checkpoint_pack's q and scales stand for."""
+    if not q.is_cuda:
+        raise RuntimeError("checkpoint_unpack runs on CUDA tensors only (there is no CPU path)")
+    _need(dtype in _lib.DTYPES, f"unsupported dtype {dtype}", TypeError)
+    _need(q.dtype == torch.int8 and scales.dtype == torch.uint8, "q must be int8 and scales uint8", TypeError)
+    _need(q.dim() >= 1 and q.shape[-1] >= 1, f"q must have a last axis, got shape {tuple(q.shape)}")
+    cols = q.shape[-1]
+    rows = q.numel() // cols
+    _need(tuple(scales.shape) == (-(-rows // _lib.ACT_BLOCK), cols) and scales.device == q.device,
+          f"scales must be [{-(-rows // _lib.ACT_BLOCK)},{cols}] on q's device, got {tuple(scales.shape)}")
+    x = torch.empty(q.shape, dtype=dtype, device=q.device)
+    _lib.rnn_act_unpack(rows, cols, _dense(q), _dense(scales), x)
+    return x
+
+
+# ---- token embedding --------------------------------------------------------------------
+class _EmbedFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, W, scale, padding_idx, status):
+        W = _dense(W)
+        out = torch.empty((ids.numel(), W.shape[1]), dtype=W.dtype, device=W.device)
+        _lib.rnn_embed_fwd(ids.numel(), W.shape[0], W.shape[1], ids, W, scale, out, status)
+        ctx.save_for_backward(ids)
+        ctx.args = (W.shape, W.dtype, scale, padding_idx)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        (ids,) = ctx.saved_tensors
+        (V, E), dtype, scale, pad = ctx.args
+        n = ids.numel()
+        dW = torch.empty((V, E), dtype=dtype, device=ids.device)
+        ws = torch.empty(_lib.rnn_embed_bwd_workspace_size(n, V, E), dtype=torch.uint8, device=ids.device)
+        _lib.rnn_embed_bwd(n, V, E, ids, pad, _dense(dout), scale, dW, ws)
+        return None, dW, None, None, None
+
+
+def embedding(ids, weight, scale: float = 1.0, padding_idx=None, status=None):
+    """scale * weight[ids]: ids [...] int32 or int64, weight [V, E] (bf16 or
+    fp32); returns [..., E]. Differentiable in weight: the gradient is dense
+    [V, E], each row the scaled fp32 sum over its tokens in a fixed order,
+    zero for padding_idx. Ids out of range give zero rows and no gradient;
+    status: an int32 CUDA tensor of one element, zeroed by the caller, in which
+    they are recorded (_lib.rnn_check_status(status) raises for it)."""
+    if not weight.is_cuda:
+        raise RuntimeError("embedding runs on CUDA tensors only (there is no CPU path)")
+    _need(weight.dim() == 2, f"weight must be [V,E], got shape {tuple(weight.shape)}")
+    _need(weight.dtype in _lib.DTYPES, f"unsupported dtype {weight.dtype}", TypeError)
+    _need(ids.dtype in (torch.int32, torch.int64), f"ids must be int32 or int64, got {ids.dtype}", TypeError)
+    _need(ids.device == weight.device, "ids must be on weight's device")
+    _need(padding_idx is None or 0 <= padding_idx < weight.shape[0],
+          f"padding_idx must be None or in 0 .. {weight.shape[0] - 1}, got {padding_idx}")
+    pad = -1 if padding_idx is None else int(padding_idx)
+    out = _EmbedFn.apply(ids.reshape(-1).contiguous(), weight, float(scale), pad, status)
+    return out.reshape(*ids.shape, weight.shape[1])

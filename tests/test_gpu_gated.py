@@ -1,0 +1,298 @@
+"""GPU parity of the gated linear scan (forward, backward, single-token step,
+8-bit checkpoint) with its fp64 oracle, and its refusals.
+
+Tolerances. bf16: every output is rounded once (2^-9 relative per element);
+the fp32 arithmetic inside is at most 2^-22 a step relative, over at most a
+few hundred steps, so L2-normwise 5e-3 and normwise-max 1e-2 as for the other
+bf16 outputs. fp32: a step's f carries a relative error of at most about
+2^-22 (exponential, sum, division, product), products of up to T of them
+T 2^-22: normwise-max 1e-6 + T 2^-22. The carried state and the gradient of
+the initial state are fp32 for either dtype; with bf16 inputs the faster
+exponential and reciprocal (2^-21 together) take the place: 1e-6 + T 2^-20."""
+import numpy as np
+import pytest
+import torch
+
+import recurrent_networks_gb300 as rn
+from oracle import gated
+from recurrent_networks_gb300 import _lib
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def close(got, ref, what, T, fp32, fast=False):
+    got = got.detach().double().cpu().numpy()
+    ref = np.asarray(ref, dtype=np.float64)
+    assert got.shape == ref.shape, what
+    assert np.isfinite(got).all(), what
+    top = max(np.abs(ref).max(), 1e-30)
+    worst = np.abs(got - ref).max() / top
+    if fp32:
+        tol = 1e-6 + T * 2.0 ** (-20 if fast else -22)
+        assert worst <= tol, f"{what}: max {worst:.3g} > {tol:.3g}"
+    else:
+        l2 = np.linalg.norm(got - ref) / max(np.linalg.norm(ref), 1e-30)
+        assert l2 <= 5e-3 and worst <= 1e-2, f"{what}: L2 {l2:.3g}, max {worst:.3g}"
+
+
+def make(function, B, T, N, D, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed + 7 * T + D)
+    G = 4 if function == "linear" else 2
+    Wx = torch.randn(B, T, G, N, D, generator=g).to(dtype).cuda()
+    b = torch.randn(G, N, D, generator=g)
+    b[G // 2 - 1] += 3  # the forget gate: long memories
+    return dict(Wx=Wx, b=b.to(dtype).cuda(), state=torch.randn(B, 1, N, D, generator=g).cuda(),
+                dh=torch.randn(B, T, N, D, generator=g).to(dtype).cuda(),
+                dlast=torch.randn(B, 1, N, D, generator=g).cuda())
+
+
+def run(p, function, reset=None, lengths=None, checkpoint=None, grads=True):
+    leaves = [p[k].clone().requires_grad_(grads) for k in ("Wx", "b", "state")]
+    h, last = rn.gated_scan(*leaves, function=function, reset=reset, lengths=lengths, checkpoint=checkpoint)
+    if not grads:
+        return h, last
+    return (h, last) + torch.autograd.grad((h, last), leaves, (p["dh"], p["dlast"]))
+
+
+def check(p, function, reset=None, lengths=None, checkpoint=None):
+    dtype, T = p["Wx"].dtype, p["Wx"].shape[1]
+    got = run(p, function, reset, lengths, checkpoint)
+    h, last, before = gated.fwd(p["Wx"], p["b"], p["state"], function, reset, lengths)
+    ref = (h, last) + gated.bwd(p["Wx"], p["b"], before, function, p["dh"], p["dlast"], reset, lengths,
+                                packed=checkpoint is not None)
+    for name, a, r in zip(("h", "last", "dWx", "db", "dstate"), got, ref):
+        state = name in ("last", "dstate")
+        close(a, r, name, T, state or dtype == F32, fast=dtype == BF)
+    return got
+
+
+# (B, T, N, D): one step; one channel; odd widths (no 4-, 8- or 16-byte rows);
+# one chunk of 128 steps, one step more and one less; several chunks; several
+# 64-channel tiles, a ragged one; enough chunks for the states to pass between
+# many blocks
+SHAPES = [(1, 1, 1, 1), (2, 16, 1, 32), (3, 5, 2, 17), (1, 127, 1, 9), (2, 128, 1, 64), (2, 129, 3, 22),
+          (1, 1000, 1, 130), (2, 515, 1, 200), (1, 5003, 1, 36)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("function", ["linear", "linear_coupled"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "B%dT%dN%dD%d" % s)
+def test_parity(shape, function, dtype):
+    check(make(function, *shape, dtype), function)
+
+
+@pytest.mark.parametrize("checkpoint", [None, "int8"])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("function", ["linear", "linear_coupled"])
+@pytest.mark.parametrize("shape", [(4, 70, 1, 33), (5, 300, 2, 40), (4, 1100, 1, 64)], ids=lambda s: "B%dT%dN%dD%d" % s)
+def test_masks(shape, function, dtype, checkpoint):
+    B, T = shape[:2]
+    p = make(function, *shape, dtype, seed=3)
+    g = torch.Generator().manual_seed(T)
+    reset = torch.rand(B, T, generator=g) < 0.05
+    reset[0, 0] = True
+    reset[1] = True  # every step its own document
+    lengths = torch.tensor([T, T - 1, 0, T // 2, 1][:B], dtype=torch.int32)
+    clean = check(p, function, reset.cuda(), lengths.cuda(), checkpoint)
+    # whatever stands past a row's length must not matter
+    dirty = {k: v.clone() for k, v in p.items()}
+    for i in range(B):
+        n = int(lengths[i])
+        dirty["Wx"][i, n:] = float("nan")
+        dirty["dh"][i, n:] = float("inf")
+    again = run(dirty, function, reset.cuda(), lengths.cuda(), checkpoint)
+    for a, b in zip(clean, again):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 40, 1, 24), (1, 321, 2, 65), (2, 260, 1, 128)], ids=lambda s: "B%dT%dN%dD%d" % s)
+@pytest.mark.parametrize("function", ["linear", "linear_coupled"])
+def test_int8_checkpoint(shape, function, dtype):
+    p = make(function, *shape, dtype, seed=5)
+    got = check(p, function, checkpoint="int8")
+    plain = run(p, function)
+    assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])  # the forward is the same
+
+
+def test_reset_drops_an_infinite_state():
+    p = make("linear", 1, 200, 1, 64, F32)
+    p["state"].fill_(float("inf"))
+    reset = torch.zeros(1, 200, dtype=torch.bool, device="cuda")
+    reset[0, 0] = True
+    h, last = run(p, "linear", reset=reset, grads=False)
+    assert torch.isfinite(h).all() and torch.isfinite(last).all()
+
+
+def test_saturated_gates():
+    """Logits of +-inf and of the types' lowest value: gates exactly 0 or 1."""
+    for dtype in (F32, BF):
+        for low in (float("-inf"), torch.finfo(dtype).min):
+            Wx = torch.zeros(1, 300, 4, 1, 64, dtype=dtype, device="cuda")
+            Wx[:, :, 0] = low   # nothing read
+            Wx[:, :, 1] = -low  # everything kept
+            Wx[:, :, 2] = 1000
+            Wx[:, :, 3] = -low
+            s = torch.full((1, 1, 1, 64), 3.0, device="cuda")
+            Wx.requires_grad_(True)
+            h, last = rn.gated_scan(Wx, None, s)
+            assert (h == 3).all() and (last == 3).all()
+            (d,) = torch.autograd.grad(h.float().sum(), Wx)
+            assert (d == 0).all()
+
+
+def test_no_steps_and_optional_arguments():
+    for dtype in (F32, BF):
+        Wx = torch.randn(2, 0, 4, 1, 8, device="cuda").to(dtype).requires_grad_(True)
+        b = torch.randn(4, 1, 8, device="cuda").to(dtype).requires_grad_(True)
+        s = torch.randn(2, 1, 1, 8, device="cuda", requires_grad=True)
+        h, last = rn.gated_scan(Wx, b, s)
+        assert h.shape == (2, 0, 1, 8) and torch.equal(last, s)
+        dl = torch.randn_like(last)
+        dx, db, ds = torch.autograd.grad(last, (Wx, b, s), dl)
+        assert dx.shape == Wx.shape and (db == 0).all() and torch.equal(ds, dl)
+        h, last = rn.gated_scan(Wx)
+        assert (last == 0).all()
+    p = make("linear", 2, 150, 1, 40, F32)
+    zero_b, zero_s = torch.zeros_like(p["b"]), torch.zeros_like(p["state"])
+    h, last = rn.gated_scan(p["Wx"])
+    h2, last2 = rn.gated_scan(p["Wx"], zero_b, zero_s)
+    assert torch.equal(h, h2) and torch.equal(last, last2)
+    # the gradient of one output alone, of one input alone
+    x = p["Wx"].clone().requires_grad_(True)
+    h, last = rn.gated_scan(x, p["b"], p["state"])
+    (d,) = torch.autograd.grad(last, x, p["dlast"])
+    _, _, before = gated.fwd(p["Wx"], p["b"], p["state"], "linear")
+    close(d, gated.bwd(p["Wx"], p["b"], before, "linear", None, p["dlast"])[0], "dWx of last", 150, True)
+    s = p["state"].clone().requires_grad_(True)
+    h, last = rn.gated_scan(p["Wx"], p["b"], s)
+    (d,) = torch.autograd.grad(h, s, p["dh"])
+    close(d, gated.bwd(p["Wx"], p["b"], before, "linear", p["dh"], None)[2], "dstate of h", 150, True)
+
+
+def test_strided_and_misaligned_inputs():
+    p = make("linear", 2, 140, 2, 24, BF)
+    ref = run(p, "linear")
+    wide = torch.empty(2, 140, 4, 2, 48, dtype=BF, device="cuda")
+    wide[..., ::2] = p["Wx"]
+    raw = torch.empty(p["b"].numel() + 1, dtype=BF, device="cuda")
+    raw[1:] = p["b"].reshape(-1)
+    q = dict(p, dh=p["dh"].transpose(2, 3).contiguous().transpose(2, 3))
+    leaves = [wide[..., ::2].requires_grad_(True), raw[1:].reshape(p["b"].shape).requires_grad_(True),
+              p["state"].clone().requires_grad_(True)]
+    h, last = rn.gated_scan(*leaves)
+    got = (h, last) + torch.autograd.grad((h, last), leaves, (q["dh"], q["dlast"]))
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
+
+
+def test_repeatable_and_independent_of_the_batch():
+    """The same bits on every run, and for a row whatever rows it runs with."""
+    for shape in ((6, 900, 1, 192), (1, 20000, 1, 40)):
+        p = make("linear", *shape, BF)
+        a, b = run(p, "linear"), run(p, "linear")
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    p = make("linear", 6, 900, 1, 192, BF)
+    a = run(p, "linear", grads=False)
+    one = {k: v[2:3].contiguous() if k != "b" else v for k, v in p.items()}
+    h, last = run(one, "linear", grads=False)
+    assert torch.equal(h[0], a[0][2]) and torch.equal(last[0], a[1][2])
+
+
+def test_continues_from_its_last_state():
+    p = make("linear", 2, 300, 1, 64, F32)
+    h, last = run(p, "linear", grads=False)
+    h1, s = rn.gated_scan(p["Wx"][:, :131].contiguous(), p["b"], p["state"])
+    h2, l2 = rn.gated_scan(p["Wx"][:, 131:].contiguous(), p["b"], s)
+    close(torch.cat([h1, h2], 1), h.double().cpu().numpy(), "h in two calls", 300, True)
+    close(l2, last.double().cpu().numpy(), "last in two calls", 300, True)
+
+
+def test_on_another_stream():
+    p = make("linear", 2, 700, 1, 96, BF)
+    ref = run(p, "linear")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        got = run(p, "linear")
+    torch.cuda.current_stream().wait_stream(st)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("function", ["linear", "linear_coupled"])
+@pytest.mark.parametrize("M,P,N,D", [(1, 1, 1, 1), (3, 5, 2, 17), (64, 80, 1, 256), (5, 9, 3, 22)])
+def test_step(M, P, N, D, function, dtype):
+    p = make(function, M, 1, N, D, dtype, seed=11)
+    g = torch.Generator().manual_seed(M)
+    pool = torch.randn(P, N, D, generator=g).cuda()
+    slots = torch.randperm(P, generator=g)[:M].to(torch.int32)
+    if M > 2:
+        slots[1] = -1
+    keep = pool.clone()
+    out = keep.clone()
+    h = rn.gated_scan_step(p["Wx"][:, 0], p["b"], pool, slots.cuda(), function, pool_out=out)
+    assert torch.equal(pool, keep)
+    ref_pool = keep.double().cpu().numpy()
+    ref_h = np.zeros((M, N, D))
+    for m in range(M):
+        s = int(slots[m])
+        if s >= 0:
+            r, last, _ = gated.fwd(p["Wx"][m:m + 1], p["b"], keep[s][None, None], function)
+            ref_h[m], ref_pool[s] = r[0, 0], last[0, 0]
+    close(h, ref_h, "h", 1, dtype == F32, fast=dtype == BF)
+    close(out, ref_pool, "pool", 1, True, fast=dtype == BF)
+    h2 = rn.gated_scan_step(p["Wx"][:, 0], p["b"], pool, slots.cuda(), function)  # in place
+    assert torch.equal(h, h2) and torch.equal(pool, out)
+
+
+def test_steps_follow_the_scan():
+    p = make("linear", 3, 20, 2, 40, F32)
+    h, last = run(p, "linear", grads=False)
+    pool = p["state"][:, 0].clone()
+    hs = torch.stack([rn.gated_scan_step(p["Wx"][:, t], p["b"], pool) for t in range(20)], 1)
+    close(hs, h.double().cpu().numpy(), "h by steps", 20, True)
+    close(pool, last[:, 0].double().cpu().numpy(), "state by steps", 20, True)
+
+
+def test_step_reports_a_slot_past_the_pool():
+    p = make("linear", 2, 1, 1, 16, F32)
+    pool = torch.randn(3, 1, 16, device="cuda")
+    keep = pool.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    slots = torch.tensor([3, 1], dtype=torch.int32, device="cuda")
+    h = rn.gated_scan_step(p["Wx"][:, 0], p["b"], pool, slots, status=status)
+    assert (h[0] == 0).all() and torch.equal(pool[0], keep[0]) and torch.equal(pool[2], keep[2])
+    with pytest.raises(_lib.RnnError) as err:
+        _lib.rnn_check_status(status)
+    assert err.value.status == _lib.RNN_ERANGE
+    _lib.rnn_check_status(status)  # read and cleared
+
+
+def test_refusals():
+    p = make("linear", 2, 3, 1, 8, F32)
+    Wx, b, s = p["Wx"], p["b"], p["state"]
+    pool = torch.zeros(2, 1, 8, device="cuda")
+    bad = [
+        lambda: rn.gated_scan(Wx, b, function="lstm"), lambda: rn.gated_scan(Wx, b, function="linear_coupled"),
+        lambda: rn.gated_scan(Wx[0], b), lambda: rn.gated_scan(Wx, b[0]), lambda: rn.gated_scan(Wx, b, s[:1]),
+        lambda: rn.gated_scan(Wx, b, reset=torch.zeros(2, 4, dtype=torch.bool, device="cuda")),
+        lambda: rn.gated_scan(Wx, b, lengths=torch.zeros(3, dtype=torch.int32, device="cuda")),
+        lambda: rn.gated_scan(Wx, b, checkpoint="int4"), lambda: rn.gated_scan(Wx, b, s.cpu()),
+        lambda: rn.gated_scan_step(Wx[:, 0], b, pool[:1]), lambda: rn.gated_scan_step(Wx[:, 0], b, pool[..., :4]),
+        lambda: rn.gated_scan_step(Wx[:, 0], b, pool, torch.zeros(2, dtype=torch.int64, device="cuda")),
+        lambda: rn.gated_scan_step(Wx[:, 0], b, pool, pool_out=torch.zeros(3, 1, 8, device="cuda")),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: rn.gated_scan(Wx.double(), b), lambda: rn.gated_scan(Wx, b.to(BF)),
+                 lambda: rn.gated_scan(Wx, b, reset=torch.zeros(2, 3, device="cuda")),
+                 lambda: rn.gated_scan(Wx, b, lengths=torch.zeros(2, device="cuda")),
+                 lambda: rn.gated_scan_step(Wx[:, 0], b, pool.to(BF))):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(_lib.RnnError):
+        rn.gated_scan(Wx[:0], b)
