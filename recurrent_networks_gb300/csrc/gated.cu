@@ -4,13 +4,31 @@
 
 #include "gated.cuh"
 #include "kernels.cuh"
+#include "ptx.cuh"
 #include "rnn.h"
 
 namespace rnn {
 namespace {
 
+// Work item: GATED_CHUNK steps of 128 bytes of channels (64 bf16, 32 fp32) of
+// one batch row, one CTA. Each of the 8 warps holds 16 consecutive steps, a
+// lane 4 bytes of channels. The recurrence is affine in its state, so a warp
+// first folds its steps into one map c -> P c + H, the CTA folds the warps'
+// maps, and the state that enters the chunk comes from the chunks before it:
+// chunks are grouped by `span`; the last chunk of a group publishes the state
+// after it, every other chunk its own map as soon as it has it, and a chunk
+// starts from the state before its group and folds the maps of the group's
+// chunks before it, in their order. The order of the sums is thus fixed, and
+// the chain through the chunks has one hop per group. Items are handed out in
+// chunk order, so whatever an item waits for is already running.
+constexpr int WARPS = 8, STEPS = GATED_CHUNK / WARPS, THREADS = WARPS * 32;
+constexpr int MAX_SPAN = 32;
+
 struct GatedArgs {
   int B, T, C, chunks;  // C = N D channels
+  int tiles_c;          // channel tiles per batch row
+  int span;             // chunks per group
+  int tma;              // rows are 16-byte multiples: tiles come by TMA
   const void* Wx;
   const void* bias;
   const float* s0;
@@ -18,119 +36,572 @@ struct GatedArgs {
   const int* lengths;
   void* h;
   float* last;
-  float* carry;              // [B][chunks][C]: the state before every chunk
-  const signed char* q;      // 8-bit pre-activations (backward)
-  const unsigned char* qs;
+  float* carry;              // [B][chunks][C]: the state before every chunk (forward: the tape, or scratch)
+  signed char* q;            // 8-bit pre-activations: written by the forward, read by the backward
+  unsigned char* qs;
   const void* dh;
   const float* dlast;
   void* dWx;
   float* ds0;
-  float* dbp;                // [B][G][C]
+  float* dbp;                // [B chunks][G][C]
+  float* dcarry;             // backward: [B][chunks][C], the state gradient that leaves a chunk
+  float* maps;               // [B][chunks][2][C]: the chunks' maps
+  unsigned* status;
+  unsigned* ticket;
+  unsigned* flags;           // [chunks][tiles]
+  unsigned long long wait_limit_ns;
 };
 
 __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
-// One thread per channel, the steps in order.
-template <typename T, int FN>
-__global__ void __launch_bounds__(128) gated_fwd_kernel(GatedArgs p) {
-  constexpr int G = gated_gates(FN);
-  constexpr bool FAST = sizeof(T) == 2;
-  const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
-  if (id >= (long long)p.B * p.C) return;
-  const int b = (int)(id / p.C), ch = (int)(id % p.C);
-  const int len = clamp_len(p.lengths, b, p.T);
-  const T* x = (const T*)p.Wx + (size_t)b * p.T * G * p.C + ch;
-  T* h = (T*)p.h + (size_t)b * p.T * p.C + ch;
-  float bias[G];
-#pragma unroll
-  for (int g = 0; g < G; ++g) bias[g] = p.bias ? to_f(((const T*)p.bias)[(size_t)g * p.C + ch]) : 0.0f;
-  float c = p.s0 ? p.s0[id] : 0.0f;
-  for (int t = 0; t < p.T; ++t) {
-    if (p.carry && t % GATED_CHUNK == 0) p.carry[((size_t)b * p.chunks + t / GATED_CHUNK) * p.C + ch] = c;
-    float y = 0.0f;
-    if (t < len) {
-      float a[G], f, u;
-#pragma unroll
-      for (int g = 0; g < G; ++g) a[g] = to_f(x[((size_t)t * G + g) * p.C]) + bias[g];
-      gated_coeff<FN, FAST>(a, f, u);
-      const bool rst = p.reset && p.reset[(size_t)b * p.T + t];
-      c = rst ? u : fmaf(f, c, u);
-      y = gated_out<FN, FAST>(a, c);
-    }
-    h[(size_t)t * p.C] = from_f<T>(y);
-  }
-  if (p.last) p.last[id] = c;
+// f x + u, with x dropped where f is 0 (a reset): 0 times an infinite x is not NaN.
+__device__ __forceinline__ float affine(float f, float x, float u) { return f == 0.0f ? u : fmaf(f, x, u); }
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
 }
 
-template <typename T, int FN>
-__global__ void __launch_bounds__(128) gated_bwd_kernel(GatedArgs p) {
-  constexpr int G = gated_gates(FN);
+// The channels of a lane: 4 bytes of the storage type.
+template <typename T> struct Lane;
+template <> struct Lane<float> {
+  static constexpr int N = 1;
+  __device__ static void unpack(uint32_t v, float* x) { x[0] = __uint_as_float(v); }
+  __device__ static uint32_t pack(const float* x) { return __float_as_uint(x[0]); }
+};
+template <> struct Lane<__nv_bfloat16> {
+  static constexpr int N = 2;
+  __device__ static void unpack(uint32_t v, float* x) {
+    x[0] = __uint_as_float(v << 16);
+    x[1] = __uint_as_float(v & 0xffff0000u);
+  }
+  __device__ static uint32_t pack(const float* x) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[0], x[1]);
+    return *(const uint32_t*)&h;
+  }
+};
+
+// A lane's channels at p (n of them inside the row: 0 .. N), and back. `wide`:
+// the row starts on 4 bytes.
+template <typename T> __device__ __forceinline__ uint32_t load_lane(const T* p, int n, bool wide) {
+  if (n <= 0) return 0;
+  if (sizeof(T) == 4 || (wide && n == 2)) return __ldg((const uint32_t*)p);
+  const unsigned short* q = (const unsigned short*)p;
+  return (uint32_t)__ldg(q) | (n == 2 ? (uint32_t)__ldg(q + 1) << 16 : 0u);
+}
+template <typename T> __device__ __forceinline__ void store_lane(T* p, uint32_t v, int n, bool wide) {
+  if (n <= 0) return;
+  if (sizeof(T) == 4 || (wide && n == 2)) {
+    *(uint32_t*)p = v;
+    return;
+  }
+  unsigned short* q = (unsigned short*)p;
+  q[0] = (unsigned short)v;
+  if (n == 2) q[1] = (unsigned short)(v >> 16);
+}
+
+// The item of this CTA and where it lies.
+struct Item {
+  int k, tile, b, ch, n, t0, len;  // ch: the lane's first channel, n: how many of its channels exist; t0: the warp's first step
+  int live;                        // the warp's steps that exist
+  unsigned rst;                    // bit j: reset at the warp's step j
+};
+template <int N, bool REVERSE> __device__ __forceinline__ Item item_of(const GatedArgs& p, unsigned* shared) {
+  unsigned id = blockIdx.x;
+  if (p.chunks > 1) {
+    if (threadIdx.x == 0) *shared = atomicAdd(p.ticket, 1u);
+    __syncthreads();
+    id = *shared;
+  }
+  const unsigned tiles = (unsigned)p.B * p.tiles_c;
+  Item it;
+  it.k = (int)(id / tiles);
+  if (REVERSE) it.k = p.chunks - 1 - it.k;
+  it.tile = (int)(id % tiles);
+  it.b = it.tile / p.tiles_c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  it.ch = (it.tile % p.tiles_c) * 32 * N + lane * N;
+  it.n = min(max(p.C - it.ch, 0), N);
+  it.t0 = it.k * GATED_CHUNK + warp * STEPS;
+  it.len = clamp_len(p.lengths, it.b, p.T);
+  it.live = min(max(it.len - it.t0, 0), STEPS);
+  bool r = false;
+  if (p.reset && lane < it.live) r = p.reset[(size_t)it.b * p.T + it.t0 + lane] != 0;
+  it.rst = __ballot_sync(0xffffffffu, r);
+  return it;
+}
+
+// A lane's fp32 values at channel it.ch of row r of a [rows][C] array.
+template <int N, bool L2> __device__ __forceinline__ void load_f(const float* a, size_t r, const GatedArgs& p, const Item& it, float* x) {
+#pragma unroll
+  for (int v = 0; v < N; ++v) {
+    const float* q = a + r * p.C + it.ch + v;
+    x[v] = v < it.n ? (L2 ? __ldcg(q) : __ldg(q)) : 0.0f;
+  }
+}
+template <int N> __device__ __forceinline__ void store_f(float* a, size_t r, const GatedArgs& p, const Item& it, const float* x) {
+#pragma unroll
+  for (int v = 0; v < N; ++v)
+    if (v < it.n) a[r * p.C + it.ch + v] = x[v];
+}
+
+// Warp 0: the state that enters the chunk (x in: the state before the first
+// chunk in processing order), given the chunk's own map (P, H). Publishes
+// what later chunks need. `order` is the chunk's place in processing order,
+// REVERSE: chunk index descends. `states` [B][chunks][C] holds the state
+// that enters a chunk.
+template <int N, bool REVERSE>
+__device__ __forceinline__ void chain(const GatedArgs& p, const Item& it, float* states, const float* P, const float* H, float* x) {
+  const int lane = threadIdx.x & 31;
+  const int o = REVERSE ? p.chunks - 1 - it.k : it.k;
+  const int first = o - o % p.span;
+  const bool ends = (o + 1) % p.span == 0, final = o + 1 == p.chunks;
+  const unsigned tiles = (unsigned)p.B * p.tiles_c;
+  auto chunk_of = [&](int order) { return REVERSE ? p.chunks - 1 - order : order; };
+  auto row_of = [&](int order) { return (size_t)it.b * p.chunks + chunk_of(order); };
+  auto raise = [&]() {
+    __syncwarp();
+    if (lane == 0)  // a release at gpu scope is cumulative: it covers the warp's stores before the barrier
+      asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(p.flags + (size_t)o * tiles + it.tile) : "memory");
+  };
+  if (!ends && !final) {
+    store_f<N>(p.maps, row_of(o) * 2, p, it, P);
+    store_f<N>(p.maps, row_of(o) * 2 + 1, p, it, H);
+    raise();
+  }
+  if (o > 0) {
+    // lane i waits for the chunk `first - 1 + i`
+    const int from = first > 0 ? first - 1 : 0;
+    bool failed = false;
+    for (int w = from + lane; w < o; w += 32)
+      counter_wait_bounded(p.flags + (size_t)w * tiles + it.tile, 1u, p.wait_limit_ns, p.status, failed);
+    __syncwarp();
+    if (first > 0) load_f<N, true>(states, row_of(first), p, it, x);
+#pragma unroll 4
+    for (int w = first; w < o; ++w) {
+      float mp[N], mh[N];
+      load_f<N, true>(p.maps, row_of(w) * 2, p, it, mp);
+      load_f<N, true>(p.maps, row_of(w) * 2 + 1, p, it, mh);
+#pragma unroll
+      for (int v = 0; v < N; ++v) x[v] = affine(mp[v], x[v], mh[v]);
+    }
+  }
+  if (ends && !final) {
+    float y[N];
+#pragma unroll
+    for (int v = 0; v < N; ++v) y[v] = affine(P[v], x[v], H[v]);
+    store_f<N>(states, row_of(o + 1), p, it, y);
+    raise();
+  }
+}
+
+// A warp's steps of a tile whose rows (t, g) are 128 bytes: one TMA box per
+// warp, or the lanes' own loads. Rows past `live` are not read.
+template <typename T, int ROWS>
+__device__ __forceinline__ void fetch_lanes(const GatedArgs& p, const Item& it, const T* src, uint32_t* dst) {
+  const int lane = threadIdx.x & 31;
+  const bool wide = p.C % 2 == 0 || sizeof(T) == 4;
+  const T* at = src + ((size_t)it.b * p.T + it.t0) * ROWS * p.C + it.ch;
+#pragma unroll 8
+  for (int r = 0; r < it.live * ROWS; ++r) dst[r * 32 + lane] = load_lane(at + (size_t)r * p.C, it.n, wide);
+}
+
+template <typename T, int FN, bool Q8>
+__global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const __grid_constant__ CUtensorMap xmap, GatedArgs p) {
+  constexpr int G = gated_gates(FN), N = Lane<T>::N;
   constexpr bool FAST = sizeof(T) == 2;
-  const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
-  if (id >= (long long)p.B * p.C) return;
-  const int b = (int)(id / p.C), ch = (int)(id % p.C);
-  const int len = clamp_len(p.lengths, b, p.T);
-  const int qblocks = (p.T + ACT_BLOCK - 1) / ACT_BLOCK;
-  float bias[G], db[G];
+  extern __shared__ __align__(128) unsigned char smem[];
+  uint32_t* tile = (uint32_t*)smem;                                   // [WARPS][STEPS][G][32]
+  float2* maps = (float2*)(tile + WARPS * STEPS * G * 32);            // [WARPS][32 N]
+  float* enter = (float*)(maps + WARPS * 32 * N);                     // [32 N]
+  uint32_t* tops = (uint32_t*)(enter + 32 * N);                       // Q8: [WARPS][G][32 N]
+  unsigned long long* bars = (unsigned long long*)(tops + (Q8 ? WARPS * G * 32 * N : 0));  // [WARPS]
+  unsigned* shared = (unsigned*)(bars + WARPS);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t bar = smem_u32(bars + warp);
+  if (p.tma && lane == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init_cluster();
+  }
+  const Item it = item_of<N, false>(p, shared);
+  uint32_t* mine = tile + warp * STEPS * G * 32;
+  if (p.tma) {
+    __syncwarp();
+    if (lane == 0 && it.live > 0) {
+      mbar_arrive_expect_tx(bar, STEPS * G * 128);
+      tma_load_4d(smem_u32(mine), &xmap, bar, (it.tile % p.tiles_c) * 32 * N, 0, it.t0, it.b);
+    }
+  } else {
+    fetch_lanes<T, G>(p, it, (const T*)p.Wx, mine);
+  }
+  const bool wide = p.C % 2 == 0;
+  float bias[G][N];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    bias[g] = p.bias ? to_f(((const T*)p.bias)[(size_t)g * p.C + ch]) : 0.0f;
-    db[g] = 0.0f;
+    uint32_t v = p.bias ? load_lane((const T*)p.bias + (size_t)g * p.C + it.ch, it.n, wide) : 0;
+    Lane<T>::unpack(v, bias[g]);
   }
-  auto load = [&](int t, float* a) {
+  float x[N];  // the state that enters the chunk
+#pragma unroll
+  for (int v = 0; v < N; ++v) x[v] = 0.0f;
+  if (warp == 0 && p.s0) load_f<N, false>(p.s0, it.b, p, it, x);
+  bool failed = false;
+  if (p.tma && it.live > 0) mbar_wait_bounded<false>(bar, 0, p.wait_limit_ns, p.status, failed);
+
+  float f[STEPS][N], u[STEPS][N], P[N], H[N];
+  uint32_t top[G][N];
+#pragma unroll
+  for (int v = 0; v < N; ++v) {
+    P[v] = 1.0f;
+    H[v] = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) top[g][v] = 0;
+  }
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    float a[G][N];
+#pragma unroll
+    for (int g = 0; g < G; ++g) Lane<T>::unpack(mine[(j * G + g) * 32 + lane], a[g]);
+    const bool on = j < it.live, rst = it.rst >> j & 1;
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      float z[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (Q8) top[g][v] = max(top[g][v], on ? __float_as_uint(fabsf(a[g][v])) : 0u);
+        z[g] = a[g][v] + bias[g][v];
+      }
+      gated_coeff<FN, FAST>(z, f[j][v], u[j][v]);
+      f[j][v] = !on ? 1.0f : rst ? 0.0f : f[j][v];
+      u[j][v] = on ? u[j][v] : 0.0f;
+      P[v] *= f[j][v];
+      H[v] = rst ? u[j][v] : fmaf(f[j][v], H[v], u[j][v]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < N; ++v) {
+    maps[warp * 32 * N + lane * N + v] = make_float2(P[v], H[v]);
+    if (Q8) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) tops[(warp * G + g) * 32 * N + lane * N + v] = top[g][v];
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w)
+#pragma unroll
+      for (int v = 0; v < N; ++v) {
+        const float2 m = maps[w * 32 * N + lane * N + v];
+        P[v] *= m.x;
+        H[v] = affine(m.x, H[v], m.y);
+      }
+    chain<N, false>(p, it, p.carry, P, H, x);
+    if (p.carry && (it.k == 0 || it.k % p.span != 0)) store_f<N>(p.carry, (size_t)it.b * p.chunks + it.k, p, it, x);
+#pragma unroll
+    for (int v = 0; v < N; ++v) enter[lane * N + v] = x[v];
+    if (p.last && it.k == p.chunks - 1) {
+#pragma unroll
+      for (int v = 0; v < N; ++v) x[v] = affine(P[v], x[v], H[v]);
+      store_f<N>(p.last, it.b, p, it, x);
+    }
+  }
+  if (Q8) {  // before the wait for the state: the tile in 8 bits
+    const int qblocks = (p.T + ACT_BLOCK - 1) / ACT_BLOCK;
+    float inv[G][N];
+    bool fin[G][N];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int v = 0; v < N; ++v) {
+        const uint32_t t = max(top[g][v], tops[((warp ^ 1) * G + g) * 32 * N + lane * N + v]);
+        const unsigned s = act_scale_byte(__uint_as_float(t));
+        inv[g][v] = act_inv_scale(s);
+        fin[g][v] = s != ACT_NONFINITE;
+        if ((warp & 1) == 0 && v < it.n && it.t0 < p.T)
+          p.qs[(((size_t)it.b * qblocks + it.t0 / ACT_BLOCK) * G + g) * p.C + it.ch + v] = (unsigned char)s;
+      }
+    signed char* q = p.q + ((size_t)it.b * p.T + it.t0) * G * p.C + it.ch;
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      if (it.t0 + j >= p.T) break;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float a[N];
+        Lane<T>::unpack(mine[(j * G + g) * 32 + lane], a);
+        int b8[N];
+#pragma unroll
+        for (int v = 0; v < N; ++v) b8[v] = j < it.live && fin[g][v] ? act_quant(a[v], inv[g][v]) : 0;
+        signed char* at = q + (size_t)(j * G + g) * p.C;
+        if (N == 2 && wide && it.n == 2)
+          *(unsigned short*)at = (unsigned short)((b8[0] & 255) | (b8[N - 1] & 255) << 8);
+        else
+#pragma unroll
+          for (int v = 0; v < N; ++v)
+            if (v < it.n) at[v] = (signed char)b8[v];
+      }
+    }
+  }
+  __syncthreads();
+  float c[N];
+#pragma unroll
+  for (int v = 0; v < N; ++v) {
+    c[v] = enter[lane * N + v];
+    for (int w = 0; w < warp; ++w) {
+      const float2 m = maps[w * 32 * N + lane * N + v];
+      c[v] = affine(m.x, c[v], m.y);
+    }
+  }
+  T* h = (T*)p.h + ((size_t)it.b * p.T + it.t0) * p.C + it.ch;
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    if (it.t0 + j >= p.T) break;
+    const bool rst = it.rst >> j & 1;
+    float a[N], y[N];
+    if (FN == GATED_LINEAR) Lane<T>::unpack(mine[(j * G + G - 1) * 32 + lane], a);
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      float z[G];
+      z[G - 1] = FN == GATED_LINEAR ? a[v] + bias[G - 1][v] : 0.0f;
+      c[v] = rst ? u[j][v] : fmaf(f[j][v], c[v], u[j][v]);
+      y[v] = j < it.live ? gated_out<FN, FAST>(z, c[v]) : 0.0f;
+    }
+    store_lane(h + (size_t)j * p.C, Lane<T>::pack(y), it.n, wide);
+  }
+}
+
+template <typename T, int FN, bool Q8>
+__global__ void __launch_bounds__(THREADS, 2) gated_bwd_kernel(const __grid_constant__ CUtensorMap xmap,
+                                                               const __grid_constant__ CUtensorMap dmap, GatedArgs p) {
+  constexpr int G = gated_gates(FN), N = Lane<T>::N;
+  constexpr bool FAST = sizeof(T) == 2;
+  constexpr int XB = Q8 ? 32 * N : 128;  // bytes of a row (t, g) of the tile
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char* tile = smem;                                          // [WARPS][STEPS][G][XB]
+  uint32_t* dtile = (uint32_t*)(tile + WARPS * STEPS * G * XB);        // [WARPS][STEPS][32]
+  float* maps = (float*)(dtile + WARPS * STEPS * 32);                  // [WARPS][3][32 N]: P, H (state), E (gradient)
+  float* enter = maps + WARPS * 3 * 32 * N;                            // [32 N]
+  float* dbs = enter + 32 * N;                                         // [WARPS][G][32 N]
+  unsigned long long* bars = (unsigned long long*)(dbs + WARPS * G * 32 * N);
+  unsigned* shared = (unsigned*)(bars + WARPS);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t bar = smem_u32(bars + warp);
+  if (p.tma && lane == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init_cluster();
+  }
+  const Item it = item_of<N, true>(p, shared);
+  unsigned char* mine = tile + warp * STEPS * G * XB;
+  uint32_t* dmine = dtile + warp * STEPS * 32;
+  const bool wide = p.C % 2 == 0;
+  if (p.tma) {
+    __syncwarp();
+    if (lane == 0 && it.live > 0) {
+      mbar_arrive_expect_tx(bar, STEPS * G * XB + (p.dh ? STEPS * 128 : 0));
+      tma_load_4d(smem_u32(mine), &xmap, bar, (it.tile % p.tiles_c) * 32 * N, 0, it.t0, it.b);
+      if (p.dh) tma_load_4d(smem_u32(dmine), &dmap, bar, (it.tile % p.tiles_c) * 32 * N, 0, it.t0, it.b);
+    }
+  } else {
+    if (Q8) {
+      const signed char* at = p.q + ((size_t)it.b * p.T + it.t0) * G * p.C + it.ch;
+#pragma unroll 8
+      for (int r = 0; r < it.live * G; ++r)
+#pragma unroll
+        for (int v = 0; v < N; ++v) mine[r * XB + lane * N + v] = v < it.n ? (unsigned char)__ldg(at + (size_t)r * p.C + v) : 0;
+    } else {
+      fetch_lanes<T, G>(p, it, (const T*)p.Wx, (uint32_t*)mine);
+    }
+    if (p.dh) fetch_lanes<T, 1>(p, it, (const T*)p.dh, dmine);
+  }
+  float bias[G][N], scale[G][N];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    uint32_t w = p.bias ? load_lane((const T*)p.bias + (size_t)g * p.C + it.ch, it.n, wide) : 0;
+    Lane<T>::unpack(w, bias[g]);
+    if (Q8) {
+      const int qblocks = (p.T + ACT_BLOCK - 1) / ACT_BLOCK;
+#pragma unroll
+      for (int v = 0; v < N; ++v)
+        scale[g][v] = v < it.n && it.t0 < p.T
+                          ? act_scale(p.qs[(((size_t)it.b * qblocks + it.t0 / ACT_BLOCK) * G + g) * p.C + it.ch + v])
+                          : 0.0f;
+    }
+  }
+  float c[N], x[N];  // c: the state that enters the chunk; x: the state gradient that enters it from later steps
+  load_f<N, false>(p.carry, (size_t)it.b * p.chunks + it.k, p, it, c);
+#pragma unroll
+  for (int v = 0; v < N; ++v) x[v] = 0.0f;
+  if (warp == 0 && p.dlast) load_f<N, false>(p.dlast, it.b, p, it, x);
+  bool failed = false;
+  if (p.tma && it.live > 0) mbar_wait_bounded<false>(bar, 0, p.wait_limit_ns, p.status, failed);
+
+  auto gates = [&](int j, float z[G][N]) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const size_t at = (((size_t)b * p.T + t) * G + g) * p.C + ch;
-      if (p.q) {
-        const unsigned s = p.qs[(((size_t)b * qblocks + t / ACT_BLOCK) * G + g) * p.C + ch];
-        a[g] = (float)p.q[at] * act_scale(s) + bias[g];
+      if (Q8) {
+        const signed char* r = (const signed char*)mine + (j * G + g) * XB + lane * N;
+        if (N == 2) {
+          const char2 v = *(const char2*)r;
+          z[g][0] = fmaf((float)v.x, scale[g][0], bias[g][0]);
+          z[g][N - 1] = fmaf((float)v.y, scale[g][N - 1], bias[g][N - 1]);
+        } else {
+          z[g][0] = fmaf((float)r[0], scale[g][0], bias[g][0]);
+        }
       } else {
-        a[g] = to_f(((const T*)p.Wx)[at]) + bias[g];
+        Lane<T>::unpack(*(const uint32_t*)(mine + (j * G + g) * XB + lane * 4), z[g]);
+#pragma unroll
+        for (int v = 0; v < N; ++v) z[g][v] += bias[g][v];
       }
     }
   };
-  float carry = p.dlast ? p.dlast[id] : 0.0f;  // f_{t+1} delta_{t+1}
-  float cs[GATED_CHUNK];
-  for (int k = p.chunks - 1; k >= 0; --k) {
-    const int t0 = k * GATED_CHUNK, t1 = min(p.T, t0 + GATED_CHUNK);
-    const float start = p.carry[((size_t)b * p.chunks + k) * p.C + ch];
-    float c = start;
-    for (int t = t0; t < min(t1, len); ++t) {
-      float a[G], f, u;
-      load(t, a);
-      gated_coeff<FN, FAST>(a, f, u);
-      c = p.reset && p.reset[(size_t)b * p.T + t] ? u : fmaf(f, c, u);
-      cs[t - t0] = c;
-    }
-    for (int t = t1 - 1; t >= t0; --t) {
-      float da[G];
+  auto upstream = [&](int j, float* d) {
+    Lane<T>::unpack(p.dh ? dmine[j * 32 + lane] : 0u, d);
+  };
+
+  float f[STEPS][N], u[STEPS][N], P[N], H[N], E[N];
 #pragma unroll
-      for (int g = 0; g < G; ++g) da[g] = 0.0f;
-      if (t < len) {
-        float a[G], f, u;
-        load(t, a);
-        gated_coeff<FN, FAST>(a, f, u);
-        const bool rst = p.reset && p.reset[(size_t)b * p.T + t];
-        const float dh = p.dh ? to_f(((const T*)p.dh)[((size_t)b * p.T + t) * p.C + ch]) : 0.0f;
-        const float delta = carry + gated_into<FN, FAST>(a, dh);
-        const float cp = rst ? 0.0f : (t > t0 ? cs[t - t0 - 1] : start);
-        gated_grad<FN, FAST>(a, cp, cs[t - t0], dh, delta, da);
-        carry = rst ? 0.0f : f * delta;
+  for (int v = 0; v < N; ++v) {
+    P[v] = 1.0f;
+    H[v] = E[v] = 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    float z[G][N], d[N];
+    gates(j, z);
+    upstream(j, d);
+    const bool on = j < it.live, rst = it.rst >> j & 1;
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      float a[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) a[g] = z[g][v];
+      gated_coeff<FN, FAST>(a, f[j][v], u[j][v]);
+      const float e = on ? gated_into<FN, FAST>(a, d[v]) : 0.0f;
+      f[j][v] = !on ? 1.0f : rst ? 0.0f : f[j][v];
+      u[j][v] = on ? u[j][v] : 0.0f;
+      // what step j's delta sends out of the warp's first step: f_0 .. f_j times it
+      P[v] *= f[j][v];
+      H[v] = rst ? u[j][v] : fmaf(f[j][v], H[v], u[j][v]);
+      E[v] = affine(P[v], e, E[v]);
+    }
+  }
+  float* m = maps + warp * 3 * 32 * N + lane * N;
+#pragma unroll
+  for (int v = 0; v < N; ++v) {
+    m[v] = P[v];
+    m[32 * N + v] = H[v];
+    m[64 * N + v] = E[v];
+  }
+  __syncthreads();
+  if (warp == 0) {  // the chunk's map of the gradient, last warp first
+    float PC[N], EC[N];
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      PC[v] = 1.0f;
+      EC[v] = 0.0f;
+    }
+#pragma unroll
+    for (int w = WARPS - 1; w >= 0; --w)
+#pragma unroll
+      for (int v = 0; v < N; ++v) {
+        const float* q = maps + w * 3 * 32 * N + lane * N + v;
+        PC[v] *= q[0];
+        EC[v] = affine(q[0], EC[v], q[64 * N]);
       }
+    chain<N, true>(p, it, p.dcarry, PC, EC, x);
+#pragma unroll
+    for (int v = 0; v < N; ++v) enter[lane * N + v] = x[v];
+    if (p.ds0 && it.k == 0) {
+#pragma unroll
+      for (int v = 0; v < N; ++v) x[v] = affine(PC[v], x[v], EC[v]);
+      store_f<N>(p.ds0, it.b, p, it, x);
+    }
+  }
+  // the states of the warp's steps, while the gradient is on its way
+#pragma unroll
+  for (int v = 0; v < N; ++v)
+    for (int w = 0; w < warp; ++w) {
+      const float* q = maps + w * 3 * 32 * N + lane * N + v;
+      c[v] = affine(q[0], c[v], q[32 * N]);
+    }
+  float first[N];
+#pragma unroll
+  for (int v = 0; v < N; ++v) first[v] = c[v];
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+    for (int v = 0; v < N; ++v) u[j][v] = c[v] = (it.rst >> j & 1) ? u[j][v] : fmaf(f[j][v], c[v], u[j][v]);
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < N; ++v) {
+    x[v] = enter[lane * N + v];
+    for (int w = WARPS - 1; w > warp; --w) {
+      const float* q = maps + w * 3 * 32 * N + lane * N + v;
+      x[v] = affine(q[0], x[v], q[64 * N]);
+    }
+  }
+  float db[G][N];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int v = 0; v < N; ++v) db[g][v] = 0.0f;
+  T* out = p.dWx ? (T*)p.dWx + ((size_t)it.b * p.T + it.t0) * G * p.C + it.ch : nullptr;
+#pragma unroll
+  for (int j = STEPS - 1; j >= 0; --j) {
+    float z[G][N], d[N], da[G][N];
+    gates(j, z);
+    upstream(j, d);
+    const bool on = j < it.live, rst = it.rst >> j & 1;
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      float a[G], r[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) a[g] = z[g][v];
+      const float delta = x[v] + gated_into<FN, FAST>(a, d[v]);
+      const float cp = rst ? 0.0f : j > 0 ? u[j - 1][v] : first[v];
+      gated_grad<FN, FAST>(a, cp, u[j][v], d[v], delta, r);
+      x[v] = on ? (rst ? 0.0f : f[j][v] * delta) : x[v];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        db[g] += da[g];
-        if (p.dWx) ((T*)p.dWx)[(((size_t)b * p.T + t) * G + g) * p.C + ch] = from_f<T>(da[g]);
+        da[g][v] = on ? r[g] : 0.0f;
+        db[g][v] += da[g][v];
       }
     }
+    if (out && it.t0 + j < p.T) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) store_lane(out + (size_t)(j * G + g) * p.C, Lane<T>::pack(da[g]), it.n, wide);
+    }
   }
-  if (p.ds0) p.ds0[id] = carry;
   if (p.dbp) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) p.dbp[((size_t)b * G + g) * p.C + ch] = db[g];
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int v = 0; v < N; ++v) dbs[(warp * G + g) * 32 * N + lane * N + v] = db[g][v];
+    __syncthreads();
+    for (int i = threadIdx.x; i < G * 32 * N; i += THREADS) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) s += dbs[w * G * 32 * N + i];
+      const int g = i / (32 * N), ch = (it.tile % p.tiles_c) * 32 * N + i % (32 * N);
+      if (ch < p.C) p.dbp[(((size_t)it.b * p.chunks + it.k) * G + g) * p.C + ch] = s;
+    }
   }
+}
+
+template <typename T, int FN, bool Q8> constexpr int fwd_smem() {
+  constexpr int G = gated_gates(FN), N = Lane<T>::N;
+  return WARPS * STEPS * G * 128 + WARPS * 32 * N * 8 + 32 * N * 4 + (Q8 ? WARPS * G * 32 * N * 4 : 0) + WARPS * 8 + 16;
+}
+template <typename T, int FN, bool Q8> constexpr int bwd_smem() {
+  constexpr int G = gated_gates(FN), N = Lane<T>::N;
+  return WARPS * STEPS * (G * (Q8 ? 32 * N : 128) + 128) + WARPS * 3 * 32 * N * 4 + 32 * N * 4 + WARPS * G * 32 * N * 4 +
+         WARPS * 8 + 16;
 }
 
 // db[j] = sum over `rows` of dbp[row][j], in row order within 8 interleaved
@@ -200,12 +671,15 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 bool gated_dims_ok(const rnn_gated_dims_t* d) {
   return d && d->B >= 1 && d->T >= 0 && d->N >= 1 && d->D >= 1 && (d->function == RNN_LINEAR || d->function == RNN_LINEAR_COUPLED) &&
          (d->dtype == RNN_F32 || d->dtype == RNN_BF16) && (d->checkpoint == RNN_CKPT_NONE || d->checkpoint == RNN_CKPT_INT8) &&
-         (long long)d->N * d->D <= (1 << 28) && (unsigned long long)d->B * d->N * d->D < (1ull << 37);
+         (long long)d->N * d->D <= (1 << 28) &&
+         // one CTA per 128 steps of 32 (at least) channels
+         (double)d->B * (d->N * (double)d->D / 32 + 1) * (d->T / (double)GATED_CHUNK + 1) < 2147483647.0;
 }
 
 struct GatedSizes {
-  int G, C, chunks, qblocks;
-  size_t esize, carry, q, qs, tape, dbp;
+  int G, C, chunks, qblocks, tiles_c, span;
+  size_t esize, carry, q, qs, tape;
+  size_t sync, maps, dbp;  // workspace: status, ticket and flags (zeroed by every call) | maps | states | db sums
 };
 GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   GatedSizes z;
@@ -214,27 +688,77 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   z.chunks = (d->T + GATED_CHUNK - 1) / GATED_CHUNK;
   z.qblocks = (d->T + ACT_BLOCK - 1) / ACT_BLOCK;
   z.esize = d->dtype == RNN_BF16 ? 2 : 4;
-  z.carry = up256((size_t)d->B * z.chunks * z.C * sizeof(float));
+  const int width = d->dtype == RNN_BF16 ? 64 : 32;
+  z.tiles_c = (z.C + width - 1) / width;
+  const size_t tiles = (size_t)d->B * z.tiles_c;
+  // With fewer tiles than CTAs run at once, chunks of one tile run side by
+  // side and wait on one another: groups of chunks then keep the chain short.
+  const size_t resident = 2 * (size_t)device_sms();
+  z.span = tiles >= resident ? 1 : (int)((2 * resident + tiles - 1) / tiles);
+  if (z.span > MAX_SPAN) z.span = MAX_SPAN;
+  const size_t states = up256((size_t)d->B * z.chunks * z.C * sizeof(float));
+  z.carry = states;
   const bool q8 = d->checkpoint == RNN_CKPT_INT8;
   z.q = q8 ? up256((size_t)d->B * d->T * z.G * z.C) : 0;
   z.qs = q8 ? up256((size_t)d->B * z.qblocks * z.G * z.C) : 0;
   z.tape = z.carry + z.q + z.qs;
-  z.dbp = up256((size_t)d->B * z.G * z.C * sizeof(float));
+  z.sync = z.chunks > 1 ? 512 + up256(tiles * z.chunks * sizeof(unsigned)) : 256;
+  z.maps = z.chunks > 1 && z.span > 1 ? 2 * states : 0;
+  z.dbp = up256((size_t)d->B * z.chunks * z.G * z.C * sizeof(float));
   return z;
 }
 
-template <typename T>
-cudaError_t gated_launch(int fn, bool bwd, const GatedArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)(((long long)a.B * a.C + 127) / 128);
-  if (fn == GATED_LINEAR) {
-    if (bwd) gated_bwd_kernel<T, GATED_LINEAR><<<grid, 128, 0, st>>>(a);
-    else gated_fwd_kernel<T, GATED_LINEAR><<<grid, 128, 0, st>>>(a);
-  } else {
-    if (bwd) gated_bwd_kernel<T, GATED_COUPLED><<<grid, 128, 0, st>>>(a);
-    else gated_fwd_kernel<T, GATED_COUPLED><<<grid, 128, 0, st>>>(a);
+// [C][rows][T][B] box of one warp's steps; elem: 1, 2 or 4 bytes
+cudaError_t tile_map(CUtensorMap* m, const void* base, int elem, const GatedArgs& a, int rows, int width) {
+  const unsigned long long dims[4] = {(unsigned long long)a.C, (unsigned long long)rows, (unsigned long long)a.T,
+                                      (unsigned long long)a.B};
+  const unsigned box[4] = {(unsigned)width, (unsigned)rows, (unsigned)STEPS, 1};
+  return encode_tensor_map(m, base, elem, 4, dims, box);
+}
+
+template <typename T, int FN, bool Q8> cudaError_t gated_launch(bool bwd, GatedArgs a, cudaStream_t st) {
+  constexpr int G = gated_gates(FN), width = 32 * Lane<T>::N;
+  const int xelem = bwd && Q8 ? 1 : (int)sizeof(T);
+  // TMA rows start on 16 bytes
+  a.tma = ((size_t)a.C * xelem) % 16 == 0 && ((size_t)a.C * sizeof(T)) % 16 == 0;
+  CUtensorMap x = {}, d = {};
+  if (a.tma) {
+    cudaError_t e = tile_map(&x, bwd && Q8 ? (const void*)a.q : a.Wx, xelem, a, G, width);
+    if (e == cudaSuccess && bwd && a.dh) e = tile_map(&d, a.dh, (int)sizeof(T), a, 1, width);
+    if (e != cudaSuccess) return e;
   }
+  const size_t items = (size_t)a.B * a.tiles_c * a.chunks;
+  const int smem = bwd ? bwd_smem<T, FN, Q8>() : fwd_smem<T, FN, Q8>();
+  const void* k = bwd ? (const void*)gated_bwd_kernel<T, FN, Q8> : (const void*)gated_fwd_kernel<T, FN, Q8>;
+  cudaError_t e = set_smem_attr(k, smem);
+  if (e != cudaSuccess) return e;
+  if (bwd) gated_bwd_kernel<T, FN, Q8><<<(unsigned)items, THREADS, smem, st>>>(x, d, a);
+  else gated_fwd_kernel<T, FN, Q8><<<(unsigned)items, THREADS, smem, st>>>(x, a);
   note_launch();
   return cudaGetLastError();
+}
+template <typename T> cudaError_t gated_launch(int fn, bool q8, bool bwd, const GatedArgs& a, cudaStream_t st) {
+  if (fn == GATED_LINEAR)
+    return q8 ? gated_launch<T, GATED_LINEAR, true>(bwd, a, st) : gated_launch<T, GATED_LINEAR, false>(bwd, a, st);
+  return q8 ? gated_launch<T, GATED_COUPLED, true>(bwd, a, st) : gated_launch<T, GATED_COUPLED, false>(bwd, a, st);
+}
+cudaError_t gated_launch(const rnn_gated_dims_t* d, bool q8, bool bwd, const GatedArgs& a, cudaStream_t st) {
+  return d->dtype == RNN_BF16 ? gated_launch<__nv_bfloat16>(d->function, q8, bwd, a, st)
+                              : gated_launch<float>(d->function, q8, bwd, a, st);
+}
+
+// What both directions take from the dims and the workspace.
+GatedArgs gated_args(const rnn_gated_dims_t* d, const GatedSizes& z, void* workspace) {
+  GatedArgs a{};
+  a.B = d->B; a.T = d->T; a.C = z.C; a.chunks = z.chunks;
+  a.tiles_c = z.tiles_c; a.span = z.span;
+  char* ws = (char*)workspace;
+  a.status = (unsigned*)ws;
+  a.ticket = (unsigned*)(ws + 256);
+  a.flags = (unsigned*)(ws + 512);
+  a.maps = (float*)(ws + z.sync);
+  a.wait_limit_ns = wait_limit_ns();
+  return a;
 }
 
 }  // namespace
@@ -252,7 +776,8 @@ size_t rnn_gated_tape_size(const rnn_gated_dims_t* d) { return gated_dims_ok(d) 
 
 size_t rnn_gated_workspace_size(const rnn_gated_dims_t* d, int kind) {
   if (!gated_dims_ok(d) || (kind != RNN_WS_FWD && kind != RNN_WS_BWD)) return 0;
-  return 256 + (kind == RNN_WS_BWD ? gated_sizes(d).dbp : 0);
+  const GatedSizes z = gated_sizes(d);
+  return z.sync + z.maps + z.carry + (kind == RNN_WS_BWD ? z.dbp : 0);
 }
 
 int rnn_gated_fwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, const void* state0,
@@ -266,7 +791,7 @@ int rnn_gated_fwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
   if (ws_bytes < rnn_gated_workspace_size(d, RNN_WS_FWD)) return RNN_ENOSPC;
   cudaStream_t st = (cudaStream_t)stream;
   const GatedSizes z = gated_sizes(d);
-  int rc = cuda_status(cudaMemsetAsync(workspace, 0, 256, st));
+  int rc = cuda_status(cudaMemsetAsync(workspace, 0, z.sync, st));
   if (rc) return rc;
   if (d->T == 0) {
     const size_t bytes = (size_t)d->B * z.C * sizeof(float);
@@ -274,16 +799,16 @@ int rnn_gated_fwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
     return cuda_status(state0 ? cudaMemcpyAsync(last, state0, bytes, cudaMemcpyDeviceToDevice, st)
                               : cudaMemsetAsync(last, 0, bytes, st));
   }
-  GatedArgs a{};
-  a.B = d->B; a.T = d->T; a.C = z.C; a.chunks = z.chunks;
+  GatedArgs a = gated_args(d, z, workspace);
   a.Wx = Wx; a.bias = b; a.s0 = (const float*)state0; a.reset = reset; a.lengths = lengths;
-  a.h = h; a.last = (float*)last; a.carry = (float*)tape;
-  rc = cuda_status(d->dtype == RNN_BF16 ? gated_launch<__nv_bfloat16>(d->function, false, a, st)
-                                        : gated_launch<float>(d->function, false, a, st));
-  if (rc == RNN_OK && tape && d->checkpoint == RNN_CKPT_INT8)
-    rc = cuda_status(act_pack_run(d->dtype, d->B, d->T, z.G * z.C, lengths, Wx, (signed char*)tape + z.carry,
-                                  (unsigned char*)tape + z.carry + z.q, st));
-  return rc;
+  a.h = h; a.last = (float*)last;
+  a.carry = tape ? (float*)tape : (float*)((char*)workspace + z.sync + z.maps);
+  const bool q8 = tape && d->checkpoint == RNN_CKPT_INT8;
+  if (q8) {
+    a.q = (signed char*)tape + z.carry;
+    a.qs = (unsigned char*)tape + z.carry + z.q;
+  }
+  return cuda_status(gated_launch(d, q8, false, a, st));
 }
 
 int rnn_gated_bwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, const unsigned char* reset,
@@ -299,7 +824,7 @@ int rnn_gated_bwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
   if (ws_bytes < rnn_gated_workspace_size(d, RNN_WS_BWD)) return RNN_ENOSPC;
   cudaStream_t st = (cudaStream_t)stream;
   const GatedSizes z = gated_sizes(d);
-  int rc = cuda_status(cudaMemsetAsync(workspace, 0, 256, st));
+  int rc = cuda_status(cudaMemsetAsync(workspace, 0, z.sync, st));
   if (rc) return rc;
   if (d->T == 0) {
     const size_t bytes = (size_t)d->B * z.C * sizeof(float);
@@ -310,24 +835,23 @@ int rnn_gated_bwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
     }
     return db ? cuda_status(cudaMemsetAsync(db, 0, (size_t)z.G * z.C * z.esize, st)) : RNN_OK;
   }
-  GatedArgs a{};
-  a.B = d->B; a.T = d->T; a.C = z.C; a.chunks = z.chunks;
+  GatedArgs a = gated_args(d, z, workspace);
   a.Wx = Wx; a.bias = b; a.reset = reset; a.lengths = lengths;
   a.carry = (float*)tape;
   if (q8) {
-    a.q = (const signed char*)tape + z.carry;
-    a.qs = (const unsigned char*)tape + z.carry + z.q;
+    a.q = (signed char*)tape + z.carry;
+    a.qs = (unsigned char*)tape + z.carry + z.q;
   }
   a.dh = dh; a.dlast = (const float*)dlast; a.dWx = dWx; a.ds0 = (float*)dstate0;
-  a.dbp = db ? (float*)((char*)workspace + 256) : nullptr;
-  rc = cuda_status(d->dtype == RNN_BF16 ? gated_launch<__nv_bfloat16>(d->function, true, a, st)
-                                        : gated_launch<float>(d->function, true, a, st));
+  a.dcarry = (float*)((char*)workspace + z.sync + z.maps);
+  a.dbp = db ? (float*)((char*)workspace + z.sync + z.maps + z.carry) : nullptr;
+  rc = cuda_status(gated_launch(d, q8, true, a, st));
   if (rc || !db) return rc;
   const int cols = z.G * z.C;
   if (d->dtype == RNN_BF16)
-    gated_db_kernel<<<(cols + 31) / 32, 256, 0, st>>>(a.dbp, (__nv_bfloat16*)db, d->B, cols);
+    gated_db_kernel<<<(cols + 31) / 32, 256, 0, st>>>(a.dbp, (__nv_bfloat16*)db, d->B * z.chunks, cols);
   else
-    gated_db_kernel<<<(cols + 31) / 32, 256, 0, st>>>(a.dbp, (float*)db, d->B, cols);
+    gated_db_kernel<<<(cols + 31) / 32, 256, 0, st>>>(a.dbp, (float*)db, d->B * z.chunks, cols);
   note_launch();
   return cuda_status(cudaGetLastError());
 }

@@ -131,9 +131,4 @@ __device__ __forceinline__ float act_inv_scale(unsigned byte) {
 }
 __device__ __forceinline__ int act_quant(float x, float inv) { return max(-127, min(127, __float2int_rn(x * inv))); }
 
-// Packs x [batch][rows][cols] into q and scales [batch][ceil(rows / 32)][cols];
-// rows at and past lengths[batch] (when given) count as zeros.
-cudaError_t act_pack_run(int dtype, int batch, long long rows, int cols, const int* lengths, const void* x,
-                         signed char* q, unsigned char* scales, cudaStream_t st);
-
 }  // namespace rnn

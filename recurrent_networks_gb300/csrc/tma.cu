@@ -66,7 +66,7 @@ cudaError_t encode_tensor_map(void* map, const void* base, int elem_bytes, int r
 cudaError_t encode_tensor_map_swizzled(void* map, const void* base, int elem_bytes, int rank,
                                        const unsigned long long* dims, const unsigned int* box, int swizzle_bytes) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (!fn || rank < 1 || rank > 5 || (elem_bytes != 2 && elem_bytes != 4)) return cudaErrorNotSupported;
+  if (!fn || rank < 1 || rank > 5 || (elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4)) return cudaErrorNotSupported;
   cuuint64_t gdim[5], gstride[4];
   cuuint32_t bdim[5], estr[5];
   unsigned long long stride = (unsigned long long)elem_bytes;  // bytes
@@ -78,7 +78,9 @@ cudaError_t encode_tensor_map_swizzled(void* map, const void* base, int elem_byt
     stride *= dims[d];
   }
   const CUtensorMapDataType ty =
-      elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+      elem_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+      : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   const CUtensorMapSwizzle sw = swizzle_bytes == 64    ? CU_TENSOR_MAP_SWIZZLE_64B
                                 : swizzle_bytes == 32  ? CU_TENSOR_MAP_SWIZZLE_32B
                                 : swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
