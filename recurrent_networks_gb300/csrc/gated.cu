@@ -29,6 +29,7 @@ struct GatedArgs {
   int tiles_c;          // channel tiles per batch row
   int span;             // chunks per group
   int tma;              // rows are 16-byte multiples: tiles come by TMA
+  int solo;  // one chunk, all CTAs at once: no waits, so block 0 clears the status word itself
   const void* Wx;
   const void* bias;
   const float* s0;
@@ -114,6 +115,7 @@ struct Item {
 };
 template <int N, bool REVERSE> __device__ __forceinline__ Item item_of(const GatedArgs& p, unsigned* shared) {
   unsigned id = blockIdx.x;
+  if (p.solo && id == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
   if (p.chunks > 1) {
     if (threadIdx.x == 0) *shared = atomicAdd(p.ticket, 1u);
     __syncthreads();
@@ -677,7 +679,7 @@ bool gated_dims_ok(const rnn_gated_dims_t* d) {
 }
 
 struct GatedSizes {
-  int G, C, chunks, qblocks, tiles_c, span;
+  int G, C, chunks, qblocks, tiles_c, span, solo;
   size_t esize, carry, q, qs, tape;
   size_t sync, maps, dbp;  // workspace: status, ticket and flags (zeroed by every call) | maps | states | db sums
 };
@@ -696,6 +698,9 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   const size_t resident = 2 * (size_t)device_sms();
   z.span = tiles >= resident ? 1 : (int)((2 * resident + tiles - 1) / tiles);
   if (z.span > MAX_SPAN) z.span = MAX_SPAN;
+  // A short sequence is all latency: without TMA there is no wait that could
+  // run out, and the clearing launch for the status word falls away.
+  z.solo = z.chunks == 1 && tiles <= resident;
   const size_t states = up256((size_t)d->B * z.chunks * z.C * sizeof(float));
   z.carry = states;
   const bool q8 = d->checkpoint == RNN_CKPT_INT8;
@@ -720,7 +725,7 @@ template <typename T, int FN, bool Q8> cudaError_t gated_launch(bool bwd, GatedA
   constexpr int G = gated_gates(FN), width = 32 * Lane<T>::N;
   const int xelem = bwd && Q8 ? 1 : (int)sizeof(T);
   // TMA rows start on 16 bytes
-  a.tma = ((size_t)a.C * xelem) % 16 == 0 && ((size_t)a.C * sizeof(T)) % 16 == 0;
+  a.tma = !a.solo && ((size_t)a.C * xelem) % 16 == 0 && ((size_t)a.C * sizeof(T)) % 16 == 0;
   CUtensorMap x = {}, d = {};
   if (a.tma) {
     cudaError_t e = tile_map(&x, bwd && Q8 ? (const void*)a.q : a.Wx, xelem, a, G, width);
@@ -751,7 +756,7 @@ cudaError_t gated_launch(const rnn_gated_dims_t* d, bool q8, bool bwd, const Gat
 GatedArgs gated_args(const rnn_gated_dims_t* d, const GatedSizes& z, void* workspace) {
   GatedArgs a{};
   a.B = d->B; a.T = d->T; a.C = z.C; a.chunks = z.chunks;
-  a.tiles_c = z.tiles_c; a.span = z.span;
+  a.tiles_c = z.tiles_c; a.span = z.span; a.solo = z.solo;
   char* ws = (char*)workspace;
   a.status = (unsigned*)ws;
   a.ticket = (unsigned*)(ws + 256);
@@ -791,7 +796,7 @@ int rnn_gated_fwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
   if (ws_bytes < rnn_gated_workspace_size(d, RNN_WS_FWD)) return RNN_ENOSPC;
   cudaStream_t st = (cudaStream_t)stream;
   const GatedSizes z = gated_sizes(d);
-  int rc = cuda_status(cudaMemsetAsync(workspace, 0, z.sync, st));
+  int rc = z.solo ? RNN_OK : cuda_status(cudaMemsetAsync(workspace, 0, z.sync, st));
   if (rc) return rc;
   if (d->T == 0) {
     const size_t bytes = (size_t)d->B * z.C * sizeof(float);
@@ -824,7 +829,7 @@ int rnn_gated_bwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
   if (ws_bytes < rnn_gated_workspace_size(d, RNN_WS_BWD)) return RNN_ENOSPC;
   cudaStream_t st = (cudaStream_t)stream;
   const GatedSizes z = gated_sizes(d);
-  int rc = cuda_status(cudaMemsetAsync(workspace, 0, z.sync, st));
+  int rc = z.solo ? RNN_OK : cuda_status(cudaMemsetAsync(workspace, 0, z.sync, st));
   if (rc) return rc;
   if (d->T == 0) {
     const size_t bytes = (size_t)d->B * z.C * sizeof(float);

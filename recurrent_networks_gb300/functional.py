@@ -151,11 +151,6 @@ def flashrnn_stack(x, layers, function: str = "lstm", backend: str = "auto"):
 
 
 # ---- gated linear scan ------------------------------------------------------------
-def _need(ok, text, kind=ValueError):
-    if not ok:
-        raise kind(text)
-
-
 def _dense(t):
     """t (or None) as the library takes it: contiguous and 16-byte aligned."""
     if t is None:
@@ -168,48 +163,62 @@ class _GatedFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Wx, b, state, function, reset, lengths, checkpoint):
         B, T, _, N, D = Wx.shape
+        dtype, dev = Wx.dtype, Wx.device
         Wx, b, state = _dense(Wx), _dense(b), _dense(state)
-        dims = _lib.make_gated_dims(B, T, N, D, function, Wx.dtype, checkpoint)
-        h = torch.empty((B, T, N, D), dtype=Wx.dtype, device=Wx.device)
-        last = torch.empty((B, 1, N, D), dtype=torch.float32, device=Wx.device)
+        dims = _lib.make_gated_dims(B, T, N, D, function, dtype, checkpoint)
+        h = torch.empty((B, T, N, D), dtype=dtype, device=dev)
+        last = torch.empty((B, 1, N, D), dtype=torch.float32, device=dev)
+        need = ctx.needs_input_grad
         tape = None
-        if any(ctx.needs_input_grad[:3]):
-            tape = torch.empty(_lib.rnn_gated_tape_size(dims), dtype=torch.uint8, device=Wx.device)
-        ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_FWD), dtype=torch.uint8, device=Wx.device)
+        if need[0] or need[1] or need[2]:
+            tape = torch.empty(_lib.rnn_gated_tape_size(dims), dtype=torch.uint8, device=dev)
+        ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_FWD), dtype=torch.uint8, device=dev)
         _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, ws)
-        ctx.dims, ctx.wx_shape = dims, Wx.shape
-        ctx.has_state = state is not None
-        ctx.set_materialize_grads(False)
-        ctx.save_for_backward(Wx if checkpoint is None else None, b, reset, lengths, tape)
+        if tape is not None:
+            ctx.dims, ctx.wx_shape, ctx.dtype = dims, Wx.shape, dtype
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(Wx if checkpoint is None else None, b, reset, lengths, tape)
         return h, last
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dh, dlast):
-        Wx, b, reset, lengths, tape = ctx.saved_tensors
-        dims, dev = ctx.dims, tape.device
-        dt = torch.bfloat16 if dims.dtype == _lib.DTYPES[torch.bfloat16] else torch.float32
-        B, _, G, N, D = ctx.wx_shape
-        need = ctx.needs_input_grad
-        dWx = torch.empty(ctx.wx_shape, dtype=dt, device=dev) if need[0] else None
-        db = torch.empty((G, N, D), dtype=dt, device=dev) if b is not None and need[1] else None
-        ds = torch.empty((B, 1, N, D), dtype=torch.float32, device=dev) if ctx.has_state and need[2] else None
-        ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_BWD), dtype=torch.uint8, device=dev)
-        _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, ws)
-        return dWx, db, ds, None, None, None, None
+        return (_gated_bwd_once if torch.is_grad_enabled() else _gated_bwd)(ctx, dh, dlast)
+
+
+def _gated_bwd(ctx, dh, dlast):
+    Wx, b, reset, lengths, tape = ctx.saved_tensors
+    dims, dev = ctx.dims, tape.device
+    B, _, G, N, D = ctx.wx_shape
+    need = ctx.needs_input_grad
+    dWx = torch.empty(ctx.wx_shape, dtype=ctx.dtype, device=dev) if need[0] else None
+    db = torch.empty((G, N, D), dtype=ctx.dtype, device=dev) if need[1] else None
+    ds = torch.empty((B, 1, N, D), dtype=torch.float32, device=dev) if need[2] else None
+    ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_BWD), dtype=torch.uint8, device=dev)
+    _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, ws)
+    return dWx, db, ds, None, None, None, None
+
+
+_gated_bwd_once = once_differentiable(_gated_bwd)
 
 
 def _gated_shapes(Wx, b, function, lead):
-    _need(function in _lib.GATED_FUNCTIONS, f"function must be one of {list(_lib.GATED_FUNCTIONS)}, got {function!r}")
-    _need(Wx.dtype in _lib.DTYPES, f"unsupported dtype {Wx.dtype}", TypeError)
-    _need(Wx.dim() == lead + 3, f"Wx must have {lead + 3} dimensions, got shape {tuple(Wx.shape)}")
+    if function not in _lib.GATED_FUNCTIONS:
+        raise ValueError(f"function must be one of {list(_lib.GATED_FUNCTIONS)}, got {function!r}")
+    if Wx.dtype not in _lib.DTYPES:
+        raise TypeError(f"unsupported dtype {Wx.dtype}")
+    if Wx.dim() != lead + 3:
+        raise ValueError(f"Wx must have {lead + 3} dimensions, got shape {tuple(Wx.shape)}")
     G, N, D = Wx.shape[lead:]
     want = 4 if function == "linear" else 2
-    _need(G == want, f"{function} needs G={want} gates, Wx has {G}")
+    if G != want:
+        raise ValueError(f"{function} needs G={want} gates, Wx has {G}")
     if b is not None:
-        _need(tuple(b.shape) == (G, N, D), f"b must be [G,N,D]={(G, N, D)}, got {tuple(b.shape)}")
-        _need(b.dtype == Wx.dtype, f"b is {b.dtype}, Wx is {Wx.dtype}", TypeError)
-        _need(b.device == Wx.device, "b must be on Wx's device")
+        if b.shape != (G, N, D):
+            raise ValueError(f"b must be [G,N,D]={(G, N, D)}, got {tuple(b.shape)}")
+        if b.dtype != Wx.dtype:
+            raise TypeError(f"b is {b.dtype}, Wx is {Wx.dtype}")
+        if b.device != Wx.device:
+            raise ValueError("b must be on Wx's device")
     return N, D
 
 
@@ -231,21 +240,32 @@ def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, len
         raise RuntimeError("gated_scan runs on CUDA tensors only (there is no CPU path)")
     N, D = _gated_shapes(Wx, b, function, 2)
     B, T = Wx.shape[:2]
-    _need(checkpoint in _lib.CHECKPOINTS, f"checkpoint must be one of {list(_lib.CHECKPOINTS)}, got {checkpoint!r}")
+    if checkpoint not in _lib.CHECKPOINTS:
+        raise ValueError(f"checkpoint must be one of {list(_lib.CHECKPOINTS)}, got {checkpoint!r}")
     if state is not None:
-        _need(tuple(state.shape) == (B, 1, N, D), f"state must be [B,1,N,D]={(B, 1, N, D)}, got {tuple(state.shape)}")
-        _need(state.device == Wx.device, "state must be on Wx's device")
+        if state.shape != (B, 1, N, D):
+            raise ValueError(f"state must be [B,1,N,D]={(B, 1, N, D)}, got {tuple(state.shape)}")
+        if state.device != Wx.device:
+            raise ValueError("state must be on Wx's device")
         state = state.float()
     if reset is not None:
-        _need(tuple(reset.shape) == (B, T), f"reset must be [B,T]={(B, T)}, got {tuple(reset.shape)}")
-        _need(reset.dtype in (torch.bool, torch.uint8), f"reset must be bool or uint8, got {reset.dtype}", TypeError)
-        _need(reset.device == Wx.device, "reset must be on Wx's device")
+        if reset.shape != (B, T):
+            raise ValueError(f"reset must be [B,T]={(B, T)}, got {tuple(reset.shape)}")
+        if reset.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"reset must be bool or uint8, got {reset.dtype}")
+        if reset.device != Wx.device:
+            raise ValueError("reset must be on Wx's device")
         reset = reset.contiguous()
     if lengths is not None:
-        _need(tuple(lengths.shape) == (B,), f"lengths must be [B]={(B,)}, got {tuple(lengths.shape)}")
-        _need(lengths.dtype in (torch.int32, torch.int64), f"lengths must be integers, got {lengths.dtype}", TypeError)
-        _need(lengths.device == Wx.device, "lengths must be on Wx's device")
-        lengths = lengths.clamp(0, T).to(torch.int32).contiguous() if lengths.dtype == torch.int64 else lengths.contiguous()
+        if lengths.shape != (B,):
+            raise ValueError(f"lengths must be [B]={(B,)}, got {tuple(lengths.shape)}")
+        if lengths.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"lengths must be integers, got {lengths.dtype}")
+        if lengths.device != Wx.device:
+            raise ValueError("lengths must be on Wx's device")
+        if lengths.dtype == torch.int64:
+            lengths = lengths.clamp(0, T).to(torch.int32)
+        lengths = lengths.contiguous()
     if not torch.is_grad_enabled():  # nothing is kept for a backward
         Wx, b, state = (v if v is None else v.detach() for v in (Wx, b, state))
     return _GatedFn.apply(Wx, b, state, function, reset, lengths, checkpoint)
@@ -264,22 +284,23 @@ def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=
         raise RuntimeError("gated_scan_step runs on CUDA tensors only (there is no CPU path)")
     N, D = _gated_shapes(Wx, b, function, 1)
     M = Wx.shape[0]
-    pool_out = pool if pool_out is None else pool_out
-    for p in (pool, pool_out):
-        _need(p.dtype == torch.float32, f"the pool must be float32, got {p.dtype}", TypeError)
-        _need(p.dim() == 3 and tuple(p.shape[1:]) == (N, D) and p.shape == pool.shape,
-              f"the pool must be [P,N,D]=[P,{N},{D}], got {tuple(p.shape)}")
-        _need(p.is_contiguous() and p.data_ptr() % 16 == 0 and p.device == Wx.device,
-              "the pool must be contiguous, 16-byte aligned and on Wx's device")
+    for p in (pool,) if pool_out is None else (pool, pool_out):
+        if p.dtype != torch.float32:
+            raise TypeError(f"the pool must be float32, got {p.dtype}")
+        if p.dim() != 3 or p.shape != (pool.shape[0], N, D):
+            raise ValueError(f"the pool must be [P,N,D]=[P,{N},{D}], got {tuple(p.shape)}")
+        if not (p.is_contiguous() and p.data_ptr() % 16 == 0 and p.device == Wx.device):
+            raise ValueError("the pool must be contiguous, 16-byte aligned and on Wx's device")
     if slots is None:
-        _need(M <= pool.shape[0], f"{M} rows need as many slots, the pool has {pool.shape[0]}")
+        if M > pool.shape[0]:
+            raise ValueError(f"{M} rows need as many slots, the pool has {pool.shape[0]}")
     else:
-        _need(tuple(slots.shape) == (M,) and slots.dtype == torch.int32 and slots.device == Wx.device,
-              f"slots must be [M]=[{M}] int32 on Wx's device")
+        if slots.shape != (M,) or slots.dtype != torch.int32 or slots.device != Wx.device:
+            raise ValueError(f"slots must be [M]=[{M}] int32 on Wx's device")
         slots = slots.contiguous()
     h = torch.empty((M, N, D), dtype=Wx.dtype, device=Wx.device)
-    _lib.rnn_gated_step(M, pool.shape[0], N, D, function, Wx.dtype, _dense(Wx), _dense(b), slots, pool, pool_out, h,
-                        status)
+    _lib.rnn_gated_step(M, pool.shape[0], N, D, function, Wx.dtype, _dense(Wx), _dense(b), slots, pool,
+                        pool if pool_out is None else pool_out, h, status)
     return h
 
 
@@ -299,8 +320,10 @@ def checkpoint_pack(x):
     block's largest magnitude. Blocks with an infinity or a NaN unpack to NaN."""
     if not x.is_cuda:
         raise RuntimeError("checkpoint_pack runs on CUDA tensors only (there is no CPU path)")
-    _need(x.dtype in _lib.DTYPES, f"unsupported dtype {x.dtype}", TypeError)
-    _need(x.dim() >= 1 and x.shape[-1] >= 1, f"x must have a last axis, got shape {tuple(x.shape)}")
+    if x.dtype not in _lib.DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if not (x.dim() >= 1 and x.shape[-1] >= 1):
+        raise ValueError(f"x must have a last axis, got shape {tuple(x.shape)}")
     q, scales = _pack(_dense(x.detach().reshape(-1, x.shape[-1])))
     return q.reshape(x.shape), scales
 
@@ -309,13 +332,16 @@ def checkpoint_unpack(q, scales, dtype=torch.bfloat16):
     """The values (exact in either dtype) that checkpoint_pack's q and scales stand for."""
     if not q.is_cuda:
         raise RuntimeError("checkpoint_unpack runs on CUDA tensors only (there is no CPU path)")
-    _need(dtype in _lib.DTYPES, f"unsupported dtype {dtype}", TypeError)
-    _need(q.dtype == torch.int8 and scales.dtype == torch.uint8, "q must be int8 and scales uint8", TypeError)
-    _need(q.dim() >= 1 and q.shape[-1] >= 1, f"q must have a last axis, got shape {tuple(q.shape)}")
+    if dtype not in _lib.DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if not (q.dtype == torch.int8 and scales.dtype == torch.uint8):
+        raise TypeError("q must be int8 and scales uint8")
+    if not (q.dim() >= 1 and q.shape[-1] >= 1):
+        raise ValueError(f"q must have a last axis, got shape {tuple(q.shape)}")
     cols = q.shape[-1]
     rows = q.numel() // cols
-    _need(tuple(scales.shape) == (-(-rows // _lib.ACT_BLOCK), cols) and scales.device == q.device,
-          f"scales must be [{-(-rows // _lib.ACT_BLOCK)},{cols}] on q's device, got {tuple(scales.shape)}")
+    if not (tuple(scales.shape) == (-(-rows // _lib.ACT_BLOCK), cols) and scales.device == q.device):
+        raise ValueError(f"scales must be [{-(-rows // _lib.ACT_BLOCK)},{cols}] on q's device, got {tuple(scales.shape)}")
     x = torch.empty(q.shape, dtype=dtype, device=q.device)
     _lib.rnn_act_unpack(rows, cols, _dense(q), _dense(scales), x)
     return x
@@ -326,22 +352,28 @@ class _EmbedFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, W, scale, padding_idx, status):
         W = _dense(W)
-        out = torch.empty((ids.numel(), W.shape[1]), dtype=W.dtype, device=W.device)
+        out = torch.empty((*ids.shape, W.shape[1]), dtype=W.dtype, device=W.device)
         _lib.rnn_embed_fwd(ids.numel(), W.shape[0], W.shape[1], ids, W, scale, out, status)
         ctx.save_for_backward(ids)
         ctx.args = (W.shape, W.dtype, scale, padding_idx)
         return out
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dout):
-        (ids,) = ctx.saved_tensors
-        (V, E), dtype, scale, pad = ctx.args
-        n = ids.numel()
-        dW = torch.empty((V, E), dtype=dtype, device=ids.device)
-        ws = torch.empty(_lib.rnn_embed_bwd_workspace_size(n, V, E), dtype=torch.uint8, device=ids.device)
-        _lib.rnn_embed_bwd(n, V, E, ids, pad, _dense(dout), scale, dW, ws)
-        return None, dW, None, None, None
+        return (_embed_bwd_once if torch.is_grad_enabled() else _embed_bwd)(ctx, dout)
+
+
+def _embed_bwd(ctx, dout):
+    (ids,) = ctx.saved_tensors
+    (V, E), dtype, scale, pad = ctx.args
+    n = ids.numel()
+    dW = torch.empty((V, E), dtype=dtype, device=ids.device)
+    ws = torch.empty(_lib.rnn_embed_bwd_workspace_size(n, V, E), dtype=torch.uint8, device=ids.device)
+    _lib.rnn_embed_bwd(n, V, E, ids, pad, _dense(dout), scale, dW, ws)
+    return None, dW, None, None, None
+
+
+_embed_bwd_once = once_differentiable(_embed_bwd)
 
 
 def embedding(ids, weight, scale: float = 1.0, padding_idx=None, status=None):
@@ -353,12 +385,15 @@ def embedding(ids, weight, scale: float = 1.0, padding_idx=None, status=None):
     they are recorded (_lib.rnn_check_status(status) raises for it)."""
     if not weight.is_cuda:
         raise RuntimeError("embedding runs on CUDA tensors only (there is no CPU path)")
-    _need(weight.dim() == 2, f"weight must be [V,E], got shape {tuple(weight.shape)}")
-    _need(weight.dtype in _lib.DTYPES, f"unsupported dtype {weight.dtype}", TypeError)
-    _need(ids.dtype in (torch.int32, torch.int64), f"ids must be int32 or int64, got {ids.dtype}", TypeError)
-    _need(ids.device == weight.device, "ids must be on weight's device")
-    _need(padding_idx is None or 0 <= padding_idx < weight.shape[0],
-          f"padding_idx must be None or in 0 .. {weight.shape[0] - 1}, got {padding_idx}")
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [V,E], got shape {tuple(weight.shape)}")
+    if weight.dtype not in _lib.DTYPES:
+        raise TypeError(f"unsupported dtype {weight.dtype}")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
+    if ids.device != weight.device:
+        raise ValueError("ids must be on weight's device")
+    if not (padding_idx is None or 0 <= padding_idx < weight.shape[0]):
+        raise ValueError(f"padding_idx must be None or in 0 .. {weight.shape[0] - 1}, got {padding_idx}")
     pad = -1 if padding_idx is None else int(padding_idx)
-    out = _EmbedFn.apply(ids.reshape(-1).contiguous(), weight, float(scale), pad, status)
-    return out.reshape(*ids.shape, weight.shape[1])
+    return _EmbedFn.apply(ids.contiguous(), weight, float(scale), pad, status)
