@@ -59,6 +59,18 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T) {
 
 // f x + u, with x dropped where f is 0 (a reset): 0 times an infinite x is not NaN.
 __device__ __forceinline__ float affine(float f, float x, float u) { return f == 0.0f ? u : fmaf(f, x, u); }
+template <int N> __device__ __forceinline__ FV<N> affine(const FV<N>& f, const FV<N>& x, const FV<N>& u) {
+  FV<N> r;
+#pragma unroll
+  for (int v = 0; v < N; ++v) r.v[v] = affine(f.v[v], x.v[v], u.v[v]);
+  return r;
+}
+template <int N> __device__ __forceinline__ FV<N> select(bool on, const FV<N>& a, const FV<N>& b) {
+  FV<N> r;
+#pragma unroll
+  for (int v = 0; v < N; ++v) r.v[v] = on ? a.v[v] : b.v[v];
+  return r;
+}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
                                             int c3) {
@@ -68,25 +80,35 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"((uint64_t)map),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
 
 // The channels of a lane: 4 bytes of the storage type.
 template <typename T> struct Lane;
 template <> struct Lane<float> {
   static constexpr int N = 1;
-  __device__ static void unpack(uint32_t v, float* x) { x[0] = __uint_as_float(v); }
-  __device__ static uint32_t pack(const float* x) { return __float_as_uint(x[0]); }
+  __device__ static FV<1> unpack(uint32_t v) { return {{__uint_as_float(v)}}; }
+  __device__ static uint32_t pack(const FV<1>& x) { return __float_as_uint(x.v[0]); }
 };
 template <> struct Lane<__nv_bfloat16> {
   static constexpr int N = 2;
-  __device__ static void unpack(uint32_t v, float* x) {
-    x[0] = __uint_as_float(v << 16);
-    x[1] = __uint_as_float(v & 0xffff0000u);
-  }
-  __device__ static uint32_t pack(const float* x) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[0], x[1]);
+  __device__ static FV<2> unpack(uint32_t v) { return {{__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)}}; }
+  __device__ static uint32_t pack(const FV<2>& x) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.v[0], x.v[1]);
     return *(const uint32_t*)&h;
   }
 };
+// N signed bytes as fp32, without the conversion unit: a byte plus 128 in the
+// low bits of 2^23 is 2^23 + 128 + q.
+__device__ __forceinline__ FV<2> bytes_f(uint32_t w, FV<2>*) {
+  w ^= 0x8080u;
+  const FV<2> m = {{__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650)), __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7651))}};
+  return add(m, splat<2>(-8388736.0f));
+}
+__device__ __forceinline__ FV<1> bytes_f(uint32_t w, FV<1>*) { return {{(float)(signed char)w}}; }
 
 // A lane's channels at p (n of them inside the row: 0 .. N), and back. `wide`:
 // the row starts on 4 bytes.
@@ -110,8 +132,10 @@ template <typename T> __device__ __forceinline__ void store_lane(T* p, uint32_t 
 // The item of this CTA and where it lies.
 struct Item {
   int k, tile, b, ch, n, t0, len;  // ch: the lane's first channel, n: how many of its channels exist; t0: the warp's first step
+  int ct;                          // the tile's first channel
   int live;                        // the warp's steps that exist
   unsigned rst;                    // bit j: reset at the warp's step j
+  bool plain;                      // every step exists, none is a reset
 };
 template <int N, bool REVERSE> __device__ __forceinline__ Item item_of(const GatedArgs& p, unsigned* shared) {
   unsigned id = blockIdx.x;
@@ -128,7 +152,8 @@ template <int N, bool REVERSE> __device__ __forceinline__ Item item_of(const Gat
   it.tile = (int)(id % tiles);
   it.b = it.tile / p.tiles_c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  it.ch = (it.tile % p.tiles_c) * 32 * N + lane * N;
+  it.ct = (it.tile % p.tiles_c) * 32 * N;
+  it.ch = it.ct + lane * N;
   it.n = min(max(p.C - it.ch, 0), N);
   it.t0 = it.k * GATED_CHUNK + warp * STEPS;
   it.len = clamp_len(p.lengths, it.b, p.T);
@@ -136,75 +161,96 @@ template <int N, bool REVERSE> __device__ __forceinline__ Item item_of(const Gat
   bool r = false;
   if (p.reset && lane < it.live) r = p.reset[(size_t)it.b * p.T + it.t0 + lane] != 0;
   it.rst = __ballot_sync(0xffffffffu, r);
+  it.plain = it.live == STEPS && it.rst == 0;
   return it;
 }
 
 // A lane's fp32 values at channel it.ch of row r of a [rows][C] array.
-template <int N, bool L2> __device__ __forceinline__ void load_f(const float* a, size_t r, const GatedArgs& p, const Item& it, float* x) {
+template <int N, bool L2> __device__ __forceinline__ FV<N> load_f(const float* a, size_t r, const GatedArgs& p, const Item& it) {
+  FV<N> x;
 #pragma unroll
   for (int v = 0; v < N; ++v) {
     const float* q = a + r * p.C + it.ch + v;
-    x[v] = v < it.n ? (L2 ? __ldcg(q) : __ldg(q)) : 0.0f;
+    x.v[v] = v < it.n ? (L2 ? __ldcg(q) : __ldg(q)) : 0.0f;
   }
+  return x;
 }
-template <int N> __device__ __forceinline__ void store_f(float* a, size_t r, const GatedArgs& p, const Item& it, const float* x) {
+template <int N> __device__ __forceinline__ void store_f(float* a, size_t r, const GatedArgs& p, const Item& it, const FV<N>& x) {
 #pragma unroll
   for (int v = 0; v < N; ++v)
-    if (v < it.n) a[r * p.C + it.ch + v] = x[v];
+    if (v < it.n) a[r * p.C + it.ch + v] = x.v[v];
 }
 
-// Warp 0: the state that enters the chunk (x in: the state before the first
-// chunk in processing order), given the chunk's own map (P, H). Publishes
-// what later chunks need. `order` is the chunk's place in processing order,
-// REVERSE: chunk index descends. `states` [B][chunks][C] holds the state
-// that enters a chunk.
-template <int N, bool REVERSE>
-__device__ __forceinline__ void chain(const GatedArgs& p, const Item& it, float* states, const float* P, const float* H, float* x) {
-  const int lane = threadIdx.x & 31;
-  const int o = REVERSE ? p.chunks - 1 - it.k : it.k;
-  const int first = o - o % p.span;
-  const bool ends = (o + 1) % p.span == 0, final = o + 1 == p.chunks;
-  const unsigned tiles = (unsigned)p.B * p.tiles_c;
-  auto chunk_of = [&](int order) { return REVERSE ? p.chunks - 1 - order : order; };
-  auto row_of = [&](int order) { return (size_t)it.b * p.chunks + chunk_of(order); };
-  auto raise = [&]() {
-    __syncwarp();
-    if (lane == 0)  // a release at gpu scope is cumulative: it covers the warp's stores before the barrier
-      asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(p.flags + (size_t)o * tiles + it.tile) : "memory");
-  };
-  if (!ends && !final) {
-    store_f<N>(p.maps, row_of(o) * 2, p, it, P);
-    store_f<N>(p.maps, row_of(o) * 2 + 1, p, it, H);
-    raise();
+// How warp 0 passes the state through the chunks of a tile. `states`
+// [B][chunks][C] holds the state that enters a chunk; REVERSE: the processing
+// order descends. The state that enters this chunk is `x` (in: the state
+// before the first chunk in processing order).
+template <int N, bool REVERSE> struct Chain {
+  const GatedArgs& p;
+  const Item& it;
+  float* states;
+  int o, first;  // this chunk's and its group's first chunk's place in processing order
+  bool ends, final, ready;
+  __device__ __forceinline__ Chain(const GatedArgs& p, const Item& it, float* states) : p(p), it(it), states(states) {
+    o = REVERSE ? p.chunks - 1 - it.k : it.k;
+    first = o - o % p.span;
+    ends = (o + 1) % p.span == 0;
+    final = o + 1 == p.chunks;
+    ready = o == 0;
   }
-  if (o > 0) {
-    // lane i waits for the chunk `first - 1 + i`
-    const int from = first > 0 ? first - 1 : 0;
-    bool failed = false;
-    for (int w = from + lane; w < o; w += 32)
-      counter_wait_bounded(p.flags + (size_t)w * tiles + it.tile, 1u, p.wait_limit_ns, p.status, failed);
+  __device__ __forceinline__ unsigned* flag(int order) const {
+    return p.flags + (size_t)order * ((unsigned)p.B * p.tiles_c) + it.tile;
+  }
+  __device__ __forceinline__ size_t row(int order) const {
+    return (size_t)it.b * p.chunks + (REVERSE ? p.chunks - 1 - order : order);
+  }
+  __device__ __forceinline__ void raise() const {
     __syncwarp();
-    if (first > 0) load_f<N, true>(states, row_of(first), p, it, x);
+    if ((threadIdx.x & 31) == 0)  // a release at gpu scope is cumulative: it covers the warp's stores before the barrier
+      asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flag(o)) : "memory");
+  }
+  // the state after the group before, through the group's chunks before this one
+  __device__ __forceinline__ void take(FV<N>& x) const {
+    if (first > 0) x = load_f<N, true>(states, row(first), p, it);
 #pragma unroll 4
-    for (int w = first; w < o; ++w) {
-      float mp[N], mh[N];
-      load_f<N, true>(p.maps, row_of(w) * 2, p, it, mp);
-      load_f<N, true>(p.maps, row_of(w) * 2 + 1, p, it, mh);
-#pragma unroll
-      for (int v = 0; v < N; ++v) x[v] = affine(mp[v], x[v], mh[v]);
+    for (int w = first; w < o; ++w)
+      x = affine(load_f<N, true>(p.maps, row(w) * 2, p, it), x, load_f<N, true>(p.maps, row(w) * 2 + 1, p, it));
+  }
+  // At the start: where everything needed is published already (the usual
+  // case with many tiles), the round trips run beside the tile's load.
+  __device__ __forceinline__ void probe(FV<N>& x) {
+    if (ready) return;
+    bool up = true;
+    for (int w = (first > 0 ? first - 1 : 0) + (threadIdx.x & 31); w < o; w += 32) up &= ld_acquire_gpu(flag(w)) != 0;
+    ready = __all_sync(0xffffffffu, up);
+    if (!ready) return;
+    __syncwarp();  // the lanes' acquires, for all of them
+    take(x);
+  }
+  // With the chunk's own map (P, H): publishes what later chunks need, and
+  // waits for x where the probe found it missing.
+  __device__ __forceinline__ void pass(const FV<N>& P, const FV<N>& H, FV<N>& x) {
+    if (!ends && !final) {
+      store_f<N>(p.maps, row(o) * 2, p, it, P);
+      store_f<N>(p.maps, row(o) * 2 + 1, p, it, H);
+      raise();
+    }
+    if (!ready) {
+      bool failed = false;
+      for (int w = (first > 0 ? first - 1 : 0) + (threadIdx.x & 31); w < o; w += 32)
+        counter_wait_bounded(flag(w), 1u, p.wait_limit_ns, p.status, failed);
+      __syncwarp();
+      take(x);
+    }
+    if (ends && !final) {
+      store_f<N>(states, row(o + 1), p, it, affine(P, x, H));
+      raise();
     }
   }
-  if (ends && !final) {
-    float y[N];
-#pragma unroll
-    for (int v = 0; v < N; ++v) y[v] = affine(P[v], x[v], H[v]);
-    store_f<N>(states, row_of(o + 1), p, it, y);
-    raise();
-  }
-}
+};
 
-// A warp's steps of a tile whose rows (t, g) are 128 bytes: one TMA box per
-// warp, or the lanes' own loads. Rows past `live` are not read.
+// A warp's steps of a tile whose rows (t, g) are 128 bytes, by the lanes' own
+// loads (rows that TMA cannot take). Rows past `live` are not read.
 template <typename T, int ROWS>
 __device__ __forceinline__ void fetch_lanes(const GatedArgs& p, const Item& it, const T* src, uint32_t* dst) {
   const int lane = threadIdx.x & 31;
@@ -214,15 +260,40 @@ __device__ __forceinline__ void fetch_lanes(const GatedArgs& p, const Item& it, 
   for (int r = 0; r < it.live * ROWS; ++r) dst[r * 32 + lane] = load_lane(at + (size_t)r * p.C, it.n, wide);
 }
 
+// A lane's biases, scaled as the gates want them.
+template <typename T, int FN, int N> __device__ __forceinline__ void load_bias(const GatedArgs& p, const Item& it, FV<N>* bias) {
+  constexpr int G = gated_gates(FN);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    bias[g] = Lane<T>::unpack(p.bias ? load_lane((const T*)p.bias + (size_t)g * p.C + it.ch, it.n, p.C % 2 == 0) : 0);
+    bias[g] = mul(bias[g], splat<N>(mul_of<FN, N>(g)));
+  }
+}
+// raw pre-activation -> gate value (see mul_of)
+template <int FN, int N> __device__ __forceinline__ FV<N> gate(int g, const FV<N>& a, const FV<N>& bias) {
+  return mul_of<FN, N>(g) == 1.0f ? add(a, bias) : fma(a, splat<N>(mul_of<FN, N>(g)), bias);
+}
+
+template <bool V> struct Flag { static constexpr bool value = V; };
+// Steps whose warp has all of them and no reset run without a test per step.
+template <typename F> __device__ __forceinline__ void by_mask(const Item& it, F&& f) {
+  if (it.plain) f(Flag<false>());
+  else f(Flag<true>());
+}
+
+// Blocks per SM: the tile is 64 KB (linear) or 32 KB (coupled). Without the
+// 8-bit copy u waits in the tile's place of i and g (coupled: f and g), which
+// are not read again, so that f alone stays in registers.
 template <typename T, int FN, bool Q8>
-__global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const __grid_constant__ CUtensorMap xmap, GatedArgs p) {
+__global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
+    gated_fwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap hmap, GatedArgs p) {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
-  constexpr bool FAST = sizeof(T) == 2;
+  constexpr int U0 = FN == GATED_LINEAR ? 0 : 1, U1 = FN == GATED_LINEAR ? 2 : 0;  // rows that hold u of channel 0, 1
   extern __shared__ __align__(128) unsigned char smem[];
   uint32_t* tile = (uint32_t*)smem;                                   // [WARPS][STEPS][G][32]
-  float2* maps = (float2*)(tile + WARPS * STEPS * G * 32);            // [WARPS][32 N]
-  float* enter = (float*)(maps + WARPS * 32 * N);                     // [32 N]
-  uint32_t* tops = (uint32_t*)(enter + 32 * N);                       // Q8: [WARPS][G][32 N]
+  float2* maps = (float2*)(tile + WARPS * STEPS * G * 32);            // [WARPS][N][32]
+  float* enter = (float*)(maps + WARPS * 32 * N);                     // [N][32]
+  uint32_t* tops = (uint32_t*)(enter + 32 * N);                       // Q8: [WARPS][G][N][32]
   unsigned long long* bars = (unsigned long long*)(tops + (Q8 ? WARPS * G * 32 * N : 0));  // [WARPS]
   unsigned* shared = (unsigned*)(bars + WARPS);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -237,61 +308,64 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const __grid_cons
     __syncwarp();
     if (lane == 0 && it.live > 0) {
       mbar_arrive_expect_tx(bar, STEPS * G * 128);
-      tma_load_4d(smem_u32(mine), &xmap, bar, (it.tile % p.tiles_c) * 32 * N, 0, it.t0, it.b);
+      tma_load_4d(smem_u32(mine), &xmap, bar, it.ct, 0, it.t0, it.b);
     }
   } else {
     fetch_lanes<T, G>(p, it, (const T*)p.Wx, mine);
   }
-  const bool wide = p.C % 2 == 0;
-  float bias[G][N];
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    uint32_t v = p.bias ? load_lane((const T*)p.bias + (size_t)g * p.C + it.ch, it.n, wide) : 0;
-    Lane<T>::unpack(v, bias[g]);
+  FV<N> bias[G];
+  load_bias<T, FN, N>(p, it, bias);
+  FV<N> x = splat<N>(0.0f);  // the state that enters the chunk
+  Chain<N, false> chain(p, it, p.carry);
+  if (warp == 0) {
+    if (p.s0) x = load_f<N, false>(p.s0, it.b, p, it);
+    chain.probe(x);
   }
-  float x[N];  // the state that enters the chunk
-#pragma unroll
-  for (int v = 0; v < N; ++v) x[v] = 0.0f;
-  if (warp == 0 && p.s0) load_f<N, false>(p.s0, it.b, p, it, x);
   bool failed = false;
   if (p.tma && it.live > 0) mbar_wait_bounded<false>(bar, 0, p.wait_limit_ns, p.status, failed);
 
-  float f[STEPS][N], u[STEPS][N], P[N], H[N];
+  FV<N> f[STEPS], u[Q8 ? STEPS : 1], P = splat<N>(1.0f), H = splat<N>(0.0f);
   uint32_t top[G][N];
 #pragma unroll
-  for (int v = 0; v < N; ++v) {
-    P[v] = 1.0f;
-    H[v] = 0.0f;
+  for (int g = 0; g < G; ++g)
 #pragma unroll
-    for (int g = 0; g < G; ++g) top[g][v] = 0;
-  }
+    for (int v = 0; v < N; ++v) top[g][v] = 0;
+  by_mask(it, [&](auto mask) {
+    constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
-  for (int j = 0; j < STEPS; ++j) {
-    float a[G][N];
+    for (int j = 0; j < STEPS; ++j) {
+      const bool on = !MASK || j < it.live, rst = MASK && (it.rst >> j & 1);
+      FV<N> z[G], w;
 #pragma unroll
-    for (int g = 0; g < G; ++g) Lane<T>::unpack(mine[(j * G + g) * 32 + lane], a[g]);
-    const bool on = j < it.live, rst = it.rst >> j & 1;
+      for (int g = 0; g < (FN == GATED_LINEAR && !Q8 ? G - 1 : G); ++g) {  // o is read when it is needed
+        const FV<N> a = Lane<T>::unpack(mine[(j * G + g) * 32 + lane]);
+        if (Q8) {
 #pragma unroll
-    for (int v = 0; v < N; ++v) {
-      float z[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        if (Q8) top[g][v] = max(top[g][v], on ? __float_as_uint(fabsf(a[g][v])) : 0u);
-        z[g] = a[g][v] + bias[g][v];
+          for (int v = 0; v < N; ++v) top[g][v] = max(top[g][v], on ? __float_as_uint(fabsf(a.v[v])) : 0u);
+        }
+        z[g] = gate<FN>(g, a, bias[g]);
       }
-      gated_coeff<FN, FAST>(z, f[j][v], u[j][v]);
-      f[j][v] = !on ? 1.0f : rst ? 0.0f : f[j][v];
-      u[j][v] = on ? u[j][v] : 0.0f;
-      P[v] *= f[j][v];
-      H[v] = rst ? u[j][v] : fmaf(f[j][v], H[v], u[j][v]);
+      gated_coeff<FN, N>(z, f[j], w);
+      if (MASK) {
+        f[j] = select(on, rst ? splat<N>(0.0f) : f[j], splat<N>(1.0f));
+        w = select(on, w, splat<N>(0.0f));
+      }
+      P = mul(P, f[j]);
+      H = MASK && rst ? w : fma(f[j], H, w);
+      if (Q8) {
+        u[j] = w;
+      } else {
+        mine[(j * G + U0) * 32 + lane] = __float_as_uint(w.v[0]);
+        if (N == 2) mine[(j * G + U1) * 32 + lane] = __float_as_uint(w.v[N - 1]);
+      }
     }
-  }
+  });
 #pragma unroll
   for (int v = 0; v < N; ++v) {
-    maps[warp * 32 * N + lane * N + v] = make_float2(P[v], H[v]);
+    maps[(warp * N + v) * 32 + lane] = make_float2(P.v[v], H.v[v]);
     if (Q8) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) tops[(warp * G + g) * 32 * N + lane * N + v] = top[g][v];
+      for (int g = 0; g < G; ++g) tops[((warp * G + g) * N + v) * 32 + lane] = top[g][v];
     }
   }
   __syncthreads();
@@ -300,21 +374,18 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const __grid_cons
     for (int w = 1; w < WARPS; ++w)
 #pragma unroll
       for (int v = 0; v < N; ++v) {
-        const float2 m = maps[w * 32 * N + lane * N + v];
-        P[v] *= m.x;
-        H[v] = affine(m.x, H[v], m.y);
+        const float2 m = maps[(w * N + v) * 32 + lane];
+        P.v[v] *= m.x;
+        H.v[v] = affine(m.x, H.v[v], m.y);
       }
-    chain<N, false>(p, it, p.carry, P, H, x);
+    chain.pass(P, H, x);
     if (p.carry && (it.k == 0 || it.k % p.span != 0)) store_f<N>(p.carry, (size_t)it.b * p.chunks + it.k, p, it, x);
 #pragma unroll
-    for (int v = 0; v < N; ++v) enter[lane * N + v] = x[v];
-    if (p.last && it.k == p.chunks - 1) {
-#pragma unroll
-      for (int v = 0; v < N; ++v) x[v] = affine(P[v], x[v], H[v]);
-      store_f<N>(p.last, it.b, p, it, x);
-    }
+    for (int v = 0; v < N; ++v) enter[v * 32 + lane] = x.v[v];
+    if (p.last && it.k == p.chunks - 1) store_f<N>(p.last, it.b, p, it, affine(P, x, H));
   }
-  if (Q8) {  // before the wait for the state: the tile in 8 bits
+  const bool wide = p.C % 2 == 0;
+  if (Q8) {  // beside the wait for the state: the tile in 8 bits
     const int qblocks = (p.T + ACT_BLOCK - 1) / ACT_BLOCK;
     float inv[G][N];
     bool fin[G][N];
@@ -322,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const __grid_cons
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int v = 0; v < N; ++v) {
-        const uint32_t t = max(top[g][v], tops[((warp ^ 1) * G + g) * 32 * N + lane * N + v]);
+        const uint32_t t = max(top[g][v], tops[(((warp ^ 1) * G + g) * N + v) * 32 + lane]);
         const unsigned s = act_scale_byte(__uint_as_float(t));
         inv[g][v] = act_inv_scale(s);
         fin[g][v] = s != ACT_NONFINITE;
@@ -335,11 +406,10 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const __grid_cons
       if (it.t0 + j >= p.T) break;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        float a[N];
-        Lane<T>::unpack(mine[(j * G + g) * 32 + lane], a);
+        const FV<N> a = Lane<T>::unpack(mine[(j * G + g) * 32 + lane]);
         int b8[N];
 #pragma unroll
-        for (int v = 0; v < N; ++v) b8[v] = j < it.live && fin[g][v] ? act_quant(a[v], inv[g][v]) : 0;
+        for (int v = 0; v < N; ++v) b8[v] = j < it.live && fin[g][v] ? act_quant(a.v[v], inv[g][v]) : 0;
         signed char* at = q + (size_t)(j * G + g) * p.C;
         if (N == 2 && wide && it.n == 2)
           *(unsigned short*)at = (unsigned short)((b8[0] & 255) | (b8[N - 1] & 255) << 8);
@@ -351,45 +421,62 @@ __global__ void __launch_bounds__(THREADS, 2) gated_fwd_kernel(const __grid_cons
     }
   }
   __syncthreads();
-  float c[N];
+  FV<N> c;
 #pragma unroll
   for (int v = 0; v < N; ++v) {
-    c[v] = enter[lane * N + v];
+    c.v[v] = enter[v * 32 + lane];
     for (int w = 0; w < warp; ++w) {
-      const float2 m = maps[w * 32 * N + lane * N + v];
-      c[v] = affine(m.x, c[v], m.y);
+      const float2 m = maps[(w * N + v) * 32 + lane];
+      c.v[v] = affine(m.x, c.v[v], m.y);
     }
   }
-  T* h = (T*)p.h + ((size_t)it.b * p.T + it.t0) * p.C + it.ch;
+  by_mask(it, [&](auto mask) {
+    constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
-  for (int j = 0; j < STEPS; ++j) {
-    if (it.t0 + j >= p.T) break;
-    const bool rst = it.rst >> j & 1;
-    float a[N], y[N];
-    if (FN == GATED_LINEAR) Lane<T>::unpack(mine[(j * G + G - 1) * 32 + lane], a);
-#pragma unroll
-    for (int v = 0; v < N; ++v) {
-      float z[G];
-      z[G - 1] = FN == GATED_LINEAR ? a[v] + bias[G - 1][v] : 0.0f;
-      c[v] = rst ? u[j][v] : fmaf(f[j][v], c[v], u[j][v]);
-      y[v] = j < it.live ? gated_out<FN, FAST>(z, c[v]) : 0.0f;
+    for (int j = 0; j < STEPS; ++j) {
+      const bool on = !MASK || j < it.live, rst = MASK && (it.rst >> j & 1);
+      FV<N> w, y, o;
+      if (FN == GATED_LINEAR)
+        o = sigmoid(gate<FN>(G - 1, Lane<T>::unpack(mine[(j * G + G - 1) * 32 + lane]), bias[G - 1]));
+      if (Q8) {
+        w = u[Q8 ? j : 0];
+      } else {
+        w.v[0] = __uint_as_float(mine[(j * G + U0) * 32 + lane]);
+        if (N == 2) w.v[N - 1] = __uint_as_float(mine[(j * G + U1) * 32 + lane]);
+      }
+      c = MASK && rst ? w : fma(f[j], c, w);
+      y = FN == GATED_LINEAR ? mul(o, c) : c;
+      if (MASK) y = select(on, y, splat<N>(0.0f));
+      // step j's row lies in a step before j (or is row 0 of step 0), all read
+      mine[j * 32 + lane] = Lane<T>::pack(y);
     }
-    store_lane(h + (size_t)j * p.C, Lane<T>::pack(y), it.n, wide);
+  });
+  if (p.tma) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && it.t0 < p.T) {
+      tma_store_4d(&hmap, smem_u32(mine), it.ct, 0, it.t0, it.b);
+      bulk_commit_group();
+      bulk_wait_group_read<0>();
+    }
+  } else {
+    T* h = (T*)p.h + ((size_t)it.b * p.T + it.t0) * p.C + it.ch;
+    for (int j = 0; j < STEPS && it.t0 + j < p.T; ++j) store_lane(h + (size_t)j * p.C, mine[j * 32 + lane], it.n, wide);
   }
 }
 
 template <typename T, int FN, bool Q8>
-__global__ void __launch_bounds__(THREADS, 2) gated_bwd_kernel(const __grid_constant__ CUtensorMap xmap,
-                                                               const __grid_constant__ CUtensorMap dmap, GatedArgs p) {
+__global__ void __launch_bounds__(THREADS, 2)
+    gated_bwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap dmap,
+                     const __grid_constant__ CUtensorMap omap, GatedArgs p) {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
-  constexpr bool FAST = sizeof(T) == 2;
   constexpr int XB = Q8 ? 32 * N : 128;  // bytes of a row (t, g) of the tile
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* tile = smem;                                          // [WARPS][STEPS][G][XB]
   uint32_t* dtile = (uint32_t*)(tile + WARPS * STEPS * G * XB);        // [WARPS][STEPS][32]
-  float* maps = (float*)(dtile + WARPS * STEPS * 32);                  // [WARPS][3][32 N]: P, H (state), E (gradient)
-  float* enter = maps + WARPS * 3 * 32 * N;                            // [32 N]
-  float* dbs = enter + 32 * N;                                         // [WARPS][G][32 N]
+  float* maps = (float*)(dtile + WARPS * STEPS * 32);                  // [WARPS][3][N][32]: P, H (state), E (gradient)
+  float* enter = maps + WARPS * 3 * 32 * N;                            // [N][32]
+  float* dbs = enter + 32 * N;                                         // [WARPS][G][N][32]
   unsigned long long* bars = (unsigned long long*)(dbs + WARPS * G * 32 * N);
   unsigned* shared = (unsigned*)(bars + WARPS);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -406,8 +493,8 @@ __global__ void __launch_bounds__(THREADS, 2) gated_bwd_kernel(const __grid_cons
     __syncwarp();
     if (lane == 0 && it.live > 0) {
       mbar_arrive_expect_tx(bar, STEPS * G * XB + (p.dh ? STEPS * 128 : 0));
-      tma_load_4d(smem_u32(mine), &xmap, bar, (it.tile % p.tiles_c) * 32 * N, 0, it.t0, it.b);
-      if (p.dh) tma_load_4d(smem_u32(dmine), &dmap, bar, (it.tile % p.tiles_c) * 32 * N, 0, it.t0, it.b);
+      tma_load_4d(smem_u32(mine), &xmap, bar, it.ct, 0, it.t0, it.b);
+      if (p.dh) tma_load_4d(smem_u32(dmine), &dmap, bar, it.ct, 0, it.t0, it.b);
     }
   } else {
     if (Q8) {
@@ -415,185 +502,170 @@ __global__ void __launch_bounds__(THREADS, 2) gated_bwd_kernel(const __grid_cons
 #pragma unroll 8
       for (int r = 0; r < it.live * G; ++r)
 #pragma unroll
-        for (int v = 0; v < N; ++v) mine[r * XB + lane * N + v] = v < it.n ? (unsigned char)__ldg(at + (size_t)r * p.C + v) : 0;
+        for (int v = 0; v < N; ++v)
+          mine[r * XB + lane * N + v] = v < it.n ? (unsigned char)__ldg(at + (size_t)r * p.C + v) : 0;
     } else {
       fetch_lanes<T, G>(p, it, (const T*)p.Wx, (uint32_t*)mine);
     }
     if (p.dh) fetch_lanes<T, 1>(p, it, (const T*)p.dh, dmine);
   }
-  float bias[G][N], scale[G][N];
+  FV<N> bias[G], scale[Q8 ? G : 1];
+  load_bias<T, FN, N>(p, it, bias);
+  if (Q8) {
+    const int qblocks = (p.T + ACT_BLOCK - 1) / ACT_BLOCK;
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    uint32_t w = p.bias ? load_lane((const T*)p.bias + (size_t)g * p.C + it.ch, it.n, wide) : 0;
-    Lane<T>::unpack(w, bias[g]);
-    if (Q8) {
-      const int qblocks = (p.T + ACT_BLOCK - 1) / ACT_BLOCK;
+    for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int v = 0; v < N; ++v)
-        scale[g][v] = v < it.n && it.t0 < p.T
-                          ? act_scale(p.qs[(((size_t)it.b * qblocks + it.t0 / ACT_BLOCK) * G + g) * p.C + it.ch + v])
-                          : 0.0f;
-    }
+        scale[Q8 ? g : 0].v[v] =
+            v < it.n && it.t0 < p.T
+                ? mul_of<FN, N>(g) * act_scale(p.qs[(((size_t)it.b * qblocks + it.t0 / ACT_BLOCK) * G + g) * p.C + it.ch + v])
+                : 0.0f;
   }
-  float c[N], x[N];  // c: the state that enters the chunk; x: the state gradient that enters it from later steps
-  load_f<N, false>(p.carry, (size_t)it.b * p.chunks + it.k, p, it, c);
-#pragma unroll
-  for (int v = 0; v < N; ++v) x[v] = 0.0f;
-  if (warp == 0 && p.dlast) load_f<N, false>(p.dlast, it.b, p, it, x);
+  FV<N> c = load_f<N, false>(p.carry, (size_t)it.b * p.chunks + it.k, p, it);  // the state that enters the chunk
+  FV<N> x = splat<N>(0.0f);  // the state gradient that enters it from later steps
+  Chain<N, true> chain(p, it, p.dcarry);
+  if (warp == 0) {
+    if (p.dlast) x = load_f<N, false>(p.dlast, it.b, p, it);
+    chain.probe(x);
+  }
   bool failed = false;
   if (p.tma && it.live > 0) mbar_wait_bounded<false>(bar, 0, p.wait_limit_ns, p.status, failed);
 
-  auto gates = [&](int j, float z[G][N]) {
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      if (Q8) {
-        const signed char* r = (const signed char*)mine + (j * G + g) * XB + lane * N;
-        if (N == 2) {
-          const char2 v = *(const char2*)r;
-          z[g][0] = fmaf((float)v.x, scale[g][0], bias[g][0]);
-          z[g][N - 1] = fmaf((float)v.y, scale[g][N - 1], bias[g][N - 1]);
-        } else {
-          z[g][0] = fmaf((float)r[0], scale[g][0], bias[g][0]);
-        }
-      } else {
-        Lane<T>::unpack(*(const uint32_t*)(mine + (j * G + g) * XB + lane * 4), z[g]);
-#pragma unroll
-        for (int v = 0; v < N; ++v) z[g][v] += bias[g][v];
-      }
+  auto gate_at = [&](int j, int g) {
+    if (Q8) {
+      const unsigned char* r = mine + (j * G + g) * XB + lane * N;
+      const uint32_t w = N == 2 ? *(const unsigned short*)r : *r;
+      return fma(bytes_f(w, (FV<N>*)nullptr), scale[Q8 ? g : 0], bias[g]);
     }
+    return gate<FN>(g, Lane<T>::unpack(*(const uint32_t*)(mine + (j * G + g) * XB + lane * 4)), bias[g]);
   };
-  auto upstream = [&](int j, float* d) {
-    Lane<T>::unpack(p.dh ? dmine[j * 32 + lane] : 0u, d);
-  };
+  if (!p.dh) {
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) dmine[j * 32 + lane] = 0;
+  }
 
-  float f[STEPS][N], u[STEPS][N], P[N], H[N], E[N];
+  FV<N> f[STEPS], u[STEPS], P = splat<N>(1.0f), H = splat<N>(0.0f), E = splat<N>(0.0f);
+  by_mask(it, [&](auto mask) {
+    constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
-  for (int v = 0; v < N; ++v) {
-    P[v] = 1.0f;
-    H[v] = E[v] = 0.0f;
-  }
+    for (int j = 0; j < STEPS; ++j) {
+      const bool on = !MASK || j < it.live, rst = MASK && (it.rst >> j & 1);
+      FV<N> z[G], e = Lane<T>::unpack(dmine[j * 32 + lane]);
 #pragma unroll
-  for (int j = 0; j < STEPS; ++j) {
-    float z[G][N], d[N];
-    gates(j, z);
-    upstream(j, d);
-    const bool on = j < it.live, rst = it.rst >> j & 1;
-#pragma unroll
-    for (int v = 0; v < N; ++v) {
-      float a[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) a[g] = z[g][v];
-      gated_coeff<FN, FAST>(a, f[j][v], u[j][v]);
-      const float e = on ? gated_into<FN, FAST>(a, d[v]) : 0.0f;
-      f[j][v] = !on ? 1.0f : rst ? 0.0f : f[j][v];
-      u[j][v] = on ? u[j][v] : 0.0f;
+      for (int g = 0; g < G; ++g) z[g] = gate_at(j, g);
+      gated_coeff<FN, N>(z, f[j], u[j]);
+      if (FN == GATED_LINEAR) e = mul(e, sigmoid(z[G - 1]));
+      if (MASK) {
+        e = select(on, e, splat<N>(0.0f));
+        f[j] = select(on, rst ? splat<N>(0.0f) : f[j], splat<N>(1.0f));
+        u[j] = select(on, u[j], splat<N>(0.0f));
+      }
       // what step j's delta sends out of the warp's first step: f_0 .. f_j times it
-      P[v] *= f[j][v];
-      H[v] = rst ? u[j][v] : fmaf(f[j][v], H[v], u[j][v]);
-      E[v] = affine(P[v], e, E[v]);
+      P = mul(P, f[j]);
+      H = MASK && rst ? u[j] : fma(f[j], H, u[j]);
+      E = MASK ? affine(P, e, E) : fma(P, e, E);
     }
-  }
-  float* m = maps + warp * 3 * 32 * N + lane * N;
+  });
 #pragma unroll
   for (int v = 0; v < N; ++v) {
-    m[v] = P[v];
-    m[32 * N + v] = H[v];
-    m[64 * N + v] = E[v];
+    float* m = maps + (warp * 3 * N + v) * 32 + lane;
+    m[0] = P.v[v];
+    m[N * 32] = H.v[v];
+    m[2 * N * 32] = E.v[v];
   }
   __syncthreads();
   if (warp == 0) {  // the chunk's map of the gradient, last warp first
-    float PC[N], EC[N];
-#pragma unroll
-    for (int v = 0; v < N; ++v) {
-      PC[v] = 1.0f;
-      EC[v] = 0.0f;
-    }
+    FV<N> PC = splat<N>(1.0f), EC = splat<N>(0.0f);
 #pragma unroll
     for (int w = WARPS - 1; w >= 0; --w)
 #pragma unroll
       for (int v = 0; v < N; ++v) {
-        const float* q = maps + w * 3 * 32 * N + lane * N + v;
-        PC[v] *= q[0];
-        EC[v] = affine(q[0], EC[v], q[64 * N]);
+        const float* m = maps + (w * 3 * N + v) * 32 + lane;
+        PC.v[v] *= m[0];
+        EC.v[v] = affine(m[0], EC.v[v], m[2 * N * 32]);
       }
-    chain<N, true>(p, it, p.dcarry, PC, EC, x);
+    chain.pass(PC, EC, x);
 #pragma unroll
-    for (int v = 0; v < N; ++v) enter[lane * N + v] = x[v];
-    if (p.ds0 && it.k == 0) {
-#pragma unroll
-      for (int v = 0; v < N; ++v) x[v] = affine(PC[v], x[v], EC[v]);
-      store_f<N>(p.ds0, it.b, p, it, x);
-    }
+    for (int v = 0; v < N; ++v) enter[v * 32 + lane] = x.v[v];
+    if (p.ds0 && it.k == 0) store_f<N>(p.ds0, it.b, p, it, affine(PC, x, EC));
   }
   // the states of the warp's steps, while the gradient is on its way
 #pragma unroll
   for (int v = 0; v < N; ++v)
     for (int w = 0; w < warp; ++w) {
-      const float* q = maps + w * 3 * 32 * N + lane * N + v;
-      c[v] = affine(q[0], c[v], q[32 * N]);
+      const float* m = maps + (w * 3 * N + v) * 32 + lane;
+      c.v[v] = affine(m[0], c.v[v], m[N * 32]);
     }
-  float first[N];
+  const FV<N> start = c;
+  by_mask(it, [&](auto mask) {
+    constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
-  for (int v = 0; v < N; ++v) first[v] = c[v];
-#pragma unroll
-  for (int j = 0; j < STEPS; ++j)
-#pragma unroll
-    for (int v = 0; v < N; ++v) u[j][v] = c[v] = (it.rst >> j & 1) ? u[j][v] : fmaf(f[j][v], c[v], u[j][v]);
+    for (int j = 0; j < STEPS; ++j) u[j] = c = MASK && (it.rst >> j & 1) ? u[j] : fma(f[j], c, u[j]);
+  });
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < N; ++v) {
-    x[v] = enter[lane * N + v];
+    x.v[v] = enter[v * 32 + lane];
     for (int w = WARPS - 1; w > warp; --w) {
-      const float* q = maps + w * 3 * 32 * N + lane * N + v;
-      x[v] = affine(q[0], x[v], q[64 * N]);
+      const float* m = maps + (w * 3 * N + v) * 32 + lane;
+      x.v[v] = affine(m[0], x.v[v], m[2 * N * 32]);
     }
   }
-  float db[G][N];
+  FV<N> db[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g)
-#pragma unroll
-    for (int v = 0; v < N; ++v) db[g][v] = 0.0f;
+  for (int g = 0; g < G; ++g) db[g] = splat<N>(0.0f);
+  // dWx leaves through the tile (in place of the pre-activations it came from)
+  // and one TMA store a warp; from the registers where the tile holds bytes or
+  // TMA cannot take the rows
+  const bool staged = !Q8 && p.tma;
   T* out = p.dWx ? (T*)p.dWx + ((size_t)it.b * p.T + it.t0) * G * p.C + it.ch : nullptr;
+  by_mask(it, [&](auto mask) {
+    constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
-  for (int j = STEPS - 1; j >= 0; --j) {
-    float z[G][N], d[N], da[G][N];
-    gates(j, z);
-    upstream(j, d);
-    const bool on = j < it.live, rst = it.rst >> j & 1;
+    for (int j = STEPS - 1; j >= 0; --j) {
+      const bool on = !MASK || j < it.live, rst = MASK && (it.rst >> j & 1);
+      FV<N> z[G], da[G], d = Lane<T>::unpack(dmine[j * 32 + lane]);
 #pragma unroll
-    for (int v = 0; v < N; ++v) {
-      float a[G], r[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) a[g] = z[g][v];
-      const float delta = x[v] + gated_into<FN, FAST>(a, d[v]);
-      const float cp = rst ? 0.0f : j > 0 ? u[j - 1][v] : first[v];
-      gated_grad<FN, FAST>(a, cp, u[j][v], d[v], delta, r);
-      x[v] = on ? (rst ? 0.0f : f[j][v] * delta) : x[v];
+      for (int g = 0; g < G; ++g) z[g] = gate_at(j, g);
+      FV<N> y = x;
+      const FV<N> cp = j > 0 ? u[j > 0 ? j - 1 : 0] : start;
+      gated_grad<FN, N>(z, f[j], MASK && rst ? splat<N>(0.0f) : cp, u[j], d, y, da);
+      x = MASK ? select(on, rst ? splat<N>(0.0f) : y, x) : y;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        da[g][v] = on ? r[g] : 0.0f;
-        db[g][v] += da[g][v];
+        if (MASK) da[g] = select(on, da[g], splat<N>(0.0f));
+        db[g] = add(db[g], da[g]);
+        if (staged)
+          *(uint32_t*)(mine + (j * G + g) * XB + lane * 4) = Lane<T>::pack(da[g]);
+        else if (out && it.t0 + j < p.T)
+          store_lane(out + (size_t)(j * G + g) * p.C, Lane<T>::pack(da[g]), it.n, wide);
       }
     }
-    if (out && it.t0 + j < p.T) {
-#pragma unroll
-      for (int g = 0; g < G; ++g) store_lane(out + (size_t)(j * G + g) * p.C, Lane<T>::pack(da[g]), it.n, wide);
+  });
+  if (staged && p.dWx) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && it.t0 < p.T) {
+      tma_store_4d(&omap, smem_u32(mine), it.ct, 0, it.t0, it.b);
+      bulk_commit_group();
     }
   }
   if (p.dbp) {
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int v = 0; v < N; ++v) dbs[(warp * G + g) * 32 * N + lane * N + v] = db[g][v];
+      for (int v = 0; v < N; ++v) dbs[((warp * G + g) * N + v) * 32 + lane] = db[g].v[v];
     __syncthreads();
     for (int i = threadIdx.x; i < G * 32 * N; i += THREADS) {
       float s = 0.0f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) s += dbs[w * G * 32 * N + i];
-      const int g = i / (32 * N), ch = (it.tile % p.tiles_c) * 32 * N + i % (32 * N);
+      const int g = i / (32 * N), ch = it.ct + i % 32 * N + i / 32 % N;
       if (ch < p.C) p.dbp[(((size_t)it.b * p.chunks + it.k) * G + g) * p.C + ch] = s;
     }
   }
+  if (staged && lane == 0) bulk_wait_group_read<0>();  // the tile is read from until then
 }
 
 template <typename T, int FN, bool Q8> constexpr int fwd_smem() {
@@ -635,30 +707,39 @@ struct StepArgs {
   unsigned* status;
 };
 
+// A thread has the N channels of a lane (4 bytes of the storage type).
 template <typename T, int FN>
 __global__ void __launch_bounds__(128) gated_step_kernel(StepArgs p) {
-  constexpr int G = gated_gates(FN);
-  constexpr bool FAST = sizeof(T) == 2;
+  constexpr int G = gated_gates(FN), N = Lane<T>::N;
+  const int lanes = (p.C + N - 1) / N;
   const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
-  if (id >= (long long)p.rows * p.C) return;
-  const int m = (int)(id / p.C), ch = (int)(id % p.C);
-  const int slot = p.slot ? p.slot[m] : m;
-  float y = 0.0f;
+  if (id >= (long long)p.rows * lanes) return;
+  const int m = (int)(id / lanes), ch = (int)(id % lanes) * N;
+  const int n = min(p.C - ch, N);
+  const bool wide = p.C % 2 == 0;
+  const int slot = p.slot ? __ldg(p.slot + m) : m;
+  FV<N> y = splat<N>(0.0f);
   if (slot >= 0 && slot < p.slots) {
-    float a[G], f, u;
+    FV<N> z[G], f, u, c;
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-      a[g] = to_f(((const T*)p.Wx)[((size_t)m * G + g) * p.C + ch]) +
-             (p.bias ? to_f(((const T*)p.bias)[(size_t)g * p.C + ch]) : 0.0f);
-    gated_coeff<FN, FAST>(a, f, u);
+    for (int g = 0; g < G; ++g) {
+      z[g] = Lane<T>::unpack(load_lane((const T*)p.Wx + ((size_t)m * G + g) * p.C + ch, n, wide));
+      FV<N> b = Lane<T>::unpack(p.bias ? load_lane((const T*)p.bias + (size_t)g * p.C + ch, n, wide) : 0);
+      z[g] = gate<FN>(g, z[g], mul(b, splat<N>(mul_of<FN, N>(g))));
+    }
     const size_t at = (size_t)slot * p.C + ch;
-    const float c = fmaf(f, p.pool[at], u);
-    p.pool_out[at] = c;
-    y = gated_out<FN, FAST>(a, c);
+#pragma unroll
+    for (int v = 0; v < N; ++v) c.v[v] = v < n ? p.pool[at + v] : 0.0f;
+    gated_coeff<FN, N>(z, f, u);
+    c = fma(f, c, u);
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+      if (v < n) p.pool_out[at + v] = c.v[v];
+    y = FN == GATED_LINEAR ? mul(sigmoid(z[G - 1]), c) : c;
   } else if (slot >= p.slots && ch == 0 && p.status) {
     atomicOr(p.status, STATUS_RANGE);
   }
-  ((T*)p.h)[id] = from_f<T>(y);
+  store_lane((T*)p.h + (size_t)m * p.C + ch, Lane<T>::pack(y), n, wide);
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -726,10 +807,12 @@ template <typename T, int FN, bool Q8> cudaError_t gated_launch(bool bwd, GatedA
   const int xelem = bwd && Q8 ? 1 : (int)sizeof(T);
   // TMA rows start on 16 bytes
   a.tma = !a.solo && ((size_t)a.C * xelem) % 16 == 0 && ((size_t)a.C * sizeof(T)) % 16 == 0;
-  CUtensorMap x = {}, d = {};
+  CUtensorMap x = {}, d = {}, out = {};
   if (a.tma) {
     cudaError_t e = tile_map(&x, bwd && Q8 ? (const void*)a.q : a.Wx, xelem, a, G, width);
     if (e == cudaSuccess && bwd && a.dh) e = tile_map(&d, a.dh, (int)sizeof(T), a, 1, width);
+    if (e == cudaSuccess && !bwd) e = tile_map(&out, a.h, (int)sizeof(T), a, 1, width);
+    if (e == cudaSuccess && bwd && a.dWx && !Q8) e = tile_map(&out, a.dWx, (int)sizeof(T), a, G, width);
     if (e != cudaSuccess) return e;
   }
   const size_t items = (size_t)a.B * a.tiles_c * a.chunks;
@@ -737,8 +820,8 @@ template <typename T, int FN, bool Q8> cudaError_t gated_launch(bool bwd, GatedA
   const void* k = bwd ? (const void*)gated_bwd_kernel<T, FN, Q8> : (const void*)gated_fwd_kernel<T, FN, Q8>;
   cudaError_t e = set_smem_attr(k, smem);
   if (e != cudaSuccess) return e;
-  if (bwd) gated_bwd_kernel<T, FN, Q8><<<(unsigned)items, THREADS, smem, st>>>(x, d, a);
-  else gated_fwd_kernel<T, FN, Q8><<<(unsigned)items, THREADS, smem, st>>>(x, a);
+  if (bwd) gated_bwd_kernel<T, FN, Q8><<<(unsigned)items, THREADS, smem, st>>>(x, d, out, a);
+  else gated_fwd_kernel<T, FN, Q8><<<(unsigned)items, THREADS, smem, st>>>(x, out, a);
   note_launch();
   return cudaGetLastError();
 }
@@ -874,7 +957,8 @@ int rnn_gated_step(int rows, int slots, int N, int D, int function, int dtype, c
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0) return RNN_OK;
   StepArgs a{rows, N * D, slots, Wx, b, slot, (const float*)pool, (float*)pool_out, h, (unsigned*)status};
-  const unsigned grid = (unsigned)(((long long)rows * a.C + 127) / 128);
+  const int n = dtype == RNN_BF16 ? 2 : 1;
+  const unsigned grid = (unsigned)(((long long)rows * ((a.C + n - 1) / n) + 127) / 128);
   if (dtype == RNN_BF16) {
     if (function == RNN_LINEAR) gated_step_kernel<__nv_bfloat16, GATED_LINEAR><<<grid, 128, 0, st>>>(a);
     else gated_step_kernel<__nv_bfloat16, GATED_COUPLED><<<grid, 128, 0, st>>>(a);

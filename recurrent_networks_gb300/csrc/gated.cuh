@@ -36,75 +36,124 @@ template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16(v); }
 
-// 1 / d to a rounding (one Newton step on the approximate reciprocal): the
-// factor f of a long memory enters every later state, and the approximation
-// alone, off to one side by up to 2^-23, moved the fp32 state of a channel
-// that remembers 2000 steps by 2e-4.
-template <bool FAST> __device__ __forceinline__ float rcp_full(float d) {
-  if (!FAST) return 1.0f / d;
-  const float r = rcp_fast(d);
-  return fmaf(r, fmaf(-d, r, 1.0f), r);
+// ---- N channels of a lane as one value ------------------------------------------
+// N = 2 (bf16 storage): the packed fp32 pair instructions of sm_100 and later
+// take one issue slot for both channels. N = 1 (fp32 storage): plain fp32.
+template <int N> struct FV { float v[N]; };
+template <int N> __device__ __forceinline__ FV<N> splat(float a) {
+  FV<N> r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r.v[i] = a;
+  return r;
 }
-template <bool FAST> __device__ __forceinline__ float sig_full(float x) {
-  if (!FAST) return 1.0f / (1.0f + expf(-x));
-  // the bound keeps the Newton step finite; the reciprocal is 0 there already
-  return rcp_full<FAST>(fminf(1.0f + exp2_fast(-1.4426950408889634f * x), 1.7e38f));
+__device__ __forceinline__ uint64_t pair_bits(const FV<2>& a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.v[0]), "f"(a.v[1]));
+  return r;
 }
-// s = sigmoid(x) and n = 1 - s without cancellation: e = exp(-x), s = 1 / (1 + e),
-// n = e s. An e past the fp32 range leaves s = 0 and n = 0 (instead of inf * 0):
-// n only ever enters the product s n, which is 0 there.
-template <bool FAST> __device__ __forceinline__ void sig_pair(float x, float& s, float& n) {
-  const float e = FAST ? exp2_fast(-1.4426950408889634f * x) : expf(-x);
-  s = FAST ? rcp_fast(1.0f + e) : 1.0f / (1.0f + e);
-  n = s * fminf(e, 3e38f);
+__device__ __forceinline__ FV<2> pair_of(uint64_t b) {
+  FV<2> r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.v[0]), "=f"(r.v[1]) : "l"(b));
+  return r;
 }
-// s = sigmoid(x) and n = sigmoid(-x), both to full relative accuracy (from
-// exp(-|x|) <= 1): the coupled cell uses n itself as the input gate.
-template <bool FAST> __device__ __forceinline__ void sig_both(float x, float& s, float& n) {
-  const float e = FAST ? exp2_fast(-1.4426950408889634f * fabsf(x)) : expf(-fabsf(x));
-  const float r = rcp_full<FAST>(1.0f + e);
-  const float er = e * r;
-  s = x >= 0.0f ? r : er;
-  n = x >= 0.0f ? er : r;
+__device__ __forceinline__ FV<2> fma(const FV<2>& a, const FV<2>& b, const FV<2>& c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return pair_of(d);
+}
+__device__ __forceinline__ FV<2> mul(const FV<2>& a, const FV<2>& b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return pair_of(d);
+}
+__device__ __forceinline__ FV<2> add(const FV<2>& a, const FV<2>& b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return pair_of(d);
+}
+__device__ __forceinline__ FV<1> fma(const FV<1>& a, const FV<1>& b, const FV<1>& c) { return {{fmaf(a.v[0], b.v[0], c.v[0])}}; }
+__device__ __forceinline__ FV<1> mul(const FV<1>& a, const FV<1>& b) { return {{a.v[0] * b.v[0]}}; }
+__device__ __forceinline__ FV<1> add(const FV<1>& a, const FV<1>& b) { return {{a.v[0] + b.v[0]}}; }
+template <int N> __device__ __forceinline__ FV<N> one_minus(const FV<N>& a) { return fma(a, splat<N>(-1.0f), splat<N>(1.0f)); }
+
+// A gate's biased pre-activation, as its function wants it: z itself, or, for
+// the sigmoids of bf16 storage, -z log2 e (the factor sits in `mul_of` and in
+// the prepared bias), so that exp(-z) is one base-2 exponential.
+template <int FN> __host__ __device__ constexpr bool gate_is_linear(int g) { return FN == GATED_LINEAR ? g == 2 : g == 1; }
+template <int FN, int N> __device__ __forceinline__ constexpr float mul_of(int g) {
+  return N == 1 || gate_is_linear<FN>(g) ? 1.0f : -1.4426950408889634f;
+}
+// e = exp(-z)
+__device__ __forceinline__ FV<2> exp_neg(const FV<2>& t) { return {{exp2_fast(t.v[0]), exp2_fast(t.v[1])}}; }
+__device__ __forceinline__ FV<1> exp_neg(const FV<1>& z) { return {{expf(-z.v[0])}}; }
+__device__ __forceinline__ FV<2> rcp(const FV<2>& d) { return {{rcp_fast(d.v[0]), rcp_fast(d.v[1])}}; }
+__device__ __forceinline__ FV<1> rcp(const FV<1>& d) { return {{1.0f / d.v[0]}}; }
+// 1 / d to a rounding, d <= 1.7e38 for N = 2 (one Newton step on the
+// approximate reciprocal): the factor f of a long memory enters every later
+// state, and the approximation alone, off to one side by up to 2^-23, moved
+// the fp32 state of a channel that remembers 2000 steps by 2e-4.
+__device__ __forceinline__ FV<2> rcp_full(const FV<2>& d) {
+  const FV<2> r = rcp(d);
+  return fma(r, fma(mul(d, splat<2>(-1.0f)), r, splat<2>(1.0f)), r);
+}
+__device__ __forceinline__ FV<1> rcp_full(const FV<1>& d) { return rcp(d); }
+
+template <int N> __device__ __forceinline__ FV<N> sigmoid(const FV<N>& z) { return rcp(add(exp_neg(z), splat<N>(1.0f))); }
+// The forget gate of `linear`. The bound keeps the Newton step finite where
+// the reciprocal is 0 already.
+__device__ __forceinline__ FV<2> sigmoid_full(const FV<2>& z) {
+  FV<2> d = add(exp_neg(z), splat<2>(1.0f));
+  d.v[0] = fminf(d.v[0], 1.7e38f);
+  d.v[1] = fminf(d.v[1], 1.7e38f);
+  return rcp_full(d);
+}
+__device__ __forceinline__ FV<1> sigmoid_full(const FV<1>& z) { return sigmoid(z); }
+// f = sigmoid(z) and n = 1 - f, both to full relative accuracy (the coupled
+// cell uses n itself as the input gate): n = exp(-z) f, with exp(-z) bounded
+// by 2^125 so that f stays a normal number and n becomes 1.
+__device__ __forceinline__ void sigmoid_both(const FV<2>& t, FV<2>& f, FV<2>& n) {
+  const FV<2> e = exp_neg(FV<2>{{fminf(t.v[0], 125.0f), fminf(t.v[1], 125.0f)}});
+  f = rcp_full(add(e, splat<2>(1.0f)));
+  n = mul(e, f);
+}
+__device__ __forceinline__ void sigmoid_both(const FV<1>& z, FV<1>& f, FV<1>& n) {
+  const float x = z.v[0], e = expf(-fabsf(x)), r = 1.0f / (1.0f + e), er = e * r;
+  f.v[0] = x >= 0.0f ? r : er;
+  n.v[0] = x >= 0.0f ? er : r;
 }
 
-// f and u of c = f c' + u from the biased pre-activations a[G]
-template <int FN, bool FAST> __device__ __forceinline__ void gated_coeff(const float* a, float& f, float& u) {
+// f and u of c = f c' + u from the gates z[G]
+template <int FN, int N> __device__ __forceinline__ void gated_coeff(const FV<N>* z, FV<N>& f, FV<N>& u) {
   if (FN == GATED_LINEAR) {
-    f = sig_full<FAST>(a[1]);
-    u = f_sigmoid<FAST>(a[0]) * a[2];
+    f = sigmoid_full(z[1]);
+    u = mul(sigmoid(z[0]), z[2]);
   } else {
-    float n;
-    sig_both<FAST>(a[0], f, n);
-    u = n * a[1];
+    FV<N> n;
+    sigmoid_both(z[0], f, n);
+    u = mul(n, z[1]);
   }
 }
-// h from c
-template <int FN, bool FAST> __device__ __forceinline__ float gated_out(const float* a, float c) {
-  return FN == GATED_LINEAR ? f_sigmoid<FAST>(a[3]) * c : c;
-}
-// the part of delta that comes from dh of the same step
-template <int FN, bool FAST> __device__ __forceinline__ float gated_into(const float* a, float dh) {
-  return FN == GATED_LINEAR ? f_sigmoid<FAST>(a[3]) * dh : dh;
-}
-// da[G] of one step from its biased pre-activations, c' (0 after a reset), c,
-// dh and delta
-template <int FN, bool FAST>
-__device__ __forceinline__ void gated_grad(const float* a, float cp, float c, float dh, float delta, float* da) {
+// da[G] of one step from its gates, f, c' (0 after a reset), c, dh and the
+// gradient x that reaches c from later steps; x becomes f delta, what the
+// step passes on (0 after a reset goes by f = 0).
+template <int FN, int N>
+__device__ __forceinline__ void gated_grad(const FV<N>* z, const FV<N>& f, const FV<N>& cp, const FV<N>& c, const FV<N>& dh,
+                                           FV<N>& x, FV<N>* da) {
   if (FN == GATED_LINEAR) {
-    float s, n;
-    sig_pair<FAST>(a[0], s, n);
-    da[0] = delta * a[2] * (s * n);
-    da[2] = delta * s;
-    sig_pair<FAST>(a[1], s, n);
-    da[1] = delta * cp * (s * n);
-    sig_pair<FAST>(a[3], s, n);
-    da[3] = dh * c * (s * n);
+    const FV<N> i = sigmoid(z[0]), o = sigmoid(z[3]);
+    const FV<N> e = mul(dh, o), delta = add(x, e);
+    x = mul(f, delta);
+    da[2] = mul(delta, i);
+    da[0] = mul(da[2], mul(z[2], one_minus(i)));
+    da[1] = mul(x, mul(cp, one_minus(f)));
+    da[3] = mul(e, mul(c, one_minus(o)));
   } else {
-    float s, n;
-    sig_both<FAST>(a[0], s, n);
-    da[0] = delta * (cp - a[1]) * (s * n);
-    da[1] = delta * n;
+    FV<N> s, n;
+    sigmoid_both(z[0], s, n);
+    const FV<N> delta = add(x, dh);
+    x = mul(f, delta);
+    da[1] = mul(delta, n);
+    da[0] = mul(mul(da[1], s), fma(z[1], splat<N>(-1.0f), cp));
   }
 }
 
