@@ -19,8 +19,12 @@ namespace {
 // after it, every other chunk its own map as soon as it has it, and a chunk
 // starts from the state before its group and folds the maps of the group's
 // chunks before it, in their order. The order of the sums is thus fixed, and
-// the chain through the chunks has one hop per group. Items are handed out in
-// chunk order, so whatever an item waits for is already running.
+// the chain through the chunks has one hop per group.
+// Published values are 8-byte words (fp32, tag) that are written and read
+// whole, so a reader polls the value itself: no fence, and one round trip.
+// CTAs stay and take item after item from a counter, in chunk order and only
+// when the last one is through its wait, so whatever an item waits for is
+// being worked on, however few of the CTAs are running.
 constexpr int WARPS = 8, STEPS = GATED_CHUNK / WARPS, THREADS = WARPS * 32;
 constexpr int MAX_SPAN = 32;
 
@@ -28,7 +32,6 @@ struct GatedArgs {
   int B, T, C, chunks;  // C = N D channels
   int tiles_c;          // channel tiles per batch row
   int span;             // chunks per group
-  int tma;              // rows are 16-byte multiples: tiles come by TMA
   int solo;  // one chunk, all CTAs at once: no waits, so block 0 clears the status word itself
   const void* Wx;
   const void* bias;
@@ -37,7 +40,7 @@ struct GatedArgs {
   const int* lengths;
   void* h;
   float* last;
-  float* carry;              // [B][chunks][C]: the state before every chunk (forward: the tape, or scratch)
+  float* carry;              // [B][chunks][C]: the state before every chunk (the tape)
   signed char* q;            // 8-bit pre-activations: written by the forward, read by the backward
   unsigned char* qs;
   const void* dh;
@@ -45,11 +48,10 @@ struct GatedArgs {
   void* dWx;
   float* ds0;
   float* dbp;                // [B chunks][G][C]
-  float* dcarry;             // backward: [B][chunks][C], the state gradient that leaves a chunk
-  float* maps;               // [B][chunks][2][C]: the chunks' maps
+  unsigned long long* states;  // [groups][tiles][N][32]: the state (or its gradient) that enters a group
+  ulonglong2* maps;            // [chunks][tiles][N][32]: the chunks' maps (P, H)
   unsigned* status;
   unsigned* ticket;
-  unsigned* flags;           // [chunks][tiles]
   unsigned long long wait_limit_ns;
 };
 
@@ -137,30 +139,32 @@ struct Item {
   unsigned rst;                    // bit j: reset at the warp's step j
   bool plain;                      // every step exists, none is a reset
 };
-template <int N, bool REVERSE> __device__ __forceinline__ Item item_of(const GatedArgs& p, unsigned* shared) {
-  unsigned id = blockIdx.x;
-  if (p.solo && id == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
-  if (p.chunks > 1) {
-    if (threadIdx.x == 0) *shared = atomicAdd(p.ticket, 1u);
-    __syncthreads();
-    id = *shared;
-  }
-  const unsigned tiles = (unsigned)p.B * p.tiles_c;
+// Thread 0 takes an item (the first one: from == blockIdx.x without a counter
+// when there is one item a CTA) and works out its place for all, the divisions
+// once; x < 0: no more items.
+template <bool REVERSE> __device__ __forceinline__ int4 place_of(const GatedArgs& p, unsigned id) {
+  const unsigned tiles = (unsigned)p.B * p.tiles_c, k = id / tiles, tile = id % tiles, b = tile / p.tiles_c;
+  if (k >= (unsigned)p.chunks) return make_int4(-1, 0, 0, 0);
+  return make_int4(REVERSE ? p.chunks - 1 - (int)k : (int)k, (int)tile, (int)b, clamp_len(p.lengths, b, p.T));
+}
+template <int N> __device__ __forceinline__ Item item_of(const GatedArgs& p, const int4& s) {
   Item it;
-  it.k = (int)(id / tiles);
-  if (REVERSE) it.k = p.chunks - 1 - it.k;
-  it.tile = (int)(id % tiles);
-  it.b = it.tile / p.tiles_c;
+  it.k = s.x;
+  it.tile = s.y;
+  it.b = s.z;
+  it.len = s.w;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  it.ct = (it.tile % p.tiles_c) * 32 * N;
+  it.ct = (it.tile - it.b * p.tiles_c) * 32 * N;
   it.ch = it.ct + lane * N;
   it.n = min(max(p.C - it.ch, 0), N);
   it.t0 = it.k * GATED_CHUNK + warp * STEPS;
-  it.len = clamp_len(p.lengths, it.b, p.T);
   it.live = min(max(it.len - it.t0, 0), STEPS);
-  bool r = false;
-  if (p.reset && lane < it.live) r = p.reset[(size_t)it.b * p.T + it.t0 + lane] != 0;
-  it.rst = __ballot_sync(0xffffffffu, r);
+  it.rst = 0;
+  if (p.reset) {
+    bool r = false;
+    if (lane < it.live) r = p.reset[(size_t)it.b * p.T + it.t0 + lane] != 0;
+    it.rst = __ballot_sync(0xffffffffu, r);
+  }
   it.plain = it.live == STEPS && it.rst == 0;
   return it;
 }
@@ -181,70 +185,141 @@ template <int N> __device__ __forceinline__ void store_f(float* a, size_t r, con
     if (v < it.n) a[r * p.C + it.ch + v] = x.v[v];
 }
 
-// How warp 0 passes the state through the chunks of a tile. `states`
-// [B][chunks][C] holds the state that enters a chunk; REVERSE: the processing
-// order descends. The state that enters this chunk is `x` (in: the state
-// before the first chunk in processing order).
+// (value, tag) words. Relaxed accesses at gpu scope: each 8-byte word is read
+// and written whole, and nothing else is ordered by it.
+__device__ __forceinline__ unsigned long long word_of(float v) { return 1ull << 32 | __float_as_uint(v); }
+__device__ __forceinline__ float value_of(unsigned long long w) { return __uint_as_float((unsigned)w); }
+__device__ __forceinline__ bool is_set(unsigned long long w) { return (w >> 32) != 0; }
+__device__ __forceinline__ unsigned long long ld_word(const unsigned long long* p) {
+  unsigned long long w;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(p) : "memory");
+  return w;
+}
+__device__ __forceinline__ void st_word(unsigned long long* p, unsigned long long w) {
+  asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(w) : "memory");
+}
+
+// How a CTA passes the state through the chunks of a tile; REVERSE: the
+// processing order descends. Warp 0 holds the chunk's own map and the state;
+// PARTS warps fold the maps of the group's chunks before this one, each a run
+// of them, so the order of the products depends on the chunk alone.
 template <int N, bool REVERSE> struct Chain {
+  static constexpr int PARTS = 4, AHEAD = 2;  // folding warps, maps in flight
   const GatedArgs& p;
   const Item& it;
-  float* states;
   int o, first;  // this chunk's and its group's first chunk's place in processing order
-  bool ends, final, ready;
-  __device__ __forceinline__ Chain(const GatedArgs& p, const Item& it, float* states) : p(p), it(it), states(states) {
+  unsigned long long early[N];
+  bool failed;
+  __device__ __forceinline__ Chain(const GatedArgs& p, const Item& it) : p(p), it(it), failed(false) {
     o = REVERSE ? p.chunks - 1 - it.k : it.k;
     first = o - o % p.span;
-    ends = (o + 1) % p.span == 0;
-    final = o + 1 == p.chunks;
-    ready = o == 0;
   }
-  __device__ __forceinline__ unsigned* flag(int order) const {
-    return p.flags + (size_t)order * ((unsigned)p.B * p.tiles_c) + it.tile;
+  __device__ __forceinline__ size_t at(int i) const {
+    return ((size_t)i * ((unsigned)p.B * p.tiles_c) + it.tile) * N * 32 + (threadIdx.x & 31);
   }
-  __device__ __forceinline__ size_t row(int order) const {
-    return (size_t)it.b * p.chunks + (REVERSE ? p.chunks - 1 - order : order);
-  }
-  __device__ __forceinline__ void raise() const {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0)  // a release at gpu scope is cumulative: it covers the warp's stores before the barrier
-      asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flag(o)) : "memory");
-  }
-  // the state after the group before, through the group's chunks before this one
-  __device__ __forceinline__ void take(FV<N>& x) const {
-    if (first > 0) x = load_f<N, true>(states, row(first), p, it);
-#pragma unroll 4
-    for (int w = first; w < o; ++w)
-      x = affine(load_f<N, true>(p.maps, row(w) * 2, p, it), x, load_f<N, true>(p.maps, row(w) * 2 + 1, p, it));
-  }
-  // At the start: where everything needed is published already (the usual
-  // case with many tiles), the round trips run beside the tile's load.
-  __device__ __forceinline__ void probe(FV<N>& x) {
-    if (ready) return;
-    bool up = true;
-    for (int w = (first > 0 ? first - 1 : 0) + (threadIdx.x & 31); w < o; w += 32) up &= ld_acquire_gpu(flag(w)) != 0;
-    ready = __all_sync(0xffffffffu, up);
-    if (!ready) return;
-    __syncwarp();  // the lanes' acquires, for all of them
-    take(x);
-  }
-  // With the chunk's own map (P, H): publishes what later chunks need, and
-  // waits for x where the probe found it missing.
-  __device__ __forceinline__ void pass(const FV<N>& P, const FV<N>& H, FV<N>& x) {
-    if (!ends && !final) {
-      store_f<N>(p.maps, row(o) * 2, p, it, P);
-      store_f<N>(p.maps, row(o) * 2 + 1, p, it, H);
-      raise();
+  // At the start: asks for the state that enters the group; where it is there
+  // already (the usual case with many tiles) the round trip runs beside the
+  // tile's load.
+  __device__ __forceinline__ void ask() {
+    if (first > 0) {
+#pragma unroll
+      for (int v = 0; v < N; ++v) early[v] = ld_word(p.states + at(first / p.span) + v * 32);
     }
-    if (!ready) {
-      bool failed = false;
-      for (int w = (first > 0 ? first - 1 : 0) + (threadIdx.x & 31); w < o; w += 32)
-        counter_wait_bounded(flag(w), 1u, p.wait_limit_ns, p.status, failed);
+  }
+  // Waits until `get` has what it wants, for at most the wait limit.
+  template <typename F> __device__ __forceinline__ void wait(F&& get) {
+    if (failed || get()) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!get()) {
+      if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+        atomicOr(p.status, STATUS_TIMEOUT);
+        failed = true;
+        return;
+      }
+    }
+  }
+  // The chunk's own map, for the group's later chunks.
+  __device__ __forceinline__ void publish(const FV<N>& P, const FV<N>& H) const {
+    if (o + 1 == first + p.span || o + 1 == p.chunks) return;
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+      asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p.maps + at(o) + v * 32), "l"(word_of(P.v[v])),
+                   "l"(word_of(H.v[v]))
+                   : "memory");
+  }
+  // All warps: the group's maps before this chunk, folded in PARTS runs into
+  // `parts` [PARTS][N][32].
+  __device__ __forceinline__ void gather(float2* parts) {
+    if (o == first) return;
+    const int part = (int)(threadIdx.x >> 5) - (WARPS - PARTS);
+    if (part >= 0) {
+      const int run = (o - first + PARTS - 1) / PARTS;
+      const int from = min(o, first + part * run), to = min(o, from + run);
+      FV<N> P = splat<N>(1.0f), H = splat<N>(0.0f);
+      for (int w0 = from; w0 < to; w0 += AHEAD) {
+        ulonglong2 m[AHEAD][N];
+        wait([&]() {
+          bool all = true;
+#pragma unroll
+          for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+            for (int v = 0; v < N; ++v)
+              if (w0 + j < to)
+                asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];"
+                             : "=l"(m[j][v].x), "=l"(m[j][v].y)
+                             : "l"(p.maps + at(w0 + j) + v * 32)
+                             : "memory");
+#pragma unroll
+          for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+            for (int v = 0; v < N; ++v)
+              if (w0 + j < to) all &= is_set(m[j][v].x) && is_set(m[j][v].y);
+          return all;
+        });
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+          for (int v = 0; v < N; ++v)
+            if (w0 + j < to) {
+              P.v[v] *= value_of(m[j][v].x);
+              H.v[v] = affine(value_of(m[j][v].x), H.v[v], value_of(m[j][v].y));
+            }
+      }
+#pragma unroll
+      for (int v = 0; v < N; ++v) parts[(part * N + v) * 32 + (threadIdx.x & 31)] = make_float2(P.v[v], H.v[v]);
+    }
+    __syncthreads();
+  }
+  // Warp 0: makes x (in: the state before the first chunk in processing
+  // order) the state that enters the chunk, and publishes what leaves a group.
+  __device__ __forceinline__ void pass(const float2* parts, const FV<N>& P, const FV<N>& H, FV<N>& x) {
+    if (first > 0) {
+      wait([&]() {
+        bool all = true;
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+          if (!is_set(early[v])) early[v] = ld_word(p.states + at(first / p.span) + v * 32);
+          all &= is_set(early[v]);
+        }
+        return all;
+      });
+#pragma unroll
+      for (int v = 0; v < N; ++v) x.v[v] = value_of(early[v]);
+    }
+    if (o > first) {
+#pragma unroll
+      for (int w = 0; w < PARTS; ++w)
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+          const float2 m = parts[(w * N + v) * 32 + (threadIdx.x & 31)];
+          x.v[v] = affine(m.x, x.v[v], m.y);
+        }
       __syncwarp();
-      take(x);
     }
-    if (ends && !final) {
-      store_f<N>(states, row(o + 1), p, it, affine(P, x, H));
-      raise();
+    if (o + 1 == first + p.span && o + 1 < p.chunks) {
+      const FV<N> y = affine(P, x, H);
+#pragma unroll
+      for (int v = 0; v < N; ++v) st_word(p.states + at((o + 1) / p.span) + v * 32, word_of(y.v[v]));
     }
   }
 };
@@ -284,7 +359,7 @@ template <typename F> __device__ __forceinline__ void by_mask(const Item& it, F&
 // Blocks per SM: the tile is 64 KB (linear) or 32 KB (coupled). Without the
 // 8-bit copy u waits in the tile's place of i and g (coupled: f and g), which
 // are not read again, so that f alone stays in registers.
-template <typename T, int FN, bool Q8>
+template <typename T, int FN, bool Q8, bool TMA>
 __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
     gated_fwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap hmap, GatedArgs p) {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
@@ -292,20 +367,24 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
   extern __shared__ __align__(128) unsigned char smem[];
   uint32_t* tile = (uint32_t*)smem;                                   // [WARPS][STEPS][G][32]
   float2* maps = (float2*)(tile + WARPS * STEPS * G * 32);            // [WARPS][N][32]
-  float* enter = (float*)(maps + WARPS * 32 * N);                     // [N][32]
-  uint32_t* tops = (uint32_t*)(enter + 32 * N);                       // Q8: [WARPS][G][N][32]
+  float* enter = (float*)(maps + WARPS * 32 * N);                     // [WARPS][N][32]: the states that enter the warps
+  uint32_t* tops = (uint32_t*)(enter + WARPS * 32 * N);                       // Q8: [WARPS][G][N][32]
   unsigned long long* bars = (unsigned long long*)(tops + (Q8 ? WARPS * G * 32 * N : 0));  // [WARPS]
-  unsigned* shared = (unsigned*)(bars + WARPS);
+  int4* shared = (int4*)(bars + WARPS);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bar = smem_u32(bars + warp);
-  if (p.tma && lane == 0) {
+  if (TMA && lane == 0) {
     mbar_init(bar, 1);
     fence_mbar_init_cluster();
   }
-  const Item it = item_of<N, false>(p, shared);
   uint32_t* mine = tile + warp * STEPS * G * 32;
-  if (p.tma) {
-    __syncwarp();
+  bool failed = false;
+  if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
+  if (threadIdx.x == 0) *shared = place_of<false>(p, p.solo ? blockIdx.x : atomicAdd(p.ticket, 1u));
+  __syncthreads();
+  for (unsigned loads = 0; shared->x >= 0;) {
+  const Item it = item_of<N>(p, *shared);
+  if (TMA) {
     if (lane == 0 && it.live > 0) {
       mbar_arrive_expect_tx(bar, STEPS * G * 128);
       tma_load_4d(smem_u32(mine), &xmap, bar, it.ct, 0, it.t0, it.b);
@@ -316,13 +395,12 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
   FV<N> bias[G];
   load_bias<T, FN, N>(p, it, bias);
   FV<N> x = splat<N>(0.0f);  // the state that enters the chunk
-  Chain<N, false> chain(p, it, p.carry);
+  Chain<N, false> chain(p, it);
   if (warp == 0) {
     if (p.s0) x = load_f<N, false>(p.s0, it.b, p, it);
-    chain.probe(x);
+    chain.ask();
   }
-  bool failed = false;
-  if (p.tma && it.live > 0) mbar_wait_bounded<false>(bar, 0, p.wait_limit_ns, p.status, failed);
+  if (TMA && it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
 
   FV<N> f[STEPS], u[Q8 ? STEPS : 1], P = splat<N>(1.0f), H = splat<N>(0.0f);
   uint32_t top[G][N];
@@ -378,11 +456,21 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
         P.v[v] *= m.x;
         H.v[v] = affine(m.x, H.v[v], m.y);
       }
-    chain.pass(P, H, x);
-    if (p.carry && (it.k == 0 || it.k % p.span != 0)) store_f<N>(p.carry, (size_t)it.b * p.chunks + it.k, p, it, x);
-#pragma unroll
-    for (int v = 0; v < N; ++v) enter[v * 32 + lane] = x.v[v];
+    chain.publish(P, H);
+  }
+  chain.gather((float2*)enter);
+  if (warp == 0) {
+    chain.pass((const float2*)enter, P, H, x);
+    if (p.carry) store_f<N>(p.carry, (size_t)it.b * p.chunks + it.k, p, it, x);
     if (p.last && it.k == p.chunks - 1) store_f<N>(p.last, it.b, p, it, affine(P, x, H));
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+      for (int v = 0; v < N; ++v) {
+        enter[(w * N + v) * 32 + lane] = x.v[v];
+        const float2 m = maps[(w * N + v) * 32 + lane];
+        x.v[v] = affine(m.x, x.v[v], m.y);
+      }
   }
   const bool wide = p.C % 2 == 0;
   if (Q8) {  // beside the wait for the state: the tile in 8 bits
@@ -421,15 +509,11 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
     }
   }
   __syncthreads();
+  unsigned next = 0xffffffffu;
+  if (threadIdx.x == 0 && !p.solo) next = atomicAdd(p.ticket, 1u);  // on its way beside the last pass
   FV<N> c;
 #pragma unroll
-  for (int v = 0; v < N; ++v) {
-    c.v[v] = enter[v * 32 + lane];
-    for (int w = 0; w < warp; ++w) {
-      const float2 m = maps[(w * N + v) * 32 + lane];
-      c.v[v] = affine(m.x, c.v[v], m.y);
-    }
-  }
+  for (int v = 0; v < N; ++v) c.v[v] = enter[(warp * N + v) * 32 + lane];
   by_mask(it, [&](auto mask) {
     constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
@@ -451,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
       mine[j * 32 + lane] = Lane<T>::pack(y);
     }
   });
-  if (p.tma) {
+  if (TMA) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0 && it.t0 < p.T) {
@@ -463,9 +547,12 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
     T* h = (T*)p.h + ((size_t)it.b * p.T + it.t0) * p.C + it.ch;
     for (int j = 0; j < STEPS && it.t0 + j < p.T; ++j) store_lane(h + (size_t)j * p.C, mine[j * 32 + lane], it.n, wide);
   }
+  if (threadIdx.x == 0) *shared = place_of<false>(p, next);
+  __syncthreads();
+  }
 }
 
-template <typename T, int FN, bool Q8>
+template <typename T, int FN, bool Q8, bool TMA>
 __global__ void __launch_bounds__(THREADS, 2)
     gated_bwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap dmap,
                      const __grid_constant__ CUtensorMap omap, GatedArgs p) {
@@ -475,22 +562,30 @@ __global__ void __launch_bounds__(THREADS, 2)
   unsigned char* tile = smem;                                          // [WARPS][STEPS][G][XB]
   uint32_t* dtile = (uint32_t*)(tile + WARPS * STEPS * G * XB);        // [WARPS][STEPS][32]
   float* maps = (float*)(dtile + WARPS * STEPS * 32);                  // [WARPS][3][N][32]: P, H (state), E (gradient)
-  float* enter = maps + WARPS * 3 * 32 * N;                            // [N][32]
-  float* dbs = enter + 32 * N;                                         // [WARPS][G][N][32]
+  float* enter = maps + WARPS * 3 * 32 * N;                            // [WARPS][N][32]
+  float* dbs = enter + WARPS * 32 * N;                                         // [WARPS][G][N][32]
   unsigned long long* bars = (unsigned long long*)(dbs + WARPS * G * 32 * N);
-  unsigned* shared = (unsigned*)(bars + WARPS);
+  int4* shared = (int4*)(bars + WARPS);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bar = smem_u32(bars + warp);
-  if (p.tma && lane == 0) {
+  if (TMA && lane == 0) {
     mbar_init(bar, 1);
     fence_mbar_init_cluster();
   }
-  const Item it = item_of<N, true>(p, shared);
   unsigned char* mine = tile + warp * STEPS * G * XB;
   uint32_t* dmine = dtile + warp * STEPS * 32;
   const bool wide = p.C % 2 == 0;
-  if (p.tma) {
-    __syncwarp();
+  bool failed = false;
+  if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
+  if (threadIdx.x == 0) *shared = place_of<true>(p, p.solo ? blockIdx.x : atomicAdd(p.ticket, 1u));
+  if (!p.dh) {
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) dmine[j * 32 + lane] = 0;
+  }
+  __syncthreads();
+  for (unsigned loads = 0; shared->x >= 0;) {
+  const Item it = item_of<N>(p, *shared);
+  if (TMA) {
     if (lane == 0 && it.live > 0) {
       mbar_arrive_expect_tx(bar, STEPS * G * XB + (p.dh ? STEPS * 128 : 0));
       tma_load_4d(smem_u32(mine), &xmap, bar, it.ct, 0, it.t0, it.b);
@@ -524,13 +619,12 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   FV<N> c = load_f<N, false>(p.carry, (size_t)it.b * p.chunks + it.k, p, it);  // the state that enters the chunk
   FV<N> x = splat<N>(0.0f);  // the state gradient that enters it from later steps
-  Chain<N, true> chain(p, it, p.dcarry);
+  Chain<N, true> chain(p, it);
   if (warp == 0) {
     if (p.dlast) x = load_f<N, false>(p.dlast, it.b, p, it);
-    chain.probe(x);
+    chain.ask();
   }
-  bool failed = false;
-  if (p.tma && it.live > 0) mbar_wait_bounded<false>(bar, 0, p.wait_limit_ns, p.status, failed);
+  if (TMA && it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
 
   auto gate_at = [&](int j, int g) {
     if (Q8) {
@@ -540,10 +634,6 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     return gate<FN>(g, Lane<T>::unpack(*(const uint32_t*)(mine + (j * G + g) * XB + lane * 4)), bias[g]);
   };
-  if (!p.dh) {
-#pragma unroll
-    for (int j = 0; j < STEPS; ++j) dmine[j * 32 + lane] = 0;
-  }
 
   FV<N> f[STEPS], u[STEPS], P = splat<N>(1.0f), H = splat<N>(0.0f), E = splat<N>(0.0f);
   by_mask(it, [&](auto mask) {
@@ -575,8 +665,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     m[2 * N * 32] = E.v[v];
   }
   __syncthreads();
+  FV<N> PC = splat<N>(1.0f), EC = splat<N>(0.0f);
   if (warp == 0) {  // the chunk's map of the gradient, last warp first
-    FV<N> PC = splat<N>(1.0f), EC = splat<N>(0.0f);
 #pragma unroll
     for (int w = WARPS - 1; w >= 0; --w)
 #pragma unroll
@@ -585,10 +675,20 @@ __global__ void __launch_bounds__(THREADS, 2)
         PC.v[v] *= m[0];
         EC.v[v] = affine(m[0], EC.v[v], m[2 * N * 32]);
       }
-    chain.pass(PC, EC, x);
-#pragma unroll
-    for (int v = 0; v < N; ++v) enter[v * 32 + lane] = x.v[v];
+    chain.publish(PC, EC);
+  }
+  chain.gather((float2*)enter);
+  if (warp == 0) {
+    chain.pass((const float2*)enter, PC, EC, x);
     if (p.ds0 && it.k == 0) store_f<N>(p.ds0, it.b, p, it, affine(PC, x, EC));
+#pragma unroll
+    for (int w = WARPS - 1; w >= 0; --w)
+#pragma unroll
+      for (int v = 0; v < N; ++v) {
+        enter[(w * N + v) * 32 + lane] = x.v[v];
+        const float* m = maps + (w * 3 * N + v) * 32 + lane;
+        x.v[v] = affine(m[0], x.v[v], m[2 * N * 32]);
+      }
   }
   // the states of the warp's steps, while the gradient is on its way
 #pragma unroll
@@ -604,21 +704,17 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int j = 0; j < STEPS; ++j) u[j] = c = MASK && (it.rst >> j & 1) ? u[j] : fma(f[j], c, u[j]);
   });
   __syncthreads();
+  unsigned next = 0xffffffffu;
+  if (threadIdx.x == 0 && !p.solo) next = atomicAdd(p.ticket, 1u);  // on its way beside the last pass
 #pragma unroll
-  for (int v = 0; v < N; ++v) {
-    x.v[v] = enter[v * 32 + lane];
-    for (int w = WARPS - 1; w > warp; --w) {
-      const float* m = maps + (w * 3 * N + v) * 32 + lane;
-      x.v[v] = affine(m[0], x.v[v], m[2 * N * 32]);
-    }
-  }
+  for (int v = 0; v < N; ++v) x.v[v] = enter[(warp * N + v) * 32 + lane];
   FV<N> db[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) db[g] = splat<N>(0.0f);
   // dWx leaves through the tile (in place of the pre-activations it came from)
   // and one TMA store a warp; from the registers where the tile holds bytes or
   // TMA cannot take the rows
-  const bool staged = !Q8 && p.tma;
+  constexpr bool staged = !Q8 && TMA;
   T* out = p.dWx ? (T*)p.dWx + ((size_t)it.b * p.T + it.t0) * G * p.C + it.ch : nullptr;
   by_mask(it, [&](auto mask) {
     constexpr bool MASK = decltype(mask)::value;
@@ -643,10 +739,10 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
     }
   });
-  if (staged && p.dWx) {
+  if (staged) {  // (the fence also puts the lanes' writes before the next item's load)
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0 && it.t0 < p.T) {
+    if (lane == 0 && p.dWx && it.t0 < p.T) {
       tma_store_4d(&omap, smem_u32(mine), it.ct, 0, it.t0, it.b);
       bulk_commit_group();
     }
@@ -666,15 +762,18 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
   }
   if (staged && lane == 0) bulk_wait_group_read<0>();  // the tile is read from until then
+  if (threadIdx.x == 0) *shared = place_of<true>(p, next);
+  __syncthreads();
+  }
 }
 
 template <typename T, int FN, bool Q8> constexpr int fwd_smem() {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
-  return WARPS * STEPS * G * 128 + WARPS * 32 * N * 8 + 32 * N * 4 + (Q8 ? WARPS * G * 32 * N * 4 : 0) + WARPS * 8 + 16;
+  return WARPS * STEPS * G * 128 + WARPS * 32 * N * 8 + WARPS * 32 * N * 4 + (Q8 ? WARPS * G * 32 * N * 4 : 0) + WARPS * 8 + 16;
 }
 template <typename T, int FN, bool Q8> constexpr int bwd_smem() {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
-  return WARPS * STEPS * (G * (Q8 ? 32 * N : 128) + 128) + WARPS * 3 * 32 * N * 4 + 32 * N * 4 + WARPS * G * 32 * N * 4 +
+  return WARPS * STEPS * (G * (Q8 ? 32 * N : 128) + 128) + WARPS * 3 * 32 * N * 4 + WARPS * 32 * N * 4 + WARPS * G * 32 * N * 4 +
          WARPS * 8 + 16;
 }
 
@@ -762,7 +861,7 @@ bool gated_dims_ok(const rnn_gated_dims_t* d) {
 struct GatedSizes {
   int G, C, chunks, qblocks, tiles_c, span, solo;
   size_t esize, carry, q, qs, tape;
-  size_t sync, maps, dbp;  // workspace: status, ticket and flags (zeroed by every call) | maps | states | db sums
+  size_t sync, states, maps, dbp;  // workspace: status, ticket, states and maps (sync: zeroed by every call) | db sums
 };
 GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   GatedSizes z;
@@ -774,22 +873,25 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   const int width = d->dtype == RNN_BF16 ? 64 : 32;
   z.tiles_c = (z.C + width - 1) / width;
   const size_t tiles = (size_t)d->B * z.tiles_c;
-  // With fewer tiles than CTAs run at once, chunks of one tile run side by
-  // side and wait on one another: groups of chunks then keep the chain short.
-  const size_t resident = 2 * (size_t)device_sms();
-  z.span = tiles >= resident ? 1 : (int)((2 * resident + tiles - 1) / tiles);
+  // A hop of the chain takes about 1.2 us, in which the GPU moves some 100
+  // tiles: with fewer tiles than that (and a margin of two), a group of chunks
+  // shares a hop.
+  const size_t sms = device_sms(), ahead = sms + sms / 2;
+  z.span = (int)((ahead + tiles - 1) / tiles);
   if (z.span > MAX_SPAN) z.span = MAX_SPAN;
   // A short sequence is all latency: without TMA there is no wait that could
   // run out, and the clearing launch for the status word falls away.
-  z.solo = z.chunks == 1 && tiles <= resident;
-  const size_t states = up256((size_t)d->B * z.chunks * z.C * sizeof(float));
-  z.carry = states;
+  z.solo = z.chunks == 1 && tiles <= 2 * sms;
+  const size_t lanes = tiles * 32 * (d->dtype == RNN_BF16 ? 2 : 1);
+  z.carry = up256((size_t)d->B * z.chunks * z.C * sizeof(float));
   const bool q8 = d->checkpoint == RNN_CKPT_INT8;
   z.q = q8 ? up256((size_t)d->B * d->T * z.G * z.C) : 0;
   z.qs = q8 ? up256((size_t)d->B * z.qblocks * z.G * z.C) : 0;
   z.tape = z.carry + z.q + z.qs;
-  z.sync = z.chunks > 1 ? 512 + up256(tiles * z.chunks * sizeof(unsigned)) : 256;
-  z.maps = z.chunks > 1 && z.span > 1 ? 2 * states : 0;
+  const size_t groups = (z.chunks + z.span - 1) / z.span;
+  z.states = z.chunks > 1 ? up256(groups * lanes * sizeof(unsigned long long)) : 0;
+  z.maps = z.chunks > 1 && z.span > 1 ? up256(z.chunks * lanes * sizeof(ulonglong2)) : 0;
+  z.sync = 512 + z.states + z.maps;
   z.dbp = up256((size_t)d->B * z.chunks * z.G * z.C * sizeof(float));
   return z;
 }
@@ -802,28 +904,32 @@ cudaError_t tile_map(CUtensorMap* m, const void* base, int elem, const GatedArgs
   return encode_tensor_map(m, base, elem, 4, dims, box);
 }
 
-template <typename T, int FN, bool Q8> cudaError_t gated_launch(bool bwd, GatedArgs a, cudaStream_t st) {
+template <typename T, int FN, bool Q8, bool TMA> cudaError_t gated_launch(bool bwd, const GatedArgs& a, cudaStream_t st) {
   constexpr int G = gated_gates(FN), width = 32 * Lane<T>::N;
-  const int xelem = bwd && Q8 ? 1 : (int)sizeof(T);
-  // TMA rows start on 16 bytes
-  a.tma = !a.solo && ((size_t)a.C * xelem) % 16 == 0 && ((size_t)a.C * sizeof(T)) % 16 == 0;
   CUtensorMap x = {}, d = {}, out = {};
-  if (a.tma) {
-    cudaError_t e = tile_map(&x, bwd && Q8 ? (const void*)a.q : a.Wx, xelem, a, G, width);
+  if (TMA) {
+    cudaError_t e = bwd && Q8 ? tile_map(&x, a.q, 1, a, G, width) : tile_map(&x, a.Wx, (int)sizeof(T), a, G, width);
     if (e == cudaSuccess && bwd && a.dh) e = tile_map(&d, a.dh, (int)sizeof(T), a, 1, width);
     if (e == cudaSuccess && !bwd) e = tile_map(&out, a.h, (int)sizeof(T), a, 1, width);
     if (e == cudaSuccess && bwd && a.dWx && !Q8) e = tile_map(&out, a.dWx, (int)sizeof(T), a, G, width);
     if (e != cudaSuccess) return e;
   }
-  const size_t items = (size_t)a.B * a.tiles_c * a.chunks;
+  const unsigned items = (unsigned)((size_t)a.B * a.tiles_c * a.chunks);
   const int smem = bwd ? bwd_smem<T, FN, Q8>() : fwd_smem<T, FN, Q8>();
-  const void* k = bwd ? (const void*)gated_bwd_kernel<T, FN, Q8> : (const void*)gated_fwd_kernel<T, FN, Q8>;
+  const void* k = bwd ? (const void*)gated_bwd_kernel<T, FN, Q8, TMA> : (const void*)gated_fwd_kernel<T, FN, Q8, TMA>;
   cudaError_t e = set_smem_attr(k, smem);
   if (e != cudaSuccess) return e;
-  if (bwd) gated_bwd_kernel<T, FN, Q8><<<(unsigned)items, THREADS, smem, st>>>(x, d, out, a);
-  else gated_fwd_kernel<T, FN, Q8><<<(unsigned)items, THREADS, smem, st>>>(x, out, a);
+  // as many CTAs as the SMs hold (see the kernels' launch bounds)
+  const unsigned most = device_sms() * (bwd || Q8 ? 2 : 3), ctas = a.solo || items < most ? items : most;
+  if (bwd) gated_bwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, d, out, a);
+  else gated_fwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, out, a);
   note_launch();
   return cudaGetLastError();
+}
+template <typename T, int FN, bool Q8> cudaError_t gated_launch(bool bwd, const GatedArgs& a, cudaStream_t st) {
+  // TMA rows start on 16 bytes
+  const bool tma = !a.solo && ((size_t)a.C * (bwd && Q8 ? 1 : sizeof(T))) % 16 == 0;
+  return tma ? gated_launch<T, FN, Q8, true>(bwd, a, st) : gated_launch<T, FN, Q8, false>(bwd, a, st);
 }
 template <typename T> cudaError_t gated_launch(int fn, bool q8, bool bwd, const GatedArgs& a, cudaStream_t st) {
   if (fn == GATED_LINEAR)
@@ -843,8 +949,8 @@ GatedArgs gated_args(const rnn_gated_dims_t* d, const GatedSizes& z, void* works
   char* ws = (char*)workspace;
   a.status = (unsigned*)ws;
   a.ticket = (unsigned*)(ws + 256);
-  a.flags = (unsigned*)(ws + 512);
-  a.maps = (float*)(ws + z.sync);
+  a.states = (unsigned long long*)(ws + 512);
+  a.maps = (ulonglong2*)(ws + 512 + z.states);
   a.wait_limit_ns = wait_limit_ns();
   return a;
 }
@@ -865,7 +971,7 @@ size_t rnn_gated_tape_size(const rnn_gated_dims_t* d) { return gated_dims_ok(d) 
 size_t rnn_gated_workspace_size(const rnn_gated_dims_t* d, int kind) {
   if (!gated_dims_ok(d) || (kind != RNN_WS_FWD && kind != RNN_WS_BWD)) return 0;
   const GatedSizes z = gated_sizes(d);
-  return z.sync + z.maps + z.carry + (kind == RNN_WS_BWD ? z.dbp : 0);
+  return z.sync + (kind == RNN_WS_BWD ? z.dbp : 0);
 }
 
 int rnn_gated_fwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, const void* state0,
@@ -890,7 +996,7 @@ int rnn_gated_fwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
   GatedArgs a = gated_args(d, z, workspace);
   a.Wx = Wx; a.bias = b; a.s0 = (const float*)state0; a.reset = reset; a.lengths = lengths;
   a.h = h; a.last = (float*)last;
-  a.carry = tape ? (float*)tape : (float*)((char*)workspace + z.sync + z.maps);
+  a.carry = (float*)tape;
   const bool q8 = tape && d->checkpoint == RNN_CKPT_INT8;
   if (q8) {
     a.q = (signed char*)tape + z.carry;
@@ -931,8 +1037,7 @@ int rnn_gated_bwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
     a.qs = (unsigned char*)tape + z.carry + z.q;
   }
   a.dh = dh; a.dlast = (const float*)dlast; a.dWx = dWx; a.ds0 = (float*)dstate0;
-  a.dcarry = (float*)((char*)workspace + z.sync + z.maps);
-  a.dbp = db ? (float*)((char*)workspace + z.sync + z.maps + z.carry) : nullptr;
+  a.dbp = db ? (float*)((char*)workspace + z.sync) : nullptr;
   rc = cuda_status(gated_launch(d, q8, true, a, st));
   if (rc || !db) return rc;
   const int cols = z.G * z.C;
