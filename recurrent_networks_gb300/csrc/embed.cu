@@ -4,6 +4,7 @@
 
 #include "gated.cuh"
 #include "kernels.cuh"
+#include "ptx.cuh"
 #include "rnn.h"
 
 namespace rnn {
@@ -68,8 +69,9 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(long long n, int V, int 
 // tokens are sorted by key, equal keys in token order: least significant digit
 // first, DIGIT_MAX bits at most a pass, each pass a count of the digits of
 // every tile of TILE tokens, a scan of the counts in (digit, tile) order and a
-// stable scatter. All counts are whole numbers, so nothing depends on timing.
-constexpr int SORT_THREADS = 256, SORT_WARPS = SORT_THREADS / 32, SORT_ROUNDS = 16;
+// stable scatter, which also counts the next pass's digits by the places it
+// writes to. All counts are whole numbers, so nothing depends on timing.
+constexpr int SORT_THREADS = 256, SORT_WARPS = SORT_THREADS / 32, SORT_ROUNDS = 4;
 constexpr int TILE = SORT_THREADS * SORT_ROUNDS;
 constexpr int DIGIT_MAX = 11;
 
@@ -80,6 +82,8 @@ struct SortArgs {
   const unsigned *kin, *pin;
   unsigned *kout, *pout;
   unsigned* hist;             // [1 << bits][tiles]
+  unsigned* total;            // [1 << bits]
+  unsigned* hist_next;        // the next pass's counts (null in the last one)
   unsigned* status;
   uint4* zero;                // this launch's share of dW to clear, by the blocks past the tiles
   size_t zeros;               // 16-byte units
@@ -99,7 +103,8 @@ __device__ __forceinline__ bool zero_share(const SortArgs& p, int first) {
   return true;
 }
 
-template <typename I, bool FIRST> __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(SortArgs p) {
+// The first pass's counts.
+template <typename I> __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(SortArgs p) {
   if (zero_share(p, p.tiles)) return;
   extern __shared__ unsigned count[];
   const int bins = 1 << p.bits;
@@ -109,59 +114,46 @@ template <typename I, bool FIRST> __global__ void __launch_bounds__(SORT_THREADS
 #pragma unroll
   for (int r = 0; r < SORT_ROUNDS; ++r) {
     const long long i = base + r * SORT_THREADS + threadIdx.x;
-    if (i < p.n) {
-      const unsigned k = FIRST ? key_of((const I*)p.ids, i, p) : p.kin[i];
-      atomicAdd(&count[k >> p.shift & (bins - 1)], 1u);
-    }
+    if (i < p.n) atomicAdd(&count[key_of((const I*)p.ids, i, p) & (bins - 1)], 1u);
   }
   __syncthreads();
   for (int d = threadIdx.x; d < bins; d += SORT_THREADS) p.hist[(size_t)d * p.tiles + blockIdx.x] = count[d];
 }
 
-// Exclusive sum of p.hist in place, one block.
-__global__ void __launch_bounds__(1024) sort_scan_kernel(SortArgs p) {
-  if (zero_share(p, 1)) return;
-  __shared__ unsigned warp_sum[32];
-  const size_t total = (size_t)p.tiles << p.bits;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Exclusive sums of p.hist along the tiles, in place, a warp a digit; the
+// digits' totals go to p.total. Clears the next pass's counts.
+__global__ void __launch_bounds__(SORT_THREADS) sort_scan_kernel(SortArgs p) {
+  const int bins = 1 << p.bits, blocks = (bins + SORT_WARPS - 1) / SORT_WARPS;
+  if (zero_share(p, blocks)) return;
+  const int d = blockIdx.x * SORT_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (d >= bins) return;
+  unsigned* row = p.hist + (size_t)d * p.tiles;
   unsigned carry = 0;
-  for (size_t base = 0; base < total; base += 4096) {
-    const size_t at = base + threadIdx.x * 4;
-    unsigned v[4], s = 0;
+  for (int base = 0; base < p.tiles; base += 128) {
+    unsigned v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = base + q * 32 + lane < p.tiles ? row[base + q * 32 + lane] : 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      v[q] = at + q < total ? p.hist[at + q] : 0;
-      s += v[q];
-    }
-    unsigned inc = s;
+      unsigned inc = v[q];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+      }
+      if (base + q * 32 + lane < p.tiles) row[base + q * 32 + lane] = carry + inc - v[q];
+      carry += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    unsigned before = carry, all = 0;
-#pragma unroll
-    for (int w = 0; w < 32; ++w) {
-      const unsigned t = warp_sum[w];
-      if (w < warp) before += t;
-      all += t;
-    }
-    unsigned x = before + inc - s;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (at + q < total) p.hist[at + q] = x;
-      x += v[q];
-    }
-    carry += all;
-    __syncthreads();
   }
+  if (lane == 0) p.total[d] = carry;
+  if (p.hist_next)
+    for (int t = lane; t < p.tiles; t += 32) p.hist_next[(size_t)d * p.tiles + t] = 0;
 }
 
 template <typename I, bool FIRST> __global__ void __launch_bounds__(SORT_THREADS) sort_scatter_kernel(SortArgs p) {
   if (zero_share(p, p.tiles)) return;
   extern __shared__ unsigned place[];  // [SORT_WARPS][bins]: the warp's counts, then where its next key of a digit goes
+  __shared__ unsigned warp_sum[SORT_WARPS];
   const int bins = 1 << p.bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int d = threadIdx.x; d < bins * SORT_WARPS; d += SORT_THREADS) place[d] = 0;
   __syncthreads();
@@ -174,9 +166,23 @@ template <typename I, bool FIRST> __global__ void __launch_bounds__(SORT_THREADS
     key[r] = i < p.n ? (FIRST ? key_of((const I*)p.ids, i, p) : p.kin[i]) : 0;
     if (i < p.n) atomicAdd(&mine[key[r] >> p.shift & (bins - 1)], 1u);
   }
+  // where a digit's keys begin: the sum of the totals of the digits before it
+  const int per = (bins + SORT_THREADS - 1) / SORT_THREADS, d0 = min(bins, (int)threadIdx.x * per), d1 = min(bins, d0 + per);
+  unsigned sum = 0;
+  for (int d = d0; d < d1; ++d) sum += p.total[d];
+  unsigned inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  for (int d = threadIdx.x; d < bins; d += SORT_THREADS) {
-    unsigned at = p.hist[(size_t)d * p.tiles + blockIdx.x];
+  unsigned begin = inc - sum;
+  for (int w = 0; w < warp; ++w) begin += warp_sum[w];
+  for (int d = d0; d < d1; ++d) {
+    unsigned at = begin + p.hist[(size_t)d * p.tiles + blockIdx.x];
+    begin += p.total[d];
 #pragma unroll
     for (int w = 0; w < SORT_WARPS; ++w) {
       const unsigned c = place[w * bins + d];
@@ -199,6 +205,7 @@ template <typename I, bool FIRST> __global__ void __launch_bounds__(SORT_THREADS
     __syncwarp();
     if (on) {
       p.kout[at] = key[r];
+      if (p.hist_next) atomicAdd(&p.hist_next[(size_t)(key[r] >> (p.shift + p.bits) & (bins - 1)) * p.tiles + at / TILE], 1u);
       p.pout[at] = FIRST ? (unsigned)i : p.pin[i];
     }
   }
@@ -216,71 +223,98 @@ struct SumArgs {
   float* part;  // [pieces][2][E]: sums of a piece's first id (begun in an earlier piece) and last id (going on in the next)
 };
 
-// A warp sums `piece` sorted tokens over 32 vectors of columns, in order. An
-// id whose tokens all lie in the piece is written to dW; what belongs to an
-// id that crosses the piece's ends goes to part.
+// N fp32 partial sums at p (aligned to their size where N is 4 or 8).
+template <int N> __device__ __forceinline__ void store_part(float* p, const float* x) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int q = 0; q < N; q += 4) *(float4*)(p + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < N; ++q) p[q] = x[q];
+  }
+}
+template <int N> __device__ __forceinline__ void load_part(const float* p, float* x) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int q = 0; q < N; q += 4) {
+      const float4 v = *(const float4*)(p + q);
+      x[q] = v.x, x[q + 1] = v.y, x[q + 2] = v.z, x[q + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < N; ++q) x[q] = p[q];
+  }
+}
+
+// A warp sums `piece` (at most 32) sorted tokens over 32 vectors of columns, in
+// order. An id whose tokens all lie in the piece is written to dW; what belongs
+// to an id that crosses the piece's ends goes to part. Bound by the gather of
+// dout's rows: every lane copies its vector of the next RING rows into its own
+// place of a ring in shared memory, so that up to 15 rows a warp are on their
+// way while one is added (two register batches of 4 rows spilled and reached
+// 2.1 TB/s).
+constexpr int PIECE_MAX = 32, RING = 16;
+template <int VB> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  static_assert(VB == 16 || VB == 8 || VB == 4, "cp.async sizes");
+  if constexpr (VB == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(VB) : "memory");
+}
 template <typename T, int VB> __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs p) {
   using X = Vec<T, VB>;
-  constexpr int AHEAD = 8;
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  __shared__ __align__(16) unsigned char ring[8][RING][32 * VB];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long w = (long long)blockIdx.x * 8 + warp;
   const long long piece = w / p.coltiles;
   if (piece >= p.pieces) return;
   const int col = ((int)(w % p.coltiles) * 32 + lane) * X::N;
   const long long i0 = piece * p.piece;
   const int count = (int)min((long long)p.piece, p.n - i0);
-  const T* dout = (const T*)p.dout;
   const unsigned none = 0xffffffffu;
+  const unsigned key = lane < count ? __ldg(p.key + i0 + lane) : none;
+  const unsigned pos = lane < count ? __ldg(p.pos + i0 + lane) : 0;
   const unsigned prev = i0 > 0 ? __ldg(p.key + i0 - 1) : none;
   const unsigned next = i0 + count < p.n ? __ldg(p.key + i0 + count) : none;
+  // the tokens without a gradient come last
+  const int sums = __popc(__ballot_sync(0xffffffffu, key < (unsigned)p.V));
   const bool on = col < p.E;
+  const T* dout = (const T*)p.dout + col;
+  const uint32_t mine = smem_u32(&ring[warp][0][lane * VB]);
+  auto ask = [&](int j, unsigned s) {
+    if (j < sums && on) {
+      if constexpr (VB >= 4)
+        copy_async<VB>(mine + j % RING * 32 * VB, dout + (size_t)s * p.E);
+      else  // rows of odd width: no asynchronous copy of 2 bytes
+        *(X*)&ring[warp][j % RING][lane * VB] = load_vec<T, VB>(dout + (size_t)s * p.E);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int j = 0; j < RING - 1; ++j) ask(j, __shfl_sync(0xffffffffu, pos, j));
   float acc[X::N];
 #pragma unroll
   for (int q = 0; q < X::N; ++q) acc[q] = 0.0f;
   unsigned cur = none;
-  auto flush = [&](bool last) {
-    if (cur == none || cur >= (unsigned)p.V || !on) return;
-    const bool head = cur == prev, tail = last && cur == next;
+  for (int j = 0; j < sums; ++j) {
+    ask(j + RING - 1, __shfl_sync(0xffffffffu, pos, (j + RING - 1) & 31));
+    const unsigned k = __shfl_sync(0xffffffffu, key, j), after = j + 1 < count ? __shfl_sync(0xffffffffu, key, j + 1) : next;
+    asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+    const X x = *(const X*)&ring[warp][j % RING][lane * VB];
+    const bool begin = k != cur;
+    cur = k;
+#pragma unroll
+    for (int q = 0; q < X::N; ++q) acc[q] = (begin ? 0.0f : acc[q]) + to_f(x.v[q]);
+    if (!on || (after == k && j + 1 < count)) continue;
+    const bool head = k == prev, tail = after == k;
     if (!head && !tail) {
-      X x;
+      X y;
 #pragma unroll
-      for (int q = 0; q < X::N; ++q) x.v[q] = from_f<T>(acc[q] * p.scale);
-      store_vec<T, VB>((T*)p.dW + (size_t)cur * p.E + col, x);
+      for (int q = 0; q < X::N; ++q) y.v[q] = from_f<T>(acc[q] * p.scale);
+      store_vec<T, VB>((T*)p.dW + (size_t)k * p.E + col, y);
     } else {
-      float* out = p.part + ((size_t)piece * 2 + (head ? 0 : 1)) * p.E + col;
-#pragma unroll
-      for (int q = 0; q < X::N; ++q) out[q] = acc[q];
-    }
-  };
-  for (int b = 0; b < count; b += 32) {
-    const int m = min(32, count - b);
-    const unsigned k32 = lane < m ? __ldg(p.key + i0 + b + lane) : none;
-    const unsigned s32 = lane < m ? __ldg(p.pos + i0 + b + lane) : 0;
-    for (int j0 = 0; j0 < m; j0 += AHEAD) {
-      X x[AHEAD];
-#pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        const unsigned k = __shfl_sync(0xffffffffu, k32, j0 + j), s = __shfl_sync(0xffffffffu, s32, j0 + j);
-        if (j0 + j < m && k < (unsigned)p.V && on) x[j] = load_vec<T, VB>(dout + (size_t)s * p.E + col);
-      }
-#pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        if (j0 + j >= m) break;
-        const unsigned k = __shfl_sync(0xffffffffu, k32, j0 + j);
-        if (k != cur) {
-          flush(false);
-          cur = k;
-#pragma unroll
-          for (int q = 0; q < X::N; ++q) acc[q] = 0.0f;
-        }
-        if (k < (unsigned)p.V && on) {
-#pragma unroll
-          for (int q = 0; q < X::N; ++q) acc[q] += to_f(x[j].v[q]);
-        }
-      }
+      store_part<X::N>(p.part + ((size_t)piece * 2 + (head ? 0 : 1)) * p.E + col, acc);
     }
   }
-  flush(true);
 }
 
 // The ids that cross pieces: a warp per piece in which such an id begins, over
@@ -288,27 +322,24 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_sum_k
 // LONG pieces is shared by the block's 8 warps, their sums added in order.
 template <typename T, int VB> __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs p) {
   using X = Vec<T, VB>;
-  constexpr int LONG = 32, N = X::N;
+  constexpr int LONG = 12, N = X::N;
   __shared__ long long long_item[8];
   __shared__ long long long_end[8];
   __shared__ float sums[8][32 * N];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto sum = [&](long long from, long long to, int col, float* acc) {  // the first-id sums of pieces from .. to-1
-    long long r = from;
-    for (; r + 4 <= to; r += 4) {
-      float v[4][N];
+    for (long long r = from; r < to; r += 8) {
+      float v[8][N];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 8; ++k)
+        if (r + k < to) load_part<N>(p.part + (size_t)(r + k) * 2 * p.E + col, v[k]);
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[k][q] = p.part[(size_t)(r + k) * 2 * p.E + col + q];
+      for (int k = 0; k < 8; ++k)
+        if (r + k < to) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int q = 0; q < N; ++q) acc[q] += v[k][q];
+          for (int q = 0; q < N; ++q) acc[q] += v[k][q];
+        }
     }
-    for (; r < to; ++r)
-#pragma unroll
-      for (int q = 0; q < N; ++q) acc[q] += p.part[(size_t)r * 2 * p.E + col + q];
   };
   auto write = [&](unsigned id, int col, const float* acc) {
     X x;
@@ -316,9 +347,10 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_join_
     for (int q = 0; q < N; ++q) x.v[q] = from_f<T>(acc[q] * p.scale);
     store_vec<T, VB>((T*)p.dW + (size_t)id * p.E + col, x);
   };
-  const long long w = (long long)blockIdx.x * 8 + warp;
-  const long long piece = w / p.coltiles;
-  const int col = ((int)(w % p.coltiles) * 32 + lane) * N;
+  // a block's warps have neighbouring pieces and the same columns, so that the
+  // column tiles of a long id go to different blocks
+  const long long piece = blockIdx.x / p.coltiles * 8ll + warp;
+  const int col = ((int)(blockIdx.x % p.coltiles) * 32 + lane) * N;
   if (lane == 0) long_item[warp] = -1;
   if (piece + 1 < p.pieces) {
     const long long i1 = (piece + 1) * p.piece;  // the next piece's first token
@@ -336,13 +368,12 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_join_
       }
       if (end - piece > LONG) {
         if (lane == 0) {
-          long_item[warp] = w;
+          long_item[warp] = piece;
           long_end[warp] = end;
         }
       } else if (col < p.E) {
         float acc[N];
-#pragma unroll
-        for (int q = 0; q < N; ++q) acc[q] = p.part[((size_t)piece * 2 + 1) * p.E + col + q];
+        load_part<N>(p.part + ((size_t)piece * 2 + 1) * p.E + col, acc);
         sum(piece + 1, end, col, acc);
         write(id, col, acc);
       }
@@ -351,12 +382,13 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_join_
   __syncthreads();
   for (int s = 0; s < 8; ++s) {
     if (long_item[s] < 0) continue;
-    const long long pc = long_item[s] / p.coltiles, end = long_end[s];
-    const int c = ((int)(long_item[s] % p.coltiles) * 32 + lane) * N;
+    const long long pc = long_item[s], end = long_end[s];
+    const int c = col;
     const long long share = (end - pc - 1 + 7) / 8, from = min(end, pc + 1 + warp * share), to = min(end, from + share);
     float acc[N];
 #pragma unroll
-    for (int q = 0; q < N; ++q) acc[q] = warp == 0 && c < p.E ? p.part[((size_t)pc * 2 + 1) * p.E + c + q] : 0.0f;
+    for (int q = 0; q < N; ++q) acc[q] = 0.0f;
+    if (warp == 0 && c < p.E) load_part<N>(p.part + ((size_t)pc * 2 + 1) * p.E + c, acc);
     if (c < p.E) sum(from, to, c, acc);
 #pragma unroll
     for (int q = 0; q < N; ++q) sums[warp][lane * N + q] = acc[q];
@@ -471,13 +503,13 @@ EmbedPlan embed_plan(long long n, int V, int E) {
   z.passes = (bits + DIGIT_MAX - 1) / DIGIT_MAX;
   z.bits = (bits + z.passes - 1) / z.passes;
   z.tiles = (int)((n + TILE - 1) / TILE);
-  // 64 tokens a warp keep the partial sums' traffic low; fewer when the warps
-  // would not fill the GPU
-  z.piece = 64;
+  // 32 tokens a warp keep the partial sums' traffic low (two fp32 rows for 32
+  // rows at most); fewer when the warps would not fill the GPU
+  z.piece = PIECE_MAX;
   const long long cols = (E + 255) / 256;
   while (z.piece > 8 && n / z.piece * cols < 8 * device_sms()) z.piece /= 2;
   z.pieces = (n + z.piece - 1) / z.piece;
-  z.hist = up256(((size_t)z.tiles << z.bits) * sizeof(unsigned));
+  z.hist = up256((((size_t)2 * z.tiles + 1) << z.bits) * sizeof(unsigned));  // two passes' counts, and the digits' totals
   z.list = up256((size_t)n * sizeof(unsigned));
   z.part = up256((size_t)z.pieces * 2 * E * sizeof(float));
   z.total = 256 + z.hist + 4 * z.list + z.part;
@@ -524,13 +556,15 @@ cudaError_t embed_bwd_launch(long long n, int V, int E, const void* ids, long lo
   s.n = n; s.pad = pad; s.V = V; s.tiles = z.tiles; s.bits = z.bits;
   s.ids = ids;
   s.status = (unsigned*)ws;
-  s.hist = (unsigned*)(ws + 256);
+  unsigned* const counts = (unsigned*)(ws + 256);
+  const size_t count_words = (size_t)z.tiles << z.bits;
+  s.total = counts + 2 * count_words;
   unsigned* list[4];
   for (int k = 0; k < 4; ++k) list[k] = (unsigned*)(ws + 256 + z.hist + k * z.list);
   // The sort is a chain of short launches that leaves most of the GPU idle:
   // the blocks past its tiles clear dW meanwhile, a share in each launch.
   const size_t bytes = (size_t)V * E * sizeof(T), units = bytes / 16;
-  const int launches = 3 * z.passes;
+  const int launches = 2 * z.passes + 1;
   const size_t share = (units + launches - 1) / launches;
   if (bytes % 16) {
     e = cudaMemsetAsync((char*)dW + units * 16, 0, bytes % 16, st);
@@ -552,18 +586,23 @@ cudaError_t embed_bwd_launch(long long n, int V, int E, const void* ids, long lo
       const size_t want = (s.zeros + 1023) / 1024;
       return (int)(want < (size_t)4 * sms ? want : (size_t)4 * sms);
     };
-    int more = clear();
-    if (first) sort_count_kernel<I, true><<<z.tiles + more, SORT_THREADS, smem / SORT_WARPS, st>>>(s);
-    else sort_count_kernel<I, false><<<z.tiles + more, SORT_THREADS, smem / SORT_WARPS, st>>>(s);
+    s.hist = counts + pass % 2 * count_words;
+    s.hist_next = pass + 1 < z.passes ? counts + (pass + 1) % 2 * count_words : nullptr;
+    int more;
+    if (first) {
+      more = clear();
+      sort_count_kernel<I><<<z.tiles + more, SORT_THREADS, smem / SORT_WARPS, st>>>(s);
+      note_launch();
+    }
     more = clear();
-    sort_scan_kernel<<<1 + (more + 3) / 4, 1024, 0, st>>>(s);
+    sort_scan_kernel<<<((1 << z.bits) + SORT_WARPS - 1) / SORT_WARPS + more, SORT_THREADS, 0, st>>>(s);
     more = clear();
     const void* k = first ? (const void*)sort_scatter_kernel<I, true> : (const void*)sort_scatter_kernel<I, false>;
     e = set_smem_attr(k, smem);
     if (e != cudaSuccess) return e;
     if (first) sort_scatter_kernel<I, true><<<z.tiles + more, SORT_THREADS, smem, st>>>(s);
     else sort_scatter_kernel<I, false><<<z.tiles + more, SORT_THREADS, smem, st>>>(s);
-    note_launch(3);
+    note_launch(2);
   }
   SumArgs a{};
   a.n = n; a.V = V; a.E = E; a.piece = z.piece; a.pieces = z.pieces;
@@ -573,7 +612,7 @@ cudaError_t embed_bwd_launch(long long n, int V, int E, const void* ids, long lo
   a.part = (float*)(ws + 256 + z.hist + 4 * z.list);
   const unsigned blocks = (unsigned)((z.pieces * a.coltiles + 7) / 8);
   embed_sum_kernel<T, VB><<<blocks, 256, 0, st>>>(a);
-  embed_join_kernel<T, VB><<<blocks, 256, 0, st>>>(a);
+  embed_join_kernel<T, VB><<<(unsigned)((z.pieces + 7) / 8 * a.coltiles), 256, 0, st>>>(a);
   note_launch(2);
   return cudaGetLastError();
 }

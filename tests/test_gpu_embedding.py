@@ -66,6 +66,12 @@ def test_parity(size, dtype):
     check(zipf(n, V, seed=n), V, E, dtype, scale=0.5 + E ** 0.5, id_dtype=torch.int32 if n % 2 else torch.int64)
 
 
+def test_more_ids_than_two_digits_hold():
+    ids = np.random.default_rng(1).integers(0, 5_000_000, 3000)
+    ids[:1000] = ids[2000]
+    check(ids, 5_000_000, 3, BF)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 def test_one_id_for_every_token(dtype):
     check(np.full(5000, 3), 8, 72, dtype)
