@@ -112,6 +112,30 @@ __device__ __forceinline__ FV<2> bytes_f(uint32_t w, FV<2>*) {
 }
 __device__ __forceinline__ FV<1> bytes_f(uint32_t w, FV<1>*) { return {{(float)(signed char)w}}; }
 
+// The largest magnitudes of a lane's channels, in the storage type's bits (an
+// infinity or NaN stays one), and the fp32 bits of channel v.
+template <typename T> __device__ __forceinline__ uint32_t mag_max(uint32_t top, uint32_t x);
+template <> __device__ __forceinline__ uint32_t mag_max<float>(uint32_t top, uint32_t x) { return max(top, x & 0x7fffffffu); }
+template <> __device__ __forceinline__ uint32_t mag_max<__nv_bfloat16>(uint32_t top, uint32_t x) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(top), "r"(x & 0x7fff7fffu));
+  return r;
+}
+template <typename T> __device__ __forceinline__ uint32_t mag_bits(uint32_t top, int v) {
+  return sizeof(T) == 4 ? top : v ? top & 0xffff0000u : top << 16;
+}
+// q of a lane's channels as bytes: a / 2^e + 1.5 2^23 rounds to nearest even
+// and leaves q in the low byte. `huge`: some block may saturate (act_scale_byte).
+template <int N> __device__ __forceinline__ uint32_t quant(const FV<N>& a, const FV<N>& inv, bool huge) {
+  FV<N> t = mul(a, inv);
+  if (huge) {
+#pragma unroll
+    for (int v = 0; v < N; ++v) t.v[v] = fminf(fmaxf(t.v[v], -127.0f), 127.0f);
+  }
+  t = add(t, splat<N>(12582912.0f));
+  return N == 1 ? __float_as_uint(t.v[0]) & 255u : __byte_perm(__float_as_uint(t.v[0]), __float_as_uint(t.v[N - 1]), 0x0040) & 0xffffu;
+}
+
 // A lane's channels at p (n of them inside the row: 0 .. N), and back. `wide`:
 // the row starts on 4 bytes.
 template <typename T> __device__ __forceinline__ uint32_t load_lane(const T* p, int n, bool wide) {
@@ -325,15 +349,53 @@ template <int N, bool REVERSE> struct Chain {
 };
 
 // A warp's steps of a tile whose rows (t, g) are 128 bytes, by the lanes' own
-// loads (rows that TMA cannot take). Rows past `live` are not read.
+// asynchronous copies (rows that TMA cannot take). Rows past `live` are not
+// read. An odd number of 2-byte channels puts every other row 2 bytes off: then
+// the words that hold the row are copied, the 33rd into `extra` [STEPS ROWS],
+// and fetch_align shifts the row once they are there.
 template <typename T, int ROWS>
-__device__ __forceinline__ void fetch_lanes(const GatedArgs& p, const Item& it, const T* src, uint32_t* dst) {
-  const int lane = threadIdx.x & 31;
-  const bool wide = p.C % 2 == 0 || sizeof(T) == 4;
-  const T* at = src + ((size_t)it.b * p.T + it.t0) * ROWS * p.C + it.ch;
+__device__ __forceinline__ void fetch_lanes(const GatedArgs& p, const Item& it, const T* src, uint32_t* dst, uint32_t* extra) {
+  const int lane = threadIdx.x & 31, rows = it.live * ROWS;
+  const size_t row0 = ((size_t)it.b * p.T + it.t0) * ROWS;
+  const uint32_t to = smem_u32(dst + lane);
+  if (p.C % 2 == 0 || sizeof(T) == 4) {
+    const T* at = src + row0 * p.C + it.ch;
+    if (it.n > 0) {
 #pragma unroll 8
-  for (int r = 0; r < it.live * ROWS; ++r) dst[r * 32 + lane] = load_lane(at + (size_t)r * p.C, it.n, wide);
+      for (int r = 0; r < rows; ++r)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + r * 128), "l"(at + (size_t)r * p.C) : "memory");
+    }
+  } else {
+    const size_t all = (size_t)p.B * p.T * ROWS * p.C;  // (the tensor's last word may be half a word)
+    const int width = min(p.C - it.ct, 64);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const size_t e0 = (row0 + r) * p.C + it.ct, end = e0 + width, e = (e0 & ~(size_t)1) + 2 * lane;
+      if (e < end)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + r * 128), "l"(src + e),
+                     "r"(e + 1 < all ? 4 : 2)
+                     : "memory");
+      if (lane == 0 && e + 64 < end)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(extra + r)), "l"(src + e + 64),
+                     "r"(e + 65 < all ? 4 : 2)
+                     : "memory");
+    }
+  }
 }
+template <typename T, int ROWS>
+__device__ __forceinline__ void fetch_align(const GatedArgs& p, const Item& it, uint32_t* dst, const uint32_t* extra) {
+  if (p.C % 2 == 0 || sizeof(T) == 4) return;
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  size_t e0 = ((size_t)it.b * p.T + it.t0) * ROWS * p.C + it.ct;
+  for (int r = 0; r < it.live * ROWS; ++r, e0 += p.C) {
+    if (!(e0 & 1)) continue;
+    const uint32_t w = dst[r * 32 + lane], up = __shfl_down_sync(0xffffffffu, w, 1);
+    dst[r * 32 + lane] = w >> 16 | (lane < 31 ? up : extra[r]) << 16;
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A lane's biases, scaled as the gates want them.
 template <typename T, int FN, int N> __device__ __forceinline__ void load_bias(const GatedArgs& p, const Item& it, FV<N>* bias) {
@@ -361,15 +423,18 @@ template <typename F> __device__ __forceinline__ void by_mask(const Item& it, F&
 // are not read again, so that f alone stays in registers.
 template <typename T, int FN, bool Q8, bool TMA>
 __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
-    gated_fwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap hmap, GatedArgs p) {
+    gated_fwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap hmap,
+                     const __grid_constant__ CUtensorMap qmap, GatedArgs p) {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
+  constexpr bool TMAQ = Q8 && TMA;  // (the rows of bytes are 16-byte multiples then, too)
   constexpr int U0 = FN == GATED_LINEAR ? 0 : 1, U1 = FN == GATED_LINEAR ? 2 : 0;  // rows that hold u of channel 0, 1
   extern __shared__ __align__(128) unsigned char smem[];
   uint32_t* tile = (uint32_t*)smem;                                   // [WARPS][STEPS][G][32]
   float2* maps = (float2*)(tile + WARPS * STEPS * G * 32);            // [WARPS][N][32]
   float* enter = (float*)(maps + WARPS * 32 * N);                     // [WARPS][N][32]: the states that enter the warps
-  uint32_t* tops = (uint32_t*)(enter + WARPS * 32 * N);                       // Q8: [WARPS][G][N][32]
-  unsigned long long* bars = (unsigned long long*)(tops + (Q8 ? WARPS * G * 32 * N : 0));  // [WARPS]
+  uint32_t* tops = (uint32_t*)(enter + WARPS * 32 * N);               // Q8: [WARPS][G][32]
+  unsigned char* qtile = (unsigned char*)(tops + (Q8 ? WARPS * G * 32 : 0));  // Q8: [WARPS][STEPS][G][32 N]
+  unsigned long long* bars = (unsigned long long*)(qtile + (Q8 ? WARPS * STEPS * G * 32 * N : 0));  // [WARPS]
   int4* shared = (int4*)(bars + WARPS);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bar = smem_u32(bars + warp);
@@ -378,6 +443,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
     fence_mbar_init_cluster();
   }
   uint32_t* mine = tile + warp * STEPS * G * 32;
+  uint32_t* extra = (uint32_t*)enter + warp * STEPS * G;  // (free until all warps have their maps)
   bool failed = false;
   if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
   if (threadIdx.x == 0) *shared = place_of<false>(p, p.solo ? blockIdx.x : atomicAdd(p.ticket, 1u));
@@ -390,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
       tma_load_4d(smem_u32(mine), &xmap, bar, it.ct, 0, it.t0, it.b);
     }
   } else {
-    fetch_lanes<T, G>(p, it, (const T*)p.Wx, mine);
+    fetch_lanes<T, G>(p, it, (const T*)p.Wx, mine, extra);
   }
   FV<N> bias[G];
   load_bias<T, FN, N>(p, it, bias);
@@ -400,14 +466,17 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
     if (p.s0) x = load_f<N, false>(p.s0, it.b, p, it);
     chain.ask();
   }
-  if (TMA && it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
+  if (TMA) {
+    if (it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
+  } else {
+    fetch_wait();
+    fetch_align<T, G>(p, it, mine, extra);
+  }
 
   FV<N> f[STEPS], u[Q8 ? STEPS : 1], P = splat<N>(1.0f), H = splat<N>(0.0f);
-  uint32_t top[G][N];
+  uint32_t top[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g)
-#pragma unroll
-    for (int v = 0; v < N; ++v) top[g][v] = 0;
+  for (int g = 0; g < G; ++g) top[g] = 0;
   by_mask(it, [&](auto mask) {
     constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
@@ -416,12 +485,9 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
       FV<N> z[G], w;
 #pragma unroll
       for (int g = 0; g < (FN == GATED_LINEAR && !Q8 ? G - 1 : G); ++g) {  // o is read when it is needed
-        const FV<N> a = Lane<T>::unpack(mine[(j * G + g) * 32 + lane]);
-        if (Q8) {
-#pragma unroll
-          for (int v = 0; v < N; ++v) top[g][v] = max(top[g][v], on ? __float_as_uint(fabsf(a.v[v])) : 0u);
-        }
-        z[g] = gate<FN>(g, a, bias[g]);
+        const uint32_t raw = mine[(j * G + g) * 32 + lane];
+        if (Q8) top[g] = on ? mag_max<T>(top[g], raw) : top[g];
+        z[g] = gate<FN>(g, Lane<T>::unpack(raw), bias[g]);
       }
       gated_coeff<FN, N>(z, f[j], w);
       if (MASK) {
@@ -441,10 +507,10 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
 #pragma unroll
   for (int v = 0; v < N; ++v) {
     maps[(warp * N + v) * 32 + lane] = make_float2(P.v[v], H.v[v]);
-    if (Q8) {
+  }
+  if (Q8) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) tops[((warp * G + g) * N + v) * 32 + lane] = top[g][v];
-    }
+    for (int g = 0; g < G; ++g) tops[(warp * G + g) * 32 + lane] = top[g];
   }
   __syncthreads();
   if (warp == 0) {
@@ -475,37 +541,51 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
   const bool wide = p.C % 2 == 0;
   if (Q8) {  // beside the wait for the state: the tile in 8 bits
     const int qblocks = (p.T + ACT_BLOCK - 1) / ACT_BLOCK;
-    float inv[G][N];
-    bool fin[G][N];
+    FV<N> inv[G];
+    bool huge = false, odd = false;  // a block that saturates, a block that is not finite
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+    for (int g = 0; g < G; ++g) {
+      const uint32_t both = mag_max<T>(top[g], tops[((warp ^ 1) * G + g) * 32 + lane]);
 #pragma unroll
       for (int v = 0; v < N; ++v) {
-        const uint32_t t = max(top[g][v], tops[(((warp ^ 1) * G + g) * N + v) * 32 + lane]);
-        const unsigned s = act_scale_byte(__uint_as_float(t));
-        inv[g][v] = act_inv_scale(s);
-        fin[g][v] = s != ACT_NONFINITE;
+        const unsigned s = act_scale_byte(__uint_as_float(mag_bits<T>(both, v)));
+        inv[g].v[v] = act_inv_scale(s);
+        huge |= s == 248;
+        odd |= s == ACT_NONFINITE;
         if ((warp & 1) == 0 && v < it.n && it.t0 < p.T)
           p.qs[(((size_t)it.b * qblocks + it.t0 / ACT_BLOCK) * G + g) * p.C + it.ch + v] = (unsigned char)s;
       }
-    signed char* q = p.q + ((size_t)it.b * p.T + it.t0) * G * p.C + it.ch;
-#pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
-      if (it.t0 + j >= p.T) break;
+    }
+    huge = __any_sync(0xffffffffu, huge);
+    odd = __any_sync(0xffffffffu, odd);
+    unsigned char* qmine = qtile + warp * STEPS * G * 32 * N;
+#pragma unroll 4
+    for (int j = 0; j < STEPS; ++j)
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const FV<N> a = Lane<T>::unpack(mine[(j * G + g) * 32 + lane]);
-        int b8[N];
-#pragma unroll
-        for (int v = 0; v < N; ++v) b8[v] = j < it.live && fin[g][v] ? act_quant(a.v[v], inv[g][v]) : 0;
-        signed char* at = q + (size_t)(j * G + g) * p.C;
-        if (N == 2 && wide && it.n == 2)
-          *(unsigned short*)at = (unsigned short)((b8[0] & 255) | (b8[N - 1] & 255) << 8);
-        else
+        uint32_t w = quant(Lane<T>::unpack(mine[(j * G + g) * 32 + lane]), inv[g], huge);
+        if (j >= it.live) w = 0;
+        if (odd) {
 #pragma unroll
           for (int v = 0; v < N; ++v)
-            if (v < it.n) at[v] = (signed char)b8[v];
+            if (inv[g].v[v] == 0.0f) w &= ~(255u << (8 * v));
+        }
+        if (N == 2) *(unsigned short*)(qmine + (j * G + g) * 64 + lane * 2) = (unsigned short)w;
+        else qmine[(j * G + g) * 32 + lane] = (unsigned char)w;
       }
+    if (TMAQ) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && it.t0 < p.T) {
+        tma_store_4d(&qmap, smem_u32(qmine), it.ct, 0, it.t0, it.b);
+        bulk_commit_group();
+      }
+    } else {
+      signed char* q = p.q + ((size_t)it.b * p.T + it.t0) * G * p.C + it.ch;
+      for (int r = 0; r < STEPS * G && it.t0 + r / G < p.T; ++r)
+#pragma unroll
+        for (int v = 0; v < N; ++v)
+          if (v < it.n) q[(size_t)r * p.C + v] = (signed char)qmine[r * 32 * N + lane * N + v];
     }
   }
   __syncthreads();
@@ -563,8 +643,10 @@ __global__ void __launch_bounds__(THREADS, 2)
   uint32_t* dtile = (uint32_t*)(tile + WARPS * STEPS * G * XB);        // [WARPS][STEPS][32]
   float* maps = (float*)(dtile + WARPS * STEPS * 32);                  // [WARPS][3][N][32]: P, H (state), E (gradient)
   float* enter = maps + WARPS * 3 * 32 * N;                            // [WARPS][N][32]
-  float* dbs = enter + WARPS * 32 * N;                                         // [WARPS][G][N][32]
-  unsigned long long* bars = (unsigned long long*)(dbs + WARPS * G * 32 * N);
+  float* dbs = enter + WARPS * 32 * N;                                 // [WARPS][G][N][32]
+  uint32_t* ring = (uint32_t*)(dbs + WARPS * G * 32 * N);              // Q8: [WARPS][8 steps][G][32]
+  uint32_t* omine = ring + (threadIdx.x >> 5) * (Q8 ? 8 * G * 32 : 0);
+  unsigned long long* bars = (unsigned long long*)(ring + (Q8 ? WARPS * 8 * G * 32 : 0));
   int4* shared = (int4*)(bars + WARPS);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bar = smem_u32(bars + warp);
@@ -574,6 +656,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   unsigned char* mine = tile + warp * STEPS * G * XB;
   uint32_t* dmine = dtile + warp * STEPS * 32;
+  uint32_t* extra = (uint32_t*)dbs + warp * STEPS * (G + 1);  // (free until the sums are written)
   const bool wide = p.C % 2 == 0;
   bool failed = false;
   if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
@@ -600,9 +683,9 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int v = 0; v < N; ++v)
           mine[r * XB + lane * N + v] = v < it.n ? (unsigned char)__ldg(at + (size_t)r * p.C + v) : 0;
     } else {
-      fetch_lanes<T, G>(p, it, (const T*)p.Wx, (uint32_t*)mine);
+      fetch_lanes<T, G>(p, it, (const T*)p.Wx, (uint32_t*)mine, extra);
     }
-    if (p.dh) fetch_lanes<T, 1>(p, it, (const T*)p.dh, dmine);
+    if (p.dh) fetch_lanes<T, 1>(p, it, (const T*)p.dh, dmine, extra + STEPS * G);
   }
   FV<N> bias[G], scale[Q8 ? G : 1];
   load_bias<T, FN, N>(p, it, bias);
@@ -624,7 +707,13 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (p.dlast) x = load_f<N, false>(p.dlast, it.b, p, it);
     chain.ask();
   }
-  if (TMA && it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
+  if (TMA) {
+    if (it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
+  } else {
+    fetch_wait();
+    if (!Q8) fetch_align<T, G>(p, it, (uint32_t*)mine, extra);
+    if (p.dh) fetch_align<T, 1>(p, it, dmine, extra + STEPS * G);
+  }
 
   auto gate_at = [&](int j, int g) {
     if (Q8) {
@@ -714,7 +803,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   // dWx leaves through the tile (in place of the pre-activations it came from)
   // and one TMA store a warp; from the registers where the tile holds bytes or
   // TMA cannot take the rows
-  constexpr bool staged = !Q8 && TMA;
+  constexpr bool staged = !Q8 && TMA, ringed = Q8 && TMA;
   T* out = p.dWx ? (T*)p.dWx + ((size_t)it.b * p.T + it.t0) * G * p.C + it.ch : nullptr;
   by_mask(it, [&](auto mask) {
     constexpr bool MASK = decltype(mask)::value;
@@ -734,8 +823,20 @@ __global__ void __launch_bounds__(THREADS, 2)
         db[g] = add(db[g], da[g]);
         if (staged)
           *(uint32_t*)(mine + (j * G + g) * XB + lane * 4) = Lane<T>::pack(da[g]);
+        else if (ringed)
+          omine[((j & 7) * G + g) * 32 + lane] = Lane<T>::pack(da[g]);
         else if (out && it.t0 + j < p.T)
           store_lane(out + (size_t)(j * G + g) * p.C, Lane<T>::pack(da[g]), it.n, wide);
+      }
+      if (ringed && j % 4 == 0) {  // four steps are whole: their store, and the place of the four before is free
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && p.dWx && it.t0 + j < p.T) {
+          tma_store_4d(&omap, smem_u32(omine + (j & 4) * G * 32), it.ct, 0, it.t0 + j, it.b);
+          bulk_commit_group();
+          bulk_wait_group_read<1>();
+        }
+        __syncwarp();
       }
     }
   });
@@ -761,7 +862,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       if (ch < p.C) p.dbp[(((size_t)it.b * p.chunks + it.k) * G + g) * p.C + ch] = s;
     }
   }
-  if (staged && lane == 0) bulk_wait_group_read<0>();  // the tile is read from until then
+  if (TMA && lane == 0) bulk_wait_group_read<0>();  // the tile is read from until then
   if (threadIdx.x == 0) *shared = place_of<true>(p, next);
   __syncthreads();
   }
@@ -769,12 +870,12 @@ __global__ void __launch_bounds__(THREADS, 2)
 
 template <typename T, int FN, bool Q8> constexpr int fwd_smem() {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
-  return WARPS * STEPS * G * 128 + WARPS * 32 * N * 8 + WARPS * 32 * N * 4 + (Q8 ? WARPS * G * 32 * N * 4 : 0) + WARPS * 8 + 16;
+  return WARPS * STEPS * G * 128 + WARPS * 32 * N * 8 + WARPS * 32 * N * 4 + (Q8 ? WARPS * G * 32 * (4 + STEPS * N) : 0) + WARPS * 8 + 16;
 }
 template <typename T, int FN, bool Q8> constexpr int bwd_smem() {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
   return WARPS * STEPS * (G * (Q8 ? 32 * N : 128) + 128) + WARPS * 3 * 32 * N * 4 + WARPS * 32 * N * 4 + WARPS * G * 32 * N * 4 +
-         WARPS * 8 + 16;
+         (Q8 ? WARPS * 8 * G * 128 : 0) + WARPS * 8 + 16;
 }
 
 // db[j] = sum over `rows` of dbp[row][j], in row order within 8 interleaved
@@ -897,21 +998,22 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
 }
 
 // [C][rows][T][B] box of one warp's steps; elem: 1, 2 or 4 bytes
-cudaError_t tile_map(CUtensorMap* m, const void* base, int elem, const GatedArgs& a, int rows, int width) {
+cudaError_t tile_map(CUtensorMap* m, const void* base, int elem, const GatedArgs& a, int rows, int width, int steps = STEPS) {
   const unsigned long long dims[4] = {(unsigned long long)a.C, (unsigned long long)rows, (unsigned long long)a.T,
                                       (unsigned long long)a.B};
-  const unsigned box[4] = {(unsigned)width, (unsigned)rows, (unsigned)STEPS, 1};
+  const unsigned box[4] = {(unsigned)width, (unsigned)rows, (unsigned)steps, 1};
   return encode_tensor_map(m, base, elem, 4, dims, box);
 }
 
 template <typename T, int FN, bool Q8, bool TMA> cudaError_t gated_launch(bool bwd, const GatedArgs& a, cudaStream_t st) {
   constexpr int G = gated_gates(FN), width = 32 * Lane<T>::N;
-  CUtensorMap x = {}, d = {}, out = {};
+  CUtensorMap x = {}, d = {}, out = {}, q = {};
   if (TMA) {
     cudaError_t e = bwd && Q8 ? tile_map(&x, a.q, 1, a, G, width) : tile_map(&x, a.Wx, (int)sizeof(T), a, G, width);
     if (e == cudaSuccess && bwd && a.dh) e = tile_map(&d, a.dh, (int)sizeof(T), a, 1, width);
+    if (e == cudaSuccess && !bwd && Q8) e = tile_map(&q, a.q, 1, a, G, width);
     if (e == cudaSuccess && !bwd) e = tile_map(&out, a.h, (int)sizeof(T), a, 1, width);
-    if (e == cudaSuccess && bwd && a.dWx && !Q8) e = tile_map(&out, a.dWx, (int)sizeof(T), a, G, width);
+    if (e == cudaSuccess && bwd && a.dWx) e = tile_map(&out, a.dWx, (int)sizeof(T), a, G, width, Q8 ? 4 : STEPS);
     if (e != cudaSuccess) return e;
   }
   const unsigned items = (unsigned)((size_t)a.B * a.tiles_c * a.chunks);
@@ -922,13 +1024,13 @@ template <typename T, int FN, bool Q8, bool TMA> cudaError_t gated_launch(bool b
   // as many CTAs as the SMs hold (see the kernels' launch bounds)
   const unsigned most = device_sms() * (bwd || Q8 ? 2 : 3), ctas = a.solo || items < most ? items : most;
   if (bwd) gated_bwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, d, out, a);
-  else gated_fwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, out, a);
+  else gated_fwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, out, q, a);
   note_launch();
   return cudaGetLastError();
 }
 template <typename T, int FN, bool Q8> cudaError_t gated_launch(bool bwd, const GatedArgs& a, cudaStream_t st) {
   // TMA rows start on 16 bytes
-  const bool tma = !a.solo && ((size_t)a.C * (bwd && Q8 ? 1 : sizeof(T))) % 16 == 0;
+  const bool tma = !a.solo && ((size_t)a.C * (Q8 ? 1 : sizeof(T))) % 16 == 0;
   return tma ? gated_launch<T, FN, Q8, true>(bwd, a, st) : gated_launch<T, FN, Q8, false>(bwd, a, st);
 }
 template <typename T> cudaError_t gated_launch(int fn, bool q8, bool bwd, const GatedArgs& a, cudaStream_t st) {
