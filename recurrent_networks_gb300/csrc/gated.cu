@@ -47,7 +47,13 @@ struct GatedArgs {
   const float* dlast;
   void* dWx;
   float* ds0;
-  float* dbp;                // [B chunks][G][C]
+  // db, by db_mode: 0 none; 1 each item's sums to dbp [B chunks][G][C], added by
+  // a launch of their own; 2 the last item of a channel tile to finish adds
+  // them, in the items' order; 3 a CTA has all items of a channel tile
+  int db_mode;
+  float* dbp;
+  void* db;
+  unsigned* done;            // [tiles_c], zeroed (mode 2)
   unsigned long long* states;  // [groups][tiles][N][32]: the state (or its gradient) that enters a group
   ulonglong2* maps;            // [chunks][tiles][N][32]: the chunks' maps (P, H)
   unsigned* status;
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   unsigned char* mine = tile + warp * STEPS * G * XB;
   uint32_t* dmine = dtile + warp * STEPS * 32;
-  uint32_t* extra = (uint32_t*)dbs + warp * STEPS * (G + 1);  // (free until the sums are written)
+  uint32_t* extra = (uint32_t*)(maps + warp * 3 * 32 * N);  // (the warp's own maps come after)
   const bool wide = p.C % 2 == 0;
   bool failed = false;
   if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
@@ -848,34 +854,60 @@ __global__ void __launch_bounds__(THREADS, 2)
       bulk_commit_group();
     }
   }
-  if (p.dbp) {
+  if (p.db_mode) {
+    float* mine_db = dbs + warp * G * N * 32 + lane;
+    const bool more = p.db_mode == 3 && it.b > 0;  // (mode 3: a channel tile's items come in the order of b)
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int v = 0; v < N; ++v) dbs[((warp * G + g) * N + v) * 32 + lane] = db[g].v[v];
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * 32 * N; i += THREADS) {
-      float s = 0.0f;
+      for (int v = 0; v < N; ++v) mine_db[(g * N + v) * 32] = more ? mine_db[(g * N + v) * 32] + db[g].v[v] : db[g].v[v];
+    if (p.db_mode != 3 || it.b + 1 == p.B) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < G * 32 * N; i += THREADS) {
+        float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) s += dbs[w * G * 32 * N + i];
-      const int g = i / (32 * N), ch = it.ct + i % 32 * N + i / 32 % N;
-      if (ch < p.C) p.dbp[(((size_t)it.b * p.chunks + it.k) * G + g) * p.C + ch] = s;
+        for (int w = 0; w < WARPS; ++w) s += dbs[w * G * 32 * N + i];
+        const int g = i / (32 * N), ch = it.ct + i % 32 * N + i / 32 % N;
+        if (ch < p.C) {
+          if (p.db_mode == 3) ((T*)p.db)[(size_t)g * p.C + ch] = from_f<T>(s);
+          else __stcg(p.dbp + (((size_t)it.b * p.chunks + it.k) * G + g) * p.C + ch, s);
+        }
+      }
+    }
+    if (p.db_mode == 2) {
+      __threadfence();  // this thread's sums, before the count
+      __syncthreads();
+      if (threadIdx.x == 0) shared[1].x = (int)atomicAdd(p.done + it.ct / (32 * N), 1u);
+      __syncthreads();
+      const int rows = p.B * p.chunks;
+      if (shared[1].x == rows - 1) {
+        __threadfence();
+        for (int i = threadIdx.x; i < G * 32 * N; i += THREADS) {
+          const int g = i / (32 * N), ch = it.ct + i % (32 * N);
+          if (ch >= p.C) continue;
+          const float* at = p.dbp + (size_t)g * p.C + ch;
+          float s = 0.0f;
+#pragma unroll 16
+          for (int r = 0; r < rows; ++r) s += __ldcg(at + (size_t)r * G * p.C);
+          ((T*)p.db)[(size_t)g * p.C + ch] = from_f<T>(s);
+        }
+      }
     }
   }
   if (TMA && lane == 0) bulk_wait_group_read<0>();  // the tile is read from until then
-  if (threadIdx.x == 0) *shared = place_of<true>(p, next);
+  if (threadIdx.x == 0) *shared = place_of<true>(p, p.db_mode == 3 ? it.tile + p.tiles_c : next);
   __syncthreads();
   }
 }
 
 template <typename T, int FN, bool Q8> constexpr int fwd_smem() {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
-  return WARPS * STEPS * G * 128 + WARPS * 32 * N * 8 + WARPS * 32 * N * 4 + (Q8 ? WARPS * G * 32 * (4 + STEPS * N) : 0) + WARPS * 8 + 16;
+  return WARPS * STEPS * G * 128 + WARPS * 32 * N * 8 + WARPS * 32 * N * 4 + (Q8 ? WARPS * G * 32 * (4 + STEPS * N) : 0) + WARPS * 8 + 32;
 }
 template <typename T, int FN, bool Q8> constexpr int bwd_smem() {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
   return WARPS * STEPS * (G * (Q8 ? 32 * N : 128) + 128) + WARPS * 3 * 32 * N * 4 + WARPS * 32 * N * 4 + WARPS * G * 32 * N * 4 +
-         (Q8 ? WARPS * 8 * G * 128 : 0) + WARPS * 8 + 16;
+         (Q8 ? WARPS * 8 * G * 128 : 0) + WARPS * 8 + 32;
 }
 
 // db[j] = sum over `rows` of dbp[row][j], in row order within 8 interleaved
@@ -960,7 +992,7 @@ bool gated_dims_ok(const rnn_gated_dims_t* d) {
 }
 
 struct GatedSizes {
-  int G, C, chunks, qblocks, tiles_c, span, solo;
+  int G, C, chunks, qblocks, tiles_c, span, solo, db_mode;
   size_t esize, carry, q, qs, tape;
   size_t sync, states, maps, dbp;  // workspace: status, ticket, states and maps (sync: zeroed by every call) | db sums
 };
@@ -992,7 +1024,12 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   const size_t groups = (z.chunks + z.span - 1) / z.span;
   z.states = z.chunks > 1 ? up256(groups * lanes * sizeof(unsigned long long)) : 0;
   z.maps = z.chunks > 1 && z.span > 1 ? up256(z.chunks * lanes * sizeof(ulonglong2)) : 0;
-  z.sync = 512 + z.states + z.maps;
+  // db: with few batch rows of one chunk, a CTA takes a channel tile's rows one
+  // after the other; with few items, the last one adds the items' sums (16
+  // loads in flight, a round trip of a microsecond each); else a launch does.
+  const long long rows = (long long)d->B * z.chunks;
+  z.db_mode = z.solo && d->B <= 8 ? 3 : !z.solo && rows <= 128 ? 2 : 1;
+  z.sync = 512 + z.states + z.maps + up256(z.tiles_c * sizeof(unsigned));
   z.dbp = up256((size_t)d->B * z.chunks * z.G * z.C * sizeof(float));
   return z;
 }
@@ -1022,7 +1059,8 @@ template <typename T, int FN, bool Q8, bool TMA> cudaError_t gated_launch(bool b
   cudaError_t e = set_smem_attr(k, smem);
   if (e != cudaSuccess) return e;
   // as many CTAs as the SMs hold (see the kernels' launch bounds)
-  const unsigned most = device_sms() * (bwd || Q8 ? 2 : 3), ctas = a.solo || items < most ? items : most;
+  const unsigned most = device_sms() * (bwd || Q8 ? 2 : 3);
+  const unsigned ctas = bwd && a.db_mode == 3 ? a.tiles_c : a.solo || items < most ? items : most;
   if (bwd) gated_bwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, d, out, a);
   else gated_fwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, out, q, a);
   note_launch();
@@ -1053,6 +1091,7 @@ GatedArgs gated_args(const rnn_gated_dims_t* d, const GatedSizes& z, void* works
   a.ticket = (unsigned*)(ws + 256);
   a.states = (unsigned long long*)(ws + 512);
   a.maps = (ulonglong2*)(ws + 512 + z.states);
+  a.done = (unsigned*)(ws + 512 + z.states + z.maps);
   a.wait_limit_ns = wait_limit_ns();
   return a;
 }
@@ -1139,9 +1178,11 @@ int rnn_gated_bwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
     a.qs = (unsigned char*)tape + z.carry + z.q;
   }
   a.dh = dh; a.dlast = (const float*)dlast; a.dWx = dWx; a.ds0 = (float*)dstate0;
-  a.dbp = db ? (float*)((char*)workspace + z.sync) : nullptr;
+  a.db = db;
+  a.db_mode = db ? z.db_mode : 0;
+  a.dbp = (float*)((char*)workspace + z.sync);
   rc = cuda_status(gated_launch(d, q8, true, a, st));
-  if (rc || !db) return rc;
+  if (rc || a.db_mode != 1) return rc;
   const int cols = z.G * z.C;
   if (d->dtype == RNN_BF16)
     gated_db_kernel<<<(cols + 31) / 32, 256, 0, st>>>(a.dbp, (__nv_bfloat16*)db, d->B * z.chunks, cols);
