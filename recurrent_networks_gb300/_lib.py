@@ -292,6 +292,12 @@ def rnn_input_proj_bwd(BT: int, I: int, C: int, x, W, dWx, dx, dW, dbias, worksp
 
 
 # ---- gated linear scan ------------------------------------------------------------
+def _ws(workspace):
+    """(pointer, bytes) of a workspace: a tensor, or (tensor, offset) for the rest of it."""
+    t, at = workspace if isinstance(workspace, tuple) else (workspace, 0)
+    return t.data_ptr() + at, t.numel() * t.element_size() - at
+
+
 def make_gated_dims(B, T, N, D, function="linear", dtype=torch.bfloat16, checkpoint=None) -> GatedDims:
     fn = GATED_FUNCTIONS[function] if isinstance(function, str) else int(function)
     dt = DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
@@ -313,15 +319,14 @@ def rnn_gated_workspace_size(dims: GatedDims, kind: int = WS_FWD) -> int:
 
 def rnn_gated_fwd(dims: GatedDims, Wx, b, state0, reset, lengths, h, last, tape, workspace, stream=None) -> int:
     rc = load().rnn_gated_fwd(ctypes.byref(dims), _p(Wx), _p(b), _p(state0), _p(reset), _p(lengths), _p(h), _p(last),
-                              _p(tape), _p(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+                              _p(tape), *_ws(workspace), _stream(stream))
     return _check(rc, "rnn_gated_fwd")
 
 
 def rnn_gated_bwd(dims: GatedDims, Wx, b, reset, lengths, tape, dh, dlast, dWx, db, dstate0, workspace,
                   stream=None) -> int:
     rc = load().rnn_gated_bwd(ctypes.byref(dims), _p(Wx), _p(b), _p(reset), _p(lengths), _p(tape), _p(dh), _p(dlast),
-                              _p(dWx), _p(db), _p(dstate0), _p(workspace),
-                              workspace.numel() * workspace.element_size(), _stream(stream))
+                              _p(dWx), _p(db), _p(dstate0), *_ws(workspace), _stream(stream))
     return _check(rc, "rnn_gated_bwd")
 
 

@@ -26,12 +26,12 @@ namespace {
 // when the last one is through its wait, so whatever an item waits for is
 // being worked on, however few of the CTAs are running.
 constexpr int WARPS = 8, STEPS = GATED_CHUNK / WARPS, THREADS = WARPS * 32;
-constexpr int MAX_SPAN = 32;
+constexpr int MAX_SPAN = 4;  // log2
 
 struct GatedArgs {
   int B, T, C, chunks;  // C = N D channels
   int tiles_c;          // channel tiles per batch row
-  int span;             // chunks per group
+  int span;             // log2 of the chunks per group
   int solo;  // one chunk, all CTAs at once: no waits, so block 0 clears the status word itself
   const void* Wx;
   const void* bias;
@@ -54,7 +54,7 @@ struct GatedArgs {
   float* dbp;
   void* db;
   unsigned* done;            // [tiles_c], zeroed (mode 2)
-  unsigned long long* states;  // [groups][tiles][N][32]: the state (or its gradient) that enters a group
+  unsigned long long* states;  // [groups, or 2 in turn][tiles][N][32]: the state (or its gradient) that enters a group
   ulonglong2* maps;            // [chunks][tiles][N][32]: the chunks' maps (P, H)
   unsigned* status;
   unsigned* ticket;
@@ -199,27 +199,14 @@ template <int N> __device__ __forceinline__ Item item_of(const GatedArgs& p, con
   return it;
 }
 
-// A lane's fp32 values at channel it.ch of row r of a [rows][C] array.
-template <int N, bool L2> __device__ __forceinline__ FV<N> load_f(const float* a, size_t r, const GatedArgs& p, const Item& it) {
-  FV<N> x;
-#pragma unroll
-  for (int v = 0; v < N; ++v) {
-    const float* q = a + r * p.C + it.ch + v;
-    x.v[v] = v < it.n ? (L2 ? __ldcg(q) : __ldg(q)) : 0.0f;
-  }
-  return x;
+// (value, tag) words; the tag is the place of the group or chunk (never 0, the
+// cleared value). Relaxed accesses at gpu scope: each 8-byte word is read and
+// written whole, and nothing else is ordered by it.
+__device__ __forceinline__ unsigned long long word_of(float v, unsigned tag) {
+  return (unsigned long long)tag << 32 | __float_as_uint(v);
 }
-template <int N> __device__ __forceinline__ void store_f(float* a, size_t r, const GatedArgs& p, const Item& it, const FV<N>& x) {
-#pragma unroll
-  for (int v = 0; v < N; ++v)
-    if (v < it.n) a[r * p.C + it.ch + v] = x.v[v];
-}
-
-// (value, tag) words. Relaxed accesses at gpu scope: each 8-byte word is read
-// and written whole, and nothing else is ordered by it.
-__device__ __forceinline__ unsigned long long word_of(float v) { return 1ull << 32 | __float_as_uint(v); }
 __device__ __forceinline__ float value_of(unsigned long long w) { return __uint_as_float((unsigned)w); }
-__device__ __forceinline__ bool is_set(unsigned long long w) { return (w >> 32) != 0; }
+__device__ __forceinline__ bool is_set(unsigned long long w, unsigned tag) { return (unsigned)(w >> 32) == tag; }
 __device__ __forceinline__ unsigned long long ld_word(const unsigned long long* p) {
   unsigned long long w;
   asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(p) : "memory");
@@ -229,128 +216,150 @@ __device__ __forceinline__ void st_word(unsigned long long* p, unsigned long lon
   asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(w) : "memory");
 }
 
+// An affine map x -> P x + H, and first `a`, then `b`.
+struct Map {
+  float P, H;
+};
+__device__ __forceinline__ Map then(const Map& a, const Map& b) { return {b.P * a.P, affine(b.P, a.H, b.H)}; }
+
 // How a CTA passes the state through the chunks of a tile; REVERSE: the
-// processing order descends. Warp 0 holds the chunk's own map and the state;
-// PARTS warps fold the maps of the group's chunks before this one, each a run
-// of them, so the order of the products depends on the chunk alone.
+// processing order descends. All threads take part, Q neighbouring lanes to a
+// channel slot (v, lane): a lane folds M of the warps' maps, scans over the Q
+// lanes give what is done to the state before each warp and by the whole
+// chunk. (One warp that folded the warps' maps one after the other, with the
+// rest of the CTA idle, cost 25 of 247 us at B=32 T=4096 C=1024.)
 template <int N, bool REVERSE> struct Chain {
-  static constexpr int PARTS = 4, AHEAD = 2;  // folding warps, maps in flight
+  static constexpr int Q = THREADS / (32 * N), M = WARPS / Q;
+  static constexpr int ROW = 32 * N + 2, EROW = 32 * N + 4;  // row lengths that spread the Q lanes over the banks
+  static constexpr unsigned ALL = 0xffffffffu;
   const GatedArgs& p;
   const Item& it;
-  int o, first;  // this chunk's and its group's first chunk's place in processing order
-  unsigned long long early[N];
-  bool failed;
-  __device__ __forceinline__ Chain(const GatedArgs& p, const Item& it) : p(p), it(it), failed(false) {
+  bool& failed;
+  int o, first, group;  // this chunk's and its group's first chunk's place in processing order, the group's place
+  int c, q, ch;         // the slot, the lane's part of it, the slot's channel
+  float x;              // the state before the first chunk, then the state that enters the chunk
+  unsigned long long early;
+  Map mine[M], before, whole;  // the lane's maps, what comes before them, the chunk's
+  __device__ __forceinline__ Chain(const GatedArgs& p, const Item& it, bool& failed) : p(p), it(it), failed(failed) {
     o = REVERSE ? p.chunks - 1 - it.k : it.k;
-    first = o - o % p.span;
+    group = o >> p.span;
+    first = group << p.span;
+    c = threadIdx.x / Q;
+    q = threadIdx.x % Q;
+    ch = it.ct + c % 32 * N + c / 32;
   }
   __device__ __forceinline__ size_t at(int i) const {
-    return ((size_t)i * ((unsigned)p.B * p.tiles_c) + it.tile) * N * 32 + (threadIdx.x & 31);
+    return ((size_t)i * ((unsigned)p.B * p.tiles_c) + it.tile) * N * 32 + c;
   }
-  // At the start: asks for the state that enters the group; where it is there
-  // already (the usual case with many tiles) the round trip runs beside the
-  // tile's load.
-  __device__ __forceinline__ void ask() {
-    if (first > 0) {
-#pragma unroll
-      for (int v = 0; v < N; ++v) early[v] = ld_word(p.states + at(first / p.span) + v * 32);
-    }
+  // Where the state that enters a group lies. Without groups of several chunks
+  // two places in turn do: group g + 2 is written after chunk g + 1 had its
+  // state, from chunk g, all of whose lanes had theirs.
+  __device__ __forceinline__ unsigned long long* state(int g) const { return p.states + at(p.span ? g : g & 1); }
+  // At the start: the state before the first chunk, or the one that enters the
+  // group; where it is there already (the usual case with many tiles) the
+  // round trip runs beside the tile's load.
+  __device__ __forceinline__ void ask(const float* init) {
+    x = 0.0f;
+    early = 0;
+    if (group > 0) early = ld_word(state(group));
+    else if (init && ch < p.C) x = __ldg(init + (size_t)it.b * p.C + ch);
   }
-  // Waits until `get` has what it wants, for at most the wait limit.
+  // The warp waits until `get` holds in all lanes, for at most the wait limit.
   template <typename F> __device__ __forceinline__ void wait(F&& get) {
-    if (failed || get()) return;
+    bool ok = failed || get();
+    if (__all_sync(ALL, ok)) return;
     const uint64_t t0 = globaltimer_ns();
-    while (!get()) {
-      if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+    do {
+      if (!ok) ok = get();
+      if (__any_sync(ALL, globaltimer_ns() - t0 > p.wait_limit_ns)) {
         atomicOr(p.status, STATUS_TIMEOUT);
         failed = true;
         return;
       }
-    }
+    } while (!__all_sync(ALL, ok));
   }
-  // The chunk's own map, for the group's later chunks.
-  __device__ __forceinline__ void publish(const FV<N>& P, const FV<N>& H) const {
-    if (o + 1 == first + p.span || o + 1 == p.chunks) return;
+  // Over the Q lanes of a slot, in their order: everything up to and including
+  // the lane's m.
+  static __device__ __forceinline__ Map scan(Map m, int q) {
 #pragma unroll
-    for (int v = 0; v < N; ++v)
-      asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p.maps + at(o) + v * 32), "l"(word_of(P.v[v])),
-                   "l"(word_of(H.v[v]))
-                   : "memory");
+    for (int d = 1; d < Q; d *= 2) {
+      const Map l = {__shfl_up_sync(ALL, m.P, d, Q), __shfl_up_sync(ALL, m.H, d, Q)};
+      if (q >= d) m = then(l, m);
+    }
+    return m;
   }
-  // All warps: the group's maps before this chunk, folded in PARTS runs into
-  // `parts` [PARTS][N][32].
-  __device__ __forceinline__ void gather(float2* parts) {
-    if (o == first) return;
-    const int part = (int)(threadIdx.x >> 5) - (WARPS - PARTS);
-    if (part >= 0) {
-      const int run = (o - first + PARTS - 1) / PARTS;
-      const int from = min(o, first + part * run), to = min(o, from + run);
-      FV<N> P = splat<N>(1.0f), H = splat<N>(0.0f);
-      for (int w0 = from; w0 < to; w0 += AHEAD) {
-        ulonglong2 m[AHEAD][N];
+  static __device__ __forceinline__ Map last_of(const Map& m) {
+    return {__shfl_sync(ALL, m.P, Q - 1, Q), __shfl_sync(ALL, m.H, Q - 1, Q)};
+  }
+  static __device__ __forceinline__ Map shifted(const Map& m, int q) {
+    Map l = {__shfl_up_sync(ALL, m.P, 1, Q), __shfl_up_sync(ALL, m.H, 1, Q)};
+    if (q == 0) l = {1.0f, 0.0f};
+    return l;
+  }
+  __device__ __forceinline__ int warp_of(int i) const { return REVERSE ? WARPS - 1 - (q * M + i) : q * M + i; }
+  // With the lane's maps in `mine`: scans them and publishes the chunk's map
+  // for the group's later chunks.
+  __device__ __forceinline__ void publish() {
+    Map m = mine[0];
+#pragma unroll
+    for (int i = 1; i < M; ++i) m = then(m, mine[i]);
+    m = scan(m, q);
+    before = shifted(m, q);
+    whole = last_of(m);
+    if (o + 1 == first + (1 << p.span) || o + 1 == p.chunks || q != 0) return;
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p.maps + at(o)), "l"(word_of(whole.P, o + 1)),
+                 "l"(word_of(whole.H, o + 1))
+                 : "memory");
+  }
+  // Makes x the state that enters the chunk, publishes the one that leaves a
+  // group, and hands every warp its own: enter [WARPS][EROW].
+  __device__ __forceinline__ void pass(float* enter) {
+    Map g = {1.0f, 0.0f};  // the group's chunks before this one, a run of them a lane
+    if (o > first) {
+      const int run = (o - first + Q - 1) / Q, from = first + q * run;
+      for (int i = 0; i < run; i += 2) {
+        ulonglong2 m[2];
         wait([&]() {
           bool all = true;
 #pragma unroll
-          for (int j = 0; j < AHEAD; ++j)
+          for (int j = 0; j < 2; ++j)
+            if (i + j < run && from + i + j < o)
+              asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];"
+                           : "=l"(m[j].x), "=l"(m[j].y)
+                           : "l"(p.maps + at(from + i + j))
+                           : "memory");
 #pragma unroll
-            for (int v = 0; v < N; ++v)
-              if (w0 + j < to)
-                asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];"
-                             : "=l"(m[j][v].x), "=l"(m[j][v].y)
-                             : "l"(p.maps + at(w0 + j) + v * 32)
-                             : "memory");
-#pragma unroll
-          for (int j = 0; j < AHEAD; ++j)
-#pragma unroll
-            for (int v = 0; v < N; ++v)
-              if (w0 + j < to) all &= is_set(m[j][v].x) && is_set(m[j][v].y);
+          for (int j = 0; j < 2; ++j)
+            if (i + j < run && from + i + j < o)
+              all &= is_set(m[j].x, from + i + j + 1) && is_set(m[j].y, from + i + j + 1);
           return all;
         });
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j)
-#pragma unroll
-          for (int v = 0; v < N; ++v)
-            if (w0 + j < to) {
-              P.v[v] *= value_of(m[j][v].x);
-              H.v[v] = affine(value_of(m[j][v].x), H.v[v], value_of(m[j][v].y));
-            }
+        for (int j = 0; j < 2; ++j)
+          if (i + j < run && from + i + j < o) g = then(g, {value_of(m[j].x), value_of(m[j].y)});
       }
-#pragma unroll
-      for (int v = 0; v < N; ++v) parts[(part * N + v) * 32 + (threadIdx.x & 31)] = make_float2(P.v[v], H.v[v]);
+      g = last_of(scan(g, q));
     }
-    __syncthreads();
-  }
-  // Warp 0: makes x (in: the state before the first chunk in processing
-  // order) the state that enters the chunk, and publishes what leaves a group.
-  __device__ __forceinline__ void pass(const float2* parts, const FV<N>& P, const FV<N>& H, FV<N>& x) {
-    if (first > 0) {
+    if (group > 0) {
       wait([&]() {
-        bool all = true;
-#pragma unroll
-        for (int v = 0; v < N; ++v) {
-          if (!is_set(early[v])) early[v] = ld_word(p.states + at(first / p.span) + v * 32);
-          all &= is_set(early[v]);
-        }
-        return all;
+        if (!is_set(early, group)) early = ld_word(state(group));
+        return is_set(early, group);
       });
-#pragma unroll
-      for (int v = 0; v < N; ++v) x.v[v] = value_of(early[v]);
+      x = value_of(early);
     }
-    if (o > first) {
+    x = affine(g.P, x, g.H);
+    if (o + 1 == first + (1 << p.span) && o + 1 < p.chunks && q == 0)
+      st_word(state(group + 1), word_of(affine(whole.P, x, whole.H), group + 1));
+    float e = affine(before.P, x, before.H);
 #pragma unroll
-      for (int w = 0; w < PARTS; ++w)
-#pragma unroll
-        for (int v = 0; v < N; ++v) {
-          const float2 m = parts[(w * N + v) * 32 + (threadIdx.x & 31)];
-          x.v[v] = affine(m.x, x.v[v], m.y);
-        }
-      __syncwarp();
+    for (int i = 0; i < M; ++i) {
+      enter[warp_of(i) * EROW + c] = e;
+      e = affine(mine[i].P, e, mine[i].H);
     }
-    if (o + 1 == first + p.span && o + 1 < p.chunks) {
-      const FV<N> y = affine(P, x, H);
-#pragma unroll
-      for (int v = 0; v < N; ++v) st_word(p.states + at((o + 1) / p.span) + v * 32, word_of(y.v[v]));
-    }
+  }
+  // Lane 0 of a slot: the value x at row r of a [rows][C] array.
+  __device__ __forceinline__ void store(float* a, size_t r, float v) const {
+    if (q == 0 && ch < p.C) a[r * p.C + ch] = v;
   }
 };
 
@@ -403,13 +412,16 @@ __device__ __forceinline__ void fetch_align(const GatedArgs& p, const Item& it, 
 }
 __device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// A lane's biases, scaled as the gates want them.
-template <typename T, int FN, int N> __device__ __forceinline__ void load_bias(const GatedArgs& p, const Item& it, FV<N>* bias) {
+// A lane's biases, scaled as the gates want them: from the copy beside the tile
+// [G][32] (TMA), or from memory.
+template <typename T, int FN, int N, bool TMA>
+__device__ __forceinline__ void load_bias(const GatedArgs& p, const Item& it, const uint32_t* copy, FV<N>* bias) {
   constexpr int G = gated_gates(FN);
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    bias[g] = Lane<T>::unpack(p.bias ? load_lane((const T*)p.bias + (size_t)g * p.C + it.ch, it.n, p.C % 2 == 0) : 0);
-    bias[g] = mul(bias[g], splat<N>(mul_of<FN, N>(g)));
+    uint32_t w = 0;
+    if (p.bias) w = TMA ? copy[g * 32 + (threadIdx.x & 31)] : load_lane((const T*)p.bias + (size_t)g * p.C + it.ch, it.n, p.C % 2 == 0);
+    bias[g] = mul(Lane<T>::unpack(w), splat<N>(mul_of<FN, N>(g)));
   }
 }
 // raw pre-activation -> gate value (see mul_of)
@@ -430,22 +442,26 @@ template <typename F> __device__ __forceinline__ void by_mask(const Item& it, F&
 template <typename T, int FN, bool Q8, bool TMA>
 __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
     gated_fwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap hmap,
-                     const __grid_constant__ CUtensorMap qmap, GatedArgs p) {
+                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap bmap, GatedArgs p) {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
   constexpr bool TMAQ = Q8 && TMA;  // (the rows of bytes are 16-byte multiples then, too)
   constexpr int U0 = FN == GATED_LINEAR ? 0 : 1, U1 = FN == GATED_LINEAR ? 2 : 0;  // rows that hold u of channel 0, 1
   extern __shared__ __align__(128) unsigned char smem[];
   uint32_t* tile = (uint32_t*)smem;                                   // [WARPS][STEPS][G][32]
-  float2* maps = (float2*)(tile + WARPS * STEPS * G * 32);            // [WARPS][N][32]
-  float* enter = (float*)(maps + WARPS * 32 * N);                     // [WARPS][N][32]: the states that enter the warps
-  uint32_t* tops = (uint32_t*)(enter + WARPS * 32 * N);               // Q8: [WARPS][G][32]
+  using Ch = Chain<N, false>;
+  uint32_t* bcopy = tile + WARPS * STEPS * G * 32;                    // [G][32]
+  float2* maps = (float2*)(bcopy + G * 32);                           // [WARPS][ROW]: slot v * 32 + lane
+  float* enter = (float*)(maps + WARPS * Ch::ROW);                    // [WARPS][EROW]: the states that enter the warps
+  uint32_t* tops = (uint32_t*)(enter + WARPS * Ch::EROW);             // Q8: [WARPS][G][32]
   unsigned char* qtile = (unsigned char*)(tops + (Q8 ? WARPS * G * 32 : 0));  // Q8: [WARPS][STEPS][G][32 N]
-  unsigned long long* bars = (unsigned long long*)(qtile + (Q8 ? WARPS * STEPS * G * 32 * N : 0));  // [WARPS]
-  int4* shared = (int4*)(bars + WARPS);
+  unsigned long long* bars = (unsigned long long*)(qtile + (Q8 ? WARPS * STEPS * G * 32 * N : 0));  // [WARPS]; the biases'
+  int4* shared = (int4*)(bars + WARPS + 2);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bar = smem_u32(bars + warp);
+  const uint32_t bbar = smem_u32(bars + WARPS);
   if (TMA && lane == 0) {
     mbar_init(bar, 1);
+    if (warp == 0) mbar_init(bbar, 1);
     fence_mbar_init_cluster();
   }
   uint32_t* mine = tile + warp * STEPS * G * 32;
@@ -454,24 +470,25 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
   if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
   if (threadIdx.x == 0) *shared = place_of<false>(p, p.solo ? blockIdx.x : atomicAdd(p.ticket, 1u));
   __syncthreads();
-  for (unsigned loads = 0; shared->x >= 0;) {
+  for (unsigned loads = 0, turn = 0; shared->x >= 0; ++turn) {
   const Item it = item_of<N>(p, *shared);
   if (TMA) {
     if (lane == 0 && it.live > 0) {
       mbar_arrive_expect_tx(bar, STEPS * G * 128);
       tma_load_4d(smem_u32(mine), &xmap, bar, it.ct, 0, it.t0, it.b);
     }
+    if (threadIdx.x == 0 && p.bias) {
+      mbar_arrive_expect_tx(bbar, G * 128);
+      tma_load_4d(smem_u32(bcopy), &bmap, bbar, it.ct, 0, 0, 0);
+    }
   } else {
     fetch_lanes<T, G>(p, it, (const T*)p.Wx, mine, extra);
   }
+  Ch chain(p, it, failed);
+  chain.ask(p.s0);
   FV<N> bias[G];
-  load_bias<T, FN, N>(p, it, bias);
-  FV<N> x = splat<N>(0.0f);  // the state that enters the chunk
-  Chain<N, false> chain(p, it);
-  if (warp == 0) {
-    if (p.s0) x = load_f<N, false>(p.s0, it.b, p, it);
-    chain.ask();
-  }
+  if (TMA && p.bias) mbar_wait_bounded<false>(bbar, turn & 1, p.wait_limit_ns, p.status, failed);
+  load_bias<T, FN, N, TMA>(p, it, bcopy, bias);
   if (TMA) {
     if (it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
   } else {
@@ -512,40 +529,21 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
   });
 #pragma unroll
   for (int v = 0; v < N; ++v) {
-    maps[(warp * N + v) * 32 + lane] = make_float2(P.v[v], H.v[v]);
+    maps[warp * Ch::ROW + v * 32 + lane] = make_float2(P.v[v], H.v[v]);
   }
   if (Q8) {
 #pragma unroll
     for (int g = 0; g < G; ++g) tops[(warp * G + g) * 32 + lane] = top[g];
   }
   __syncthreads();
-  if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w)
-#pragma unroll
-      for (int v = 0; v < N; ++v) {
-        const float2 m = maps[(w * N + v) * 32 + lane];
-        P.v[v] *= m.x;
-        H.v[v] = affine(m.x, H.v[v], m.y);
-      }
-    chain.publish(P, H);
+  for (int i = 0; i < Ch::M; ++i) {
+    const float2 m = maps[chain.warp_of(i) * Ch::ROW + chain.c];
+    chain.mine[i] = {m.x, m.y};
   }
-  chain.gather((float2*)enter);
-  if (warp == 0) {
-    chain.pass((const float2*)enter, P, H, x);
-    if (p.carry) store_f<N>(p.carry, (size_t)it.b * p.chunks + it.k, p, it, x);
-    if (p.last && it.k == p.chunks - 1) store_f<N>(p.last, it.b, p, it, affine(P, x, H));
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w)
-#pragma unroll
-      for (int v = 0; v < N; ++v) {
-        enter[(w * N + v) * 32 + lane] = x.v[v];
-        const float2 m = maps[(w * N + v) * 32 + lane];
-        x.v[v] = affine(m.x, x.v[v], m.y);
-      }
-  }
+  chain.publish();
   const bool wide = p.C % 2 == 0;
-  if (Q8) {  // beside the wait for the state: the tile in 8 bits
+  if (Q8) {  // before the wait for the state: the tile in 8 bits
     const int qblocks = (p.T + ACT_BLOCK - 1) / ACT_BLOCK;
     FV<N> inv[G];
     bool huge = false, odd = false;  // a block that saturates, a block that is not finite
@@ -594,12 +592,15 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
           if (v < it.n) q[(size_t)r * p.C + v] = (signed char)qmine[r * 32 * N + lane * N + v];
     }
   }
+  chain.pass(enter);
+  if (p.carry) chain.store(p.carry, (size_t)it.b * p.chunks + it.k, chain.x);
+  if (p.last && it.k == p.chunks - 1) chain.store(p.last, it.b, affine(chain.whole.P, chain.x, chain.whole.H));
   __syncthreads();
   unsigned next = 0xffffffffu;
   if (threadIdx.x == 0 && !p.solo) next = atomicAdd(p.ticket, 1u);  // on its way beside the last pass
   FV<N> c;
 #pragma unroll
-  for (int v = 0; v < N; ++v) c.v[v] = enter[(warp * N + v) * 32 + lane];
+  for (int v = 0; v < N; ++v) c.v[v] = enter[warp * Ch::EROW + v * 32 + lane];
   by_mask(it, [&](auto mask) {
     constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
@@ -641,28 +642,34 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
 template <typename T, int FN, bool Q8, bool TMA>
 __global__ void __launch_bounds__(THREADS, 2)
     gated_bwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap dmap,
-                     const __grid_constant__ CUtensorMap omap, GatedArgs p) {
+                     const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap bmap, GatedArgs p) {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
   constexpr int XB = Q8 ? 32 * N : 128;  // bytes of a row (t, g) of the tile
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* tile = smem;                                          // [WARPS][STEPS][G][XB]
   uint32_t* dtile = (uint32_t*)(tile + WARPS * STEPS * G * XB);        // [WARPS][STEPS][32]
-  float* maps = (float*)(dtile + WARPS * STEPS * 32);                  // [WARPS][3][N][32]: P, H (state), E (gradient)
-  float* enter = maps + WARPS * 3 * 32 * N;                            // [WARPS][N][32]
-  float* dbs = enter + WARPS * 32 * N;                                 // [WARPS][G][N][32]
+  using Ch = Chain<N, true>;
+  uint32_t* bcopy = dtile + WARPS * STEPS * 32;                        // [G][32]
+  float2* maps = (float2*)(bcopy + G * 32);                            // [WARPS][ROW]: P, H of the state; slot v * 32 + lane
+  float* mapE = (float*)(maps + WARPS * Ch::ROW);                      // [WARPS][EROW]: with P, the gradient's
+  float* enter = mapE + WARPS * Ch::EROW;                              // [WARPS][EROW]: the gradients that enter the warps
+  float* begin = enter + WARPS * Ch::EROW;                             // [WARPS][EROW]: the states that do
+  float* dbs = begin + WARPS * Ch::EROW;                               // [WARPS][G][N][32]
   uint32_t* ring = (uint32_t*)(dbs + WARPS * G * 32 * N);              // Q8: [WARPS][8 steps][G][32]
   uint32_t* omine = ring + (threadIdx.x >> 5) * (Q8 ? 8 * G * 32 : 0);
   unsigned long long* bars = (unsigned long long*)(ring + (Q8 ? WARPS * 8 * G * 32 : 0));
-  int4* shared = (int4*)(bars + WARPS);
+  int4* shared = (int4*)(bars + WARPS + 2);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bar = smem_u32(bars + warp);
+  const uint32_t bbar = smem_u32(bars + WARPS);
   if (TMA && lane == 0) {
     mbar_init(bar, 1);
+    if (warp == 0) mbar_init(bbar, 1);
     fence_mbar_init_cluster();
   }
   unsigned char* mine = tile + warp * STEPS * G * XB;
   uint32_t* dmine = dtile + warp * STEPS * 32;
-  uint32_t* extra = (uint32_t*)(maps + warp * 3 * 32 * N);  // (the warp's own maps come after)
+  uint32_t* extra = (uint32_t*)enter + warp * STEPS * (G + 1);  // (enter and begin are free until all warps have their maps)
   const bool wide = p.C % 2 == 0;
   bool failed = false;
   if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
@@ -672,13 +679,17 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int j = 0; j < STEPS; ++j) dmine[j * 32 + lane] = 0;
   }
   __syncthreads();
-  for (unsigned loads = 0; shared->x >= 0;) {
+  for (unsigned loads = 0, turn = 0; shared->x >= 0; ++turn) {
   const Item it = item_of<N>(p, *shared);
   if (TMA) {
     if (lane == 0 && it.live > 0) {
       mbar_arrive_expect_tx(bar, STEPS * G * XB + (p.dh ? STEPS * 128 : 0));
       tma_load_4d(smem_u32(mine), &xmap, bar, it.ct, 0, it.t0, it.b);
       if (p.dh) tma_load_4d(smem_u32(dmine), &dmap, bar, it.ct, 0, it.t0, it.b);
+    }
+    if (threadIdx.x == 0 && p.bias) {
+      mbar_arrive_expect_tx(bbar, G * 128);
+      tma_load_4d(smem_u32(bcopy), &bmap, bbar, it.ct, 0, 0, 0);
     }
   } else {
     if (Q8) {
@@ -693,8 +704,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     if (p.dh) fetch_lanes<T, 1>(p, it, (const T*)p.dh, dmine, extra + STEPS * G);
   }
+  Ch chain(p, it, failed);
+  chain.ask(p.dlast);
+  const float cc = chain.ch < p.C ? __ldg(p.carry + ((size_t)it.b * p.chunks + it.k) * p.C + chain.ch) : 0.0f;  // the state that enters the chunk
   FV<N> bias[G], scale[Q8 ? G : 1];
-  load_bias<T, FN, N>(p, it, bias);
   if (Q8) {
     const int qblocks = (p.T + ACT_BLOCK - 1) / ACT_BLOCK;
 #pragma unroll
@@ -706,13 +719,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                 ? mul_of<FN, N>(g) * act_scale(p.qs[(((size_t)it.b * qblocks + it.t0 / ACT_BLOCK) * G + g) * p.C + it.ch + v])
                 : 0.0f;
   }
-  FV<N> c = load_f<N, false>(p.carry, (size_t)it.b * p.chunks + it.k, p, it);  // the state that enters the chunk
-  FV<N> x = splat<N>(0.0f);  // the state gradient that enters it from later steps
-  Chain<N, true> chain(p, it);
-  if (warp == 0) {
-    if (p.dlast) x = load_f<N, false>(p.dlast, it.b, p, it);
-    chain.ask();
-  }
+  if (TMA && p.bias) mbar_wait_bounded<false>(bbar, turn & 1, p.wait_limit_ns, p.status, failed);
+  load_bias<T, FN, N, TMA>(p, it, bcopy, bias);
   if (TMA) {
     if (it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
   } else {
@@ -754,55 +762,53 @@ __global__ void __launch_bounds__(THREADS, 2)
   });
 #pragma unroll
   for (int v = 0; v < N; ++v) {
-    float* m = maps + (warp * 3 * N + v) * 32 + lane;
-    m[0] = P.v[v];
-    m[N * 32] = H.v[v];
-    m[2 * N * 32] = E.v[v];
+    maps[warp * Ch::ROW + v * 32 + lane] = make_float2(P.v[v], H.v[v]);
+    mapE[warp * Ch::EROW + v * 32 + lane] = E.v[v];
   }
   __syncthreads();
-  FV<N> PC = splat<N>(1.0f), EC = splat<N>(0.0f);
-  if (warp == 0) {  // the chunk's map of the gradient, last warp first
+  Map own[Ch::M];  // the state's maps of the lane's warps
 #pragma unroll
-    for (int w = WARPS - 1; w >= 0; --w)
-#pragma unroll
-      for (int v = 0; v < N; ++v) {
-        const float* m = maps + (w * 3 * N + v) * 32 + lane;
-        PC.v[v] *= m[0];
-        EC.v[v] = affine(m[0], EC.v[v], m[2 * N * 32]);
-      }
-    chain.publish(PC, EC);
+  for (int i = 0; i < Ch::M; ++i) {
+    const float2 m = maps[chain.warp_of(i) * Ch::ROW + chain.c];
+    own[i] = {m.x, m.y};
+    chain.mine[i] = {m.x, mapE[chain.warp_of(i) * Ch::EROW + chain.c]};
   }
-  chain.gather((float2*)enter);
-  if (warp == 0) {
-    chain.pass((const float2*)enter, PC, EC, x);
-    if (p.ds0 && it.k == 0) store_f<N>(p.ds0, it.b, p, it, affine(PC, x, EC));
+  chain.publish();
+  {  // the states that enter the warps: the lanes of a slot hold descending warps
+    Map m = own[Ch::M - 1];
 #pragma unroll
-    for (int w = WARPS - 1; w >= 0; --w)
+    for (int i = Ch::M - 2; i >= 0; --i) m = then(m, own[i]);
 #pragma unroll
-      for (int v = 0; v < N; ++v) {
-        enter[(w * N + v) * 32 + lane] = x.v[v];
-        const float* m = maps + (w * 3 * N + v) * 32 + lane;
-        x.v[v] = affine(m[0], x.v[v], m[2 * N * 32]);
-      }
-  }
-  // the states of the warp's steps, while the gradient is on its way
-#pragma unroll
-  for (int v = 0; v < N; ++v)
-    for (int w = 0; w < warp; ++w) {
-      const float* m = maps + (w * 3 * N + v) * 32 + lane;
-      c.v[v] = affine(m[0], c.v[v], m[N * 32]);
+    for (int d = 1; d < Ch::Q; d *= 2) {
+      const Map l = {__shfl_down_sync(0xffffffffu, m.P, d, Ch::Q), __shfl_down_sync(0xffffffffu, m.H, d, Ch::Q)};
+      if (chain.q + d < Ch::Q) m = then(l, m);
     }
+    Map l = {__shfl_down_sync(0xffffffffu, m.P, 1, Ch::Q), __shfl_down_sync(0xffffffffu, m.H, 1, Ch::Q)};
+    if (chain.q == Ch::Q - 1) l = {1.0f, 0.0f};
+    float e = affine(l.P, cc, l.H);
+#pragma unroll
+    for (int i = Ch::M - 1; i >= 0; --i) {
+      begin[chain.warp_of(i) * Ch::EROW + chain.c] = e;
+      e = affine(own[i].P, e, own[i].H);
+    }
+  }
+  chain.pass(enter);
+  if (p.ds0 && it.k == 0) chain.store(p.ds0, it.b, affine(chain.whole.P, chain.x, chain.whole.H));
+  __syncthreads();
+  unsigned next = 0xffffffffu;
+  if (threadIdx.x == 0 && !p.solo) next = atomicAdd(p.ticket, 1u);  // on its way beside the last pass
+  FV<N> c, x;  // the state before the warp's steps, the gradient that reaches it from after them
+#pragma unroll
+  for (int v = 0; v < N; ++v) {
+    c.v[v] = begin[warp * Ch::EROW + v * 32 + lane];
+    x.v[v] = enter[warp * Ch::EROW + v * 32 + lane];
+  }
   const FV<N> start = c;
   by_mask(it, [&](auto mask) {
     constexpr bool MASK = decltype(mask)::value;
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) u[j] = c = MASK && (it.rst >> j & 1) ? u[j] : fma(f[j], c, u[j]);
   });
-  __syncthreads();
-  unsigned next = 0xffffffffu;
-  if (threadIdx.x == 0 && !p.solo) next = atomicAdd(p.ticket, 1u);  // on its way beside the last pass
-#pragma unroll
-  for (int v = 0; v < N; ++v) x.v[v] = enter[(warp * N + v) * 32 + lane];
   FV<N> db[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) db[g] = splat<N>(0.0f);
@@ -901,29 +907,32 @@ __global__ void __launch_bounds__(THREADS, 2)
 }
 
 template <typename T, int FN, bool Q8> constexpr int fwd_smem() {
-  constexpr int G = gated_gates(FN), N = Lane<T>::N;
-  return WARPS * STEPS * G * 128 + WARPS * 32 * N * 8 + WARPS * 32 * N * 4 + (Q8 ? WARPS * G * 32 * (4 + STEPS * N) : 0) + WARPS * 8 + 32;
+  constexpr int G = gated_gates(FN), N = Lane<T>::N, W = 32 * N;
+  return WARPS * STEPS * G * 128 + G * 128 + WARPS * (W + 2) * 8 + WARPS * (W + 4) * 4 +
+         (Q8 ? WARPS * G * 32 * (4 + STEPS * N) : 0) + WARPS * 8 + 48;
 }
 template <typename T, int FN, bool Q8> constexpr int bwd_smem() {
-  constexpr int G = gated_gates(FN), N = Lane<T>::N;
-  return WARPS * STEPS * (G * (Q8 ? 32 * N : 128) + 128) + WARPS * 3 * 32 * N * 4 + WARPS * 32 * N * 4 + WARPS * G * 32 * N * 4 +
-         (Q8 ? WARPS * 8 * G * 128 : 0) + WARPS * 8 + 32;
+  constexpr int G = gated_gates(FN), N = Lane<T>::N, W = 32 * N;
+  return WARPS * STEPS * (G * (Q8 ? W : 128) + 128) + G * 128 + WARPS * (W + 2) * 8 + 3 * WARPS * (W + 4) * 4 +
+         WARPS * G * W * 4 + (Q8 ? WARPS * 8 * G * 128 : 0) + WARPS * 8 + 48;
 }
 
-// db[j] = sum over `rows` of dbp[row][j], in row order within 8 interleaved
+// db[j] = sum over `rows` of dbp[row][j], in row order within 32 interleaved
 // lanes, then the lanes in order.
 template <typename T>
-__global__ void __launch_bounds__(256) gated_db_kernel(const float* dbp, T* db, int rows, int cols) {
-  __shared__ float red[8][32];
+__global__ void __launch_bounds__(1024) gated_db_kernel(const float* dbp, T* db, int rows, int cols) {
+  __shared__ float red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int j = blockIdx.x * 32 + tx;
   float s = 0.0f;
   if (j < cols)
-    for (int r = ty; r < rows; r += 8) s += dbp[(size_t)r * cols + j];
+#pragma unroll 8
+    for (int r = ty; r < rows; r += 32) s += dbp[(size_t)r * cols + j];
   red[ty][tx] = s;
   __syncthreads();
   if (ty == 0 && j < cols) {
-    for (int k = 1; k < 8; ++k) s += red[k][tx];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) s += red[k][tx];
     db[j] = from_f<T>(s);
   }
 }
@@ -1010,8 +1019,8 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   // tiles: with fewer tiles than that (and a margin of two), a group of chunks
   // shares a hop.
   const size_t sms = device_sms(), ahead = sms + sms / 2;
-  z.span = (int)((ahead + tiles - 1) / tiles);
-  if (z.span > MAX_SPAN) z.span = MAX_SPAN;
+  z.span = 0;
+  while (z.span < MAX_SPAN && (tiles << z.span) < ahead) ++z.span;
   // A short sequence is all latency: without TMA there is no wait that could
   // run out, and the clearing launch for the status word falls away.
   z.solo = z.chunks == 1 && tiles <= 2 * sms;
@@ -1021,9 +1030,9 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   z.q = q8 ? up256((size_t)d->B * d->T * z.G * z.C) : 0;
   z.qs = q8 ? up256((size_t)d->B * z.qblocks * z.G * z.C) : 0;
   z.tape = z.carry + z.q + z.qs;
-  const size_t groups = (z.chunks + z.span - 1) / z.span;
+  const size_t groups = z.span ? ((size_t)(z.chunks - 1) >> z.span) + 1 : 2;
   z.states = z.chunks > 1 ? up256(groups * lanes * sizeof(unsigned long long)) : 0;
-  z.maps = z.chunks > 1 && z.span > 1 ? up256(z.chunks * lanes * sizeof(ulonglong2)) : 0;
+  z.maps = z.chunks > 1 && z.span > 0 ? up256(z.chunks * lanes * sizeof(ulonglong2)) : 0;
   // db: with few batch rows of one chunk, a CTA takes a channel tile's rows one
   // after the other; with few items, the last one adds the items' sums (16
   // loads in flight, a round trip of a microsecond each); else a launch does.
@@ -1044,9 +1053,14 @@ cudaError_t tile_map(CUtensorMap* m, const void* base, int elem, const GatedArgs
 
 template <typename T, int FN, bool Q8, bool TMA> cudaError_t gated_launch(bool bwd, const GatedArgs& a, cudaStream_t st) {
   constexpr int G = gated_gates(FN), width = 32 * Lane<T>::N;
-  CUtensorMap x = {}, d = {}, out = {}, q = {};
+  CUtensorMap x = {}, d = {}, out = {}, q = {}, bias = {};
   if (TMA) {
     cudaError_t e = bwd && Q8 ? tile_map(&x, a.q, 1, a, G, width) : tile_map(&x, a.Wx, (int)sizeof(T), a, G, width);
+    if (e == cudaSuccess && a.bias) {
+      const unsigned long long dims[4] = {(unsigned long long)a.C, G, 1, 1};
+      const unsigned box[4] = {width, G, 1, 1};
+      e = encode_tensor_map(&bias, a.bias, (int)sizeof(T), 4, dims, box);
+    }
     if (e == cudaSuccess && bwd && a.dh) e = tile_map(&d, a.dh, (int)sizeof(T), a, 1, width);
     if (e == cudaSuccess && !bwd && Q8) e = tile_map(&q, a.q, 1, a, G, width);
     if (e == cudaSuccess && !bwd) e = tile_map(&out, a.h, (int)sizeof(T), a, 1, width);
@@ -1061,8 +1075,8 @@ template <typename T, int FN, bool Q8, bool TMA> cudaError_t gated_launch(bool b
   // as many CTAs as the SMs hold (see the kernels' launch bounds)
   const unsigned most = device_sms() * (bwd || Q8 ? 2 : 3);
   const unsigned ctas = bwd && a.db_mode == 3 ? a.tiles_c : a.solo || items < most ? items : most;
-  if (bwd) gated_bwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, d, out, a);
-  else gated_fwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, out, q, a);
+  if (bwd) gated_bwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, d, out, bias, a);
+  else gated_fwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, out, q, bias, a);
   note_launch();
   return cudaGetLastError();
 }
@@ -1185,9 +1199,9 @@ int rnn_gated_bwd(const rnn_gated_dims_t* d, const void* Wx, const void* b, cons
   if (rc || a.db_mode != 1) return rc;
   const int cols = z.G * z.C;
   if (d->dtype == RNN_BF16)
-    gated_db_kernel<<<(cols + 31) / 32, 256, 0, st>>>(a.dbp, (__nv_bfloat16*)db, d->B * z.chunks, cols);
+    gated_db_kernel<<<(cols + 31) / 32, 1024, 0, st>>>(a.dbp, (__nv_bfloat16*)db, d->B * z.chunks, cols);
   else
-    gated_db_kernel<<<(cols + 31) / 32, 256, 0, st>>>(a.dbp, (float*)db, d->B * z.chunks, cols);
+    gated_db_kernel<<<(cols + 31) / 32, 1024, 0, st>>>(a.dbp, (float*)db, d->B * z.chunks, cols);
   note_launch();
   return cuda_status(cudaGetLastError());
 }

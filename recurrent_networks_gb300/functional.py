@@ -169,15 +169,20 @@ class _GatedFn(torch.autograd.Function):
         h = torch.empty((B, T, N, D), dtype=dtype, device=dev)
         last = torch.empty((B, 1, N, D), dtype=torch.float32, device=dev)
         need = ctx.needs_input_grad
-        tape = None
         if need[0] or need[1] or need[2]:
-            tape = torch.empty(_lib.rnn_gated_tape_size(dims), dtype=torch.uint8, device=dev)
-        ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_FWD), dtype=torch.uint8, device=dev)
-        _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, ws)
-        if tape is not None:
-            ctx.dims, ctx.wx_shape, ctx.dtype = dims, Wx.shape, dtype
+            # the tape, and after it the workspace of both directions (small
+            # beside Wx): one allocation a pass
+            size = _lib.rnn_gated_tape_size(dims)
+            tape = torch.empty(size + max(_lib.rnn_gated_workspace_size(dims, _lib.WS_FWD),
+                                          _lib.rnn_gated_workspace_size(dims, _lib.WS_BWD)),
+                               dtype=torch.uint8, device=dev)
+            _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, (tape, size))
+            ctx.dims, ctx.wx_shape, ctx.dtype, ctx.size = dims, Wx.shape, dtype, size
             ctx.set_materialize_grads(False)
             ctx.save_for_backward(Wx if checkpoint is None else None, b, reset, lengths, tape)
+        else:
+            ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_FWD), dtype=torch.uint8, device=dev)
+            _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, None, ws)
         return h, last
 
     @staticmethod
@@ -193,8 +198,7 @@ def _gated_bwd(ctx, dh, dlast):
     dWx = torch.empty(ctx.wx_shape, dtype=ctx.dtype, device=dev) if need[0] else None
     db = torch.empty((G, N, D), dtype=ctx.dtype, device=dev) if need[1] else None
     ds = torch.empty((B, 1, N, D), dtype=torch.float32, device=dev) if need[2] else None
-    ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_BWD), dtype=torch.uint8, device=dev)
-    _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, ws)
+    _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, (tape, ctx.size))
     return dWx, db, ds, None, None, None, None
 
 
