@@ -316,6 +316,7 @@ template <int N, bool REVERSE> struct Chain {
   __device__ __forceinline__ void pass(float* enter) {
     Map g = {1.0f, 0.0f};  // the group's chunks before this one, a run of them a lane
     if (o > first) {
+      if (group > 0 && !is_set(early, group)) early = ld_word(state(group));  // beside the maps' round trip
       const int run = (o - first + Q - 1) / Q, from = first + q * run;
       for (int i = 0; i < run; i += 2) {
         ulonglong2 m[2];

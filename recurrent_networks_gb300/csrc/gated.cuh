@@ -83,11 +83,25 @@ template <int FN> __host__ __device__ constexpr bool gate_is_linear(int g) { ret
 template <int FN, int N> __device__ __forceinline__ constexpr float mul_of(int g) {
   return N == 1 || gate_is_linear<FN>(g) ? 1.0f : -1.4426950408889634f;
 }
-// e = exp(-z)
+// e = exp(-z). For fp32 z log2 e in two parts, the product and what its
+// rounding and the constant's left out, so that e keeps the exponential's own
+// 2^-22; z held to -88 .. 88 (e finite, NaN stays), where the sigmoid has
+// reached 0 and 1: 12 instructions to a sigmoid where expf and a division take
+// about twice that.
 __device__ __forceinline__ FV<2> exp_neg(const FV<2>& t) { return {{exp2_fast(t.v[0]), exp2_fast(t.v[1])}}; }
-__device__ __forceinline__ FV<1> exp_neg(const FV<1>& z) { return {{expf(-z.v[0])}}; }
+__device__ __forceinline__ FV<1> exp_neg(const FV<1>& z) {
+  float x;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(-z.v[0]), "f"(-88.0f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(88.0f));
+  const float t = x * 1.44269502f, l = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -t));  // log2 e = 1.44269502 + 1.926e-8
+  const float e = exp2_fast(t);
+  return {{fmaf(e, l * 0.693147181f, e)}};
+}
 __device__ __forceinline__ FV<2> rcp(const FV<2>& d) { return {{rcp_fast(d.v[0]), rcp_fast(d.v[1])}}; }
-__device__ __forceinline__ FV<1> rcp(const FV<1>& d) { return {{1.0f / d.v[0]}}; }
+__device__ __forceinline__ FV<1> rcp(const FV<1>& d) {
+  const float r = rcp_fast(d.v[0]);
+  return {{fmaf(r, fmaf(-d.v[0], r, 1.0f), r)}};
+}
 // 1 / d to a rounding, d <= 1.7e38 for N = 2 (one Newton step on the
 // approximate reciprocal): the factor f of a long memory enters every later
 // state, and the approximation alone, off to one side by up to 2^-23, moved
@@ -117,9 +131,11 @@ __device__ __forceinline__ void sigmoid_both(const FV<2>& t, FV<2>& f, FV<2>& n)
   n = mul(e, f);
 }
 __device__ __forceinline__ void sigmoid_both(const FV<1>& z, FV<1>& f, FV<1>& n) {
-  const float x = z.v[0], e = expf(-fabsf(x)), r = 1.0f / (1.0f + e), er = e * r;
-  f.v[0] = x >= 0.0f ? r : er;
-  n.v[0] = x >= 0.0f ? er : r;
+  float x;  // exp(-z) bounded as above
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(z.v[0]), "f"(-86.0f));
+  const FV<1> e = exp_neg(FV<1>{{x}});
+  f = rcp(add(e, splat<1>(1.0f)));
+  n = mul(e, f);
 }
 
 // f and u of c = f c' + u from the gates z[G]
