@@ -48,11 +48,15 @@ class GatedDims(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+# The same library through a binding that keeps the interpreter lock: for the
+# short calls that only enqueue. Giving the lock up and taking it again costs
+# tens of microseconds a call while autograd's thread runs beside.
+_short = None
 
 
 def load(path: str | None = None):
     """Load (building first if needed) the CUDA library; raises if impossible."""
-    global _lib
+    global _lib, _short
     with _lock:
         if _lib is None:
             lib = ctypes.CDLL(path or _build.build())
@@ -88,22 +92,19 @@ def load(path: str | None = None):
             lib.rnn_input_proj_fwd.argtypes = [i, i, i] + [vp] * 5 + [sz, vp]
             lib.rnn_input_proj_bwd.argtypes = [i, i, i] + [vp] * 7 + [sz, vp]
             gp, ll, f = ctypes.POINTER(GatedDims), ctypes.c_longlong, ctypes.c_float
-            lib.rnn_gated_num_gates.argtypes = [i]
-            lib.rnn_gated_tape_size.argtypes = [gp]
-            lib.rnn_gated_tape_size.restype = sz
-            lib.rnn_gated_workspace_size.argtypes = [gp, i]
-            lib.rnn_gated_workspace_size.restype = sz
-            lib.rnn_gated_fwd.argtypes = [gp] + [vp] * 9 + [sz, vp]
-            lib.rnn_gated_bwd.argtypes = [gp] + [vp] * 11 + [sz, vp]
-            lib.rnn_gated_step.argtypes = [i] * 6 + [vp] * 8
-            lib.rnn_act_scale_bytes.argtypes = [ll, i]
-            lib.rnn_act_scale_bytes.restype = sz
-            lib.rnn_act_pack.argtypes = [ll, i, i] + [vp] * 4
-            lib.rnn_act_unpack.argtypes = [ll, i, i] + [vp] * 4
-            lib.rnn_embed_bwd_workspace_size.argtypes = [ll, i, i]
-            lib.rnn_embed_bwd_workspace_size.restype = sz
-            lib.rnn_embed_fwd.argtypes = [ll, i, i, i, i, vp, vp, f, vp, vp, vp]
-            lib.rnn_embed_bwd.argtypes = [ll, i, i, i, i, vp, ll, vp, f, vp, vp, sz, vp]
+            short = ctypes.PyDLL(lib._name)
+            for name, args in (("rnn_gated_num_gates", [i]), ("rnn_gated_tape_size", [gp]),
+                               ("rnn_gated_workspace_size", [gp, i]), ("rnn_gated_fwd", [gp] + [vp] * 9 + [sz, vp]),
+                               ("rnn_gated_bwd", [gp] + [vp] * 11 + [sz, vp]), ("rnn_gated_step", [i] * 6 + [vp] * 8),
+                               ("rnn_act_scale_bytes", [ll, i]), ("rnn_act_pack", [ll, i, i] + [vp] * 4),
+                               ("rnn_act_unpack", [ll, i, i] + [vp] * 4), ("rnn_embed_bwd_workspace_size", [ll, i, i]),
+                               ("rnn_embed_fwd", [ll, i, i, i, i, vp, vp, f, vp, vp, vp]),
+                               ("rnn_embed_bwd", [ll, i, i, i, i, vp, ll, vp, f, vp, vp, sz, vp])):
+                for binding in (lib, short):
+                    getattr(binding, name).argtypes = args
+                    if name.endswith(("_size", "_bytes")):
+                        getattr(binding, name).restype = sz
+            _short = short
             _lib = lib
     return _lib
 
@@ -292,6 +293,12 @@ def rnn_input_proj_bwd(BT: int, I: int, C: int, x, W, dWx, dx, dW, dbias, worksp
 
 
 # ---- gated linear scan ------------------------------------------------------------
+def _quick():
+    if _short is None:
+        load()
+    return _short
+
+
 def _ws(workspace):
     """(pointer, bytes) of a workspace: a tensor, or (tensor, offset) for the rest of it."""
     t, at = workspace if isinstance(workspace, tuple) else (workspace, 0)
@@ -306,59 +313,59 @@ def make_gated_dims(B, T, N, D, function="linear", dtype=torch.bfloat16, checkpo
 
 
 def rnn_gated_num_gates(function) -> int:
-    return load().rnn_gated_num_gates(GATED_FUNCTIONS.get(function, -1) if isinstance(function, str) else function)
+    return _quick().rnn_gated_num_gates(GATED_FUNCTIONS.get(function, -1) if isinstance(function, str) else function)
 
 
 def rnn_gated_tape_size(dims: GatedDims) -> int:
-    return load().rnn_gated_tape_size(ctypes.byref(dims))
+    return _quick().rnn_gated_tape_size(ctypes.byref(dims))
 
 
 def rnn_gated_workspace_size(dims: GatedDims, kind: int = WS_FWD) -> int:
-    return load().rnn_gated_workspace_size(ctypes.byref(dims), kind)
+    return _quick().rnn_gated_workspace_size(ctypes.byref(dims), kind)
 
 
 def rnn_gated_fwd(dims: GatedDims, Wx, b, state0, reset, lengths, h, last, tape, workspace, stream=None) -> int:
-    rc = load().rnn_gated_fwd(ctypes.byref(dims), _p(Wx), _p(b), _p(state0), _p(reset), _p(lengths), _p(h), _p(last),
+    rc = _quick().rnn_gated_fwd(ctypes.byref(dims), _p(Wx), _p(b), _p(state0), _p(reset), _p(lengths), _p(h), _p(last),
                               _p(tape), *_ws(workspace), _stream(stream))
     return _check(rc, "rnn_gated_fwd")
 
 
 def rnn_gated_bwd(dims: GatedDims, Wx, b, reset, lengths, tape, dh, dlast, dWx, db, dstate0, workspace,
                   stream=None) -> int:
-    rc = load().rnn_gated_bwd(ctypes.byref(dims), _p(Wx), _p(b), _p(reset), _p(lengths), _p(tape), _p(dh), _p(dlast),
+    rc = _quick().rnn_gated_bwd(ctypes.byref(dims), _p(Wx), _p(b), _p(reset), _p(lengths), _p(tape), _p(dh), _p(dlast),
                               _p(dWx), _p(db), _p(dstate0), *_ws(workspace), _stream(stream))
     return _check(rc, "rnn_gated_bwd")
 
 
 def rnn_gated_step(rows, slots, N, D, function, dtype, Wx, b, slot, pool, pool_out, h, status=None, stream=None) -> int:
     fn = GATED_FUNCTIONS[function] if isinstance(function, str) else int(function)
-    rc = load().rnn_gated_step(int(rows), int(slots), int(N), int(D), fn, DTYPES[dtype], _p(Wx), _p(b), _p(slot),
+    rc = _quick().rnn_gated_step(int(rows), int(slots), int(N), int(D), fn, DTYPES[dtype], _p(Wx), _p(b), _p(slot),
                                _p(pool), _p(pool_out), _p(h), _p(status), _stream(stream))
     return _check(rc, "rnn_gated_step")
 
 
 # ---- 8-bit activation checkpoints ------------------------------------------------------
 def rnn_act_scale_bytes(rows: int, cols: int) -> int:
-    return int(load().rnn_act_scale_bytes(int(rows), int(cols)))
+    return int(_quick().rnn_act_scale_bytes(int(rows), int(cols)))
 
 
 def rnn_act_pack(rows: int, cols: int, x, q, scales, stream=None) -> int:
-    return _check(load().rnn_act_pack(int(rows), int(cols), DTYPES[x.dtype], _p(x), _p(q), _p(scales),
+    return _check(_quick().rnn_act_pack(int(rows), int(cols), DTYPES[x.dtype], _p(x), _p(q), _p(scales),
                                       _stream(stream)), "rnn_act_pack")
 
 
 def rnn_act_unpack(rows: int, cols: int, q, scales, x, stream=None) -> int:
-    return _check(load().rnn_act_unpack(int(rows), int(cols), DTYPES[x.dtype], _p(q), _p(scales), _p(x),
+    return _check(_quick().rnn_act_unpack(int(rows), int(cols), DTYPES[x.dtype], _p(q), _p(scales), _p(x),
                                         _stream(stream)), "rnn_act_unpack")
 
 
 # ---- token embedding -----------------------------------------------------------------------
 def rnn_embed_bwd_workspace_size(n: int, V: int, E: int) -> int:
-    return int(load().rnn_embed_bwd_workspace_size(int(n), int(V), int(E)))
+    return int(_quick().rnn_embed_bwd_workspace_size(int(n), int(V), int(E)))
 
 
 def rnn_embed_fwd(n: int, V: int, E: int, ids, W, scale: float, out, status=None, stream=None) -> int:
-    rc = load().rnn_embed_fwd(int(n), int(V), int(E), DTYPES[W.dtype], ids.element_size(), _p(ids), _p(W),
+    rc = _quick().rnn_embed_fwd(int(n), int(V), int(E), DTYPES[W.dtype], ids.element_size(), _p(ids), _p(W),
                               float(scale), _p(out), _p(status), _stream(stream))
     return _check(rc, "rnn_embed_fwd")
 
@@ -366,7 +373,7 @@ def rnn_embed_fwd(n: int, V: int, E: int, ids, W, scale: float, out, status=None
 def rnn_embed_bwd(n: int, V: int, E: int, ids, padding_idx: int, dout, scale: float, dW, workspace,
                   stream=None) -> int:
     """dW [V][E] from dout [n][E] (see include/rnn.h); padding_idx -1 = none."""
-    rc = load().rnn_embed_bwd(int(n), int(V), int(E), DTYPES[dW.dtype], ids.element_size(), _p(ids), int(padding_idx),
+    rc = _quick().rnn_embed_bwd(int(n), int(V), int(E), DTYPES[dW.dtype], ids.element_size(), _p(ids), int(padding_idx),
                               _p(dout), float(scale), _p(dW), _p(workspace),
                               workspace.numel() * workspace.element_size(), _stream(stream))
     return _check(rc, "rnn_embed_bwd")

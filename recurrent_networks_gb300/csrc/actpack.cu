@@ -9,77 +9,103 @@
 namespace rnn {
 namespace {
 
-// A thread packs one block of 32 rows of V columns, a warp 32 V neighbouring
-// columns. All rows are loaded before the scale is known, so each value is read
-// once: 32 loads in flight hide the memory's latency. V = 4 where the columns
-// allow (8- or 16-byte loads, 4-byte stores of q), else 1.
+// Four threads pack a block of 32 rows of V columns, 8 rows each (lanes 8
+// apart: a warp has 8 V neighbouring columns, 128 bytes of a row where V is 8
+// bf16 or 4 fp32). Every value is read once; 8 loads of 16 bytes a thread and
+// some 40 registers keep 150 KB and more of an SM's loads in flight (a thread
+// with all 32 rows took 160 registers and reached 3.9 TB/s).
 template <typename T, int V> struct Cols;
-template <> struct Cols<__nv_bfloat16, 4> {
-  uint2 r;
-  __device__ void load(const __nv_bfloat16* p) { r = __ldcs((const uint2*)p); }
-  __device__ void clear() { r = make_uint2(0, 0); }
-  __device__ float get(int v) const {
-    const uint32_t w = v < 2 ? r.x : r.y;
-    return __uint_as_float(v & 1 ? w & 0xffff0000u : w << 16);
-  }
+template <> struct Cols<__nv_bfloat16, 8> {
+  static constexpr int W = 4, N = 2;  // words, columns of a word
+  uint32_t w[4];
+  __device__ void load(const __nv_bfloat16* p) { *(uint4*)w = __ldcs((const uint4*)p); }
 };
 template <> struct Cols<float, 4> {
-  float4 r;
-  __device__ void load(const float* p) { r = __ldcs((const float4*)p); }
-  __device__ void clear() { r = make_float4(0, 0, 0, 0); }
-  __device__ float get(int v) const { return v == 0 ? r.x : v == 1 ? r.y : v == 2 ? r.z : r.w; }
+  static constexpr int W = 4, N = 1;
+  uint32_t w[4];
+  __device__ void load(const float* p) { *(uint4*)w = __ldcs((const uint4*)p); }
 };
-template <typename T> struct Cols<T, 1> {
-  T r;
-  __device__ void load(const T* p) { r = *p; }
-  __device__ void clear() { r = from_f<T>(0.0f); }
-  __device__ float get(int) const { return to_f(r); }
+template <> struct Cols<__nv_bfloat16, 1> {
+  static constexpr int W = 1, N = 1;
+  uint32_t w[1];
+  __device__ void load(const __nv_bfloat16* p) { w[0] = *(const unsigned short*)p; }
 };
-__device__ __forceinline__ void store_q(signed char* p, const int (&q)[4]) {
-  *(uint32_t*)p = (q[0] & 255) | (q[1] & 255) << 8 | (q[2] & 255) << 16 | (uint32_t)q[3] << 24;
+template <> struct Cols<float, 1> {
+  static constexpr int W = 1, N = 1;
+  uint32_t w[1];
+  __device__ void load(const float* p) { w[0] = *(const uint32_t*)p; }
+};
+template <typename T> __device__ __forceinline__ FV<1> word_values(uint32_t w, FV<1>*) {
+  return {{__uint_as_float(sizeof(T) == 4 ? w : w << 16)}};
 }
-__device__ __forceinline__ void store_q(signed char* p, const int (&q)[1]) { *p = (signed char)q[0]; }
+template <typename T> __device__ __forceinline__ FV<2> word_values(uint32_t w, FV<2>*) {
+  return {{__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}};
+}
+// V bytes at p
+template <int V> __device__ __forceinline__ void store_bytes(void* p, const uint32_t (&b)[2]) {
+  if constexpr (V == 8) *(uint2*)p = make_uint2(b[0], b[1]);
+  else if constexpr (V == 4) *(uint32_t*)p = b[0];
+  else *(unsigned char*)p = (unsigned char)b[0];
+}
 
 template <typename T, int V>
-__global__ void __launch_bounds__(128) act_pack_kernel(long long rows, int cols, const T* x, signed char* q,
+__global__ void __launch_bounds__(256) act_pack_kernel(long long rows, int cols, const T* x, signed char* q,
                                                        unsigned char* scales) {
+  using X = Cols<T, V>;
+  constexpr int W = X::W, N = X::N, ROWS = 8;
   const long long blocks = (rows + ACT_BLOCK - 1) / ACT_BLOCK;
-  const int groups = (cols + V - 1) / V;
-  for (long long id = (long long)blockIdx.x * 128 + threadIdx.x; id < blocks * groups;
-       id += (long long)gridDim.x * 128) {
+  const int lane = threadIdx.x & 31, part = lane >> 3;
+  const int groups = (cols + 8 * V - 1) / (8 * V);  // of 8 V columns, a warp's
+  for (long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); id < blocks * groups; id += (long long)gridDim.x * 8) {
     const long long k = id / groups;
-    const int c = (int)(id % groups) * V;
-    const int n = (int)(rows - k * ACT_BLOCK < ACT_BLOCK ? rows - k * ACT_BLOCK : ACT_BLOCK);
-    const size_t at = (size_t)k * ACT_BLOCK * cols + c;
-    Cols<T, V> w[ACT_BLOCK];
+    const int c = ((int)(id % groups) * 8 + (lane & 7)) * V;
+    const bool on = c < cols;
+    const long long r0 = k * ACT_BLOCK + part * ROWS;
+    const int n = on ? (int)max(0ll, min((long long)ROWS, rows - r0)) : 0;
+    const size_t at = (size_t)r0 * cols + c;
+    X v[ROWS];
 #pragma unroll
-    for (int r = 0; r < ACT_BLOCK; ++r) {
-      if (r < n) w[r].load(x + at + (size_t)r * cols);
-      else w[r].clear();
+    for (int r = 0; r < ROWS; ++r) {
+      if (r < n) v[r].load(x + at + (size_t)r * cols);
+      else
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[r].w[i] = 0;
     }
-    float inv[V];
-    bool fin[V];
-    uint32_t bytes = 0;
+    FV<N> inv[W];
+    uint32_t bytes[2] = {0, 0};
+    bool huge = false, odd = false;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      uint32_t top = 0;  // magnitudes compared as bits: NaN and infinity are the largest
+    for (int i = 0; i < W; ++i) {
+      uint32_t top = 0;
 #pragma unroll
-      for (int r = 0; r < ACT_BLOCK; ++r) top = max(top, __float_as_uint(fabsf(w[r].get(v))));
-      const unsigned s = act_scale_byte(__uint_as_float(top));
-      inv[v] = act_inv_scale(s);
-      fin[v] = s != ACT_NONFINITE;
-      bytes |= s << (8 * v);
+      for (int r = 0; r < ROWS; ++r) top = mag_max<T>(top, v[r].w[i]);
+      top = mag_max<T>(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      top = mag_max<T>(top, __shfl_xor_sync(0xffffffffu, top, 16));
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const unsigned s = act_scale_byte(__uint_as_float(mag_bits<T>(top, j)));
+        inv[i].v[j] = act_inv_scale(s);
+        huge |= s == 248;
+        odd |= s == ACT_NONFINITE;
+        bytes[(i * N + j) / 4] |= s << (8 * ((i * N + j) % 4));
+      }
     }
-    unsigned char* sc = scales + (size_t)k * cols + c;
-    if (V == 4) *(uint32_t*)sc = bytes;
-    else *sc = (unsigned char)bytes;
+    if (on && part == 0) store_bytes<V>(scales + (size_t)k * cols + c, bytes);
 #pragma unroll
-    for (int r = 0; r < ACT_BLOCK; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
       if (r >= n) break;
-      int b[V];
+      uint32_t b[2] = {0, 0};
 #pragma unroll
-      for (int v = 0; v < V; ++v) b[v] = fin[v] ? act_quant(w[r].get(v), inv[v]) : 0;
-      store_q(q + at + (size_t)r * cols, b);
+      for (int i = 0; i < W; ++i) {
+        uint32_t w = quant(word_values<T>(v[r].w[i], (FV<N>*)nullptr), inv[i], huge);
+        if (odd) {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (inv[i].v[j] == 0.0f) w &= ~(255u << (8 * j));
+        }
+        b[i * N / 4] |= w << (8 * (i * N % 4));
+      }
+      store_bytes<V>(q + at + (size_t)r * cols, b);
     }
   }
 }
@@ -135,19 +161,20 @@ bool act_ok(long long rows, int cols, int dtype) {
   return rows >= 0 && rows < (1ll << 40) && cols >= 1 && (dtype == RNN_F32 || dtype == RNN_BF16);
 }
 
-unsigned act_blocks(long long threads) {
-  const long long n = (threads + 127) / 128;
-  return (unsigned)(n < (1ll << 30) ? n : (1ll << 30));
+unsigned act_blocks(long long n) { return (unsigned)(n < (1ll << 30) ? n : (1ll << 30)); }
+template <typename T, int V>
+cudaError_t act_pack_run(long long rows, int cols, const void* x, void* q, void* scales, cudaStream_t st) {
+  const long long warps = (rows + ACT_BLOCK - 1) / ACT_BLOCK * ((cols + 8 * V - 1) / (8 * V));
+  act_pack_kernel<T, V><<<act_blocks((warps + 7) / 8), 256, 0, st>>>(rows, cols, (const T*)x, (signed char*)q,
+                                                                     (unsigned char*)scales);
+  note_launch();
+  return cudaGetLastError();
 }
 template <typename T, int V>
-cudaError_t act_run(bool pack, long long rows, int cols, void* x, void* q, void* scales, cudaStream_t st) {
-  const long long groups = (cols + V - 1) / V;
-  if (pack)
-    act_pack_kernel<T, V><<<act_blocks((rows + ACT_BLOCK - 1) / ACT_BLOCK * groups), 128, 0, st>>>(
-        rows, cols, (const T*)x, (signed char*)q, (unsigned char*)scales);
-  else
-    act_unpack_kernel<T, V><<<act_blocks((rows + 7) / 8 * groups), 128, 0, st>>>(
-        rows, cols, (const signed char*)q, (const unsigned char*)scales, (T*)x);
+cudaError_t act_unpack_run(long long rows, int cols, const void* q, const void* scales, void* x, cudaStream_t st) {
+  const long long threads = (rows + 7) / 8 * ((cols + V - 1) / V);
+  act_unpack_kernel<T, V><<<act_blocks((threads + 127) / 128), 128, 0, st>>>(rows, cols, (const signed char*)q,
+                                                                             (const unsigned char*)scales, (T*)x);
   note_launch();
   return cudaGetLastError();
 }
@@ -156,12 +183,17 @@ int act_call(bool pack, long long rows, int cols, int dtype, void* x, void* q, v
   if (rows == 0) return RNN_OK;
   if (!x || !q || !scales || !al16(x) || !al16(q) || !al16(scales)) return RNN_EINVAL;
   cudaStream_t st = (cudaStream_t)stream;
+  const bool bf = dtype == RNN_BF16;
+  if (pack)
+    return cuda_status(bf ? cols % 8 == 0 ? act_pack_run<__nv_bfloat16, 8>(rows, cols, x, q, scales, st)
+                                          : act_pack_run<__nv_bfloat16, 1>(rows, cols, x, q, scales, st)
+                       : cols % 4 == 0 ? act_pack_run<float, 4>(rows, cols, x, q, scales, st)
+                                       : act_pack_run<float, 1>(rows, cols, x, q, scales, st));
   const bool four = cols % 4 == 0;
-  if (dtype == RNN_BF16)
-    return cuda_status(four ? act_run<__nv_bfloat16, 4>(pack, rows, cols, x, q, scales, st)
-                            : act_run<__nv_bfloat16, 1>(pack, rows, cols, x, q, scales, st));
-  return cuda_status(four ? act_run<float, 4>(pack, rows, cols, x, q, scales, st)
-                          : act_run<float, 1>(pack, rows, cols, x, q, scales, st));
+  return cuda_status(bf ? four ? act_unpack_run<__nv_bfloat16, 4>(rows, cols, q, scales, x, st)
+                               : act_unpack_run<__nv_bfloat16, 1>(rows, cols, q, scales, x, st)
+                     : four ? act_unpack_run<float, 4>(rows, cols, q, scales, x, st)
+                            : act_unpack_run<float, 1>(rows, cols, q, scales, x, st));
 }
 
 }  // namespace

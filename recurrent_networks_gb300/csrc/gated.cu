@@ -118,30 +118,6 @@ __device__ __forceinline__ FV<2> bytes_f(uint32_t w, FV<2>*) {
 }
 __device__ __forceinline__ FV<1> bytes_f(uint32_t w, FV<1>*) { return {{(float)(signed char)w}}; }
 
-// The largest magnitudes of a lane's channels, in the storage type's bits (an
-// infinity or NaN stays one), and the fp32 bits of channel v.
-template <typename T> __device__ __forceinline__ uint32_t mag_max(uint32_t top, uint32_t x);
-template <> __device__ __forceinline__ uint32_t mag_max<float>(uint32_t top, uint32_t x) { return max(top, x & 0x7fffffffu); }
-template <> __device__ __forceinline__ uint32_t mag_max<__nv_bfloat16>(uint32_t top, uint32_t x) {
-  uint32_t r;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(top), "r"(x & 0x7fff7fffu));
-  return r;
-}
-template <typename T> __device__ __forceinline__ uint32_t mag_bits(uint32_t top, int v) {
-  return sizeof(T) == 4 ? top : v ? top & 0xffff0000u : top << 16;
-}
-// q of a lane's channels as bytes: a / 2^e + 1.5 2^23 rounds to nearest even
-// and leaves q in the low byte. `huge`: some block may saturate (act_scale_byte).
-template <int N> __device__ __forceinline__ uint32_t quant(const FV<N>& a, const FV<N>& inv, bool huge) {
-  FV<N> t = mul(a, inv);
-  if (huge) {
-#pragma unroll
-    for (int v = 0; v < N; ++v) t.v[v] = fminf(fmaxf(t.v[v], -127.0f), 127.0f);
-  }
-  t = add(t, splat<N>(12582912.0f));
-  return N == 1 ? __float_as_uint(t.v[0]) & 255u : __byte_perm(__float_as_uint(t.v[0]), __float_as_uint(t.v[N - 1]), 0x0040) & 0xffffu;
-}
-
 // A lane's channels at p (n of them inside the row: 0 .. N), and back. `wide`:
 // the row starts on 4 bytes.
 template <typename T> __device__ __forceinline__ uint32_t load_lane(const T* p, int n, bool wide) {

