@@ -656,6 +656,20 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int j = 0; j < STEPS; ++j) dmine[j * 32 + lane] = 0;
   }
   __syncthreads();
+  // db's sums over the warps of an item
+  auto sum_db = [&](int b, int k, int ct) {
+    for (int i = threadIdx.x; i < G * 32 * N; i += THREADS) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) s += dbs[w * G * 32 * N + i];
+      const int g = i / (32 * N), ch = ct + i % 32 * N + i / 32 % N;
+      if (ch < p.C) {
+        if (p.db_mode == 3) ((T*)p.db)[(size_t)g * p.C + ch] = from_f<T>(s);
+        else __stcg(p.dbp + (((size_t)b * p.chunks + k) * G + g) * p.C + ch, s);
+      }
+    }
+  };
+  int last_b = -1, last_k = 0, last_ct = 0;  // mode 1: the item whose sums wait for the next load
   for (unsigned loads = 0, turn = 0; shared->x >= 0; ++turn) {
   const Item it = item_of<N>(p, *shared);
   if (TMA) {
@@ -683,6 +697,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   Ch chain(p, it, failed);
   chain.ask(p.dlast);
+  if (last_b >= 0) sum_db(last_b, last_k, last_ct);
   const float cc = chain.ch < p.C ? __ldg(p.carry + ((size_t)it.b * p.chunks + it.k) * p.C + chain.ch) : 0.0f;  // the state that enters the chunk
   FV<N> bias[G], scale[Q8 ? G : 1];
   if (Q8) {
@@ -844,18 +859,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int v = 0; v < N; ++v) mine_db[(g * N + v) * 32] = more ? mine_db[(g * N + v) * 32] + db[g].v[v] : db[g].v[v];
-    if (p.db_mode != 3 || it.b + 1 == p.B) {
+    if (p.db_mode == 2 || (p.db_mode == 3 && it.b + 1 == p.B)) {
       __syncthreads();
-      for (int i = threadIdx.x; i < G * 32 * N; i += THREADS) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += dbs[w * G * 32 * N + i];
-        const int g = i / (32 * N), ch = it.ct + i % 32 * N + i / 32 % N;
-        if (ch < p.C) {
-          if (p.db_mode == 3) ((T*)p.db)[(size_t)g * p.C + ch] = from_f<T>(s);
-          else __stcg(p.dbp + (((size_t)it.b * p.chunks + it.k) * G + g) * p.C + ch, s);
-        }
-      }
+      sum_db(it.b, it.k, it.ct);
     }
     if (p.db_mode == 2) {
       __threadfence();  // this thread's sums, before the count
@@ -879,8 +885,10 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   if (TMA && lane == 0) bulk_wait_group_read<0>();  // the tile is read from until then
   if (threadIdx.x == 0) *shared = place_of<true>(p, p.db_mode == 3 ? it.tile + p.tiles_c : next);
+  if (p.db_mode == 1) last_b = it.b, last_k = it.k, last_ct = it.ct;
   __syncthreads();
   }
+  if (last_b >= 0) sum_db(last_b, last_k, last_ct);
 }
 
 template <typename T, int FN, bool Q8> constexpr int fwd_smem() {
