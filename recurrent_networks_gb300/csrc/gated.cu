@@ -31,6 +31,7 @@ constexpr int MAX_SPAN = 4;  // log2
 struct GatedArgs {
   int B, T, C, chunks;  // C = N D channels
   int tiles_c;          // channel tiles per batch row
+  int width;            // channels of a tile: a full row of lanes, or 28 lanes' (see fetch_rows)
   int span;             // log2 of the chunks per group
   int solo;  // one chunk, all CTAs at once: no waits, so block 0 clears the status word itself
   const void* Wx;
@@ -160,9 +161,9 @@ template <int N> __device__ __forceinline__ Item item_of(const GatedArgs& p, con
   it.b = s.z;
   it.len = s.w;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  it.ct = (it.tile - it.b * p.tiles_c) * 32 * N;
+  it.ct = (it.tile - it.b * p.tiles_c) * p.width;
   it.ch = it.ct + lane * N;
-  it.n = min(max(p.C - it.ch, 0), N);
+  it.n = min(max(min(p.C, it.ct + p.width) - it.ch, 0), N);
   it.t0 = it.k * GATED_CHUNK + warp * STEPS;
   it.live = min(max(it.len - it.t0, 0), STEPS);
   it.rst = 0;
@@ -222,7 +223,7 @@ template <int N, bool REVERSE> struct Chain {
     first = group << p.span;
     c = threadIdx.x / Q;
     q = threadIdx.x % Q;
-    ch = it.ct + c % 32 * N + c / 32;
+    ch = c % 32 * N < p.width ? it.ct + c % 32 * N + c / 32 : p.C;  // (p.C: a slot without a channel)
   }
   __device__ __forceinline__ size_t at(int i) const {
     return ((size_t)i * ((unsigned)p.B * p.tiles_c) + it.tile) * N * 32 + c;
@@ -340,54 +341,52 @@ template <int N, bool REVERSE> struct Chain {
   }
 };
 
-// A warp's steps of a tile whose rows (t, g) are 128 bytes, by the lanes' own
-// asynchronous copies (rows that TMA cannot take). Rows past `live` are not
-// read. An odd number of 2-byte channels puts every other row 2 bytes off: then
-// the words that hold the row are copied, the 33rd into `extra` [STEPS ROWS],
-// and fetch_align shifts the row once they are there.
+// A warp's steps of a tile by the lanes' own asynchronous copies, for rows that
+// TMA cannot take (or must not, see `solo`). Rows that are no multiple of 16
+// bytes start anywhere in one; the tile then has 28 lanes' channels, 112 bytes,
+// which lie in the 8 aligned 16-byte pieces that a row's 128-byte place holds.
+// They are copied as they lie, 4 rows an instruction, and read with the row's
+// shift (Rows). (4-byte copies to the final places took 20 of 51 us forward at
+// B=4 T=2048 C=998.) Rows past `live` are not read, nor anything past the end.
 template <typename T, int ROWS>
-__device__ __forceinline__ void fetch_lanes(const GatedArgs& p, const Item& it, const T* src, uint32_t* dst, uint32_t* extra) {
-  const int lane = threadIdx.x & 31, rows = it.live * ROWS;
-  const size_t row0 = ((size_t)it.b * p.T + it.t0) * ROWS;
-  const uint32_t to = smem_u32(dst + lane);
-  if (p.C % 2 == 0 || sizeof(T) == 4) {
-    const T* at = src + row0 * p.C + it.ch;
-    if (it.n > 0) {
-#pragma unroll 8
-      for (int r = 0; r < rows; ++r)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + r * 128), "l"(at + (size_t)r * p.C) : "memory");
-    }
-  } else {
-    const size_t all = (size_t)p.B * p.T * ROWS * p.C;  // (the tensor's last word may be half a word)
-    const int width = min(p.C - it.ct, 64);
+__device__ __forceinline__ void fetch_rows(const GatedArgs& p, const Item& it, const T* src, uint32_t* dst) {
+  const int lane = threadIdx.x & 31, rows = it.live * ROWS, piece = lane & 7;
+  const int bytes = max(min(p.C - it.ct, p.width), 0) * (int)sizeof(T);
+  const size_t all = (size_t)p.B * p.T * ROWS * p.C * sizeof(T);
+  const uint32_t to = smem_u32(dst) + piece * 16;
+  size_t at = ((((size_t)it.b * p.T + it.t0) * ROWS + (lane >> 3)) * p.C + it.ct) * sizeof(T);
+  const size_t step = (size_t)4 * p.C * sizeof(T);
 #pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      const size_t e0 = (row0 + r) * p.C + it.ct, end = e0 + width, e = (e0 & ~(size_t)1) + 2 * lane;
-      if (e < end)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + r * 128), "l"(src + e),
-                     "r"(e + 1 < all ? 4 : 2)
-                     : "memory");
-      if (lane == 0 && e + 64 < end)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(extra + r)), "l"(src + e + 64),
-                     "r"(e + 65 < all ? 4 : 2)
-                     : "memory");
+  for (int r = lane >> 3; r < rows; r += 4, at += step) {
+    const size_t from = (at & ~(size_t)15) + piece * 16;
+    if (from < at + bytes)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + r * 128), "l"((const char*)src + from),
+                   "r"((int)(all - from < 16 ? all - from : 16))
+                   : "memory");
+  }
+}
+__device__ __forceinline__ void fetch_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();  // the lanes read one another's pieces
+}
+// The 4-byte words of a lane in a warp's rows of a tile.
+template <typename T, int ROWS, bool TMA> struct Rows {
+  const uint32_t* at;  // the lane's word of the first row
+  unsigned e0, step;   // of a row: elements from the 16-byte boundary, mod 16 bytes; of the next one more
+  __device__ __forceinline__ Rows(const GatedArgs& p, const Item& it, const uint32_t* tile) : at(tile + (threadIdx.x & 31)) {
+    if (!TMA) {
+      e0 = (unsigned)(((size_t)it.b * p.T + it.t0) * ROWS * p.C + it.ct);
+      step = (unsigned)p.C;
     }
   }
-}
-template <typename T, int ROWS>
-__device__ __forceinline__ void fetch_align(const GatedArgs& p, const Item& it, uint32_t* dst, const uint32_t* extra) {
-  if (p.C % 2 == 0 || sizeof(T) == 4) return;
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
-  size_t e0 = ((size_t)it.b * p.T + it.t0) * ROWS * p.C + it.ct;
-  for (int r = 0; r < it.live * ROWS; ++r, e0 += p.C) {
-    if (!(e0 & 1)) continue;
-    const uint32_t w = dst[r * 32 + lane], up = __shfl_down_sync(0xffffffffu, w, 1);
-    dst[r * 32 + lane] = w >> 16 | (lane < 31 ? up : extra[r]) << 16;
+  __device__ __forceinline__ uint32_t operator()(int r) const {
+    if (TMA) return at[r * 32];
+    const unsigned e = e0 + r * step;
+    if (sizeof(T) == 4) return at[r * 32 + (e & 3)];
+    const uint32_t* w = at + r * 32 + ((e & 7) >> 1);
+    return e & 1 ? w[0] >> 16 | w[1] << 16 : w[0];
   }
-  __syncwarp();
-}
-__device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+};
 
 // A lane's biases, scaled as the gates want them: from the copy beside the tile
 // [G][32] (TMA), or from memory.
@@ -442,7 +441,6 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
     fence_mbar_init_cluster();
   }
   uint32_t* mine = tile + warp * STEPS * G * 32;
-  uint32_t* extra = (uint32_t*)enter + warp * STEPS * G;  // (free until all warps have their maps)
   bool failed = false;
   if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
   if (threadIdx.x == 0) *shared = place_of<false>(p, p.solo ? blockIdx.x : atomicAdd(p.ticket, 1u));
@@ -459,7 +457,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
       tma_load_4d(smem_u32(bcopy), &bmap, bbar, it.ct, 0, 0, 0);
     }
   } else {
-    fetch_lanes<T, G>(p, it, (const T*)p.Wx, mine, extra);
+    fetch_rows<T, G>(p, it, (const T*)p.Wx, mine);
   }
   Ch chain(p, it, failed);
   chain.ask(p.s0);
@@ -470,9 +468,9 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
     if (it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
   } else {
     fetch_wait();
-    fetch_align<T, G>(p, it, mine, extra);
   }
 
+  const Rows<T, G, TMA> raws(p, it, mine);
   FV<N> f[STEPS], u[Q8 ? STEPS : 1], P = splat<N>(1.0f), H = splat<N>(0.0f);
   uint32_t top[G];
 #pragma unroll
@@ -485,7 +483,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
       FV<N> z[G], w;
 #pragma unroll
       for (int g = 0; g < (FN == GATED_LINEAR && !Q8 ? G - 1 : G); ++g) {  // o is read when it is needed
-        const uint32_t raw = mine[(j * G + g) * 32 + lane];
+        const uint32_t raw = raws(j * G + g);
         if (Q8) top[g] = on ? mag_max<T>(top[g], raw) : top[g];
         z[g] = gate<FN>(g, Lane<T>::unpack(raw), bias[g]);
       }
@@ -499,6 +497,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
       if (Q8) {
         u[j] = w;
       } else {
+        if (!TMA) __syncwarp();  // the rows are read across the lanes
         mine[(j * G + U0) * 32 + lane] = __float_as_uint(w.v[0]);
         if (N == 2) mine[(j * G + U1) * 32 + lane] = __float_as_uint(w.v[N - 1]);
       }
@@ -544,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
     for (int j = 0; j < STEPS; ++j)
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        uint32_t w = quant(Lane<T>::unpack(mine[(j * G + g) * 32 + lane]), inv[g], huge);
+        uint32_t w = quant(Lane<T>::unpack(raws(j * G + g)), inv[g], huge);
         if (j >= it.live) w = 0;
         if (odd) {
 #pragma unroll
@@ -585,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
       const bool on = !MASK || j < it.live, rst = MASK && (it.rst >> j & 1);
       FV<N> w, y, o;
       if (FN == GATED_LINEAR)
-        o = sigmoid(gate<FN>(G - 1, Lane<T>::unpack(mine[(j * G + G - 1) * 32 + lane]), bias[G - 1]));
+        o = sigmoid(gate<FN>(G - 1, Lane<T>::unpack(raws(j * G + G - 1)), bias[G - 1]));
       if (Q8) {
         w = u[Q8 ? j : 0];
       } else {
@@ -596,6 +595,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
       y = FN == GATED_LINEAR ? mul(o, c) : c;
       if (MASK) y = select(on, y, splat<N>(0.0f));
       // step j's row lies in a step before j (or is row 0 of step 0), all read
+      if (!TMA) __syncwarp();
       mine[j * 32 + lane] = Lane<T>::pack(y);
     }
   });
@@ -646,7 +646,6 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   unsigned char* mine = tile + warp * STEPS * G * XB;
   uint32_t* dmine = dtile + warp * STEPS * 32;
-  uint32_t* extra = (uint32_t*)enter + warp * STEPS * (G + 1);  // (enter and begin are free until all warps have their maps)
   const bool wide = p.C % 2 == 0;
   bool failed = false;
   if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
@@ -662,8 +661,8 @@ __global__ void __launch_bounds__(THREADS, 2)
       float s = 0.0f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) s += dbs[w * G * 32 * N + i];
-      const int g = i / (32 * N), ch = ct + i % 32 * N + i / 32 % N;
-      if (ch < p.C) {
+      const int g = i / (32 * N), at = i % 32 * N + i / 32 % N, ch = ct + at;
+      if (at < p.width && ch < p.C) {
         if (p.db_mode == 3) ((T*)p.db)[(size_t)g * p.C + ch] = from_f<T>(s);
         else __stcg(p.dbp + (((size_t)b * p.chunks + k) * G + g) * p.C + ch, s);
       }
@@ -691,9 +690,9 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int v = 0; v < N; ++v)
           mine[r * XB + lane * N + v] = v < it.n ? (unsigned char)__ldg(at + (size_t)r * p.C + v) : 0;
     } else {
-      fetch_lanes<T, G>(p, it, (const T*)p.Wx, (uint32_t*)mine, extra);
+      fetch_rows<T, G>(p, it, (const T*)p.Wx, (uint32_t*)mine);
     }
-    if (p.dh) fetch_lanes<T, 1>(p, it, (const T*)p.dh, dmine, extra + STEPS * G);
+    if (p.dh) fetch_rows<T, 1>(p, it, (const T*)p.dh, dmine);
   }
   Ch chain(p, it, failed);
   chain.ask(p.dlast);
@@ -717,17 +716,17 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
   } else {
     fetch_wait();
-    if (!Q8) fetch_align<T, G>(p, it, (uint32_t*)mine, extra);
-    if (p.dh) fetch_align<T, 1>(p, it, dmine, extra + STEPS * G);
   }
 
+  const Rows<T, G, TMA> raws(p, it, (const uint32_t*)mine);
+  const Rows<T, 1, TMA> drows(p, it, dmine);
   auto gate_at = [&](int j, int g) {
     if (Q8) {
       const unsigned char* r = mine + (j * G + g) * XB + lane * N;
       const uint32_t w = N == 2 ? *(const unsigned short*)r : *r;
       return fma(bytes_f(w, (FV<N>*)nullptr), scale[Q8 ? g : 0], bias[g]);
     }
-    return gate<FN>(g, Lane<T>::unpack(*(const uint32_t*)(mine + (j * G + g) * XB + lane * 4)), bias[g]);
+    return gate<FN>(g, Lane<T>::unpack(raws(j * G + g)), bias[g]);
   };
 
   FV<N> f[STEPS], u[STEPS], P = splat<N>(1.0f), H = splat<N>(0.0f), E = splat<N>(0.0f);
@@ -736,7 +735,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
       const bool on = !MASK || j < it.live, rst = MASK && (it.rst >> j & 1);
-      FV<N> z[G], e = Lane<T>::unpack(dmine[j * 32 + lane]);
+      FV<N> z[G], e = Lane<T>::unpack(drows(j));
 #pragma unroll
       for (int g = 0; g < G; ++g) z[g] = gate_at(j, g);
       gated_coeff<FN, N>(z, f[j], u[j]);
@@ -814,7 +813,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
     for (int j = STEPS - 1; j >= 0; --j) {
       const bool on = !MASK || j < it.live, rst = MASK && (it.rst >> j & 1);
-      FV<N> z[G], da[G], d = Lane<T>::unpack(dmine[j * 32 + lane]);
+      FV<N> z[G], da[G], d = Lane<T>::unpack(drows(j));
 #pragma unroll
       for (int g = 0; g < G; ++g) z[g] = gate_at(j, g);
       FV<N> y = x;
@@ -866,14 +865,14 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (p.db_mode == 2) {
       __threadfence();  // this thread's sums, before the count
       __syncthreads();
-      if (threadIdx.x == 0) shared[1].x = (int)atomicAdd(p.done + it.ct / (32 * N), 1u);
+      if (threadIdx.x == 0) shared[1].x = (int)atomicAdd(p.done + it.ct / p.width, 1u);
       __syncthreads();
       const int rows = p.B * p.chunks;
       if (shared[1].x == rows - 1) {
         __threadfence();
         for (int i = threadIdx.x; i < G * 32 * N; i += THREADS) {
           const int g = i / (32 * N), ch = it.ct + i % (32 * N);
-          if (ch >= p.C) continue;
+          if (ch >= min(p.C, it.ct + p.width)) continue;
           const float* at = p.dbp + (size_t)g * p.C + ch;
           float s = 0.0f;
 #pragma unroll 16
@@ -981,12 +980,12 @@ bool gated_dims_ok(const rnn_gated_dims_t* d) {
   return d && d->B >= 1 && d->T >= 0 && d->N >= 1 && d->D >= 1 && (d->function == RNN_LINEAR || d->function == RNN_LINEAR_COUPLED) &&
          (d->dtype == RNN_F32 || d->dtype == RNN_BF16) && (d->checkpoint == RNN_CKPT_NONE || d->checkpoint == RNN_CKPT_INT8) &&
          (long long)d->N * d->D <= (1 << 28) &&
-         // one CTA per 128 steps of 32 (at least) channels
-         (double)d->B * (d->N * (double)d->D / 32 + 1) * (d->T / (double)GATED_CHUNK + 1) < 2147483647.0;
+         // one item per 128 steps of 28 (at least) channels
+         (double)d->B * (d->N * (double)d->D / 28 + 1) * (d->T / (double)GATED_CHUNK + 1) < 2147483647.0;
 }
 
 struct GatedSizes {
-  int G, C, chunks, qblocks, tiles_c, span, solo, db_mode;
+  int G, C, chunks, qblocks, width, tiles_c, span, solo, db_mode;
   size_t esize, carry, q, qs, tape;
   size_t sync, states, maps, dbp;  // workspace: status, ticket, states and maps (sync: zeroed by every call) | db sums
 };
@@ -997,8 +996,10 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   z.chunks = (d->T + GATED_CHUNK - 1) / GATED_CHUNK;
   z.qblocks = (d->T + ACT_BLOCK - 1) / ACT_BLOCK;
   z.esize = d->dtype == RNN_BF16 ? 2 : 4;
-  const int width = d->dtype == RNN_BF16 ? 64 : 32;
-  z.tiles_c = (z.C + width - 1) / width;
+  // whole rows of lanes where rows are 16-byte multiples, else 28 lanes (fetch_rows)
+  const int lane = d->dtype == RNN_BF16 ? 2 : 1;
+  z.width = (z.C * z.esize) % 16 == 0 ? 32 * lane : 28 * lane;
+  z.tiles_c = (z.C + z.width - 1) / z.width;
   const size_t tiles = (size_t)d->B * z.tiles_c;
   // A hop of the chain takes about 1.2 us, in which the GPU moves some 100
   // tiles: with fewer tiles than that (and a margin of two), a group of chunks
@@ -1084,7 +1085,7 @@ cudaError_t gated_launch(const rnn_gated_dims_t* d, bool q8, bool bwd, const Gat
 GatedArgs gated_args(const rnn_gated_dims_t* d, const GatedSizes& z, void* workspace) {
   GatedArgs a{};
   a.B = d->B; a.T = d->T; a.C = z.C; a.chunks = z.chunks;
-  a.tiles_c = z.tiles_c; a.span = z.span; a.solo = z.solo;
+  a.tiles_c = z.tiles_c; a.width = z.width; a.span = z.span; a.solo = z.solo;
   char* ws = (char*)workspace;
   a.status = (unsigned*)ws;
   a.ticket = (unsigned*)(ws + 256);

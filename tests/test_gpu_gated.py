@@ -73,7 +73,7 @@ def check(p, function, reset=None, lengths=None, checkpoint=None):
 # 64-channel tiles, a ragged one; enough chunks for the states to pass between
 # many blocks
 SHAPES = [(1, 1, 1, 1), (2, 16, 1, 32), (3, 5, 2, 17), (1, 127, 1, 9), (2, 128, 1, 64), (2, 129, 3, 22),
-          (1, 1000, 1, 130), (2, 515, 1, 200), (1, 5003, 1, 36)]
+          (1, 1000, 1, 130), (2, 515, 1, 200), (1, 5003, 1, 36), (2, 300, 1, 115), (1, 260, 1, 174)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
