@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(THREADS, 2)
           if (ch >= min(p.C, it.ct + p.width)) continue;
           const float* at = p.dbp + (size_t)g * p.C + ch;
           float s = 0.0f;
-#pragma unroll 16
+#pragma unroll 32
           for (int r = 0; r < rows; ++r) s += __ldcg(at + (size_t)r * G * p.C);
           ((T*)p.db)[(size_t)g * p.C + ch] = from_f<T>(s);
         }
@@ -1001,12 +1001,14 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   z.width = (z.C * z.esize) % 16 == 0 ? 32 * lane : 28 * lane;
   z.tiles_c = (z.C + z.width - 1) / z.width;
   const size_t tiles = (size_t)d->B * z.tiles_c;
-  // A hop of the chain takes about 1.2 us, in which the GPU moves some 100
-  // tiles: with fewer tiles than that (and a margin of two), a group of chunks
-  // shares a hop.
-  const size_t sms = device_sms(), ahead = sms + sms / 2;
+  // With fewer tiles than SMs, chunks of one tile wait on one another: the more
+  // of them run side by side, the more share a hop of the chain. Measured at
+  // 12 tiles (B=1 T=65537 C=768, forward): groups of 1, 2, 4, 8, 16, 32 chunks
+  // take 310, 167, 124, 119, 121, 126 us; at 128 tiles (B=8 T=4096 C=1024) 1
+  // takes 70 us, 2 to 8 74, 32 81.
+  const size_t sms = device_sms();
   z.span = 0;
-  while (z.span < MAX_SPAN && (tiles << z.span) < ahead) ++z.span;
+  while (z.span < MAX_SPAN && (tiles << (z.span + 1)) <= sms) ++z.span;
   // A short sequence is all latency: without TMA there is no wait that could
   // run out, and the clearing launch for the status word falls away.
   z.solo = z.chunks == 1 && tiles <= 2 * sms;
@@ -1021,9 +1023,10 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   z.maps = z.chunks > 1 && z.span > 0 ? up256(z.chunks * lanes * sizeof(ulonglong2)) : 0;
   // db: with few batch rows of one chunk, a CTA takes a channel tile's rows one
   // after the other; with few items, the last one adds the items' sums (16
-  // loads in flight, a round trip of a microsecond each); else a launch does.
+  // loads in flight, a round trip of a microsecond each); else a launch does
+  // (128 items: 24 us after the last one against 6 for the launch).
   const long long rows = (long long)d->B * z.chunks;
-  z.db_mode = z.solo && d->B <= 8 ? 3 : !z.solo && rows <= 128 ? 2 : 1;
+  z.db_mode = z.solo && d->B <= 8 ? 3 : !z.solo && rows <= 64 ? 2 : 1;
   z.sync = 512 + z.states + z.maps + up256(z.tiles_c * sizeof(unsigned));
   z.dbp = up256((size_t)d->B * z.chunks * z.G * z.C * sizeof(float));
   return z;
