@@ -180,6 +180,7 @@ def rnn_plan_describe(dims: Dims, for_backward: bool = False) -> tuple[int, str]
 
 def rnn_plan_set_limits(sms: int = 0, smem_per_cta: int = 227 * 1024, max_cluster: int = 16) -> int:
     """Plan for a stated device (sms > 0) or the current one (sms <= 0)."""
+    _gated_plans.clear()
     return _check(load().rnn_plan_set_limits(int(sms), int(smem_per_cta), int(max_cluster)),
                   "rnn_plan_set_limits")
 
@@ -293,6 +294,9 @@ def rnn_input_proj_bwd(BT: int, I: int, C: int, x, W, dWx, dx, dW, dbias, worksp
 
 
 # ---- gated linear scan ------------------------------------------------------------
+# These entry points are called once a layer and step, so the marshalling is
+# kept short: the interpreter lock is held (see _short), pointers are taken in
+# place, and what follows from the dims alone is worked out once (gated_plan).
 def _quick():
     if _short is None:
         load()
@@ -305,11 +309,31 @@ def _ws(workspace):
     return t.data_ptr() + at, t.numel() * t.element_size() - at
 
 
+def _raw_stream(t, stream):
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
+
+
 def make_gated_dims(B, T, N, D, function="linear", dtype=torch.bfloat16, checkpoint=None) -> GatedDims:
     fn = GATED_FUNCTIONS[function] if isinstance(function, str) else int(function)
     dt = DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
     ck = checkpoint if isinstance(checkpoint, int) else CHECKPOINTS[checkpoint]
     return GatedDims(int(B), int(T), int(N), int(D), fn, dt, ck)
+
+
+_gated_plans: dict = {}
+
+
+def gated_plan(B, T, N, D, function, dtype, checkpoint):
+    """(dims, tape bytes, forward and backward workspace bytes), kept per dims."""
+    key = (B, T, N, D, function, dtype, checkpoint)
+    plan = _gated_plans.get(key)
+    if plan is None:
+        dims = make_gated_dims(*key)
+        if len(_gated_plans) >= 4096:
+            _gated_plans.clear()
+        plan = _gated_plans[key] = (dims, rnn_gated_tape_size(dims), rnn_gated_workspace_size(dims, WS_FWD),
+                                    rnn_gated_workspace_size(dims, WS_BWD))
+    return plan
 
 
 def rnn_gated_num_gates(function) -> int:
@@ -325,23 +349,34 @@ def rnn_gated_workspace_size(dims: GatedDims, kind: int = WS_FWD) -> int:
 
 
 def rnn_gated_fwd(dims: GatedDims, Wx, b, state0, reset, lengths, h, last, tape, workspace, stream=None) -> int:
-    rc = _quick().rnn_gated_fwd(ctypes.byref(dims), _p(Wx), _p(b), _p(state0), _p(reset), _p(lengths), _p(h), _p(last),
-                              _p(tape), *_ws(workspace), _stream(stream))
-    return _check(rc, "rnn_gated_fwd")
+    ptr, size = _ws(workspace)
+    rc = _quick().rnn_gated_fwd(
+        ctypes.byref(dims), Wx.data_ptr(), None if b is None else b.data_ptr(),
+        None if state0 is None else state0.data_ptr(), None if reset is None else reset.data_ptr(),
+        None if lengths is None else lengths.data_ptr(), h.data_ptr(), None if last is None else last.data_ptr(),
+        None if tape is None else tape.data_ptr(), ptr, size, _raw_stream(h, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_gated_fwd")
 
 
 def rnn_gated_bwd(dims: GatedDims, Wx, b, reset, lengths, tape, dh, dlast, dWx, db, dstate0, workspace,
                   stream=None) -> int:
-    rc = _quick().rnn_gated_bwd(ctypes.byref(dims), _p(Wx), _p(b), _p(reset), _p(lengths), _p(tape), _p(dh), _p(dlast),
-                              _p(dWx), _p(db), _p(dstate0), *_ws(workspace), _stream(stream))
-    return _check(rc, "rnn_gated_bwd")
+    ptr, size = _ws(workspace)
+    rc = _quick().rnn_gated_bwd(
+        ctypes.byref(dims), None if Wx is None else Wx.data_ptr(), None if b is None else b.data_ptr(),
+        None if reset is None else reset.data_ptr(), None if lengths is None else lengths.data_ptr(), tape.data_ptr(),
+        None if dh is None else dh.data_ptr(), None if dlast is None else dlast.data_ptr(),
+        None if dWx is None else dWx.data_ptr(), None if db is None else db.data_ptr(),
+        None if dstate0 is None else dstate0.data_ptr(), ptr, size, _raw_stream(tape, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_gated_bwd")
 
 
 def rnn_gated_step(rows, slots, N, D, function, dtype, Wx, b, slot, pool, pool_out, h, status=None, stream=None) -> int:
-    fn = GATED_FUNCTIONS[function] if isinstance(function, str) else int(function)
-    rc = _quick().rnn_gated_step(int(rows), int(slots), int(N), int(D), fn, DTYPES[dtype], _p(Wx), _p(b), _p(slot),
-                               _p(pool), _p(pool_out), _p(h), _p(status), _stream(stream))
-    return _check(rc, "rnn_gated_step")
+    rc = _quick().rnn_gated_step(
+        rows, slots, N, D, GATED_FUNCTIONS[function] if isinstance(function, str) else function, DTYPES[dtype],
+        Wx.data_ptr(), None if b is None else b.data_ptr(), None if slot is None else slot.data_ptr(),
+        pool.data_ptr(), pool_out.data_ptr(), h.data_ptr(), None if status is None else status.data_ptr(),
+        _raw_stream(h, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_gated_step")
 
 
 # ---- 8-bit activation checkpoints ------------------------------------------------------
@@ -350,13 +385,15 @@ def rnn_act_scale_bytes(rows: int, cols: int) -> int:
 
 
 def rnn_act_pack(rows: int, cols: int, x, q, scales, stream=None) -> int:
-    return _check(_quick().rnn_act_pack(int(rows), int(cols), DTYPES[x.dtype], _p(x), _p(q), _p(scales),
-                                      _stream(stream)), "rnn_act_pack")
+    rc = _quick().rnn_act_pack(rows, cols, DTYPES[x.dtype], x.data_ptr(), q.data_ptr(), scales.data_ptr(),
+                               _raw_stream(x, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_act_pack")
 
 
 def rnn_act_unpack(rows: int, cols: int, q, scales, x, stream=None) -> int:
-    return _check(_quick().rnn_act_unpack(int(rows), int(cols), DTYPES[x.dtype], _p(q), _p(scales), _p(x),
-                                        _stream(stream)), "rnn_act_unpack")
+    rc = _quick().rnn_act_unpack(rows, cols, DTYPES[x.dtype], q.data_ptr(), scales.data_ptr(), x.data_ptr(),
+                                 _raw_stream(x, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_act_unpack")
 
 
 # ---- token embedding -----------------------------------------------------------------------
@@ -365,15 +402,15 @@ def rnn_embed_bwd_workspace_size(n: int, V: int, E: int) -> int:
 
 
 def rnn_embed_fwd(n: int, V: int, E: int, ids, W, scale: float, out, status=None, stream=None) -> int:
-    rc = _quick().rnn_embed_fwd(int(n), int(V), int(E), DTYPES[W.dtype], ids.element_size(), _p(ids), _p(W),
-                              float(scale), _p(out), _p(status), _stream(stream))
-    return _check(rc, "rnn_embed_fwd")
+    rc = _quick().rnn_embed_fwd(n, V, E, DTYPES[W.dtype], ids.element_size(), ids.data_ptr(), W.data_ptr(), scale,
+                                out.data_ptr(), None if status is None else status.data_ptr(), _raw_stream(W, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_embed_fwd")
 
 
 def rnn_embed_bwd(n: int, V: int, E: int, ids, padding_idx: int, dout, scale: float, dW, workspace,
                   stream=None) -> int:
     """dW [V][E] from dout [n][E] (see include/rnn.h); padding_idx -1 = none."""
-    rc = _quick().rnn_embed_bwd(int(n), int(V), int(E), DTYPES[dW.dtype], ids.element_size(), _p(ids), int(padding_idx),
-                              _p(dout), float(scale), _p(dW), _p(workspace),
-                              workspace.numel() * workspace.element_size(), _stream(stream))
-    return _check(rc, "rnn_embed_bwd")
+    ptr, size = _ws(workspace)
+    rc = _quick().rnn_embed_bwd(n, V, E, DTYPES[dW.dtype], ids.element_size(), ids.data_ptr(), padding_idx,
+                                dout.data_ptr(), scale, dW.data_ptr(), ptr, size, _raw_stream(dW, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_embed_bwd")

@@ -17,9 +17,10 @@ namespace {
 // maps, and the state that enters the chunk comes from the chunks before it:
 // chunks are grouped by `span`; the last chunk of a group publishes the state
 // after it, every other chunk its own map as soon as it has it, and a chunk
-// starts from the state before its group and folds the maps of the group's
-// chunks before it, in their order. The order of the sums is thus fixed, and
-// the chain through the chunks has one hop per group.
+// starts from the state before its group and applies the maps of the group's
+// chunks before it, in their order. The order of the sums is thus fixed, the
+// same for any grouping and any batch, and the chain through the chunks has
+// one hop per group.
 // Published values are 8-byte words (fp32, tag) that are written and read
 // whole, so a reader polls the value itself: no fence, and one round trip.
 // CTAs stay and take item after item from a counter, in chunk order and only
@@ -208,6 +209,7 @@ __device__ __forceinline__ Map then(const Map& a, const Map& b) { return {b.P * 
 template <int N, bool REVERSE> struct Chain {
   static constexpr int Q = THREADS / (32 * N), M = WARPS / Q;
   static constexpr int ROW = 32 * N + 2, EROW = 32 * N + 4;  // row lengths that spread the Q lanes over the banks
+  static constexpr int RUN = ((1 << MAX_SPAN) + Q - 1) / Q;   // chunks of a group to a lane, at most
   static constexpr unsigned ALL = 0xffffffffu;
   const GatedArgs& p;
   const Item& it;
@@ -291,32 +293,28 @@ template <int N, bool REVERSE> struct Chain {
   // Makes x the state that enters the chunk, publishes the one that leaves a
   // group, and hands every warp its own: enter [WARPS][EROW].
   __device__ __forceinline__ void pass(float* enter) {
-    Map g = {1.0f, 0.0f};  // the group's chunks before this one, a run of them a lane
+    // the group's chunks before this one, a run of them a lane
+    const int run = (o - first + Q - 1) / Q, from = first + q * run;
+    Map r[RUN];
     if (o > first) {
       if (group > 0 && !is_set(early, group)) early = ld_word(state(group));  // beside the maps' round trip
-      const int run = (o - first + Q - 1) / Q, from = first + q * run;
-      for (int i = 0; i < run; i += 2) {
-        ulonglong2 m[2];
-        wait([&]() {
-          bool all = true;
+      ulonglong2 m[RUN];
+      wait([&]() {
+        bool all = true;
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (i + j < run && from + i + j < o)
-              asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];"
-                           : "=l"(m[j].x), "=l"(m[j].y)
-                           : "l"(p.maps + at(from + i + j))
-                           : "memory");
+        for (int i = 0; i < RUN; ++i)
+          if (i < run && from + i < o)
+            asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];"
+                         : "=l"(m[i].x), "=l"(m[i].y)
+                         : "l"(p.maps + at(from + i))
+                         : "memory");
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (i + j < run && from + i + j < o)
-              all &= is_set(m[j].x, from + i + j + 1) && is_set(m[j].y, from + i + j + 1);
-          return all;
-        });
+        for (int i = 0; i < RUN; ++i)
+          if (i < run && from + i < o) all &= is_set(m[i].x, from + i + 1) && is_set(m[i].y, from + i + 1);
+        return all;
+      });
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (i + j < run && from + i + j < o) g = then(g, {value_of(m[j].x), value_of(m[j].y)});
-      }
-      g = last_of(scan(g, q));
+      for (int i = 0; i < RUN; ++i) r[i] = {value_of(m[i].x), value_of(m[i].y)};
     }
     if (group > 0) {
       wait([&]() {
@@ -325,7 +323,17 @@ template <int N, bool REVERSE> struct Chain {
       });
       x = value_of(early);
     }
-    x = affine(g.P, x, g.H);
+    if (o > first) {
+      // one chunk's map after the other, as if the state had come from the
+      // chunk before: the bits do not depend on the groups
+      for (int l = 0; l * run < o - first; ++l) {
+        float y = x;
+#pragma unroll
+        for (int i = 0; i < RUN; ++i)
+          if (i < run && from + i < o) y = affine(r[i].P, y, r[i].H);
+        x = __shfl_sync(ALL, y, l, Q);
+      }
+    }
     if (o + 1 == first + (1 << p.span) && o + 1 < p.chunks && q == 0)
       st_word(state(group + 1), word_of(affine(whole.P, x, whole.H), group + 1));
     float e = affine(before.P, x, before.H);
@@ -412,11 +420,20 @@ template <typename F> __device__ __forceinline__ void by_mask(const Item& it, F&
   else f(Flag<true>());
 }
 
-// Blocks per SM: the tile is 64 KB (linear) or 32 KB (coupled). Without the
-// 8-bit copy u waits in the tile's place of i and g (coupled: f and g), which
-// are not read again, so that f alone stays in registers.
+// CTAs an SM holds: what the tiles (64 KB linear, 32 KB coupled; the backward's
+// and the 8-bit copies' more) and the registers of f and u allow. Measured with
+// one more or less: coupled forward 146 us with 4, 163 with 3 (B=32 T=4096
+// C=1024 bf16); coupled backward bf16 311 with 2, 404 with 3 (spills), fp32 82
+// and 74 (B=16 T=2048 C=512); linear forward 247 with 3, 258 with 2.
+template <typename T, int FN, bool Q8> __host__ __device__ constexpr int ctas_per_sm(bool bwd) {
+  if (bwd) return FN == GATED_COUPLED && !Q8 && sizeof(T) == 4 ? 3 : 2;
+  return Q8 ? 2 : FN == GATED_COUPLED ? 4 : 3;
+}
+
+// Without the 8-bit copy u waits in the tile's place of i and g (coupled: f and
+// g), which are not read again, so that f alone stays in registers.
 template <typename T, int FN, bool Q8, bool TMA>
-__global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
+__global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(false)))
     gated_fwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap hmap,
                      const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap bmap, GatedArgs p) {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
@@ -617,7 +634,7 @@ __global__ void __launch_bounds__(THREADS, Q8 ? 2 : 3)
 }
 
 template <typename T, int FN, bool Q8, bool TMA>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(true)))
     gated_bwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap dmap,
                      const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap bmap, GatedArgs p) {
   constexpr int G = gated_gates(FN), N = Lane<T>::N;
@@ -1061,8 +1078,7 @@ template <typename T, int FN, bool Q8, bool TMA> cudaError_t gated_launch(bool b
   const void* k = bwd ? (const void*)gated_bwd_kernel<T, FN, Q8, TMA> : (const void*)gated_fwd_kernel<T, FN, Q8, TMA>;
   cudaError_t e = set_smem_attr(k, smem);
   if (e != cudaSuccess) return e;
-  // as many CTAs as the SMs hold (see the kernels' launch bounds)
-  const unsigned most = device_sms() * (bwd || Q8 ? 2 : 3);
+  const unsigned most = device_sms() * ctas_per_sm<T, FN, Q8>(bwd);
   const unsigned ctas = bwd && a.db_mode == 3 ? a.tiles_c : a.solo || items < most ? items : most;
   if (bwd) gated_bwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, d, out, bias, a);
   else gated_fwd_kernel<T, FN, Q8, TMA><<<ctas, THREADS, smem, st>>>(x, out, q, bias, a);

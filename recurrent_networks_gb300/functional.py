@@ -153,36 +153,38 @@ def flashrnn_stack(x, layers, function: str = "lstm", backend: str = "auto"):
 # ---- gated linear scan ------------------------------------------------------------
 def _dense(t):
     """t (or None) as the library takes it: contiguous and 16-byte aligned."""
-    if t is None:
-        return None
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _gated_run(Wx, b, state, function, reset, lengths, checkpoint, keep):
+    """(h, last, Wx and b as the library took them, plan, tape or None). The
+    tape's tensor holds, after it, the workspace of both directions (small
+    beside Wx): one allocation a pass."""
+    B, T, _, N, D = Wx.shape
+    plan = _lib.gated_plan(B, T, N, D, function, Wx.dtype, checkpoint)
+    Wx, b, state = _dense(Wx), _dense(b), _dense(state)
+    h = Wx.new_empty((B, T, N, D))
+    last = torch.empty((B, 1, N, D), dtype=torch.float32, device=h.device)
+    dims, size, fwd, bwd = plan
+    if keep:
+        tape = torch.empty(size + (fwd if fwd > bwd else bwd), dtype=torch.uint8, device=h.device)
+        _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, (tape, size))
+    else:
+        tape = None
+        ws = torch.empty(fwd, dtype=torch.uint8, device=h.device)
+        _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, None, ws)
+    return h, last, Wx, b, plan, tape
 
 
 class _GatedFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Wx, b, state, function, reset, lengths, checkpoint):
-        B, T, _, N, D = Wx.shape
-        dtype, dev = Wx.dtype, Wx.device
-        Wx, b, state = _dense(Wx), _dense(b), _dense(state)
-        dims = _lib.make_gated_dims(B, T, N, D, function, dtype, checkpoint)
-        h = torch.empty((B, T, N, D), dtype=dtype, device=dev)
-        last = torch.empty((B, 1, N, D), dtype=torch.float32, device=dev)
-        need = ctx.needs_input_grad
-        if need[0] or need[1] or need[2]:
-            # the tape, and after it the workspace of both directions (small
-            # beside Wx): one allocation a pass
-            size = _lib.rnn_gated_tape_size(dims)
-            tape = torch.empty(size + max(_lib.rnn_gated_workspace_size(dims, _lib.WS_FWD),
-                                          _lib.rnn_gated_workspace_size(dims, _lib.WS_BWD)),
-                               dtype=torch.uint8, device=dev)
-            _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, (tape, size))
-            ctx.dims, ctx.wx_shape, ctx.dtype, ctx.size = dims, Wx.shape, dtype, size
-            ctx.set_materialize_grads(False)
-            ctx.save_for_backward(Wx if checkpoint is None else None, b, reset, lengths, tape)
-        else:
-            ws = torch.empty(_lib.rnn_gated_workspace_size(dims, _lib.WS_FWD), dtype=torch.uint8, device=dev)
-            _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, None, ws)
+        h, last, Wx, b, ctx.plan, tape = _gated_run(Wx, b, state, function, reset, lengths, checkpoint, True)
+        ctx.shape = Wx.shape
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(Wx if checkpoint is None else None, b, reset, lengths, tape)
         return h, last
 
     @staticmethod
@@ -192,13 +194,14 @@ class _GatedFn(torch.autograd.Function):
 
 def _gated_bwd(ctx, dh, dlast):
     Wx, b, reset, lengths, tape = ctx.saved_tensors
-    dims, dev = ctx.dims, tape.device
-    B, _, G, N, D = ctx.wx_shape
+    dims, size = ctx.plan[:2]
+    B, _, G, N, D = ctx.shape
     need = ctx.needs_input_grad
-    dWx = torch.empty(ctx.wx_shape, dtype=ctx.dtype, device=dev) if need[0] else None
-    db = torch.empty((G, N, D), dtype=ctx.dtype, device=dev) if need[1] else None
-    ds = torch.empty((B, 1, N, D), dtype=torch.float32, device=dev) if need[2] else None
-    _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, (tape, ctx.size))
+    dtype = torch.bfloat16 if dims.dtype == _lib.DTYPES[torch.bfloat16] else torch.float32
+    dWx = torch.empty(ctx.shape, dtype=dtype, device=tape.device) if need[0] else None
+    db = torch.empty((G, N, D), dtype=dtype, device=tape.device) if need[1] else None
+    ds = torch.empty((B, 1, N, D), dtype=torch.float32, device=tape.device) if need[2] else None
+    _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, (tape, size))
     return dWx, db, ds, None, None, None, None
 
 
@@ -206,22 +209,23 @@ _gated_bwd_once = once_differentiable(_gated_bwd)
 
 
 def _gated_shapes(Wx, b, function, lead):
+    shape, dtype = Wx.shape, Wx.dtype
     if function not in _lib.GATED_FUNCTIONS:
         raise ValueError(f"function must be one of {list(_lib.GATED_FUNCTIONS)}, got {function!r}")
-    if Wx.dtype not in _lib.DTYPES:
-        raise TypeError(f"unsupported dtype {Wx.dtype}")
-    if Wx.dim() != lead + 3:
-        raise ValueError(f"Wx must have {lead + 3} dimensions, got shape {tuple(Wx.shape)}")
-    G, N, D = Wx.shape[lead:]
+    if dtype not in _lib.DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if len(shape) != lead + 3:
+        raise ValueError(f"Wx must have {lead + 3} dimensions, got shape {tuple(shape)}")
+    G, N, D = shape[lead:]
     want = 4 if function == "linear" else 2
     if G != want:
         raise ValueError(f"{function} needs G={want} gates, Wx has {G}")
     if b is not None:
         if b.shape != (G, N, D):
             raise ValueError(f"b must be [G,N,D]={(G, N, D)}, got {tuple(b.shape)}")
-        if b.dtype != Wx.dtype:
-            raise TypeError(f"b is {b.dtype}, Wx is {Wx.dtype}")
-        if b.device != Wx.device:
+        if b.dtype != dtype:
+            raise TypeError(f"b is {b.dtype}, Wx is {dtype}")
+        if b.get_device() != Wx.get_device():
             raise ValueError("b must be on Wx's device")
     return N, D
 
@@ -249,9 +253,10 @@ def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, len
     if state is not None:
         if state.shape != (B, 1, N, D):
             raise ValueError(f"state must be [B,1,N,D]={(B, 1, N, D)}, got {tuple(state.shape)}")
-        if state.device != Wx.device:
+        if state.get_device() != Wx.get_device():
             raise ValueError("state must be on Wx's device")
-        state = state.float()
+        if state.dtype != torch.float32:
+            state = state.float()
     if reset is not None:
         if reset.shape != (B, T):
             raise ValueError(f"reset must be [B,T]={(B, T)}, got {tuple(reset.shape)}")
@@ -270,9 +275,10 @@ def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, len
         if lengths.dtype == torch.int64:
             lengths = lengths.clamp(0, T).to(torch.int32)
         lengths = lengths.contiguous()
-    if not torch.is_grad_enabled():  # nothing is kept for a backward
-        Wx, b, state = (v if v is None else v.detach() for v in (Wx, b, state))
-    return _GatedFn.apply(Wx, b, state, function, reset, lengths, checkpoint)
+    if torch.is_grad_enabled() and (Wx.requires_grad or (b is not None and b.requires_grad) or
+                                    (state is not None and state.requires_grad)):
+        return _GatedFn.apply(Wx, b, state, function, reset, lengths, checkpoint)
+    return _gated_run(Wx, b, state, function, reset, lengths, checkpoint, False)[:2]
 
 
 def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=None, status=None):
@@ -288,22 +294,24 @@ def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=
         raise RuntimeError("gated_scan_step runs on CUDA tensors only (there is no CPU path)")
     N, D = _gated_shapes(Wx, b, function, 1)
     M = Wx.shape[0]
+    dev = Wx.get_device()
     for p in (pool,) if pool_out is None else (pool, pool_out):
         if p.dtype != torch.float32:
             raise TypeError(f"the pool must be float32, got {p.dtype}")
         if p.dim() != 3 or p.shape != (pool.shape[0], N, D):
             raise ValueError(f"the pool must be [P,N,D]=[P,{N},{D}], got {tuple(p.shape)}")
-        if not (p.is_contiguous() and p.data_ptr() % 16 == 0 and p.device == Wx.device):
+        if not p.is_contiguous() or p.data_ptr() % 16 or p.get_device() != dev:
             raise ValueError("the pool must be contiguous, 16-byte aligned and on Wx's device")
+    P = pool.shape[0]
     if slots is None:
-        if M > pool.shape[0]:
-            raise ValueError(f"{M} rows need as many slots, the pool has {pool.shape[0]}")
+        if M > P:
+            raise ValueError(f"{M} rows need as many slots, the pool has {P}")
     else:
-        if slots.shape != (M,) or slots.dtype != torch.int32 or slots.device != Wx.device:
+        if slots.shape != (M,) or slots.dtype != torch.int32 or slots.get_device() != dev:
             raise ValueError(f"slots must be [M]=[{M}] int32 on Wx's device")
         slots = slots.contiguous()
-    h = torch.empty((M, N, D), dtype=Wx.dtype, device=Wx.device)
-    _lib.rnn_gated_step(M, pool.shape[0], N, D, function, Wx.dtype, _dense(Wx), _dense(b), slots, pool,
+    h = Wx.new_empty((M, N, D))
+    _lib.rnn_gated_step(M, P, N, D, function, Wx.dtype, _dense(Wx), _dense(b), slots, pool,
                         pool if pool_out is None else pool_out, h, status)
     return h
 
@@ -352,15 +360,20 @@ def checkpoint_unpack(q, scales, dtype=torch.bfloat16):
 
 
 # ---- token embedding --------------------------------------------------------------------
+def _embed_run(ids, W, scale, status):
+    W = _dense(W)
+    V, E = W.shape
+    out = W.new_empty((*ids.shape, E))
+    _lib.rnn_embed_fwd(ids.numel(), V, E, ids, W, scale, out, status)
+    return out
+
+
 class _EmbedFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, W, scale, padding_idx, status):
-        W = _dense(W)
-        out = torch.empty((*ids.shape, W.shape[1]), dtype=W.dtype, device=W.device)
-        _lib.rnn_embed_fwd(ids.numel(), W.shape[0], W.shape[1], ids, W, scale, out, status)
         ctx.save_for_backward(ids)
         ctx.args = (W.shape, W.dtype, scale, padding_idx)
-        return out
+        return _embed_run(ids, W, scale, status)
 
     @staticmethod
     def backward(ctx, dout):
@@ -395,9 +408,12 @@ def embedding(ids, weight, scale: float = 1.0, padding_idx=None, status=None):
         raise TypeError(f"unsupported dtype {weight.dtype}")
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
-    if ids.device != weight.device:
+    if ids.get_device() != weight.get_device():
         raise ValueError("ids must be on weight's device")
     if not (padding_idx is None or 0 <= padding_idx < weight.shape[0]):
         raise ValueError(f"padding_idx must be None or in 0 .. {weight.shape[0] - 1}, got {padding_idx}")
     pad = -1 if padding_idx is None else int(padding_idx)
-    return _EmbedFn.apply(ids.contiguous(), weight, float(scale), pad, status)
+    ids = ids.contiguous()
+    if torch.is_grad_enabled() and weight.requires_grad:
+        return _EmbedFn.apply(ids, weight, float(scale), pad, status)
+    return _embed_run(ids, weight, float(scale), status)

@@ -194,11 +194,15 @@ def test_repeatable_and_independent_of_the_batch():
         p = make("linear", *shape, BF)
         a, b = run(p, "linear"), run(p, "linear")
         assert all(torch.equal(x, y) for x, y in zip(a, b))
-    p = make("linear", 6, 900, 1, 192, BF)
-    a = run(p, "linear", grads=False)
-    one = {k: v[2:3].contiguous() if k != "b" else v for k, v in p.items()}
-    h, last = run(one, "linear", grads=False)
-    assert torch.equal(h[0], a[0][2]) and torch.equal(last[0], a[1][2])
+    # 32 chunks of 128 steps, in groups that depend on the number of rows
+    for dtype, function in ((BF, "linear"), (F32, "linear_coupled")):
+        p = make(function, 40, 4000, 1, 192, dtype)
+        a = run(p, function)
+        for rows in (slice(2, 3), slice(1, 9)):
+            part = {k: v[rows].contiguous() if k != "b" else v for k, v in p.items()}
+            b = run(part, function)
+            for k in (0, 1, 2, 4):  # all but db, which sums over the rows
+                assert torch.equal(b[k], a[k][rows])
 
 
 def test_continues_from_its_last_state():
