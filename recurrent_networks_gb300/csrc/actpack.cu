@@ -91,19 +91,30 @@ __global__ void __launch_bounds__(256) act_pack_kernel(long long rows, int cols,
       }
     }
     if (on && part == 0) store_bytes<V>(scales + (size_t)k * cols + c, bytes);
+    huge = __any_sync(0xffffffffu, huge);
+    odd = __any_sync(0xffffffffu, odd);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       if (r >= n) break;
-      uint32_t b[2] = {0, 0};
+      FV<N> t[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        uint32_t w = quant(word_values<T>(v[r].w[i], (FV<N>*)nullptr), inv[i], huge);
+        t[i] = quant(word_values<T>(v[r].w[i], (FV<N>*)nullptr), inv[i], huge);
         if (odd) {
 #pragma unroll
           for (int j = 0; j < N; ++j)
-            if (inv[i].v[j] == 0.0f) w &= ~(255u << (8 * j));
+            if (inv[i].v[j] == 0.0f) t[i].v[j] = 0.0f;
         }
-        b[i * N / 4] |= w << (8 * (i * N % 4));
+      }
+      uint32_t b[2];
+      if constexpr (V == 1) {
+        b[0] = __float_as_uint(t[0].v[0]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+          auto value = [&](int k) { return t[(i * 4 + k) / N].v[(i * 4 + k) % N]; };
+          b[i] = __byte_perm(low_bytes(value(0), value(1)), low_bytes(value(2), value(3)), 0x5410);
+        }
       }
       store_bytes<V>(q + at + (size_t)r * cols, b);
     }

@@ -28,6 +28,40 @@ template <typename T, int VB> __device__ __forceinline__ void store_vec(T* p, co
   *(typename Raw<VB>::type*)p = *(const typename Raw<VB>::type*)&v;
 }
 
+// A vector's values in fp32, by the pair for bf16 (packed instructions), and back.
+template <typename T, int VB> struct Wide {
+  static constexpr int P = sizeof(T) == 2 && VB >= 4 ? 2 : 1, W = VB / (int)sizeof(T) / P;
+  FV<P> f[W];
+  __device__ __forceinline__ void set(const Vec<T, VB>& v) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if constexpr (P == 2) {
+        const uint32_t w = ((const uint32_t*)&v)[i];
+        f[i] = FV<P>{{__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}};
+      } else {
+        f[i].v[0] = to_f(v.v[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void scale(float s) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[i] = mul(f[i], splat<P>(s));
+  }
+  __device__ __forceinline__ Vec<T, VB> get() const {
+    Vec<T, VB> v;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if constexpr (P == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[i].v[0], f[i].v[P - 1]);
+        ((uint32_t*)&v)[i] = *(const uint32_t*)&h;
+      } else {
+        v.v[i] = from_f<T>(f[i].v[0]);
+      }
+    }
+    return v;
+  }
+};
+
 // ---- forward --------------------------------------------------------------------
 // `lanes` lanes (a power of two) to a token, 16-byte vectors where the rows
 // allow, ROWS tokens of a lane group in flight.
@@ -56,9 +90,10 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(long long n, int V, int 
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
         if (i0 + r >= n) break;
-#pragma unroll
-        for (int q = 0; q < X::N; ++q) x[r].v[q] = src[r] ? from_f<T>(to_f(x[r].v[q]) * scale) : from_f<T>(0.0f);
-        store_vec<T, VB>(out + (size_t)(i0 + r) * E + (size_t)e * X::N, x[r]);
+        Wide<T, VB> w = {};
+        if (src[r]) w.set(x[r]);
+        if (src[r]) w.scale(scale);
+        store_vec<T, VB>(out + (size_t)(i0 + r) * E + (size_t)e * X::N, w.get());
       }
     }
   }
@@ -291,28 +326,29 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_sum_k
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   for (int j = 0; j < RING - 1; ++j) ask(j, __shfl_sync(0xffffffffu, pos, j));
-  float acc[X::N];
-#pragma unroll
-  for (int q = 0; q < X::N; ++q) acc[q] = 0.0f;
+  Wide<T, VB> acc = {};
   unsigned cur = none;
   for (int j = 0; j < sums; ++j) {
     ask(j + RING - 1, __shfl_sync(0xffffffffu, pos, (j + RING - 1) & 31));
     const unsigned k = __shfl_sync(0xffffffffu, key, j), after = j + 1 < count ? __shfl_sync(0xffffffffu, key, j + 1) : next;
     asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
     const X x = *(const X*)&ring[warp][j % RING][lane * VB];
-    const bool begin = k != cur;
-    cur = k;
+    Wide<T, VB> w;
+    w.set(x);
+    if (k != cur) {
+      acc = w;
+    } else {
 #pragma unroll
-    for (int q = 0; q < X::N; ++q) acc[q] = (begin ? 0.0f : acc[q]) + to_f(x.v[q]);
+      for (int i = 0; i < acc.W; ++i) acc.f[i] = add(acc.f[i], w.f[i]);
+    }
+    cur = k;
     if (!on || (after == k && j + 1 < count)) continue;
     const bool head = k == prev, tail = after == k;
     if (!head && !tail) {
-      X y;
-#pragma unroll
-      for (int q = 0; q < X::N; ++q) y.v[q] = from_f<T>(acc[q] * p.scale);
-      store_vec<T, VB>((T*)p.dW + (size_t)k * p.E + col, y);
+      acc.scale(p.scale);
+      store_vec<T, VB>((T*)p.dW + (size_t)k * p.E + col, acc.get());
     } else {
-      store_part<X::N>(p.part + ((size_t)piece * 2 + (head ? 0 : 1)) * p.E + col, acc);
+      store_part<X::N>(p.part + ((size_t)piece * 2 + (head ? 0 : 1)) * p.E + col, (const float*)acc.f);
     }
   }
 }

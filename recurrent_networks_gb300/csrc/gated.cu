@@ -27,7 +27,7 @@ namespace {
 // when the last one is through its wait, so whatever an item waits for is
 // being worked on, however few of the CTAs are running.
 constexpr int WARPS = 8, STEPS = GATED_CHUNK / WARPS, THREADS = WARPS * 32;
-constexpr int MAX_SPAN = 4;  // log2
+constexpr int MAX_SPAN = 3;  // log2
 
 struct GatedArgs {
   int B, T, C, chunks;  // C = N D channels
@@ -556,20 +556,24 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(false)))
     huge = __any_sync(0xffffffffu, huge);
     odd = __any_sync(0xffffffffu, odd);
     unsigned char* qmine = qtile + warp * STEPS * G * 32 * N;
+    auto pack = [&](auto mask) {  // MASK: steps that do not exist, saturated or non-finite blocks
+      constexpr bool MASK = decltype(mask)::value;
 #pragma unroll 4
-    for (int j = 0; j < STEPS; ++j)
+      for (int j = 0; j < STEPS; ++j)
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        uint32_t w = quant(Lane<T>::unpack(raws(j * G + g)), inv[g], huge);
-        if (j >= it.live) w = 0;
-        if (odd) {
+        for (int g = 0; g < G; ++g) {
+          FV<N> t = quant(Lane<T>::unpack(raws(j * G + g)), inv[g], MASK && huge);
+          if (MASK) {
 #pragma unroll
-          for (int v = 0; v < N; ++v)
-            if (inv[g].v[v] == 0.0f) w &= ~(255u << (8 * v));
+            for (int v = 0; v < N; ++v)
+              if (j >= it.live || inv[g].v[v] == 0.0f) t.v[v] = 0.0f;
+          }
+          if (N == 2) *(unsigned short*)(qmine + (j * G + g) * 64 + lane * 2) = (unsigned short)low_bytes(t.v[0], t.v[N - 1]);
+          else qmine[(j * G + g) * 32 + lane] = (unsigned char)__float_as_uint(t.v[0]);
         }
-        if (N == 2) *(unsigned short*)(qmine + (j * G + g) * 64 + lane * 2) = (unsigned short)w;
-        else qmine[(j * G + g) * 32 + lane] = (unsigned char)w;
-      }
+    };
+    if (it.live == STEPS && !huge && !odd) pack(Flag<false>());
+    else pack(Flag<true>());
     if (TMAQ) {
       fence_proxy_async_smem();
       __syncwarp();

@@ -206,16 +206,21 @@ template <> __device__ __forceinline__ uint32_t mag_max<__nv_bfloat16>(uint32_t 
 template <typename T> __device__ __forceinline__ uint32_t mag_bits(uint32_t top, int v) {
   return sizeof(T) == 4 ? top : v ? top & 0xffff0000u : top << 16;
 }
-// q of a lane's channels as bytes: a / 2^e + 1.5 2^23 rounds to nearest even
-// and leaves q in the low byte. `huge`: some block may saturate (act_scale_byte).
-template <int N> __device__ __forceinline__ uint32_t quant(const FV<N>& a, const FV<N>& inv, bool huge) {
-  FV<N> t = mul(a, inv);
+// q of N channels, each in the low byte of its word: a / 2^e + 1.5 2^23 rounds to
+// nearest even (the product is exact, so one fused instruction) and leaves q
+// there. `huge`: some block may saturate (act_scale_byte).
+template <int N> __device__ __forceinline__ FV<N> quant(const FV<N>& a, const FV<N>& inv, bool huge) {
   if (huge) {
+    FV<N> t = mul(a, inv);
 #pragma unroll
     for (int v = 0; v < N; ++v) t.v[v] = fminf(fmaxf(t.v[v], -127.0f), 127.0f);
+    return add(t, splat<N>(12582912.0f));
   }
-  t = add(t, splat<N>(12582912.0f));
-  return N == 1 ? __float_as_uint(t.v[0]) & 255u : __byte_perm(__float_as_uint(t.v[0]), __float_as_uint(t.v[N - 1]), 0x0040) & 0xffffu;
+  return fma(a, inv, splat<N>(12582912.0f));
+}
+// the low bytes of two words, in the low half
+__device__ __forceinline__ uint32_t low_bytes(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
 }
 
 }  // namespace rnn
