@@ -64,7 +64,10 @@ template <typename T, int VB> struct Wide {
 
 // ---- forward --------------------------------------------------------------------
 // `lanes` lanes (a power of two) to a token, 16-byte vectors where the rows
-// allow, ROWS tokens of a lane group in flight.
+// allow, ROWS tokens of a lane group in flight. Bound by out's bytes (the rows of
+// frequent tokens come from L2): n=131072 E=1024 bf16 60 us, 5.5 TB/s of the 338
+// MB that have to move. Scaling pair by pair in fp32; element by element the
+// conversions alone kept 74 % of the issue slots busy.
 template <typename T, typename I, int VB>
 __global__ void __launch_bounds__(256) embed_fwd_kernel(long long n, int V, int E, int lanes, const I* ids, const T* W,
                                                         float scale, T* out, unsigned* status) {
@@ -286,8 +289,8 @@ template <int N> __device__ __forceinline__ void load_part(const float* p, float
 // to an id that crosses the piece's ends goes to part. Bound by the gather of
 // dout's rows: every lane copies its vector of the next RING rows into its own
 // place of a ring in shared memory, so that up to 15 rows a warp are on their
-// way while one is added (two register batches of 4 rows spilled and reached
-// 2.1 TB/s).
+// way while one is added: 56 us for n=131072 E=1024 bf16, 5.6 TB/s (two register
+// batches of 4 rows spilled and reached 2.1 TB/s).
 constexpr int PIECE_MAX = 32, RING = 16;
 template <int VB> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   static_assert(VB == 16 || VB == 8 || VB == 4, "cp.async sizes");
@@ -353,7 +356,8 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_sum_k
   }
 }
 
-// The ids that cross pieces: a warp per piece in which such an id begins, over
+// The ids that cross pieces (20 us of the 127 us backward at n=131072 V=50000
+// E=1024: the latency of the most frequent id's sums): a warp per piece in which such an id begins, over
 // 32 vectors of columns, adds the pieces' sums in order. An id over more than
 // LONG pieces is shared by the block's 8 warps, their sums added in order.
 template <typename T, int VB> __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs p) {
