@@ -181,6 +181,7 @@ def rnn_plan_describe(dims: Dims, for_backward: bool = False) -> tuple[int, str]
 def rnn_plan_set_limits(sms: int = 0, smem_per_cta: int = 227 * 1024, max_cluster: int = 16) -> int:
     """Plan for a stated device (sms > 0) or the current one (sms <= 0)."""
     _gated_plans.clear()
+    _embed_sizes.clear()
     return _check(load().rnn_plan_set_limits(int(sms), int(smem_per_cta), int(max_cluster)),
                   "rnn_plan_set_limits")
 
@@ -397,8 +398,28 @@ def rnn_act_unpack(rows: int, cols: int, q, scales, x, stream=None) -> int:
 
 
 # ---- token embedding -----------------------------------------------------------------------
+_embed_sizes: dict = {}
+
+
 def rnn_embed_bwd_workspace_size(n: int, V: int, E: int) -> int:
-    return int(_quick().rnn_embed_bwd_workspace_size(int(n), int(V), int(E)))
+    size = _embed_sizes.get((n, V, E))
+    if size is None:
+        if len(_embed_sizes) >= 4096:
+            _embed_sizes.clear()
+        size = _embed_sizes[n, V, E] = int(_quick().rnn_embed_bwd_workspace_size(int(n), int(V), int(E)))
+    return size
+
+
+_status_words: dict = {}
+
+
+def status_word(t):
+    """256 bytes on t's device, kept: the workspace of calls that need no more
+    than a status word, when nobody asks for the status."""
+    word = _status_words.get(t.get_device())
+    if word is None:
+        word = _status_words[t.get_device()] = torch.zeros(256, dtype=torch.uint8, device=t.device)
+    return word
 
 
 def rnn_embed_fwd(n: int, V: int, E: int, ids, W, scale: float, out, status=None, stream=None) -> int:

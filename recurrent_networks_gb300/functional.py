@@ -385,7 +385,8 @@ def _embed_bwd(ctx, dout):
     (V, E), dtype, scale, pad = ctx.args
     n = ids.numel()
     dW = torch.empty((V, E), dtype=dtype, device=ids.device)
-    ws = torch.empty(_lib.rnn_embed_bwd_workspace_size(n, V, E), dtype=torch.uint8, device=ids.device)
+    size = _lib.rnn_embed_bwd_workspace_size(n, V, E)
+    ws = _lib.status_word(ids) if size <= 256 else torch.empty(size, dtype=torch.uint8, device=ids.device)
     _lib.rnn_embed_bwd(n, V, E, ids, pad, _dense(dout), scale, dW, ws)
     return None, dW, None, None, None
 
