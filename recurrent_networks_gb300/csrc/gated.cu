@@ -67,8 +67,16 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
-// f x + u, with x dropped where f is 0 (a reset): 0 times an infinite x is not NaN.
-__device__ __forceinline__ float affine(float f, float x, float u) { return f == 0.0f ? u : fmaf(f, x, u); }
+// Factors of maps are products of sigmoids, so not negative; -0 marks a reset
+// among their steps. A reset drops what came before even where that is an
+// infinity or NaN; a factor that merely underflowed to 0 leaves it non-finite.
+constexpr unsigned RESET = 0x80000000u;
+__device__ __forceinline__ float affine(float f, float x, float u) {
+  return __float_as_uint(f) == RESET ? u : fmaf(f, x, u);
+}
+__device__ __forceinline__ float factor(float a, float b) {
+  return __uint_as_float(__float_as_uint(a * b) | ((__float_as_uint(a) | __float_as_uint(b)) & RESET));
+}
 template <int N> __device__ __forceinline__ FV<N> affine(const FV<N>& f, const FV<N>& x, const FV<N>& u) {
   FV<N> r;
 #pragma unroll
@@ -198,7 +206,7 @@ __device__ __forceinline__ void st_word(unsigned long long* p, unsigned long lon
 struct Map {
   float P, H;
 };
-__device__ __forceinline__ Map then(const Map& a, const Map& b) { return {b.P * a.P, affine(b.P, a.H, b.H)}; }
+__device__ __forceinline__ Map then(const Map& a, const Map& b) { return {factor(a.P, b.P), affine(b.P, a.H, b.H)}; }
 
 // How a CTA passes the state through the chunks of a tile; REVERSE: the
 // processing order descends. All threads take part, Q neighbouring lanes to a
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(false)))
         f[j] = select(on, rst ? splat<N>(0.0f) : f[j], splat<N>(1.0f));
         w = select(on, w, splat<N>(0.0f));
       }
-      P = mul(P, f[j]);
+      P = MASK && rst ? splat<N>(-0.0f) : mul(P, f[j]);
       H = MASK && rst ? w : fma(f[j], H, w);
       if (Q8) {
         u[j] = w;
@@ -792,7 +800,7 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(true)))
         u[j] = select(on, u[j], splat<N>(0.0f));
       }
       // what step j's delta sends out of the warp's first step: f_0 .. f_j times it
-      P = mul(P, f[j]);
+      P = MASK && rst ? splat<N>(-0.0f) : mul(P, f[j]);
       H = MASK && rst ? u[j] : fma(f[j], H, u[j]);
       E = MASK ? affine(P, e, E) : fma(P, e, E);
     }

@@ -83,6 +83,17 @@ template <int FN> __host__ __device__ constexpr bool gate_is_linear(int g) { ret
 template <int FN, int N> __device__ __forceinline__ constexpr float mul_of(int g) {
   return N == 1 || gate_is_linear<FN>(g) ? 1.0f : -1.4426950408889634f;
 }
+// the smaller one; a NaN stays one (fminf would hide it)
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // e = exp(-z). For fp32 z log2 e in two parts, the product and what its
 // rounding and the constant's left out, so that e keeps the exponential's own
 // 2^-22; z held to -88 .. 88 (e finite, NaN stays), where the sigmoid has
@@ -90,9 +101,7 @@ template <int FN, int N> __device__ __forceinline__ constexpr float mul_of(int g
 // about twice that.
 __device__ __forceinline__ FV<2> exp_neg(const FV<2>& t) { return {{exp2_fast(t.v[0]), exp2_fast(t.v[1])}}; }
 __device__ __forceinline__ FV<1> exp_neg(const FV<1>& z) {
-  float x;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(-z.v[0]), "f"(-88.0f));
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(88.0f));
+  const float x = min_nan(max_nan(-z.v[0], -88.0f), 88.0f);
   const float t = x * 1.44269502f, l = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -t));  // log2 e = 1.44269502 + 1.926e-8
   const float e = exp2_fast(t);
   return {{fmaf(e, l * 0.693147181f, e)}};
@@ -117,8 +126,8 @@ template <int N> __device__ __forceinline__ FV<N> sigmoid(const FV<N>& z) { retu
 // the reciprocal is 0 already.
 __device__ __forceinline__ FV<2> sigmoid_full(const FV<2>& z) {
   FV<2> d = add(exp_neg(z), splat<2>(1.0f));
-  d.v[0] = fminf(d.v[0], 1.7e38f);
-  d.v[1] = fminf(d.v[1], 1.7e38f);
+  d.v[0] = min_nan(d.v[0], 1.7e38f);
+  d.v[1] = min_nan(d.v[1], 1.7e38f);
   return rcp_full(d);
 }
 __device__ __forceinline__ FV<1> sigmoid_full(const FV<1>& z) { return sigmoid(z); }
@@ -126,14 +135,12 @@ __device__ __forceinline__ FV<1> sigmoid_full(const FV<1>& z) { return sigmoid(z
 // cell uses n itself as the input gate): n = exp(-z) f, with exp(-z) bounded
 // by 2^125 so that f stays a normal number and n becomes 1.
 __device__ __forceinline__ void sigmoid_both(const FV<2>& t, FV<2>& f, FV<2>& n) {
-  const FV<2> e = exp_neg(FV<2>{{fminf(t.v[0], 125.0f), fminf(t.v[1], 125.0f)}});
+  const FV<2> e = exp_neg(FV<2>{{min_nan(t.v[0], 125.0f), min_nan(t.v[1], 125.0f)}});
   f = rcp_full(add(e, splat<2>(1.0f)));
   n = mul(e, f);
 }
 __device__ __forceinline__ void sigmoid_both(const FV<1>& z, FV<1>& f, FV<1>& n) {
-  float x;  // exp(-z) bounded as above
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(z.v[0]), "f"(-86.0f));
-  const FV<1> e = exp_neg(FV<1>{{x}});
+  const FV<1> e = exp_neg(FV<1>{{max_nan(z.v[0], -86.0f)}});  // exp(-z) bounded as above
   f = rcp(add(e, splat<1>(1.0f)));
   n = mul(e, f);
 }

@@ -126,6 +126,29 @@ def test_reset_drops_an_infinite_state():
     assert torch.isfinite(h).all() and torch.isfinite(last).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("function", ["linear", "linear_coupled"])
+def test_nan_stays_until_a_reset(function, dtype):
+    """A NaN in a gate that is looked at reaches every later step of its channel
+    (also through factors that underflow) and no other channel, up to a reset;
+    backward it reaches the earlier steps of its document alone."""
+    p = make(function, 1, 400, 1, 70, dtype)
+    f = 1 if function == "linear" else 0
+    p["Wx"][0, :, f] = -12  # f = 6e-6: a few steps' product underflows
+    p["Wx"][0, 150, f, 0, 33] = float("nan")
+    reset = torch.zeros(1, 400, dtype=torch.bool, device="cuda")
+    reset[0, [100, 300]] = True
+    h, last, dWx, _, ds = run(p, function, reset=reset)
+    bad = torch.isnan(h[0, :, 0])
+    want = torch.zeros_like(bad)
+    want[150:300, 33] = True
+    assert torch.equal(bad, want)
+    assert torch.isfinite(last).all() and torch.isfinite(ds).all()
+    bad = torch.isnan(dWx[0, :, :, 0]).any(1)
+    assert not bad[:100].any() and not bad[300:].any()
+    assert bad[100:300, 33].all() and bad.sum() == 200
+
+
 def test_saturated_gates():
     """Logits of +-inf and of the types' lowest value: gates exactly 0 or 1."""
     for dtype in (F32, BF):
