@@ -356,11 +356,12 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_sum_k
   }
 }
 
-// The ids that cross pieces (20 us of the 127 us backward at n=131072 V=50000
-// E=1024: the latency of the most frequent id's sums): a warp per piece in which such an id begins, over
+// The ids that cross pieces (16 us of the 122 us backward at n=131072 V=50000
+// E=1024, latency: few registers keep four blocks an SM, 21 us with two): a warp
+// per piece in which such an id begins, over
 // 32 vectors of columns, adds the pieces' sums in order. An id over more than
 // LONG pieces is shared by the block's 8 warps, their sums added in order.
-template <typename T, int VB> __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs p) {
+template <typename T, int VB> __global__ void __launch_bounds__(256, 4) embed_join_kernel(SumArgs p) {
   using X = Vec<T, VB>;
   constexpr int LONG = 12, N = X::N;
   __shared__ long long long_item[8];
@@ -368,13 +369,13 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_join_
   __shared__ float sums[8][32 * N];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto sum = [&](long long from, long long to, int col, float* acc) {  // the first-id sums of pieces from .. to-1
-    for (long long r = from; r < to; r += 8) {
-      float v[8][N];
+    for (long long r = from; r < to; r += 4) {
+      float v[4][N];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < 4; ++k)
         if (r + k < to) load_part<N>(p.part + (size_t)(r + k) * 2 * p.E + col, v[k]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < 4; ++k)
         if (r + k < to) {
 #pragma unroll
           for (int q = 0; q < N; ++q) acc[q] += v[k][q];
@@ -394,9 +395,9 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_join_
   if (lane == 0) long_item[warp] = -1;
   if (piece + 1 < p.pieces) {
     const long long i1 = (piece + 1) * p.piece;  // the next piece's first token
-    const unsigned id = __ldg(p.key + i1 - 1);
-    const bool begins = piece == 0 || __ldg(p.key + piece * p.piece - 1) != id;
-    if (id < (unsigned)p.V && begins && __ldg(p.key + i1) == id) {
+    const unsigned id = __ldg(p.key + i1 - 1), next = __ldg(p.key + i1);
+    const unsigned prev = piece > 0 ? __ldg(p.key + piece * p.piece - 1) : 0xffffffffu;
+    if (id < (unsigned)p.V && prev != id && next == id) {
       long long end = piece + 2;  // the id's last piece + 1
       for (bool more = true; more; end += 32) {
         const long long r = end + lane;
