@@ -358,9 +358,9 @@ template <typename T, int VB> __global__ void __launch_bounds__(256) embed_sum_k
 
 // The ids that cross pieces (16 us of the 122 us backward at n=131072 V=50000
 // E=1024, latency: few registers keep four blocks an SM, 21 us with two): a warp
-// per piece in which such an id begins, over
-// 32 vectors of columns, adds the pieces' sums in order. An id over more than
-// LONG pieces is shared by the block's 8 warps, their sums added in order.
+// per piece in which such an id begins, over 32 vectors of columns, adds the
+// pieces' sums in order. An id over more than LONG pieces is shared by the
+// block's 8 warps, their sums added in order.
 template <typename T, int VB> __global__ void __launch_bounds__(256, 4) embed_join_kernel(SumArgs p) {
   using X = Vec<T, VB>;
   constexpr int LONG = 12, N = X::N;
