@@ -70,12 +70,18 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T) {
 // Factors of maps are products of sigmoids, so not negative; -0 marks a reset
 // among their steps. A reset drops what came before even where that is an
 // infinity or NaN; a factor that merely underflowed to 0 leaves it non-finite.
+// The mark stays whatever else is in the product, a NaN too.
 constexpr unsigned RESET = 0x80000000u;
-__device__ __forceinline__ float affine(float f, float x, float u) {
-  return __float_as_uint(f) == RESET ? u : fmaf(f, x, u);
-}
+__device__ __forceinline__ bool is_reset(float f) { return __float_as_uint(f) == RESET; }
+__device__ __forceinline__ float affine(float f, float x, float u) { return is_reset(f) ? u : fmaf(f, x, u); }
 __device__ __forceinline__ float factor(float a, float b) {
-  return __uint_as_float(__float_as_uint(a * b) | ((__float_as_uint(a) | __float_as_uint(b)) & RESET));
+  return is_reset(a) || is_reset(b) ? __uint_as_float(RESET) : a * b;
+}
+template <int N> __device__ __forceinline__ FV<N> factor(const FV<N>& a, const FV<N>& b) {
+  FV<N> r;
+#pragma unroll
+  for (int v = 0; v < N; ++v) r.v[v] = factor(a.v[v], b.v[v]);
+  return r;
 }
 template <int N> __device__ __forceinline__ FV<N> affine(const FV<N>& f, const FV<N>& x, const FV<N>& u) {
   FV<N> r;
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(false)))
         f[j] = select(on, rst ? splat<N>(0.0f) : f[j], splat<N>(1.0f));
         w = select(on, w, splat<N>(0.0f));
       }
-      P = MASK && rst ? splat<N>(-0.0f) : mul(P, f[j]);
+      P = MASK ? factor(P, rst ? splat<N>(-0.0f) : f[j]) : mul(P, f[j]);
       H = MASK && rst ? w : fma(f[j], H, w);
       if (Q8) {
         u[j] = w;
@@ -800,7 +806,7 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(true)))
         u[j] = select(on, u[j], splat<N>(0.0f));
       }
       // what step j's delta sends out of the warp's first step: f_0 .. f_j times it
-      P = MASK && rst ? splat<N>(-0.0f) : mul(P, f[j]);
+      P = MASK ? factor(P, rst ? splat<N>(-0.0f) : f[j]) : mul(P, f[j]);
       H = MASK && rst ? u[j] : fma(f[j], H, u[j]);
       E = MASK ? affine(P, e, E) : fma(P, e, E);
     }

@@ -149,6 +149,41 @@ def test_nan_stays_until_a_reset(function, dtype):
     assert bad[100:300, 33].all() and bad.sum() == 200
 
 
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("function", ["linear", "linear_coupled"])
+@pytest.mark.parametrize("T,nan,resets", [
+    (400, 150, [200]), (400, 200, [150]),  # one chunk of 128 steps, different warps of 16
+    (400, 148, [155]), (400, 155, [148]),  # one warp
+    (400, 10, [60, 300]), (400, 390, [395]), (100, 20, [60]), (100, 60, [20]), (100, 18, [25]), (100, 25, [18])])
+def test_nan_keeps_to_its_document(T, nan, resets, function, dtype):
+    """As above with the NaN and a reset in the same chunk, in both orders: what
+    is NaN is the NaN's channel from its step to the end of its document, and the
+    gradients of that document's steps of the channel."""
+    g = torch.Generator().manual_seed(T + nan)
+    G, C, ch = 4 if function == "linear" else 2, 70, 33
+    Wx = torch.randn(2, T, G, 1, C, generator=g)
+    Wx[1, nan, G // 2 - 1, 0, ch] = float("nan")  # the forget gate
+    leaves = [Wx.to(dtype).cuda(), torch.randn(G, 1, C, generator=g).to(dtype).cuda(),
+              torch.randn(2, 1, 1, C, generator=g).cuda()]
+    leaves = [x.requires_grad_(True) for x in leaves]
+    reset = torch.zeros(2, T, dtype=torch.bool)
+    reset[1, resets] = True
+    h, last = rn.gated_scan(*leaves, function=function, reset=reset.cuda())
+    dWx, _, ds = torch.autograd.grad((h, last), leaves, (torch.ones_like(h), torch.ones_like(last)))
+    begin, end = max([0] + [r for r in resets if r <= nan]), min([T] + [r for r in resets if r > nan])
+
+    def only(steps, on=True):
+        want = torch.zeros(2, *steps, C, dtype=torch.bool)
+        want[1, ..., ch] = on
+        return want
+
+    t = torch.arange(T)
+    assert torch.equal(torch.isnan(h[:, :, 0]).cpu(), only((T,), (t >= nan) & (t < end)))
+    assert torch.equal(torch.isnan(last[:, 0, 0]).cpu(), only((), end == T))
+    assert torch.equal(torch.isnan(dWx[:, :, :, 0]).any(2).cpu(), only((T,), (t >= begin) & (t < end)))
+    assert torch.equal(torch.isnan(ds[:, 0, 0]).cpu(), only((), begin == 0))
+
+
 def test_saturated_gates():
     """Logits of +-inf and of the types' lowest value: gates exactly 0 or 1."""
     for dtype in (F32, BF):
