@@ -67,15 +67,17 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
-// Factors of maps are products of sigmoids, so not negative; -0 marks a reset
-// among their steps. A reset drops what came before even where that is an
-// infinity or NaN; a factor that merely underflowed to 0 leaves it non-finite.
-// The mark stays whatever else is in the product, a NaN too.
+// Factors of maps are products of sigmoids, so not negative, and a NaN that a
+// product or a sum gives is 0x7fffffff: the sign bit is free to mark a reset
+// among their steps (-0, or with a NaN among them 0xffffffff). A reset drops what
+// came before even where that is an infinity or NaN; a factor that merely
+// underflowed to 0 leaves it non-finite.
 constexpr unsigned RESET = 0x80000000u;
-__device__ __forceinline__ bool is_reset(float f) { return __float_as_uint(f) == RESET; }
-__device__ __forceinline__ float affine(float f, float x, float u) { return is_reset(f) ? u : fmaf(f, x, u); }
+__device__ __forceinline__ float affine(float f, float x, float u) {
+  return (int)__float_as_uint(f) < 0 ? u : fmaf(f, x, u);
+}
 __device__ __forceinline__ float factor(float a, float b) {
-  return is_reset(a) || is_reset(b) ? __uint_as_float(RESET) : a * b;
+  return __uint_as_float(__float_as_uint(a * b) | ((__float_as_uint(a) | __float_as_uint(b)) & RESET));
 }
 template <int N> __device__ __forceinline__ FV<N> factor(const FV<N>& a, const FV<N>& b) {
   FV<N> r;

@@ -162,7 +162,7 @@ def test_nan_keeps_to_its_document(T, nan, resets, function, dtype):
     g = torch.Generator().manual_seed(T + nan)
     G, C, ch = 4 if function == "linear" else 2, 70, 33
     Wx = torch.randn(2, T, G, 1, C, generator=g)
-    Wx[1, nan, G // 2 - 1, 0, ch] = float("nan")  # the forget gate
+    Wx[1, nan, G // 2 - 1, 0, ch] = torch.tensor(float("nan")).copysign(torch.tensor(0.5 - nan % 2))  # the forget gate
     leaves = [Wx.to(dtype).cuda(), torch.randn(G, 1, C, generator=g).to(dtype).cuda(),
               torch.randn(2, 1, 1, C, generator=g).cuda()]
     leaves = [x.requires_grad_(True) for x in leaves]
