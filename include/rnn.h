@@ -281,7 +281,9 @@ int rnn_trace(void *buf, int t0, int steps);
  * most limit_ns (1 ns .. 10 s). The wait runs out, the kernel records the
  * time-out in the workspace status word and carries on; the step exchange
  * itself is untouched, so results stay correct and rnn_check_status reports
- * RNN_ETIMEOUT. step < 0 switches injection off. Process-global; returns
+ * RNN_ETIMEOUT. The gated scan, forward and backward, does the same in the
+ * first tile of channels at its chunk number `step` (in processing order) where
+ * the sequence has more than one chunk. step < 0 switches injection off. Process-global; returns
  * RNN_OK or RNN_EINVAL. */
 int rnn_debug_inject_wait(int step, unsigned long long limit_ns);
 

@@ -359,9 +359,13 @@ unsigned long long wait_limit_ns() { return g_wait_limit_ns; }
 // Phase trace of the persistent kernels (rnn_trace).
 static unsigned long long* g_trace_buf = nullptr;
 static int g_trace_t0 = 0, g_trace_steps = 0;
-// Fault injection of the forward persistent kernels (rnn_debug_inject_wait).
+// Fault injection of the forward persistent kernels and the gated scan (rnn_debug_inject_wait).
 static int g_inject_step = -1;
 static unsigned long long g_inject_limit_ns = 0;
+void inject_wait(int* step, unsigned long long* limit_ns) {
+  *step = g_inject_step;
+  *limit_ns = g_inject_limit_ns;
+}
 
 static void with_trace(FusedArgs* f) {
   f->trace = g_trace_buf;

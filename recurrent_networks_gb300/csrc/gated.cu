@@ -61,6 +61,10 @@ struct GatedArgs {
   unsigned* status;
   unsigned* ticket;
   unsigned long long wait_limit_ns;
+  // fault injection (rnn_debug_inject_wait): at this chunk (in processing order)
+  // of the first tile a wait for a word that nothing writes; -1: off
+  int inject_chunk;
+  unsigned long long inject_limit_ns;
 };
 
 __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T) {
@@ -259,20 +263,24 @@ template <int N, bool REVERSE> struct Chain {
     if (group > 0) early = ld_word(state(group));
     else if (init && ch < p.C) x = __ldg(init + (size_t)it.b * p.C + ch);
   }
-  // The warp waits until `get` holds in all lanes, for at most the wait limit.
-  template <typename F> __device__ __forceinline__ void wait(F&& get) {
-    bool ok = failed || get();
+  // The warp waits until `get` holds in all lanes, for at most limit_ns. When
+  // that runs out the state is whatever was read: the status word tells, this
+  // warp's later waits return at once, and the items still go to their end,
+  // publishing what they have, so that nobody waits for them in turn.
+  template <typename F> __device__ __forceinline__ void wait(F&& get, bool& lost, unsigned long long limit_ns) {
+    bool ok = lost || get();
     if (__all_sync(ALL, ok)) return;
     const uint64_t t0 = globaltimer_ns();
     do {
       if (!ok) ok = get();
-      if (__any_sync(ALL, globaltimer_ns() - t0 > p.wait_limit_ns)) {
+      if (__any_sync(ALL, globaltimer_ns() - t0 > limit_ns)) {
         atomicOr(p.status, STATUS_TIMEOUT);
-        failed = true;
+        lost = true;
         return;
       }
     } while (!__all_sync(ALL, ok));
   }
+  template <typename F> __device__ __forceinline__ void wait(F&& get) { wait(get, failed, p.wait_limit_ns); }
   // Over the Q lanes of a slot, in their order: everything up to and including
   // the lane's m.
   static __device__ __forceinline__ Map scan(Map m, int q) {
@@ -309,6 +317,10 @@ template <int N, bool REVERSE> struct Chain {
   // Makes x the state that enters the chunk, publishes the one that leaves a
   // group, and hands every warp its own: enter [WARPS][EROW].
   __device__ __forceinline__ void pass(float* enter) {
+    if (o == p.inject_chunk && it.tile == 0) {
+      bool lost = false;  // (the chunks' own waits are left untouched)
+      wait([&]() { return ld_word((const unsigned long long*)p.ticket + 1) != 0; }, lost, p.inject_limit_ns);
+    }
     // the group's chunks before this one, a run of them a lane
     const int run = (o - first + Q - 1) / Q, from = first + q * run;
     Map r[RUN];
@@ -412,6 +424,36 @@ template <typename T, int ROWS, bool TMA> struct Rows {
   }
 };
 
+// The TMA loads of a warp (its tile, asked for by lane 0) and of the CTA (the
+// biases, by thread 0), as every thread follows them: `phase` has the parity of
+// each barrier's next load. Once a wait has run out (`failed`) no more are asked
+// for, so that no barrier's phases get mixed up, and before the CTA leaves it
+// waits (again with the limit) for what is in flight: nothing may be written to
+// shared memory that is another CTA's by then.
+struct Loads {
+  static constexpr unsigned TILE = 1, BIAS = 2;
+  unsigned phase = 0;
+  bool& failed;
+  __device__ __forceinline__ explicit Loads(bool& failed) : failed(failed) {}
+  template <unsigned WHICH> __device__ __forceinline__ bool ask(bool wanted) {
+    wanted = wanted && !failed;
+    if (wanted) phase ^= WHICH;
+    return wanted;
+  }
+  template <unsigned WHICH> __device__ __forceinline__ unsigned last() const { return phase & WHICH ? 0 : 1; }
+  template <unsigned WHICH> __device__ __forceinline__ void wait(const GatedArgs& p, uint32_t bar) {
+    mbar_wait_bounded<false>(bar, last<WHICH>(), p.wait_limit_ns, p.status, failed);
+  }
+  // (A barrier that was never asked counts as past the phase before its first.)
+  __device__ __forceinline__ void leave(const GatedArgs& p, uint32_t bar, uint32_t bias_bar) {
+    if (!failed || threadIdx.x % 32 != 0) return;
+    bool late = false;
+    mbar_wait_bounded<false>(bar, last<TILE>(), p.wait_limit_ns, nullptr, late);
+    late = false;
+    if (threadIdx.x == 0) mbar_wait_bounded<false>(bias_bar, last<BIAS>(), p.wait_limit_ns, nullptr, late);
+  }
+};
+
 // A lane's biases, scaled as the gates want them: from the copy beside the tile
 // [G][32] (TMA), or from memory.
 template <typename T, int FN, int N, bool TMA>
@@ -489,14 +531,15 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(false)))
   if (p.solo && blockIdx.x == 0 && threadIdx.x == 0) *p.status = STATUS_OK;
   if (threadIdx.x == 0) *shared = place_of<false>(p, p.solo ? blockIdx.x : atomicAdd(p.ticket, 1u));
   __syncthreads();
-  for (unsigned loads = 0, turn = 0; shared->x >= 0; ++turn) {
+  Loads loads(failed);
+  while (shared->x >= 0) {
   const Item it = item_of<N>(p, *shared);
   if (TMA) {
-    if (lane == 0 && it.live > 0) {
+    if (loads.ask<Loads::TILE>(it.live > 0) && lane == 0) {
       mbar_arrive_expect_tx(bar, STEPS * G * 128);
       tma_load_4d(smem_u32(mine), &xmap, bar, it.ct, 0, it.t0, it.b);
     }
-    if (threadIdx.x == 0 && p.bias) {
+    if (loads.ask<Loads::BIAS>(p.bias != nullptr) && threadIdx.x == 0) {
       mbar_arrive_expect_tx(bbar, G * 128);
       tma_load_4d(smem_u32(bcopy), &bmap, bbar, it.ct, 0, 0, 0);
     }
@@ -506,10 +549,10 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(false)))
   Ch chain(p, it, failed);
   chain.ask(p.s0);
   FV<N> bias[G];
-  if (TMA && p.bias) mbar_wait_bounded<false>(bbar, turn & 1, p.wait_limit_ns, p.status, failed);
+  if (TMA && p.bias) loads.wait<Loads::BIAS>(p, bbar);
   load_bias<T, FN, N, TMA>(p, it, bcopy, bias);
   if (TMA) {
-    if (it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
+    if (it.live > 0) loads.wait<Loads::TILE>(p, bar);
   } else {
     fetch_wait();
   }
@@ -662,6 +705,7 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(false)))
   if (threadIdx.x == 0) *shared = place_of<false>(p, next);
   __syncthreads();
   }
+  if (TMA) loads.leave(p, bar, bbar);
 }
 
 // Backward: 18 bytes a channel and step for linear bf16 (Wx, dh in; dWx out).
@@ -731,15 +775,16 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(true)))
     }
   };
   int last_b = -1, last_k = 0, last_ct = 0;  // mode 1: the item whose sums wait for the next load
-  for (unsigned loads = 0, turn = 0; shared->x >= 0; ++turn) {
+  Loads loads(failed);
+  while (shared->x >= 0) {
   const Item it = item_of<N>(p, *shared);
   if (TMA) {
-    if (lane == 0 && it.live > 0) {
+    if (loads.ask<Loads::TILE>(it.live > 0) && lane == 0) {
       mbar_arrive_expect_tx(bar, STEPS * G * XB + (p.dh ? STEPS * 128 : 0));
       tma_load_4d(smem_u32(mine), &xmap, bar, it.ct, 0, it.t0, it.b);
       if (p.dh) tma_load_4d(smem_u32(dmine), &dmap, bar, it.ct, 0, it.t0, it.b);
     }
-    if (threadIdx.x == 0 && p.bias) {
+    if (loads.ask<Loads::BIAS>(p.bias != nullptr) && threadIdx.x == 0) {
       mbar_arrive_expect_tx(bbar, G * 128);
       tma_load_4d(smem_u32(bcopy), &bmap, bbar, it.ct, 0, 0, 0);
     }
@@ -772,10 +817,10 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(true)))
                 ? mul_of<FN, N>(g) * act_scale(p.qs[(((size_t)it.b * qblocks + it.t0 / ACT_BLOCK) * G + g) * p.C + it.ch + v])
                 : 0.0f;
   }
-  if (TMA && p.bias) mbar_wait_bounded<false>(bbar, turn & 1, p.wait_limit_ns, p.status, failed);
+  if (TMA && p.bias) loads.wait<Loads::BIAS>(p, bbar);
   load_bias<T, FN, N, TMA>(p, it, bcopy, bias);
   if (TMA) {
-    if (it.live > 0) mbar_wait_bounded<false>(bar, loads++ & 1, p.wait_limit_ns, p.status, failed);
+    if (it.live > 0) loads.wait<Loads::TILE>(p, bar);
   } else {
     fetch_wait();
   }
@@ -950,6 +995,7 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(true)))
   __syncthreads();
   }
   if (last_b >= 0) sum_db(last_b, last_k, last_ct);
+  if (TMA) loads.leave(p, bar, bbar);
 }
 
 template <typename T, int FN, bool Q8> constexpr int fwd_smem() {
@@ -1159,6 +1205,8 @@ GatedArgs gated_args(const rnn_gated_dims_t* d, const GatedSizes& z, void* works
   a.maps = (ulonglong2*)(ws + 512 + z.states);
   a.done = (unsigned*)(ws + 512 + z.states + z.maps);
   a.wait_limit_ns = wait_limit_ns();
+  inject_wait(&a.inject_chunk, &a.inject_limit_ns);
+  if (z.solo) a.inject_chunk = -1;
   return a;
 }
 

@@ -14,6 +14,9 @@ void note_launch(int count = 1);
 // The upper bound (ns) every device-side wait of the library's kernels uses.
 unsigned long long wait_limit_ns();
 
+// What rnn_debug_inject_wait set: the step (-1: off) and the limit.
+void inject_wait(int* step, unsigned long long* limit_ns);
+
 // cudaFuncSetAttribute, called once per (device, kernel) for the largest
 // dynamic shared memory requested so far (and once for the non-portable
 // cluster size): the runtime call costs microseconds of host time that a

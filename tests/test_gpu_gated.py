@@ -310,6 +310,42 @@ def test_step(M, P, N, D, function, dtype):
     assert torch.equal(h, h2) and torch.equal(pool, out)
 
 
+def test_waits_that_run_out_are_reported():
+    """A wait in the pass of the state that nothing ends runs out, forward and
+    backward; the status word tells, and everything else went on as it should."""
+    for function, dtype, shape in (("linear", BF, (2, 900, 1, 64)), ("linear_coupled", F32, (1, 400, 1, 33))):
+        B, T, N, D = shape
+        p = make(function, *shape, dtype)
+        dims = _lib.make_gated_dims(B, T, N, D, function, dtype)
+        ws = [torch.empty(_lib.rnn_gated_workspace_size(dims, k), dtype=torch.uint8, device="cuda")
+              for k in (_lib.WS_FWD, _lib.WS_BWD)]
+
+        def passes():
+            h, last = torch.empty_like(p["dh"]), torch.empty_like(p["state"])
+            tape = torch.empty(_lib.rnn_gated_tape_size(dims), dtype=torch.uint8, device="cuda")
+            dWx, db, ds = (torch.empty_like(p[k]) for k in ("Wx", "b", "state"))
+            _lib.rnn_gated_fwd(dims, p["Wx"], p["b"], p["state"], None, None, h, last, tape, ws[0])
+            _lib.rnn_gated_bwd(dims, p["Wx"], p["b"], None, None, tape, p["dh"], p["dlast"], dWx, db, ds, ws[1])
+            return h, last, dWx, db, ds
+
+        ref = passes()
+        for w in ws:
+            _lib.rnn_check_status(w)
+        _lib.rnn_debug_inject_wait(1, 2_000_000)  # 2 ms
+        try:
+            got = passes()
+        finally:
+            _lib.rnn_debug_inject_wait(-1)
+        for w in ws:
+            with pytest.raises(_lib.RnnError) as err:
+                _lib.rnn_check_status(w)
+            assert err.value.status == _lib.RNN_ETIMEOUT
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        assert all(torch.equal(a, b) for a, b in zip(passes(), ref))
+        for w in ws:
+            _lib.rnn_check_status(w)
+
+
 def test_steps_follow_the_scan():
     p = make("linear", 3, 20, 2, 40, F32)
     h, last = run(p, "linear", grads=False)
