@@ -8,6 +8,7 @@ the backward through time run in librnn_gb300.so's kernels via the C ABI.
 from __future__ import annotations
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 from torch.autograd.function import once_differentiable
 
 from . import _lib
@@ -151,6 +152,23 @@ def flashrnn_stack(x, layers, function: str = "lstm", backend: str = "auto"):
 
 
 # ---- gated linear scan ------------------------------------------------------------
+def _tracked(*tensors):
+    """Whether autograd has to see a call on these tensors (None: absent): for a
+    gradient, or to refuse a forward-mode tangent, which the call would drop."""
+    tensors = [t for t in tensors if t is not None]
+    return torch.is_grad_enabled() and any(t.requires_grad for t in tensors) or any(_is_dual(t) for t in tensors)
+
+
+def _is_dual(t):
+    return t is not None and unpack_dual(t).tangent is not None
+
+
+def _first_order(*grads):
+    """Refuses forward over reverse: the gradients' kernels would drop the tangent."""
+    if any(_is_dual(g) for g in grads):
+        raise NotImplementedError("the backward has no forward-mode derivative")
+
+
 def _dense(t):
     """t (or None) as the library takes it: contiguous and 16-byte aligned."""
     if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
@@ -193,6 +211,7 @@ class _GatedFn(torch.autograd.Function):
 
 
 def _gated_bwd(ctx, dh, dlast):
+    _first_order(dh, dlast)
     Wx, b, reset, lengths, tape = ctx.saved_tensors
     dims, size = ctx.plan[:2]
     B, _, G, N, D = ctx.shape
@@ -275,8 +294,7 @@ def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, len
         if lengths.dtype == torch.int64:
             lengths = lengths.clamp(0, T).to(torch.int32)
         lengths = lengths.contiguous()
-    if torch.is_grad_enabled() and (Wx.requires_grad or (b is not None and b.requires_grad) or
-                                    (state is not None and state.requires_grad)):
+    if _tracked(Wx, b, state):
         return _GatedFn.apply(Wx, b, state, function, reset, lengths, checkpoint)
     return _gated_run(Wx, b, state, function, reset, lengths, checkpoint, False)[:2]
 
@@ -381,6 +399,7 @@ class _EmbedFn(torch.autograd.Function):
 
 
 def _embed_bwd(ctx, dout):
+    _first_order(dout)
     (ids,) = ctx.saved_tensors
     (V, E), dtype, scale, pad = ctx.args
     n = ids.numel()
@@ -415,6 +434,6 @@ def embedding(ids, weight, scale: float = 1.0, padding_idx=None, status=None):
         raise ValueError(f"padding_idx must be None or in 0 .. {weight.shape[0] - 1}, got {padding_idx}")
     pad = -1 if padding_idx is None else int(padding_idx)
     ids = ids.contiguous()
-    if torch.is_grad_enabled() and weight.requires_grad:
+    if _tracked(weight):
         return _EmbedFn.apply(ids, weight, float(scale), pad, status)
     return _embed_run(ids, weight, float(scale), status)

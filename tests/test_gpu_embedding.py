@@ -8,6 +8,7 @@ k 2^-23."""
 import numpy as np
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import recurrent_networks_gb300 as rn
 from oracle import gated
@@ -162,3 +163,17 @@ def test_refusals():
     for call in (lambda: rn.embedding(ids.float(), W), lambda: rn.embedding(ids, W.double())):
         with pytest.raises(TypeError):
             call()
+
+
+def test_forward_mode_is_refused():
+    W, ids = torch.randn(7, 8, device="cuda"), torch.arange(3, device="cuda")
+    for grad in (True, False):
+        with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+            with pytest.raises(NotImplementedError):
+                rn.embedding(ids, forward_ad.make_dual(W, torch.ones_like(W)))
+            rn.embedding(ids, W)
+    W.requires_grad_(True)
+    with forward_ad.dual_level():
+        out = rn.embedding(ids, W)
+        with pytest.raises(NotImplementedError):  # forward over reverse
+            torch.autograd.grad(out, W, forward_ad.make_dual(torch.ones_like(out), torch.ones_like(out)))

@@ -12,6 +12,7 @@ exponential and reciprocal (2^-21 together) take the place: 1e-6 + T 2^-20."""
 import numpy as np
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import recurrent_networks_gb300 as rn
 from oracle import gated
@@ -394,3 +395,26 @@ def test_refusals():
             call()
     with pytest.raises(_lib.RnnError):
         rn.gated_scan(Wx[:0], b)
+
+
+def test_forward_mode_is_refused():
+    """The operators have no forward-mode derivative: a dual tensor raises, also
+    where no gradient is asked for, and does not lose its tangent."""
+    args = [torch.randn(1, 5, 4, 1, 8, device="cuda"), torch.randn(4, 1, 8, device="cuda"),
+            torch.randn(1, 1, 1, 8, device="cuda")]
+    for k in range(3):
+        for grad in (True, False):
+            with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+                duals = list(args)
+                duals[k] = forward_ad.make_dual(args[k], torch.ones_like(args[k]))
+                with pytest.raises(NotImplementedError):
+                    rn.gated_scan(*duals)
+                rn.gated_scan(*args)
+    # forward over reverse
+    x = args[0].clone().requires_grad_(True)
+    with forward_ad.dual_level():
+        h, last = rn.gated_scan(x, *args[1:])
+        for out in (h, last):
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(out, x, forward_ad.make_dual(torch.ones_like(out), torch.ones_like(out)),
+                                    retain_graph=True)
