@@ -360,6 +360,7 @@ size_t rnn_gated_workspace_size(const rnn_gated_dims_t *dims, int kind);
  *   h       [B,T,N,D]                                                   (out)
  *   last    [B,1,N,D] fp32, the state after the last step, or NULL       (out)
  *   tape    rnn_gated_tape_size() bytes, or NULL (no backward to come)   (out)
+ * N D <= 2^28, T < 2^31 - RNN_GATED_CHUNK.
  * Errors: RNN_EINVAL, RNN_ENOSPC, RNN_ECUDA; RNN_ETIMEOUT by rnn_check_status. */
 int rnn_gated_fwd(const rnn_gated_dims_t *dims, const void *Wx, const void *b, const void *state0,
                   const unsigned char *reset, const int *lengths, void *h, void *last, void *tape,
@@ -397,13 +398,14 @@ int rnn_gated_step(int rows, int slots, int N, int D, int function, int dtype, c
  * x / 2^e rounded to nearest even. e is at most 121: magnitudes past 127 * 2^121
  * (3.38e38) saturate there instead of unpacking to an infinity. A block with an infinity or a NaN gets the
  * byte 255 and unpacks to NaN. Unpacking gives q * 2^e, exact in bf16 too.
+ * rows < 2^40, cols < 2^31 - 64.
  * Errors: RNN_EINVAL, RNN_ECUDA. */
 size_t rnn_act_scale_bytes(long long rows, int cols);
 int rnn_act_pack(long long rows, int cols, int dtype, const void *x, void *q, void *scales, void *stream);
 int rnn_act_unpack(long long rows, int cols, int dtype, const void *q, const void *scales, void *x, void *stream);
 
 /* ---- token embedding --------------------------------------------------------------- */
-/* out[i] = scale * W[ids[i]] for n < 2^31 tokens; W [V][E], out [n][E], ids int32
+/* out[i] = scale * W[ids[i]] for n < 2^31 tokens; W [V][E] (E <= 2^30), out [n][E], ids int32
  * (id_bytes 4) or int64 (8). A token outside 0 .. V-1 gives a zero row and sets
  * RNN_ERANGE in `status` (a device word that rnn_check_status reads, not
  * cleared by this call, or NULL).

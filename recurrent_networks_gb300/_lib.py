@@ -314,11 +314,17 @@ def _raw_stream(t, stream):
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
 
 
+def _int32(v):
+    """v as the C int it becomes: past 32 bits -1, which every entry point refuses
+    (ctypes would pass on the low bits)."""
+    return v if -0x80000000 <= v <= 0x7fffffff else -1
+
+
 def make_gated_dims(B, T, N, D, function="linear", dtype=torch.bfloat16, checkpoint=None) -> GatedDims:
     fn = GATED_FUNCTIONS[function] if isinstance(function, str) else int(function)
     dt = DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
     ck = checkpoint if isinstance(checkpoint, int) else CHECKPOINTS[checkpoint]
-    return GatedDims(int(B), int(T), int(N), int(D), fn, dt, ck)
+    return GatedDims(*(_int32(int(v)) for v in (B, T, N, D)), fn, dt, ck)
 
 
 _gated_plans: dict = {}
@@ -373,7 +379,7 @@ def rnn_gated_bwd(dims: GatedDims, Wx, b, reset, lengths, tape, dh, dlast, dWx, 
 
 def rnn_gated_step(rows, slots, N, D, function, dtype, Wx, b, slot, pool, pool_out, h, status=None, stream=None) -> int:
     rc = _quick().rnn_gated_step(
-        rows, slots, N, D, GATED_FUNCTIONS[function] if isinstance(function, str) else function, DTYPES[dtype],
+        _int32(rows), _int32(slots), _int32(N), _int32(D), GATED_FUNCTIONS[function] if isinstance(function, str) else function, DTYPES[dtype],
         Wx.data_ptr(), None if b is None else b.data_ptr(), None if slot is None else slot.data_ptr(),
         pool.data_ptr(), pool_out.data_ptr(), h.data_ptr(), None if status is None else status.data_ptr(),
         _raw_stream(h, stream))
@@ -382,17 +388,17 @@ def rnn_gated_step(rows, slots, N, D, function, dtype, Wx, b, slot, pool, pool_o
 
 # ---- 8-bit activation checkpoints ------------------------------------------------------
 def rnn_act_scale_bytes(rows: int, cols: int) -> int:
-    return int(_quick().rnn_act_scale_bytes(int(rows), int(cols)))
+    return int(_quick().rnn_act_scale_bytes(int(rows), _int32(int(cols))))
 
 
 def rnn_act_pack(rows: int, cols: int, x, q, scales, stream=None) -> int:
-    rc = _quick().rnn_act_pack(rows, cols, DTYPES[x.dtype], x.data_ptr(), q.data_ptr(), scales.data_ptr(),
+    rc = _quick().rnn_act_pack(rows, _int32(cols), DTYPES[x.dtype], x.data_ptr(), q.data_ptr(), scales.data_ptr(),
                                _raw_stream(x, stream))
     return rc if rc == RNN_OK else _check(rc, "rnn_act_pack")
 
 
 def rnn_act_unpack(rows: int, cols: int, q, scales, x, stream=None) -> int:
-    rc = _quick().rnn_act_unpack(rows, cols, DTYPES[x.dtype], q.data_ptr(), scales.data_ptr(), x.data_ptr(),
+    rc = _quick().rnn_act_unpack(rows, _int32(cols), DTYPES[x.dtype], q.data_ptr(), scales.data_ptr(), x.data_ptr(),
                                  _raw_stream(x, stream))
     return rc if rc == RNN_OK else _check(rc, "rnn_act_unpack")
 
@@ -406,7 +412,7 @@ def rnn_embed_bwd_workspace_size(n: int, V: int, E: int) -> int:
     if size is None:
         if len(_embed_sizes) >= 4096:
             _embed_sizes.clear()
-        size = _embed_sizes[n, V, E] = int(_quick().rnn_embed_bwd_workspace_size(int(n), int(V), int(E)))
+        size = _embed_sizes[n, V, E] = int(_quick().rnn_embed_bwd_workspace_size(int(n), _int32(int(V)), _int32(int(E))))
     return size
 
 
@@ -423,7 +429,7 @@ def status_word(t):
 
 
 def rnn_embed_fwd(n: int, V: int, E: int, ids, W, scale: float, out, status=None, stream=None) -> int:
-    rc = _quick().rnn_embed_fwd(n, V, E, DTYPES[W.dtype], ids.element_size(), ids.data_ptr(), W.data_ptr(), scale,
+    rc = _quick().rnn_embed_fwd(n, _int32(V), _int32(E), DTYPES[W.dtype], ids.element_size(), ids.data_ptr(), W.data_ptr(), scale,
                                 out.data_ptr(), None if status is None else status.data_ptr(), _raw_stream(W, stream))
     return rc if rc == RNN_OK else _check(rc, "rnn_embed_fwd")
 
@@ -432,6 +438,6 @@ def rnn_embed_bwd(n: int, V: int, E: int, ids, padding_idx: int, dout, scale: fl
                   stream=None) -> int:
     """dW [V][E] from dout [n][E] (see include/rnn.h); padding_idx -1 = none."""
     ptr, size = _ws(workspace)
-    rc = _quick().rnn_embed_bwd(n, V, E, DTYPES[dW.dtype], ids.element_size(), ids.data_ptr(), padding_idx,
+    rc = _quick().rnn_embed_bwd(n, _int32(V), _int32(E), DTYPES[dW.dtype], ids.element_size(), ids.data_ptr(), padding_idx,
                                 dout.data_ptr(), scale, dW.data_ptr(), ptr, size, _raw_stream(dW, stream))
     return rc if rc == RNN_OK else _check(rc, "rnn_embed_bwd")

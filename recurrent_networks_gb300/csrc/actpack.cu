@@ -1,5 +1,6 @@
 // 8-bit activation checkpoints: int8 values with one power-of-two scale per
 // block of 32 rows of a column (include/rnn.h).
+#include <limits.h>
 #include <stdio.h>
 
 #include "gated.cuh"
@@ -170,7 +171,7 @@ int cuda_status(cudaError_t e) {
 }
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool act_ok(long long rows, int cols, int dtype) {
-  return rows >= 0 && rows < (1ll << 40) && cols >= 1 && (dtype == RNN_F32 || dtype == RNN_BF16);
+  return rows >= 0 && rows < (1ll << 40) && cols >= 1 && cols <= INT_MAX - 64 && (dtype == RNN_F32 || dtype == RNN_BF16);
 }
 
 unsigned act_blocks(long long n) { return (unsigned)(n < (1ll << 30) ? n : (1ll << 30)); }

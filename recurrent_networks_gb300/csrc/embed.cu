@@ -525,8 +525,9 @@ int cuda_status(cudaError_t e) {
 }
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+constexpr int EMBED_E_MAX = 1 << 30;  // column numbers and strides stay within 32 bits
 bool embed_ok(long long n, int V, int E, int dtype, int id_bytes) {
-  return n >= 0 && n < (1ll << 31) && V >= 1 && E >= 1 && (dtype == RNN_F32 || dtype == RNN_BF16) &&
+  return n >= 0 && n < (1ll << 31) && V >= 1 && E >= 1 && E <= EMBED_E_MAX && (dtype == RNN_F32 || dtype == RNN_BF16) &&
          (id_bytes == 4 || id_bytes == 8);
 }
 
@@ -565,7 +566,7 @@ template <typename T> int vec_bytes(int E) {
 template <typename T, typename I, int VB>
 cudaError_t embed_fwd_launch(long long n, int V, int E, const void* ids, const void* W, float scale, void* out,
                              unsigned* status, cudaStream_t st) {
-  const int nv = E * (int)sizeof(T) / VB;
+  const int nv = E / Vec<T, VB>::N;
   int lanes = 1;
   while (lanes < nv && lanes < 256) lanes *= 2;
   const long long per_block = 256 / lanes * 4;

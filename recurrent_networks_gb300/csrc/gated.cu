@@ -1,5 +1,6 @@
 // The gated linear scan: forward, backward and the single-token step, and
 // their C entry points (include/rnn.h).
+#include <limits.h>
 #include <stdio.h>
 
 #include "gated.cuh"
@@ -1087,7 +1088,7 @@ bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool gated_dims_ok(const rnn_gated_dims_t* d) {
-  return d && d->B >= 1 && d->T >= 0 && d->N >= 1 && d->D >= 1 && (d->function == RNN_LINEAR || d->function == RNN_LINEAR_COUPLED) &&
+  return d && d->B >= 1 && d->T >= 0 && d->T <= INT_MAX - GATED_CHUNK && d->N >= 1 && d->D >= 1 && (d->function == RNN_LINEAR || d->function == RNN_LINEAR_COUPLED) &&
          (d->dtype == RNN_F32 || d->dtype == RNN_BF16) && (d->checkpoint == RNN_CKPT_NONE || d->checkpoint == RNN_CKPT_INT8) &&
          (long long)d->N * d->D <= (1 << 28) &&
          // one item per 128 steps of 28 (at least) channels

@@ -130,3 +130,26 @@ def test_functions_refuse_cpu_tensors():
                  lambda: rn.embedding(torch.zeros(2, dtype=torch.int64), x[0, 0, 0])):
         with pytest.raises(RuntimeError, match="no CPU path"):
             call()
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Neither the low bits of a longer size nor an overflow on the way to it."""
+    for bad in (dict(T=2**32 + 3), dict(B=2**32 + 1), dict(N=2**32 + 1), dict(D=2**32 + 8), dict(B=1, T=2**31 - 1, D=1)):
+        assert _lib.rnn_gated_tape_size(_dims(**bad)) == 0
+        assert _lib.rnn_gated_workspace_size(_dims(**bad), _lib.WS_FWD) == 0
+    assert _lib.rnn_gated_tape_size(_dims(B=1, T=2**31 - 129, D=1)) >= (2**31 - 129) // 128 * 4
+    for cols in (2**32 + 8, 2**31 - 1):
+        assert _lib.rnn_act_scale_bytes(1, cols) == 0
+    assert _lib.rnn_act_scale_bytes(1, 2**31 - 65) == 2**31 - 65
+    for V, E in ((2**32 + 5, 8), (5, 2**32 + 8), (5, 2**31 - 1)):
+        assert _lib.rnn_embed_bwd_workspace_size(10, V, E) == 0
+    assert _lib.rnn_embed_bwd_workspace_size(10, 5, 2**30) > 0
+    x = torch.zeros(64)  # refused before it is followed
+    for call in (lambda: _lib.rnn_gated_step(2**32 + 1, 4, 1, 8, "linear", torch.float32, x, None, None, x, x, x, stream=0),
+                 lambda: _lib.rnn_act_pack(1, 2**32 + 8, x, x, x, stream=0),
+                 lambda: _lib.rnn_act_unpack(1, 2**32 + 8, x, x, x, stream=0),
+                 lambda: _lib.rnn_embed_fwd(4, 2**32 + 5, 8, x, x, 1.0, x, stream=0),
+                 lambda: _lib.rnn_embed_bwd(4, 2**32 + 5, 8, x, -1, x, 1.0, x, x, stream=0)):
+        with pytest.raises(_lib.RnnError) as err:
+            call()
+        assert err.value.status == _lib.RNN_EINVAL
