@@ -310,8 +310,19 @@ def _ws(workspace):
     return t.data_ptr() + at, t.numel() * t.element_size() - at
 
 
+def check_device(t) -> None:
+    """The library launches on the current device, so t has to be there."""
+    device, current = t.get_device(), torch.cuda.current_device()
+    if device != current:
+        raise ValueError(f"a tensor is on cuda:{device} and the current device is cuda:{current}: "
+                         f"make the call inside torch.cuda.device({device})")
+
+
 def _raw_stream(t, stream):
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
+    if stream is not None:
+        return _stream(stream)
+    check_device(t)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _int32(v):
@@ -330,12 +341,13 @@ def make_gated_dims(B, T, N, D, function="linear", dtype=torch.bfloat16, checkpo
 _gated_plans: dict = {}
 
 
-def gated_plan(B, T, N, D, function, dtype, checkpoint):
-    """(dims, tape bytes, forward and backward workspace bytes), kept per dims."""
-    key = (B, T, N, D, function, dtype, checkpoint)
+def gated_plan(B, T, N, D, function, dtype, checkpoint, device):
+    """(dims, tape bytes, forward and backward workspace bytes), kept per dims
+    and device: the sizes follow from the current device, which is `device`."""
+    key = (B, T, N, D, function, dtype, checkpoint, device)
     plan = _gated_plans.get(key)
     if plan is None:
-        dims = make_gated_dims(*key)
+        dims = make_gated_dims(*key[:-1])
         if len(_gated_plans) >= 4096:
             _gated_plans.clear()
         plan = _gated_plans[key] = (dims, rnn_gated_tape_size(dims), rnn_gated_workspace_size(dims, WS_FWD),
@@ -407,12 +419,15 @@ def rnn_act_unpack(rows: int, cols: int, q, scales, x, stream=None) -> int:
 _embed_sizes: dict = {}
 
 
-def rnn_embed_bwd_workspace_size(n: int, V: int, E: int) -> int:
-    size = _embed_sizes.get((n, V, E))
+def rnn_embed_bwd_workspace_size(n: int, V: int, E: int, device=None) -> int:
+    """Kept per `device`, the current one (None: whichever that is)."""
+    size = _embed_sizes.get((n, V, E, device)) if device is not None else None
     if size is None:
-        if len(_embed_sizes) >= 4096:
-            _embed_sizes.clear()
-        size = _embed_sizes[n, V, E] = int(_quick().rnn_embed_bwd_workspace_size(int(n), _int32(int(V)), _int32(int(E))))
+        size = int(_quick().rnn_embed_bwd_workspace_size(int(n), _int32(int(V)), _int32(int(E))))
+        if device is not None:
+            if len(_embed_sizes) >= 4096:
+                _embed_sizes.clear()
+            _embed_sizes[n, V, E, device] = size
     return size
 
 

@@ -152,6 +152,12 @@ def flashrnn_stack(x, layers, function: str = "lstm", backend: str = "auto"):
 
 
 # ---- gated linear scan ------------------------------------------------------------
+def _on_gpu(t, name):
+    if not t.is_cuda:
+        raise RuntimeError(f"{name} runs on CUDA tensors only (there is no CPU path)")
+    _lib.check_device(t)
+
+
 def _tracked(*tensors):
     """Whether autograd has to see a call on these tensors (None: absent): for a
     gradient, or to refuse a forward-mode tangent, which the call would drop."""
@@ -181,7 +187,7 @@ def _gated_run(Wx, b, state, function, reset, lengths, checkpoint, keep):
     tape's tensor holds, after it, the workspace of both directions (small
     beside Wx): one allocation a pass."""
     B, T, _, N, D = Wx.shape
-    plan = _lib.gated_plan(B, T, N, D, function, Wx.dtype, checkpoint)
+    plan = _lib.gated_plan(B, T, N, D, function, Wx.dtype, checkpoint, Wx.get_device())
     Wx, b, state = _dense(Wx), _dense(b), _dense(state)
     h = Wx.new_empty((B, T, N, D))
     last = torch.empty((B, 1, N, D), dtype=torch.float32, device=h.device)
@@ -263,8 +269,7 @@ def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, len
     states from those kept every 128 steps. checkpoint="int8" keeps Wx for the
     backward in 8 bits (a power-of-two scale per 32 steps of a channel and
     gate) instead of Wx itself; the gradient is then taken at those values."""
-    if not Wx.is_cuda:
-        raise RuntimeError("gated_scan runs on CUDA tensors only (there is no CPU path)")
+    _on_gpu(Wx, "gated_scan")
     N, D = _gated_shapes(Wx, b, function, 2)
     B, T = Wx.shape[:2]
     if checkpoint not in _lib.CHECKPOINTS:
@@ -308,8 +313,7 @@ def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=
     [M,N,D]. status: an int32 CUDA tensor of one element, zeroed by the caller,
     in which a slot past the pool is recorded (such a row counts as unused);
     _lib.rnn_check_status(status) raises for it."""
-    if not Wx.is_cuda:
-        raise RuntimeError("gated_scan_step runs on CUDA tensors only (there is no CPU path)")
+    _on_gpu(Wx, "gated_scan_step")
     N, D = _gated_shapes(Wx, b, function, 1)
     M = Wx.shape[0]
     dev = Wx.get_device()
@@ -348,8 +352,7 @@ def checkpoint_pack(x):
     (uint8, [ceil(rows / 32), cols], rows being the flattened leading axes): one
     power of two per 32 rows of a column, the smallest whose 127-fold holds the
     block's largest magnitude. Blocks with an infinity or a NaN unpack to NaN."""
-    if not x.is_cuda:
-        raise RuntimeError("checkpoint_pack runs on CUDA tensors only (there is no CPU path)")
+    _on_gpu(x, "checkpoint_pack")
     if x.dtype not in _lib.DTYPES:
         raise TypeError(f"unsupported dtype {x.dtype}")
     if not (x.dim() >= 1 and x.shape[-1] >= 1):
@@ -360,8 +363,7 @@ def checkpoint_pack(x):
 
 def checkpoint_unpack(q, scales, dtype=torch.bfloat16):
     """The values (exact in either dtype) that checkpoint_pack's q and scales stand for."""
-    if not q.is_cuda:
-        raise RuntimeError("checkpoint_unpack runs on CUDA tensors only (there is no CPU path)")
+    _on_gpu(q, "checkpoint_unpack")
     if dtype not in _lib.DTYPES:
         raise TypeError(f"unsupported dtype {dtype}")
     if not (q.dtype == torch.int8 and scales.dtype == torch.uint8):
@@ -404,7 +406,7 @@ def _embed_bwd(ctx, dout):
     (V, E), dtype, scale, pad = ctx.args
     n = ids.numel()
     dW = torch.empty((V, E), dtype=dtype, device=ids.device)
-    size = _lib.rnn_embed_bwd_workspace_size(n, V, E)
+    size = _lib.rnn_embed_bwd_workspace_size(n, V, E, ids.get_device())
     ws = _lib.status_word(ids) if size <= 256 else torch.empty(size, dtype=torch.uint8, device=ids.device)
     _lib.rnn_embed_bwd(n, V, E, ids, pad, _dense(dout), scale, dW, ws)
     return None, dW, None, None, None
@@ -420,8 +422,7 @@ def embedding(ids, weight, scale: float = 1.0, padding_idx=None, status=None):
     zero for padding_idx. Ids out of range give zero rows and no gradient;
     status: an int32 CUDA tensor of one element, zeroed by the caller, in which
     they are recorded (_lib.rnn_check_status(status) raises for it)."""
-    if not weight.is_cuda:
-        raise RuntimeError("embedding runs on CUDA tensors only (there is no CPU path)")
+    _on_gpu(weight, "embedding")
     if weight.dim() != 2:
         raise ValueError(f"weight must be [V,E], got shape {tuple(weight.shape)}")
     if weight.dtype not in _lib.DTYPES:

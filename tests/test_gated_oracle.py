@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import recurrent_networks_gb300 as rn
 from oracle import gated
 from recurrent_networks_gb300 import _lib
 
@@ -153,3 +154,46 @@ def test_sizes_past_32_bits_are_refused():
         with pytest.raises(_lib.RnnError) as err:
             call()
         assert err.value.status == _lib.RNN_EINVAL
+
+
+def test_tensors_off_the_current_device_are_refused(monkeypatch):
+    """The library launches on the current device; a call on another device's
+    tensors must not reach it (the devices are stand-ins: no GPU is needed)."""
+    class There(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    def there(*shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(There)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x, i8, u8, ids = there(2, 3, 4, 1, 8), there(4, 8, dtype=torch.int8), there(1, 8, dtype=torch.uint8), there(3, dtype=torch.int64)
+    for call in (lambda: rn.gated_scan(x), lambda: rn.gated_scan_step(x[:, 0], None, there(2, 1, 8)),
+                 lambda: rn.checkpoint_pack(there(4, 8)), lambda: rn.checkpoint_unpack(i8, u8),
+                 lambda: rn.embedding(ids, there(5, 8)),
+                 lambda: _lib.rnn_gated_fwd(_dims(), x, None, None, None, None, x, None, None, x),
+                 lambda: _lib.rnn_gated_bwd(_dims(), x, None, None, None, x, None, None, None, None, None, x),
+                 lambda: _lib.rnn_gated_step(2, 2, 1, 8, "linear", torch.float32, x, None, None, x, x, x),
+                 lambda: _lib.rnn_act_pack(1, 8, x, i8, u8), lambda: _lib.rnn_act_unpack(1, 8, i8, u8, x),
+                 lambda: _lib.rnn_embed_fwd(3, 5, 8, ids, x, 1.0, x),
+                 lambda: _lib.rnn_embed_bwd(3, 5, 8, ids, -1, x, 1.0, x, x)):
+        with pytest.raises(ValueError, match="cuda:1 and the current device is cuda:0"):
+            call()
+
+
+def test_kept_sizes_belong_to_a_device(monkeypatch):
+    """With the number of SMs that the library plans for changed in between, as
+    another current device would change it, each device keeps its own sizes."""
+    args = (1, 4000, 1, 64, "linear", torch.float32, None)
+    try:
+        for device, sms in ((0, 8), (1, 148)):
+            _lib.load().rnn_plan_set_limits(sms, 227 * 1024, 16)
+            assert _lib.gated_plan(*args, device)[2] == _lib.rnn_gated_workspace_size(_lib.make_gated_dims(*args))
+            assert (_lib.rnn_embed_bwd_workspace_size(4000, 50, 64, device) ==
+                    _lib.load().rnn_embed_bwd_workspace_size(4000, 50, 64))
+        assert _lib.gated_plan(*args, 0)[2] != _lib.gated_plan(*args, 1)[2]
+        assert _lib.rnn_embed_bwd_workspace_size(4000, 50, 64, 0) != _lib.rnn_embed_bwd_workspace_size(4000, 50, 64, 1)
+    finally:
+        _lib.rnn_plan_set_limits(0)
