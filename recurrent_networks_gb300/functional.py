@@ -17,6 +17,12 @@ BACKENDS = {"auto": "auto", "cuda_fused": "fused", "fused": "fused", "cuda": "al
             "alternating": "alternating", "simt": "simt", "grid": "grid"}
 
 
+def _on_gpu(t, name):
+    if not t.is_cuda:
+        raise RuntimeError(f"{name} runs on CUDA tensors only (there is no CPU path)")
+    _lib.check_device(t)
+
+
 def _dims(Wx, R, function, backend):
     B, T, G, N, D = Wx.shape
     if G != _lib.rnn_num_gates(function):
@@ -72,8 +78,7 @@ def flashrnn(Wx, R, b, states=None, function: str = "lstm", backend: str = "auto
     states [S,B,1,N,D] or None (zeros). Returns (states [S,B,T,N,D], last
     [S,B,1,N,D]). function: lstm | gru | elman | slstm. backend: auto |
     cuda_fused (fused) | cuda (alternating) | simt."""
-    if not Wx.is_cuda:
-        raise RuntimeError("flashrnn runs on CUDA tensors only (there is no CPU path)")
+    _on_gpu(Wx, "flashrnn")
     return _ScanFn.apply(Wx, R, b, states, function, backend)
 
 
@@ -121,8 +126,7 @@ def input_projection(x, W, bias=None, checkpoint=None):
     checkpoint="int8" keeps x for the backward in 8 bits (checkpoint_pack over
     the flattened rows) instead of x itself: dW is then taken at the unpacked
     values; the result, dx and dbias are unchanged."""
-    if not x.is_cuda:
-        raise RuntimeError("input_projection runs on CUDA tensors only (there is no CPU path)")
+    _on_gpu(x, "input_projection")
     if checkpoint not in _lib.CHECKPOINTS:
         raise ValueError(f"checkpoint must be one of {list(_lib.CHECKPOINTS)}, got {checkpoint!r}")
     lead = x.shape[:-1]
@@ -152,12 +156,6 @@ def flashrnn_stack(x, layers, function: str = "lstm", backend: str = "auto"):
 
 
 # ---- gated linear scan ------------------------------------------------------------
-def _on_gpu(t, name):
-    if not t.is_cuda:
-        raise RuntimeError(f"{name} runs on CUDA tensors only (there is no CPU path)")
-    _lib.check_device(t)
-
-
 def _tracked(*tensors):
     """Whether autograd has to see a call on these tensors (None: absent): for a
     gradient, or to refuse a forward-mode tangent, which the call would drop."""

@@ -170,7 +170,9 @@ def test_tensors_off_the_current_device_are_refused(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     x, i8, u8, ids = there(2, 3, 4, 1, 8), there(4, 8, dtype=torch.int8), there(1, 8, dtype=torch.uint8), there(3, dtype=torch.int64)
-    for call in (lambda: rn.gated_scan(x), lambda: rn.gated_scan_step(x[:, 0], None, there(2, 1, 8)),
+    for call in (lambda: rn.flashrnn(there(2, 3, 4, 1, 8), there(4, 1, 8, 8), there(4, 1, 8)),
+                 lambda: rn.input_projection(there(3, 64), there(64, 64)),
+                 lambda: rn.gated_scan(x), lambda: rn.gated_scan_step(x[:, 0], None, there(2, 1, 8)),
                  lambda: rn.checkpoint_pack(there(4, 8)), lambda: rn.checkpoint_unpack(i8, u8),
                  lambda: rn.embedding(ids, there(5, 8)),
                  lambda: _lib.rnn_gated_fwd(_dims(), x, None, None, None, None, x, None, None, x),
