@@ -156,6 +156,17 @@ def flashrnn_stack(x, layers, function: str = "lstm", backend: str = "auto"):
 
 
 # ---- gated linear scan ------------------------------------------------------------
+def _check_status(status, t):
+    """The kernels write to the status word, so it has to be one that they can."""
+    if status is None:
+        return
+    if status.dtype != torch.int32:
+        raise TypeError(f"status must be int32, got {status.dtype}")
+    if status.numel() != 1 or status.get_device() != t.get_device():
+        raise ValueError(f"status must be one element on cuda:{t.get_device()}, got shape {tuple(status.shape)} "
+                         f"on {status.device}")
+
+
 def _tracked(*tensors):
     """Whether autograd has to see a call on these tensors (None: absent): for a
     gradient, or to refuse a forward-mode tangent, which the call would drop."""
@@ -313,6 +324,7 @@ def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=
     _lib.rnn_check_status(status) raises for it."""
     _on_gpu(Wx, "gated_scan_step")
     N, D = _gated_shapes(Wx, b, function, 1)
+    _check_status(status, Wx)
     M = Wx.shape[0]
     dev = Wx.get_device()
     for p in (pool,) if pool_out is None else (pool, pool_out):
@@ -431,6 +443,7 @@ def embedding(ids, weight, scale: float = 1.0, padding_idx=None, status=None):
         raise ValueError("ids must be on weight's device")
     if not (padding_idx is None or 0 <= padding_idx < weight.shape[0]):
         raise ValueError(f"padding_idx must be None or in 0 .. {weight.shape[0] - 1}, got {padding_idx}")
+    _check_status(status, weight)
     pad = -1 if padding_idx is None else int(padding_idx)
     ids = ids.contiguous()
     if _tracked(weight):

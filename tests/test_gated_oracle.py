@@ -156,18 +156,21 @@ def test_sizes_past_32_bits_are_refused():
         assert err.value.status == _lib.RNN_EINVAL
 
 
+class There(torch.Tensor):
+    """A stand-in for a tensor on cuda:1."""
+    is_cuda = True
+
+    def get_device(self):
+        return 1
+
+
+def there(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(There)
+
+
 def test_tensors_off_the_current_device_are_refused(monkeypatch):
     """The library launches on the current device; a call on another device's
     tensors must not reach it (the devices are stand-ins: no GPU is needed)."""
-    class There(torch.Tensor):
-        is_cuda = True
-
-        def get_device(self):
-            return 1
-
-    def there(*shape, dtype=torch.float32):
-        return torch.zeros(*shape, dtype=dtype).as_subclass(There)
-
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     x, i8, u8, ids = there(2, 3, 4, 1, 8), there(4, 8, dtype=torch.int8), there(1, 8, dtype=torch.uint8), there(3, dtype=torch.int64)
     for call in (lambda: rn.flashrnn(there(2, 3, 4, 1, 8), there(4, 1, 8, 8), there(4, 1, 8)),
@@ -199,3 +202,15 @@ def test_kept_sizes_belong_to_a_device(monkeypatch):
         assert _lib.rnn_embed_bwd_workspace_size(4000, 50, 64, 0) != _lib.rnn_embed_bwd_workspace_size(4000, 50, 64, 1)
     finally:
         _lib.rnn_plan_set_limits(0)
+
+
+def test_status_words_that_the_kernels_cannot_write_are_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    i32 = torch.int32
+    for status, error in ((torch.zeros(1, dtype=i32), ValueError), (there(1), TypeError),
+                          (there(1, dtype=torch.int64), TypeError), (there(0, dtype=i32), ValueError),
+                          (there(2, dtype=i32), ValueError)):
+        for call in (lambda: rn.gated_scan_step(there(2, 4, 1, 8), None, there(2, 1, 8), status=status),
+                     lambda: rn.embedding(there(3, dtype=torch.int64), there(5, 8), status=status)):
+            with pytest.raises(error, match="status"):
+                call()
