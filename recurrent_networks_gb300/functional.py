@@ -162,8 +162,8 @@ def _check_status(status, t):
         return
     if status.dtype != torch.int32:
         raise TypeError(f"status must be int32, got {status.dtype}")
-    if status.numel() != 1 or status.get_device() != t.get_device():
-        raise ValueError(f"status must be one element on cuda:{t.get_device()}, got shape {tuple(status.shape)} "
+    if status.numel() < 1 or status.get_device() != t.get_device():
+        raise ValueError(f"status must be an element on cuda:{t.get_device()}, got shape {tuple(status.shape)} "
                          f"on {status.device}")
 
 
