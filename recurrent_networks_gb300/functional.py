@@ -343,8 +343,10 @@ def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=
             raise ValueError(f"slots must be [M]=[{M}] int32 on Wx's device")
         slots = slots.contiguous()
     h = Wx.new_empty((M, N, D))
-    _lib.rnn_gated_step(M, P, N, D, function, Wx.dtype, _dense(Wx), _dense(b), slots, pool,
-                        pool if pool_out is None else pool_out, h, status)
+    out = pool if pool_out is None else pool_out
+    _lib.rnn_gated_step(M, P, N, D, function, Wx.dtype, _dense(Wx), _dense(b), slots, pool, out, h, status)
+    if not out.is_inference():  # a graph that saved the old states has to learn of the write
+        torch.autograd.graph.increment_version(out)
     return h
 
 

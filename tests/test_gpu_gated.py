@@ -418,3 +418,23 @@ def test_forward_mode_is_refused():
             with pytest.raises(NotImplementedError):
                 torch.autograd.grad(out, x, forward_ad.make_dual(torch.ones_like(out), torch.ones_like(out)),
                                     retain_graph=True)
+
+
+def test_step_tells_autograd_that_it_writes_the_pool():
+    Wx, pool, other = torch.randn(2, 4, 1, 8, device="cuda"), torch.randn(3, 1, 8, device="cuda"), torch.zeros(3, 1, 8, device="cuda")
+    w = torch.ones(3, 1, 8, device="cuda", requires_grad=True)
+    rn.gated_scan_step(Wx, None, pool)
+    kept = (w * pool).sum()  # saves the pool
+    rn.gated_scan_step(Wx, None, pool, pool_out=other)
+    kept.backward(retain_graph=True)  # the pool was only read
+    rn.gated_scan_step(Wx, None, pool)
+    with pytest.raises(RuntimeError, match="inplace"):
+        kept.backward()
+    kept = (w * other).sum()
+    rn.gated_scan_step(Wx, None, pool, pool_out=other)
+    with pytest.raises(RuntimeError, match="inplace"):
+        kept.backward()
+    with torch.inference_mode():  # a pool without a version, also outside
+        pool = torch.randn(3, 1, 8, device="cuda")
+        rn.gated_scan_step(Wx, None, pool)
+    rn.gated_scan_step(Wx, None, pool)
