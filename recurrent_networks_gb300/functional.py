@@ -191,7 +191,13 @@ def _dense(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
-def _gated_run(Wx, b, state, function, reset, lengths, checkpoint, keep):
+def _add_status(status, workspace, at=0):
+    """What the kernels running on the workspace report, added to the caller's word."""
+    if status is not None:
+        status.as_strided((1,), (1,)).bitwise_or_(workspace[at:at + 4].view(torch.int32))
+
+
+def _gated_run(Wx, b, state, function, reset, lengths, checkpoint, status, keep):
     """(h, last, Wx and b as the library took them, plan, tape or None). The
     tape's tensor holds, after it, the workspace of both directions (small
     beside Wx): one allocation a pass."""
@@ -204,17 +210,20 @@ def _gated_run(Wx, b, state, function, reset, lengths, checkpoint, keep):
     if keep:
         tape = torch.empty(size + (fwd if fwd > bwd else bwd), dtype=torch.uint8, device=h.device)
         _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, (tape, size))
+        _add_status(status, tape, size)
     else:
         tape = None
         ws = torch.empty(fwd, dtype=torch.uint8, device=h.device)
         _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, None, ws)
+        _add_status(status, ws)
     return h, last, Wx, b, plan, tape
 
 
 class _GatedFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, Wx, b, state, function, reset, lengths, checkpoint):
-        h, last, Wx, b, ctx.plan, tape = _gated_run(Wx, b, state, function, reset, lengths, checkpoint, True)
+    def forward(ctx, Wx, b, state, function, reset, lengths, checkpoint, status):
+        h, last, Wx, b, ctx.plan, tape = _gated_run(Wx, b, state, function, reset, lengths, checkpoint, status, True)
+        ctx.status = status
         ctx.shape = Wx.shape
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(Wx if checkpoint is None else None, b, reset, lengths, tape)
@@ -236,7 +245,8 @@ def _gated_bwd(ctx, dh, dlast):
     db = torch.empty((G, N, D), dtype=dtype, device=tape.device) if need[1] else None
     ds = torch.empty((B, 1, N, D), dtype=torch.float32, device=tape.device) if need[2] else None
     _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, (tape, size))
-    return dWx, db, ds, None, None, None, None
+    _add_status(ctx.status, tape, size)
+    return dWx, db, ds, None, None, None, None, None
 
 
 _gated_bwd_once = once_differentiable(_gated_bwd)
@@ -264,7 +274,7 @@ def _gated_shapes(Wx, b, function, lead):
     return N, D
 
 
-def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, lengths=None, checkpoint=None):
+def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, lengths=None, checkpoint=None, status=None):
     """Gated linear scan: the recurrence without R, linear in its state.
 
     Wx [B,T,G,N,D] (bf16 or fp32), b [G,N,D] or None, state [B,1,N,D] or None
@@ -277,12 +287,16 @@ def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, len
     step, fp32). Differentiable in Wx, b and state; the backward recomputes the
     states from those kept every 128 steps. checkpoint="int8" keeps Wx for the
     backward in 8 bits (a power-of-two scale per 32 steps of a channel and
-    gate) instead of Wx itself; the gradient is then taken at those values."""
+    gate) instead of Wx itself; the gradient is then taken at those values.
+    status: an int32 CUDA tensor of one element, zeroed by the caller, in which
+    the forward and the backward record a device-side wait that ran out (their
+    results are then not valid); _lib.rnn_check_status(status) raises for it."""
     _on_gpu(Wx, "gated_scan")
     N, D = _gated_shapes(Wx, b, function, 2)
     B, T = Wx.shape[:2]
     if checkpoint not in _lib.CHECKPOINTS:
         raise ValueError(f"checkpoint must be one of {list(_lib.CHECKPOINTS)}, got {checkpoint!r}")
+    _check_status(status, Wx)
     if state is not None:
         if state.shape != (B, 1, N, D):
             raise ValueError(f"state must be [B,1,N,D]={(B, 1, N, D)}, got {tuple(state.shape)}")
@@ -309,8 +323,8 @@ def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, len
             lengths = lengths.clamp(0, T).to(torch.int32)
         lengths = lengths.contiguous()
     if _tracked(Wx, b, state):
-        return _GatedFn.apply(Wx, b, state, function, reset, lengths, checkpoint)
-    return _gated_run(Wx, b, state, function, reset, lengths, checkpoint, False)[:2]
+        return _GatedFn.apply(Wx, b, state, function, reset, lengths, checkpoint, status)
+    return _gated_run(Wx, b, state, function, reset, lengths, checkpoint, status, False)[:2]
 
 
 def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=None, status=None):

@@ -210,6 +210,7 @@ def test_status_words_that_the_kernels_cannot_write_are_refused(monkeypatch):
     for status, error in ((torch.zeros(1, dtype=i32), ValueError), (there(1), TypeError),
                           (there(1, dtype=torch.int64), TypeError), (there(0, dtype=i32), ValueError)):
         for call in (lambda: rn.gated_scan_step(there(2, 4, 1, 8), None, there(2, 1, 8), status=status),
+                     lambda: rn.gated_scan(there(2, 3, 4, 1, 8), status=status),
                      lambda: rn.embedding(there(3, dtype=torch.int64), there(5, 8), status=status)):
             with pytest.raises(error, match="status"):
                 call()

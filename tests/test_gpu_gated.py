@@ -347,6 +347,42 @@ def test_waits_that_run_out_are_reported():
             _lib.rnn_check_status(w)
 
 
+@pytest.mark.parametrize("checkpoint", [None, "int8"])
+def test_time_outs_reach_the_callers_status_word(checkpoint):
+    p = make("linear", 2, 700, 1, 64, BF)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def told():
+        try:
+            _lib.rnn_check_status(status)
+        except _lib.RnnError as e:
+            return e.status == _lib.RNN_ETIMEOUT
+        return False
+
+    def scan(grad, inject):
+        x = p["Wx"].clone().requires_grad_(grad)
+        _lib.rnn_debug_inject_wait(1 if inject else -1, 2_000_000)
+        try:
+            return x, rn.gated_scan(x, p["b"], p["state"], checkpoint=checkpoint, status=status)[0]
+        finally:
+            _lib.rnn_debug_inject_wait(-1)
+
+    for grad in (False, True):
+        scan(grad, False)
+        assert not told()
+        scan(grad, True)
+        assert told() and not told()  # read and cleared
+    x, h = scan(True, False)
+    torch.autograd.grad(h, x, p["dh"], retain_graph=True)
+    assert not told()
+    _lib.rnn_debug_inject_wait(1, 2_000_000)
+    try:
+        torch.autograd.grad(h, x, p["dh"])
+    finally:
+        _lib.rnn_debug_inject_wait(-1)
+    assert told()
+
+
 def test_steps_follow_the_scan():
     p = make("linear", 3, 20, 2, 40, F32)
     h, last = run(p, "linear", grads=False)
