@@ -304,10 +304,9 @@ def _quick():
     return _short
 
 
-def _ws(workspace):
-    """(pointer, bytes) of a workspace: a tensor, or (tensor, offset) for the rest of it."""
-    t, at = workspace if isinstance(workspace, tuple) else (workspace, 0)
-    return t.data_ptr() + at, t.numel() * t.element_size() - at
+def _ws(t):
+    """(pointer, bytes) of a workspace."""
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def check_device(t) -> None:

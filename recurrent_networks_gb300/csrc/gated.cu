@@ -1139,7 +1139,7 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   const long long rows = (long long)d->B * z.chunks;
   z.db_mode = z.solo && d->B <= 8 ? 3 : !z.solo && rows <= 64 ? 2 : 1;
   z.sync = 512 + z.states + z.maps + up256(z.tiles_c * sizeof(unsigned));
-  z.dbp = up256((size_t)d->B * z.chunks * z.G * z.C * sizeof(float));
+  z.dbp = z.db_mode == 3 ? 0 : up256((size_t)d->B * z.chunks * z.G * z.C * sizeof(float));
   return z;
 }
 

@@ -191,31 +191,24 @@ def _dense(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
-def _add_status(status, workspace, at=0):
+def _add_status(status, workspace):
     """What the kernels running on the workspace report, added to the caller's word."""
     if status is not None:
-        status.as_strided((1,), (1,)).bitwise_or_(workspace[at:at + 4].view(torch.int32))
+        status.as_strided((1,), (1,)).bitwise_or_(workspace[:4].view(torch.int32))
 
 
 def _gated_run(Wx, b, state, function, reset, lengths, checkpoint, status, keep):
-    """(h, last, Wx and b as the library took them, plan, tape or None). The
-    tape's tensor holds, after it, the workspace of both directions (small
-    beside Wx): one allocation a pass."""
+    """(h, last, Wx and b as the library took them, plan, tape or None)."""
     B, T, _, N, D = Wx.shape
     plan = _lib.gated_plan(B, T, N, D, function, Wx.dtype, checkpoint, Wx.get_device())
     Wx, b, state = _dense(Wx), _dense(b), _dense(state)
     h = Wx.new_empty((B, T, N, D))
     last = torch.empty((B, 1, N, D), dtype=torch.float32, device=h.device)
-    dims, size, fwd, bwd = plan
-    if keep:
-        tape = torch.empty(size + (fwd if fwd > bwd else bwd), dtype=torch.uint8, device=h.device)
-        _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, (tape, size))
-        _add_status(status, tape, size)
-    else:
-        tape = None
-        ws = torch.empty(fwd, dtype=torch.uint8, device=h.device)
-        _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, None, ws)
-        _add_status(status, ws)
+    dims, size, fwd, _ = plan
+    tape = torch.empty(size, dtype=torch.uint8, device=h.device) if keep else None
+    ws = torch.empty(fwd, dtype=torch.uint8, device=h.device)
+    _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, ws)
+    _add_status(status, ws)
     return h, last, Wx, b, plan, tape
 
 
@@ -237,15 +230,16 @@ class _GatedFn(torch.autograd.Function):
 def _gated_bwd(ctx, dh, dlast):
     _first_order(dh, dlast)
     Wx, b, reset, lengths, tape = ctx.saved_tensors
-    dims, size = ctx.plan[:2]
+    dims, _, _, size = ctx.plan
     B, _, G, N, D = ctx.shape
     need = ctx.needs_input_grad
     dtype = torch.bfloat16 if dims.dtype == _lib.DTYPES[torch.bfloat16] else torch.float32
     dWx = torch.empty(ctx.shape, dtype=dtype, device=tape.device) if need[0] else None
     db = torch.empty((G, N, D), dtype=dtype, device=tape.device) if need[1] else None
     ds = torch.empty((B, 1, N, D), dtype=torch.float32, device=tape.device) if need[2] else None
-    _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, (tape, size))
-    _add_status(ctx.status, tape, size)
+    ws = torch.empty(size, dtype=torch.uint8, device=tape.device)
+    _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, ws)
+    _add_status(ctx.status, ws)
     return dWx, db, ds, None, None, None, None, None
 
 

@@ -383,6 +383,18 @@ def test_time_outs_reach_the_callers_status_word(checkpoint):
     assert told()
 
 
+@pytest.mark.parametrize("checkpoint", [None, "int8"])
+@pytest.mark.parametrize("T", [1, 10, 700])
+def test_what_a_training_forward_keeps(T, checkpoint):
+    """Between forward and backward: the tape, and Wx itself unless its 8-bit copy is in the tape."""
+    Wx = torch.randn(16, T, 4, 1, 512, device="cuda").to(BF).requires_grad_(True)
+    b = torch.randn(4, 1, 512, device="cuda").to(BF).requires_grad_(True)
+    h, _ = rn.gated_scan(Wx, b, checkpoint=checkpoint)
+    kept = sum(t.numel() * t.element_size() for t in h.grad_fn.saved_tensors if t is not None and t is not b)
+    tape = _lib.rnn_gated_tape_size(_lib.make_gated_dims(16, T, 1, 512, "linear", BF, checkpoint))
+    assert kept <= tape + (0 if checkpoint else Wx.numel() * 2) + b.numel() * 2
+
+
 def test_steps_follow_the_scan():
     p = make("linear", 3, 20, 2, 40, F32)
     h, last = run(p, "linear", grads=False)
