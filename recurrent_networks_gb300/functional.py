@@ -129,6 +129,8 @@ def input_projection(x, W, bias=None, checkpoint=None):
     _on_gpu(x, "input_projection")
     if checkpoint not in _lib.CHECKPOINTS:
         raise ValueError(f"checkpoint must be one of {list(_lib.CHECKPOINTS)}, got {checkpoint!r}")
+    if not torch.is_grad_enabled():  # no backward to come, nothing to keep
+        checkpoint = None
     lead = x.shape[:-1]
     y = _ProjFn.apply(x.reshape(-1, x.shape[-1]), W, bias, checkpoint)
     return y.reshape(*lead, W.shape[0])

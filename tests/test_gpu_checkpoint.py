@@ -6,6 +6,7 @@ import torch
 
 import recurrent_networks_gb300 as rn
 from oracle import gated, projection
+from recurrent_networks_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -93,3 +94,18 @@ def test_projection_with_a_packed_input(BT, I, C):
     # W frozen: nothing of x is needed
     (dx1,) = torch.autograd.grad(rn.input_projection(x, W.detach(), checkpoint="int8"), x, dy)
     assert torch.equal(dx1, dx)
+
+
+def test_projection_packs_only_for_a_backward():
+    x, W = torch.randn(64, 64, device="cuda").to(torch.bfloat16), torch.randn(64, 64, device="cuda").to(torch.bfloat16)
+    ref = rn.input_projection(x, W)
+
+    def launches(checkpoint):
+        before = _lib.rnn_kernel_launches()
+        y = rn.input_projection(x, W.requires_grad_(True), checkpoint=checkpoint)
+        assert torch.equal(y, ref)
+        return _lib.rnn_kernel_launches() - before
+
+    assert launches("int8") == launches(None) + 1  # the packing
+    with torch.no_grad():
+        assert launches("int8") == launches(None)
