@@ -48,15 +48,11 @@ class GatedDims(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
-# The same library through a binding that keeps the interpreter lock: for the
-# short calls that only enqueue. Giving the lock up and taking it again costs
-# tens of microseconds a call while autograd's thread runs beside.
-_short = None
 
 
 def load(path: str | None = None):
     """Load (building first if needed) the CUDA library; raises if impossible."""
-    global _lib, _short
+    global _lib
     with _lock:
         if _lib is None:
             lib = ctypes.CDLL(path or _build.build())
@@ -92,7 +88,6 @@ def load(path: str | None = None):
             lib.rnn_input_proj_fwd.argtypes = [i, i, i] + [vp] * 5 + [sz, vp]
             lib.rnn_input_proj_bwd.argtypes = [i, i, i] + [vp] * 7 + [sz, vp]
             gp, ll, f = ctypes.POINTER(GatedDims), ctypes.c_longlong, ctypes.c_float
-            short = ctypes.PyDLL(lib._name)
             for name, args in (("rnn_gated_num_gates", [i]), ("rnn_gated_tape_size", [gp]),
                                ("rnn_gated_workspace_size", [gp, i]), ("rnn_gated_fwd", [gp] + [vp] * 9 + [sz, vp]),
                                ("rnn_gated_bwd", [gp] + [vp] * 11 + [sz, vp]), ("rnn_gated_step", [i] * 6 + [vp] * 8),
@@ -100,11 +95,9 @@ def load(path: str | None = None):
                                ("rnn_act_unpack", [ll, i, i] + [vp] * 4), ("rnn_embed_bwd_workspace_size", [ll, i, i]),
                                ("rnn_embed_fwd", [ll, i, i, i, i, vp, vp, f, vp, vp, vp]),
                                ("rnn_embed_bwd", [ll, i, i, i, i, vp, ll, vp, f, vp, vp, sz, vp])):
-                for binding in (lib, short):
-                    getattr(binding, name).argtypes = args
-                    if name.endswith(("_size", "_bytes")):
-                        getattr(binding, name).restype = sz
-            _short = short
+                getattr(lib, name).argtypes = args
+                if name.endswith(("_size", "_bytes")):
+                    getattr(lib, name).restype = sz
             _lib = lib
     return _lib
 
@@ -296,12 +289,12 @@ def rnn_input_proj_bwd(BT: int, I: int, C: int, x, W, dWx, dx, dW, dbias, worksp
 
 # ---- gated linear scan ------------------------------------------------------------
 # These entry points are called once a layer and step, so the marshalling is
-# kept short: the interpreter lock is held (see _short), pointers are taken in
-# place, and what follows from the dims alone is worked out once (gated_plan).
+# kept short: pointers are taken in place, and what follows from the dims alone is
+# worked out once (gated_plan). The interpreter lock is given up all the same: a
+# launch waits while the stream's queue is full, and what the queue waits for may
+# need the lock (a host callback).
 def _quick():
-    if _short is None:
-        load()
-    return _short
+    return load() if _lib is None else _lib
 
 
 def _ws(t):

@@ -214,3 +214,10 @@ def test_status_words_that_the_kernels_cannot_write_are_refused(monkeypatch):
                      lambda: rn.embedding(there(3, dtype=torch.int64), there(5, 8), status=status)):
             with pytest.raises(error, match="status"):
                 call()
+
+
+def test_calls_give_up_the_interpreter_lock():
+    """A launch can wait for the stream's queue, and the queue for a host callback that needs the lock."""
+    lib = _lib._quick()
+    for name in _lib.EXPORTS:
+        assert not getattr(lib, name)._flags_ & ctypes.PyDLL._func_flags_ & ~ctypes.CDLL._func_flags_, name
