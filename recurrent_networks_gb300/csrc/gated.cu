@@ -1098,7 +1098,9 @@ bool gated_dims_ok(const rnn_gated_dims_t* d) {
 struct GatedSizes {
   int G, C, chunks, qblocks, width, tiles_c, span, solo, db_mode;
   size_t esize, carry, q, qs, tape;
-  size_t sync, states, maps, dbp;  // workspace: status, ticket, states and maps (sync: zeroed by every call) | db sums
+  // workspace: status, ticket, states, maps, counts (sync: zeroed by every call;
+  // solo: the status alone, written by it) | db sums
+  size_t sync, states, maps, dbp;
 };
 GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   GatedSizes z;
@@ -1138,7 +1140,7 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   // (128 items: 24 us after the last one against 6 for the launch).
   const long long rows = (long long)d->B * z.chunks;
   z.db_mode = z.solo && d->B <= 8 ? 3 : !z.solo && rows <= 64 ? 2 : 1;
-  z.sync = 512 + z.states + z.maps + up256(z.tiles_c * sizeof(unsigned));
+  z.sync = z.solo ? 256 : 512 + z.states + z.maps + up256(z.tiles_c * sizeof(unsigned));
   z.dbp = z.db_mode == 3 ? 0 : up256((size_t)d->B * z.chunks * z.G * z.C * sizeof(float));
   return z;
 }
@@ -1201,10 +1203,12 @@ GatedArgs gated_args(const rnn_gated_dims_t* d, const GatedSizes& z, void* works
   a.tiles_c = z.tiles_c; a.width = z.width; a.span = z.span; a.solo = z.solo;
   char* ws = (char*)workspace;
   a.status = (unsigned*)ws;
-  a.ticket = (unsigned*)(ws + 256);
-  a.states = (unsigned long long*)(ws + 512);
-  a.maps = (ulonglong2*)(ws + 512 + z.states);
-  a.done = (unsigned*)(ws + 512 + z.states + z.maps);
+  if (!z.solo) {
+    a.ticket = (unsigned*)(ws + 256);
+    a.states = (unsigned long long*)(ws + 512);
+    a.maps = (ulonglong2*)(ws + 512 + z.states);
+    a.done = (unsigned*)(ws + 512 + z.states + z.maps);
+  }
   a.wait_limit_ns = wait_limit_ns();
   inject_wait(&a.inject_chunk, &a.inject_limit_ns);
   if (z.solo) a.inject_chunk = -1;

@@ -8,7 +8,7 @@ the backward through time run in librnn_gb300.so's kernels via the C ABI.
 from __future__ import annotations
 
 import torch
-from torch.autograd.forward_ad import unpack_dual
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib
@@ -169,20 +169,25 @@ def _check_status(status, t):
                          f"on {status.device}")
 
 
+def _any_dual(*tensors):
+    if getattr(forward_ad, "_current_level", 0) < 0:  # no dual level is open (asking each tensor costs more)
+        return False
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def _tracked(*tensors):
     """Whether autograd has to see a call on these tensors (None: absent): for a
     gradient, or to refuse a forward-mode tangent, which the call would drop."""
-    tensors = [t for t in tensors if t is not None]
-    return torch.is_grad_enabled() and any(t.requires_grad for t in tensors) or any(_is_dual(t) for t in tensors)
-
-
-def _is_dual(t):
-    return t is not None and unpack_dual(t).tangent is not None
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return _any_dual(*tensors)
 
 
 def _first_order(*grads):
     """Refuses forward over reverse: the gradients' kernels would drop the tangent."""
-    if any(_is_dual(g) for g in grads):
+    if _any_dual(*grads):
         raise NotImplementedError("the backward has no forward-mode derivative")
 
 
@@ -191,6 +196,14 @@ def _dense(t):
     if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
         return t
     return t.clone(memory_format=torch.contiguous_format)
+
+
+def _workspace(size, t, status):
+    """Workspace on t's device: the kept word where the call needs no more than a
+    status word and nobody asks for it."""
+    if size <= 256 and status is None:
+        return _lib.status_word(t)
+    return torch.empty(size, dtype=torch.uint8, device=t.device)
 
 
 def _add_status(status, workspace):
@@ -208,7 +221,7 @@ def _gated_run(Wx, b, state, function, reset, lengths, checkpoint, status, keep)
     last = torch.empty((B, 1, N, D), dtype=torch.float32, device=h.device)
     dims, size, fwd, _ = plan
     tape = torch.empty(size, dtype=torch.uint8, device=h.device) if keep else None
-    ws = torch.empty(fwd, dtype=torch.uint8, device=h.device)
+    ws = _workspace(fwd, h, status)
     _lib.rnn_gated_fwd(dims, Wx, b, state, reset, lengths, h, last, tape, ws)
     _add_status(status, ws)
     return h, last, Wx, b, plan, tape
@@ -239,7 +252,7 @@ def _gated_bwd(ctx, dh, dlast):
     dWx = torch.empty(ctx.shape, dtype=dtype, device=tape.device) if need[0] else None
     db = torch.empty((G, N, D), dtype=dtype, device=tape.device) if need[1] else None
     ds = torch.empty((B, 1, N, D), dtype=torch.float32, device=tape.device) if need[2] else None
-    ws = torch.empty(size, dtype=torch.uint8, device=tape.device)
+    ws = _workspace(size, tape, ctx.status)
     _lib.rnn_gated_bwd(dims, Wx, b, reset, lengths, tape, _dense(dh), _dense(dlast), dWx, db, ds, ws)
     _add_status(ctx.status, ws)
     return dWx, db, ds, None, None, None, None, None
@@ -429,7 +442,7 @@ def _embed_bwd(ctx, dout):
     n = ids.numel()
     dW = torch.empty((V, E), dtype=dtype, device=ids.device)
     size = _lib.rnn_embed_bwd_workspace_size(n, V, E, ids.get_device())
-    ws = _lib.status_word(ids) if size <= 256 else torch.empty(size, dtype=torch.uint8, device=ids.device)
+    ws = _workspace(size, ids, None)
     _lib.rnn_embed_bwd(n, V, E, ids, pad, _dense(dout), scale, dW, ws)
     return None, dW, None, None, None
 
