@@ -132,17 +132,23 @@ __device__ __forceinline__ FV<2> sigmoid_full(const FV<2>& z) {
 }
 __device__ __forceinline__ FV<1> sigmoid_full(const FV<1>& z) { return sigmoid(z); }
 // f = sigmoid(z) and n = 1 - f, both to full relative accuracy (the coupled
-// cell uses n itself as the input gate): n = exp(-z) f, with exp(-z) bounded
-// by 2^125 so that f stays a normal number and n becomes 1.
+// cell uses n itself as the input gate). fp32: with e = exp(-|z|), which cannot
+// overflow, 1 / (1 + e) and e / (1 + e), the larger one f where z > 0. bf16
+// storage: f = 1 / (1 + e) and n = e f with e = exp(-z) bounded by 2^125, so that
+// n becomes 1; the least f, 2^-125, is taken off again, so that a gate of
+// -infinity is 0 (the other form takes 156 + 323 us, this one 149 + 308, at B=32
+// T=4096 C=1024).
 __device__ __forceinline__ void sigmoid_both(const FV<2>& t, FV<2>& f, FV<2>& n) {
   const FV<2> e = exp_neg(FV<2>{{min_nan(t.v[0], 125.0f), min_nan(t.v[1], 125.0f)}});
-  f = rcp_full(add(e, splat<2>(1.0f)));
-  n = mul(e, f);
+  const FV<2> r = rcp_full(add(e, splat<2>(1.0f)));
+  n = mul(e, r);
+  f = add(r, splat<2>(-2.350988702e-38f));
 }
 __device__ __forceinline__ void sigmoid_both(const FV<1>& z, FV<1>& f, FV<1>& n) {
-  const FV<1> e = exp_neg(FV<1>{{max_nan(z.v[0], -86.0f)}});  // exp(-z) bounded as above
-  f = rcp(add(e, splat<1>(1.0f)));
-  n = mul(e, f);
+  const FV<1> e = exp_neg(FV<1>{{fabsf(z.v[0])}}), hi = rcp(add(e, splat<1>(1.0f))), lo = mul(e, hi);
+  const bool open = z.v[0] > 0.0f;
+  f.v[0] = open ? hi.v[0] : lo.v[0];
+  n.v[0] = open ? lo.v[0] : hi.v[0];
 }
 
 // f and u of c = f c' + u from the gates z[G]
