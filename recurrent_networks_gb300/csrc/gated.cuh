@@ -135,9 +135,9 @@ __device__ __forceinline__ FV<1> sigmoid_full(const FV<1>& z) { return sigmoid(z
 // cell uses n itself as the input gate). fp32: with e = exp(-|z|), which cannot
 // overflow, 1 / (1 + e) and e / (1 + e), the larger one f where z > 0. bf16
 // storage: f = 1 / (1 + e) and n = e f with e = exp(-z) bounded by 2^125, so that
-// n becomes 1; the least f, 2^-125, is taken off again, so that a gate of
-// -infinity is 0 (the other form takes 156 + 323 us, this one 149 + 308, at B=32
-// T=4096 C=1024).
+// n becomes 1; the least f, 2^-125 (1 / (1 + e) rounds to no less, so f stays
+// non-negative), is taken off again, so that a gate of -infinity is 0. (The
+// other form takes 156 + 323 us, this one 150 + 311, at B=32 T=4096 C=1024.)
 __device__ __forceinline__ void sigmoid_both(const FV<2>& t, FV<2>& f, FV<2>& n) {
   const FV<2> e = exp_neg(FV<2>{{min_nan(t.v[0], 125.0f), min_nan(t.v[1], 125.0f)}});
   const FV<2> r = rcp_full(add(e, splat<2>(1.0f)));

@@ -17,17 +17,22 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("function", ["linear", "linear_coupled"])
 def test_long_memories(function, dtype):
     """The carried state and the gradient of the initial state, fp32 for either
-    dtype, in channels that remember 2 to 2000 steps.
+    dtype, in channels that remember 2 to 2000 steps; inputs and gradients of one
+    sign, so that an error to one side adds up.
 
-    Tolerance: f, and the sum that it enters, are each off by at most 2^-23
-    relative a step, to either side alike. Over a memory of 2000 steps these add
-    up to a standard deviation of sqrt(2 * 2000) 2^-23 / sqrt(3) = 4.4e-6 of the
-    state: 3e-5 is beyond six of them. An error of f to one side would add up to
-    2000 of it: a reciprocal good to 2^-23 that is always too large, 1e-4 and more."""
-    B, T, D = 2, 6000, 72
+    Tolerance: a step rounds 1 + e, f and the sum that f enters, each by at most
+    2^-24 relative to either side alike: a standard deviation of 2^-24 together.
+    Over a memory of M = 2000 steps they add up with the weights f^k, whose
+    squares sum to M / 2: sqrt(1000) 2^-24 = 1.9e-6 of the state, and 1.2e-5 is six
+    of them. An error to one side adds up to M of it: an eighth of 2^-23 on
+    average would show."""
+    B, T, D = 1, 12000, 72
     p = make(function, B, T, 1, D, dtype)
     f = 1 if function == "linear" else 0
     p["Wx"][:, :, f] *= 0.25
+    for x in (p["Wx"][:, :, f + 1], p["state"], p["dh"], p["dlast"]):
+        x.abs_()
+    p["b"][f + 1] = 0
     tau = torch.logspace(np.log10(2), np.log10(2000), D)
     p["b"][f, 0] = torch.log(tau - 1).to(dtype).cuda()
     _, last, _, _, ds = run(p, function)
@@ -36,7 +41,7 @@ def test_long_memories(function, dtype):
     for got, ref, what in ((last, rlast, "last"), (ds, rds, "dstate")):
         worst = np.abs(got.detach().double().cpu().numpy() - ref).max() / np.abs(ref).max()
         print(function, dtype, what, worst)
-        assert worst <= 3e-5, (what, worst)
+        assert worst <= 1.2e-5, (what, worst)
 
 
 # (B, T, N, D) and what it reaches: sums of db by a launch of their own (more than
