@@ -302,19 +302,20 @@ def _ws(t):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def check_device(t) -> None:
-    """The library launches on the current device, so t has to be there."""
-    device, current = t.get_device(), torch.cuda.current_device()
-    if device != current:
-        raise ValueError(f"a tensor is on cuda:{device} and the current device is cuda:{current}: "
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def check_device(t) -> int:
+    """The number of t's device, where the library is about to launch: the current one."""
+    device = t.get_device()
+    if device != _current_device():
+        raise ValueError(f"a tensor is on cuda:{device} and the current device is cuda:{_current_device()}: "
                          f"make the call inside torch.cuda.device({device})")
+    return device
 
 
 def _raw_stream(t, stream):
-    if stream is not None:
-        return _stream(stream)
-    check_device(t)
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return torch._C._cuda_getCurrentRawStream(check_device(t)) if stream is None else _stream(stream)
 
 
 def _int32(v):
@@ -403,7 +404,7 @@ def rnn_act_pack(rows: int, cols: int, x, q, scales, stream=None) -> int:
 
 def rnn_act_unpack(rows: int, cols: int, q, scales, x, stream=None) -> int:
     rc = _quick().rnn_act_unpack(rows, _int32(cols), DTYPES[x.dtype], q.data_ptr(), scales.data_ptr(), x.data_ptr(),
-                                 _raw_stream(x, stream))
+                                 _raw_stream(q, stream))
     return rc if rc == RNN_OK else _check(rc, "rnn_act_unpack")
 
 

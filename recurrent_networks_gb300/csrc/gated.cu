@@ -1135,7 +1135,7 @@ GatedSizes gated_sizes(const rnn_gated_dims_t* d) {
   z.states = z.chunks > 1 ? up256(groups * lanes * sizeof(unsigned long long)) : 0;
   z.maps = z.chunks > 1 && z.span > 0 ? up256(z.chunks * lanes * sizeof(ulonglong2)) : 0;
   // db: with few batch rows of one chunk, a CTA takes a channel tile's rows one
-  // after the other; with few items, the last one adds the items' sums (16
+  // after the other; with few items, the last one adds the items' sums (32
   // loads in flight, a round trip of a microsecond each); else a launch does
   // (128 items: 24 us after the last one against 6 for the launch).
   const long long rows = (long long)d->B * z.chunks;

@@ -20,7 +20,6 @@ BACKENDS = {"auto": "auto", "cuda_fused": "fused", "fused": "fused", "cuda": "al
 def _on_gpu(t, name):
     if not t.is_cuda:
         raise RuntimeError(f"{name} runs on CUDA tensors only (there is no CPU path)")
-    _lib.check_device(t)
 
 
 def _dims(Wx, R, function, backend):
@@ -79,6 +78,7 @@ def flashrnn(Wx, R, b, states=None, function: str = "lstm", backend: str = "auto
     [S,B,1,N,D]). function: lstm | gru | elman | slstm. backend: auto |
     cuda_fused (fused) | cuda (alternating) | simt."""
     _on_gpu(Wx, "flashrnn")
+    _lib.check_device(Wx)
     return _ScanFn.apply(Wx, R, b, states, function, backend)
 
 
@@ -127,6 +127,7 @@ def input_projection(x, W, bias=None, checkpoint=None):
     the flattened rows) instead of x itself: dW is then taken at the unpacked
     values; the result, dx and dbias are unchanged."""
     _on_gpu(x, "input_projection")
+    _lib.check_device(x)
     if checkpoint not in _lib.CHECKPOINTS:
         raise ValueError(f"checkpoint must be one of {list(_lib.CHECKPOINTS)}, got {checkpoint!r}")
     if not torch.is_grad_enabled():  # no backward to come, nothing to keep
@@ -215,7 +216,7 @@ def _add_status(status, workspace):
 def _gated_run(Wx, b, state, function, reset, lengths, checkpoint, status, keep):
     """(h, last, Wx and b as the library took them, plan, tape or None)."""
     B, T, _, N, D = Wx.shape
-    plan = _lib.gated_plan(B, T, N, D, function, Wx.dtype, checkpoint, Wx.get_device())
+    plan = _lib.gated_plan(B, T, N, D, function, Wx.dtype, checkpoint, _lib.check_device(Wx))
     Wx, b, state = _dense(Wx), _dense(b), _dense(state)
     h = Wx.new_empty((B, T, N, D))
     last = torch.empty((B, 1, N, D), dtype=torch.float32, device=h.device)

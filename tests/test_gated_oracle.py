@@ -171,7 +171,7 @@ def there(*shape, dtype=torch.float32):
 def test_tensors_off_the_current_device_are_refused(monkeypatch):
     """The library launches on the current device; a call on another device's
     tensors must not reach it (the devices are stand-ins: no GPU is needed)."""
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(_lib, "_current_device", lambda: 0)
     x, i8, u8, ids = there(2, 3, 4, 1, 8), there(4, 8, dtype=torch.int8), there(1, 8, dtype=torch.uint8), there(3, dtype=torch.int64)
     for call in (lambda: rn.flashrnn(there(2, 3, 4, 1, 8), there(4, 1, 8, 8), there(4, 1, 8)),
                  lambda: rn.input_projection(there(3, 64), there(64, 64)),
@@ -205,7 +205,7 @@ def test_kept_sizes_belong_to_a_device(monkeypatch):
 
 
 def test_status_words_that_the_kernels_cannot_write_are_refused(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(_lib, "_current_device", lambda: 1)
     i32 = torch.int32
     for status, error in ((torch.zeros(1, dtype=i32), ValueError), (there(1), TypeError),
                           (there(1, dtype=torch.int64), TypeError), (there(0, dtype=i32), ValueError)):
