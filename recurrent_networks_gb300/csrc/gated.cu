@@ -497,11 +497,11 @@ template <typename T, int FN, bool Q8> __host__ __device__ constexpr int ctas_pe
 // and lays h where the tile was, from where one TMA store a warp takes it.
 // Without the 8-bit copy u waits in the tile's place of i and g (coupled: f and
 // g), which are not read again, so that f alone stays in registers and three
-// tiles fit an SM. Measured: B=32 T=4096 C=1024 linear bf16 214 us, 6.27 TB/s,
-// 94 % of the copy bandwidth (loads and stores alone, without arithmetic or
-// state, 201 us); B=1 T=65537 C=768 119 us, where each tile's chunks wait for one
+// tiles fit an SM. Measured: B=32 T=4096 C=1024 linear bf16 216 us, 6.22 TB/s,
+// 93 % of the copy bandwidth (loads and stores alone, without arithmetic or
+// state, 201 us); B=1 T=65537 C=768 120 us, where each tile's chunks wait for one
 // another (loads and stores alone 80 us); with the 8-bit copy, which takes the
-// shared memory of the third tile, B=8 T=4099 C=1024 124 us, 3.8 TB/s.
+// shared memory of the third tile, B=8 T=4099 C=1024 120 us, 4.0 TB/s.
 template <typename T, int FN, bool Q8, bool TMA>
 __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(false)))
     gated_fwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap hmap,
@@ -719,10 +719,10 @@ __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(false)))
 // tile, whose rows are too short, through a ring of 8 steps. Sums for db stay in
 // registers over a warp's steps and are added over warps and items in a fixed
 // order. Two 80 KB tiles fit an SM, and the time an item spends outside its loads
-// (two passes of about 1.5 us, the state, the store) is what keeps it at 5.45
-// TB/s: B=32 T=4096 C=1024 linear bf16 443 us with db, 431 without (362 at the
+// (two passes of about 1.5 us, the state, the store) is what keeps it at 5.5
+// TB/s: B=32 T=4096 C=1024 linear bf16 439 us with db, 429 without (362 at the
 // copy bandwidth; without special functions 20 us less); fp32 B=16 T=2048 C=512
-// 122 us, 4.97 TB/s; int8 checkpoint B=8 T=4099 C=1024 137 us.
+// 122 us, 4.97 TB/s; int8 checkpoint B=8 T=4099 C=1024 138 us.
 template <typename T, int FN, bool Q8, bool TMA>
 __global__ void __launch_bounds__(THREADS, (ctas_per_sm<T, FN, Q8>(true)))
     gated_bwd_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap dmap,
