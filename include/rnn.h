@@ -390,6 +390,58 @@ int rnn_gated_bwd(const rnn_gated_dims_t *dims, const void *Wx, const void *b, c
 int rnn_gated_step(int rows, int slots, int N, int D, int function, int dtype, const void *Wx, const void *b,
                    const int *slot, const void *pool, void *pool_out, void *h, void *status, void *stream);
 
+/* ---- gated delta rule ------------------------------------------------------------- */
+/*
+ * A scan whose state is a matrix S [Dk,Dv] per head, fp32:
+ *   u_t = beta_t (v_t - a_t S_{t-1}^T k_t),  S_t = a_t S_{t-1} + k_t u_t^T,
+ *   o_t = scale S_t^T q_t,                   a_t = exp(g_t)
+ * q, k [B,T,Nk,Dk], v [B,T,N,Dv]: v head n goes with q and k head n / (N / Nk)
+ * (N a multiple of Nk). g (the decay's logarithm) and beta [B,T,N] are fp32.
+ * Keys are taken as they are; the recurrence is stable for beta |k|^2 <= 2.
+ * reset and lengths as for the gated scan: a reset takes S_{t-1} as zero at its
+ * step, whatever it holds (so does a g below -104, whose exponential is 0);
+ * steps past a length are not looked at, o and the gradients are 0 there. An
+ * infinity or a NaN in an input may reach every step of its row and head.
+ * Chunks of 64 steps (bf16) or 32 (fp32) are taken at once by matrix products
+ * whose operands are held to 2^-17 (bf16) or 2^-24 (fp32) of their values.
+ */
+#define RNN_DELTA_MAX_D 256 /* the largest Dk and Dv */
+typedef struct {
+  int B, T, Nk, N, Dk, Dv;
+  int dtype; /* rnn_dtype_t, of q, k, v, o, dO, dq, dk, dv */
+} rnn_delta_dims_t;
+
+/* Bytes of the tape (what the forward works on and the backward needs: about
+ * 2 Dk Dv / 32 + 6 Dv + 512 bytes a step and head for bf16) and of the
+ * backward's workspace; 0 for invalid dims. */
+size_t rnn_delta_tape_size(const rnn_delta_dims_t *dims);
+size_t rnn_delta_bwd_workspace_size(const rnn_delta_dims_t *dims);
+
+/* Forward: state0 [B,1,N,Dk,Dv] fp32 or NULL = zeros, reset [B,T] bytes or
+ * NULL, lengths [B] int32 or NULL; o [B,T,N,Dv], last [B,1,N,Dk,Dv] fp32 or
+ * NULL. The tape may be dropped after the call when no backward comes.
+ * Errors: RNN_EINVAL, RNN_ENOSPC, RNN_ECUDA. */
+int rnn_delta_fwd(const rnn_delta_dims_t *dims, const void *q, const void *k, const void *v, const void *g,
+                  const void *beta, const void *state0, const unsigned char *reset, const int *lengths, float scale,
+                  void *o, void *last, void *tape, size_t tape_bytes, void *stream);
+
+/* Backward: the gradient of sum(o*dO) + sum(last*dlast). q, k, lengths, scale
+ * and the tape as in / from the forward; dO [B,T,N,Dv] and dlast
+ * [B,1,N,Dk,Dv] fp32 may be NULL (zero). Outputs dq, dk [B,T,Nk,Dk] (sums over
+ * the heads that share them, in the heads' order), dv [B,T,N,Dv], dg, dbeta
+ * [B,T,N] fp32, dstate0 [B,1,N,Dk,Dv] fp32 or NULL. Errors: as the forward. */
+int rnn_delta_bwd(const rnn_delta_dims_t *dims, const void *q, const void *k, const int *lengths, float scale,
+                  const void *tape, size_t tape_bytes, const void *dO, const void *dlast, void *dq, void *dk, void *dv,
+                  void *dg, void *dbeta, void *dstate0, void *workspace, size_t ws_bytes, void *stream);
+
+/* One step of `rows` sequences whose states live in a pool [slots,N,Dk,Dv]
+ * fp32: q, k [rows,Nk,Dk], v [rows,N,Dv], g, beta [rows,N] fp32, o [rows,N,Dv].
+ * slot, pool_out and status as for rnn_gated_step.
+ * Errors: RNN_EINVAL, RNN_ECUDA. */
+int rnn_delta_step(int rows, int slots, int Nk, int N, int Dk, int Dv, int dtype, const void *q, const void *k,
+                   const void *v, const void *g, const void *beta, const int *slot, const void *pool, void *pool_out,
+                   float scale, void *o, void *status, void *stream);
+
 /* ---- 8-bit activation checkpoints ----------------------------------------------- */
 /* Packs x [rows][cols] (dtype) into int8 q [rows][cols] and one scale byte per
  * RNN_ACT_BLOCK rows of a column, scales [ceil(rows/32)][cols]

@@ -20,6 +20,7 @@ WS_FWD, WS_BWD, WS_BWD_RECOMPUTE = 0, 1, 2
 GATED_FUNCTIONS = {"linear": 0, "linear_coupled": 1}
 CHECKPOINTS = {None: 0, "int8": 1}
 ACT_BLOCK = 32  # rows that share a scale in an 8-bit checkpoint
+DELTA_MAX_D = 256  # the delta rule's largest Dk and Dv
 
 EXPORTS = ["rnn_num_gates", "rnn_num_states", "rnn_tape_size", "rnn_workspace_size", "rnn_fwd",
            "rnn_bwd", "rnn_check_status", "rnn_plan_describe", "rnn_strerror", "rnn_kernel_launches",
@@ -27,7 +28,8 @@ EXPORTS = ["rnn_num_gates", "rnn_num_states", "rnn_tape_size", "rnn_workspace_si
            "rnn_debug_inject_wait", "rnn_plan_set_limits", "rnn_die_layout", "rnn_die_plan_for",
            "rnn_gated_num_gates", "rnn_gated_tape_size", "rnn_gated_workspace_size", "rnn_gated_fwd",
            "rnn_gated_bwd", "rnn_gated_step", "rnn_act_scale_bytes", "rnn_act_pack", "rnn_act_unpack",
-           "rnn_embed_bwd_workspace_size", "rnn_embed_fwd", "rnn_embed_bwd"]
+           "rnn_embed_bwd_workspace_size", "rnn_embed_fwd", "rnn_embed_bwd", "rnn_delta_tape_size",
+           "rnn_delta_bwd_workspace_size", "rnn_delta_fwd", "rnn_delta_bwd", "rnn_delta_step"]
 
 
 class RnnError(RuntimeError):
@@ -44,6 +46,11 @@ class Dims(ctypes.Structure):
 class GatedDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("N", ctypes.c_int), ("D", ctypes.c_int),
                 ("function", ctypes.c_int), ("dtype", ctypes.c_int), ("checkpoint", ctypes.c_int)]
+
+
+class DeltaDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("Nk", ctypes.c_int), ("N", ctypes.c_int),
+                ("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -88,13 +95,18 @@ def load(path: str | None = None):
             lib.rnn_input_proj_fwd.argtypes = [i, i, i] + [vp] * 5 + [sz, vp]
             lib.rnn_input_proj_bwd.argtypes = [i, i, i] + [vp] * 7 + [sz, vp]
             gp, ll, f = ctypes.POINTER(GatedDims), ctypes.c_longlong, ctypes.c_float
+            ep = ctypes.POINTER(DeltaDims)
             for name, args in (("rnn_gated_num_gates", [i]), ("rnn_gated_tape_size", [gp]),
                                ("rnn_gated_workspace_size", [gp, i]), ("rnn_gated_fwd", [gp] + [vp] * 9 + [sz, vp]),
                                ("rnn_gated_bwd", [gp] + [vp] * 11 + [sz, vp]), ("rnn_gated_step", [i] * 6 + [vp] * 8),
                                ("rnn_act_scale_bytes", [ll, i]), ("rnn_act_pack", [ll, i, i] + [vp] * 4),
                                ("rnn_act_unpack", [ll, i, i] + [vp] * 4), ("rnn_embed_bwd_workspace_size", [ll, i, i]),
                                ("rnn_embed_fwd", [ll, i, i, i, i, vp, vp, f, vp, vp, vp]),
-                               ("rnn_embed_bwd", [ll, i, i, i, i, vp, ll, vp, f, vp, vp, sz, vp])):
+                               ("rnn_embed_bwd", [ll, i, i, i, i, vp, ll, vp, f, vp, vp, sz, vp]),
+                               ("rnn_delta_tape_size", [ep]), ("rnn_delta_bwd_workspace_size", [ep]),
+                               ("rnn_delta_fwd", [ep] + [vp] * 8 + [f, vp, vp, vp, sz, vp]),
+                               ("rnn_delta_bwd", [ep, vp, vp, vp, f, vp, sz] + [vp] * 9 + [sz, vp]),
+                               ("rnn_delta_step", [i] * 7 + [vp] * 8 + [f, vp, vp, vp])):
                 getattr(lib, name).argtypes = args
                 if name.endswith(("_size", "_bytes")):
                     getattr(lib, name).restype = sz
@@ -175,6 +187,7 @@ def rnn_plan_set_limits(sms: int = 0, smem_per_cta: int = 227 * 1024, max_cluste
     """Plan for a stated device (sms > 0) or the current one (sms <= 0)."""
     _gated_plans.clear()
     _embed_sizes.clear()
+    _delta_plans.clear()
     return _check(load().rnn_plan_set_limits(int(sms), int(smem_per_cta), int(max_cluster)),
                   "rnn_plan_set_limits")
 
@@ -389,6 +402,69 @@ def rnn_gated_step(rows, slots, N, D, function, dtype, Wx, b, slot, pool, pool_o
         pool.data_ptr(), pool_out.data_ptr(), h.data_ptr(), None if status is None else status.data_ptr(),
         _raw_stream(h, stream))
     return rc if rc == RNN_OK else _check(rc, "rnn_gated_step")
+
+
+# ---- gated delta rule ----------------------------------------------------------------
+def make_delta_dims(B, T, Nk, N, Dk, Dv, dtype=torch.bfloat16) -> DeltaDims:
+    dt = DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return DeltaDims(*(_int32(int(v)) for v in (B, T, Nk, N, Dk, Dv)), dt)
+
+
+_delta_plans: dict = {}
+
+
+def delta_plan(B, T, Nk, N, Dk, Dv, dtype, device):
+    """(dims, tape bytes, backward workspace bytes), kept per dims and device: the
+    sizes follow from the current device, which is `device`."""
+    key = (B, T, Nk, N, Dk, Dv, dtype, device)
+    plan = _delta_plans.get(key)
+    if plan is None:
+        dims = make_delta_dims(*key[:-1])
+        if len(_delta_plans) >= 4096:
+            _delta_plans.clear()
+        plan = _delta_plans[key] = (dims, rnn_delta_tape_size(dims), rnn_delta_bwd_workspace_size(dims))
+    return plan
+
+
+def rnn_delta_tape_size(dims: DeltaDims) -> int:
+    return _quick().rnn_delta_tape_size(ctypes.byref(dims))
+
+
+def rnn_delta_bwd_workspace_size(dims: DeltaDims) -> int:
+    return _quick().rnn_delta_bwd_workspace_size(ctypes.byref(dims))
+
+
+def rnn_delta_fwd(dims: DeltaDims, q, k, v, g, beta, state0, reset, lengths, scale: float, o, last, tape,
+                  stream=None) -> int:
+    ptr, size = _ws(tape)
+    rc = _quick().rnn_delta_fwd(
+        ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+        None if state0 is None else state0.data_ptr(), None if reset is None else reset.data_ptr(),
+        None if lengths is None else lengths.data_ptr(), scale, o.data_ptr(), None if last is None else last.data_ptr(),
+        ptr, size, _raw_stream(o, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_delta_fwd")
+
+
+def rnn_delta_bwd(dims: DeltaDims, q, k, lengths, scale: float, tape, dO, dlast, dq, dk, dv, dg, dbeta, dstate0,
+                  workspace, stream=None) -> int:
+    tptr, tsize = _ws(tape)
+    ptr, size = _ws(workspace)
+    rc = _quick().rnn_delta_bwd(
+        ctypes.byref(dims), q.data_ptr(), k.data_ptr(), None if lengths is None else lengths.data_ptr(), scale, tptr,
+        tsize, None if dO is None else dO.data_ptr(), None if dlast is None else dlast.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), None if dstate0 is None else dstate0.data_ptr(),
+        ptr, size, _raw_stream(tape, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_delta_bwd")
+
+
+def rnn_delta_step(rows, slots, Nk, N, Dk, Dv, q, k, v, g, beta, slot, pool, pool_out, scale: float, o, status=None,
+                   stream=None) -> int:
+    rc = _quick().rnn_delta_step(
+        _int32(rows), _int32(slots), _int32(Nk), _int32(N), _int32(Dk), _int32(Dv), DTYPES[q.dtype], q.data_ptr(),
+        k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), None if slot is None else slot.data_ptr(),
+        pool.data_ptr(), pool_out.data_ptr(), scale, o.data_ptr(), None if status is None else status.data_ptr(),
+        _raw_stream(o, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_delta_step")
 
 
 # ---- 8-bit activation checkpoints ------------------------------------------------------

@@ -1,0 +1,289 @@
+// Gated delta rule: C entry points, sizes, and the single-token step on a pool
+// of states (include/rnn.h).
+#include <limits.h>
+#include <stdio.h>
+
+#include "delta.h"
+#include "kernels.cuh"
+#include "rnn.h"
+
+namespace rnn {
+namespace {
+
+// ---- one step -------------------------------------------------------------------
+struct StepArgs {
+  int rows, slots, Nk, N, Dk, Dv, tiles;
+  const void *q, *k, *v;
+  const float *g, *beta;
+  const int* slot;
+  const float* pool;
+  float* out;
+  float scale;
+  void* o;
+  unsigned* status;
+};
+
+// A CTA takes 32 columns of one row's and head's state: the state is read once
+// into registers (8 rows of 4 columns a thread, or 32 rows of one where rows are
+// not whole 16-byte vectors), k^T S and q^T S are summed over the CTA, and
+// o = q^T S' = a q^T S + (q.k) u needs no second pass before the new state is
+// written. Bound by memory: 8 bytes a state element.
+template <typename T, int VEC> __global__ void __launch_bounds__(256) delta_step_kernel(StepArgs p) {
+  constexpr int CL = 32 / VEC, RG = 256 / CL, NR = 256 / RG;  // column lanes, row groups, rows a thread
+  __shared__ float ks[256], qs[256], red[8][2][32], dot[8], us[32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile = (int)(blockIdx.x % p.tiles), mn = (int)(blockIdx.x / p.tiles), n = mn % p.N, m = mn / p.N;
+  const int c0 = tile * 32, cols = min(32, p.Dv - c0);
+  const int slot = p.slot ? __ldg(p.slot + m) : m;
+  T* o = (T*)p.o + ((size_t)m * p.N + n) * p.Dv + c0;
+  if (slot < 0 || slot >= p.slots) {
+    if (tid < cols) o[tid] = from_f<T>(0.0f);
+    if (slot >= p.slots && tile == 0 && n == 0 && tid == 0 && p.status) atomicOr(p.status, STATUS_RANGE);
+    return;
+  }
+  const int cl = tid % CL, rg = tid / CL, c = cl * VEC;
+  const size_t at = (((size_t)slot * p.N + n) * p.Dk) * p.Dv + c0 + c;
+  float s[NR][VEC];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int r = rg + RG * i;
+    const bool on = r < p.Dk && c < cols;
+    if constexpr (VEC == 4) {
+      const float4 x = on ? __ldcs((const float4*)(p.pool + at + (size_t)r * p.Dv)) : make_float4(0, 0, 0, 0);
+      s[i][0] = x.x, s[i][1] = x.y, s[i][2] = x.z, s[i][3] = x.w;
+    } else {
+      s[i][0] = on ? __ldcs(p.pool + at + (size_t)r * p.Dv) : 0.0f;
+    }
+  }
+  const size_t kat = ((size_t)m * p.Nk + n / (p.N / p.Nk)) * p.Dk;
+  float kv = 0.0f, qv = 0.0f;
+  if (tid < p.Dk) {
+    kv = to_f(((const T*)p.k)[kat + tid]);
+    qv = to_f(((const T*)p.q)[kat + tid]);
+  }
+  ks[tid] = kv;
+  qs[tid] = qv;
+  float d = kv * qv;
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
+  if (lane == 0) dot[warp] = d;
+  const float decay = expf(p.g[(size_t)m * p.N + n]);
+  __syncthreads();
+  float sk[VEC] = {}, sq[VEC] = {};
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int r = rg + RG * i;
+    const float kr = ks[r], qr = qs[r];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      s[i][e] = decay != 0.0f ? decay * s[i][e] : 0.0f;  // nothing is left of the state, whatever it holds
+      sk[e] += kr * s[i][e];
+      sq[e] += qr * s[i][e];
+    }
+  }
+  if constexpr (CL < 32) {  // the warp's row groups
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+#pragma unroll
+      for (int k = CL; k < 32; k <<= 1) {
+        sk[e] += __shfl_xor_sync(0xffffffffu, sk[e], k);
+        sq[e] += __shfl_xor_sync(0xffffffffu, sq[e], k);
+      }
+  }
+  if (lane < CL) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      red[warp][0][c + e] = sk[e];
+      red[warp][1][c + e] = sq[e];
+    }
+  }
+  __syncthreads();
+  if (tid < 32) {
+    float x = 0.0f, y = 0.0f, qk = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      x += red[w][0][tid];
+      y += red[w][1][tid];
+      qk += dot[w];
+    }
+    float u = 0.0f;
+    if (tid < cols) {
+      u = p.beta[(size_t)m * p.N + n] * (to_f(((const T*)p.v)[((size_t)m * p.N + n) * p.Dv + c0 + tid]) - x);
+      o[tid] = from_f<T>(p.scale * (y + qk * u));
+    }
+    us[tid] = u;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int r = rg + RG * i;
+    if (r >= p.Dk || c >= cols) continue;
+    const float kr = ks[r];
+    float* w = p.out + at + (size_t)r * p.Dv;
+    if constexpr (VEC == 4)
+      __stcs((float4*)w, make_float4(s[i][0] + kr * us[c], s[i][1] + kr * us[c + 1], s[i][2] + kr * us[c + 2],
+                                     s[i][3] + kr * us[c + 3]));
+    else
+      __stcs(w, s[i][0] + kr * us[c]);
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return RNN_OK;
+  fprintf(stderr, "librnn_gb300: CUDA error: %s\n", cudaGetErrorString(e));
+  return RNN_ECUDA;
+}
+bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct DeltaSizes {
+  bool bf;
+  int C, NP, BV, DKP, nvt;
+  long long nc, items;
+  size_t rec, tri, S, Z;  // bytes of the tape's parts
+  size_t tape, part, bwd;
+};
+
+bool delta_heads_ok(int Nk, int N, int Dk, int Dv, int dtype) {
+  return Nk >= 1 && N >= Nk && N <= 65536 && N % Nk == 0 && Dk >= 1 && Dk <= RNN_DELTA_MAX_D && Dv >= 1 &&
+         Dv <= RNN_DELTA_MAX_D && (dtype == RNN_F32 || dtype == RNN_BF16);
+}
+
+bool delta_sizes(const rnn_delta_dims_t* d, DeltaSizes* z) {
+  if (!d || d->B < 1 || d->T < 0 || d->T > INT_MAX - 64 || !delta_heads_ok(d->Nk, d->N, d->Dk, d->Dv, d->dtype)) return false;
+  z->bf = d->dtype == RNN_BF16;
+  z->C = z->bf ? DeltaCfg<bf16>::C : DeltaCfg<float>::C;
+  z->NP = z->bf ? DeltaCfg<bf16>::NP : DeltaCfg<float>::NP;
+  z->DKP = (d->Dk + 15) / 16 * 16;
+  z->BV = delta_bv(z->bf, d->B, d->N, d->Dv, z->DKP, device_sms());
+  z->nvt = (d->Dv + z->BV - 1) / z->BV;
+  z->nc = ((long long)d->T + z->C - 1) / z->C;
+  z->items = z->nc * d->B * d->N;
+  // the kernels count the items' tiles and the heads' tiles in 32 bits
+  if (z->items * z->nvt > INT_MAX || (long long)d->B * d->N * z->nvt > INT_MAX) return false;
+  const size_t n = (size_t)z->items;
+  z->rec = up256(n * REC_N * z->C * 4);
+  z->tri = up256(n * z->NP * z->C * z->C * 2);
+  z->S = up256(n * z->nvt * z->NP * z->DKP * z->BV * 2);
+  z->Z = up256(n * z->nvt * z->NP * z->C * z->BV * 2);
+  z->tape = z->rec + 2 * z->tri + z->S + z->Z;
+  z->part = d->N != d->Nk ? up256((size_t)d->B * d->T * d->N * d->Dk * 4) : 0;
+  z->bwd = z->S + z->Z + 2 * z->part;
+  return true;
+}
+
+DeltaArgs delta_args(const rnn_delta_dims_t* d, const DeltaSizes& z, const void* tape) {
+  DeltaArgs a{};
+  a.B = d->B; a.T = d->T; a.Nk = d->Nk; a.N = d->N; a.Dk = d->Dk; a.Dv = d->Dv;
+  a.DKP = z.DKP; a.nvt = z.nvt; a.nc = (int)z.nc;
+  char* t = (char*)tape;
+  a.rec = (float*)t;
+  a.tm = (bf16*)(t + z.rec);
+  a.pm = (bf16*)(t + z.rec + z.tri);
+  a.S = (bf16*)(t + z.rec + 2 * z.tri);
+  a.Z = (bf16*)(t + z.rec + 2 * z.tri + z.S);
+  return a;
+}
+
+}  // namespace
+}  // namespace rnn
+
+using namespace rnn;
+
+extern "C" {
+
+size_t rnn_delta_tape_size(const rnn_delta_dims_t* d) {
+  DeltaSizes z;
+  return delta_sizes(d, &z) ? 256 + z.tape : 0;
+}
+
+size_t rnn_delta_bwd_workspace_size(const rnn_delta_dims_t* d) {
+  DeltaSizes z;
+  return delta_sizes(d, &z) ? 256 + z.bwd : 0;
+}
+
+int rnn_delta_fwd(const rnn_delta_dims_t* d, const void* q, const void* k, const void* v, const void* g,
+                  const void* beta, const void* state0, const unsigned char* reset, const int* lengths, float scale,
+                  void* o, void* last, void* tape, size_t tape_bytes, void* stream) {
+  DeltaSizes z;
+  if (!delta_sizes(d, &z) || (d->T > 0 && (!q || !k || !v || !g || !beta || !o || !tape))) return RNN_EINVAL;
+  const void* ptrs[] = {q, k, v, g, beta, state0, o, last, tape};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return RNN_EINVAL;
+  if (!al4(lengths)) return RNN_EINVAL;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (d->T == 0) {
+    const size_t bytes = (size_t)d->B * d->N * d->Dk * d->Dv * sizeof(float);
+    if (!last) return RNN_OK;
+    return cuda_status(state0 ? cudaMemcpyAsync(last, state0, bytes, cudaMemcpyDeviceToDevice, st)
+                              : cudaMemsetAsync(last, 0, bytes, st));
+  }
+  if (tape_bytes < 256 + z.tape) return RNN_ENOSPC;
+  DeltaArgs a = delta_args(d, z, tape);
+  a.q = q; a.k = k; a.v = v; a.g = (const float*)g; a.beta = (const float*)beta; a.s0 = (const float*)state0;
+  a.reset = reset; a.lengths = lengths; a.scale = scale; a.o = o; a.last = (float*)last;
+  return cuda_status(delta_fwd_launch(z.bf, z.BV, a, st));
+}
+
+int rnn_delta_bwd(const rnn_delta_dims_t* d, const void* q, const void* k, const int* lengths, float scale,
+                  const void* tape, size_t tape_bytes, const void* dO, const void* dlast, void* dq, void* dk, void* dv,
+                  void* dg, void* dbeta, void* dstate0, void* workspace, size_t ws_bytes, void* stream) {
+  DeltaSizes z;
+  if (!delta_sizes(d, &z)) return RNN_EINVAL;
+  if (d->T > 0 && (!q || !k || !tape || !dq || !dk || !dv || !dg || !dbeta || !workspace)) return RNN_EINVAL;
+  const void* ptrs[] = {q, k, tape, dO, dlast, dq, dk, dv, dg, dbeta, dstate0, workspace};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return RNN_EINVAL;
+  if (!al4(lengths)) return RNN_EINVAL;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (d->T == 0) {
+    const size_t bytes = (size_t)d->B * d->N * d->Dk * d->Dv * sizeof(float);
+    if (!dstate0) return RNN_OK;
+    return cuda_status(dlast ? cudaMemcpyAsync(dstate0, dlast, bytes, cudaMemcpyDeviceToDevice, st)
+                             : cudaMemsetAsync(dstate0, 0, bytes, st));
+  }
+  if (tape_bytes < 256 + z.tape || ws_bytes < 256 + z.bwd) return RNN_ENOSPC;
+  DeltaArgs a = delta_args(d, z, tape);
+  a.q = q; a.k = k; a.lengths = lengths; a.scale = scale;
+  a.dO = dO; a.dlast = (const float*)dlast;
+  a.dq = dq; a.dk = dk; a.dv = dv; a.dg = (float*)dg; a.dbeta = (float*)dbeta; a.ds0 = (float*)dstate0;
+  char* w = (char*)workspace;
+  a.dS = (bf16*)w;
+  a.dY = (bf16*)(w + z.S);
+  if (z.part) {
+    a.pq = (float*)(w + z.S + z.Z);
+    a.pk = (float*)(w + z.S + z.Z + z.part);
+  }
+  return cuda_status(delta_bwd_launch(z.bf, z.BV, a, st));
+}
+
+int rnn_delta_step(int rows, int slots, int Nk, int N, int Dk, int Dv, int dtype, const void* q, const void* k,
+                   const void* v, const void* g, const void* beta, const int* slot, const void* pool, void* pool_out,
+                   float scale, void* o, void* status, void* stream) {
+  if (rows < 0 || slots < 1 || !delta_heads_ok(Nk, N, Dk, Dv, dtype) || (!slot && rows > slots)) return RNN_EINVAL;
+  if (!pool || !pool_out || (rows > 0 && (!q || !k || !v || !g || !beta || !o))) return RNN_EINVAL;
+  const void* ptrs[] = {q, k, v, g, beta, pool, pool_out, o};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return RNN_EINVAL;
+  if (!al4(slot) || !al4(status)) return RNN_EINVAL;
+  const int tiles = (Dv + 31) / 32;
+  if ((long long)rows * N * tiles > INT_MAX) return RNN_EINVAL;
+  if (rows == 0) return RNN_OK;
+  StepArgs a{rows, slots, Nk, N, Dk, Dv, tiles, q, k, v, (const float*)g, (const float*)beta, slot, (const float*)pool,
+             (float*)pool_out, scale, o, (unsigned*)status};
+  const unsigned grid = (unsigned)((long long)rows * N * tiles);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == RNN_BF16) {
+    if (Dv % 4 == 0) delta_step_kernel<bf16, 4><<<grid, 256, 0, st>>>(a);
+    else delta_step_kernel<bf16, 1><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (Dv % 4 == 0) delta_step_kernel<float, 4><<<grid, 256, 0, st>>>(a);
+    else delta_step_kernel<float, 1><<<grid, 256, 0, st>>>(a);
+  }
+  note_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -284,6 +284,48 @@ def _gated_shapes(Wx, b, function, lead):
     return N, D
 
 
+def _marks(reset, lengths, B, T, t, name):
+    """reset and lengths as the library takes them, beside the tensor t called `name`."""
+    if reset is not None:
+        if reset.shape != (B, T):
+            raise ValueError(f"reset must be [B,T]={(B, T)}, got {tuple(reset.shape)}")
+        if reset.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"reset must be bool or uint8, got {reset.dtype}")
+        if reset.device != t.device:
+            raise ValueError(f"reset must be on {name}'s device")
+        reset = reset.contiguous()
+    if lengths is not None:
+        if lengths.shape != (B,):
+            raise ValueError(f"lengths must be [B]={(B,)}, got {tuple(lengths.shape)}")
+        if lengths.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"lengths must be integers, got {lengths.dtype}")
+        if lengths.device != t.device:
+            raise ValueError(f"lengths must be on {name}'s device")
+        if lengths.dtype == torch.int64:
+            lengths = lengths.clamp(0, T).to(torch.int32)
+        lengths = lengths.contiguous()
+    return reset, lengths
+
+
+def _check_pool(pools, slots, M, shape, names, t, name):
+    """The state pools ([P, *shape] fp32) and slots of M rows, beside the tensor t called `name`."""
+    dev = t.get_device()
+    for p in pools:
+        if p.dtype != torch.float32:
+            raise TypeError(f"the pool must be float32, got {p.dtype}")
+        if p.dim() != len(shape) + 1 or p.shape != (pools[0].shape[0], *shape):
+            raise ValueError(f"the pool must be [P,{names}]=[P,{','.join(map(str, shape))}], got {tuple(p.shape)}")
+        if not p.is_contiguous() or p.data_ptr() % 16 or p.get_device() != dev:
+            raise ValueError(f"the pool must be contiguous, 16-byte aligned and on {name}'s device")
+    P = pools[0].shape[0]
+    if slots is None:
+        if M > P:
+            raise ValueError(f"{M} rows need as many slots, the pool has {P}")
+    elif slots.shape != (M,) or slots.dtype != torch.int32 or slots.get_device() != dev:
+        raise ValueError(f"slots must be [M]=[{M}] int32 on {name}'s device")
+    return P
+
+
 def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, lengths=None, checkpoint=None, status=None):
     """Gated linear scan: the recurrence without R, linear in its state.
 
@@ -314,24 +356,7 @@ def gated_scan(Wx, b=None, state=None, function: str = "linear", reset=None, len
             raise ValueError("state must be on Wx's device")
         if state.dtype != torch.float32:
             state = state.float()
-    if reset is not None:
-        if reset.shape != (B, T):
-            raise ValueError(f"reset must be [B,T]={(B, T)}, got {tuple(reset.shape)}")
-        if reset.dtype not in (torch.bool, torch.uint8):
-            raise TypeError(f"reset must be bool or uint8, got {reset.dtype}")
-        if reset.device != Wx.device:
-            raise ValueError("reset must be on Wx's device")
-        reset = reset.contiguous()
-    if lengths is not None:
-        if lengths.shape != (B,):
-            raise ValueError(f"lengths must be [B]={(B,)}, got {tuple(lengths.shape)}")
-        if lengths.dtype not in (torch.int32, torch.int64):
-            raise TypeError(f"lengths must be integers, got {lengths.dtype}")
-        if lengths.device != Wx.device:
-            raise ValueError("lengths must be on Wx's device")
-        if lengths.dtype == torch.int64:
-            lengths = lengths.clamp(0, T).to(torch.int32)
-        lengths = lengths.contiguous()
+    reset, lengths = _marks(reset, lengths, B, T, Wx, "Wx")
     if _tracked(Wx, b, state):
         return _GatedFn.apply(Wx, b, state, function, reset, lengths, checkpoint, status)
     return _gated_run(Wx, b, state, function, reset, lengths, checkpoint, status, False)[:2]
@@ -350,21 +375,8 @@ def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=
     N, D = _gated_shapes(Wx, b, function, 1)
     _check_status(status, Wx)
     M = Wx.shape[0]
-    dev = Wx.get_device()
-    for p in (pool,) if pool_out is None else (pool, pool_out):
-        if p.dtype != torch.float32:
-            raise TypeError(f"the pool must be float32, got {p.dtype}")
-        if p.dim() != 3 or p.shape != (pool.shape[0], N, D):
-            raise ValueError(f"the pool must be [P,N,D]=[P,{N},{D}], got {tuple(p.shape)}")
-        if not p.is_contiguous() or p.data_ptr() % 16 or p.get_device() != dev:
-            raise ValueError("the pool must be contiguous, 16-byte aligned and on Wx's device")
-    P = pool.shape[0]
-    if slots is None:
-        if M > P:
-            raise ValueError(f"{M} rows need as many slots, the pool has {P}")
-    else:
-        if slots.shape != (M,) or slots.dtype != torch.int32 or slots.get_device() != dev:
-            raise ValueError(f"slots must be [M]=[{M}] int32 on Wx's device")
+    P = _check_pool((pool,) if pool_out is None else (pool, pool_out), slots, M, (N, D), "N,D", Wx, "Wx")
+    if slots is not None:
         slots = slots.contiguous()
     h = Wx.new_empty((M, N, D))
     out = pool if pool_out is None else pool_out
@@ -372,6 +384,140 @@ def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=
     if not out.is_inference():  # a graph that saved the old states has to learn of the write
         torch.autograd.graph.increment_version(out)
     return h
+
+
+# ---- gated delta rule ----------------------------------------------------------------
+def _delta_run(q, k, v, g, beta, state, reset, lengths, scale):
+    """(o, last, q and k as the library took them, plan, tape)."""
+    B, T, Nk, Dk = q.shape
+    N, Dv = v.shape[2:]
+    plan = _lib.delta_plan(B, T, Nk, N, Dk, Dv, q.dtype, _lib.check_device(q))
+    q, k, v, g, beta, state = (_dense(t) for t in (q, k, v, g, beta, state))
+    o = torch.empty_like(v)
+    last = torch.empty((B, 1, N, Dk, Dv), dtype=torch.float32, device=v.device)
+    tape = torch.empty(plan[1], dtype=torch.uint8, device=v.device)
+    _lib.rnn_delta_fwd(plan[0], q, k, v, g, beta, state, reset, lengths, scale, o, last, tape)
+    return o, last, q, k, plan, tape
+
+
+class _DeltaFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, state, reset, lengths, scale):
+        o, last, q, k, ctx.plan, tape = _delta_run(q, k, v, g, beta, state, reset, lengths, scale)
+        ctx.scale, ctx.shape = scale, v.shape
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(q, k, lengths, tape)
+        return o, last
+
+    @staticmethod
+    def backward(ctx, do, dlast):
+        return (_delta_bwd_once if torch.is_grad_enabled() else _delta_bwd)(ctx, do, dlast)
+
+
+def _delta_bwd(ctx, do, dlast):
+    _first_order(do, dlast)
+    q, k, lengths, tape = ctx.saved_tensors
+    dims, _, size = ctx.plan
+    B, T, N, Dv = ctx.shape
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), q.new_empty(ctx.shape)
+    dg, dbeta = (torch.empty((B, T, N), dtype=torch.float32, device=q.device) for _ in range(2))
+    ds = torch.empty((B, 1, N, q.shape[3], Dv), dtype=torch.float32, device=q.device) if ctx.needs_input_grad[5] else None
+    ws = torch.empty(size, dtype=torch.uint8, device=q.device)
+    _lib.rnn_delta_bwd(dims, q, k, lengths, ctx.scale, tape, _dense(do), _dense(dlast), dq, dk, dv, dg, dbeta, ds, ws)
+    return dq, dk, dv, dg, dbeta, ds, None, None, None
+
+
+_delta_bwd_once = once_differentiable(_delta_bwd)
+
+
+def _delta_shapes(q, k, v, g, beta, lead):
+    """Checks the inputs of the delta rule, whose leading axes are lead; returns (Nk, N, Dk, Dv)."""
+    n = len(lead)
+    if q.dtype not in _lib.DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    if q.dim() != n + 2 or v.dim() != n + 2:
+        raise ValueError(f"q and v must have {n + 2} dimensions, got shapes {tuple(q.shape)} and {tuple(v.shape)}")
+    (Nk, Dk), (N, Dv) = q.shape[n:], v.shape[n:]
+    if q.shape[:n] != lead or k.shape != q.shape or v.shape[:n] != lead:
+        raise ValueError(f"q and k must have one shape and v the same leading axes, got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)} and {tuple(v.shape)}")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError(f"q, k and v must have one dtype, got {q.dtype}, {k.dtype} and {v.dtype}")
+    if Nk < 1 or N < 1 or N % Nk:
+        raise ValueError(f"v's {N} heads must be a multiple of q's and k's {Nk}")
+    if not (1 <= Dk <= _lib.DELTA_MAX_D and 1 <= Dv <= _lib.DELTA_MAX_D):
+        raise ValueError(f"heads of 1 to {_lib.DELTA_MAX_D} channels, got {Dk} and {Dv}")
+    for t, name in ((g, "g"), (beta, "beta")):
+        if t.shape != (*lead, N):
+            raise ValueError(f"{name} must be {(*lead, N)}, got {tuple(t.shape)}")
+        if t.dtype not in (torch.float32, q.dtype):
+            raise TypeError(f"{name} must be float32 or {q.dtype}, got {t.dtype}")
+    for t, name in ((k, "k"), (v, "v"), (g, "g"), (beta, "beta")):
+        if t.get_device() != q.get_device():
+            raise ValueError(f"{name} must be on q's device")
+    return Nk, N, Dk, Dv
+
+
+def gated_delta(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=None):
+    """Gated delta rule: a scan whose state is a matrix S [Dk,Dv] per head,
+    u_t = beta_t (v_t - a_t S_{t-1}^T k_t), S_t = a_t S_{t-1} + k_t u_t^T,
+    o_t = scale S_t^T q_t, a_t = exp(g_t).
+
+    q, k [B,T,Nk,Dk] and v [B,T,N,Dv] (bf16 or fp32; N a multiple of Nk: v head n
+    goes with q and k head n // (N // Nk); Dk and Dv up to 256), g and beta
+    [B,T,N] (fp32 or q's dtype), state [B,1,N,Dk,Dv] or None (zeros), scale None =
+    Dk ** -0.5. Keys are taken as they are: beta |k|^2 past 2 lets the state
+    grow.
+    reset [B,T] (bool or uint8): S_{t-1} counts as zero at the marked steps
+    (packed documents), whatever it holds. lengths [B]: row b has lengths[b]
+    steps; past them nothing is looked at, o is zero and the state is kept.
+    Returns (o [B,T,N,Dv], last [B,1,N,Dk,Dv]: the state after the last step,
+    fp32). Differentiable in q, k, v, g, beta and state. An infinity or a NaN in
+    an input may reach every step of its row and head."""
+    _on_gpu(q, "gated_delta")
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B,T,Nk,Dk], got shape {tuple(q.shape)}")
+    B, T = q.shape[:2]
+    _, N, Dk, Dv = _delta_shapes(q, k, v, g, beta, (B, T))
+    if state is not None:
+        if state.shape != (B, 1, N, Dk, Dv):
+            raise ValueError(f"state must be [B,1,N,Dk,Dv]={(B, 1, N, Dk, Dv)}, got {tuple(state.shape)}")
+        if state.get_device() != q.get_device():
+            raise ValueError("state must be on q's device")
+        if state.dtype != torch.float32:
+            state = state.float()
+    reset, lengths = _marks(reset, lengths, B, T, q, "q")
+    scale = Dk ** -0.5 if scale is None else float(scale)
+    if g.dtype != torch.float32:
+        g = g.float()
+    if beta.dtype != torch.float32:
+        beta = beta.float()
+    if _tracked(q, k, v, g, beta, state):
+        return _DeltaFn.apply(q, k, v, g, beta, state, reset, lengths, scale)
+    return _delta_run(q, k, v, g, beta, state, reset, lengths, scale)[:2]
+
+
+def gated_delta_step(q, k, v, g, beta, pool, slots=None, scale=None, pool_out=None, status=None):
+    """One step of running sequences whose states live in a pool (serving; not
+    differentiable). q, k [M,Nk,Dk], v [M,N,Dv], g and beta [M,N] as for
+    gated_delta, pool [P,N,Dk,Dv] fp32; slots, pool_out and status as for
+    gated_scan_step. Returns o [M,N,Dv]."""
+    _on_gpu(q, "gated_delta_step")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [M,Nk,Dk], got shape {tuple(q.shape)}")
+    M = q.shape[0]
+    Nk, N, Dk, Dv = _delta_shapes(q, k, v, g, beta, (M,))
+    _check_status(status, q)
+    P = _check_pool((pool,) if pool_out is None else (pool, pool_out), slots, M, (N, Dk, Dv), "N,Dk,Dv", q, "q")
+    if slots is not None:
+        slots = slots.contiguous()
+    o = v.new_empty((M, N, Dv))
+    out = pool if pool_out is None else pool_out
+    _lib.rnn_delta_step(M, P, Nk, N, Dk, Dv, _dense(q), _dense(k), _dense(v), _dense(g.float()), _dense(beta.float()),
+                        slots, pool, out, Dk ** -0.5 if scale is None else float(scale), o, status)
+    if not out.is_inference():  # a graph that saved the old states has to learn of the write
+        torch.autograd.graph.increment_version(out)
+    return o
 
 
 # ---- 8-bit activation checkpoints -----------------------------------------------------
