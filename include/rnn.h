@@ -442,6 +442,28 @@ int rnn_delta_step(int rows, int slots, int Nk, int N, int Dk, int Dv, int dtype
                    const void *v, const void *g, const void *beta, const int *slot, const void *pool, void *pool_out,
                    float scale, void *o, void *status, void *stream);
 
+/* ---- group norm with an activation, channels last ---------------------------------- */
+/*
+ * x [rows][groups][width] (dtype), statistics over the width channels of one
+ * group of one row (a head of a scan's output at one step; groups = 1: a layer
+ * norm):
+ *   n = (x - m) / sqrt(var + eps), t = n * w + b, y = act(t)
+ * or, with a gate z of x's shape, y = t * act(z). centered = 0 leaves the mean
+ * out (m = 0, var the mean square). w, b [groups][width] or NULL (1, 0).
+ * rows < 2^40, width <= RNN_NORM_MAX_WIDTH, groups <= 65535, groups width <= 2^28.
+ * The backward writes dx, dgate (with a gate), and dw, db (each may be NULL; the
+ * sums over rows run in a fixed order), for which alone it needs the workspace.
+ * Errors: RNN_EINVAL, RNN_ENOSPC, RNN_ECUDA.
+ */
+typedef enum { RNN_ACT_NONE = 0, RNN_ACT_SILU = 1, RNN_ACT_SIGMOID = 2 } rnn_activation_t;
+#define RNN_NORM_MAX_WIDTH 14336
+size_t rnn_group_norm_workspace_size(long long rows, int groups, int width, int dtype); /* 0 for invalid sizes */
+int rnn_group_norm_fwd(long long rows, int groups, int width, int dtype, int act, int centered, float eps,
+                       const void *x, const void *w, const void *b, const void *gate, void *y, void *stream);
+int rnn_group_norm_bwd(long long rows, int groups, int width, int dtype, int act, int centered, float eps,
+                       const void *x, const void *w, const void *b, const void *gate, const void *dy, void *dx,
+                       void *dgate, void *dw, void *db, void *workspace, size_t ws_bytes, void *stream);
+
 /* ---- 8-bit activation checkpoints ----------------------------------------------- */
 /* Packs x [rows][cols] (dtype) into int8 q [rows][cols] and one scale byte per
  * RNN_ACT_BLOCK rows of a column, scales [ceil(rows/32)][cols]

@@ -88,7 +88,8 @@ def _act(x, activation):
 
 
 def group_norm(x, groups, weight=None, bias=None, gate=None, activation=None, eps=1e-5, centered=True, dy=None):
-    """x [..., C] -> y, or with dy (y, dx, dgate, dweight, dbias)."""
+    """x [..., C] -> y, or with dy (y, dx, dgate, dweight, dbias, the largest term
+    of dx's difference)."""
     x, weight, bias, gate, dy = (f64(t) for t in (x, weight, bias, gate, dy))
     C = x.shape[-1]
     flat = x.reshape(-1, groups, C // groups)
@@ -108,4 +109,5 @@ def group_norm(x, groups, weight=None, bias=None, gate=None, activation=None, ep
     if centered:
         dx = dx - dn.mean(2, keepdims=True)
     lead = tuple(range(x.ndim - 1))
-    return y, (dx * r).reshape(x.shape), dgate, (dt * n.reshape(x.shape)).sum(lead), dt.sum(lead)
+    return y, (dx * r).reshape(x.shape), dgate, (dt * n.reshape(x.shape)).sum(lead), dt.sum(lead), np.abs(
+        dn * r).max(initial=0.0)

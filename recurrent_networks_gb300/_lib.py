@@ -20,6 +20,8 @@ WS_FWD, WS_BWD, WS_BWD_RECOMPUTE = 0, 1, 2
 GATED_FUNCTIONS = {"linear": 0, "linear_coupled": 1}
 CHECKPOINTS = {None: 0, "int8": 1}
 ACT_BLOCK = 32  # rows that share a scale in an 8-bit checkpoint
+ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
+NORM_MAX_WIDTH = 14336  # the group norm's widest group
 DELTA_MAX_D = 256  # the delta rule's largest Dk and Dv
 
 EXPORTS = ["rnn_num_gates", "rnn_num_states", "rnn_tape_size", "rnn_workspace_size", "rnn_fwd",
@@ -29,7 +31,8 @@ EXPORTS = ["rnn_num_gates", "rnn_num_states", "rnn_tape_size", "rnn_workspace_si
            "rnn_gated_num_gates", "rnn_gated_tape_size", "rnn_gated_workspace_size", "rnn_gated_fwd",
            "rnn_gated_bwd", "rnn_gated_step", "rnn_act_scale_bytes", "rnn_act_pack", "rnn_act_unpack",
            "rnn_embed_bwd_workspace_size", "rnn_embed_fwd", "rnn_embed_bwd", "rnn_delta_tape_size",
-           "rnn_delta_bwd_workspace_size", "rnn_delta_fwd", "rnn_delta_bwd", "rnn_delta_step"]
+           "rnn_delta_bwd_workspace_size", "rnn_delta_fwd", "rnn_delta_bwd", "rnn_delta_step",
+           "rnn_group_norm_workspace_size", "rnn_group_norm_fwd", "rnn_group_norm_bwd"]
 
 
 class RnnError(RuntimeError):
@@ -106,7 +109,10 @@ def load(path: str | None = None):
                                ("rnn_delta_tape_size", [ep]), ("rnn_delta_bwd_workspace_size", [ep]),
                                ("rnn_delta_fwd", [ep] + [vp] * 8 + [f, vp, vp, vp, sz, vp]),
                                ("rnn_delta_bwd", [ep, vp, vp, vp, f, vp, sz] + [vp] * 9 + [sz, vp]),
-                               ("rnn_delta_step", [i] * 7 + [vp] * 8 + [f, vp, vp, vp])):
+                               ("rnn_delta_step", [i] * 7 + [vp] * 8 + [f, vp, vp, vp]),
+                               ("rnn_group_norm_workspace_size", [ll, i, i, i]),
+                               ("rnn_group_norm_fwd", [ll, i, i, i, i, i, f] + [vp] * 6),
+                               ("rnn_group_norm_bwd", [ll, i, i, i, i, i, f] + [vp] * 10 + [sz, vp])):
                 getattr(lib, name).argtypes = args
                 if name.endswith(("_size", "_bytes")):
                     getattr(lib, name).restype = sz
@@ -188,6 +194,7 @@ def rnn_plan_set_limits(sms: int = 0, smem_per_cta: int = 227 * 1024, max_cluste
     _gated_plans.clear()
     _embed_sizes.clear()
     _delta_plans.clear()
+    _norm_sizes.clear()
     return _check(load().rnn_plan_set_limits(int(sms), int(smem_per_cta), int(max_cluster)),
                   "rnn_plan_set_limits")
 
@@ -465,6 +472,43 @@ def rnn_delta_step(rows, slots, Nk, N, Dk, Dv, q, k, v, g, beta, slot, pool, poo
         pool.data_ptr(), pool_out.data_ptr(), scale, o.data_ptr(), None if status is None else status.data_ptr(),
         _raw_stream(o, stream))
     return rc if rc == RNN_OK else _check(rc, "rnn_delta_step")
+
+
+# ---- group norm ------------------------------------------------------------------------
+_norm_sizes: dict = {}
+
+
+def rnn_group_norm_workspace_size(rows: int, groups: int, width: int, dtype, device=None) -> int:
+    """Kept per `device`, the current one (None: whichever that is)."""
+    key = (rows, groups, width, dtype, device)
+    size = _norm_sizes.get(key) if device is not None else None
+    if size is None:
+        size = int(_quick().rnn_group_norm_workspace_size(int(rows), _int32(int(groups)), _int32(int(width)), DTYPES[dtype]))
+        if device is not None:
+            if len(_norm_sizes) >= 4096:
+                _norm_sizes.clear()
+            _norm_sizes[key] = size
+    return size
+
+
+def rnn_group_norm_fwd(rows, groups, width, activation, centered, eps, x, w, b, gate, y, stream=None) -> int:
+    rc = _quick().rnn_group_norm_fwd(
+        rows, _int32(groups), _int32(width), DTYPES[x.dtype], ACTIVATIONS[activation], int(centered), eps, x.data_ptr(),
+        None if w is None else w.data_ptr(), None if b is None else b.data_ptr(),
+        None if gate is None else gate.data_ptr(), y.data_ptr(), _raw_stream(x, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_group_norm_fwd")
+
+
+def rnn_group_norm_bwd(rows, groups, width, activation, centered, eps, x, w, b, gate, dy, dx, dgate, dw, db, workspace,
+                       stream=None) -> int:
+    ptr, size = (None, 0) if workspace is None else _ws(workspace)
+    rc = _quick().rnn_group_norm_bwd(
+        rows, _int32(groups), _int32(width), DTYPES[x.dtype], ACTIVATIONS[activation], int(centered), eps, x.data_ptr(),
+        None if w is None else w.data_ptr(), None if b is None else b.data_ptr(),
+        None if gate is None else gate.data_ptr(), dy.data_ptr(), dx.data_ptr(),
+        None if dgate is None else dgate.data_ptr(), None if dw is None else dw.data_ptr(),
+        None if db is None else db.data_ptr(), ptr, size, _raw_stream(x, stream))
+    return rc if rc == RNN_OK else _check(rc, "rnn_group_norm_bwd")
 
 
 # ---- 8-bit activation checkpoints ------------------------------------------------------

@@ -21,7 +21,7 @@
 // The products run on mma.sync with operands in bf16 planes: a value computed
 // in fp32 (S, Y, Z, Tm, ...) is the sum of NP planes, each the rounding of what
 // the planes before it left, and a product takes the plane pairs (i, j) with
-// i + j < NP. Two planes (bf16 storage) hold 2^-17 of a value, three (fp32
+// i + j < NP. Two planes (bf16 storage) hold 2^-16 of a value, three (fp32
 // storage) 2^-24; the inputs q, k, v, dO of bf16 storage are one exact plane.
 #pragma once
 #include <cuda_bf16.h>
@@ -95,7 +95,11 @@ __device__ __forceinline__ Opnd opnd(const bf16* p, int ld, int plane) { return 
 
 // acc[NT] (16 x 8 NT) += A(m0.., :) B(:, n0..) over K (a multiple of 16).
 // A(m, k) is stored [m][k] (AT: [k][m]); B(k, n) is stored [k][n] (BK: [n][k]).
-// PA, PB: planes; the pairs (i, j) with i + j < max(PA, PB) are summed.
+// PA, PB: planes; the pairs (i, j) with i + j < max(PA, PB) are summed. The
+// tensor cores cut an accumulator off at each addition, always towards zero
+// (2^-23 of it), so the large products (0, 0) have an accumulator to themselves
+// and the sum so far joins by a rounded addition: 24 additions of six products
+// into the running state were 7e-6 off after a few chunks of fp32.
 template <int NT, int PA, int PB, bool AT, bool BK>
 __device__ __forceinline__ void mma_acc(float (&acc)[NT][4], const Opnd& A, int m0, const Opnd& B, int n0, int K) {
   constexpr int PT = PA > PB ? PA : PB;
@@ -106,6 +110,14 @@ __device__ __forceinline__ void mma_acc(float (&acc)[NT][4], const Opnd& A, int 
   const int kofs = (id & 1) * 8, nofs = (id >> 1) * 8;
   uint32_t bat = B.at + 2u * (uint32_t)(BK ? (n0 + nofs + r) * B.ld + kofs : (kofs + r) * B.ld + n0 + nofs);
   const uint32_t bstep = BK ? 32u : 32u * B.ld, bpair = BK ? 32u * B.ld : 32u;
+  float hi[NT][4], lo[PT > 1 ? NT : 1][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      hi[t][e] = 0.0f;
+      if constexpr (PT > 1) lo[t][e] = 0.0f;
+    }
 #pragma unroll 2
   for (int k = 0; k < K; k += 16, aat += astep, bat += bstep) {
     uint32_t a[PA][4];
@@ -126,11 +138,23 @@ __device__ __forceinline__ void mma_acc(float (&acc)[NT][4], const Opnd& A, int 
         for (int pa = 0; pa < PA; ++pa) {
           const int pb = s - pa;
           if (pb < 0 || pb >= PB) continue;
-          mma_bf16_16816(acc[2 * j], a[pa], b[pb][0], b[pb][1]);
-          if (2 * j + 1 < NT) mma_bf16_16816(acc[2 * j + 1], a[pa], b[pb][2], b[pb][3]);
+          if constexpr (PT > 1) {
+            mma_bf16_16816(s ? lo[2 * j] : hi[2 * j], a[pa], b[pb][0], b[pb][1]);
+            if (2 * j + 1 < NT) mma_bf16_16816(s ? lo[2 * j + 1] : hi[2 * j + 1], a[pa], b[pb][2], b[pb][3]);
+          } else {
+            mma_bf16_16816(hi[2 * j], a[pa], b[pb][0], b[pb][1]);
+            if (2 * j + 1 < NT) mma_bf16_16816(hi[2 * j + 1], a[pa], b[pb][2], b[pb][3]);
+          }
         }
     }
   }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (PT > 1) acc[t][e] += hi[t][e] + lo[t][e];
+      else acc[t][e] += hi[t][e];
+    }
 }
 template <int NT> __device__ __forceinline__ void zero(float (&acc)[NT][4]) {
 #pragma unroll

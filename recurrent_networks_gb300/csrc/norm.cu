@@ -1,0 +1,511 @@
+// Group norm with an activation, channels last (include/rnn.h): statistics over
+// the W channels of one group of one row,
+//   m = mean x (0 where not centred), r = (mean (x - m)^2 + eps)^-1/2,
+//   n = (x - m) r, t = n w + b, y = act(t), or t act(z) with a gate z.
+// Backward: dt = dy act'(t), or dy act(z) and dz = dy t act'(z); dn = dt w,
+//   dx = r (dn - mean dn - n mean(dn n)) (without mean dn where not centred),
+//   dw = sum over rows of dt n, db of dt.
+// All in fp32. The backward takes the statistics from x again: x is read in any
+// case, and nothing is kept from the forward.
+#include <limits.h>
+#include <stdio.h>
+
+#include "gated.cuh"
+#include "kernels.cuh"
+#include "rnn.h"
+
+namespace rnn {
+namespace {
+
+typedef __nv_bfloat16 bf16;
+
+struct NormArgs {
+  long long rows;
+  int G, W, act, centered;
+  float eps;
+  const void *x, *w, *b, *gate, *dy;
+  void *y, *dx, *dgate;
+  float* part;  // [gridDim.x][2][C]: sums of dt n and dt over a CTA's rows, or null
+  int lanes, gp, rp;  // threads of a group; groups and rows that a CTA takes at once
+};
+
+// VEC values of T at p, 16 bytes at once where VEC > 1
+template <typename T, int VEC> __device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = to_f(p[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 x = *(const float4*)p;
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  } else {
+    const uint4 x = *(const uint4*)p;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+template <typename T, int VEC> __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    p[0] = from_f<T>(v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *(const uint32_t*)&h;
+    }
+    *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The sigmoid: bf16 storage takes the approximate exponential and reciprocal
+// (2^-21 together), fp32 the exact ones.
+template <typename T> __device__ __forceinline__ float sigm(float x) {
+  if constexpr (sizeof(T) == 2) return rcp_fast(1.0f + exp2_fast(-1.4426950408889634f * x));
+  else return 1.0f / (1.0f + expf(-x));
+}
+// act(x) and, for the backward, its slope
+template <typename T> __device__ __forceinline__ float act_of(int act, float x) {
+  if (act == RNN_ACT_NONE) return x;
+  const float s = sigm<T>(x);
+  return act == RNN_ACT_SILU ? x * s : s;
+}
+template <typename T> __device__ __forceinline__ void act_both(int act, float x, float& a, float& slope) {
+  if (act == RNN_ACT_NONE) {
+    a = x;
+    slope = 1.0f;
+    return;
+  }
+  const float s = sigm<T>(x), c = s * (1.0f - s);
+  a = act == RNN_ACT_SILU ? x * s : s;
+  slope = act == RNN_ACT_SILU ? fmaf(x, c, s) : c;
+}
+
+// The sum over a group's threads: a power of two of a warp's lanes, or (MANY)
+// whole warps, whose sums pass through red [8]. A place of red is written again
+// three such sums later, with barriers between.
+template <bool MANY> __device__ __forceinline__ float lane_sum(float v, int lanes, float* red) {
+  if constexpr (!MANY) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  } else {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int warp = threadIdx.x >> 5, n = lanes >> 5, w0 = warp & ~(n - 1);
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int i = 0; i < n; ++i) v += red[w0 + i];
+    return v;
+  }
+}
+
+// What both directions do with a value once the statistics are known.
+template <typename T, bool GATE>
+__device__ __forceinline__ float forward_value(int act, float n, float w, float b, float z) {
+  const float t = fmaf(n, w, b);
+  return GATE ? t * act_of<T>(act, z) : act_of<T>(act, t);
+}
+// dt (returned) and dz
+template <typename T, bool GATE>
+__device__ __forceinline__ float backward_value(int act, float n, float w, float b, float z, float dy, float& dz) {
+  const float t = fmaf(n, w, b);
+  float a, slope;
+  act_both<T>(act, GATE ? z : t, a, slope);
+  dz = dy * t * slope;
+  return GATE ? dy * a : dy * slope;
+}
+
+// Groups of up to 256 * NV vectors: `lanes` threads (a power of two; MANY: of
+// several warps) hold a group's channels in registers. A CTA takes gp groups of
+// rp rows at once, the same groups for all its rows, so that a thread's sums of
+// dw and db are over one set of columns. One pass over the data.
+template <typename T, int VEC, int NV, bool GATE, bool BWD, bool MANY>
+__global__ void __launch_bounds__(256) norm_kernel(NormArgs p) {
+  extern __shared__ float sums[];  // [2][gp * W], BWD with p.part
+  __shared__ float red[4][8];
+  const int li = threadIdx.x % p.lanes, slot = threadIdx.x / p.lanes;
+  const int gi = slot % p.gp, ri = slot / p.gp;
+  const int g = blockIdx.y * p.gp + gi;
+  const bool on = ri < p.rp && g < p.G;
+  const long long C = (long long)p.G * p.W;
+  const float inv = 1.0f / (float)p.W;
+  float w[NV][VEC], b[NV][VEC];
+  bool have[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (li + v * p.lanes) * VEC;
+    have[v] = on && c < p.W;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[v][e] = 1.0f, b[v][e] = 0.0f;
+    if (have[v] && p.w) load_vec<T, VEC>((const T*)p.w + (size_t)g * p.W + c, w[v]);
+    if (have[v] && p.b) load_vec<T, VEC>((const T*)p.b + (size_t)g * p.W + c, b[v]);
+  }
+  float dw[BWD ? NV : 1][VEC], db[BWD ? NV : 1][VEC];
+  if constexpr (BWD) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) dw[v][e] = db[v][e] = 0.0f;
+  }
+  // all threads of a warp stay in the loop: the sums are over the warp's lanes
+  for (long long r0 = (long long)blockIdx.x * p.rp; r0 < p.rows; r0 += (long long)gridDim.x * p.rp) {
+    const long long r = r0 + ri;
+    const bool live = on && r < p.rows;
+    const size_t at = (size_t)(live ? r : 0) * C + (size_t)(on ? g : 0) * p.W;
+    float x[NV][VEC], z[GATE ? NV : 1][VEC], dy[BWD ? NV : 1][VEC];
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (li + v * p.lanes) * VEC;
+      if (live && have[v]) {
+        load_vec<T, VEC>((const T*)p.x + at + c, x[v]);
+        if constexpr (GATE) load_vec<T, VEC>((const T*)p.gate + at + c, z[v]);
+        if constexpr (BWD) load_vec<T, VEC>((const T*)p.dy + at + c, dy[v]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          x[v][e] = 0.0f;
+          if constexpr (GATE) z[v][e] = 0.0f;
+          if constexpr (BWD) dy[v][e] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += x[v][e];
+    }
+    const float mean = p.centered ? lane_sum<MANY>(s, p.lanes, red[0]) * inv : 0.0f;
+    s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        x[v][e] = have[v] ? x[v][e] - mean : 0.0f;
+        s = fmaf(x[v][e], x[v][e], s);
+      }
+    const float rstd = 1.0f / sqrtf(fmaf(lane_sum<MANY>(s, p.lanes, red[1]), inv, p.eps));
+    if constexpr (!BWD) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (!live || !have[v]) continue;
+        float y[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          y[e] = forward_value<T, GATE>(p.act, x[v][e] * rstd, w[v][e], b[v][e], GATE ? z[GATE ? v : 0][e] : 0.0f);
+        store_vec<T, VEC>((T*)p.y + at + (li + v * p.lanes) * VEC, y);
+      }
+    } else {
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float n = x[v][e] * rstd;
+          float dz;
+          const float dt = backward_value<T, GATE>(p.act, n, w[v][e], b[v][e], GATE ? z[GATE ? v : 0][e] : 0.0f, dy[v][e], dz);
+          if constexpr (GATE) z[v][e] = dz;
+          if (live && have[v]) {
+            dw[v][e] = fmaf(dt, n, dw[v][e]);
+            db[v][e] += dt;
+          }
+          x[v][e] = n;
+          const float dn = live && have[v] ? dt * w[v][e] : 0.0f;
+          dy[v][e] = dn;
+          s1 += dn;
+          s2 = fmaf(dn, n, s2);
+        }
+      s1 = p.centered ? lane_sum<MANY>(s1, p.lanes, red[2]) * inv : 0.0f;
+      s2 = lane_sum<MANY>(s2, p.lanes, red[3]) * inv;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (!live || !have[v]) continue;
+        const size_t to = at + (li + v * p.lanes) * VEC;
+        float dx[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dx[e] = rstd * (dy[v][e] - s1 - x[v][e] * s2);
+        store_vec<T, VEC>((T*)p.dx + to, dx);
+        if constexpr (GATE) store_vec<T, VEC>((T*)p.dgate + to, z[v]);
+      }
+    }
+  }
+  if constexpr (BWD) {
+    if (!p.part) return;
+    // the CTA's rows, one after the other, then its sums to its own place
+    const int n = p.gp * p.W;
+    for (int q = 0; q < p.rp; ++q) {
+      if (on && ri == q) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if (!have[v]) continue;
+          const int c = gi * p.W + (li + v * p.lanes) * VEC;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            sums[c + e] = (q ? sums[c + e] : 0.0f) + dw[v][e];
+            sums[n + c + e] = (q ? sums[n + c + e] : 0.0f) + db[v][e];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    const long long c0 = (long long)blockIdx.y * n;
+    for (int c = threadIdx.x; c < n; c += 256)
+      if (c0 + c < C) {
+        p.part[(size_t)blockIdx.x * 2 * C + c0 + c] = sums[c];
+        p.part[((size_t)blockIdx.x * 2 + 1) * C + c0 + c] = sums[n + c];
+      }
+  }
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s += red[i];
+  return s;
+}
+
+// Wider groups, or rows that are not whole vectors: a CTA takes one group, the
+// row in shared memory. dw and db are summed into this CTA's place of p.part.
+template <typename T, bool GATE, bool BWD> __global__ void __launch_bounds__(512) norm_wide_kernel(NormArgs p) {
+  extern __shared__ float sm[];
+  float *xs = sm, *ds = sm + p.W, *dw = sm + 2 * p.W, *db = sm + 3 * p.W;  // ds, dw, db: BWD
+  __shared__ float red[16];
+  const int g = blockIdx.y, W = p.W;
+  const long long C = (long long)p.G * W;
+  const T* w = p.w ? (const T*)p.w + (size_t)g * W : nullptr;
+  const T* b = p.b ? (const T*)p.b + (size_t)g * W : nullptr;
+  const float inv = 1.0f / (float)W;
+  if (BWD && p.part)
+    for (int c = threadIdx.x; c < W; c += 512) dw[c] = db[c] = 0.0f;
+  for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    const size_t at = (size_t)r * C + (size_t)g * W;
+    const T* x = (const T*)p.x + at;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < W; c += 512) {
+      const float v = to_f(x[c]);
+      xs[c] = v;
+      s += v;
+    }
+    const float mean = p.centered ? block_sum(s, red) * inv : 0.0f;
+    s = 0.0f;
+    for (int c = threadIdx.x; c < W; c += 512) {
+      const float v = xs[c] - mean;
+      xs[c] = v;
+      s = fmaf(v, v, s);
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(block_sum(s, red), inv, p.eps));
+    if constexpr (!BWD) {
+#pragma unroll 4
+      for (int c = threadIdx.x; c < W; c += 512)
+        ((T*)p.y)[at + c] = from_f<T>(forward_value<T, GATE>(p.act, xs[c] * rstd, w ? to_f(w[c]) : 1.0f, b ? to_f(b[c]) : 0.0f,
+                                                             GATE ? to_f(((const T*)p.gate)[at + c]) : 0.0f));
+    } else {
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll 2
+      for (int c = threadIdx.x; c < W; c += 512) {
+        const float n = xs[c] * rstd, wc = w ? to_f(w[c]) : 1.0f;
+        float dz;
+        const float dt = backward_value<T, GATE>(p.act, n, wc, b ? to_f(b[c]) : 0.0f, GATE ? to_f(((const T*)p.gate)[at + c]) : 0.0f,
+                                                 to_f(((const T*)p.dy)[at + c]), dz);
+        if constexpr (GATE) ((T*)p.dgate)[at + c] = from_f<T>(dz);
+        if (p.part) {
+          dw[c] = fmaf(dt, n, dw[c]);
+          db[c] += dt;
+        }
+        const float dn = dt * wc;
+        xs[c] = n;
+        ds[c] = dn;
+        s1 += dn;
+        s2 = fmaf(dn, n, s2);
+      }
+      s1 = block_sum(s1, red) * inv;
+      if (!p.centered) s1 = 0.0f;
+      s2 = block_sum(s2, red) * inv;
+      for (int c = threadIdx.x; c < W; c += 512) ((T*)p.dx)[at + c] = from_f<T>(rstd * (ds[c] - s1 - xs[c] * s2));
+    }
+  }
+  if (BWD && p.part)
+    for (int c = threadIdx.x; c < W; c += 512) {
+      p.part[(size_t)blockIdx.x * 2 * C + (size_t)g * W + c] = dw[c];
+      p.part[((size_t)blockIdx.x * 2 + 1) * C + (size_t)g * W + c] = db[c];
+    }
+}
+
+// out[c] = sum of part[k][c], k in order; 32 columns a block
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const float* part, int parts, long long C, T* dw, T* db) {
+  __shared__ float red[32][33];
+  const long long c = (long long)blockIdx.x * 32 + (threadIdx.x & 31);  // of 2 C
+  const int k0 = threadIdx.x >> 5;
+  float s = 0.0f;
+  if (c < 2 * C)
+#pragma unroll 4
+    for (int k = k0; k < parts; k += 32) s += part[(size_t)k * 2 * C + c];
+  red[k0][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (k0 == 0 && c < 2 * C) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) t += red[k][threadIdx.x];
+    if (c < C) {
+      if (dw) dw[c] = from_f<T>(t);
+    } else if (db) {
+      db[c - C] = from_f<T>(t);
+    }
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return RNN_OK;
+  fprintf(stderr, "librnn_gb300: CUDA error: %s\n", cudaGetErrorString(e));
+  return RNN_ECUDA;
+}
+bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+constexpr int NORM_MAX_W = RNN_NORM_MAX_WIDTH;
+
+bool norm_ok(long long rows, int G, int W, int dtype) {
+  return rows >= 0 && rows < (1LL << 40) && G >= 1 && W >= 1 && W <= NORM_MAX_W && (long long)G * W <= (1 << 28) &&
+         G <= 65535 && (dtype == RNN_F32 || dtype == RNN_BF16);
+}
+
+// How a problem is laid over the GPU: vectors of vec values, nv of them a
+// thread (0: the wide kernel), and the grid.
+struct NormPlan {
+  int vec, nv, lanes, gp, rp;
+  unsigned gx, gy;
+};
+NormPlan norm_plan(long long rows, int G, int W, int dtype) {
+  NormPlan p{};
+  const int full = dtype == RNN_BF16 ? 8 : 4;
+  p.vec = W % full == 0 ? full : 1;
+  const int n = (W + p.vec - 1) / p.vec;  // vectors of a group
+  const int most = p.vec == 1 ? 8 : 2;  // a thread's, so that the registers suffice
+  if (n > 256 * most) {
+    p.gp = p.rp = 1;
+    p.gy = (unsigned)G;
+  } else {
+    p.lanes = 1;
+    while (p.lanes < 32 && p.lanes < n) p.lanes *= 2;
+    while (p.lanes * most < n) p.lanes *= 2;
+    p.nv = 1;
+    while (p.nv * p.lanes < n) p.nv *= 2;
+    const int slots = 256 / p.lanes;
+    p.gp = G < slots ? G : slots;
+    p.rp = slots / p.gp;
+    p.gy = (unsigned)((G + p.gp - 1) / p.gp);
+  }
+  const long long want = (rows + p.rp - 1) / p.rp;
+  long long most_ctas = (long long)device_sms() * (p.nv ? 6 : 2) / p.gy;
+  if (most_ctas < 1) most_ctas = 1;
+  p.gx = (unsigned)(want < 1 ? 1 : want < most_ctas ? want : most_ctas);
+  return p;
+}
+
+template <typename T, int VEC, int NV, bool MANY> auto norm_kernel_of(bool gate, bool bwd) {
+  return bwd ? (gate ? norm_kernel<T, VEC, NV, true, true, MANY> : norm_kernel<T, VEC, NV, false, true, MANY>)
+             : (gate ? norm_kernel<T, VEC, NV, true, false, MANY> : norm_kernel<T, VEC, NV, false, false, MANY>);
+}
+template <typename T, int VEC, int NV> cudaError_t narrow(const NormPlan& pl, const NormArgs& a, bool bwd, cudaStream_t st) {
+  void (*k)(NormArgs) = pl.lanes > 32 ? norm_kernel_of<T, VEC, NV, true>(a.gate, bwd) : norm_kernel_of<T, VEC, NV, false>(a.gate, bwd);
+  const size_t sm = bwd && a.part ? (size_t)2 * pl.gp * a.W * 4 : 0;
+  cudaError_t e = set_smem_attr((const void*)k, sm);
+  if (e != cudaSuccess) return e;
+  k<<<dim3(pl.gx, pl.gy), 256, sm, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+template <typename T, int VEC> cudaError_t launch_nv(const NormPlan& pl, const NormArgs& a, bool bwd, cudaStream_t st) {
+  if (pl.nv == 1) return narrow<T, VEC, 1>(pl, a, bwd, st);
+  if (pl.nv == 2) return narrow<T, VEC, 2>(pl, a, bwd, st);
+  if constexpr (VEC == 1) return pl.nv == 4 ? narrow<T, 1, 4>(pl, a, bwd, st) : narrow<T, 1, 8>(pl, a, bwd, st);
+  return cudaErrorInvalidValue;
+}
+template <typename T> cudaError_t launch(const NormPlan& pl, const NormArgs& a, bool bwd, cudaStream_t st) {
+  constexpr int FULL = 16 / sizeof(T);
+  if (pl.nv) return pl.vec == 1 ? launch_nv<T, 1>(pl, a, bwd, st) : launch_nv<T, FULL>(pl, a, bwd, st);
+  void (*k)(NormArgs) = bwd ? (a.gate ? norm_wide_kernel<T, true, true> : norm_wide_kernel<T, false, true>)
+                            : (a.gate ? norm_wide_kernel<T, true, false> : norm_wide_kernel<T, false, false>);
+  const size_t sm = (size_t)(bwd ? (a.part ? 4 : 2) : 1) * a.W * 4;
+  cudaError_t e = set_smem_attr((const void*)k, sm);
+  if (e != cudaSuccess) return e;
+  k<<<dim3(pl.gx, pl.gy), 512, sm, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+NormArgs norm_args(const NormPlan& pl, long long rows, int G, int W, int act, int centered, float eps) {
+  NormArgs a{};
+  a.rows = rows; a.G = G; a.W = W; a.act = act; a.centered = centered; a.eps = eps;
+  a.lanes = pl.lanes; a.gp = pl.gp; a.rp = pl.rp;
+  return a;
+}
+
+}  // namespace
+}  // namespace rnn
+
+using namespace rnn;
+
+extern "C" {
+
+size_t rnn_group_norm_workspace_size(long long rows, int groups, int width, int dtype) {
+  if (!norm_ok(rows, groups, width, dtype)) return 0;
+  return 256 + (size_t)norm_plan(rows, groups, width, dtype).gx * 2 * groups * width * sizeof(float);
+}
+
+int rnn_group_norm_fwd(long long rows, int groups, int width, int dtype, int act, int centered, float eps, const void* x,
+                       const void* w, const void* b, const void* gate, void* y, void* stream) {
+  if (!norm_ok(rows, groups, width, dtype) || act < RNN_ACT_NONE || act > RNN_ACT_SIGMOID || !(eps >= 0)) return RNN_EINVAL;
+  if (rows > 0 && (!x || !y)) return RNN_EINVAL;
+  const void* ptrs[] = {x, w, b, gate, y};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return RNN_EINVAL;
+  if (rows == 0) return RNN_OK;
+  const NormPlan pl = norm_plan(rows, groups, width, dtype);
+  NormArgs a = norm_args(pl, rows, groups, width, act, centered, eps);
+  a.x = x; a.w = w; a.b = b; a.gate = gate; a.y = y;
+  cudaStream_t st = (cudaStream_t)stream;
+  return cuda_status(dtype == RNN_BF16 ? launch<bf16>(pl, a, false, st) : launch<float>(pl, a, false, st));
+}
+
+int rnn_group_norm_bwd(long long rows, int groups, int width, int dtype, int act, int centered, float eps, const void* x,
+                       const void* w, const void* b, const void* gate, const void* dy, void* dx, void* dgate, void* dw,
+                       void* db, void* workspace, size_t ws_bytes, void* stream) {
+  if (!norm_ok(rows, groups, width, dtype) || act < RNN_ACT_NONE || act > RNN_ACT_SIGMOID || !(eps >= 0)) return RNN_EINVAL;
+  if (rows > 0 && (!x || !dy || !dx || !gate != !dgate)) return RNN_EINVAL;
+  const void* ptrs[] = {x, w, b, gate, dy, dx, dgate, dw, db, workspace};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return RNN_EINVAL;
+  cudaStream_t st = (cudaStream_t)stream;
+  const size_t C = (size_t)groups * width, e = dtype == RNN_BF16 ? 2 : 4;
+  if (rows == 0) {
+    int rc = dw ? cuda_status(cudaMemsetAsync(dw, 0, C * e, st)) : RNN_OK;
+    return rc || !db ? rc : cuda_status(cudaMemsetAsync(db, 0, C * e, st));
+  }
+  const NormPlan pl = norm_plan(rows, groups, width, dtype);
+  NormArgs a = norm_args(pl, rows, groups, width, act, centered, eps);
+  a.x = x; a.w = w; a.b = b; a.gate = gate; a.dy = dy; a.dx = dx; a.dgate = dgate;
+  if (dw || db) {
+    if (!workspace) return RNN_EINVAL;
+    if (ws_bytes < rnn_group_norm_workspace_size(rows, groups, width, dtype)) return RNN_ENOSPC;
+    a.part = (float*)workspace;
+  }
+  int rc = cuda_status(dtype == RNN_BF16 ? launch<bf16>(pl, a, true, st) : launch<float>(pl, a, true, st));
+  if (rc || !a.part) return rc;
+  const unsigned blocks = (unsigned)((2 * C + 31) / 32);
+  if (dtype == RNN_BF16) norm_sums_kernel<bf16><<<blocks, 1024, 0, st>>>(a.part, (int)pl.gx, (long long)C, (bf16*)dw, (bf16*)db);
+  else norm_sums_kernel<float><<<blocks, 1024, 0, st>>>(a.part, (int)pl.gx, (long long)C, (float*)dw, (float*)db);
+  note_launch();
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -520,6 +520,92 @@ def gated_delta_step(q, k, v, g, beta, pool, slots=None, scale=None, pool_out=No
     return o
 
 
+# ---- group norm ------------------------------------------------------------------------
+def _norm_run(x, weight, bias, gate, groups, activation, eps, centered):
+    """(y, and the tensors as the library took them)."""
+    _lib.check_device(x)
+    x, weight, bias, gate = _dense(x), _dense(weight), _dense(bias), _dense(gate)
+    C = x.shape[-1]
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _lib.rnn_group_norm_fwd(x.numel() // C, groups, C // groups, activation, centered, eps, x, weight, bias, gate, y)
+    return y, x, weight, bias, gate
+
+
+class _NormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, gate, groups, activation, eps, centered):
+        y, *kept = _norm_run(x, weight, bias, gate, groups, activation, eps, centered)
+        ctx.args = (groups, activation, eps, centered)
+        ctx.save_for_backward(*kept)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        return (_norm_bwd_once if torch.is_grad_enabled() else _norm_bwd)(ctx, dy)
+
+
+def _norm_bwd(ctx, dy):
+    _first_order(dy)
+    x, weight, bias, gate = ctx.saved_tensors
+    groups, activation, eps, centered = ctx.args
+    need = ctx.needs_input_grad
+    C = x.shape[-1]
+    rows, width = x.numel() // C, C // groups
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    dx = new(x)
+    dgate = None if gate is None else new(gate)
+    dw = new(weight) if need[1] else None
+    db = new(bias) if need[2] else None
+    ws = None
+    if dw is not None or db is not None:
+        size = _lib.rnn_group_norm_workspace_size(rows, groups, width, x.dtype, x.get_device())
+        ws = torch.empty(size, dtype=torch.uint8, device=x.device)
+    _lib.rnn_group_norm_bwd(rows, groups, width, activation, centered, eps, x, weight, bias, gate, _dense(dy), dx, dgate,
+                            dw, db, ws)
+    return dx if need[0] else None, dw, db, dgate if need[3] else None, None, None, None, None
+
+
+_norm_bwd_once = once_differentiable(_norm_bwd)
+
+
+def group_norm(x, groups: int, weight=None, bias=None, gate=None, activation=None, eps: float = 1e-5,
+               centered: bool = True):
+    """Group norm with an activation, channels last: x [..., C] (bf16 or fp32), C
+    in `groups` groups of neighbouring channels (the heads of a scan's output),
+    statistics over one group's channels of one row. n = (x - mean) / sqrt(var +
+    eps), t = n * weight + bias, y = act(t) or, with a gate of x's shape,
+    t * act(gate). weight, bias [C] or None; activation None, "silu" or
+    "sigmoid"; centered=False leaves the mean out (var is then the mean square).
+    Differentiable in x, weight, bias and gate; the statistics and all sums are
+    fp32. Groups of up to 14336 channels."""
+    _on_gpu(x, "group_norm")
+    if x.dtype not in _lib.DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must have channels, got shape {tuple(x.shape)}")
+    C = x.shape[-1]
+    if groups < 1 or C % groups:
+        raise ValueError(f"{C} channels do not make {groups} groups")
+    if C // groups > _lib.NORM_MAX_WIDTH:
+        raise ValueError(f"groups of up to {_lib.NORM_MAX_WIDTH} channels, got {C // groups}")
+    if activation not in _lib.ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(_lib.ACTIVATIONS)}, got {activation!r}")
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps}")
+    for t, name, shape in ((weight, "weight", (C,)), (bias, "bias", (C,)), (gate, "gate", x.shape)):
+        if t is None:
+            continue
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype != x.dtype:
+            raise TypeError(f"{name} is {t.dtype}, x is {x.dtype}")
+        if t.get_device() != x.get_device():
+            raise ValueError(f"{name} must be on x's device")
+    if _tracked(x, weight, bias, gate):
+        return _NormFn.apply(x, weight, bias, gate, int(groups), activation, float(eps), bool(centered))
+    return _norm_run(x, weight, bias, gate, int(groups), activation, float(eps), bool(centered))[0]
+
+
 # ---- 8-bit activation checkpoints -----------------------------------------------------
 def _pack(x):
     rows, cols = x.shape
