@@ -403,7 +403,8 @@ int rnn_gated_step(int rows, int slots, int N, int D, int function, int dtype, c
  * steps past a length are not looked at, o and the gradients are 0 there. An
  * infinity or a NaN in an input may reach every step of its row and head.
  * Chunks of 64 steps (bf16) or 32 (fp32) are taken at once by matrix products
- * whose operands are held to 2^-17 (bf16) or 2^-24 (fp32) of their values.
+ * whose computed operands are held to 2^-24; bf16 dq and dk are taken from
+ * operands rounded to bf16 once.
  */
 #define RNN_DELTA_MAX_D 256 /* the largest Dk and Dv */
 typedef struct {
@@ -411,28 +412,30 @@ typedef struct {
   int dtype; /* rnn_dtype_t, of q, k, v, o, dO, dq, dk, dv */
 } rnn_delta_dims_t;
 
-/* Bytes of the tape (what the forward works on and the backward needs: about
- * 2 Dk Dv / 32 + 6 Dv + 512 bytes a step and head for bf16) and of the
- * backward's workspace; 0 for invalid dims. */
-size_t rnn_delta_tape_size(const rnn_delta_dims_t *dims);
+/* Bytes of the tape: what the forward works on and, with keep != 0, what the
+ * backward needs (for bf16 and Dk = Dv = 128 about 2.5 KB a step and head,
+ * without a backward 0.8 KB), and of the backward's workspace; 0 for invalid
+ * dims. The tape's first word is a status word (rnn_check_status): a device-side
+ * wait of the forward or the backward that ran out. */
+size_t rnn_delta_tape_size(const rnn_delta_dims_t *dims, int keep);
 size_t rnn_delta_bwd_workspace_size(const rnn_delta_dims_t *dims);
 
 /* Forward: state0 [B,1,N,Dk,Dv] fp32 or NULL = zeros, reset [B,T] bytes or
  * NULL, lengths [B] int32 or NULL; o [B,T,N,Dv], last [B,1,N,Dk,Dv] fp32 or
- * NULL. The tape may be dropped after the call when no backward comes.
- * Errors: RNN_EINVAL, RNN_ENOSPC, RNN_ECUDA. */
+ * NULL; keep != 0: a backward comes.
+ * Errors: RNN_EINVAL, RNN_ENOSPC, RNN_ECUDA; RNN_ETIMEOUT by rnn_check_status. */
 int rnn_delta_fwd(const rnn_delta_dims_t *dims, const void *q, const void *k, const void *v, const void *g,
                   const void *beta, const void *state0, const unsigned char *reset, const int *lengths, float scale,
-                  void *o, void *last, void *tape, size_t tape_bytes, void *stream);
+                  void *o, void *last, int keep, void *tape, size_t tape_bytes, void *stream);
 
-/* Backward: the gradient of sum(o*dO) + sum(last*dlast). q, k, lengths, scale
- * and the tape as in / from the forward; dO [B,T,N,Dv] and dlast
+/* Backward: the gradient of sum(o*dO) + sum(last*dlast). q, k, v, lengths, scale
+ * and the tape as in / from the forward (keep != 0); dO [B,T,N,Dv] and dlast
  * [B,1,N,Dk,Dv] fp32 may be NULL (zero). Outputs dq, dk [B,T,Nk,Dk] (sums over
  * the heads that share them, in the heads' order), dv [B,T,N,Dv], dg, dbeta
  * [B,T,N] fp32, dstate0 [B,1,N,Dk,Dv] fp32 or NULL. Errors: as the forward. */
-int rnn_delta_bwd(const rnn_delta_dims_t *dims, const void *q, const void *k, const int *lengths, float scale,
-                  const void *tape, size_t tape_bytes, const void *dO, const void *dlast, void *dq, void *dk, void *dv,
-                  void *dg, void *dbeta, void *dstate0, void *workspace, size_t ws_bytes, void *stream);
+int rnn_delta_bwd(const rnn_delta_dims_t *dims, const void *q, const void *k, const void *v, const int *lengths,
+                  float scale, void *tape, size_t tape_bytes, const void *dO, const void *dlast, void *dq, void *dk,
+                  void *dv, void *dg, void *dbeta, void *dstate0, void *workspace, size_t ws_bytes, void *stream);
 
 /* One step of `rows` sequences whose states live in a pool [slots,N,Dk,Dv]
  * fp32: q, k [rows,Nk,Dk], v [rows,N,Dv], g, beta [rows,N] fp32, o [rows,N,Dv].

@@ -47,13 +47,15 @@ def fwd(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=None):
 
 
 def bwd(q, k, v, g, beta, trail, do=None, dlast=None, scale=None):
-    """Gradients of sum(o do) + sum(last dlast): (dq, dk, dv, dg, dbeta, dstate)."""
+    """Gradients of sum(o do) + sum(last dlast): (dq, dk, dv, dg, dbeta, dstate,
+    and the two products that each of dq and dk is the sum of)."""
     q, k, v, g, beta, do, dlast = (f64(x) for x in (q, k, v, g, beta, do, dlast))
     B, T, Nk, Dk = q.shape
     N, Dv = v.shape[2:]
     share = N // Nk
     scale = Dk ** -0.5 if scale is None else scale
     dq, dk = np.zeros((B, T, N, Dk)), np.zeros((B, T, N, Dk))
+    parts = np.zeros((4, B, T, N, Dk))
     dv, dg, db = np.zeros(v.shape), np.zeros(g.shape), np.zeros(g.shape)
     ds = np.zeros((B, 1, N, Dk, Dv))
     for i in range(B):
@@ -63,18 +65,22 @@ def bwd(q, k, v, g, beta, trail, do=None, dlast=None, scale=None):
             kt, qt = _rows(k, i, t, share), _rows(q, i, t, share)
             d = np.zeros((N, Dv)) if do is None else scale * do[i, t]
             dS = dS + qt[:, :, None] * d[:, None]
-            dq[i, t] = np.einsum("nkv,nv->nk", S, d)
             du = np.einsum("nkv,nk->nv", dS, kt)
             u = beta[i, t][:, None] * e
             dv[i, t] = beta[i, t][:, None] * du
             db[i, t] = (du * e).sum(1)
-            dk[i, t] = np.einsum("nkv,nv->nk", dS, u) - np.einsum("nkv,nv->nk", D, dv[i, t])
+            parts[0, i, t] = np.einsum("nkv,nv->nk", D, d)
+            parts[1, i, t] = kt * (u * d).sum(1)[:, None]
+            parts[2, i, t] = np.einsum("nkv,nv->nk", dS, u)
+            parts[3, i, t] = -np.einsum("nkv,nv->nk", D, dv[i, t])
+            dq[i, t] = parts[0, i, t] + parts[1, i, t]
+            dk[i, t] = parts[2, i, t] + parts[3, i, t]
             dD = dS - kt[:, :, None] * dv[i, t][:, None]
             dg[i, t] = (D * dD).sum((1, 2))
             dS = a[:, None, None] * dD
         ds[i, 0] = dS
     fold = lambda x: x.reshape(B, T, Nk, share, Dk).sum(3)  # noqa: E731
-    return fold(dq), fold(dk), dv, dg, db, ds
+    return fold(dq), fold(dk), dv, dg, db, ds, parts
 
 
 def _act(x, activation):

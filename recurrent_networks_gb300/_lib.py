@@ -106,9 +106,9 @@ def load(path: str | None = None):
                                ("rnn_act_unpack", [ll, i, i] + [vp] * 4), ("rnn_embed_bwd_workspace_size", [ll, i, i]),
                                ("rnn_embed_fwd", [ll, i, i, i, i, vp, vp, f, vp, vp, vp]),
                                ("rnn_embed_bwd", [ll, i, i, i, i, vp, ll, vp, f, vp, vp, sz, vp]),
-                               ("rnn_delta_tape_size", [ep]), ("rnn_delta_bwd_workspace_size", [ep]),
-                               ("rnn_delta_fwd", [ep] + [vp] * 8 + [f, vp, vp, vp, sz, vp]),
-                               ("rnn_delta_bwd", [ep, vp, vp, vp, f, vp, sz] + [vp] * 9 + [sz, vp]),
+                               ("rnn_delta_tape_size", [ep, i]), ("rnn_delta_bwd_workspace_size", [ep]),
+                               ("rnn_delta_fwd", [ep] + [vp] * 8 + [f, vp, vp, i, vp, sz, vp]),
+                               ("rnn_delta_bwd", [ep, vp, vp, vp, vp, f, vp, sz] + [vp] * 9 + [sz, vp]),
                                ("rnn_delta_step", [i] * 7 + [vp] * 8 + [f, vp, vp, vp]),
                                ("rnn_group_norm_workspace_size", [ll, i, i, i]),
                                ("rnn_group_norm_fwd", [ll, i, i, i, i, i, f] + [vp] * 6),
@@ -421,44 +421,45 @@ _delta_plans: dict = {}
 
 
 def delta_plan(B, T, Nk, N, Dk, Dv, dtype, device):
-    """(dims, tape bytes, backward workspace bytes), kept per dims and device: the
-    sizes follow from the current device, which is `device`."""
+    """(dims, tape bytes without and with a backward, backward workspace bytes), kept
+    per dims and device: the sizes follow from the current device, which is `device`."""
     key = (B, T, Nk, N, Dk, Dv, dtype, device)
     plan = _delta_plans.get(key)
     if plan is None:
         dims = make_delta_dims(*key[:-1])
         if len(_delta_plans) >= 4096:
             _delta_plans.clear()
-        plan = _delta_plans[key] = (dims, rnn_delta_tape_size(dims), rnn_delta_bwd_workspace_size(dims))
+        plan = _delta_plans[key] = (dims, rnn_delta_tape_size(dims, False), rnn_delta_tape_size(dims, True),
+                                    rnn_delta_bwd_workspace_size(dims))
     return plan
 
 
-def rnn_delta_tape_size(dims: DeltaDims) -> int:
-    return _quick().rnn_delta_tape_size(ctypes.byref(dims))
+def rnn_delta_tape_size(dims: DeltaDims, keep: bool = True) -> int:
+    return _quick().rnn_delta_tape_size(ctypes.byref(dims), int(keep))
 
 
 def rnn_delta_bwd_workspace_size(dims: DeltaDims) -> int:
     return _quick().rnn_delta_bwd_workspace_size(ctypes.byref(dims))
 
 
-def rnn_delta_fwd(dims: DeltaDims, q, k, v, g, beta, state0, reset, lengths, scale: float, o, last, tape,
+def rnn_delta_fwd(dims: DeltaDims, q, k, v, g, beta, state0, reset, lengths, scale: float, o, last, keep: bool, tape,
                   stream=None) -> int:
     ptr, size = _ws(tape)
     rc = _quick().rnn_delta_fwd(
         ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
         None if state0 is None else state0.data_ptr(), None if reset is None else reset.data_ptr(),
         None if lengths is None else lengths.data_ptr(), scale, o.data_ptr(), None if last is None else last.data_ptr(),
-        ptr, size, _raw_stream(o, stream))
+        int(keep), ptr, size, _raw_stream(o, stream))
     return rc if rc == RNN_OK else _check(rc, "rnn_delta_fwd")
 
 
-def rnn_delta_bwd(dims: DeltaDims, q, k, lengths, scale: float, tape, dO, dlast, dq, dk, dv, dg, dbeta, dstate0,
+def rnn_delta_bwd(dims: DeltaDims, q, k, v, lengths, scale: float, tape, dO, dlast, dq, dk, dv, dg, dbeta, dstate0,
                   workspace, stream=None) -> int:
     tptr, tsize = _ws(tape)
     ptr, size = _ws(workspace)
     rc = _quick().rnn_delta_bwd(
-        ctypes.byref(dims), q.data_ptr(), k.data_ptr(), None if lengths is None else lengths.data_ptr(), scale, tptr,
-        tsize, None if dO is None else dO.data_ptr(), None if dlast is None else dlast.data_ptr(), dq.data_ptr(),
+        ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), None if lengths is None else lengths.data_ptr(),
+        scale, tptr, tsize, None if dO is None else dO.data_ptr(), None if dlast is None else dlast.data_ptr(), dq.data_ptr(),
         dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), None if dstate0 is None else dstate0.data_ptr(),
         ptr, size, _raw_stream(tape, stream))
     return rc if rc == RNN_OK else _check(rc, "rnn_delta_bwd")

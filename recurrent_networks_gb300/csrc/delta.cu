@@ -4,6 +4,7 @@
 #include <stdio.h>
 
 #include "delta.h"
+#include "delta_tc.cuh"
 #include "kernels.cuh"
 #include "rnn.h"
 
@@ -138,12 +139,14 @@ bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// What the calls lay out in the tape (behind the status word) and the workspace.
 struct DeltaSizes {
   bool bf;
-  int C, NP, BV, DKP, nvt;
-  long long nc, items;
-  size_t rec, tri, S, Z;  // bytes of the tape's parts
-  size_t tape, part, bwd;
+  int C, NP, BV, KP, nvt, np;
+  long long nc, items, ne;
+  size_t rec, tri, S, Z, zf, sf;  // bytes
+  size_t tape, scratch;           // with what a backward needs, and without
+  size_t dots, edge, part, bwd;
 };
 
 bool delta_heads_ok(int Nk, int N, int Dk, int Dv, int dtype) {
@@ -153,37 +156,73 @@ bool delta_heads_ok(int Nk, int N, int Dk, int Dv, int dtype) {
 
 bool delta_sizes(const rnn_delta_dims_t* d, DeltaSizes* z) {
   if (!d || d->B < 1 || d->T < 0 || d->T > INT_MAX - 64 || !delta_heads_ok(d->Nk, d->N, d->Dk, d->Dv, d->dtype)) return false;
+  *z = DeltaSizes{};
   z->bf = d->dtype == RNN_BF16;
-  z->C = z->bf ? DeltaCfg<bf16>::C : DeltaCfg<float>::C;
-  z->NP = z->bf ? DeltaCfg<bf16>::NP : DeltaCfg<float>::NP;
-  z->DKP = (d->Dk + 15) / 16 * 16;
-  z->BV = delta_bv(z->bf, d->B, d->N, d->Dv, z->DKP, device_sms());
+  z->C = z->bf ? TC_C : DeltaCfg<float>::C;
+  z->NP = 3;
+  z->KP = (d->Dk + 15) / 16 * 16;
+  z->BV = delta_bv(z->bf, d->B, d->N, d->Dv, z->KP, device_sms());
   z->nvt = (d->Dv + z->BV - 1) / z->BV;
+  z->np = (d->Dv + 63) / 64;
   z->nc = ((long long)d->T + z->C - 1) / z->C;
   z->items = z->nc * d->B * d->N;
   // the kernels count the items' tiles and the heads' tiles in 32 bits
   if (z->items * z->nvt > INT_MAX || (long long)d->B * d->N * z->nvt > INT_MAX) return false;
-  const size_t n = (size_t)z->items;
+  const size_t n = (size_t)z->items, heads = (size_t)d->B * d->N;
   z->rec = up256(n * REC_N * z->C * 4);
-  z->tri = up256(n * z->NP * z->C * z->C * 2);
-  z->S = up256(n * z->nvt * z->NP * z->DKP * z->BV * 2);
-  z->Z = up256(n * z->nvt * z->NP * z->C * z->BV * 2);
-  z->tape = z->rec + 2 * z->tri + z->S + z->Z;
+  if (z->bf) {
+    z->ne = z->nc / TC_EDGE + 1;
+    z->tri = up256(n * 3 * 128 * TC_C * 2);  // TP
+    z->S = up256(n * z->np * z->KP * 64 * 2);
+    z->Z = up256(n * z->np * 64 * 64 * 2);
+    z->zf = up256(n * z->nvt * 64 * z->BV * 4);
+    z->sf = up256(heads * z->ne * z->nvt * (z->KP > 128 ? 256 : 128) * z->BV * 4);
+    z->scratch = z->rec + z->tri;
+    z->tape = z->scratch + z->S + z->Z + 2 * z->zf + z->sf;
+    z->dots = up256(n * z->nvt * 6 * TC_C * 4);
+    z->edge = up256(heads * z->ne * z->nvt * 8 * 4);
+    z->bwd = z->S + z->dots + z->edge;
+  } else {
+    z->tri = up256(n * z->NP * z->C * z->C * 2);  // each of Tm and P
+    z->S = up256(n * z->nvt * z->NP * z->KP * z->BV * 2);
+    z->Z = up256(n * z->nvt * z->NP * z->C * z->BV * 2);
+    z->scratch = z->tape = z->rec + 2 * z->tri + z->S + z->Z;
+    z->bwd = z->S + z->Z;
+  }
   z->part = d->N != d->Nk ? up256((size_t)d->B * d->T * d->N * d->Dk * 4) : 0;
-  z->bwd = z->S + z->Z + 2 * z->part;
+  z->bwd += 2 * z->part;
   return true;
 }
 
-DeltaArgs delta_args(const rnn_delta_dims_t* d, const DeltaSizes& z, const void* tape) {
+DeltaArgs delta_args(const rnn_delta_dims_t* d, const DeltaSizes& z, void* tape) {
   DeltaArgs a{};
   a.B = d->B; a.T = d->T; a.Nk = d->Nk; a.N = d->N; a.Dk = d->Dk; a.Dv = d->Dv;
-  a.DKP = z.DKP; a.nvt = z.nvt; a.nc = (int)z.nc;
-  char* t = (char*)tape;
+  a.DKP = z.KP; a.nvt = z.nvt; a.nc = (int)z.nc;
+  a.status = (unsigned*)tape;
+  char* t = (char*)tape + 256;
   a.rec = (float*)t;
   a.tm = (bf16*)(t + z.rec);
   a.pm = (bf16*)(t + z.rec + z.tri);
   a.S = (bf16*)(t + z.rec + 2 * z.tri);
   a.Z = (bf16*)(t + z.rec + 2 * z.tri + z.S);
+  return a;
+}
+
+DeltaTcArgs delta_tc_args(const rnn_delta_dims_t* d, const DeltaSizes& z, void* tape, bool keep) {
+  DeltaTcArgs a{};
+  a.B = d->B; a.T = d->T; a.Nk = d->Nk; a.N = d->N; a.Dk = d->Dk; a.Dv = d->Dv;
+  a.KP = z.KP; a.np = z.np; a.nvt = z.nvt; a.nc = (int)z.nc; a.ne = (int)z.ne;
+  a.status = (unsigned*)tape;
+  a.wait_limit_ns = wait_limit_ns();
+  char* t = (char*)tape + 256;
+  a.rec = (float*)t;
+  a.tp = (bf16*)(t += z.rec);
+  if (!keep) return a;
+  a.Sh = (bf16*)(t += z.tri);
+  a.Zh = (bf16*)(t += z.S);
+  a.zf = (float*)(t += z.Z);
+  a.of = (float*)(t += z.zf);
+  a.sf = (float*)(t += z.zf);
   return a;
 }
 
@@ -194,9 +233,9 @@ using namespace rnn;
 
 extern "C" {
 
-size_t rnn_delta_tape_size(const rnn_delta_dims_t* d) {
+size_t rnn_delta_tape_size(const rnn_delta_dims_t* d, int keep) {
   DeltaSizes z;
-  return delta_sizes(d, &z) ? 256 + z.tape : 0;
+  return delta_sizes(d, &z) ? 256 + (keep ? z.tape : z.scratch) : 0;
 }
 
 size_t rnn_delta_bwd_workspace_size(const rnn_delta_dims_t* d) {
@@ -206,34 +245,43 @@ size_t rnn_delta_bwd_workspace_size(const rnn_delta_dims_t* d) {
 
 int rnn_delta_fwd(const rnn_delta_dims_t* d, const void* q, const void* k, const void* v, const void* g,
                   const void* beta, const void* state0, const unsigned char* reset, const int* lengths, float scale,
-                  void* o, void* last, void* tape, size_t tape_bytes, void* stream) {
+                  void* o, void* last, int keep, void* tape, size_t tape_bytes, void* stream) {
   DeltaSizes z;
-  if (!delta_sizes(d, &z) || (d->T > 0 && (!q || !k || !v || !g || !beta || !o || !tape))) return RNN_EINVAL;
+  if (!delta_sizes(d, &z) || !tape || (d->T > 0 && (!q || !k || !v || !g || !beta || !o))) return RNN_EINVAL;
   const void* ptrs[] = {q, k, v, g, beta, state0, o, last, tape};
   for (const void* p : ptrs)
     if (p && !al16(p)) return RNN_EINVAL;
   if (!al4(lengths)) return RNN_EINVAL;
+  if (tape_bytes < 256 + (keep ? z.tape : z.scratch)) return RNN_ENOSPC;
   cudaStream_t st = (cudaStream_t)stream;
   if (d->T == 0) {
     const size_t bytes = (size_t)d->B * d->N * d->Dk * d->Dv * sizeof(float);
-    if (!last) return RNN_OK;
+    const int rc = cuda_status(cudaMemsetAsync(tape, 0, 256, st));
+    if (rc || !last) return rc;
     return cuda_status(state0 ? cudaMemcpyAsync(last, state0, bytes, cudaMemcpyDeviceToDevice, st)
                               : cudaMemsetAsync(last, 0, bytes, st));
   }
-  if (tape_bytes < 256 + z.tape) return RNN_ENOSPC;
+  auto fill = [&](auto& a) {
+    a.q = q; a.k = k; a.v = v; a.g = (const float*)g; a.beta = (const float*)beta; a.s0 = (const float*)state0;
+    a.reset = reset; a.lengths = lengths; a.scale = scale; a.o = o; a.last = (float*)last;
+  };
+  if (z.bf) {
+    DeltaTcArgs a = delta_tc_args(d, z, tape, keep != 0);
+    fill(a);
+    return cuda_status(delta_tc_fwd_launch(z.BV, a, st));
+  }
   DeltaArgs a = delta_args(d, z, tape);
-  a.q = q; a.k = k; a.v = v; a.g = (const float*)g; a.beta = (const float*)beta; a.s0 = (const float*)state0;
-  a.reset = reset; a.lengths = lengths; a.scale = scale; a.o = o; a.last = (float*)last;
-  return cuda_status(delta_fwd_launch(z.bf, z.BV, a, st));
+  fill(a);
+  return cuda_status(delta_fwd_launch(a, st));
 }
 
-int rnn_delta_bwd(const rnn_delta_dims_t* d, const void* q, const void* k, const int* lengths, float scale,
-                  const void* tape, size_t tape_bytes, const void* dO, const void* dlast, void* dq, void* dk, void* dv,
+int rnn_delta_bwd(const rnn_delta_dims_t* d, const void* q, const void* k, const void* v, const int* lengths, float scale,
+                  void* tape, size_t tape_bytes, const void* dO, const void* dlast, void* dq, void* dk, void* dv,
                   void* dg, void* dbeta, void* dstate0, void* workspace, size_t ws_bytes, void* stream) {
   DeltaSizes z;
   if (!delta_sizes(d, &z)) return RNN_EINVAL;
-  if (d->T > 0 && (!q || !k || !tape || !dq || !dk || !dv || !dg || !dbeta || !workspace)) return RNN_EINVAL;
-  const void* ptrs[] = {q, k, tape, dO, dlast, dq, dk, dv, dg, dbeta, dstate0, workspace};
+  if (d->T > 0 && (!q || !k || !v || !tape || !dq || !dk || !dv || !dg || !dbeta || !workspace)) return RNN_EINVAL;
+  const void* ptrs[] = {q, k, v, tape, dO, dlast, dq, dk, dv, dg, dbeta, dstate0, workspace};
   for (const void* p : ptrs)
     if (p && !al16(p)) return RNN_EINVAL;
   if (!al4(lengths)) return RNN_EINVAL;
@@ -245,18 +293,29 @@ int rnn_delta_bwd(const rnn_delta_dims_t* d, const void* q, const void* k, const
                              : cudaMemsetAsync(dstate0, 0, bytes, st));
   }
   if (tape_bytes < 256 + z.tape || ws_bytes < 256 + z.bwd) return RNN_ENOSPC;
-  DeltaArgs a = delta_args(d, z, tape);
-  a.q = q; a.k = k; a.lengths = lengths; a.scale = scale;
-  a.dO = dO; a.dlast = (const float*)dlast;
-  a.dq = dq; a.dk = dk; a.dv = dv; a.dg = (float*)dg; a.dbeta = (float*)dbeta; a.ds0 = (float*)dstate0;
   char* w = (char*)workspace;
+  auto fill = [&](auto& a) {
+    a.q = q; a.k = k; a.v = v; a.lengths = lengths; a.scale = scale;
+    a.dO = dO; a.dlast = (const float*)dlast;
+    a.dq = dq; a.dk = dk; a.dv = dv; a.dg = (float*)dg; a.dbeta = (float*)dbeta; a.ds0 = (float*)dstate0;
+    if (z.part) {
+      a.pq = (float*)(w + z.bwd - 2 * z.part);
+      a.pk = (float*)(w + z.bwd - z.part);
+    }
+  };
+  if (z.bf) {
+    DeltaTcArgs a = delta_tc_args(d, z, tape, true);
+    fill(a);
+    a.dSh = (bf16*)w;
+    a.dots = (float*)(w + z.S);
+    a.edge = (float*)(w + z.S + z.dots);
+    return cuda_status(delta_tc_bwd_launch(z.BV, a, st));
+  }
+  DeltaArgs a = delta_args(d, z, tape);
+  fill(a);
   a.dS = (bf16*)w;
   a.dY = (bf16*)(w + z.S);
-  if (z.part) {
-    a.pq = (float*)(w + z.S + z.Z);
-    a.pk = (float*)(w + z.S + z.Z + z.part);
-  }
-  return cuda_status(delta_bwd_launch(z.bf, z.BV, a, st));
+  return cuda_status(delta_bwd_launch(a, st));
 }
 
 int rnn_delta_step(int rows, int slots, int Nk, int N, int Dk, int Dv, int dtype, const void* q, const void* k,

@@ -53,6 +53,7 @@ struct DeltaArgs {
   const unsigned char* reset;
   const int* lengths;
   float scale;
+  unsigned* status;
   void* o;
   float* last;
   float* rec;  // [items][REC_N][C], items = (b N + n) nc + chunk

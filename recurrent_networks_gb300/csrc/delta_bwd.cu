@@ -539,9 +539,6 @@ template <typename T, int BV> cudaError_t run(const DeltaArgs& a, cudaStream_t s
 
 }  // namespace
 
-cudaError_t delta_bwd_launch(bool bf, int BV, const DeltaArgs& a, cudaStream_t st) {
-  if (!bf) return run<float, 32>(a, st);
-  return BV == 64 ? run<bf16, 64>(a, st) : run<bf16, 32>(a, st);
-}
+cudaError_t delta_bwd_launch(const DeltaArgs& a, cudaStream_t st) { return run<float, 32>(a, st); }
 
 }  // namespace rnn

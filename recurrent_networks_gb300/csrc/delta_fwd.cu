@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(2 * DeltaCfg<T>::C) delta_prep_kernel(DeltaArg
   float* rec = Lf + C * (C + 4);           // [REC_N][C]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long item = blockIdx.x;
+  if (item == 0 && tid == 0) *a.status = 0;  // no kernel of fp32 storage waits for another
   const int ch = (int)(item % a.nc), bn = (int)(item / a.nc), n = bn % a.N, b = bn / a.N;
   const int live = live_steps(a, b, ch, C);
   if (live == 0) return;
@@ -406,9 +407,6 @@ template <typename T, int BV> cudaError_t run(const DeltaArgs& a, cudaStream_t s
 
 }  // namespace
 
-cudaError_t delta_fwd_launch(bool bf, int BV, const DeltaArgs& a, cudaStream_t st) {
-  if (!bf) return run<float, 32>(a, st);
-  return BV == 64 ? run<bf16, 64>(a, st) : run<bf16, 32>(a, st);
-}
+cudaError_t delta_fwd_launch(const DeltaArgs& a, cudaStream_t st) { return run<float, 32>(a, st); }
 
 }  // namespace rnn

@@ -1,0 +1,255 @@
+// Gated delta rule, bf16 storage: the products on the 5th-generation tensor
+// cores (tcgen05, accumulators in tensor memory). The formulas are in delta.cuh;
+// here
+//   P carries the scale, PT = P Tm, and the stacked matrices are
+//   KQ = [K; Q] (128 rows) and TP = [Tm; PT] (128 x 64).
+// Forward, a chunk:
+//   [K S0; Q S0] = KQ S0,  Y = V - gam K S0,
+//   [Z; PT Y] = TP Y,      O = scale gam Q S0 + PT Y,
+//   S1 = gam_63 S0 + K^T (beta rho Z).
+// Backward:
+//   W = beta rho (K dS1),  dY = Tm^T W + PT^T dO = dV,
+//   dS0 = gam_63 dS1 + KQ^T [-gam dY; scale gam dO],
+//   [dK; dQ] = rows of [-gam dY S0^T + beta rho Z dS1^T; scale gam dO S0^T] + [M + M^T, R^T; R, 0] KQ.
+// With u = beta z, v's and o's own definitions give the scalars' gradients from
+// row products alone (pairs of steps inside a chunk cancel in dc):
+//   dbeta_j = z_j.dY_j / beta_j,   dc_i = dO_i.o_i - dY_i.v_i,
+//   dg_t = the sum of dc_i over i >= t of t's document, to the chunk's end, +
+//          <S1, dS1> where the document goes on.
+// dY_j carries the factor beta_j throughout, so the quotient keeps its digits
+// for any beta_j but 0, which therefore counts as 2^-60 (far below a rounding
+// of anything it enters).
+//
+// The states, o, dY and all that fp32 outputs follow from are held to fp32: the
+// computed operands (S, Y, Z, TP, ...) in three bf16 planes, plane pairs (i, j)
+// with i + j < 3 summed, the pair (0, 0) in an accumulator of its own (delta.cuh
+// says why). dQ and dK, bf16 themselves, are taken from operands rounded to bf16
+// once (dY, Z, S0, dS1, M, R).
+//
+// Shared-memory images are rows of 128 bytes (64 columns; 64 bytes where a tile
+// of v has 32), 16-byte pieces swizzled as the tensor cores read them, panels of
+// 64 columns one after the other. The same image serves as an operand whose rows
+// are the outer index (K-major) or the summed one (MN-major).
+#pragma once
+#include "delta.cuh"
+#include "kernels.cuh"
+
+namespace rnn {
+
+constexpr int TC_C = 64;        // steps of a chunk
+constexpr int TC_EDGE = 8;      // chunks between the states kept in fp32 for dg
+constexpr int TC_PANEL = 16384; // bytes of a panel of 128 rows
+
+struct DeltaTcArgs {
+  int B, T, Nk, N, Dk, Dv;
+  int KP, np, nvt, nc, ne;  // Dk rounded to 16, panels of 64 and tiles of BV columns of v, chunks, kept states a head
+  const void *q, *k, *v;
+  const float *g, *beta, *s0;
+  const unsigned char* reset;
+  const int* lengths;
+  float scale;
+  void* o;
+  float* last;
+  unsigned* status;
+  unsigned long long wait_limit_ns;
+  float* rec;  // [items][REC_N][64]
+  bf16* tp;    // [items][3][128 x 64 image]
+  // what a backward needs besides (null: none comes)
+  bf16 *Sh, *Zh;       // [items][np][KP x 64 image] of S0, [items][np][64 x 64 image] of Z
+  float *zf, *of;      // [items][nvt][...] z and o in fp32, as the threads hold them
+  float* sf;           // [B N][ne][nvt][...] S at the end (0) and at every TC_EDGE-th chunk's start
+  // backward
+  const void* dO;
+  const float* dlast;
+  bf16* dSh;           // as Sh, of dS1
+  float* dots;         // [items][nvt][3][2][64]: z.dY, -v.dY, o.dO of half a tile's columns
+  float* edge;         // [B N][ne][nvt][8]: <S, dS> there, by warp
+  void *dq, *dk, *dv;
+  float *dg, *dbeta, *ds0;
+  float *pq, *pk;
+};
+
+// ---- tensor memory -----------------------------------------------------------------
+__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+template <int COLS> __device__ __forceinline__ void tm_alloc(uint32_t* slot) {  // one warp
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "n"(COLS) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <int COLS> __device__ __forceinline__ void tm_free(uint32_t at) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "n"(COLS) : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 16 columns of this warp's 32 lanes
+__device__ __forceinline__ void tm_ld16(uint32_t* r, uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+// x[N] = the sum of the accumulators at hi and lo, N columns of the warp's lanes
+template <int N> __device__ __forceinline__ void tm_sum(float (&x)[N], uint32_t hi, uint32_t lo) {
+  uint32_t a[N], b[N];
+#pragma unroll
+  for (int c = 0; c < N; c += 16) {
+    tm_ld16(a + c, hi + c);
+    tm_ld16(b + c, lo + c);
+  }
+  tm_wait_ld();
+#pragma unroll
+  for (int c = 0; c < N; ++c) x[c] = __uint_as_float(a[c]) + __uint_as_float(b[c]);
+}
+
+// Instruction of 128 x n products, bf16 operands, fp32 accumulator.
+__device__ __forceinline__ constexpr uint32_t tc_idesc(int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         (8u << 24);
+}
+// Operand at `at`. K-major (rows = outer index): lbo 16; MN-major (rows = summed
+// index): lbo the distance of the panels. RB: bytes of a row.
+template <int RB = 128> __device__ __forceinline__ uint64_t tc_desc(uint32_t at, uint32_t lbo) {
+  return (uint64_t)((at >> 4) & 0x3FFF) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(8 * RB >> 4) << 32) | (1ull << 46) |
+         ((RB == 128 ? 2ull : 4ull) << 61);
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The end of a kernel, whose thread 0 has issued all products: they are over (also
+// after a wait ran out) when the CTA goes on. bar is used here alone.
+__device__ __forceinline__ void tc_finish(uint32_t bar, unsigned long long limit_ns) {
+  if (threadIdx.x == 0) {
+    bool failed = false;
+    tc_commit(bar);
+    mbar_wait_bounded<false>(bar, 0, limit_ns, nullptr, failed);
+  }
+  tm_fence_before();
+  __syncthreads();
+}
+
+// Byte offset of 16-byte piece c of row r of an image with rows of RB bytes.
+template <int RB> __device__ __forceinline__ uint32_t img(int r, int c) {
+  return RB == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// 8 values as three planes of one 16-byte piece each
+__device__ __forceinline__ void split8(const float* x, uint4 (&p)[3]) {
+  uint32_t w[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      w[k][i] = *(const uint32_t*)&h;
+      if (k < 2) {
+        a -= __uint_as_float(w[k][i] << 16);
+        b -= __uint_as_float(w[k][i] & 0xffff0000u);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) p[k] = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+}
+__device__ __forceinline__ uint4 round8(const float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *(const uint32_t*)&h;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void widen8(const uint4& v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+// Piece c of row r of a panel's image; lone: the piece 32 columns further is zero.
+__device__ __forceinline__ void put_piece(unsigned char* im, int r, int c, const uint4& v, bool lone) {
+  *(uint4*)(im + img<128>(r, c)) = v;
+  if (lone) *(uint4*)(im + img<128>(r, c + 4)) = make_uint4(0, 0, 0, 0);
+}
+// N values of row r, from column c0 (a multiple of 8) on, into the planes of an
+// image (plane bytes apart)
+template <int RB, int N> __device__ __forceinline__ void put_planes(unsigned char* im, int plane, int r, int c0, const float (&x)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; c += 8) {
+    uint4 p[3];
+    split8(x + c, p);
+    const uint32_t at = img<RB>(r, (c0 + c) >> 3);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *(uint4*)(im + k * plane + at) = p[k];
+  }
+}
+
+// 64 rows of an input (rows `stride` elements apart) from column c0, `pieces`
+// 16-byte pieces a row, into rows row0 .. of panels of 128 rows; rows from `live`
+// on and columns past D are zero and not read.
+template <int RB>
+__device__ __forceinline__ void load_img(unsigned char* im, int row0, const bf16* src, size_t stride, int live, int D, int c0,
+                                         int pieces, int panel_bytes, int nthreads) {
+  constexpr int PR = RB / 16;  // pieces of a panel's row
+  const bool vec = D % 8 == 0;
+  for (int i = threadIdx.x; i < 64 * pieces; i += nthreads) {
+    const int r = i / pieces, c = i - r * pieces, col = c0 + c * 8;
+    unsigned char* d = im + (c / PR) * panel_bytes + img<RB>(row0 + r, c % PR);
+    const bf16* s = src + (size_t)r * stride + col;
+    if (vec) {
+      const bool on = r < live && col < D;
+      cp16(smem_u32(d), on ? s : src, on);
+    } else {
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (r < live) {
+        const unsigned short* p = (const unsigned short*)s;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + e < D) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+      }
+      *(uint4*)d = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+// `bytes` of an image that global memory holds as it stands
+__device__ __forceinline__ void load_plain(unsigned char* im, const void* src, int bytes) {
+  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) cp16(smem_u32(im + i), (const unsigned char*)src + i, true);
+}
+
+// N values of a row of a tensor whose rows have D - c valid columns from p on
+template <int N> __device__ __forceinline__ void store_row(bf16* p, const float (&x)[N], int valid, bool vec) {
+#pragma unroll
+  for (int c = 0; c < N; c += 8) {
+    if (vec) {
+      if (c < valid) *(uint4*)(p + c) = round8(x + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < valid) p[c + e] = __float2bfloat16_rn(x[c + e]);
+    }
+  }
+}
+
+__device__ __forceinline__ int tc_live(const DeltaTcArgs& a, int b, int ch) {
+  int len = a.T;
+  if (a.lengths) len = max(0, min(a.T, __ldg(a.lengths + b)));
+  const long long left = (long long)len - (long long)ch * TC_C;
+  return left < 0 ? 0 : (int)(left < TC_C ? left : TC_C);
+}
+__device__ __forceinline__ int tc_chunks(const DeltaTcArgs& a, int b) {
+  int len = a.T;
+  if (a.lengths) len = max(0, min(a.T, __ldg(a.lengths + b)));
+  return (len + TC_C - 1) / TC_C;
+}
+
+}  // namespace rnn

@@ -1,0 +1,615 @@
+// Gated delta rule, bf16 storage, backward (delta_tc.cuh has the formulas), from
+// what the forward left.
+//   chain  per head and tile of BV columns of v, the chunks from the last to the
+//          first: dV and the state's gradient
+//   grad   every chunk by itself: dQ, dK
+//   gates  dg and dbeta from the chain's row products
+// and, where heads share q and k, the sums of dQ and dK over them.
+#include "delta.h"
+#include "delta_tc.cuh"
+
+namespace rnn {
+namespace {
+
+// ---- chain --------------------------------------------------------------------------
+template <int BV, int MT> struct TcBack {
+  static constexpr int RB = 2 * BV, KST = MT == 1 ? 2 : 1;
+  static constexpr int KQ = 2 * MT * TC_PANEL, TP = 3 * TC_PANEL, SPLANE = MT * 128 * RB, GPLANE = 128 * RB;
+  static constexpr int AT_TP = KST * KQ, AT_S = AT_TP + TP, AT_G = AT_S + 3 * SPLANE, AT_O = AT_G + 3 * GPLANE;
+  static constexpr int AT_REC = AT_O + 64 * RB, BYTES = AT_REC + 2 * 2 * 64 * 4 + 64 + 1024;
+};
+
+// Warps and threads as in the forward's chain. The image G holds, by planes, W in
+// rows 0 .. 63 until dY's products have read it, then -gam dY; rows 64 .. 127
+// scale gam dO, written by the threads of Q's steps while the first product runs.
+// The products for dY take TP by columns, 64 of them; the other 64 rows of the
+// accumulator come from whatever lies a panel further (inside this CTA's shared
+// memory) and are not looked at.
+template <int BV, int MT>
+__global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
+  using L = TcBack<BV, MT>;
+  constexpr int RB = L::RB, NC = BV / 2, KST = L::KST;
+  static_assert(3 * L::SPLANE >= TC_PANEL, "what TP's last plane is read past");
+  extern __shared__ unsigned char sm_raw[];
+  unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *GS = sm + L::AT_G, *OS = sm + L::AT_O;
+  float* recs = (float*)(sm + L::AT_REC);  // [2][gam, br][64]
+  uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
+  uint32_t* slot = (uint32_t*)(barp + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
+  const int vt = blockIdx.x % a.nvt, bn = blockIdx.x / a.nvt, n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
+  const int nch = tc_chunks(a, b);
+  const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv;
+  const size_t kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
+  const uint32_t bar = smem_u32(barp);
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    mbar_init(bar + 8, 1);
+    fence_mbar_init_cluster();
+  }
+  if (warp == 0) tm_alloc<512>(slot);
+  auto load_kq = [&](int ch) {
+    unsigned char* d = sm + (ch % KST) * L::KQ;
+    const int live = tc_live(a, b, ch);
+    load_img<128>(d, 0, (const bf16*)a.k + kat + (size_t)ch * TC_C * kstride, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
+    load_img<128>(d, 64, (const bf16*)a.q + kat + (size_t)ch * TC_C * kstride, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
+  };
+  auto load_o = [&](int ch) {
+    load_img<RB>(OS, 0, (const bf16*)(a.dO ? a.dO : a.k) + (a.dO ? vat + (size_t)ch * TC_C * vstride : 0), vstride,
+                 a.dO ? tc_live(a, b, ch) : 0, a.Dv, vt * BV, BV / 8, 0, 256);
+    const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
+    float* d = recs + (ch & 1) * 2 * TC_C;
+    if (tid < 16) cp16(smem_u32(d + tid * 4), r + REC_GAM * TC_C + tid * 4, true);
+    else if (tid < 32) cp16(smem_u32(d + tid * 4), r + REC_BR * TC_C + (tid - 16) * 4, true);
+  };
+  auto load_tp = [&](int ch) { load_plain(TP, a.tp + ((size_t)bn * a.nc + ch) * 3 * 128 * TC_C, L::TP); };
+
+  float S[MT][NC];  // dS
+  const int c0 = half * NC, v0 = vt * BV + c0, valid = a.Dv - v0;
+  const bool lone = BV == 32 && vt == a.nvt - 1 && vt % 2 == 0;  // nobody has the other half of the panel
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = mt * 128 + quad * 32 + lane;
+    const float* s = a.dlast ? a.dlast + ((size_t)bn * a.Dk + r) * a.Dv + v0 : nullptr;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) S[mt][c] = s && r < a.Dk && c < valid ? s[c] : 0.0f;
+  }
+  auto put_state = [&]() {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) put_planes<RB, NC>(SS, L::SPLANE, mt * 128 + quad * 32 + lane, c0, S[mt]);
+  };
+  // <S, dS> at a kept state
+  auto put_edge = [&](int e) {
+    float s = 0.0f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const float4* f = (const float4*)(a.sf + (((size_t)bn * a.ne + e) * a.nvt + vt) * MT * 128 * BV) +
+                        (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
+      if (mt * 128 + quad * 32 + lane < a.Dk) {
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) {
+          const float4 x = f[(c / 4) * 128];
+          s = fmaf(x.x, S[mt][c], s);
+          s = fmaf(x.y, S[mt][c + 1], s);
+          s = fmaf(x.z, S[mt][c + 2], s);
+          s = fmaf(x.w, S[mt][c + 3], s);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) a.edge[(((size_t)bn * a.ne + e) * a.nvt + vt) * 8 + warp] = s;
+  };
+  if (nch > 0) {
+    load_kq(nch - 1);
+    load_o(nch - 1);
+    cp_commit();
+    load_tp(nch - 1);
+    cp_commit();
+    put_state();
+    put_edge(0);
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = *slot, row = tm + ((uint32_t)(quad * 32) << 16);
+  constexpr int D1 = 0, D2 = 2 * BV, D3 = 4 * BV;
+  uint32_t parity = 0;
+  bool failed = false;
+  auto wait = [&]() {
+    mbar_wait_bounded<false>(bar, parity, a.wait_limit_ns, a.status, failed);
+    parity ^= 1;
+    tm_fence_after();
+  };
+  for (int ch = nch - 1; ch >= 0; --ch) {
+    const size_t item = (size_t)bn * a.nc + ch, tile = item * a.nvt + vt;
+    const bool more = ch > 0;
+    const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
+    const int live = tc_live(a, b, ch), i = (quad & 1) * 32 + lane;
+    if (KST == 2) cp_wait<1>();  // all but TP
+    else cp_wait<0>();
+    fence_proxy_async_smem();
+    tm_fence_before();
+    __syncthreads();
+    if (tid == 0 && !failed) {
+      tm_fence_after();
+      constexpr uint32_t id = tc_idesc(BV, false, true);
+      for (int p = 0; p < 3; ++p)
+        for (int k = 0; k < a.KP; k += 16)
+          tc_mma(tm + D1 + (p ? BV : 0), tc_desc(kq + (k >> 6) * TC_PANEL + (k & 63) * 2, 16),
+                 tc_desc<RB>(smem_u32(SS) + p * L::SPLANE + k * RB, 16), id, p == 2 || k);
+      tc_commit(bar);
+    }
+    if (KST == 2) {
+      if (more) load_kq(ch - 1);
+      cp_commit();
+    }
+    const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
+    {  // the gradient of the chunk's last state, rounded, in the image of its panel
+      unsigned char* d = (unsigned char*)(a.dSh + (item * a.np + (v0 >> 6)) * a.KP * 64);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 128 + quad * 32 + lane;
+        if (r < a.KP)
+#pragma unroll
+          for (int c = 0; c < NC; c += 8) put_piece(d, r, ((v0 & 63) + c) >> 3, round8(S[mt] + c), lone);
+      }
+    }
+    const float gi = gam[i];
+    float kept[NC];  // z (K's steps) or o (Q's), in fp32
+    {
+      const float4* f = (const float4*)((quad < 2 ? a.zf : a.of) + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
+#pragma unroll
+      for (int c = 0; c < NC; c += 4) {
+        const float4 x = f[(c / 4) * 64];
+        kept[c] = x.x, kept[c + 1] = x.y, kept[c + 2] = x.z, kept[c + 3] = x.w;
+      }
+    }
+    if (quad >= 2) {
+      const float f = gi * a.scale;
+      float d[NC], s = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(OS + img<RB>(i, (c0 + c) >> 3)), d + c);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        s = fmaf(d[c], kept[c], s);
+        d[c] = gi != 0.0f ? f * d[c] : 0.0f;
+      }
+      put_planes<RB, NC>(GS, L::GPLANE, 64 + i, c0, d);
+      a.dots[((tile * 3 + 2) * 2 + half) * TC_C + i] = i < live ? s : 0.0f;
+    }
+    wait();
+    if (quad < 2) {
+      float x[NC];
+      tm_sum<NC>(x, row + D1 + c0, row + D1 + BV + c0);
+      const float f = br[i];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) x[c] = f != 0.0f ? f * x[c] : 0.0f;  // no part of it before a later document
+      put_planes<RB, NC>(GS, L::GPLANE, i, c0, x);
+    }
+    if (KST == 2) cp_wait<1>();  // TP
+    fence_proxy_async_smem();
+    tm_fence_before();
+    __syncthreads();
+    if (tid == 0 && !failed) {
+      tm_fence_after();
+      constexpr uint32_t id = tc_idesc(BV, true, true);
+      auto part = [&](int pa, int pb, uint32_t d, bool first) {  // Tm^T W
+        for (int k = 0; k < TC_C; k += 16)
+          tc_mma(d, tc_desc(smem_u32(TP) + pa * TC_PANEL + k * 128, TC_PANEL),
+                 tc_desc<RB>(smem_u32(GS) + pb * L::GPLANE + k * RB, 16), id, !first || k);
+      };
+      auto direct = [&](int pa, uint32_t d) {  // PT^T dO
+        for (int k = 0; k < TC_C; k += 16)
+          tc_mma(d, tc_desc(smem_u32(TP) + pa * TC_PANEL + (64 + k) * 128, TC_PANEL), tc_desc<RB>(smem_u32(OS) + k * RB, 16), id,
+                 true);
+      };
+      part(0, 0, tm + D2, true);
+      direct(0, tm + D2);
+      part(0, 2, tm + D2 + BV, true);
+      part(1, 1, tm + D2 + BV, false);
+      part(2, 0, tm + D2 + BV, false);
+      direct(2, tm + D2 + BV);
+      part(0, 1, tm + D2 + BV, false);
+      part(1, 0, tm + D2 + BV, false);
+      direct(1, tm + D2 + BV);
+      tc_commit(bar);
+    }
+    const int t = ch * TC_C + i;
+    float v[NC];
+    if (quad < 2) {  // v's row, for dc
+      const bf16* s = (const bf16*)a.v + vat + (size_t)t * vstride + v0;
+#pragma unroll
+      for (int c = 0; c < NC; c += 8) {
+        if (a.Dv % 8 == 0) {
+          widen8(i < live && c < valid ? *(const uint4*)(s + c) : make_uint4(0, 0, 0, 0), v + c);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[c + e] = i < live && c + e < valid ? __bfloat162float(s[c + e]) : 0.0f;
+        }
+      }
+    }
+    wait();
+    if (quad < 2) {
+      float y[NC];
+      tm_sum<NC>(y, row + D2 + c0, row + D2 + BV + c0);
+      float zy = 0.0f, vy = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        zy = fmaf(kept[c], y[c], zy);
+        vy = fmaf(v[c], y[c], vy);
+      }
+      a.dots[((tile * 3 + 0) * 2 + half) * TC_C + i] = zy;
+      a.dots[((tile * 3 + 1) * 2 + half) * TC_C + i] = -vy;
+      if (t < a.T) store_row<NC>((bf16*)a.dv + vat + (size_t)t * vstride + v0, y, valid, a.Dv % 8 == 0);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) y[c] = gi != 0.0f ? -gi * y[c] : 0.0f;
+      put_planes<RB, NC>(GS, L::GPLANE, i, c0, y);
+    }
+    fence_proxy_async_smem();
+    tm_fence_before();
+    __syncthreads();
+    if (tid == 0 && !failed) {
+      tm_fence_after();
+      constexpr uint32_t id = tc_idesc(BV, true, true);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        for (int p = 0; p < 3; ++p)
+          for (int k = 0; k < 2 * TC_C; k += 16)
+            tc_mma(tm + D3 + (2 * mt + (p ? 1 : 0)) * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 128, TC_PANEL),
+                   tc_desc<RB>(smem_u32(GS) + p * L::GPLANE + k * RB, 16), id, p == 2 || k);
+      tc_commit(bar);
+    }
+    if (more) load_o(ch - 1);
+    cp_commit();
+    if (more) load_tp(ch - 1);
+    cp_commit();
+    wait();
+    if (KST == 1) {
+      if (more) load_kq(ch - 1);
+      cp_commit();
+    }
+    const float gC = gam[TC_C - 1];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float d[NC];
+      tm_sum<NC>(d, row + D3 + 2 * mt * BV + c0, row + D3 + (2 * mt + 1) * BV + c0);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
+    }
+    if (more) {
+      put_state();
+      if (ch % TC_EDGE == 0) put_edge(ch / TC_EDGE);
+    }
+  }
+  const int t0 = nch * TC_C, cols = min(BV, a.Dv - vt * BV);
+  for (long long i = tid; i < (long long)(a.T - t0) * cols; i += 256)
+    ((bf16*)a.dv)[vat + (size_t)(t0 + i / cols) * vstride + vt * BV + i % cols] = __float2bfloat16_rn(0.0f);
+  if (a.ds0) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = mt * 128 + quad * 32 + lane;
+      if (r < a.Dk) {
+        float* s = a.ds0 + ((size_t)bn * a.Dk + r) * a.Dv + v0;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (c < valid) s[c] = S[mt][c];
+      }
+    }
+  }
+  cp_wait<0>();
+  tc_finish(bar + 8, a.wait_limit_ns);
+  if (warp == 0) tm_free<512>(tm);
+}
+
+// ---- grad ----------------------------------------------------------------------------
+// TMEM: two accumulators of KT columns; the second one's hold N and F before.
+template <int KT> struct TcGrad {  // KT: Dk rounded up to 128 or 256
+  static constexpr int KQ = KT / 64 * TC_PANEL, SB = KT * 128;  // bytes of KQ and of a panel of S0
+  static constexpr int XZ = TC_PANEL + TC_PANEL / 2;            // a panel of X = [dY; dO] and of Z
+  static __host__ __device__ int at_sd(int np) { return np * XZ > KQ ? np * XZ : KQ; }
+  static __host__ __device__ size_t bytes(int np) { return (size_t)at_sd(np) + 2 * SB + 6 * TC_C * 4 + 64 + 1024; }
+  static constexpr int COLS = KT == 128 ? 256 : 512;
+};
+
+// X and Z stay in shared memory, S0 and dS1 pass by panels of 64 columns of v. N
+// and F go to registers, M and R are made from them while the state's products
+// run, and multiply KQ from the buffers of S0 and dS1, KQ in X's and Z's. The
+// product of Z's 64 rows reads as many rows behind them, whose results are not
+// looked at.
+template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delta_tc_grad_kernel(DeltaTcArgs a) {
+  using L = TcGrad<KT>;
+  extern __shared__ unsigned char sm_raw[];
+  unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char *X = sm, *KQ = sm, *SD = sm + L::at_sd(a.np);
+  float* rec = (float*)(SD + 2 * L::SB);  // chi, clo, seg, gam, br, beta
+  const float* beta = rec + 5 * TC_C;
+  uint64_t* barp = (uint64_t*)(rec + 6 * TC_C);
+  uint32_t* slot = (uint32_t*)(barp + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
+  const long long item = blockIdx.x;
+  const int ch = (int)(item % a.nc), bn = (int)(item / a.nc), n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
+  const int live = tc_live(a, b, ch), steps = min(TC_C, a.T - ch * TC_C);
+  const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv, row0 = (size_t)b * a.T + (size_t)ch * TC_C;
+  const size_t kat = row0 * kstride + (size_t)nk * a.Dk, vat = row0 * vstride + (size_t)n * a.Dv;
+  const bool shared_heads = a.pq != nullptr;
+  const size_t pstride = (size_t)a.N * a.Dk, pat = row0 * pstride + (size_t)n * a.Dk;
+  if (live == 0) {  // nothing of the chunk exists
+    for (int i = tid; i < steps * a.Dk; i += 256) {
+      const int r = i / a.Dk, c = i % a.Dk;
+      if (shared_heads) a.pq[pat + r * pstride + c] = a.pk[pat + r * pstride + c] = 0.0f;
+      else ((bf16*)a.dq)[kat + r * kstride + c] = ((bf16*)a.dk)[kat + r * kstride + c] = __float2bfloat16_rn(0.0f);
+    }
+    return;
+  }
+  const uint32_t bar = smem_u32(barp);
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    mbar_init(bar + 8, 1);
+    fence_mbar_init_cluster();
+  }
+  auto load_sd = [&](int p) {
+    const size_t at = ((size_t)item * a.np + p) * a.KP * 64;
+    load_plain(SD, a.Sh + at, a.KP * 128);
+    load_plain(SD + L::SB, a.dSh + at, a.KP * 128);
+  };
+  for (int p = 0; p < a.np; ++p) {
+    unsigned char* x = X + (size_t)p * L::XZ;
+    load_img<128>(x, 0, (const bf16*)a.dv + vat, vstride, live, a.Dv, p * 64, 8, 0, 256);
+    load_img<128>(x, 64, (const bf16*)(a.dO ? a.dO : a.dv) + vat, vstride, a.dO ? live : 0, a.Dv, p * 64, 8, 0, 256);
+    load_plain(x + TC_PANEL, a.Zh + ((size_t)item * a.np + p) * 64 * 64, 64 * 128);
+  }
+  cp_commit();
+  load_sd(0);
+  cp_commit();
+  if (tid < TC_C) {
+    const float* r = a.rec + (size_t)item * REC_N * TC_C + tid;
+    rec[tid] = r[REC_CHI * TC_C];
+    rec[TC_C + tid] = r[REC_CLO * TC_C];
+    rec[2 * TC_C + tid] = r[REC_SEG * TC_C];
+    rec[3 * TC_C + tid] = r[REC_GAM * TC_C];
+    rec[4 * TC_C + tid] = r[REC_BR * TC_C];
+    rec[5 * TC_C + tid] = r[REC_BETA * TC_C];
+  }
+  if (warp == 0) tm_alloc<L::COLS>(slot);
+  cp_wait<1>();
+  fence_proxy_async_smem();
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = *slot, row = tm + ((uint32_t)(quad * 32) << 16);
+  uint32_t parity = 0;
+  bool failed = false;
+  auto wait = [&]() {
+    mbar_wait_bounded<false>(bar, parity, a.wait_limit_ns, a.status, failed);
+    parity ^= 1;
+    tm_fence_after();
+  };
+  if (tid == 0) {  // [N; F] = X Z^T, in the second accumulator's columns
+    constexpr uint32_t id = tc_idesc(64, false, false);
+    for (int p = 0; p < a.np; ++p)
+      for (int k = 0; k < 64; k += 16) {
+        const uint32_t x = smem_u32(X) + p * L::XZ + k * 2;
+        tc_mma(tm + KT, tc_desc(x, 16), tc_desc(x + TC_PANEL, 16), id, p || k);
+      }
+    tc_commit(bar);
+  }
+  const int i = (quad & 1) * 32 + lane, j0 = half * 32;
+  wait();
+  float nf[32];
+  {
+    uint32_t r[32];
+    tm_ld16(r, row + KT + j0);
+    tm_ld16(r + 16, row + KT + j0 + 16);
+    tm_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) nf[c] = __uint_as_float(r[c]);
+  }
+  for (int p = 0; p < a.np; ++p) {
+    cp_wait<0>();
+    fence_proxy_async_smem();
+    tm_fence_before();
+    __syncthreads();
+    if (tid == 0 && !failed) {
+      tm_fence_after();
+      const uint32_t id = tc_idesc(a.KP, false, false);
+      for (int k = 0; k < 64; k += 16) {
+        const uint32_t x = smem_u32(X) + p * L::XZ + k * 2, s = smem_u32(SD) + k * 2;
+        tc_mma(tm, tc_desc(x, 16), tc_desc(s, 16), id, p || k);                              // [dY; dO] S0^T
+        tc_mma(tm + KT, tc_desc(x + TC_PANEL, 16), tc_desc(s + L::SB, 16), id, p || k);      // Z dS1^T (rows 0 .. 63)
+      }
+      tc_commit(bar);
+    }
+    if (p == 0) {  // R_ij (Q's steps) or M_ij (K's), i the thread's step
+      const float ci = rec[i], li = rec[TC_C + i];
+      const int si = __float_as_int(rec[2 * TC_C + i]);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const int j = j0 + c;
+        const bool on = (quad < 2 ? i > j : i >= j) && si == __float_as_int(rec[2 * TC_C + j]);
+        nf[c] = on ? (quad < 2 ? -nf[c] : a.scale * nf[c]) * expf((ci - rec[j]) + (li - rec[TC_C + j])) * beta[j] : 0.0f;
+      }
+    }
+    wait();
+    if (p + 1 < a.np) {
+      load_sd(p + 1);
+    } else {  // X and Z are done with
+      load_img<128>(KQ, 0, (const bf16*)a.k + kat, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
+      load_img<128>(KQ, 64, (const bf16*)a.q + kat, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
+    }
+    cp_commit();
+  }
+  {  // [M + M^T, R^T; R, 0] over the buffers of S0 and dS1: two panels of 128 rows
+    if (quad >= 2) {
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) {
+        *(uint4*)(SD + img<128>(64 + i, (j0 + c) >> 3)) = round8(nf + c);
+        *(uint4*)(SD + TC_PANEL + img<128>(64 + i, (j0 + c) >> 3)) = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        *(bf16*)(SD + TC_PANEL + img<128>(j0 + c, i >> 3) + (i & 7) * 2) = __float2bfloat16_rn(nf[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const int j = j0 + c;
+        const bf16 m = __float2bfloat16_rn(nf[c]);
+        if (j <= i) *(bf16*)(SD + img<128>(i, j >> 3) + (j & 7) * 2) = m;
+        if (j < i) *(bf16*)(SD + img<128>(j, i >> 3) + (i & 7) * 2) = m;
+      }
+    }
+  }
+  // The state's parts, scaled by rows in fp32, back into the first accumulator
+  const float gi = rec[3 * TC_C + i];
+  const float f0 = quad < 2 ? -gi : a.scale * gi, f1 = quad < 2 ? rec[4 * TC_C + i] : 0.0f;
+  for (int c = half * 16; c < a.KP; c += 32) {
+    uint32_t x[16], h[16];
+    tm_ld16(x, row + c);
+    tm_ld16(h, row + KT + c);
+    tm_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float s = f0 != 0.0f ? f0 * __uint_as_float(x[e]) : 0.0f;
+      if (f1 != 0.0f) s = fmaf(f1, __uint_as_float(h[e]), s);
+      x[e] = __float_as_uint(s);
+    }
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(row + c),
+        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]),
+        "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
+        : "memory");
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+  cp_wait<0>();
+  fence_proxy_async_smem();
+  tm_fence_before();
+  __syncthreads();
+  if (tid == 0 && !failed) {
+    tm_fence_after();
+    const uint32_t id = tc_idesc(a.KP, false, true);
+    for (int k = 0; k < 128; k += 16)
+      tc_mma(tm, tc_desc(smem_u32(SD) + (k >> 6) * TC_PANEL + (k & 63) * 2, 16), tc_desc(smem_u32(KQ) + k * 128, TC_PANEL), id, true);
+    tc_commit(bar);
+  }
+  wait();
+  for (int c = half * 16; c < a.KP; c += 32) {
+    uint32_t r[16];
+    tm_ld16(r, row + c);
+    tm_wait_ld();
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]);
+    if (i < steps) {
+      const int valid = a.Dk - c;
+      if (shared_heads) {
+        float* p = (quad < 2 ? a.pk : a.pq) + pat + (size_t)i * pstride + c;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e < valid) p[e] = x[e];
+      } else {
+        store_row<16>((bf16*)(quad < 2 ? a.dk : a.dq) + kat + (size_t)i * kstride + c, x, valid, a.Dk % 8 == 0);
+      }
+    }
+    __syncwarp();
+  }
+  tc_finish(bar + 8, a.wait_limit_ns);
+  if (warp == 0) tm_free<L::COLS>(tm);
+}
+
+// ---- gates ---------------------------------------------------------------------------
+// dg and dbeta of TC_EDGE chunks, from the last to the first; a thread has a step.
+__global__ void __launch_bounds__(TC_C) delta_tc_gates_kernel(DeltaTcArgs a) {
+  __shared__ float dc[TC_C], from[TC_C], seg_sm[TC_C];
+  const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE, i = threadIdx.x;
+  const int bn = blockIdx.x / groups, gr = blockIdx.x % groups, n = bn % a.N, b = bn / a.N;
+  const int nch = tc_chunks(a, b), lo = gr * TC_EDGE, hi = min(a.nc, lo + TC_EDGE);
+  float e = 0.0f;  // <S, dS> at the end of the chunk at hand
+  if (lo < nch) {
+    const int at = hi >= nch ? 0 : gr + 1;
+    for (int w = 0; w < a.nvt * 8; ++w) e += a.edge[((size_t)bn * a.ne + at) * a.nvt * 8 + w];
+  }
+  for (int ch = hi - 1; ch >= lo; --ch) {
+    const size_t item = (size_t)bn * a.nc + ch;
+    const int t = ch * TC_C + i, live = tc_live(a, b, ch);
+    const size_t out = ((size_t)b * a.T + t) * a.N + n;
+    if (live == 0) {
+      if (t < a.T) a.dg[out] = a.dbeta[out] = 0.0f;
+      continue;
+    }
+    const float* rec = a.rec + item * REC_N * TC_C;
+    float zy = 0.0f, c = 0.0f;
+    for (int vt = 0; vt < a.nvt; ++vt) {
+      const float* d = a.dots + (item * a.nvt + vt) * 6 * TC_C;
+      zy += d[i] + d[TC_C + i];
+      c += (d[2 * TC_C + i] + d[3 * TC_C + i]) + (d[4 * TC_C + i] + d[5 * TC_C + i]);
+    }
+    __syncthreads();
+    dc[i] = c;
+    seg_sm[i] = rec[REC_SEG * TC_C + i];
+    __syncthreads();
+    const int mine = __float_as_int(seg_sm[i]), last = __float_as_int(seg_sm[TC_C - 1]);
+    float s = mine == last ? e : 0.0f;
+    for (int j = TC_C - 1; j >= i; --j)
+      if (__float_as_int(seg_sm[j]) == mine) s += dc[j];
+    from[i] = s;
+    const bool mark = mine != (i ? __float_as_int(seg_sm[i - 1]) : 0);
+    if (t < a.T) {
+      a.dg[out] = i < live && !mark ? s : 0.0f;
+      a.dbeta[out] = i < live ? zy / rec[REC_BETA * TC_C + i] : 0.0f;
+    }
+    __syncthreads();
+    e = __float_as_int(seg_sm[0]) == 0 ? from[0] : 0.0f;  // a chunk that begins a document needs nothing before it
+  }
+}
+
+// dq, dk [rows, Nk, Dk] = sums of pq, pk [rows, Nk, share, Dk], in the heads' order
+__global__ void __launch_bounds__(256) delta_tc_share_kernel(const float* pq, const float* pk, bf16* dq, bf16* dk, long long n,
+                                                             int share, int Dk) {
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    const long long r = i / Dk;
+    const size_t at = (size_t)r * share * Dk + (size_t)(i - r * Dk);
+    float x = 0.0f, y = 0.0f;
+    for (int s = 0; s < share; ++s) {
+      x += pq[at + (size_t)s * Dk];
+      y += pk[at + (size_t)s * Dk];
+    }
+    dq[i] = __float2bfloat16_rn(x);
+    dk[i] = __float2bfloat16_rn(y);
+  }
+}
+
+template <int BV, int MT> cudaError_t back(const DeltaTcArgs& a, cudaStream_t st) {
+  constexpr int sm = TcBack<BV, MT>::BYTES;
+  cudaError_t e = set_smem_attr((const void*)delta_tc_back_kernel<BV, MT>, sm);
+  if (e != cudaSuccess) return e;
+  delta_tc_back_kernel<BV, MT><<<(unsigned)(a.B * a.N * a.nvt), 256, sm, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+template <int KT> cudaError_t grad(const DeltaTcArgs& a, cudaStream_t st) {
+  const size_t sm = TcGrad<KT>::bytes(a.np);
+  cudaError_t e = set_smem_attr((const void*)delta_tc_grad_kernel<KT>, sm);
+  if (e != cudaSuccess) return e;
+  delta_tc_grad_kernel<KT><<<(unsigned)((long long)a.B * a.N * a.nc), 256, sm, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t delta_tc_bwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st) {
+  cudaError_t e = a.KP > 128 ? back<32, 2>(a, st) : BV == 64 ? back<64, 1>(a, st) : back<32, 1>(a, st);
+  if (e != cudaSuccess) return e;
+  if ((e = a.KP > 128 ? grad<256>(a, st) : grad<128>(a, st)) != cudaSuccess) return e;
+  const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE;
+  delta_tc_gates_kernel<<<(unsigned)(a.B * a.N * groups), TC_C, 0, st>>>(a);
+  note_launch();
+  if ((e = cudaGetLastError()) != cudaSuccess || !a.pq) return e;
+  const long long n = (long long)a.B * a.T * a.Nk * a.Dk, blocks = (n + 255) / 256, most = 16LL * device_sms();
+  delta_tc_share_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(a.pq, a.pk, (bf16*)a.dq, (bf16*)a.dk, n,
+                                                                                a.N / a.Nk, a.Dk);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace rnn

@@ -1,0 +1,437 @@
+// Gated delta rule, bf16 storage, forward (delta_tc.cuh has the formulas).
+//   prep   every chunk by itself: TP and the per-step factors
+//   chain  per head and tile of BV columns of v, the chunks one after the other:
+//          o and the state, and what a backward needs
+#include "delta.h"
+#include "delta_tc.cuh"
+
+namespace rnn {
+namespace {
+
+// ---- prep --------------------------------------------------------------------------
+__host__ __device__ constexpr size_t prep_smem(int KP) {
+  return (size_t)2 * TC_C * (KP + 8) * 2 + (size_t)2 * TC_C * (TC_C + 4) * 4 + REC_N * TC_C * 4;
+}
+
+// A warp takes 16 rows of K K^T and Q K^T (mma.sync). Tm by forward substitution,
+// a column to a thread with its values in registers, and PT from it.
+__global__ void __launch_bounds__(128) delta_tc_prep_kernel(DeltaTcArgs a) {
+  constexpr int C = TC_C, NT = C / 8, LDF = C + 4;
+  extern __shared__ __align__(16) unsigned char sm_raw[];
+  const int LDK = a.KP + 8, kplane = C * LDK;
+  bf16* Ks = (bf16*)sm_raw;
+  bf16* Qs = Ks + kplane;
+  float* Lf = (float*)(Qs + kplane);  // [C][LDF]
+  float* Pf = Lf + C * LDF;           // [C][LDF]
+  float* rec = Pf + C * LDF;          // [REC_N][C]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long item = blockIdx.x;
+  if (item == 0 && tid == 0) *a.status = 0;  // the kernels behind this one report there
+  const int ch = (int)(item % a.nc), bn = (int)(item / a.nc), n = bn % a.N, b = bn / a.N;
+  const int live = tc_live(a, b, ch);
+  if (live == 0) return;
+  const size_t stride = (size_t)a.Nk * a.Dk;
+  const size_t at = ((size_t)b * a.T + (size_t)ch * C) * stride + (size_t)(n / (a.N / a.Nk)) * a.Dk;
+  load_rows<bf16, C>(Ks, LDK, kplane, (const bf16*)a.k + at, stride, live, a.Dk, 0, a.KP);
+  load_rows<bf16, C>(Qs, LDK, kplane, (const bf16*)a.q + at, stride, live, a.Dk, 0, a.KP);
+  cp_commit();
+  if (warp == 0) {  // the running sum of g, in 64 bits, and the documents
+    double run = 0.0, cs[2];
+    int seg = 0, sg[2];
+    float chi[2], clo[2], be[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = h * 32 + lane;
+      float g = 0.0f;
+      bool mark = false;
+      be[h] = 0.0f;
+      if (i < live) {
+        const size_t row = (size_t)b * a.T + (size_t)ch * C + i;
+        g = a.g[row * a.N + n];
+        be[h] = a.beta[row * a.N + n];
+        if (be[h] == 0.0f) be[h] = 0x1p-60f;
+        mark = a.reset && a.reset[row];
+        if (g < -104.0f) mark = true;  // exp(g) is 0
+        if (mark) g = 0.0f;
+      }
+      double c = (double)g;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += v;
+      }
+      c += run;
+      run = __shfl_sync(0xffffffffu, c, 31);
+      const unsigned m = __ballot_sync(0xffffffffu, mark);
+      sg[h] = seg + __popc(m & (0xffffffffu >> (31 - lane)));
+      seg += __popc(m);
+      cs[h] = c;
+      chi[h] = (float)c;
+      clo[h] = (float)(c - (double)chi[h]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = h * 32 + lane;
+      const float rho = sg[h] == seg ? expf((float)(run - cs[h])) : 0.0f;
+      rec[REC_CHI * C + i] = chi[h];
+      rec[REC_CLO * C + i] = clo[h];
+      rec[REC_SEG * C + i] = __int_as_float(sg[h]);
+      rec[REC_GAM * C + i] = sg[h] == 0 ? expf((float)cs[h]) : 0.0f;
+      rec[REC_RHO * C + i] = rho;
+      rec[REC_BETA * C + i] = be[h];
+      rec[REC_BR * C + i] = be[h] * rho;
+    }
+  }
+  cp_wait<0>();
+  __syncthreads();
+  for (int i = tid; i < REC_N * C; i += 128) a.rec[(size_t)item * REC_N * C + i] = rec[i];
+  const Opnd K = opnd(Ks, LDK, kplane), Q = opnd(Qs, LDK, kplane);
+  const int m0 = warp * 16;
+  float kk[NT][4], qk[NT][4];
+  zero(kk);
+  zero(qk);
+  mma_acc<NT, 1, 1, false, true>(kk, K, m0, K, 0, a.KP);
+  mma_acc<NT, 1, 1, false, true>(qk, Q, m0, K, 0, a.KP);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = m0 + (lane >> 2) + 8 * h;
+    const float ci = rec[REC_CHI * C + i], li = rec[REC_CLO * C + i];
+    const int si = __float_as_int(rec[REC_SEG * C + i]);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = t * 8 + (lane & 3) * 2 + e;
+        const bool on = i >= j && si == __float_as_int(rec[REC_SEG * C + j]);
+        const float gb = on ? expf((ci - rec[REC_CHI * C + j]) + (li - rec[REC_CLO * C + j])) * rec[REC_BETA * C + j] : 0.0f;
+        Pf[i * LDF + j] = on ? a.scale * qk[t][2 * h + e] * gb : 0.0f;
+        Lf[i * LDF + j] = on && i > j ? kk[t][2 * h + e] * gb : 0.0f;
+      }
+  }
+  __syncthreads();
+  unsigned char* tp = (unsigned char*)(a.tp + (size_t)item * 3 * 128 * C);
+  auto put = [&](int r, float x) {
+    const uint32_t to = img<128>(r, tid >> 3) + (tid & 7) * 2;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      const bf16 h = __float2bfloat16_rn(x);
+      *(bf16*)(tp + p * TC_PANEL + to) = h;
+      x -= __bfloat162float(h);
+    }
+  };
+  if (tid < C) {
+    float x[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float s[4] = {i == tid ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < i; k += 4) {
+        const float4 l = *(const float4*)(Lf + i * LDF + k);
+        s[0] -= l.x * x[k];
+        if (k + 1 < i) s[1] -= l.y * x[k + 1];
+        if (k + 2 < i) s[2] -= l.z * x[k + 2];
+        if (k + 3 < i) s[3] -= l.w * x[k + 3];
+      }
+      x[i] = (s[0] + s[1]) + (s[2] + s[3]);
+      put(i, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k <= i; k += 4) {
+        const float4 l = *(const float4*)(Pf + i * LDF + k);
+        s[0] += l.x * x[k];
+        if (k + 1 <= i) s[1] += l.y * x[k + 1];
+        if (k + 2 <= i) s[2] += l.z * x[k + 2];
+        if (k + 3 <= i) s[3] += l.w * x[k + 3];
+      }
+      put(C + i, (s[0] + s[1]) + (s[2] + s[3]));
+    }
+  }
+}
+
+// ---- chain --------------------------------------------------------------------------
+template <int BV, int MT> struct TcChain {
+  static constexpr int RB = 2 * BV, KST = MT == 1 ? 2 : 1;  // bytes of a tile's row; stages of KQ
+  static constexpr int KQ = 2 * MT * TC_PANEL, TP = 3 * TC_PANEL, SPLANE = MT * 128 * RB, YPLANE = 64 * RB;
+  static constexpr int AT_TP = KST * KQ, AT_S = AT_TP + TP, AT_Y = AT_S + 3 * SPLANE, AT_V = AT_Y + 3 * YPLANE;
+  static constexpr int AT_REC = AT_V + YPLANE, BYTES = AT_REC + 2 * 2 * 64 * 4 + 64 + 1024;
+};
+
+// 8 warps: warp w has lanes 32 (w % 4) .. of the accumulators (rows 0 .. 63: K's
+// steps, 64 .. 127: Q's; or rows of the state) and half of the tile's columns.
+// One thread issues the products, the rest of the CTA loads the next chunk
+// meanwhile. MT: tiles of 128 state rows, whose fp32 values stay in registers.
+// A chunk is three dependent products (1900 cycles of tensor cores for BV = 64,
+// Dk = 128) and their ways through registers, one after the other.
+template <int BV, int MT>
+__global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
+  using L = TcChain<BV, MT>;
+  constexpr int RB = L::RB, NC = BV / 2, KST = L::KST;
+  extern __shared__ unsigned char sm_raw[];
+  unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *YS = sm + L::AT_Y, *VS = sm + L::AT_V;
+  float* recs = (float*)(sm + L::AT_REC);  // [2][gam, br][64]
+  uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
+  uint32_t* slot = (uint32_t*)(barp + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
+  const int vt = blockIdx.x % a.nvt, bn = blockIdx.x / a.nvt, n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
+  const int nch = tc_chunks(a, b);
+  const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv;
+  const size_t kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
+  const uint32_t bar = smem_u32(barp);
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    mbar_init(bar + 8, 1);
+    fence_mbar_init_cluster();
+  }
+  if (warp == 0) tm_alloc<512>(slot);
+  auto load_kq = [&](int ch) {
+    unsigned char* d = sm + (ch % KST) * L::KQ;
+    const int live = tc_live(a, b, ch);
+    load_img<128>(d, 0, (const bf16*)a.k + kat + (size_t)ch * TC_C * kstride, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
+    load_img<128>(d, 64, (const bf16*)a.q + kat + (size_t)ch * TC_C * kstride, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
+  };
+  auto load_v = [&](int ch) {
+    load_img<RB>(VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv, vt * BV, BV / 8,
+                 0, 256);
+    const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
+    float* d = recs + (ch & 1) * 2 * TC_C;
+    if (tid < 16) cp16(smem_u32(d + tid * 4), r + REC_GAM * TC_C + tid * 4, true);
+    else if (tid < 32) cp16(smem_u32(d + tid * 4), r + REC_BR * TC_C + (tid - 16) * 4, true);
+  };
+  auto load_tp = [&](int ch) { load_plain(TP, a.tp + ((size_t)bn * a.nc + ch) * 3 * 128 * TC_C, L::TP); };
+
+  float S[MT][NC];
+  const int c0 = half * NC, v0 = vt * BV + c0;  // this thread's columns, in the tile and in v
+  const int valid = a.Dv - v0;
+  const bool lone = BV == 32 && vt == a.nvt - 1 && vt % 2 == 0;  // nobody has the other half of the panel
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = mt * 128 + quad * 32 + lane;
+    const float* s = a.s0 ? a.s0 + ((size_t)bn * a.Dk + r) * a.Dv + v0 : nullptr;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) S[mt][c] = s && r < a.Dk && c < valid ? s[c] : 0.0f;
+  }
+  auto put_state = [&]() {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) put_planes<RB, NC>(SS, L::SPLANE, mt * 128 + quad * 32 + lane, c0, S[mt]);
+  };
+  if (nch > 0) {
+    load_kq(0);
+    load_v(0);
+    cp_commit();
+    load_tp(0);
+    cp_commit();
+    put_state();
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = *slot, row = tm + ((uint32_t)(quad * 32) << 16);
+  // accumulators: D1 (K S0, Q S0), D2 (Z, PT Y), D3 (the state's change, by tile), each hi and lo
+  constexpr int D1 = 0, D2 = 2 * BV, D3 = 4 * BV;
+  uint32_t parity = 0;
+  bool failed = false;
+  auto wait = [&]() {
+    mbar_wait_bounded<false>(bar, parity, a.wait_limit_ns, a.status, failed);
+    parity ^= 1;
+    tm_fence_after();
+  };
+  for (int ch = 0; ch < nch; ++ch) {
+    const size_t item = (size_t)bn * a.nc + ch, tile = item * a.nvt + vt;
+    const bool more = ch + 1 < nch;
+    const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
+    if (KST == 2) cp_wait<1>();  // all but TP
+    else cp_wait<0>();
+    fence_proxy_async_smem();
+    tm_fence_before();
+    __syncthreads();
+    if (tid == 0 && !failed) {
+      tm_fence_after();
+      constexpr uint32_t id = tc_idesc(BV, false, true);
+      for (int p = 0; p < 3; ++p)
+        for (int k = 0; k < a.KP; k += 16)
+          tc_mma(tm + D1 + (p ? BV : 0), tc_desc(kq + (k >> 6) * TC_PANEL + (k & 63) * 2, 16),
+                 tc_desc<RB>(smem_u32(SS) + p * L::SPLANE + k * RB, 16), id, p == 2 || k);
+      tc_commit(bar);
+    }
+    if (KST == 2) {
+      if (more) load_kq(ch + 1);
+      cp_commit();
+    }
+    const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
+    if (a.Sh) {  // the chunk's starting state, rounded, in the image of its panel
+      unsigned char* d = (unsigned char*)(a.Sh + (item * a.np + (v0 >> 6)) * a.KP * 64);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 128 + quad * 32 + lane;
+        if (r < a.KP)
+#pragma unroll
+          for (int c = 0; c < NC; c += 8) put_piece(d, r, ((v0 & 63) + c) >> 3, round8(S[mt] + c), lone);
+      }
+    }
+    wait();
+    const int i = (quad & 1) * 32 + lane;  // this thread's step
+    const float gi = gam[i];
+    float x[NC];
+    tm_sum<NC>(x, row + D1 + c0, row + D1 + BV + c0);
+    if (quad < 2) {
+      float y[NC];
+#pragma unroll
+      for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(VS + img<RB>(i, (c0 + c) >> 3)), y + c);
+      if (gi != 0.0f)  // behind a reset the old state has no part, whatever it holds
+#pragma unroll
+        for (int c = 0; c < NC; ++c) y[c] = fmaf(-gi, x[c], y[c]);
+      put_planes<RB, NC>(YS, L::YPLANE, i, c0, y);
+    } else {
+      const float f = gi * a.scale;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) x[c] = gi != 0.0f ? f * x[c] : 0.0f;
+    }
+    if (KST == 2) cp_wait<1>();  // TP
+    fence_proxy_async_smem();
+    tm_fence_before();
+    __syncthreads();
+    if (tid == 0 && !failed) {
+      tm_fence_after();
+      constexpr uint32_t id = tc_idesc(BV, false, true);
+      auto part = [&](int pa, int pb, uint32_t d, bool first) {
+        for (int k = 0; k < TC_C; k += 16)
+          tc_mma(d, tc_desc(smem_u32(TP) + pa * TC_PANEL + k * 2, 16), tc_desc<RB>(smem_u32(YS) + pb * L::YPLANE + k * RB, 16), id,
+                 !first || k);
+      };
+      part(0, 0, tm + D2, true);
+      part(0, 2, tm + D2 + BV, true);
+      part(1, 1, tm + D2 + BV, false);
+      part(2, 0, tm + D2 + BV, false);
+      part(0, 1, tm + D2 + BV, false);
+      part(1, 0, tm + D2 + BV, false);
+      tc_commit(bar);
+    }
+    if (more) load_v(ch + 1);
+    cp_commit();
+    wait();
+    float z[NC];
+    tm_sum<NC>(z, row + D2 + c0, row + D2 + BV + c0);
+    if (quad < 2) {
+      if (a.Zh) {
+        unsigned char* d = (unsigned char*)(a.Zh + (item * a.np + (v0 >> 6)) * 64 * 64);
+        float4* f = (float4*)(a.zf + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
+#pragma unroll
+        for (int c = 0; c < NC; c += 8) put_piece(d, i, ((v0 & 63) + c) >> 3, round8(z + c), lone);
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
+      }
+      const float f = br[i];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) z[c] *= f;
+      put_planes<RB, NC>(YS, L::YPLANE, i, c0, z);  // the products have read Y
+    } else {
+      const int t = ch * TC_C + i;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) z[c] += x[c];
+      if (a.of) {
+        float4* f = (float4*)(a.of + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
+      }
+      if (t < a.T) {
+        if (i >= tc_live(a, b, ch))
+#pragma unroll
+          for (int c = 0; c < NC; ++c) z[c] = 0.0f;
+        store_row<NC>((bf16*)a.o + vat + (size_t)t * vstride + v0, z, valid, a.Dv % 8 == 0);
+      }
+    }
+    fence_proxy_async_smem();
+    tm_fence_before();
+    __syncthreads();
+    if (tid == 0 && !failed) {
+      tm_fence_after();
+      constexpr uint32_t id = tc_idesc(BV, true, true);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        for (int p = 0; p < 3; ++p)
+          for (int k = 0; k < TC_C; k += 16)
+            tc_mma(tm + D3 + (2 * mt + (p ? 1 : 0)) * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 128, TC_PANEL),
+                   tc_desc<RB>(smem_u32(YS) + p * L::YPLANE + k * RB, 16), id, p == 2 || k);
+      tc_commit(bar);
+    }
+    if (more) load_tp(ch + 1);
+    cp_commit();
+    wait();
+    if (KST == 1) {
+      if (more) load_kq(ch + 1);
+      cp_commit();
+    }
+    const float gC = gam[TC_C - 1];
+    const int end = ch + 1 == nch ? 0 : (ch + 1) % TC_EDGE == 0 ? (ch + 1) / TC_EDGE : -1;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float d[NC];
+      tm_sum<NC>(d, row + D3 + 2 * mt * BV + c0, row + D3 + (2 * mt + 1) * BV + c0);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
+      if (a.sf && end >= 0) {
+        float4* f = (float4*)(a.sf + (((size_t)bn * a.ne + end) * a.nvt + vt) * MT * 128 * BV) +
+                    (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) f[(c / 4) * 128] = make_float4(S[mt][c], S[mt][c + 1], S[mt][c + 2], S[mt][c + 3]);
+      }
+    }
+    if (more) put_state();
+  }
+  // steps past the row's length
+  const int t0 = nch * TC_C, cols = min(BV, a.Dv - vt * BV);
+  for (long long i = tid; i < (long long)(a.T - t0) * cols; i += 256)
+    ((bf16*)a.o)[vat + (size_t)(t0 + i / cols) * vstride + vt * BV + i % cols] = __float2bfloat16_rn(0.0f);
+  if (a.last) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = mt * 128 + quad * 32 + lane;
+      if (r < a.Dk) {
+        float* s = a.last + ((size_t)bn * a.Dk + r) * a.Dv + v0;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (c < valid) s[c] = S[mt][c];
+      }
+    }
+  }
+  if (nch == 0 && a.sf) {  // no chunk: the end is the start
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float4* f = (float4*)(a.sf + ((size_t)bn * a.ne * a.nvt + vt) * MT * 128 * BV) +
+                  (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
+#pragma unroll
+      for (int c = 0; c < NC; c += 4) f[(c / 4) * 128] = make_float4(S[mt][c], S[mt][c + 1], S[mt][c + 2], S[mt][c + 3]);
+    }
+  }
+  cp_wait<0>();
+  tc_finish(bar + 8, a.wait_limit_ns);
+  if (warp == 0) tm_free<512>(tm);
+}
+
+template <int BV, int MT> cudaError_t chain(const DeltaTcArgs& a, cudaStream_t st) {
+  constexpr int sm = TcChain<BV, MT>::BYTES;
+  cudaError_t e = set_smem_attr((const void*)delta_tc_chain_kernel<BV, MT>, sm);
+  if (e != cudaSuccess) return e;
+  delta_tc_chain_kernel<BV, MT><<<(unsigned)(a.B * a.N * a.nvt), 256, sm, st>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t delta_tc_fwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st) {
+  const size_t sm = prep_smem(a.KP);
+  cudaError_t e = set_smem_attr((const void*)delta_tc_prep_kernel, sm);
+  if (e != cudaSuccess) return e;
+  delta_tc_prep_kernel<<<(unsigned)((long long)a.B * a.N * a.nc), 128, sm, st>>>(a);
+  note_launch();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.KP > 128) return chain<32, 2>(a, st);
+  return BV == 64 ? chain<64, 1>(a, st) : chain<32, 1>(a, st);
+}
+
+}  // namespace rnn

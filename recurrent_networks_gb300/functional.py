@@ -387,26 +387,27 @@ def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=
 
 
 # ---- gated delta rule ----------------------------------------------------------------
-def _delta_run(q, k, v, g, beta, state, reset, lengths, scale):
-    """(o, last, q and k as the library took them, plan, tape)."""
+def _delta_run(q, k, v, g, beta, state, reset, lengths, scale, status, keep):
+    """(o, last, q, k and v as the library took them, plan, tape)."""
     B, T, Nk, Dk = q.shape
     N, Dv = v.shape[2:]
     plan = _lib.delta_plan(B, T, Nk, N, Dk, Dv, q.dtype, _lib.check_device(q))
     q, k, v, g, beta, state = (_dense(t) for t in (q, k, v, g, beta, state))
-    o = torch.empty_like(v)
+    o = q.new_empty((B, T, N, Dv))
     last = torch.empty((B, 1, N, Dk, Dv), dtype=torch.float32, device=v.device)
-    tape = torch.empty(plan[1], dtype=torch.uint8, device=v.device)
-    _lib.rnn_delta_fwd(plan[0], q, k, v, g, beta, state, reset, lengths, scale, o, last, tape)
-    return o, last, q, k, plan, tape
+    tape = torch.empty(plan[2 if keep else 1], dtype=torch.uint8, device=v.device)
+    _lib.rnn_delta_fwd(plan[0], q, k, v, g, beta, state, reset, lengths, scale, o, last, keep, tape)
+    _add_status(status, tape)
+    return o, last, q, k, v, plan, tape
 
 
 class _DeltaFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, g, beta, state, reset, lengths, scale):
-        o, last, q, k, ctx.plan, tape = _delta_run(q, k, v, g, beta, state, reset, lengths, scale)
-        ctx.scale, ctx.shape = scale, v.shape
+    def forward(ctx, q, k, v, g, beta, state, reset, lengths, scale, status):
+        o, last, q, k, v, ctx.plan, tape = _delta_run(q, k, v, g, beta, state, reset, lengths, scale, status, True)
+        ctx.scale, ctx.status = scale, status
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(q, k, lengths, tape)
+        ctx.save_for_backward(q, k, v, lengths, tape)
         return o, last
 
     @staticmethod
@@ -416,15 +417,16 @@ class _DeltaFn(torch.autograd.Function):
 
 def _delta_bwd(ctx, do, dlast):
     _first_order(do, dlast)
-    q, k, lengths, tape = ctx.saved_tensors
-    dims, _, size = ctx.plan
-    B, T, N, Dv = ctx.shape
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), q.new_empty(ctx.shape)
+    q, k, v, lengths, tape = ctx.saved_tensors
+    dims, _, _, size = ctx.plan
+    B, T, N, Dv = v.shape
+    dq, dk, dv = q.new_empty(q.shape), q.new_empty(q.shape), q.new_empty(v.shape)
     dg, dbeta = (torch.empty((B, T, N), dtype=torch.float32, device=q.device) for _ in range(2))
     ds = torch.empty((B, 1, N, q.shape[3], Dv), dtype=torch.float32, device=q.device) if ctx.needs_input_grad[5] else None
     ws = torch.empty(size, dtype=torch.uint8, device=q.device)
-    _lib.rnn_delta_bwd(dims, q, k, lengths, ctx.scale, tape, _dense(do), _dense(dlast), dq, dk, dv, dg, dbeta, ds, ws)
-    return dq, dk, dv, dg, dbeta, ds, None, None, None
+    _lib.rnn_delta_bwd(dims, q, k, v, lengths, ctx.scale, tape, _dense(do), _dense(dlast), dq, dk, dv, dg, dbeta, ds, ws)
+    _add_status(ctx.status, tape)
+    return dq, dk, dv, dg, dbeta, ds, None, None, None, None
 
 
 _delta_bwd_once = once_differentiable(_delta_bwd)
@@ -458,7 +460,7 @@ def _delta_shapes(q, k, v, g, beta, lead):
     return Nk, N, Dk, Dv
 
 
-def gated_delta(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=None):
+def gated_delta(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=None, status=None):
     """Gated delta rule: a scan whose state is a matrix S [Dk,Dv] per head,
     u_t = beta_t (v_t - a_t S_{t-1}^T k_t), S_t = a_t S_{t-1} + k_t u_t^T,
     o_t = scale S_t^T q_t, a_t = exp(g_t).
@@ -472,8 +474,12 @@ def gated_delta(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=No
     (packed documents), whatever it holds. lengths [B]: row b has lengths[b]
     steps; past them nothing is looked at, o is zero and the state is kept.
     Returns (o [B,T,N,Dv], last [B,1,N,Dk,Dv]: the state after the last step,
-    fp32). Differentiable in q, k, v, g, beta and state. An infinity or a NaN in
-    an input may reach every step of its row and head."""
+    fp32). Differentiable in q, k, v, g, beta and state; what is fp32 is fp32
+    throughout, bf16 gradients of q and k come from operands rounded to bf16 once.
+    An infinity or a NaN in an input may reach every step of its row and head.
+    status: an int32 CUDA tensor of one element, zeroed by the caller, in which
+    the forward and the backward record a device-side wait that ran out (their
+    results are then not valid); _lib.rnn_check_status(status) raises for it."""
     _on_gpu(q, "gated_delta")
     if q.dim() != 4:
         raise ValueError(f"q must be [B,T,Nk,Dk], got shape {tuple(q.shape)}")
@@ -486,6 +492,7 @@ def gated_delta(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=No
             raise ValueError("state must be on q's device")
         if state.dtype != torch.float32:
             state = state.float()
+    _check_status(status, q)
     reset, lengths = _marks(reset, lengths, B, T, q, "q")
     scale = Dk ** -0.5 if scale is None else float(scale)
     if g.dtype != torch.float32:
@@ -493,8 +500,8 @@ def gated_delta(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=No
     if beta.dtype != torch.float32:
         beta = beta.float()
     if _tracked(q, k, v, g, beta, state):
-        return _DeltaFn.apply(q, k, v, g, beta, state, reset, lengths, scale)
-    return _delta_run(q, k, v, g, beta, state, reset, lengths, scale)[:2]
+        return _DeltaFn.apply(q, k, v, g, beta, state, reset, lengths, scale, status)
+    return _delta_run(q, k, v, g, beta, state, reset, lengths, scale, status, False)[:2]
 
 
 def gated_delta_step(q, k, v, g, beta, pool, slots=None, scale=None, pool_out=None, status=None):

@@ -1,15 +1,23 @@
 """GPU parity of the gated delta rule (forward, backward, single-token step)
 with its fp64 oracle, and what its calls promise.
 
-Tolerances. Every product's operands are held to 2^-17 of their values (bf16
-storage; 2^-24 for fp32) and summed in fp32. An element of an output is a sum
-over the earlier steps of a chain of products; with unit keys and beta in (0, 1)
-every factor of the recurrence is a contraction, so the errors of its steps add
-up without growing: at most as many as there are steps, 1 / (1 - decay) of them
-in a memory that fades, and the triangular inverse of a chunk doubles them a few
-times. Normwise-max 2^-17 * 32 (bf16's fp32 outputs: 2.4e-4) and 2^-24 * (64 +
-T / 4) (fp32). bf16 outputs are rounded once on top, by 2^-8 of the element at
-most: L2 3e-3 (a uniform rounding is 1.7e-3), normwise-max 2^-8 + 2.4e-4."""
+Tolerances. Every product's operands are held to 2^-24 of their values and
+summed in fp32. An element of an output is a sum over the earlier steps of a
+chain of products; with unit keys and beta in (0, 1) every factor of the
+recurrence is a contraction, so the errors of its steps add up without growing,
+and the triangular inverse of a chunk doubles them a few times: normwise-max
+2^-24 * (64 + T / 4) for fp32 outputs of either storage. dg of bf16 storage is a
+sum of up to 8 * 64 row products that cancel where memories are short, 2^-24 *
+sqrt(512) = 23 times 2^-24 of a row product each: 2^-24 * (256 + T / 4). bf16
+outputs are rounded once on top, by 2^-8 of the element at most: L2 3e-3 (a
+uniform rounding is 1.7e-3), normwise-max 2^-8 + the above. dq and dk of bf16
+storage are sums of products of two operands that were rounded to bf16 once (dY,
+Z, S0, dS1), inside a chunk of three (dY, Z, and M or R): 1.7e-3 each,
+independently, sqrt(3 + 1) * 1.7e-3 = 3.4e-3 with the output's own: L2 4e-3; the
+normwise maximum four roundings of 2^-8. Those roundings are of the terms, and
+dq = scale (D dO + k u.dO) and dk = dS u - D dv (D the decayed state) are sums of
+two that can cancel where a head has few channels: the two are measured against
+the larger of the sum and its terms."""
 import numpy as np
 import pytest
 import torch
@@ -23,7 +31,7 @@ BF, F32 = torch.bfloat16, torch.float32
 NAMES = ("o", "last", "dq", "dk", "dv", "dg", "dbeta", "dstate")
 
 
-def close(got, ref, what, T, storage):
+def close(got, ref, what, T, storage, terms=()):
     ref = np.asarray(ref, dtype=np.float64)
     assert tuple(got.shape) == ref.shape, what
     out = got.dtype
@@ -31,12 +39,13 @@ def close(got, ref, what, T, storage):
     assert np.isfinite(got).all(), what
     if ref.size == 0:
         return
-    top = max(np.abs(ref).max(), 1e-30)
+    top = max([np.abs(x).max() for x in (ref, *terms)] + [1e-30])
     worst = np.abs(got - ref).max() / top
-    l2 = np.linalg.norm(got - ref) / max(np.linalg.norm(ref), 1e-30)
-    inner = 2.0 ** -24 * (64 + T / 4) if storage == F32 else 2.0 ** -17 * 32
+    l2 = np.linalg.norm(got - ref) / max([np.linalg.norm(x) for x in (ref, *terms)] + [1e-30])
+    inner = 2.0 ** -24 * ((256 if what == "dg" and storage == BF else 64) + T / 4)
     if out == BF:
-        assert l2 <= 3e-3 and worst <= 2.0 ** -8 + inner, f"{what}: L2 {l2:.3g}, max {worst:.3g}"
+        rounds = 4 if what in ("dq", "dk") else 1
+        assert l2 <= (4e-3 if rounds > 1 else 3e-3) and worst <= rounds * 2.0 ** -8 + inner, f"{what}: L2 {l2:.3g}, max {worst:.3g}"
     else:
         assert worst <= inner, f"{what}: max {worst:.3g} > {inner:.3g}"
 
@@ -77,8 +86,10 @@ def oracle(p, reset=None, lengths=None, scale=None):
 
 def check(p, reset=None, lengths=None, scale=None):
     got = run(p, reset, lengths, scale)
-    for name, a, r in zip(NAMES, got, oracle(p, reset, lengths, scale)):
-        close(a, r, name, p["q"].shape[1], p["q"].dtype)
+    *ref, parts = oracle(p, reset, lengths, scale)
+    for name, a, r in zip(NAMES, got, ref):
+        terms = parts[:2] if name == "dq" else parts[2:] if name == "dk" else ()
+        close(a, r, name, p["q"].shape[1], p["q"].dtype, terms)
     return got
 
 
