@@ -22,8 +22,10 @@
 //
 // The states, o, dY and all that fp32 outputs follow from are held to fp32: the
 // computed operands (S, Y, Z, TP, ...) in three bf16 planes, plane pairs (i, j)
-// with i + j < 3 summed, the pair (0, 0) in an accumulator of its own (delta.cuh
-// says why). dQ and dK, bf16 themselves, are taken from operands rounded to bf16
+// with i + j < 3 summed, those of equal i + j in an accumulator of their own
+// (delta.cuh says why). An operand's planes are one operand of three times the
+// columns: the other operand is read once for all three (a 128 x 64 x 16 product
+// reads 6 KB of shared memory in the time it multiplies 4 KB). dQ and dK, bf16 themselves, are taken from operands rounded to bf16
 // once (dY, Z, S0, dS1, M, R).
 //
 // Shared-memory images are rows of 128 bytes (64 columns; 64 bytes where a tile
@@ -88,17 +90,18 @@ __device__ __forceinline__ void tm_ld16(uint32_t* r, uint32_t at) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at));
 }
-// x[N] = the sum of the accumulators at hi and lo, N columns of the warp's lanes
-template <int N> __device__ __forceinline__ void tm_sum(float (&x)[N], uint32_t hi, uint32_t lo) {
-  uint32_t a[N], b[N];
+// x[N] = the sum of N columns, from column at on, of the three accumulators, STEP
+// columns apart, that an operand's planes have
+template <int N, int STEP> __device__ __forceinline__ void tm_sum(float (&x)[N], uint32_t at) {
 #pragma unroll
   for (int c = 0; c < N; c += 16) {
-    tm_ld16(a + c, hi + c);
-    tm_ld16(b + c, lo + c);
-  }
-  tm_wait_ld();
+    uint32_t a[3][16];
 #pragma unroll
-  for (int c = 0; c < N; ++c) x[c] = __uint_as_float(a[c]) + __uint_as_float(b[c]);
+    for (int p = 0; p < 3; ++p) tm_ld16(a[p], at + p * STEP + c);
+    tm_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[c + e] = __uint_as_float(a[0][e]) + (__uint_as_float(a[1][e]) + __uint_as_float(a[2][e]));
+  }
 }
 
 // Instruction of 128 x n products, bf16 operands, fp32 accumulator.
@@ -107,7 +110,9 @@ __device__ __forceinline__ constexpr uint32_t tc_idesc(int n, bool a_mn, bool b_
          (8u << 24);
 }
 // Operand at `at`. K-major (rows = outer index): lbo 16; MN-major (rows = summed
-// index): lbo the distance of the panels. RB: bytes of a row.
+// index): lbo the distance of the panels, or of the planes that make one operand
+// of three times the columns. RB: bytes of a row. An address moves on by adding
+// its 16-byte pieces to the descriptor.
 template <int RB = 128> __device__ __forceinline__ uint64_t tc_desc(uint32_t at, uint32_t lbo) {
   return (uint64_t)((at >> 4) & 0x3FFF) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(8 * RB >> 4) << 32) | (1ull << 46) |
          ((RB == 128 ? 2ull : 4ull) << 61);
@@ -194,36 +199,62 @@ template <int RB, int N> __device__ __forceinline__ void put_planes(unsigned cha
   }
 }
 
-// 64 rows of an input (rows `stride` elements apart) from column c0, `pieces`
-// 16-byte pieces a row, into rows row0 .. of panels of 128 rows; rows from `live`
-// on and columns past D are zero and not read.
-template <int RB>
+// 64 rows of an input (rows `stride` elements apart), its columns c0 .. c0 + cols
+// (at most 8 P), into rows row0 .. of panels; rows from `live` on and columns past
+// D are zero and not read. For 256 threads: thread t has piece t % P of every
+// 256 / P-th row, so that nothing but the row moves on.
+template <int RB, int P>
 __device__ __forceinline__ void load_img(unsigned char* im, int row0, const bf16* src, size_t stride, int live, int D, int c0,
-                                         int pieces, int panel_bytes, int nthreads) {
-  constexpr int PR = RB / 16;  // pieces of a panel's row
-  const bool vec = D % 8 == 0;
-  for (int i = threadIdx.x; i < 64 * pieces; i += nthreads) {
-    const int r = i / pieces, c = i - r * pieces, col = c0 + c * 8;
-    unsigned char* d = im + (c / PR) * panel_bytes + img<RB>(row0 + r, c % PR);
-    const bf16* s = src + (size_t)r * stride + col;
-    if (vec) {
-      const bool on = r < live && col < D;
-      cp16(smem_u32(d), on ? s : src, on);
-    } else {
+                                         int cols, int panel_bytes) {
+  constexpr int PR = RB / 16, STEP = 256 / P, IT = 64 / STEP;  // pieces of a panel's row
+  static_assert(STEP % 8 == 0 && IT >= 1, "rows of one swizzle phase");
+  const int c = threadIdx.x % P, r = threadIdx.x / P, col = c0 + c * 8;
+  if (c * 8 >= cols) return;
+  unsigned char* d = im + (c / PR) * panel_bytes + img<RB>(row0 + r, c % PR);
+  const bf16* s = src + (size_t)r * stride + col;
+  if (D % 8 == 0) {
+    const uint32_t to = smem_u32(d);
+    const bool in = col < D;
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const bool on = in && r + k * STEP < live;
+      cp16(to + k * STEP * RB, on ? s + (size_t)k * STEP * stride : src, on);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
       uint32_t w[4] = {0, 0, 0, 0};
-      if (r < live) {
-        const unsigned short* p = (const unsigned short*)s;
+      if (r + k * STEP < live) {
+        const unsigned short* p = (const unsigned short*)(s + (size_t)k * STEP * stride);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (col + e < D) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
       }
-      *(uint4*)d = make_uint4(w[0], w[1], w[2], w[3]);
+      *(uint4*)(d + k * STEP * RB) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
-// `bytes` of an image that global memory holds as it stands
+// `bytes` of an image that global memory holds as it stands, by 256 threads
 __device__ __forceinline__ void load_plain(unsigned char* im, const void* src, int bytes) {
-  for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) cp16(smem_u32(im + i), (const unsigned char*)src + i, true);
+  const uint32_t to = smem_u32(im);
+#pragma unroll 4
+  for (int i = threadIdx.x * 16; i < bytes; i += 256 * 16) cp16(to + i, (const unsigned char*)src + i, true);
+}
+// the same by one thread, counted by the barrier
+__device__ __forceinline__ void load_bulk(unsigned char* im, const void* src, uint32_t bytes, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, bytes);
+  bulk_load_global(smem_u32(im), src, bytes, bar);
+}
+
+// The products of one operand's K-major image (KP columns, panels of 128 rows)
+// with the MN-major planes at b (rows of RB bytes, PLANE bytes apart), n columns.
+template <int RB>
+__device__ __forceinline__ void tc_wide(uint32_t d, uint32_t a, uint32_t b, int plane, int KP, uint32_t id) {
+  uint64_t ad = tc_desc(a, 16), bd = tc_desc<RB>(b, plane);
+  for (int k = 0; k < KP; k += 64, ad += TC_PANEL >> 4, bd += 4 * RB)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k + 16 * j < KP) tc_mma(d, ad + 2 * j, bd + j * RB, id, k || j);
 }
 
 // N values of a row of a tensor whose rows have D - c valid columns from p on

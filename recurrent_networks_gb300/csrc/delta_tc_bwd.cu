@@ -28,41 +28,82 @@ template <int BV, int MT> struct TcBack {
 template <int BV, int MT>
 __global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
   using L = TcBack<BV, MT>;
-  constexpr int RB = L::RB, NC = BV / 2, KST = L::KST;
+  constexpr int RB = L::RB, NC = BV / 2, KST = L::KST, P = MT * 16;
   static_assert(3 * L::SPLANE >= TC_PANEL, "what TP's last plane is read past");
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
   unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *GS = sm + L::AT_G, *OS = sm + L::AT_O;
   float* recs = (float*)(sm + L::AT_REC);  // [2][gam, br][64]
   uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
-  uint32_t* slot = (uint32_t*)(barp + 2);
+  uint32_t* slot = (uint32_t*)(barp + 3);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
   const int vt = blockIdx.x % a.nvt, bn = blockIdx.x / a.nvt, n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
   const int nch = tc_chunks(a, b);
   const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv;
   const size_t kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
-  const uint32_t bar = smem_u32(barp);
+  const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16;
   if (tid == 0) {
-    mbar_init(bar, 1);
-    mbar_init(bar + 8, 1);
+    for (int k = 0; k < 3; ++k) mbar_init(bar + 8 * k, 1);
     fence_mbar_init_cluster();
   }
   if (warp == 0) tm_alloc<512>(slot);
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = *slot, row = tm + ((uint32_t)(quad * 32) << 16);
+  constexpr int D1 = 0, D2 = 3 * BV * MT, D3 = 0;  // as in the forward: K dS1; dY; the state's change
+  bool failed = false;
+  uint32_t parity = 0;
+  auto wait = [&](uint32_t which, uint32_t par) { mbar_wait_bounded<false>(which, par, a.wait_limit_ns, a.status, failed); };
+
+  // thread 0 issues the products and brings TP
+  const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
+  if (tid == 0 && nch > 0) load_bulk(TP, tp + (size_t)(nch - 1) * L::TP, L::TP, bar_tp);
+  const uint64_t td = tc_desc(smem_u32(TP), TC_PANEL), gd = tc_desc<RB>(smem_u32(GS), L::GPLANE), od = tc_desc<RB>(smem_u32(OS), 16);
+  auto first = [&](uint32_t kq) {
+    tm_fence_after();
+    tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
+    tc_commit(bar);
+  };
+  auto second = [&](int ch) {
+    wait(bar_tp, (nch - 1 - ch) & 1);
+    if (failed) return;
+    tm_fence_after();
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // Tm's plane p with W's first 3 - p, PT's with dO
+        tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + k * 128, gd + k * RB, tc_idesc((3 - p) * BV, true, true), p || k);
+        tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + 512 + k * 128, od + k * RB, tc_idesc(BV, true, true), true);
+      }
+    tc_commit(bar);
+  };
+  auto third = [&](int ch, uint32_t kq) {
+    tm_fence_after();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        tc_mma(tm + D3 + 3 * mt * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 2048, TC_PANEL), gd + k * RB,
+               tc_idesc(3 * BV, true, true), k);
+    tc_commit(bar);
+    if (ch > 0) load_bulk(TP, tp + (size_t)(ch - 1) * L::TP, L::TP, bar_tp);  // the second products have read it
+  };
   auto load_kq = [&](int ch) {
     unsigned char* d = sm + (ch % KST) * L::KQ;
     const int live = tc_live(a, b, ch);
-    load_img<128>(d, 0, (const bf16*)a.k + kat + (size_t)ch * TC_C * kstride, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
-    load_img<128>(d, 64, (const bf16*)a.q + kat + (size_t)ch * TC_C * kstride, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
+    const size_t at = kat + (size_t)ch * TC_C * kstride;
+    load_img<128, P>(d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+    load_img<128, P>(d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
   };
   auto load_o = [&](int ch) {
-    load_img<RB>(OS, 0, (const bf16*)(a.dO ? a.dO : a.k) + (a.dO ? vat + (size_t)ch * TC_C * vstride : 0), vstride,
-                 a.dO ? tc_live(a, b, ch) : 0, a.Dv, vt * BV, BV / 8, 0, 256);
+    load_img<RB, BV / 8>(OS, 0, (const bf16*)(a.dO ? a.dO : a.k) + (a.dO ? vat + (size_t)ch * TC_C * vstride : 0), vstride,
+                         a.dO ? tc_live(a, b, ch) : 0, a.Dv, vt * BV, BV, 0);
     const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
     float* d = recs + (ch & 1) * 2 * TC_C;
     if (tid < 16) cp16(smem_u32(d + tid * 4), r + REC_GAM * TC_C + tid * 4, true);
     else if (tid < 32) cp16(smem_u32(d + tid * 4), r + REC_BR * TC_C + (tid - 16) * 4, true);
   };
-  auto load_tp = [&](int ch) { load_plain(TP, a.tp + ((size_t)bn * a.nc + ch) * 3 * 128 * TC_C, L::TP); };
 
   float S[MT][NC];  // dS
   const int c0 = half * NC, v0 = vt * BV + c0, valid = a.Dv - v0;
@@ -104,46 +145,20 @@ __global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
     load_kq(nch - 1);
     load_o(nch - 1);
     cp_commit();
-    load_tp(nch - 1);
-    cp_commit();
     put_state();
     put_edge(0);
   }
-  tm_fence_before();
-  __syncthreads();
-  tm_fence_after();
-  const uint32_t tm = *slot, row = tm + ((uint32_t)(quad * 32) << 16);
-  constexpr int D1 = 0, D2 = 2 * BV, D3 = 4 * BV;
-  uint32_t parity = 0;
-  bool failed = false;
-  auto wait = [&]() {
-    mbar_wait_bounded<false>(bar, parity, a.wait_limit_ns, a.status, failed);
-    parity ^= 1;
-    tm_fence_after();
-  };
   for (int ch = nch - 1; ch >= 0; --ch) {
     const size_t item = (size_t)bn * a.nc + ch, tile = item * a.nvt + vt;
     const bool more = ch > 0;
     const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
     const int live = tc_live(a, b, ch), i = (quad & 1) * 32 + lane;
-    if (KST == 2) cp_wait<1>();  // all but TP
-    else cp_wait<0>();
+    cp_wait<0>();
     fence_proxy_async_smem();
     tm_fence_before();
-    __syncthreads();
-    if (tid == 0 && !failed) {
-      tm_fence_after();
-      constexpr uint32_t id = tc_idesc(BV, false, true);
-      for (int p = 0; p < 3; ++p)
-        for (int k = 0; k < a.KP; k += 16)
-          tc_mma(tm + D1 + (p ? BV : 0), tc_desc(kq + (k >> 6) * TC_PANEL + (k & 63) * 2, 16),
-                 tc_desc<RB>(smem_u32(SS) + p * L::SPLANE + k * RB, 16), id, p == 2 || k);
-      tc_commit(bar);
-    }
-    if (KST == 2) {
-      if (more) load_kq(ch - 1);
-      cp_commit();
-    }
+    __syncthreads();  // KQ, dO and dS's planes are there
+    if (tid == 0 && !failed) first(kq);
+    if (KST == 2 && more) load_kq(ch - 1);
     const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
     {  // the gradient of the chunk's last state, rounded, in the image of its panel
       unsigned char* d = (unsigned char*)(a.dSh + (item * a.np + (v0 >> 6)) * a.KP * 64);
@@ -178,43 +193,21 @@ __global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
       put_planes<RB, NC>(GS, L::GPLANE, 64 + i, c0, d);
       a.dots[((tile * 3 + 2) * 2 + half) * TC_C + i] = i < live ? s : 0.0f;
     }
-    wait();
+    wait(bar, parity);
+    parity ^= 1;
+    tm_fence_after();
     if (quad < 2) {
       float x[NC];
-      tm_sum<NC>(x, row + D1 + c0, row + D1 + BV + c0);
+      tm_sum<NC, BV>(x, row + D1 + c0);
       const float f = br[i];
 #pragma unroll
       for (int c = 0; c < NC; ++c) x[c] = f != 0.0f ? f * x[c] : 0.0f;  // no part of it before a later document
       put_planes<RB, NC>(GS, L::GPLANE, i, c0, x);
     }
-    if (KST == 2) cp_wait<1>();  // TP
     fence_proxy_async_smem();
     tm_fence_before();
-    __syncthreads();
-    if (tid == 0 && !failed) {
-      tm_fence_after();
-      constexpr uint32_t id = tc_idesc(BV, true, true);
-      auto part = [&](int pa, int pb, uint32_t d, bool first) {  // Tm^T W
-        for (int k = 0; k < TC_C; k += 16)
-          tc_mma(d, tc_desc(smem_u32(TP) + pa * TC_PANEL + k * 128, TC_PANEL),
-                 tc_desc<RB>(smem_u32(GS) + pb * L::GPLANE + k * RB, 16), id, !first || k);
-      };
-      auto direct = [&](int pa, uint32_t d) {  // PT^T dO
-        for (int k = 0; k < TC_C; k += 16)
-          tc_mma(d, tc_desc(smem_u32(TP) + pa * TC_PANEL + (64 + k) * 128, TC_PANEL), tc_desc<RB>(smem_u32(OS) + k * RB, 16), id,
-                 true);
-      };
-      part(0, 0, tm + D2, true);
-      direct(0, tm + D2);
-      part(0, 2, tm + D2 + BV, true);
-      part(1, 1, tm + D2 + BV, false);
-      part(2, 0, tm + D2 + BV, false);
-      direct(2, tm + D2 + BV);
-      part(0, 1, tm + D2 + BV, false);
-      part(1, 0, tm + D2 + BV, false);
-      direct(1, tm + D2 + BV);
-      tc_commit(bar);
-    }
+    __syncthreads();  // W's planes are there
+    if (tid == 0 && !failed) second(ch);
     const int t = ch * TC_C + i;
     float v[NC];
     if (quad < 2) {  // v's row, for dc
@@ -229,10 +222,24 @@ __global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
         }
       }
     }
-    wait();
+    wait(bar, parity);
+    parity ^= 1;
+    tm_fence_after();
+    float y[NC];
     if (quad < 2) {
-      float y[NC];
-      tm_sum<NC>(y, row + D2 + c0, row + D2 + BV + c0);
+      tm_sum<NC, BV>(y, row + D2 + c0);
+      float g[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) g[c] = gi != 0.0f ? -gi * y[c] : 0.0f;
+      put_planes<RB, NC>(GS, L::GPLANE, i, c0, g);
+    }
+    fence_proxy_async_smem();
+    tm_fence_before();
+    __syncthreads();  // -gam dY's planes are there, dO is read
+    if (tid == 0 && !failed) third(ch, kq);
+    if (more) load_o(ch - 1);
+    cp_commit();
+    if (quad < 2) {  // what leaves for memory goes while the product runs
       float zy = 0.0f, vy = 0.0f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -242,29 +249,10 @@ __global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
       a.dots[((tile * 3 + 0) * 2 + half) * TC_C + i] = zy;
       a.dots[((tile * 3 + 1) * 2 + half) * TC_C + i] = -vy;
       if (t < a.T) store_row<NC>((bf16*)a.dv + vat + (size_t)t * vstride + v0, y, valid, a.Dv % 8 == 0);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) y[c] = gi != 0.0f ? -gi * y[c] : 0.0f;
-      put_planes<RB, NC>(GS, L::GPLANE, i, c0, y);
     }
-    fence_proxy_async_smem();
-    tm_fence_before();
-    __syncthreads();
-    if (tid == 0 && !failed) {
-      tm_fence_after();
-      constexpr uint32_t id = tc_idesc(BV, true, true);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        for (int p = 0; p < 3; ++p)
-          for (int k = 0; k < 2 * TC_C; k += 16)
-            tc_mma(tm + D3 + (2 * mt + (p ? 1 : 0)) * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 128, TC_PANEL),
-                   tc_desc<RB>(smem_u32(GS) + p * L::GPLANE + k * RB, 16), id, p == 2 || k);
-      tc_commit(bar);
-    }
-    if (more) load_o(ch - 1);
-    cp_commit();
-    if (more) load_tp(ch - 1);
-    cp_commit();
-    wait();
+    wait(bar, parity);
+    parity ^= 1;
+    tm_fence_after();
     if (KST == 1) {
       if (more) load_kq(ch - 1);
       cp_commit();
@@ -273,7 +261,7 @@ __global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       float d[NC];
-      tm_sum<NC>(d, row + D3 + 2 * mt * BV + c0, row + D3 + (2 * mt + 1) * BV + c0);
+      tm_sum<NC, BV>(d, row + D3 + 3 * mt * BV + c0);
 #pragma unroll
       for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
     }
@@ -298,7 +286,13 @@ __global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
     }
   }
   cp_wait<0>();
-  tc_finish(bar + 8, a.wait_limit_ns);
+  if (tid == 0 && failed) {  // a copy of TP that nobody waited for lands before the CTA ends
+    for (int p = 0; p < 2; ++p) {
+      bool f = false;
+      mbar_wait_bounded<false>(bar_tp, p, a.wait_limit_ns, nullptr, f);
+    }
+  }
+  tc_finish(bar_end, a.wait_limit_ns);
   if (warp == 0) tm_free<512>(tm);
 }
 
@@ -355,8 +349,8 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
   };
   for (int p = 0; p < a.np; ++p) {
     unsigned char* x = X + (size_t)p * L::XZ;
-    load_img<128>(x, 0, (const bf16*)a.dv + vat, vstride, live, a.Dv, p * 64, 8, 0, 256);
-    load_img<128>(x, 64, (const bf16*)(a.dO ? a.dO : a.dv) + vat, vstride, a.dO ? live : 0, a.Dv, p * 64, 8, 0, 256);
+    load_img<128, 8>(x, 0, (const bf16*)a.dv + vat, vstride, live, a.Dv, p * 64, 64, 0);
+    load_img<128, 8>(x, 64, (const bf16*)(a.dO ? a.dO : a.dv) + vat, vstride, a.dO ? live : 0, a.Dv, p * 64, 64, 0);
     load_plain(x + TC_PANEL, a.Zh + ((size_t)item * a.np + p) * 64 * 64, 64 * 128);
   }
   cp_commit();
@@ -387,11 +381,11 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
   };
   if (tid == 0) {  // [N; F] = X Z^T, in the second accumulator's columns
     constexpr uint32_t id = tc_idesc(64, false, false);
-    for (int p = 0; p < a.np; ++p)
-      for (int k = 0; k < 64; k += 16) {
-        const uint32_t x = smem_u32(X) + p * L::XZ + k * 2;
-        tc_mma(tm + KT, tc_desc(x, 16), tc_desc(x + TC_PANEL, 16), id, p || k);
-      }
+    for (int p = 0; p < a.np; ++p) {
+      const uint64_t x = tc_desc(smem_u32(X) + p * L::XZ, 16);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tc_mma(tm + KT, x + 2 * k, x + (TC_PANEL >> 4) + 2 * k, id, p || k);
+    }
     tc_commit(bar);
   }
   const int i = (quad & 1) * 32 + lane, j0 = half * 32;
@@ -413,10 +407,11 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
     if (tid == 0 && !failed) {
       tm_fence_after();
       const uint32_t id = tc_idesc(a.KP, false, false);
-      for (int k = 0; k < 64; k += 16) {
-        const uint32_t x = smem_u32(X) + p * L::XZ + k * 2, s = smem_u32(SD) + k * 2;
-        tc_mma(tm, tc_desc(x, 16), tc_desc(s, 16), id, p || k);                              // [dY; dO] S0^T
-        tc_mma(tm + KT, tc_desc(x + TC_PANEL, 16), tc_desc(s + L::SB, 16), id, p || k);      // Z dS1^T (rows 0 .. 63)
+      const uint64_t x = tc_desc(smem_u32(X) + p * L::XZ, 16), s = tc_desc(smem_u32(SD), 16);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        tc_mma(tm, x + 2 * k, s + 2 * k, id, p || k);                                              // [dY; dO] S0^T
+        tc_mma(tm + KT, x + (TC_PANEL >> 4) + 2 * k, s + (L::SB >> 4) + 2 * k, id, p || k);        // Z dS1^T (rows 0 .. 63)
       }
       tc_commit(bar);
     }
@@ -434,8 +429,8 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
     if (p + 1 < a.np) {
       load_sd(p + 1);
     } else {  // X and Z are done with
-      load_img<128>(KQ, 0, (const bf16*)a.k + kat, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
-      load_img<128>(KQ, 64, (const bf16*)a.q + kat, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
+      load_img<128, KT / 8>(KQ, 0, (const bf16*)a.k + kat, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+      load_img<128, KT / 8>(KQ, 64, (const bf16*)a.q + kat, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
     }
     cp_commit();
   }
@@ -487,8 +482,9 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
   if (tid == 0 && !failed) {
     tm_fence_after();
     const uint32_t id = tc_idesc(a.KP, false, true);
-    for (int k = 0; k < 128; k += 16)
-      tc_mma(tm, tc_desc(smem_u32(SD) + (k >> 6) * TC_PANEL + (k & 63) * 2, 16), tc_desc(smem_u32(KQ) + k * 128, TC_PANEL), id, true);
+    const uint64_t m = tc_desc(smem_u32(SD), 16), k0 = tc_desc(smem_u32(KQ), TC_PANEL);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) tc_mma(tm, m + (k >> 2) * (TC_PANEL >> 4) + (k & 3) * 2, k0 + k * 128, id, true);
     tc_commit(bar);
   }
   wait();
@@ -517,49 +513,57 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
 }
 
 // ---- gates ---------------------------------------------------------------------------
-// dg and dbeta of TC_EDGE chunks, from the last to the first; a thread has a step.
-__global__ void __launch_bounds__(TC_C) delta_tc_gates_kernel(DeltaTcArgs a) {
-  __shared__ float dc[TC_C], from[TC_C], seg_sm[TC_C];
-  const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE, i = threadIdx.x;
+// dg and dbeta of TC_EDGE chunks: a thread has a step, sums its document's dc to
+// the chunk's end, and what lies beyond comes from chunk to chunk after that.
+__global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcArgs a) {
+  __shared__ float dc[TC_EDGE][TC_C], seg_sm[TC_EDGE][TC_C], from[TC_EDGE], after[TC_EDGE], es[32];
+  const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE, k = threadIdx.x / TC_C, i = threadIdx.x % TC_C;
   const int bn = blockIdx.x / groups, gr = blockIdx.x % groups, n = bn % a.N, b = bn / a.N;
-  const int nch = tc_chunks(a, b), lo = gr * TC_EDGE, hi = min(a.nc, lo + TC_EDGE);
-  float e = 0.0f;  // <S, dS> at the end of the chunk at hand
-  if (lo < nch) {
-    const int at = hi >= nch ? 0 : gr + 1;
-    for (int w = 0; w < a.nvt * 8; ++w) e += a.edge[((size_t)bn * a.ne + at) * a.nvt * 8 + w];
-  }
-  for (int ch = hi - 1; ch >= lo; --ch) {
-    const size_t item = (size_t)bn * a.nc + ch;
-    const int t = ch * TC_C + i, live = tc_live(a, b, ch);
-    const size_t out = ((size_t)b * a.T + t) * a.N + n;
-    if (live == 0) {
-      if (t < a.T) a.dg[out] = a.dbeta[out] = 0.0f;
-      continue;
-    }
-    const float* rec = a.rec + item * REC_N * TC_C;
-    float zy = 0.0f, c = 0.0f;
+  const int nch = tc_chunks(a, b), lo = gr * TC_EDGE, ch = lo + k, t = ch * TC_C + i;
+  const int live = ch < a.nc ? tc_live(a, b, ch) : 0;
+  const size_t item = (size_t)bn * a.nc + ch, out = ((size_t)b * a.T + t) * a.N + n;
+  const float* rec = a.rec + item * REC_N * TC_C;
+  float zy = 0.0f, c = 0.0f, bt = 1.0f;
+  if (live > 0) {
+#pragma unroll 2
     for (int vt = 0; vt < a.nvt; ++vt) {
       const float* d = a.dots + (item * a.nvt + vt) * 6 * TC_C;
       zy += d[i] + d[TC_C + i];
       c += (d[2 * TC_C + i] + d[3 * TC_C + i]) + (d[4 * TC_C + i] + d[5 * TC_C + i]);
     }
-    __syncthreads();
-    dc[i] = c;
-    seg_sm[i] = rec[REC_SEG * TC_C + i];
-    __syncthreads();
-    const int mine = __float_as_int(seg_sm[i]), last = __float_as_int(seg_sm[TC_C - 1]);
-    float s = mine == last ? e : 0.0f;
-    for (int j = TC_C - 1; j >= i; --j)
-      if (__float_as_int(seg_sm[j]) == mine) s += dc[j];
-    from[i] = s;
-    const bool mark = mine != (i ? __float_as_int(seg_sm[i - 1]) : 0);
-    if (t < a.T) {
-      a.dg[out] = i < live && !mark ? s : 0.0f;
-      a.dbeta[out] = i < live ? zy / rec[REC_BETA * TC_C + i] : 0.0f;
-    }
-    __syncthreads();
-    e = __float_as_int(seg_sm[0]) == 0 ? from[0] : 0.0f;  // a chunk that begins a document needs nothing before it
+    bt = rec[REC_BETA * TC_C + i];
   }
+  dc[k][i] = c;
+  seg_sm[k][i] = live > 0 ? rec[REC_SEG * TC_C + i] : 0.0f;
+  if (threadIdx.x < 32) {  // <S, dS> at the group's end: a lane has every 32nd part
+    const int at = lo + TC_EDGE >= nch ? 0 : gr + 1;
+    float e = 0.0f;
+    if (lo < nch)
+      for (int w = threadIdx.x; w < a.nvt * 8; w += 32) e += a.edge[((size_t)bn * a.ne + at) * a.nvt * 8 + w];
+    es[threadIdx.x] = e;
+  }
+  __syncthreads();
+  const int mine = __float_as_int(seg_sm[k][i]), last = __float_as_int(seg_sm[k][TC_C - 1]);
+  float s = 0.0f;
+  for (int j = TC_C - 1; j >= i; --j)
+    if (__float_as_int(seg_sm[k][j]) == mine) s += dc[k][j];
+  if (i == 0) from[k] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float e = 0.0f;
+    for (int w = 0; w < 32; ++w) e += es[w];
+    for (int q = min(TC_EDGE, nch - lo) - 1; q >= 0; --q) {
+      after[q] = e;
+      const int first = __float_as_int(seg_sm[q][0]), end = __float_as_int(seg_sm[q][TC_C - 1]);
+      e = first == 0 ? from[q] + (end == 0 ? e : 0.0f) : 0.0f;  // a chunk that begins a document needs nothing before it
+    }
+  }
+  __syncthreads();
+  if (ch >= a.nc || t >= a.T) return;
+  const bool mark = mine != (i ? __float_as_int(seg_sm[k][i - 1]) : 0);
+  if (i < live && mine == last) s += after[k];
+  a.dg[out] = i < live && !mark ? s : 0.0f;
+  a.dbeta[out] = i < live ? zy / bt : 0.0f;
 }
 
 // dq, dk [rows, Nk, Dk] = sums of pq, pk [rows, Nk, share, Dk], in the heads' order
@@ -602,7 +606,7 @@ cudaError_t delta_tc_bwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if ((e = a.KP > 128 ? grad<256>(a, st) : grad<128>(a, st)) != cudaSuccess) return e;
   const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE;
-  delta_tc_gates_kernel<<<(unsigned)(a.B * a.N * groups), TC_C, 0, st>>>(a);
+  delta_tc_gates_kernel<<<(unsigned)(a.B * a.N * groups), TC_EDGE * TC_C, 0, st>>>(a);
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess || !a.pq) return e;
   const long long n = (long long)a.B * a.T * a.Nk * a.Dk, blocks = (n + 255) / 256, most = 16LL * device_sms();

@@ -9,21 +9,27 @@ namespace rnn {
 namespace {
 
 // ---- prep --------------------------------------------------------------------------
+constexpr int PREP_LD = TC_C + 4;
 __host__ __device__ constexpr size_t prep_smem(int KP) {
-  return (size_t)2 * TC_C * (KP + 8) * 2 + (size_t)2 * TC_C * (TC_C + 4) * 4 + REC_N * TC_C * 4;
+  const size_t kq = (size_t)2 * TC_C * (KP + 8) * 2, tf = (size_t)2 * TC_C * PREP_LD * 4;  // K and Q; then Tm and PT
+  return (kq > tf ? kq : tf) + tf + REC_N * TC_C * 4;
 }
 
-// A warp takes 16 rows of K K^T and Q K^T (mma.sync). Tm by forward substitution,
-// a column to a thread with its values in registers, and PT from it.
+// K K^T and Q K^T by mma.sync, 16 rows a warp; the rest in fp32 on the plain
+// cores. Tm: its two diagonal blocks of 32 by forward substitution, a column to a
+// thread, then T21 = -T22 (L21 T11); PT a column and every other row to a thread.
+// Bound by instructions: about 2500 a warp.
 __global__ void __launch_bounds__(128) delta_tc_prep_kernel(DeltaTcArgs a) {
-  constexpr int C = TC_C, NT = C / 8, LDF = C + 4;
+  constexpr int C = TC_C, NT = C / 8, LD = PREP_LD, H = C / 2;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   const int LDK = a.KP + 8, kplane = C * LDK;
+  const size_t kq = (size_t)2 * kplane * 2, tf = (size_t)2 * C * LD * 4;
   bf16* Ks = (bf16*)sm_raw;
   bf16* Qs = Ks + kplane;
-  float* Lf = (float*)(Qs + kplane);  // [C][LDF]
-  float* Pf = Lf + C * LDF;           // [C][LDF]
-  float* rec = Pf + C * LDF;          // [REC_N][C]
+  float* Tf = (float*)sm_raw;  // [2 C][LD]: Tm, then PT, over K and Q
+  float* Lf = (float*)(sm_raw + (kq > tf ? kq : tf));  // [C][LD]; L21's place takes L21 T11
+  float* Pf = Lf + C * LD;                             // [C][LD]
+  float* rec = Pf + C * LD;                            // [REC_N][C]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long item = blockIdx.x;
   if (item == 0 && tid == 0) *a.status = 0;  // the kernels behind this one report there
@@ -104,50 +110,96 @@ __global__ void __launch_bounds__(128) delta_tc_prep_kernel(DeltaTcArgs a) {
         const int j = t * 8 + (lane & 3) * 2 + e;
         const bool on = i >= j && si == __float_as_int(rec[REC_SEG * C + j]);
         const float gb = on ? expf((ci - rec[REC_CHI * C + j]) + (li - rec[REC_CLO * C + j])) * rec[REC_BETA * C + j] : 0.0f;
-        Pf[i * LDF + j] = on ? a.scale * qk[t][2 * h + e] * gb : 0.0f;
-        Lf[i * LDF + j] = on && i > j ? kk[t][2 * h + e] * gb : 0.0f;
+        Pf[i * LD + j] = on ? a.scale * qk[t][2 * h + e] * gb : 0.0f;
+        Lf[i * LD + j] = on && i > j ? kk[t][2 * h + e] * gb : 0.0f;
       }
   }
   __syncthreads();
-  unsigned char* tp = (unsigned char*)(a.tp + (size_t)item * 3 * 128 * C);
-  auto put = [&](int r, float x) {
-    const uint32_t to = img<128>(r, tid >> 3) + (tid & 7) * 2;
+  if (warp < 2) {  // T11 and T22
+    const int o = warp * H;
+    float x[H];
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      const bf16 h = __float2bfloat16_rn(x);
-      *(bf16*)(tp + p * TC_PANEL + to) = h;
-      x -= __bfloat162float(h);
-    }
-  };
-  if (tid < C) {
-    float x[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      float s[4] = {i == tid ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < H; ++i) {
+      float s[4] = {i == lane ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < i; k += 4) {
-        const float4 l = *(const float4*)(Lf + i * LDF + k);
+        const float4 l = *(const float4*)(Lf + (o + i) * LD + o + k);
         s[0] -= l.x * x[k];
         if (k + 1 < i) s[1] -= l.y * x[k + 1];
         if (k + 2 < i) s[2] -= l.z * x[k + 2];
         if (k + 3 < i) s[3] -= l.w * x[k + 3];
       }
       x[i] = (s[0] + s[1]) + (s[2] + s[3]);
-      put(i, x[i]);
     }
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
+    for (int i = 0; i < H; ++i) Tf[(o + i) * LD + o + lane] = x[i];
+  } else {  // T12 = 0
+    for (int i = warp - 2; i < H; i += 2) Tf[i * LD + H + lane] = 0.0f;
+  }
+  __syncthreads();
+  // two products of 32 x 32: 8 rows of column `lane` a thread
+  auto small = [&](const float* A, const float* B, float (&s)[8]) {
+    float col[H];
+#pragma unroll
+    for (int k = 0; k < H; ++k) col[k] = B[k * LD + lane];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      float t[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < H; k += 4) {
+        const float4 l = *(const float4*)(A + (warp * 8 + r) * LD + k);
+        t[0] = fmaf(l.x, col[k], t[0]);
+        t[1] = fmaf(l.y, col[k + 1], t[1]);
+        t[0] = fmaf(l.z, col[k + 2], t[0]);
+        t[1] = fmaf(l.w, col[k + 3], t[1]);
+      }
+      s[r] = t[0] + t[1];
+    }
+  };
+  float s8[8];
+  small(Lf + H * LD, Tf, s8);
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 8; ++r) Lf[(H + warp * 8 + r) * LD + lane] = s8[r];
+  __syncthreads();
+  small(Tf + H * LD + H, Lf + H * LD, s8);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) Tf[(H + warp * 8 + r) * LD + lane] = -s8[r];
+  __syncthreads();
+  {  // PT = P Tm
+    const int j = tid & (C - 1), odd = tid >> 6;
+    float x[C];
+#pragma unroll
+    for (int k = 0; k < C; ++k) x[k] = Tf[k * LD + j];
+#pragma unroll
+    for (int i = 0; i < C; i += 2) {
+      const float* p = Pf + (i + odd) * LD;  // zero past column i + odd
       float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int k = 0; k <= i; k += 4) {
-        const float4 l = *(const float4*)(Pf + i * LDF + k);
-        s[0] += l.x * x[k];
-        if (k + 1 <= i) s[1] += l.y * x[k + 1];
-        if (k + 2 <= i) s[2] += l.z * x[k + 2];
-        if (k + 3 <= i) s[3] += l.w * x[k + 3];
+      for (int k = 0; k < i + 2; k += 4) {
+        const float4 l = *(const float4*)(p + k);
+        s[0] = fmaf(l.x, x[k], s[0]);
+        s[1] = fmaf(l.y, x[k + 1], s[1]);
+        if (k + 2 < i + 2) {
+          s[2] = fmaf(l.z, x[k + 2], s[2]);
+          s[3] = fmaf(l.w, x[k + 3], s[3]);
+        }
       }
-      put(C + i, (s[0] + s[1]) + (s[2] + s[3]));
+      Tf[(C + i + odd) * LD + j] = (s[0] + s[1]) + (s[2] + s[3]);
     }
+  }
+  __syncthreads();
+  unsigned char* tp = (unsigned char*)(a.tp + (size_t)item * 3 * 128 * C);
+#pragma unroll 2
+  for (int i = tid; i < 128 * 8; i += 128) {
+    const int r = i >> 3, c = i & 7;
+    float x[8];
+    *(float4*)x = *(const float4*)(Tf + r * LD + c * 8);
+    *(float4*)(x + 4) = *(const float4*)(Tf + r * LD + c * 8 + 4);
+    uint4 p[3];
+    split8(x, p);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *(uint4*)(tp + k * TC_PANEL + img<128>(r, c)) = p[k];
   }
 }
 
@@ -161,48 +213,89 @@ template <int BV, int MT> struct TcChain {
 
 // 8 warps: warp w has lanes 32 (w % 4) .. of the accumulators (rows 0 .. 63: K's
 // steps, 64 .. 127: Q's; or rows of the state) and half of the tile's columns.
-// One thread issues the products, the rest of the CTA loads the next chunk
-// meanwhile. MT: tiles of 128 state rows, whose fp32 values stay in registers.
-// A chunk is three dependent products (1900 cycles of tensor cores for BV = 64,
-// Dk = 128) and their ways through registers, one after the other.
+// Thread 0 issues the products (with their operands' addresses worked out before:
+// 100 cycles a product otherwise) and brings TP by one bulk copy, the others load
+// the rest of the next chunk while the products run. MT: tiles of 128 state rows,
+// whose fp32 values stay in registers. A chunk is three dependent products and
+// their ways through registers.
 template <int BV, int MT>
 __global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
   using L = TcChain<BV, MT>;
-  constexpr int RB = L::RB, NC = BV / 2, KST = L::KST;
+  constexpr int RB = L::RB, NC = BV / 2, KST = L::KST, P = MT * 16;
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
   unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *YS = sm + L::AT_Y, *VS = sm + L::AT_V;
   float* recs = (float*)(sm + L::AT_REC);  // [2][gam, br][64]
   uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
-  uint32_t* slot = (uint32_t*)(barp + 2);
+  uint32_t* slot = (uint32_t*)(barp + 3);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
   const int vt = blockIdx.x % a.nvt, bn = blockIdx.x / a.nvt, n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
   const int nch = tc_chunks(a, b);
-  const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv;
-  const size_t kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
-  const uint32_t bar = smem_u32(barp);
+  const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16;
   if (tid == 0) {
-    mbar_init(bar, 1);
-    mbar_init(bar + 8, 1);
+    for (int k = 0; k < 3; ++k) mbar_init(bar + 8 * k, 1);
     fence_mbar_init_cluster();
   }
   if (warp == 0) tm_alloc<512>(slot);
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = *slot;
+  // accumulators, three blocks of BV columns each: D1 (K S0, Q S0) and D3 (the state's change, by tile), D2 (Z, PT Y)
+  constexpr int D1 = 0, D2 = 3 * BV * MT, D3 = 0;
+  bool failed = false;
+  uint32_t parity = 0;
+  auto wait = [&](uint32_t which, uint32_t par) { mbar_wait_bounded<false>(which, par, a.wait_limit_ns, a.status, failed); };
+
+  // thread 0 issues the products and brings TP
+  const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
+  if (tid == 0 && nch > 0) load_bulk(TP, tp, L::TP, bar_tp);
+  const uint64_t td = tc_desc(smem_u32(TP), 16), yd = tc_desc<RB>(smem_u32(YS), L::YPLANE);
+  auto first = [&](uint32_t kq) {
+    tm_fence_after();
+    tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
+    tc_commit(bar);
+  };
+  auto second = [&](int ch) {
+    wait(bar_tp, ch & 1);
+    if (failed) return;
+    tm_fence_after();
+#pragma unroll
+    for (int p = 0; p < 3; ++p)  // plane p of TP, the first 3 - p of Y
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + 2 * k, yd + k * RB, tc_idesc((3 - p) * BV, false, true), p || k);
+    tc_commit(bar);
+  };
+  auto third = [&](int ch, uint32_t kq) {
+    tm_fence_after();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        tc_mma(tm + D3 + 3 * mt * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 2048, TC_PANEL), yd + k * RB,
+               tc_idesc(3 * BV, true, true), k);
+    tc_commit(bar);
+    if (ch + 1 < nch) load_bulk(TP, tp + (size_t)(ch + 1) * L::TP, L::TP, bar_tp);  // the second products have read it
+  };
+  const uint32_t row = tm + ((uint32_t)(quad * 32) << 16);
+  const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv;
+  const size_t kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
   auto load_kq = [&](int ch) {
     unsigned char* d = sm + (ch % KST) * L::KQ;
     const int live = tc_live(a, b, ch);
-    load_img<128>(d, 0, (const bf16*)a.k + kat + (size_t)ch * TC_C * kstride, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
-    load_img<128>(d, 64, (const bf16*)a.q + kat + (size_t)ch * TC_C * kstride, kstride, live, a.Dk, 0, a.KP / 8, TC_PANEL, 256);
+    const size_t at = kat + (size_t)ch * TC_C * kstride;
+    load_img<128, P>(d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+    load_img<128, P>(d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
   };
   auto load_v = [&](int ch) {
-    load_img<RB>(VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv, vt * BV, BV / 8,
-                 0, 256);
+    load_img<RB, BV / 8>(VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv, vt * BV,
+                         BV, 0);
     const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
     float* d = recs + (ch & 1) * 2 * TC_C;
     if (tid < 16) cp16(smem_u32(d + tid * 4), r + REC_GAM * TC_C + tid * 4, true);
     else if (tid < 32) cp16(smem_u32(d + tid * 4), r + REC_BR * TC_C + (tid - 16) * 4, true);
   };
-  auto load_tp = [&](int ch) { load_plain(TP, a.tp + ((size_t)bn * a.nc + ch) * 3 * 128 * TC_C, L::TP); };
-
   float S[MT][NC];
   const int c0 = half * NC, v0 = vt * BV + c0;  // this thread's columns, in the tile and in v
   const int valid = a.Dv - v0;
@@ -218,50 +311,37 @@ __global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) put_planes<RB, NC>(SS, L::SPLANE, mt * 128 + quad * 32 + lane, c0, S[mt]);
   };
+  // S, as the threads hold it, to kept state e
+  auto keep_state = [&](int e) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float4* f = (float4*)(a.sf + (((size_t)bn * a.ne + e) * a.nvt + vt) * MT * 128 * BV) +
+                  (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
+#pragma unroll
+      for (int c = 0; c < NC; c += 4) f[(c / 4) * 128] = make_float4(S[mt][c], S[mt][c + 1], S[mt][c + 2], S[mt][c + 3]);
+    }
+  };
   if (nch > 0) {
     load_kq(0);
     load_v(0);
     cp_commit();
-    load_tp(0);
-    cp_commit();
     put_state();
+  } else if (a.sf) {
+    keep_state(0);
   }
-  tm_fence_before();
-  __syncthreads();
-  tm_fence_after();
-  const uint32_t tm = *slot, row = tm + ((uint32_t)(quad * 32) << 16);
-  // accumulators: D1 (K S0, Q S0), D2 (Z, PT Y), D3 (the state's change, by tile), each hi and lo
-  constexpr int D1 = 0, D2 = 2 * BV, D3 = 4 * BV;
-  uint32_t parity = 0;
-  bool failed = false;
-  auto wait = [&]() {
-    mbar_wait_bounded<false>(bar, parity, a.wait_limit_ns, a.status, failed);
-    parity ^= 1;
-    tm_fence_after();
-  };
+  const int i = (quad & 1) * 32 + lane;  // this thread's step
   for (int ch = 0; ch < nch; ++ch) {
     const size_t item = (size_t)bn * a.nc + ch, tile = item * a.nvt + vt;
     const bool more = ch + 1 < nch;
-    const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
-    if (KST == 2) cp_wait<1>();  // all but TP
-    else cp_wait<0>();
+    cp_wait<0>();
     fence_proxy_async_smem();
     tm_fence_before();
-    __syncthreads();
-    if (tid == 0 && !failed) {
-      tm_fence_after();
-      constexpr uint32_t id = tc_idesc(BV, false, true);
-      for (int p = 0; p < 3; ++p)
-        for (int k = 0; k < a.KP; k += 16)
-          tc_mma(tm + D1 + (p ? BV : 0), tc_desc(kq + (k >> 6) * TC_PANEL + (k & 63) * 2, 16),
-                 tc_desc<RB>(smem_u32(SS) + p * L::SPLANE + k * RB, 16), id, p == 2 || k);
-      tc_commit(bar);
-    }
-    if (KST == 2) {
-      if (more) load_kq(ch + 1);
-      cp_commit();
-    }
+    __syncthreads();  // KQ, V and S's planes are there
+    const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
+    if (tid == 0 && !failed) first(kq);
+    if (KST == 2 && more) load_kq(ch + 1);
     const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
+    const float gi = gam[i];
     if (a.Sh) {  // the chunk's starting state, rounded, in the image of its panel
       unsigned char* d = (unsigned char*)(a.Sh + (item * a.np + (v0 >> 6)) * a.KP * 64);
 #pragma unroll
@@ -272,15 +352,16 @@ __global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
           for (int c = 0; c < NC; c += 8) put_piece(d, r, ((v0 & 63) + c) >> 3, round8(S[mt] + c), lone);
       }
     }
-    wait();
-    const int i = (quad & 1) * 32 + lane;  // this thread's step
-    const float gi = gam[i];
-    float x[NC];
-    tm_sum<NC>(x, row + D1 + c0, row + D1 + BV + c0);
-    if (quad < 2) {
-      float y[NC];
+    float y[NC];
+    if (quad < 2)
 #pragma unroll
       for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(VS + img<RB>(i, (c0 + c) >> 3)), y + c);
+    wait(bar, parity);
+    parity ^= 1;
+    tm_fence_after();
+    float x[NC];
+    tm_sum<NC, BV>(x, row + D1 + c0);
+    if (quad < 2) {
       if (gi != 0.0f)  // behind a reset the old state has no part, whatever it holds
 #pragma unroll
         for (int c = 0; c < NC; ++c) y[c] = fmaf(-gi, x[c], y[c]);
@@ -290,31 +371,28 @@ __global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) x[c] = gi != 0.0f ? f * x[c] : 0.0f;
     }
-    if (KST == 2) cp_wait<1>();  // TP
     fence_proxy_async_smem();
     tm_fence_before();
-    __syncthreads();
-    if (tid == 0 && !failed) {
-      tm_fence_after();
-      constexpr uint32_t id = tc_idesc(BV, false, true);
-      auto part = [&](int pa, int pb, uint32_t d, bool first) {
-        for (int k = 0; k < TC_C; k += 16)
-          tc_mma(d, tc_desc(smem_u32(TP) + pa * TC_PANEL + k * 2, 16), tc_desc<RB>(smem_u32(YS) + pb * L::YPLANE + k * RB, 16), id,
-                 !first || k);
-      };
-      part(0, 0, tm + D2, true);
-      part(0, 2, tm + D2 + BV, true);
-      part(1, 1, tm + D2 + BV, false);
-      part(2, 0, tm + D2 + BV, false);
-      part(0, 1, tm + D2 + BV, false);
-      part(1, 0, tm + D2 + BV, false);
-      tc_commit(bar);
-    }
+    __syncthreads();  // Y's planes are there, V is read
+    if (tid == 0 && !failed) second(ch);
     if (more) load_v(ch + 1);
     cp_commit();
-    wait();
+    wait(bar, parity);
+    parity ^= 1;
+    tm_fence_after();
     float z[NC];
-    tm_sum<NC>(z, row + D2 + c0, row + D2 + BV + c0);
+    tm_sum<NC, BV>(z, row + D2 + c0);
+    if (quad < 2) {
+      const float f = br[i];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) y[c] = f * z[c];
+      put_planes<RB, NC>(YS, L::YPLANE, i, c0, y);  // the products have read Y
+    }
+    fence_proxy_async_smem();
+    tm_fence_before();
+    __syncthreads();  // beta rho Z's planes are there
+    if (tid == 0 && !failed) third(ch, kq);
+    // what leaves for memory goes while the product runs
     if (quad < 2) {
       if (a.Zh) {
         unsigned char* d = (unsigned char*)(a.Zh + (item * a.np + (v0 >> 6)) * 64 * 64);
@@ -324,10 +402,6 @@ __global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
 #pragma unroll
         for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
       }
-      const float f = br[i];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) z[c] *= f;
-      put_planes<RB, NC>(YS, L::YPLANE, i, c0, z);  // the products have read Y
     } else {
       const int t = ch * TC_C + i;
 #pragma unroll
@@ -344,48 +418,29 @@ __global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
         store_row<NC>((bf16*)a.o + vat + (size_t)t * vstride + v0, z, valid, a.Dv % 8 == 0);
       }
     }
-    fence_proxy_async_smem();
-    tm_fence_before();
-    __syncthreads();
-    if (tid == 0 && !failed) {
-      tm_fence_after();
-      constexpr uint32_t id = tc_idesc(BV, true, true);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        for (int p = 0; p < 3; ++p)
-          for (int k = 0; k < TC_C; k += 16)
-            tc_mma(tm + D3 + (2 * mt + (p ? 1 : 0)) * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 128, TC_PANEL),
-                   tc_desc<RB>(smem_u32(YS) + p * L::YPLANE + k * RB, 16), id, p == 2 || k);
-      tc_commit(bar);
-    }
-    if (more) load_tp(ch + 1);
-    cp_commit();
-    wait();
+    const float gC = gam[TC_C - 1];
+    wait(bar, parity);
+    parity ^= 1;
+    tm_fence_after();
     if (KST == 1) {
       if (more) load_kq(ch + 1);
       cp_commit();
     }
-    const float gC = gam[TC_C - 1];
-    const int end = ch + 1 == nch ? 0 : (ch + 1) % TC_EDGE == 0 ? (ch + 1) / TC_EDGE : -1;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       float d[NC];
-      tm_sum<NC>(d, row + D3 + 2 * mt * BV + c0, row + D3 + (2 * mt + 1) * BV + c0);
+      tm_sum<NC, BV>(d, row + D3 + 3 * mt * BV + c0);
 #pragma unroll
       for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
-      if (a.sf && end >= 0) {
-        float4* f = (float4*)(a.sf + (((size_t)bn * a.ne + end) * a.nvt + vt) * MT * 128 * BV) +
-                    (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
-#pragma unroll
-        for (int c = 0; c < NC; c += 4) f[(c / 4) * 128] = make_float4(S[mt][c], S[mt][c + 1], S[mt][c + 2], S[mt][c + 3]);
-      }
     }
     if (more) put_state();
+    const int end = !more ? 0 : (ch + 1) % TC_EDGE == 0 ? (ch + 1) / TC_EDGE : -1;
+    if (a.sf && end >= 0) keep_state(end);
   }
   // steps past the row's length
   const int t0 = nch * TC_C, cols = min(BV, a.Dv - vt * BV);
-  for (long long i = tid; i < (long long)(a.T - t0) * cols; i += 256)
-    ((bf16*)a.o)[vat + (size_t)(t0 + i / cols) * vstride + vt * BV + i % cols] = __float2bfloat16_rn(0.0f);
+  for (long long k = tid; k < (long long)(a.T - t0) * cols; k += 256)
+    ((bf16*)a.o)[vat + (size_t)(t0 + k / cols) * vstride + vt * BV + k % cols] = __float2bfloat16_rn(0.0f);
   if (a.last) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -398,17 +453,14 @@ __global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
       }
     }
   }
-  if (nch == 0 && a.sf) {  // no chunk: the end is the start
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float4* f = (float4*)(a.sf + ((size_t)bn * a.ne * a.nvt + vt) * MT * 128 * BV) +
-                  (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
-#pragma unroll
-      for (int c = 0; c < NC; c += 4) f[(c / 4) * 128] = make_float4(S[mt][c], S[mt][c + 1], S[mt][c + 2], S[mt][c + 3]);
+  cp_wait<0>();
+  if (tid == 0 && failed) {  // a copy of TP that nobody waited for lands before the CTA ends
+    for (int p = 0; p < 2; ++p) {
+      bool f = false;
+      mbar_wait_bounded<false>(bar_tp, p, a.wait_limit_ns, nullptr, f);
     }
   }
-  cp_wait<0>();
-  tc_finish(bar + 8, a.wait_limit_ns);
+  tc_finish(bar_end, a.wait_limit_ns);
   if (warp == 0) tm_free<512>(tm);
 }
 
