@@ -142,7 +142,7 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 // What the calls lay out in the tape (behind the status word) and the workspace.
 struct DeltaSizes {
   bool bf;
-  int C, NP, BV, KP, nvt, np;
+  int C, NP, BV, KP, nvt;
   long long nc, items, ne;
   size_t rec, tri, S, Z, zf, sf;  // bytes
   size_t tape, scratch;           // with what a backward needs, and without
@@ -163,7 +163,6 @@ bool delta_sizes(const rnn_delta_dims_t* d, DeltaSizes* z) {
   z->KP = (d->Dk + 15) / 16 * 16;
   z->BV = delta_bv(z->bf, d->B, d->N, d->Dv, z->KP, device_sms());
   z->nvt = (d->Dv + z->BV - 1) / z->BV;
-  z->np = (d->Dv + 63) / 64;
   z->nc = ((long long)d->T + z->C - 1) / z->C;
   z->items = z->nc * d->B * d->N;
   // the kernels count the items' tiles and the heads' tiles in 32 bits
@@ -173,8 +172,8 @@ bool delta_sizes(const rnn_delta_dims_t* d, DeltaSizes* z) {
   if (z->bf) {
     z->ne = z->nc / TC_EDGE + 1;
     z->tri = up256(n * 3 * 128 * TC_C * 2);  // TP
-    z->S = up256(n * z->np * z->KP * 64 * 2);
-    z->Z = up256(n * z->np * 64 * 64 * 2);
+    z->S = up256(n * z->nvt * z->KP * z->BV * 2);
+    z->Z = up256(n * z->nvt * 64 * z->BV * 2);
     z->zf = up256(n * z->nvt * 64 * z->BV * 4);
     z->sf = up256(heads * z->ne * z->nvt * (z->KP > 128 ? 256 : 128) * z->BV * 4);
     z->scratch = z->rec + z->tri;
@@ -211,7 +210,7 @@ DeltaArgs delta_args(const rnn_delta_dims_t* d, const DeltaSizes& z, void* tape)
 DeltaTcArgs delta_tc_args(const rnn_delta_dims_t* d, const DeltaSizes& z, void* tape, bool keep) {
   DeltaTcArgs a{};
   a.B = d->B; a.T = d->T; a.Nk = d->Nk; a.N = d->N; a.Dk = d->Dk; a.Dv = d->Dv;
-  a.KP = z.KP; a.np = z.np; a.nvt = z.nvt; a.nc = (int)z.nc; a.ne = (int)z.ne;
+  a.KP = z.KP; a.nvt = z.nvt; a.nc = (int)z.nc; a.ne = (int)z.ne;
   a.status = (unsigned*)tape;
   a.wait_limit_ns = wait_limit_ns();
   char* t = (char*)tape + 256;

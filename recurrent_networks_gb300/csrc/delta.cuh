@@ -203,6 +203,8 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // rows x cols (cols a multiple of 8) of a dense 16-byte-aligned matrix with
 // rows of `src_ld`, into rows of ld elements
 __device__ __forceinline__ void cp_tile(bf16* dst, int ld, const bf16* src, int src_ld, int rows, int cols) {

@@ -44,7 +44,7 @@ constexpr int TC_PANEL = 16384; // bytes of a panel of 128 rows
 
 struct DeltaTcArgs {
   int B, T, Nk, N, Dk, Dv;
-  int KP, np, nvt, nc, ne;  // Dk rounded to 16, panels of 64 and tiles of BV columns of v, chunks, kept states a head
+  int KP, nvt, nc, ne;  // Dk rounded to 16, tiles of BV columns of v, chunks, kept states a head
   const void *q, *k, *v;
   const float *g, *beta, *s0;
   const unsigned char* reset;
@@ -57,7 +57,7 @@ struct DeltaTcArgs {
   float* rec;  // [items][REC_N][64]
   bf16* tp;    // [items][3][128 x 64 image]
   // what a backward needs besides (null: none comes)
-  bf16 *Sh, *Zh;       // [items][np][KP x 64 image] of S0, [items][np][64 x 64 image] of Z
+  bf16 *Sh, *Zh;       // [items][nvt][KP x BV image] of S0, [items][nvt][64 x BV image] of Z
   float *zf, *of;      // [items][nvt][...] z and o in fp32, as the threads hold them
   float* sf;           // [B N][ne][nvt][...] S at the end (0) and at every TC_EDGE-th chunk's start
   // backward
@@ -181,11 +181,6 @@ __device__ __forceinline__ void widen8(const uint4& v, float* x) {
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-// Piece c of row r of a panel's image; lone: the piece 32 columns further is zero.
-__device__ __forceinline__ void put_piece(unsigned char* im, int r, int c, const uint4& v, bool lone) {
-  *(uint4*)(im + img<128>(r, c)) = v;
-  if (lone) *(uint4*)(im + img<128>(r, c + 4)) = make_uint4(0, 0, 0, 0);
-}
 // N values of row r, from column c0 (a multiple of 8) on, into the planes of an
 // image (plane bytes apart)
 template <int RB, int N> __device__ __forceinline__ void put_planes(unsigned char* im, int plane, int r, int c0, const float (&x)[N]) {
@@ -201,49 +196,67 @@ template <int RB, int N> __device__ __forceinline__ void put_planes(unsigned cha
 
 // 64 rows of an input (rows `stride` elements apart), its columns c0 .. c0 + cols
 // (at most 8 P), into rows row0 .. of panels; rows from `live` on and columns past
-// D are zero and not read. For 256 threads: thread t has piece t % P of every
-// 256 / P-th row, so that nothing but the row moves on.
-template <int RB, int P>
-__device__ __forceinline__ void load_img(unsigned char* im, int row0, const bf16* src, size_t stride, int live, int D, int c0,
-                                         int cols, int panel_bytes) {
-  constexpr int PR = RB / 16, STEP = 256 / P, IT = 64 / STEP;  // pieces of a panel's row
-  static_assert(STEP % 8 == 0 && IT >= 1, "rows of one swizzle phase");
-  const int c = threadIdx.x % P, r = threadIdx.x / P, col = c0 + c * 8;
+// D are zero and not read. Thread t of NTH has piece t % P of every NTH / P-th row.
+template <int RB, int P, int NTH>
+__device__ __forceinline__ void load_img(int t, unsigned char* im, int row0, const bf16* src, size_t stride, int live, int D,
+                                         int c0, int cols, int panel_bytes) {
+  constexpr int PR = RB / 16, STEP = NTH / P, IT = 64 / STEP;  // pieces of a panel's row
+  static_assert(STEP >= 1 && IT >= 1, "whole rows a step");
+  const int c = t % P, r = t / P, col = c0 + c * 8;
   if (c * 8 >= cols) return;
-  unsigned char* d = im + (c / PR) * panel_bytes + img<RB>(row0 + r, c % PR);
+  unsigned char* d = im + (c / PR) * panel_bytes;
   const bf16* s = src + (size_t)r * stride + col;
   if (D % 8 == 0) {
     const uint32_t to = smem_u32(d);
     const bool in = col < D;
-#pragma unroll
-    for (int k = 0; k < IT; ++k) {
+#pragma unroll 4
+    for (int k = 0; k < IT; ++k, s += (size_t)STEP * stride) {
       const bool on = in && r + k * STEP < live;
-      cp16(to + k * STEP * RB, on ? s + (size_t)k * STEP * stride : src, on);
+      cp16(to + img<RB>(row0 + r + k * STEP, c % PR), on ? s : src, on);
     }
   } else {
-#pragma unroll
-    for (int k = 0; k < IT; ++k) {
+#pragma unroll 4
+    for (int k = 0; k < IT; ++k, s += (size_t)STEP * stride) {
       uint32_t w[4] = {0, 0, 0, 0};
       if (r + k * STEP < live) {
-        const unsigned short* p = (const unsigned short*)(s + (size_t)k * STEP * stride);
+        const unsigned short* p = (const unsigned short*)s;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (col + e < D) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
       }
-      *(uint4*)(d + k * STEP * RB) = make_uint4(w[0], w[1], w[2], w[3]);
+      *(uint4*)(d + img<RB>(row0 + r + k * STEP, c % PR)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
-// `bytes` of an image that global memory holds as it stands, by 256 threads
-__device__ __forceinline__ void load_plain(unsigned char* im, const void* src, int bytes) {
-  const uint32_t to = smem_u32(im);
+// The first `rows` rows of an image of 64 rows to the columns c0 .. of a tensor
+// whose rows have D columns: 128 bytes (64) of a row to 8 (4) threads.
+template <int RB, int NTH>
+__device__ __forceinline__ void store_img(int t, const unsigned char* im, bf16* dst, size_t stride, int rows, int D, int c0) {
+  constexpr int P = RB / 16, STEP = NTH / P;
+  const int c = t % P, col = c0 + c * 8;
 #pragma unroll 4
-  for (int i = threadIdx.x * 16; i < bytes; i += 256 * 16) cp16(to + i, (const unsigned char*)src + i, true);
+  for (int r = t / P; r < rows; r += STEP) {
+    const uint4 v = *(const uint4*)(im + img<RB>(r, c));
+    bf16* p = dst + (size_t)r * stride + col;
+    if (D % 8 == 0) {
+      if (col < D) *(uint4*)p = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col + e < D) ((unsigned short*)p)[e] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
 }
-// the same by one thread, counted by the barrier
+// `bytes` of an image that global memory holds as it stands, by one thread, counted
+// by the barrier; and an image to global memory (bulk_commit_group and
+// bulk_wait_group_read follow)
 __device__ __forceinline__ void load_bulk(unsigned char* im, const void* src, uint32_t bytes, uint32_t bar) {
   mbar_arrive_expect_tx(bar, bytes);
   bulk_load_global(smem_u32(im), src, bytes, bar);
+}
+__device__ __forceinline__ void store_bulk(void* dst, const unsigned char* im, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(im)), "r"(bytes) : "memory");
 }
 
 // The products of one operand's K-major image (KP columns, panels of 128 rows)

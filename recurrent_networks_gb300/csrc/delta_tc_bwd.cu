@@ -16,31 +16,31 @@ template <int BV, int MT> struct TcBack {
   static constexpr int RB = 2 * BV, KST = MT == 1 ? 2 : 1;
   static constexpr int KQ = 2 * MT * TC_PANEL, TP = 3 * TC_PANEL, SPLANE = MT * 128 * RB, GPLANE = 128 * RB;
   static constexpr int AT_TP = KST * KQ, AT_S = AT_TP + TP, AT_G = AT_S + 3 * SPLANE, AT_O = AT_G + 3 * GPLANE;
-  static constexpr int AT_REC = AT_O + 64 * RB, BYTES = AT_REC + 2 * 2 * 64 * 4 + 64 + 1024;
+  static constexpr int AT_V = AT_O + 64 * RB, AT_REC = AT_V + 64 * RB, BYTES = AT_REC + 2 * 2 * 64 * 4 + 64 + 1024;
 };
 
-// Warps and threads as in the forward's chain. The image G holds, by planes, W in
-// rows 0 .. 63 until dY's products have read it, then -gam dY; rows 64 .. 127
-// scale gam dO, written by the threads of Q's steps while the first product runs.
+// Warps as in the forward's chain. The image G holds, by planes, W in rows 0 .. 63
+// until dY's products have read it, then -gam dY; rows 64 .. 127 scale gam dO,
+// written by the threads of Q's steps while the first product runs. dY goes out
+// through V's image, each value in the place of the v that its thread has read.
 // The products for dY take TP by columns, 64 of them; the other 64 rows of the
 // accumulator come from whatever lies a panel further (inside this CTA's shared
 // memory) and are not looked at.
 template <int BV, int MT>
-__global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
+__global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
   using L = TcBack<BV, MT>;
   constexpr int RB = L::RB, NC = BV / 2, KST = L::KST, P = MT * 16;
   static_assert(3 * L::SPLANE >= TC_PANEL, "what TP's last plane is read past");
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
-  unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *GS = sm + L::AT_G, *OS = sm + L::AT_O;
+  unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *GS = sm + L::AT_G, *OS = sm + L::AT_O, *VS = sm + L::AT_V;
   float* recs = (float*)(sm + L::AT_REC);  // [2][gam, br][64]
   uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
   uint32_t* slot = (uint32_t*)(barp + 3);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
   const int vt = blockIdx.x % a.nvt, bn = blockIdx.x / a.nvt, n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
   const int nch = tc_chunks(a, b);
-  const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv;
-  const size_t kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
+  const size_t vstride = (size_t)a.N * a.Dv, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
   const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16;
   if (tid == 0) {
     for (int k = 0; k < 3; ++k) mbar_init(bar + 8 * k, 1);
@@ -50,276 +50,305 @@ __global__ void __launch_bounds__(256, 1) delta_tc_back_kernel(DeltaTcArgs a) {
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
-  const uint32_t tm = *slot, row = tm + ((uint32_t)(quad * 32) << 16);
+  const uint32_t tm = *slot;
   constexpr int D1 = 0, D2 = 3 * BV * MT, D3 = 0;  // as in the forward: K dS1; dY; the state's change
   bool failed = false;
-  uint32_t parity = 0;
   auto wait = [&](uint32_t which, uint32_t par) { mbar_wait_bounded<false>(which, par, a.wait_limit_ns, a.status, failed); };
 
-  // thread 0 issues the products and brings TP
-  const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
-  if (tid == 0 && nch > 0) load_bulk(TP, tp + (size_t)(nch - 1) * L::TP, L::TP, bar_tp);
-  const uint64_t td = tc_desc(smem_u32(TP), TC_PANEL), gd = tc_desc<RB>(smem_u32(GS), L::GPLANE), od = tc_desc<RB>(smem_u32(OS), 16);
-  auto first = [&](uint32_t kq) {
-    tm_fence_after();
-    tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
-    tc_commit(bar);
-  };
-  auto second = [&](int ch) {
-    wait(bar_tp, (nch - 1 - ch) & 1);
-    if (failed) return;
-    tm_fence_after();
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 8) {  // ---- products, bulk copies
+      const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
+      const bool one = lane == 0;
+      if (one && nch > 0) load_bulk(TP, tp + (size_t)(nch - 1) * L::TP, L::TP, bar_tp);
+      const uint64_t td = tc_desc(smem_u32(TP), TC_PANEL), gd = tc_desc<RB>(smem_u32(GS), L::GPLANE), od = tc_desc<RB>(smem_u32(OS), 16);
+      for (int ch = nch - 1; ch >= 0; --ch) {
+        const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
+        const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
+        __syncthreads();  // 1
+        if (one && !failed) {
+          tm_fence_after();
+          tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
+          tc_commit(bar);
+          // the gradient of the chunk's last state, rounded: its first plane
+          store_bulk(a.dSh + tile * a.KP * BV, SS, a.KP * RB);
+          bulk_commit_group();
+        }
+        __syncthreads();  // 2
+        if (one) {
+          wait(bar_tp, (nch - 1 - ch) & 1);
+          if (!failed) {
+            tm_fence_after();
 #pragma unroll
-    for (int p = 0; p < 3; ++p)
+            for (int p = 0; p < 3; ++p)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {  // Tm's plane p with W's first 3 - p, PT's with dO
-        tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + k * 128, gd + k * RB, tc_idesc((3 - p) * BV, true, true), p || k);
-        tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + 512 + k * 128, od + k * RB, tc_idesc(BV, true, true), true);
+              for (int k = 0; k < 4; ++k) {  // Tm's plane p with W's first 3 - p, PT's with dO
+                tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + k * 128, gd + k * RB, tc_idesc((3 - p) * BV, true, true), p || k);
+                tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + 512 + k * 128, od + k * RB, tc_idesc(BV, true, true), true);
+              }
+            tc_commit(bar);
+          }
+          bulk_wait_group_read<0>();  // the state's planes may be written again
+        }
+        __syncthreads();  // 3
+        if (one && !failed) {
+          tm_fence_after();
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma(tm + D3 + 3 * mt * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 2048, TC_PANEL), gd + k * RB,
+                     tc_idesc(3 * BV, true, true), k);
+          tc_commit(bar);
+          if (ch > 0) load_bulk(TP, tp + (size_t)(ch - 1) * L::TP, L::TP, bar_tp);  // the second products have read it
+        }
+        __syncthreads();  // 4
       }
-    tc_commit(bar);
-  };
-  auto third = [&](int ch, uint32_t kq) {
-    tm_fence_after();
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        tc_mma(tm + D3 + 3 * mt * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 2048, TC_PANEL), gd + k * RB,
-               tc_idesc(3 * BV, true, true), k);
-    tc_commit(bar);
-    if (ch > 0) load_bulk(TP, tp + (size_t)(ch - 1) * L::TP, L::TP, bar_tp);  // the second products have read it
-  };
-  auto load_kq = [&](int ch) {
-    unsigned char* d = sm + (ch % KST) * L::KQ;
-    const int live = tc_live(a, b, ch);
-    const size_t at = kat + (size_t)ch * TC_C * kstride;
-    load_img<128, P>(d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
-    load_img<128, P>(d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
-  };
-  auto load_o = [&](int ch) {
-    load_img<RB, BV / 8>(OS, 0, (const bf16*)(a.dO ? a.dO : a.k) + (a.dO ? vat + (size_t)ch * TC_C * vstride : 0), vstride,
-                         a.dO ? tc_live(a, b, ch) : 0, a.Dv, vt * BV, BV, 0);
-    const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
-    float* d = recs + (ch & 1) * 2 * TC_C;
-    if (tid < 16) cp16(smem_u32(d + tid * 4), r + REC_GAM * TC_C + tid * 4, true);
-    else if (tid < 32) cp16(smem_u32(d + tid * 4), r + REC_BR * TC_C + (tid - 16) * 4, true);
-  };
-
-  float S[MT][NC];  // dS
-  const int c0 = half * NC, v0 = vt * BV + c0, valid = a.Dv - v0;
-  const bool lone = BV == 32 && vt == a.nvt - 1 && vt % 2 == 0;  // nobody has the other half of the panel
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int r = mt * 128 + quad * 32 + lane;
-    const float* s = a.dlast ? a.dlast + ((size_t)bn * a.Dk + r) * a.Dv + v0 : nullptr;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) S[mt][c] = s && r < a.Dk && c < valid ? s[c] : 0.0f;
-  }
-  auto put_state = [&]() {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) put_planes<RB, NC>(SS, L::SPLANE, mt * 128 + quad * 32 + lane, c0, S[mt]);
-  };
-  // <S, dS> at a kept state
-  auto put_edge = [&](int e) {
-    float s = 0.0f;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const float4* f = (const float4*)(a.sf + (((size_t)bn * a.ne + e) * a.nvt + vt) * MT * 128 * BV) +
-                        (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
-      if (mt * 128 + quad * 32 + lane < a.Dk) {
-#pragma unroll
-        for (int c = 0; c < NC; c += 4) {
-          const float4 x = f[(c / 4) * 128];
-          s = fmaf(x.x, S[mt][c], s);
-          s = fmaf(x.y, S[mt][c + 1], s);
-          s = fmaf(x.z, S[mt][c + 2], s);
-          s = fmaf(x.w, S[mt][c + 3], s);
+      if (one) {
+        bulk_wait_group_all();
+        bool f = false;
+        tc_commit(bar_end);
+        mbar_wait_bounded<false>(bar_end, 0, a.wait_limit_ns, nullptr, f);
+        if (failed)  // a copy of TP that nobody waited for lands before the CTA ends
+          for (int p = 0; p < 2; ++p) {
+            f = false;
+            mbar_wait_bounded<false>(bar_tp, p, a.wait_limit_ns, nullptr, f);
+          }
+      }
+    } else {  // ---- rows
+      const int t = tid - 320;  // warps 10 and 11
+      const size_t kstride = (size_t)a.Nk * a.Dk, kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk;
+      auto load_kq = [&](int ch) {
+        unsigned char* d = sm + (ch % KST) * L::KQ;
+        const int live = tc_live(a, b, ch);
+        const size_t at = kat + (size_t)ch * TC_C * kstride;
+        load_img<128, P, 64>(t, d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+        load_img<128, P, 64>(t, d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+      };
+      auto load_o = [&](int ch) {
+        load_img<RB, BV / 8, 64>(t, OS, 0, (const bf16*)(a.dO ? a.dO : a.v) + vat + (size_t)ch * TC_C * vstride, vstride,
+                                 a.dO ? tc_live(a, b, ch) : 0, a.Dv, vt * BV, BV, 0);
+        const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
+        float* d = recs + (ch & 1) * 2 * TC_C;
+        if (t < 32) cp16(smem_u32(d + t * 4), r + (t < 16 ? REC_GAM * TC_C + t * 4 : REC_BR * TC_C + (t - 16) * 4), true);
+      };
+      auto store_dv = [&](int ch) {
+        store_img<RB, 64>(t, VS, (bf16*)a.dv + vat + (size_t)ch * TC_C * vstride, vstride, min(TC_C, a.T - ch * TC_C), a.Dv, vt * BV);
+      };
+      if (t >= 0 && nch > 0) {
+        load_kq(nch - 1);
+        load_o(nch - 1);
+        cp_wait_all();
+        fence_proxy_async_smem();
+      }
+      for (int ch = nch - 1; ch >= 0; --ch) {
+        const bool more = ch > 0 && t >= 0;
+        __syncthreads();  // 1
+        if (t >= 0) {
+          if (ch + 1 < nch) store_dv(ch + 1);
+          asm volatile("bar.sync 1, 64;" ::: "memory");  // the rows are read: V's may follow
+          load_img<RB, BV / 8, 64>(t, VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv,
+                                   vt * BV, BV, 0);
+          cp_commit();
+        }
+        if (KST == 2 && more) load_kq(ch - 1);
+        cp_commit();
+        __syncthreads();  // 2
+        cp_wait<1>();     // V
+        __syncthreads();  // 3
+        if (more) load_o(ch - 1);
+        __syncthreads();  // 4
+        if (KST == 1 && more) load_kq(ch - 1);
+        if (more) {
+          cp_wait_all();
+          fence_proxy_async_smem();
         }
       }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) a.edge[(((size_t)bn * a.ne + e) * a.nvt + vt) * 8 + warp] = s;
-  };
-  if (nch > 0) {
-    load_kq(nch - 1);
-    load_o(nch - 1);
-    cp_commit();
-    put_state();
-    put_edge(0);
-  }
-  for (int ch = nch - 1; ch >= 0; --ch) {
-    const size_t item = (size_t)bn * a.nc + ch, tile = item * a.nvt + vt;
-    const bool more = ch > 0;
-    const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
-    const int live = tc_live(a, b, ch), i = (quad & 1) * 32 + lane;
-    cp_wait<0>();
-    fence_proxy_async_smem();
-    tm_fence_before();
-    __syncthreads();  // KQ, dO and dS's planes are there
-    if (tid == 0 && !failed) first(kq);
-    if (KST == 2 && more) load_kq(ch - 1);
-    const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
-    {  // the gradient of the chunk's last state, rounded, in the image of its panel
-      unsigned char* d = (unsigned char*)(a.dSh + (item * a.np + (v0 >> 6)) * a.KP * 64);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int r = mt * 128 + quad * 32 + lane;
-        if (r < a.KP)
-#pragma unroll
-          for (int c = 0; c < NC; c += 8) put_piece(d, r, ((v0 & 63) + c) >> 3, round8(S[mt] + c), lone);
+      if (t >= 0) {
+        if (nch > 0) store_dv(0);
+        const int t0 = nch * TC_C, cols = min(BV, a.Dv - vt * BV);
+        for (long long k = t; k < (long long)(a.T - t0) * cols; k += 64)
+          ((bf16*)a.dv)[vat + (size_t)(t0 + k / cols) * vstride + vt * BV + k % cols] = __float2bfloat16_rn(0.0f);
       }
     }
-    const float gi = gam[i];
-    float kept[NC];  // z (K's steps) or o (Q's), in fp32
-    {
-      const float4* f = (const float4*)((quad < 2 ? a.zf : a.of) + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
-#pragma unroll
-      for (int c = 0; c < NC; c += 4) {
-        const float4 x = f[(c / 4) * 64];
-        kept[c] = x.x, kept[c + 1] = x.y, kept[c + 2] = x.z, kept[c + 3] = x.w;
-      }
-    }
-    if (quad >= 2) {
-      const float f = gi * a.scale;
-      float d[NC], s = 0.0f;
-#pragma unroll
-      for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(OS + img<RB>(i, (c0 + c) >> 3)), d + c);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        s = fmaf(d[c], kept[c], s);
-        d[c] = gi != 0.0f ? f * d[c] : 0.0f;
-      }
-      put_planes<RB, NC>(GS, L::GPLANE, 64 + i, c0, d);
-      a.dots[((tile * 3 + 2) * 2 + half) * TC_C + i] = i < live ? s : 0.0f;
-    }
-    wait(bar, parity);
-    parity ^= 1;
-    tm_fence_after();
-    if (quad < 2) {
-      float x[NC];
-      tm_sum<NC, BV>(x, row + D1 + c0);
-      const float f = br[i];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) x[c] = f != 0.0f ? f * x[c] : 0.0f;  // no part of it before a later document
-      put_planes<RB, NC>(GS, L::GPLANE, i, c0, x);
-    }
-    fence_proxy_async_smem();
-    tm_fence_before();
-    __syncthreads();  // W's planes are there
-    if (tid == 0 && !failed) second(ch);
-    const int t = ch * TC_C + i;
-    float v[NC];
-    if (quad < 2) {  // v's row, for dc
-      const bf16* s = (const bf16*)a.v + vat + (size_t)t * vstride + v0;
-#pragma unroll
-      for (int c = 0; c < NC; c += 8) {
-        if (a.Dv % 8 == 0) {
-          widen8(i < live && c < valid ? *(const uint4*)(s + c) : make_uint4(0, 0, 0, 0), v + c);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[c + e] = i < live && c + e < valid ? __bfloat162float(s[c + e]) : 0.0f;
-        }
-      }
-    }
-    wait(bar, parity);
-    parity ^= 1;
-    tm_fence_after();
-    float y[NC];
-    if (quad < 2) {
-      tm_sum<NC, BV>(y, row + D2 + c0);
-      float g[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) g[c] = gi != 0.0f ? -gi * y[c] : 0.0f;
-      put_planes<RB, NC>(GS, L::GPLANE, i, c0, g);
-    }
-    fence_proxy_async_smem();
-    tm_fence_before();
-    __syncthreads();  // -gam dY's planes are there, dO is read
-    if (tid == 0 && !failed) third(ch, kq);
-    if (more) load_o(ch - 1);
-    cp_commit();
-    if (quad < 2) {  // what leaves for memory goes while the product runs
-      float zy = 0.0f, vy = 0.0f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        zy = fmaf(kept[c], y[c], zy);
-        vy = fmaf(v[c], y[c], vy);
-      }
-      a.dots[((tile * 3 + 0) * 2 + half) * TC_C + i] = zy;
-      a.dots[((tile * 3 + 1) * 2 + half) * TC_C + i] = -vy;
-      if (t < a.T) store_row<NC>((bf16*)a.dv + vat + (size_t)t * vstride + v0, y, valid, a.Dv % 8 == 0);
-    }
-    wait(bar, parity);
-    parity ^= 1;
-    tm_fence_after();
-    if (KST == 1) {
-      if (more) load_kq(ch - 1);
-      cp_commit();
-    }
-    const float gC = gam[TC_C - 1];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float d[NC];
-      tm_sum<NC, BV>(d, row + D3 + 3 * mt * BV + c0);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
-    }
-    if (more) {
-      put_state();
-      if (ch % TC_EDGE == 0) put_edge(ch / TC_EDGE);
-    }
-  }
-  const int t0 = nch * TC_C, cols = min(BV, a.Dv - vt * BV);
-  for (long long i = tid; i < (long long)(a.T - t0) * cols; i += 256)
-    ((bf16*)a.dv)[vat + (size_t)(t0 + i / cols) * vstride + vt * BV + i % cols] = __float2bfloat16_rn(0.0f);
-  if (a.ds0) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const uint32_t row = tm + ((uint32_t)(quad * 32) << 16);
+    float S[MT][NC];  // dS
+    const int c0 = half * NC, v0 = vt * BV + c0, valid = a.Dv - v0;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int r = mt * 128 + quad * 32 + lane;
-      if (r < a.Dk) {
-        float* s = a.ds0 + ((size_t)bn * a.Dk + r) * a.Dv + v0;
+      const float* s = a.dlast ? a.dlast + ((size_t)bn * a.Dk + r) * a.Dv + v0 : nullptr;
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-          if (c < valid) s[c] = S[mt][c];
+      for (int c = 0; c < NC; ++c) S[mt][c] = s && r < a.Dk && c < valid ? s[c] : 0.0f;
+    }
+    auto put_state = [&]() {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) put_planes<RB, NC>(SS, L::SPLANE, mt * 128 + quad * 32 + lane, c0, S[mt]);
+    };
+    // <S, dS> at a kept state
+    auto put_edge = [&](int e) {
+      float s = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const float4* f = (const float4*)(a.sf + (((size_t)bn * a.ne + e) * a.nvt + vt) * MT * 128 * BV) +
+                          (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
+        if (mt * 128 + quad * 32 + lane < a.Dk) {
+#pragma unroll
+          for (int c = 0; c < NC; c += 4) {
+            const float4 x = f[(c / 4) * 128];
+            s = fmaf(x.x, S[mt][c], s);
+            s = fmaf(x.y, S[mt][c + 1], s);
+            s = fmaf(x.z, S[mt][c + 2], s);
+            s = fmaf(x.w, S[mt][c + 3], s);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) a.edge[(((size_t)bn * a.ne + e) * a.nvt + vt) * 8 + warp] = s;
+    };
+    if (nch > 0) {
+      put_state();
+      put_edge(0);
+    }
+    const int i = (quad & 1) * 32 + lane;  // this thread's step
+    uint32_t parity = 0;
+    auto take = [&]() {
+      wait(bar, parity);
+      parity ^= 1;
+      tm_fence_after();
+    };
+    auto leave = [&]() {
+      fence_proxy_async_smem();
+      tm_fence_before();
+      __syncthreads();
+    };
+    for (int ch = nch - 1; ch >= 0; --ch) {
+      const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
+      const bool more = ch > 0;
+      leave();  // 1: KQ, dO and dS's planes are there
+      const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
+      const float gi = gam[i], bi = br[i];
+      float kept[NC];  // z (K's steps) or o (Q's), in fp32
+      {
+        const float4* f = (const float4*)((quad < 2 ? a.zf : a.of) + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) {
+          const float4 x = __ldcs(f + (c / 4) * 64);
+          kept[c] = x.x, kept[c + 1] = x.y, kept[c + 2] = x.z, kept[c + 3] = x.w;
+        }
+      }
+      if (quad >= 2) {
+        const float f = gi * a.scale;
+        float d[NC], s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(OS + img<RB>(i, (c0 + c) >> 3)), d + c);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) s = fmaf(d[c], kept[c], s);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) d[c] = gi != 0.0f ? f * d[c] : 0.0f;
+        put_planes<RB, NC>(GS, L::GPLANE, 64 + i, c0, d);
+        a.dots[((tile * 3 + 2) * 2 + half) * TC_C + i] = i < tc_live(a, b, ch) ? s : 0.0f;
+      }
+      take();
+      if (quad < 2) {
+        float x[NC];
+        tm_sum<NC, BV>(x, row + D1 + c0);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) x[c] = bi != 0.0f ? bi * x[c] : 0.0f;  // no part of it before a later document
+        put_planes<RB, NC>(GS, L::GPLANE, i, c0, x);
+      }
+      leave();  // 2: W's planes are there
+      take();
+      float y[NC];
+      if (quad < 2) {
+        tm_sum<NC, BV>(y, row + D2 + c0);
+        float g[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) g[c] = gi != 0.0f ? -gi * y[c] : 0.0f;
+        put_planes<RB, NC>(GS, L::GPLANE, i, c0, g);
+      }
+      leave();  // 3: -gam dY's planes are there, dO is read, V is there
+      if (quad < 2) {  // what leaves for memory goes while the product runs
+        float zy = 0.0f, vy = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; c += 8) {
+          uint4* at = (uint4*)(VS + img<RB>(i, (c0 + c) >> 3));
+          float v[8];
+          widen8(*at, v);
+          *at = round8(y + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            zy = fmaf(kept[c + e], y[c + e], zy);
+            vy = fmaf(v[e], y[c + e], vy);
+          }
+        }
+        a.dots[((tile * 3 + 0) * 2 + half) * TC_C + i] = zy;
+        a.dots[((tile * 3 + 1) * 2 + half) * TC_C + i] = -vy;
+      }
+      const float gC = gam[TC_C - 1];
+      take();
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float d[NC];
+        tm_sum<NC, BV>(d, row + D3 + 3 * mt * BV + c0);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
+      }
+      leave();  // 4: the products are over, dY's image is there
+      if (more) {
+        put_state();
+        if (ch % TC_EDGE == 0) put_edge(ch / TC_EDGE);
+      }
+    }
+    if (a.ds0) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 128 + quad * 32 + lane;
+        if (r < a.Dk) {
+          float* s = a.ds0 + ((size_t)bn * a.Dk + r) * a.Dv + v0;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if (c < valid) s[c] = S[mt][c];
+        }
       }
     }
   }
-  cp_wait<0>();
-  if (tid == 0 && failed) {  // a copy of TP that nobody waited for lands before the CTA ends
-    for (int p = 0; p < 2; ++p) {
-      bool f = false;
-      mbar_wait_bounded<false>(bar_tp, p, a.wait_limit_ns, nullptr, f);
-    }
-  }
-  tc_finish(bar_end, a.wait_limit_ns);
+  tm_fence_before();
+  __syncthreads();
   if (warp == 0) tm_free<512>(tm);
 }
 
 // ---- grad ----------------------------------------------------------------------------
 // TMEM: two accumulators of KT columns; the second one's hold N and F before.
-template <int KT> struct TcGrad {  // KT: Dk rounded up to 128 or 256
-  static constexpr int KQ = KT / 64 * TC_PANEL, SB = KT * 128;  // bytes of KQ and of a panel of S0
-  static constexpr int XZ = TC_PANEL + TC_PANEL / 2;            // a panel of X = [dY; dO] and of Z
-  static __host__ __device__ int at_sd(int np) { return np * XZ > KQ ? np * XZ : KQ; }
-  static __host__ __device__ size_t bytes(int np) { return (size_t)at_sd(np) + 2 * SB + 6 * TC_C * 4 + 64 + 1024; }
+template <int KT, int BV> struct TcGrad {  // KT: Dk rounded up to 128 or 256
+  static constexpr int RB = 2 * BV;
+  static constexpr int KQ = KT / 64 * TC_PANEL, SB = KT * RB;  // bytes of KQ and of a tile of S0
+  static constexpr int XB = 128 * RB, XZ = XB + 64 * RB;       // a tile of X = [dY; dO], and of it and Z
+  static constexpr int STAGES = KT == 128 && BV == 64 ? 1 : 2;  // tiles of S0 and dS1 at once; one where two CTAs an SM fit then
+  static constexpr int SD = STAGES * 2 * SB > 2 * TC_PANEL ? STAGES * 2 * SB : 2 * TC_PANEL;
+  static __host__ __device__ int at_sd(int nvt) { return (nvt * XZ > KQ ? nvt * XZ : KQ) + 1023 & ~1023; }
+  static __host__ __device__ size_t bytes(int nvt) { return (size_t)at_sd(nvt) + SD + 6 * TC_C * 4 + 64 + 1024; }
   static constexpr int COLS = KT == 128 ? 256 : 512;
 };
 
-// X and Z stay in shared memory, S0 and dS1 pass by panels of 64 columns of v. N
+// X and Z stay in shared memory, S0 and dS1 pass by tiles of BV columns of v. N
 // and F go to registers, M and R are made from them while the state's products
 // run, and multiply KQ from the buffers of S0 and dS1, KQ in X's and Z's. The
 // product of Z's 64 rows reads as many rows behind them, whose results are not
 // looked at.
-template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delta_tc_grad_kernel(DeltaTcArgs a) {
-  using L = TcGrad<KT>;
+template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delta_tc_grad_kernel(DeltaTcArgs a) {
+  using L = TcGrad<KT, BV>;
+  constexpr int RB = L::RB;
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
-  unsigned char *X = sm, *KQ = sm, *SD = sm + L::at_sd(a.np);
-  float* rec = (float*)(SD + 2 * L::SB);  // chi, clo, seg, gam, br, beta
+  unsigned char *X = sm, *KQ = sm, *SD = sm + L::at_sd(a.nvt);
+  float* rec = (float*)(SD + L::SD);  // chi, clo, seg, gam, br, beta
   const float* beta = rec + 5 * TC_C;
   uint64_t* barp = (uint64_t*)(rec + 6 * TC_C);
-  uint32_t* slot = (uint32_t*)(barp + 2);
+  uint32_t* slot = (uint32_t*)(barp + 6);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
   const long long item = blockIdx.x;
   const int ch = (int)(item % a.nc), bn = (int)(item / a.nc), n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
@@ -336,25 +365,30 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
     }
     return;
   }
-  const uint32_t bar = smem_u32(barp);
+  const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_z = bar + 16, bar_s = bar + 24, bar_m = bar + 40;  // bar_s: by stage
   if (tid == 0) {
-    mbar_init(bar, 1);
-    mbar_init(bar + 8, 1);
+    for (int k = 0; k < 6; ++k) mbar_init(bar + 8 * k, 1);
     fence_mbar_init_cluster();
+    const bf16* z = a.Zh + (size_t)item * a.nvt * 64 * BV;
+    mbar_arrive_expect_tx(bar_z, a.nvt * 64 * RB);
+    for (int p = 0; p < a.nvt; ++p) bulk_load_global(smem_u32(X + p * L::XZ + L::XB), z + (size_t)p * 64 * BV, 64 * RB, bar_z);
   }
-  auto load_sd = [&](int p) {
-    const size_t at = ((size_t)item * a.np + p) * a.KP * 64;
-    load_plain(SD, a.Sh + at, a.KP * 128);
-    load_plain(SD + L::SB, a.dSh + at, a.KP * 128);
+  auto load_sd = [&](int p) {  // one thread
+    const size_t at = ((size_t)item * a.nvt + p) * a.KP * BV;
+    const uint32_t bytes = a.KP * RB, to = smem_u32(SD + (p % L::STAGES) * 2 * L::SB), br = bar_s + 8 * (p % L::STAGES);
+    mbar_arrive_expect_tx(br, 2 * bytes);
+    bulk_load_global(to, a.Sh + at, bytes, br);
+    bulk_load_global(to + L::SB, a.dSh + at, bytes, br);
   };
-  for (int p = 0; p < a.np; ++p) {
-    unsigned char* x = X + (size_t)p * L::XZ;
-    load_img<128, 8>(x, 0, (const bf16*)a.dv + vat, vstride, live, a.Dv, p * 64, 64, 0);
-    load_img<128, 8>(x, 64, (const bf16*)(a.dO ? a.dO : a.dv) + vat, vstride, a.dO ? live : 0, a.Dv, p * 64, 64, 0);
-    load_plain(x + TC_PANEL, a.Zh + ((size_t)item * a.np + p) * 64 * 64, 64 * 128);
+  if (tid == 0) {
+    load_sd(0);
+    if (L::STAGES == 2 && a.nvt > 1) load_sd(1);
   }
-  cp_commit();
-  load_sd(0);
+  for (int p = 0; p < a.nvt; ++p) {
+    unsigned char* x = X + p * L::XZ;
+    load_img<RB, BV / 8, 256>(tid, x, 0, (const bf16*)a.dv + vat, vstride, live, a.Dv, p * BV, BV, 0);
+    load_img<RB, BV / 8, 256>(tid, x, 64, (const bf16*)(a.dO ? a.dO : a.dv) + vat, vstride, a.dO ? live : 0, a.Dv, p * BV, BV, 0);
+  }
   cp_commit();
   if (tid < TC_C) {
     const float* r = a.rec + (size_t)item * REC_N * TC_C + tid;
@@ -366,7 +400,7 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
     rec[5 * TC_C + tid] = r[REC_BETA * TC_C];
   }
   if (warp == 0) tm_alloc<L::COLS>(slot);
-  cp_wait<1>();
+  cp_wait_all();
   fence_proxy_async_smem();
   tm_fence_before();
   __syncthreads();
@@ -374,22 +408,39 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
   const uint32_t tm = *slot, row = tm + ((uint32_t)(quad * 32) << 16);
   uint32_t parity = 0;
   bool failed = false;
-  auto wait = [&]() {
-    mbar_wait_bounded<false>(bar, parity, a.wait_limit_ns, a.status, failed);
+  auto wait = [&](uint32_t which, uint32_t par) { mbar_wait_bounded<false>(which, par, a.wait_limit_ns, a.status, failed); };
+  auto take = [&]() {
+    wait(bar, parity);
     parity ^= 1;
     tm_fence_after();
   };
-  if (tid == 0) {  // [N; F] = X Z^T, in the second accumulator's columns
-    constexpr uint32_t id = tc_idesc(64, false, false);
-    for (int p = 0; p < a.np; ++p) {
-      const uint64_t x = tc_desc(smem_u32(X) + p * L::XZ, 16);
+  // the state's products of tile p
+  auto state = [&](int p) {
+    wait(bar_s + 8 * (p % L::STAGES), (p / L::STAGES) & 1);
+    if (failed) return;
+    const uint32_t id = tc_idesc(a.KP, false, false);
+    const uint64_t x = tc_desc<RB>(smem_u32(X) + p * L::XZ, 16), s = tc_desc<RB>(smem_u32(SD) + (p % L::STAGES) * 2 * L::SB, 16);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tc_mma(tm + KT, x + 2 * k, x + (TC_PANEL >> 4) + 2 * k, id, p || k);
+    for (int k = 0; k < BV / 16; ++k) tc_mma(tm, x + 2 * k, s + 2 * k, id, p || k);  // [dY; dO] S0^T
+#pragma unroll
+    for (int k = 0; k < BV / 16; ++k)  // Z dS1^T (rows 0 .. 63)
+      tc_mma(tm + KT, x + (L::XB >> 4) + 2 * k, s + (L::SB >> 4) + 2 * k, id, p || k);
+    tc_commit(p + 1 < a.nvt ? bar_m : bar);  // the CTA waits for the last tile's alone
+  };
+  if (tid == 0) {  // [N; F] = X Z^T, in the second accumulator's columns
+    wait(bar_z, 0);
+    constexpr uint32_t id = tc_idesc(64, false, false);
+    if (!failed) {
+      for (int p = 0; p < a.nvt; ++p) {
+        const uint64_t x = tc_desc<RB>(smem_u32(X) + p * L::XZ, 16);
+#pragma unroll
+        for (int k = 0; k < BV / 16; ++k) tc_mma(tm + KT, x + 2 * k, x + (L::XB >> 4) + 2 * k, id, p || k);
+      }
+      tc_commit(bar);
     }
-    tc_commit(bar);
   }
   const int i = (quad & 1) * 32 + lane, j0 = half * 32;
-  wait();
+  take();
   float nf[32];
   {
     uint32_t r[32];
@@ -399,59 +450,51 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
 #pragma unroll
     for (int c = 0; c < 32; ++c) nf[c] = __uint_as_float(r[c]);
   }
-  for (int p = 0; p < a.np; ++p) {
-    cp_wait<0>();
-    fence_proxy_async_smem();
-    tm_fence_before();
-    __syncthreads();
-    if (tid == 0 && !failed) {
-      tm_fence_after();
-      const uint32_t id = tc_idesc(a.KP, false, false);
-      const uint64_t x = tc_desc(smem_u32(X) + p * L::XZ, 16), s = tc_desc(smem_u32(SD), 16);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        tc_mma(tm, x + 2 * k, s + 2 * k, id, p || k);                                              // [dY; dO] S0^T
-        tc_mma(tm + KT, x + (TC_PANEL >> 4) + 2 * k, s + (L::SB >> 4) + 2 * k, id, p || k);        // Z dS1^T (rows 0 .. 63)
-      }
-      tc_commit(bar);
-    }
-    if (p == 0) {  // R_ij (Q's steps) or M_ij (K's), i the thread's step
-      const float ci = rec[i], li = rec[TC_C + i];
-      const int si = __float_as_int(rec[2 * TC_C + i]);
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const int j = j0 + c;
-        const bool on = (quad < 2 ? i > j : i >= j) && si == __float_as_int(rec[2 * TC_C + j]);
-        nf[c] = on ? (quad < 2 ? -nf[c] : a.scale * nf[c]) * expf((ci - rec[j]) + (li - rec[TC_C + j])) * beta[j] : 0.0f;
-      }
-    }
-    wait();
-    if (p + 1 < a.np) {
-      load_sd(p + 1);
-    } else {  // X and Z are done with
-      load_img<128, KT / 8>(KQ, 0, (const bf16*)a.k + kat, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
-      load_img<128, KT / 8>(KQ, 64, (const bf16*)a.q + kat, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
-    }
-    cp_commit();
+  tm_fence_before();
+  __syncthreads();
+  if (tid == 0 && !failed) {
+    tm_fence_after();
+    state(0);
   }
-  {  // [M + M^T, R^T; R, 0] over the buffers of S0 and dS1: two panels of 128 rows
-    if (quad >= 2) {
+  {  // R_ij (Q's steps) or M_ij (K's), i the thread's step
+    const float ci = rec[i], li = rec[TC_C + i];
+    const int si = __float_as_int(rec[2 * TC_C + i]);
 #pragma unroll
-      for (int c = 0; c < 32; c += 8) {
-        *(uint4*)(SD + img<128>(64 + i, (j0 + c) >> 3)) = round8(nf + c);
-        *(uint4*)(SD + TC_PANEL + img<128>(64 + i, (j0 + c) >> 3)) = make_uint4(0, 0, 0, 0);
-      }
+    for (int c = 0; c < 32; ++c) {
+      const int j = j0 + c;
+      const bool on = (quad < 2 ? i > j : i >= j) && si == __float_as_int(rec[2 * TC_C + j]);
+      nf[c] = on ? (quad < 2 ? -nf[c] : a.scale * nf[c]) * __expf((ci - rec[j]) + (li - rec[TC_C + j])) * beta[j] : 0.0f;
+    }
+  }
+  if (tid == 0)
+    for (int p = 1; p < a.nvt && !failed; ++p) {
+      wait(bar_m, (p - 1) & 1);  // before the next commit: the barrier's parity tells two phases apart
+      if (L::STAGES == 1) load_sd(p);
+      else if (p + 1 < a.nvt) load_sd(p + 1);
+      state(p);
+    }
+  take();
+  // X and Z are done with
+  load_img<128, KT / 8, 256>(tid, KQ, 0, (const bf16*)a.k + kat, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+  load_img<128, KT / 8, 256>(tid, KQ, 64, (const bf16*)a.q + kat, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+  cp_commit();
+  // [M + M^T, R^T; R, 0] over the buffers of S0 and dS1: two panels of 128 rows
+  if (quad >= 2) {
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        *(bf16*)(SD + TC_PANEL + img<128>(j0 + c, i >> 3) + (i & 7) * 2) = __float2bfloat16_rn(nf[c]);
-    } else {
+    for (int c = 0; c < 32; c += 8) {
+      *(uint4*)(SD + img<128>(64 + i, (j0 + c) >> 3)) = round8(nf + c);
+      *(uint4*)(SD + TC_PANEL + img<128>(64 + i, (j0 + c) >> 3)) = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const int j = j0 + c;
-        const bf16 m = __float2bfloat16_rn(nf[c]);
-        if (j <= i) *(bf16*)(SD + img<128>(i, j >> 3) + (j & 7) * 2) = m;
-        if (j < i) *(bf16*)(SD + img<128>(j, i >> 3) + (i & 7) * 2) = m;
-      }
+    for (int c = 0; c < 32; ++c)
+      *(bf16*)(SD + TC_PANEL + img<128>(j0 + c, i >> 3) + (i & 7) * 2) = __float2bfloat16_rn(nf[c]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const int j = j0 + c;
+      const bf16 m = __float2bfloat16_rn(nf[c]);
+      if (j <= i) *(bf16*)(SD + img<128>(i, j >> 3) + (j & 7) * 2) = m;
+      if (j < i) *(bf16*)(SD + img<128>(j, i >> 3) + (i & 7) * 2) = m;
     }
   }
   // The state's parts, scaled by rows in fp32, back into the first accumulator
@@ -475,7 +518,7 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
         : "memory");
   }
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-  cp_wait<0>();
+  cp_wait_all();
   fence_proxy_async_smem();
   tm_fence_before();
   __syncthreads();
@@ -487,28 +530,46 @@ template <int KT> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delt
     for (int k = 0; k < 8; ++k) tc_mma(tm, m + (k >> 2) * (TC_PANEL >> 4) + (k & 3) * 2, k0 + k * 128, id, true);
     tc_commit(bar);
   }
-  wait();
-  for (int c = half * 16; c < a.KP; c += 32) {
-    uint32_t r[16];
-    tm_ld16(r, row + c);
-    tm_wait_ld();
-    float x[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]);
-    if (i < steps) {
-      const int valid = a.Dk - c;
-      if (shared_heads) {
+  take();
+  if (shared_heads) {
+    for (int c = half * 16; c < a.KP; c += 32) {
+      uint32_t r[16];
+      tm_ld16(r, row + c);
+      tm_wait_ld();
+      if (i < steps) {
         float* p = (quad < 2 ? a.pk : a.pq) + pat + (size_t)i * pstride + c;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (e < valid) p[e] = x[e];
-      } else {
-        store_row<16>((bf16*)(quad < 2 ? a.dk : a.dq) + kat + (size_t)i * kstride + c, x, valid, a.Dk % 8 == 0);
+          if (e < a.Dk - c) p[e] = __uint_as_float(r[e]);
       }
+      __syncwarp();
     }
-    __syncwarp();
+  } else {  // dK and dQ by way of KQ's image, so that rows leave whole
+    for (int c = half * 16; c < a.KP; c += 32) {
+      uint32_t r[16];
+      tm_ld16(r, row + c);
+      tm_wait_ld();
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]);
+      unsigned char* d = KQ + (c >> 6) * TC_PANEL;
+      *(uint4*)(d + img<128>(quad * 32 + lane, (c & 63) >> 3)) = round8(x);
+      *(uint4*)(d + img<128>(quad * 32 + lane, ((c & 63) >> 3) + 1)) = round8(x + 8);
+    }
+    __syncthreads();
+    for (int c = 0; c < a.Dk; c += 64) {
+      store_img<128, 256>(tid, KQ + (c >> 6) * TC_PANEL, (bf16*)a.dk + kat, kstride, steps, a.Dk, c);
+      store_img<128, 256>(tid, KQ + (c >> 6) * TC_PANEL + 64 * 128, (bf16*)a.dq + kat, kstride, steps, a.Dk, c);
+    }
   }
-  tc_finish(bar + 8, a.wait_limit_ns);
+  if (tid == 0 && failed) {  // copies that nobody waited for land before the CTA ends
+    for (int k = 0; k < 1 + L::STAGES; ++k)
+      for (int q = 0; q < 2; ++q) {
+        bool f = false;
+        mbar_wait_bounded<false>(bar_z + 8 * k, q, a.wait_limit_ns, nullptr, f);
+      }
+  }
+  tc_finish(bar_end, a.wait_limit_ns);
   if (warp == 0) tm_free<L::COLS>(tm);
 }
 
@@ -586,15 +647,15 @@ template <int BV, int MT> cudaError_t back(const DeltaTcArgs& a, cudaStream_t st
   constexpr int sm = TcBack<BV, MT>::BYTES;
   cudaError_t e = set_smem_attr((const void*)delta_tc_back_kernel<BV, MT>, sm);
   if (e != cudaSuccess) return e;
-  delta_tc_back_kernel<BV, MT><<<(unsigned)(a.B * a.N * a.nvt), 256, sm, st>>>(a);
+  delta_tc_back_kernel<BV, MT><<<(unsigned)(a.B * a.N * a.nvt), 384, sm, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }
-template <int KT> cudaError_t grad(const DeltaTcArgs& a, cudaStream_t st) {
-  const size_t sm = TcGrad<KT>::bytes(a.np);
-  cudaError_t e = set_smem_attr((const void*)delta_tc_grad_kernel<KT>, sm);
+template <int KT, int BV> cudaError_t grad(const DeltaTcArgs& a, cudaStream_t st) {
+  const size_t sm = TcGrad<KT, BV>::bytes(a.nvt);
+  cudaError_t e = set_smem_attr((const void*)delta_tc_grad_kernel<KT, BV>, sm);
   if (e != cudaSuccess) return e;
-  delta_tc_grad_kernel<KT><<<(unsigned)((long long)a.B * a.N * a.nc), 256, sm, st>>>(a);
+  delta_tc_grad_kernel<KT, BV><<<(unsigned)((long long)a.B * a.N * a.nc), 256, sm, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }
@@ -604,7 +665,7 @@ template <int KT> cudaError_t grad(const DeltaTcArgs& a, cudaStream_t st) {
 cudaError_t delta_tc_bwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st) {
   cudaError_t e = a.KP > 128 ? back<32, 2>(a, st) : BV == 64 ? back<64, 1>(a, st) : back<32, 1>(a, st);
   if (e != cudaSuccess) return e;
-  if ((e = a.KP > 128 ? grad<256>(a, st) : grad<128>(a, st)) != cudaSuccess) return e;
+  if ((e = a.KP > 128 ? grad<256, 32>(a, st) : BV == 64 ? grad<128, 64>(a, st) : grad<128, 32>(a, st)) != cudaSuccess) return e;
   const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE;
   delta_tc_gates_kernel<<<(unsigned)(a.B * a.N * groups), TC_EDGE * TC_C, 0, st>>>(a);
   note_launch();

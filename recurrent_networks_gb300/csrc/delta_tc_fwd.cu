@@ -208,29 +208,33 @@ template <int BV, int MT> struct TcChain {
   static constexpr int RB = 2 * BV, KST = MT == 1 ? 2 : 1;  // bytes of a tile's row; stages of KQ
   static constexpr int KQ = 2 * MT * TC_PANEL, TP = 3 * TC_PANEL, SPLANE = MT * 128 * RB, YPLANE = 64 * RB;
   static constexpr int AT_TP = KST * KQ, AT_S = AT_TP + TP, AT_Y = AT_S + 3 * SPLANE, AT_V = AT_Y + 3 * YPLANE;
-  static constexpr int AT_REC = AT_V + YPLANE, BYTES = AT_REC + 2 * 2 * 64 * 4 + 64 + 1024;
+  static constexpr int AT_Z = AT_V + YPLANE, AT_O = AT_Z + YPLANE;  // rounded, on their way out
+  static constexpr int AT_REC = AT_O + YPLANE, BYTES = AT_REC + 2 * 2 * 64 * 4 + 64 + 1024;
 };
 
-// 8 warps: warp w has lanes 32 (w % 4) .. of the accumulators (rows 0 .. 63: K's
-// steps, 64 .. 127: Q's; or rows of the state) and half of the tile's columns.
-// Thread 0 issues the products (with their operands' addresses worked out before:
-// 100 cycles a product otherwise) and brings TP by one bulk copy, the others load
-// the rest of the next chunk while the products run. MT: tiles of 128 state rows,
-// whose fp32 values stay in registers. A chunk is three dependent products and
-// their ways through registers.
+// Warps 0 .. 7 take values through registers: warp w has lanes 32 (w % 4) .. of
+// the accumulators (rows 0 .. 63: K's steps, 64 .. 127: Q's; or rows of the state)
+// and half of the tile's columns. Thread 256 issues the products and the bulk
+// copies of images (an issuing thread waits while earlier products run: 150
+// cycles a product), warps 10 and 11 load and store the rows of tensors. The third
+// warpgroup gives registers to the other two: 256 * 200 + 128 * 104 = 384 * 168.
+// MT: tiles of 128 state rows, whose fp32 values stay in registers. A chunk is
+// three dependent products (2000 cycles for BV = 64, Dk = 128) and their ways
+// through registers between barriers of the whole CTA.
 template <int BV, int MT>
-__global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
+__global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
   using L = TcChain<BV, MT>;
   constexpr int RB = L::RB, NC = BV / 2, KST = L::KST, P = MT * 16;
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
-  unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *YS = sm + L::AT_Y, *VS = sm + L::AT_V;
+  unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *YS = sm + L::AT_Y, *VS = sm + L::AT_V, *ZS = sm + L::AT_Z, *OS = sm + L::AT_O;
   float* recs = (float*)(sm + L::AT_REC);  // [2][gam, br][64]
   uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
   uint32_t* slot = (uint32_t*)(barp + 3);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
   const int vt = blockIdx.x % a.nvt, bn = blockIdx.x / a.nvt, n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
   const int nch = tc_chunks(a, b);
+  const size_t vstride = (size_t)a.N * a.Dv, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
   const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16;
   if (tid == 0) {
     for (int k = 0; k < 3; ++k) mbar_init(bar + 8 * k, 1);
@@ -244,223 +248,245 @@ __global__ void __launch_bounds__(256, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
   // accumulators, three blocks of BV columns each: D1 (K S0, Q S0) and D3 (the state's change, by tile), D2 (Z, PT Y)
   constexpr int D1 = 0, D2 = 3 * BV * MT, D3 = 0;
   bool failed = false;
-  uint32_t parity = 0;
   auto wait = [&](uint32_t which, uint32_t par) { mbar_wait_bounded<false>(which, par, a.wait_limit_ns, a.status, failed); };
 
-  // thread 0 issues the products and brings TP
-  const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
-  if (tid == 0 && nch > 0) load_bulk(TP, tp, L::TP, bar_tp);
-  const uint64_t td = tc_desc(smem_u32(TP), 16), yd = tc_desc<RB>(smem_u32(YS), L::YPLANE);
-  auto first = [&](uint32_t kq) {
-    tm_fence_after();
-    tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
-    tc_commit(bar);
-  };
-  auto second = [&](int ch) {
-    wait(bar_tp, ch & 1);
-    if (failed) return;
-    tm_fence_after();
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 8) {  // ---- products, bulk copies
+      const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
+      const bool one = lane == 0;
+      if (one && nch > 0) load_bulk(TP, tp, L::TP, bar_tp);
+      const uint64_t td = tc_desc(smem_u32(TP), 16), yd = tc_desc<RB>(smem_u32(YS), L::YPLANE);
+      for (int ch = 0; ch < nch; ++ch) {
+        const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
+        const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
+        __syncthreads();  // 1
+        if (one && !failed) {
+          tm_fence_after();
+          tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
+          tc_commit(bar);
+          if (a.Sh) {  // the chunk's starting state, rounded: its first plane
+            store_bulk(a.Sh + tile * a.KP * BV, SS, a.KP * RB);
+            bulk_commit_group();
+          }
+        }
+        __syncthreads();  // 2
+        if (one) {
+          wait(bar_tp, ch & 1);
+          if (!failed) {
+            tm_fence_after();
 #pragma unroll
-    for (int p = 0; p < 3; ++p)  // plane p of TP, the first 3 - p of Y
+            for (int p = 0; p < 3; ++p)  // plane p of TP, the first 3 - p of Y
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + 2 * k, yd + k * RB, tc_idesc((3 - p) * BV, false, true), p || k);
-    tc_commit(bar);
-  };
-  auto third = [&](int ch, uint32_t kq) {
-    tm_fence_after();
+              for (int k = 0; k < 4; ++k)
+                tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + 2 * k, yd + k * RB, tc_idesc((3 - p) * BV, false, true), p || k);
+            tc_commit(bar);
+          }
+          bulk_wait_group_read<0>();  // the state's planes and Z's image may be written again
+        }
+        __syncthreads();  // 3
+        if (one && !failed) {
+          tm_fence_after();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc_mma(tm + D3 + 3 * mt * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 2048, TC_PANEL), yd + k * RB,
-               tc_idesc(3 * BV, true, true), k);
-    tc_commit(bar);
-    if (ch + 1 < nch) load_bulk(TP, tp + (size_t)(ch + 1) * L::TP, L::TP, bar_tp);  // the second products have read it
-  };
-  const uint32_t row = tm + ((uint32_t)(quad * 32) << 16);
-  const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv;
-  const size_t kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
-  auto load_kq = [&](int ch) {
-    unsigned char* d = sm + (ch % KST) * L::KQ;
-    const int live = tc_live(a, b, ch);
-    const size_t at = kat + (size_t)ch * TC_C * kstride;
-    load_img<128, P>(d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
-    load_img<128, P>(d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
-  };
-  auto load_v = [&](int ch) {
-    load_img<RB, BV / 8>(VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv, vt * BV,
-                         BV, 0);
-    const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
-    float* d = recs + (ch & 1) * 2 * TC_C;
-    if (tid < 16) cp16(smem_u32(d + tid * 4), r + REC_GAM * TC_C + tid * 4, true);
-    else if (tid < 32) cp16(smem_u32(d + tid * 4), r + REC_BR * TC_C + (tid - 16) * 4, true);
-  };
-  float S[MT][NC];
-  const int c0 = half * NC, v0 = vt * BV + c0;  // this thread's columns, in the tile and in v
-  const int valid = a.Dv - v0;
-  const bool lone = BV == 32 && vt == a.nvt - 1 && vt % 2 == 0;  // nobody has the other half of the panel
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int r = mt * 128 + quad * 32 + lane;
-    const float* s = a.s0 ? a.s0 + ((size_t)bn * a.Dk + r) * a.Dv + v0 : nullptr;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) S[mt][c] = s && r < a.Dk && c < valid ? s[c] : 0.0f;
-  }
-  auto put_state = [&]() {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) put_planes<RB, NC>(SS, L::SPLANE, mt * 128 + quad * 32 + lane, c0, S[mt]);
-  };
-  // S, as the threads hold it, to kept state e
-  auto keep_state = [&](int e) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float4* f = (float4*)(a.sf + (((size_t)bn * a.ne + e) * a.nvt + vt) * MT * 128 * BV) +
-                  (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
-#pragma unroll
-      for (int c = 0; c < NC; c += 4) f[(c / 4) * 128] = make_float4(S[mt][c], S[mt][c + 1], S[mt][c + 2], S[mt][c + 3]);
-    }
-  };
-  if (nch > 0) {
-    load_kq(0);
-    load_v(0);
-    cp_commit();
-    put_state();
-  } else if (a.sf) {
-    keep_state(0);
-  }
-  const int i = (quad & 1) * 32 + lane;  // this thread's step
-  for (int ch = 0; ch < nch; ++ch) {
-    const size_t item = (size_t)bn * a.nc + ch, tile = item * a.nvt + vt;
-    const bool more = ch + 1 < nch;
-    cp_wait<0>();
-    fence_proxy_async_smem();
-    tm_fence_before();
-    __syncthreads();  // KQ, V and S's planes are there
-    const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
-    if (tid == 0 && !failed) first(kq);
-    if (KST == 2 && more) load_kq(ch + 1);
-    const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
-    const float gi = gam[i];
-    if (a.Sh) {  // the chunk's starting state, rounded, in the image of its panel
-      unsigned char* d = (unsigned char*)(a.Sh + (item * a.np + (v0 >> 6)) * a.KP * 64);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int r = mt * 128 + quad * 32 + lane;
-        if (r < a.KP)
-#pragma unroll
-          for (int c = 0; c < NC; c += 8) put_piece(d, r, ((v0 & 63) + c) >> 3, round8(S[mt] + c), lone);
+            for (int k = 0; k < 4; ++k)
+              tc_mma(tm + D3 + 3 * mt * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 2048, TC_PANEL), yd + k * RB,
+                     tc_idesc(3 * BV, true, true), k);
+          tc_commit(bar);
+          if (ch + 1 < nch) load_bulk(TP, tp + (size_t)(ch + 1) * L::TP, L::TP, bar_tp);  // the second products have read it
+        }
+        __syncthreads();  // 4
+        if (one && a.Zh && !failed) {
+          store_bulk(a.Zh + tile * 64 * BV, ZS, L::YPLANE);
+          bulk_commit_group();
+        }
+      }
+      if (one) {
+        bulk_wait_group_all();
+        bool f = false;
+        tc_commit(bar_end);
+        mbar_wait_bounded<false>(bar_end, 0, a.wait_limit_ns, nullptr, f);
+        if (failed)  // a copy of TP that nobody waited for lands before the CTA ends
+          for (int p = 0; p < 2; ++p) {
+            f = false;
+            mbar_wait_bounded<false>(bar_tp, p, a.wait_limit_ns, nullptr, f);
+          }
+      }
+    } else {  // ---- rows
+      const int t = tid - 320;  // warps 10 and 11
+      const size_t kstride = (size_t)a.Nk * a.Dk, kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk;
+      auto load_kq = [&](int ch) {
+        unsigned char* d = sm + (ch % KST) * L::KQ;
+        const int live = tc_live(a, b, ch);
+        const size_t at = kat + (size_t)ch * TC_C * kstride;
+        load_img<128, P, 64>(t, d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+        load_img<128, P, 64>(t, d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+      };
+      auto load_v = [&](int ch) {
+        load_img<RB, BV / 8, 64>(t, VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv,
+                                 vt * BV, BV, 0);
+        const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
+        float* d = recs + (ch & 1) * 2 * TC_C;
+        if (t < 32) cp16(smem_u32(d + t * 4), r + (t < 16 ? REC_GAM * TC_C + t * 4 : REC_BR * TC_C + (t - 16) * 4), true);
+      };
+      auto store_o = [&](int ch) {
+        store_img<RB, 64>(t, OS, (bf16*)a.o + vat + (size_t)ch * TC_C * vstride, vstride, min(TC_C, a.T - ch * TC_C), a.Dv, vt * BV);
+      };
+      if (t >= 0 && nch > 0) {
+        load_kq(0);
+        load_v(0);
+        cp_wait_all();
+        fence_proxy_async_smem();
+      }
+      for (int ch = 0; ch < nch; ++ch) {
+        const bool more = ch + 1 < nch && t >= 0;
+        __syncthreads();  // 1
+        if (KST == 2 && more) load_kq(ch + 1);
+        if (t >= 0 && ch > 0) store_o(ch - 1);
+        __syncthreads();  // 2
+        if (more) load_v(ch + 1);
+        __syncthreads();  // 3
+        __syncthreads();  // 4
+        if (KST == 1 && more) load_kq(ch + 1);
+        if (more) {
+          cp_wait_all();
+          fence_proxy_async_smem();
+        }
+      }
+      if (t >= 0) {
+        if (nch > 0) store_o(nch - 1);
+        // steps past the row's length
+        const int t0 = nch * TC_C, cols = min(BV, a.Dv - vt * BV);
+        for (long long k = t; k < (long long)(a.T - t0) * cols; k += 64)
+          ((bf16*)a.o)[vat + (size_t)(t0 + k / cols) * vstride + vt * BV + k % cols] = __float2bfloat16_rn(0.0f);
       }
     }
-    float y[NC];
-    if (quad < 2)
-#pragma unroll
-      for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(VS + img<RB>(i, (c0 + c) >> 3)), y + c);
-    wait(bar, parity);
-    parity ^= 1;
-    tm_fence_after();
-    float x[NC];
-    tm_sum<NC, BV>(x, row + D1 + c0);
-    if (quad < 2) {
-      if (gi != 0.0f)  // behind a reset the old state has no part, whatever it holds
-#pragma unroll
-        for (int c = 0; c < NC; ++c) y[c] = fmaf(-gi, x[c], y[c]);
-      put_planes<RB, NC>(YS, L::YPLANE, i, c0, y);
-    } else {
-      const float f = gi * a.scale;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) x[c] = gi != 0.0f ? f * x[c] : 0.0f;
-    }
-    fence_proxy_async_smem();
-    tm_fence_before();
-    __syncthreads();  // Y's planes are there, V is read
-    if (tid == 0 && !failed) second(ch);
-    if (more) load_v(ch + 1);
-    cp_commit();
-    wait(bar, parity);
-    parity ^= 1;
-    tm_fence_after();
-    float z[NC];
-    tm_sum<NC, BV>(z, row + D2 + c0);
-    if (quad < 2) {
-      const float f = br[i];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) y[c] = f * z[c];
-      put_planes<RB, NC>(YS, L::YPLANE, i, c0, y);  // the products have read Y
-    }
-    fence_proxy_async_smem();
-    tm_fence_before();
-    __syncthreads();  // beta rho Z's planes are there
-    if (tid == 0 && !failed) third(ch, kq);
-    // what leaves for memory goes while the product runs
-    if (quad < 2) {
-      if (a.Zh) {
-        unsigned char* d = (unsigned char*)(a.Zh + (item * a.np + (v0 >> 6)) * 64 * 64);
-        float4* f = (float4*)(a.zf + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
-#pragma unroll
-        for (int c = 0; c < NC; c += 8) put_piece(d, i, ((v0 & 63) + c) >> 3, round8(z + c), lone);
-#pragma unroll
-        for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
-      }
-    } else {
-      const int t = ch * TC_C + i;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) z[c] += x[c];
-      if (a.of) {
-        float4* f = (float4*)(a.of + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
-#pragma unroll
-        for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
-      }
-      if (t < a.T) {
-        if (i >= tc_live(a, b, ch))
-#pragma unroll
-          for (int c = 0; c < NC; ++c) z[c] = 0.0f;
-        store_row<NC>((bf16*)a.o + vat + (size_t)t * vstride + v0, z, valid, a.Dv % 8 == 0);
-      }
-    }
-    const float gC = gam[TC_C - 1];
-    wait(bar, parity);
-    parity ^= 1;
-    tm_fence_after();
-    if (KST == 1) {
-      if (more) load_kq(ch + 1);
-      cp_commit();
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float d[NC];
-      tm_sum<NC, BV>(d, row + D3 + 3 * mt * BV + c0);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
-    }
-    if (more) put_state();
-    const int end = !more ? 0 : (ch + 1) % TC_EDGE == 0 ? (ch + 1) / TC_EDGE : -1;
-    if (a.sf && end >= 0) keep_state(end);
-  }
-  // steps past the row's length
-  const int t0 = nch * TC_C, cols = min(BV, a.Dv - vt * BV);
-  for (long long k = tid; k < (long long)(a.T - t0) * cols; k += 256)
-    ((bf16*)a.o)[vat + (size_t)(t0 + k / cols) * vstride + vt * BV + k % cols] = __float2bfloat16_rn(0.0f);
-  if (a.last) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const uint32_t row = tm + ((uint32_t)(quad * 32) << 16);
+    float S[MT][NC];
+    const int c0 = half * NC, v0 = vt * BV + c0;  // this thread's columns, in the tile and in v
+    const int valid = a.Dv - v0;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int r = mt * 128 + quad * 32 + lane;
-      if (r < a.Dk) {
-        float* s = a.last + ((size_t)bn * a.Dk + r) * a.Dv + v0;
+      const float* s = a.s0 ? a.s0 + ((size_t)bn * a.Dk + r) * a.Dv + v0 : nullptr;
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-          if (c < valid) s[c] = S[mt][c];
+      for (int c = 0; c < NC; ++c) S[mt][c] = s && r < a.Dk && c < valid ? s[c] : 0.0f;
+    }
+    auto put_state = [&]() {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) put_planes<RB, NC>(SS, L::SPLANE, mt * 128 + quad * 32 + lane, c0, S[mt]);
+    };
+    // S, as the threads hold it, to kept state e
+    auto keep_state = [&](int e) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float4* f = (float4*)(a.sf + (((size_t)bn * a.ne + e) * a.nvt + vt) * MT * 128 * BV) +
+                    (size_t)(half * MT + mt) * (NC / 4) * 128 + quad * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) f[(c / 4) * 128] = make_float4(S[mt][c], S[mt][c + 1], S[mt][c + 2], S[mt][c + 3]);
+      }
+    };
+    if (nch > 0) put_state();
+    else if (a.sf) keep_state(0);
+    const int i = (quad & 1) * 32 + lane;  // this thread's step
+    uint32_t parity = 0;
+    auto take = [&]() {
+      wait(bar, parity);
+      parity ^= 1;
+      tm_fence_after();
+    };
+    auto leave = [&]() {
+      fence_proxy_async_smem();
+      tm_fence_before();
+      __syncthreads();
+    };
+    for (int ch = 0; ch < nch; ++ch) {
+      const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
+      const bool more = ch + 1 < nch;
+      leave();  // 1: KQ, V and S's planes are there
+      const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
+      const float gi = gam[i];
+      float y[NC];
+      if (quad < 2)
+#pragma unroll
+        for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(VS + img<RB>(i, (c0 + c) >> 3)), y + c);
+      take();
+      float x[NC];
+      tm_sum<NC, BV>(x, row + D1 + c0);
+      if (quad < 2) {
+        if (gi != 0.0f)  // behind a reset the old state has no part, whatever it holds
+#pragma unroll
+          for (int c = 0; c < NC; ++c) y[c] = fmaf(-gi, x[c], y[c]);
+        put_planes<RB, NC>(YS, L::YPLANE, i, c0, y);
+      } else {
+        const float f = gi * a.scale;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) x[c] = gi != 0.0f ? f * x[c] : 0.0f;
+      }
+      leave();  // 2: Y's planes are there, V is read
+      const int live = tc_live(a, b, ch);
+      const float bi = br[i];
+      take();
+      float z[NC];
+      tm_sum<NC, BV>(z, row + D2 + c0);
+      if (quad < 2) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) y[c] = bi * z[c];
+        put_planes<RB, NC>(YS, L::YPLANE, i, c0, y);  // the products have read Y
+      }
+      leave();  // 3: beta rho Z's planes are there
+      // what leaves for memory goes while the product runs
+      if (quad < 2) {
+        if (a.Zh) {
+          float4* f = (float4*)(a.zf + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
+#pragma unroll
+          for (int c = 0; c < NC; c += 8) *(uint4*)(ZS + img<RB>(i, (c0 + c) >> 3)) = round8(z + c);
+#pragma unroll
+          for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) z[c] = i < live ? z[c] + x[c] : 0.0f;
+        if (a.of) {
+          float4* f = (float4*)(a.of + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
+#pragma unroll
+          for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; c += 8) *(uint4*)(OS + img<RB>(i, (c0 + c) >> 3)) = round8(z + c);
+      }
+      const float gC = gam[TC_C - 1];
+      take();
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float d[NC];
+        tm_sum<NC, BV>(d, row + D3 + 3 * mt * BV + c0);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
+      }
+      leave();  // 4: the products are over, Z's image is there
+      if (more) put_state();
+      const int end = !more ? 0 : (ch + 1) % TC_EDGE == 0 ? (ch + 1) / TC_EDGE : -1;
+      if (a.sf && end >= 0) keep_state(end);
+    }
+    if (a.last) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 128 + quad * 32 + lane;
+        if (r < a.Dk) {
+          float* s = a.last + ((size_t)bn * a.Dk + r) * a.Dv + v0;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if (c < valid) s[c] = S[mt][c];
+        }
       }
     }
   }
-  cp_wait<0>();
-  if (tid == 0 && failed) {  // a copy of TP that nobody waited for lands before the CTA ends
-    for (int p = 0; p < 2; ++p) {
-      bool f = false;
-      mbar_wait_bounded<false>(bar_tp, p, a.wait_limit_ns, nullptr, f);
-    }
-  }
-  tc_finish(bar_end, a.wait_limit_ns);
+  tm_fence_before();
+  __syncthreads();
   if (warp == 0) tm_free<512>(tm);
 }
 
@@ -468,7 +494,7 @@ template <int BV, int MT> cudaError_t chain(const DeltaTcArgs& a, cudaStream_t s
   constexpr int sm = TcChain<BV, MT>::BYTES;
   cudaError_t e = set_smem_attr((const void*)delta_tc_chain_kernel<BV, MT>, sm);
   if (e != cudaSuccess) return e;
-  delta_tc_chain_kernel<BV, MT><<<(unsigned)(a.B * a.N * a.nvt), 256, sm, st>>>(a);
+  delta_tc_chain_kernel<BV, MT><<<(unsigned)(a.B * a.N * a.nvt), 384, sm, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }
