@@ -142,10 +142,11 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 // What the calls lay out in the tape (behind the status word) and the workspace.
 struct DeltaSizes {
   bool bf;
-  int C, NP, BV, KP, nvt;
+  int C, NP, BV, KP, nvt, segs, seglen;
   long long nc, items, ne;
   size_t rec, tri, S, Z, zf, sf;  // bytes
-  size_t tape, scratch;           // with what a backward needs, and without
+  size_t M, H;                    // of the segments' maps, of H and of the states between
+  size_t tape;
   size_t dots, edge, part, bwd;
 };
 
@@ -154,19 +155,21 @@ bool delta_heads_ok(int Nk, int N, int Dk, int Dv, int dtype) {
          Dv <= RNN_DELTA_MAX_D && (dtype == RNN_F32 || dtype == RNN_BF16);
 }
 
-bool delta_sizes(const rnn_delta_dims_t* d, DeltaSizes* z) {
+// keep: with what a backward needs
+bool delta_sizes(const rnn_delta_dims_t* d, bool keep, DeltaSizes* z) {
   if (!d || d->B < 1 || d->T < 0 || d->T > INT_MAX - 64 || !delta_heads_ok(d->Nk, d->N, d->Dk, d->Dv, d->dtype)) return false;
   *z = DeltaSizes{};
   z->bf = d->dtype == RNN_BF16;
   z->C = z->bf ? TC_C : DeltaCfg<float>::C;
   z->NP = 3;
   z->KP = (d->Dk + 15) / 16 * 16;
-  z->BV = delta_bv(z->bf, d->B, d->N, d->Dv, z->KP, device_sms());
-  z->nvt = (d->Dv + z->BV - 1) / z->BV;
   z->nc = ((long long)d->T + z->C - 1) / z->C;
   z->items = z->nc * d->B * d->N;
-  // the kernels count the items' tiles and the heads' tiles in 32 bits
-  if (z->items * z->nvt > INT_MAX || (long long)d->B * d->N * z->nvt > INT_MAX) return false;
+  if ((long long)d->B * d->N * 64 > INT_MAX || z->items > INT_MAX / 16) return false;  // counted in 32 bits with their tiles
+  DeltaLay lay{32, 1, 0};
+  if (z->bf) lay = delta_lay((long long)d->B * d->N, d->Dv, z->KP, z->nc, device_sms(), keep);
+  z->BV = lay.BV; z->segs = lay.segs; z->seglen = lay.seglen;
+  z->nvt = (d->Dv + z->BV - 1) / z->BV;
   const size_t n = (size_t)z->items, heads = (size_t)d->B * d->N;
   z->rec = up256(n * REC_N * z->C * 4);
   if (z->bf) {
@@ -176,16 +179,21 @@ bool delta_sizes(const rnn_delta_dims_t* d, DeltaSizes* z) {
     z->Z = up256(n * z->nvt * 64 * z->BV * 2);
     z->zf = up256(n * z->nvt * 64 * z->BV * 4);
     z->sf = up256(heads * z->ne * z->nvt * (z->KP > 128 ? 256 : 128) * z->BV * 4);
-    z->scratch = z->rec + z->tri;
-    z->tape = z->scratch + z->S + z->Z + 2 * z->zf + z->sf;
+    if (z->segs > 1) {
+      const size_t KR = z->KP > 128 ? 256 : 128;
+      z->M = up256(heads * z->segs * KR * KR * 4);
+      z->H = up256(heads * z->segs * z->nvt * z->BV * KR * 4);
+    }
+    z->tape = z->rec + z->tri + z->M + 2 * z->H;
+    if (keep) z->tape += z->S + z->Z + 2 * z->zf + z->sf;
     z->dots = up256(n * z->nvt * 6 * TC_C * 4);
     z->edge = up256(heads * z->ne * z->nvt * 8 * 4);
-    z->bwd = z->S + z->dots + z->edge;
+    z->bwd = z->S + z->dots + z->edge + 2 * z->H;
   } else {
     z->tri = up256(n * z->NP * z->C * z->C * 2);  // each of Tm and P
     z->S = up256(n * z->nvt * z->NP * z->KP * z->BV * 2);
     z->Z = up256(n * z->nvt * z->NP * z->C * z->BV * 2);
-    z->scratch = z->tape = z->rec + 2 * z->tri + z->S + z->Z;
+    z->tape = z->rec + 2 * z->tri + z->S + z->Z;
     z->bwd = z->S + z->Z;
   }
   z->part = d->N != d->Nk ? up256((size_t)d->B * d->T * d->N * d->Dk * 4) : 0;
@@ -213,11 +221,16 @@ DeltaTcArgs delta_tc_args(const rnn_delta_dims_t* d, const DeltaSizes& z, void* 
   a.KP = z.KP; a.nvt = z.nvt; a.nc = (int)z.nc; a.ne = (int)z.ne;
   a.status = (unsigned*)tape;
   a.wait_limit_ns = wait_limit_ns();
+  a.segs = z.segs; a.seglen = z.seglen;
   char* t = (char*)tape + 256;
   a.rec = (float*)t;
   a.tp = (bf16*)(t += z.rec);
+  a.Mt = (float*)(t += z.tri);
+  a.Ht = (float*)(t += z.M);
+  a.St = (float*)(t += z.H);
+  t += z.H;
   if (!keep) return a;
-  a.Sh = (bf16*)(t += z.tri);
+  a.Sh = (bf16*)t;
   a.Zh = (bf16*)(t += z.S);
   a.zf = (float*)(t += z.Z);
   a.of = (float*)(t += z.zf);
@@ -234,24 +247,24 @@ extern "C" {
 
 size_t rnn_delta_tape_size(const rnn_delta_dims_t* d, int keep) {
   DeltaSizes z;
-  return delta_sizes(d, &z) ? 256 + (keep ? z.tape : z.scratch) : 0;
+  return delta_sizes(d, keep != 0, &z) ? 256 + z.tape : 0;
 }
 
 size_t rnn_delta_bwd_workspace_size(const rnn_delta_dims_t* d) {
   DeltaSizes z;
-  return delta_sizes(d, &z) ? 256 + z.bwd : 0;
+  return delta_sizes(d, true, &z) ? 256 + z.bwd : 0;
 }
 
 int rnn_delta_fwd(const rnn_delta_dims_t* d, const void* q, const void* k, const void* v, const void* g,
                   const void* beta, const void* state0, const unsigned char* reset, const int* lengths, float scale,
                   void* o, void* last, int keep, void* tape, size_t tape_bytes, void* stream) {
   DeltaSizes z;
-  if (!delta_sizes(d, &z) || !tape || (d->T > 0 && (!q || !k || !v || !g || !beta || !o))) return RNN_EINVAL;
+  if (!delta_sizes(d, keep != 0, &z) || !tape || (d->T > 0 && (!q || !k || !v || !g || !beta || !o))) return RNN_EINVAL;
   const void* ptrs[] = {q, k, v, g, beta, state0, o, last, tape};
   for (const void* p : ptrs)
     if (p && !al16(p)) return RNN_EINVAL;
   if (!al4(lengths)) return RNN_EINVAL;
-  if (tape_bytes < 256 + (keep ? z.tape : z.scratch)) return RNN_ENOSPC;
+  if (tape_bytes < 256 + z.tape) return RNN_ENOSPC;
   cudaStream_t st = (cudaStream_t)stream;
   if (d->T == 0) {
     const size_t bytes = (size_t)d->B * d->N * d->Dk * d->Dv * sizeof(float);
@@ -278,7 +291,7 @@ int rnn_delta_bwd(const rnn_delta_dims_t* d, const void* q, const void* k, const
                   void* tape, size_t tape_bytes, const void* dO, const void* dlast, void* dq, void* dk, void* dv,
                   void* dg, void* dbeta, void* dstate0, void* workspace, size_t ws_bytes, void* stream) {
   DeltaSizes z;
-  if (!delta_sizes(d, &z)) return RNN_EINVAL;
+  if (!delta_sizes(d, true, &z)) return RNN_EINVAL;
   if (d->T > 0 && (!q || !k || !v || !tape || !dq || !dk || !dv || !dg || !dbeta || !workspace)) return RNN_EINVAL;
   const void* ptrs[] = {q, k, v, tape, dO, dlast, dq, dk, dv, dg, dbeta, dstate0, workspace};
   for (const void* p : ptrs)
@@ -308,6 +321,8 @@ int rnn_delta_bwd(const rnn_delta_dims_t* d, const void* q, const void* k, const
     a.dSh = (bf16*)w;
     a.dots = (float*)(w + z.S);
     a.edge = (float*)(w + z.S + z.dots);
+    a.Ht = (float*)(w + z.S + z.dots + z.edge);
+    a.St = (float*)(w + z.S + z.dots + z.edge + z.H);
     return cuda_status(delta_tc_bwd_launch(z.BV, a, st));
   }
   DeltaArgs a = delta_args(d, z, tape);

@@ -6,12 +6,37 @@
 
 namespace rnn {
 
-// Columns of v that one chain of chunks carries: 64 or, where half of the SMs
-// would be without a chain then, v has no more, or keys past 128 channels leave
-// no shared memory for it, 32. fp32: 32.
-inline int delta_bv(bool bf, int B, int N, int Dv, int KP, int sms) {
-  if (!bf || KP > 128 || Dv <= 32) return 32;
-  return (long long)B * N * ((Dv + 63) / 64) * 2 < sms ? 32 : 64;
+// How a bf16 problem's chains of chunks are laid over the GPU: tiles of BV columns
+// of v, and segments (delta_tc.cuh). A CTA an SM, so the time is the number of
+// rounds that the CTAs take times the chunks of a segment; segments cost the pass
+// of maps (the identity's tiles among them, forward) and the join. Microseconds a
+// chunk as measured: forward 4.3 (BV = 64) and 2.9 (32; 3.6 for keys past 128
+// channels), backward 5.9, 3.8 and 4.9; a join 2.6 a segment, 15 a further launch.
+struct DeltaLay {
+  int BV, segs, seglen;
+};
+inline DeltaLay delta_lay(long long heads, int Dv, int KP, long long nc, int sms, bool keep) {
+  DeltaLay best{32, 1, (int)(nc > 0 ? nc : 1)};
+  double least = 1e300;
+  for (int BV = 64; BV >= 32; BV -= 32) {
+    if (BV == 64 && (KP > 128 || Dv <= 32)) continue;
+    const double f = BV == 64 ? 4.3 : KP > 128 ? 3.6 : 2.9, w = keep ? (BV == 64 ? 5.9 : KP > 128 ? 4.9 : 3.8) : 0.0;
+    const long long nvt = (Dv + BV - 1) / BV, ki = (KP + BV - 1) / BV;
+    auto rounds = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
+    for (int segs = 1; segs <= 64; ++segs) {
+      const long long len = ((nc + segs - 1) / segs + 7) / 8 * 8;
+      if (segs > 1 && (len * (segs - 1) >= nc)) break;  // a segment would be empty
+      const double own = rounds(heads * segs * nvt) * (segs > 1 ? len : nc);
+      double cost = own * (f + w);
+      if (segs > 1)
+        cost += rounds(heads * segs * (nvt + ki)) * len * f + own * w + (2.6 * segs + 30.0) * (keep ? 2 : 1);
+      if (cost < least * 0.97) {
+        least = cost;
+        best = DeltaLay{BV, segs, (int)(segs > 1 ? len : (nc > 0 ? nc : 1))};
+      }
+    }
+  }
+  return best;
 }
 
 struct DeltaTcArgs;
@@ -19,5 +44,6 @@ cudaError_t delta_fwd_launch(const DeltaArgs& a, cudaStream_t st);  // fp32
 cudaError_t delta_bwd_launch(const DeltaArgs& a, cudaStream_t st);
 cudaError_t delta_tc_fwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st);  // bf16
 cudaError_t delta_tc_bwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st);
+cudaError_t delta_tc_join_back(int BV, const DeltaTcArgs& a, cudaStream_t st);
 
 }  // namespace rnn

@@ -45,6 +45,12 @@ constexpr int TC_PANEL = 16384; // bytes of a panel of 128 rows
 struct DeltaTcArgs {
   int B, T, Nk, N, Dk, Dv;
   int KP, nvt, nc, ne;  // Dk rounded to 16, tiles of BV columns of v, chunks, kept states a head
+  // The chunks in `segs` segments of `seglen` (a multiple of TC_EDGE), which run
+  // side by side once the states between them are known: the chain kernels first
+  // run with maps = 1, each segment from zeros (H) and, forward, from the identity
+  // (M), and S at a segment's end is M S + H (the gradient at its start M^T dS + H).
+  int segs, seglen, maps;
+  float *Mt, *Ht, *St;  // [B N][segs][KR][KR] M by columns, [B N][segs][nvt BV][KR] H and S at the start (backward: end), by columns
   const void *q, *k, *v;
   const float *g, *beta, *s0;
   const unsigned char* reset;
@@ -280,6 +286,23 @@ template <int N> __device__ __forceinline__ void store_row(bf16* p, const float 
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (c + e < valid) p[c + e] = __float2bfloat16_rn(x[c + e]);
+    }
+  }
+}
+
+// Rows from t0 to T of a tile's columns are zero; all threads of the CTA.
+template <int BV>
+__device__ __forceinline__ void tc_zero_tail(bf16* p, size_t stride, int t0, int T, int c0, int D) {
+  constexpr int P = BV / 8;
+  const int c = c0 + threadIdx.x % P * 8;
+  if (c >= D) return;
+  for (int t = t0 + threadIdx.x / P; t < T; t += blockDim.x / P) {
+    bf16* d = p + (size_t)t * stride + c;
+    if (D % 8 == 0) {
+      *(uint4*)d = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int e = 0; e < 8; ++e)
+        if (c + e < D) d[e] = __float2bfloat16_rn(0.0f);
     }
   }
 }

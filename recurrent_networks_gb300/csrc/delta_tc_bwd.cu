@@ -38,8 +38,11 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
   uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
   uint32_t* slot = (uint32_t*)(barp + 3);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
-  const int vt = blockIdx.x % a.nvt, bn = blockIdx.x / a.nvt, n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
-  const int nch = tc_chunks(a, b);
+  constexpr int KR = MT * 128;
+  const int vt = blockIdx.x % a.nvt, seg = blockIdx.x / a.nvt % a.segs, bn = blockIdx.x / a.nvt / a.segs;
+  const int n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
+  if (a.maps && seg == 0) return;  // nothing comes before it
+  const int nch = tc_chunks(a, b), ch0 = min(nch, seg * a.seglen), ch1 = min(nch, ch0 + a.seglen);
   const size_t vstride = (size_t)a.N * a.Dv, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
   const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16;
   if (tid == 0) {
@@ -60,9 +63,9 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
     if (warp == 8) {  // ---- products, bulk copies
       const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
       const bool one = lane == 0;
-      if (one && nch > 0) load_bulk(TP, tp + (size_t)(nch - 1) * L::TP, L::TP, bar_tp);
+      if (one && ch0 < ch1) load_bulk(TP, tp + (size_t)(ch1 - 1) * L::TP, L::TP, bar_tp);
       const uint64_t td = tc_desc(smem_u32(TP), TC_PANEL), gd = tc_desc<RB>(smem_u32(GS), L::GPLANE), od = tc_desc<RB>(smem_u32(OS), 16);
-      for (int ch = nch - 1; ch >= 0; --ch) {
+      for (int ch = ch1 - 1; ch >= ch0; --ch) {
         const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
         const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
         __syncthreads();  // 1
@@ -70,13 +73,14 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
           tm_fence_after();
           tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
           tc_commit(bar);
-          // the gradient of the chunk's last state, rounded: its first plane
-          store_bulk(a.dSh + tile * a.KP * BV, SS, a.KP * RB);
-          bulk_commit_group();
+          if (!a.maps) {  // the gradient of the chunk's last state, rounded: its first plane
+            store_bulk(a.dSh + tile * a.KP * BV, SS, a.KP * RB);
+            bulk_commit_group();
+          }
         }
         __syncthreads();  // 2
         if (one) {
-          wait(bar_tp, (nch - 1 - ch) & 1);
+          wait(bar_tp, (ch1 - 1 - ch) & 1);
           if (!failed) {
             tm_fence_after();
 #pragma unroll
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
               tc_mma(tm + D3 + 3 * mt * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 2048, TC_PANEL), gd + k * RB,
                      tc_idesc(3 * BV, true, true), k);
           tc_commit(bar);
-          if (ch > 0) load_bulk(TP, tp + (size_t)(ch - 1) * L::TP, L::TP, bar_tp);  // the second products have read it
+          if (ch > ch0) load_bulk(TP, tp + (size_t)(ch - 1) * L::TP, L::TP, bar_tp);  // the second products have read it
         }
         __syncthreads();  // 4
       }
@@ -135,17 +139,17 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
       auto store_dv = [&](int ch) {
         store_img<RB, 64>(t, VS, (bf16*)a.dv + vat + (size_t)ch * TC_C * vstride, vstride, min(TC_C, a.T - ch * TC_C), a.Dv, vt * BV);
       };
-      if (t >= 0 && nch > 0) {
-        load_kq(nch - 1);
-        load_o(nch - 1);
+      if (t >= 0 && ch0 < ch1) {
+        load_kq(ch1 - 1);
+        load_o(ch1 - 1);
         cp_wait_all();
         fence_proxy_async_smem();
       }
-      for (int ch = nch - 1; ch >= 0; --ch) {
-        const bool more = ch > 0 && t >= 0;
+      for (int ch = ch1 - 1; ch >= ch0; --ch) {
+        const bool more = ch > ch0 && t >= 0;
         __syncthreads();  // 1
-        if (t >= 0) {
-          if (ch + 1 < nch) store_dv(ch + 1);
+        if (t >= 0 && !a.maps) {
+          if (ch + 1 < ch1) store_dv(ch + 1);
           asm volatile("bar.sync 1, 64;" ::: "memory");  // the rows are read: V's may follow
           load_img<RB, BV / 8, 64>(t, VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv,
                                    vt * BV, BV, 0);
@@ -164,12 +168,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
           fence_proxy_async_smem();
         }
       }
-      if (t >= 0) {
-        if (nch > 0) store_dv(0);
-        const int t0 = nch * TC_C, cols = min(BV, a.Dv - vt * BV);
-        for (long long k = t; k < (long long)(a.T - t0) * cols; k += 64)
-          ((bf16*)a.dv)[vat + (size_t)(t0 + k / cols) * vstride + vt * BV + k % cols] = __float2bfloat16_rn(0.0f);
-      }
+      if (t >= 0 && ch0 < ch1 && !a.maps) store_dv(ch0);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -180,8 +179,10 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
     for (int mt = 0; mt < MT; ++mt) {
       const int r = mt * 128 + quad * 32 + lane;
       const float* s = a.dlast ? a.dlast + ((size_t)bn * a.Dk + r) * a.Dv + v0 : nullptr;
+      const float* st = seg < a.segs - 1 && !a.maps ? a.St + (((size_t)bn * a.segs + seg) * a.nvt * BV + v0) * KR + r : nullptr;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) S[mt][c] = s && r < a.Dk && c < valid ? s[c] : 0.0f;
+      for (int c = 0; c < NC; ++c)
+        S[mt][c] = st ? st[(size_t)c * KR] : s && !a.maps && r < a.Dk && c < valid ? s[c] : 0.0f;
     }
     auto put_state = [&]() {
 #pragma unroll
@@ -209,9 +210,9 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (lane == 0) a.edge[(((size_t)bn * a.ne + e) * a.nvt + vt) * 8 + warp] = s;
     };
-    if (nch > 0) {
+    if (ch0 < ch1) {
       put_state();
-      put_edge(0);
+      if (ch1 == nch && !a.maps) put_edge(0);
     }
     const int i = (quad & 1) * 32 + lane;  // this thread's step
     uint32_t parity = 0;
@@ -225,14 +226,14 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
       tm_fence_before();
       __syncthreads();
     };
-    for (int ch = nch - 1; ch >= 0; --ch) {
+    for (int ch = ch1 - 1; ch >= ch0; --ch) {
       const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
-      const bool more = ch > 0;
+      const bool more = ch > ch0;
       leave();  // 1: KQ, dO and dS's planes are there
       const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
       const float gi = gam[i], bi = br[i];
       float kept[NC];  // z (K's steps) or o (Q's), in fp32
-      {
+      if (!a.maps) {
         const float4* f = (const float4*)((quad < 2 ? a.zf : a.of) + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
@@ -245,12 +246,13 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
         float d[NC], s = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(OS + img<RB>(i, (c0 + c) >> 3)), d + c);
+        if (!a.maps)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) s = fmaf(d[c], kept[c], s);
+          for (int c = 0; c < NC; ++c) s = fmaf(d[c], kept[c], s);
 #pragma unroll
         for (int c = 0; c < NC; ++c) d[c] = gi != 0.0f ? f * d[c] : 0.0f;
         put_planes<RB, NC>(GS, L::GPLANE, 64 + i, c0, d);
-        a.dots[((tile * 3 + 2) * 2 + half) * TC_C + i] = i < tc_live(a, b, ch) ? s : 0.0f;
+        if (!a.maps) a.dots[((tile * 3 + 2) * 2 + half) * TC_C + i] = i < tc_live(a, b, ch) ? s : 0.0f;
       }
       take();
       if (quad < 2) {
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
         put_planes<RB, NC>(GS, L::GPLANE, i, c0, g);
       }
       leave();  // 3: -gam dY's planes are there, dO is read, V is there
-      if (quad < 2) {  // what leaves for memory goes while the product runs
+      if (quad < 2 && !a.maps) {  // what leaves for memory goes while the product runs
         float zy = 0.0f, vy = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; c += 8) {
@@ -298,12 +300,18 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
         for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
       }
       leave();  // 4: the products are over, dY's image is there
-      if (more) {
-        put_state();
-        if (ch % TC_EDGE == 0) put_edge(ch / TC_EDGE);
-      }
+      if (more) put_state();
+      if (ch > 0 && ch % TC_EDGE == 0 && !a.maps) put_edge(ch / TC_EDGE);
     }
-    if (a.ds0) {
+    if (a.maps) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 128 + quad * 32 + lane;
+        float* s = a.Ht + (((size_t)bn * a.segs + seg) * a.nvt * BV + v0) * KR + r;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) s[(size_t)c * KR] = r < a.KP ? S[mt][c] : 0.0f;
+      }
+    } else if (a.ds0 && seg == 0) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const int r = mt * 128 + quad * 32 + lane;
@@ -316,6 +324,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
       }
     }
   }
+  if (!a.maps && seg == a.segs - 1) tc_zero_tail<BV>((bf16*)a.dv + vat, vstride, nch * TC_C, a.T, vt * BV, a.Dv);
   tm_fence_before();
   __syncthreads();
   if (warp == 0) tm_free<512>(tm);
@@ -643,11 +652,20 @@ __global__ void __launch_bounds__(256) delta_tc_share_kernel(const float* pq, co
   }
 }
 
-template <int BV, int MT> cudaError_t back(const DeltaTcArgs& a, cudaStream_t st) {
+template <int BV, int MT> cudaError_t back(DeltaTcArgs a, cudaStream_t st) {
   constexpr int sm = TcBack<BV, MT>::BYTES;
   cudaError_t e = set_smem_attr((const void*)delta_tc_back_kernel<BV, MT>, sm);
   if (e != cudaSuccess) return e;
-  delta_tc_back_kernel<BV, MT><<<(unsigned)(a.B * a.N * a.nvt), 384, sm, st>>>(a);
+  const unsigned grid = (unsigned)(a.B * a.N * a.segs * a.nvt);
+  if (a.segs > 1) {
+    a.maps = 1;
+    delta_tc_back_kernel<BV, MT><<<grid, 384, sm, st>>>(a);
+    note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = delta_tc_join_back(BV, a, st)) != cudaSuccess) return e;
+    a.maps = 0;
+  }
+  delta_tc_back_kernel<BV, MT><<<grid, 384, sm, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }

@@ -232,8 +232,13 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
   uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
   uint32_t* slot = (uint32_t*)(barp + 3);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
-  const int vt = blockIdx.x % a.nvt, bn = blockIdx.x / a.nvt, n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
-  const int nch = tc_chunks(a, b);
+  constexpr int KR = MT * 128;
+  const int tiles = a.maps ? a.nvt + (a.KP + BV - 1) / BV : a.nvt;  // maps: and those of the identity
+  const int vt = blockIdx.x % tiles, seg = blockIdx.x / tiles % a.segs, bn = blockIdx.x / tiles / a.segs;
+  const int n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
+  const bool ident = vt >= a.nvt;
+  if (a.maps && seg == a.segs - 1 && !(ident && a.Sh)) return;  // nothing follows it; a backward wants its M
+  const int nch = tc_chunks(a, b), ch0 = min(nch, seg * a.seglen), ch1 = min(nch, ch0 + a.seglen);
   const size_t vstride = (size_t)a.N * a.Dv, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
   const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16;
   if (tid == 0) {
@@ -255,9 +260,9 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
     if (warp == 8) {  // ---- products, bulk copies
       const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
       const bool one = lane == 0;
-      if (one && nch > 0) load_bulk(TP, tp, L::TP, bar_tp);
+      if (one && ch0 < ch1) load_bulk(TP, tp + (size_t)ch0 * L::TP, L::TP, bar_tp);
       const uint64_t td = tc_desc(smem_u32(TP), 16), yd = tc_desc<RB>(smem_u32(YS), L::YPLANE);
-      for (int ch = 0; ch < nch; ++ch) {
+      for (int ch = ch0; ch < ch1; ++ch) {
         const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
         const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
         __syncthreads();  // 1
@@ -265,14 +270,14 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
           tm_fence_after();
           tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
           tc_commit(bar);
-          if (a.Sh) {  // the chunk's starting state, rounded: its first plane
+          if (a.Sh && !a.maps) {  // the chunk's starting state, rounded: its first plane
             store_bulk(a.Sh + tile * a.KP * BV, SS, a.KP * RB);
             bulk_commit_group();
           }
         }
         __syncthreads();  // 2
         if (one) {
-          wait(bar_tp, ch & 1);
+          wait(bar_tp, (ch - ch0) & 1);
           if (!failed) {
             tm_fence_after();
 #pragma unroll
@@ -294,10 +299,10 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
               tc_mma(tm + D3 + 3 * mt * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 2048, TC_PANEL), yd + k * RB,
                      tc_idesc(3 * BV, true, true), k);
           tc_commit(bar);
-          if (ch + 1 < nch) load_bulk(TP, tp + (size_t)(ch + 1) * L::TP, L::TP, bar_tp);  // the second products have read it
+          if (ch + 1 < ch1) load_bulk(TP, tp + (size_t)(ch + 1) * L::TP, L::TP, bar_tp);  // the second products have read it
         }
         __syncthreads();  // 4
-        if (one && a.Zh && !failed) {
+        if (one && a.Zh && !a.maps && !failed) {
           store_bulk(a.Zh + tile * 64 * BV, ZS, L::YPLANE);
           bulk_commit_group();
         }
@@ -324,8 +329,9 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
         load_img<128, P, 64>(t, d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
       };
       auto load_v = [&](int ch) {
-        load_img<RB, BV / 8, 64>(t, VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv,
-                                 vt * BV, BV, 0);
+        if (!ident)
+          load_img<RB, BV / 8, 64>(t, VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv,
+                                   vt * BV, BV, 0);
         const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
         float* d = recs + (ch & 1) * 2 * TC_C;
         if (t < 32) cp16(smem_u32(d + t * 4), r + (t < 16 ? REC_GAM * TC_C + t * 4 : REC_BR * TC_C + (t - 16) * 4), true);
@@ -333,17 +339,17 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
       auto store_o = [&](int ch) {
         store_img<RB, 64>(t, OS, (bf16*)a.o + vat + (size_t)ch * TC_C * vstride, vstride, min(TC_C, a.T - ch * TC_C), a.Dv, vt * BV);
       };
-      if (t >= 0 && nch > 0) {
-        load_kq(0);
-        load_v(0);
+      if (t >= 0 && ch0 < ch1) {
+        load_kq(ch0);
+        load_v(ch0);
         cp_wait_all();
         fence_proxy_async_smem();
       }
-      for (int ch = 0; ch < nch; ++ch) {
-        const bool more = ch + 1 < nch && t >= 0;
+      for (int ch = ch0; ch < ch1; ++ch) {
+        const bool more = ch + 1 < ch1 && t >= 0;
         __syncthreads();  // 1
         if (KST == 2 && more) load_kq(ch + 1);
-        if (t >= 0 && ch > 0) store_o(ch - 1);
+        if (t >= 0 && ch > ch0 && !a.maps) store_o(ch - 1);
         __syncthreads();  // 2
         if (more) load_v(ch + 1);
         __syncthreads();  // 3
@@ -354,13 +360,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
           fence_proxy_async_smem();
         }
       }
-      if (t >= 0) {
-        if (nch > 0) store_o(nch - 1);
-        // steps past the row's length
-        const int t0 = nch * TC_C, cols = min(BV, a.Dv - vt * BV);
-        for (long long k = t; k < (long long)(a.T - t0) * cols; k += 64)
-          ((bf16*)a.o)[vat + (size_t)(t0 + k / cols) * vstride + vt * BV + k % cols] = __float2bfloat16_rn(0.0f);
-      }
+      if (t >= 0 && ch0 < ch1 && !a.maps) store_o(ch1 - 1);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -372,8 +372,12 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
     for (int mt = 0; mt < MT; ++mt) {
       const int r = mt * 128 + quad * 32 + lane;
       const float* s = a.s0 ? a.s0 + ((size_t)bn * a.Dk + r) * a.Dv + v0 : nullptr;
+      const float* st = seg && !a.maps ? a.St + (((size_t)bn * a.segs + seg) * a.nvt * BV + v0) * KR + r : nullptr;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) S[mt][c] = s && r < a.Dk && c < valid ? s[c] : 0.0f;
+      for (int c = 0; c < NC; ++c)
+        S[mt][c] = ident ? (r == v0 - a.nvt * BV + c ? 1.0f : 0.0f)
+                   : st ? st[(size_t)c * KR]
+                        : s && !a.maps && r < a.Dk && c < valid ? s[c] : 0.0f;
     }
     auto put_state = [&]() {
 #pragma unroll
@@ -389,8 +393,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
         for (int c = 0; c < NC; c += 4) f[(c / 4) * 128] = make_float4(S[mt][c], S[mt][c + 1], S[mt][c + 2], S[mt][c + 3]);
       }
     };
-    if (nch > 0) put_state();
-    else if (a.sf) keep_state(0);
+    if (ch0 < ch1) put_state();
+    else if (nch == 0 && seg == 0 && a.sf && !a.maps) keep_state(0);
     const int i = (quad & 1) * 32 + lane;  // this thread's step
     uint32_t parity = 0;
     auto take = [&]() {
@@ -403,14 +407,17 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
       tm_fence_before();
       __syncthreads();
     };
-    for (int ch = 0; ch < nch; ++ch) {
+    for (int ch = ch0; ch < ch1; ++ch) {
       const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
-      const bool more = ch + 1 < nch;
+      const bool more = ch + 1 < ch1;
       leave();  // 1: KQ, V and S's planes are there
       const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
       const float gi = gam[i];
       float y[NC];
-      if (quad < 2)
+      if (ident)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) y[c] = 0.0f;
+      else if (quad < 2)
 #pragma unroll
         for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(VS + img<RB>(i, (c0 + c) >> 3)), y + c);
       take();
@@ -439,7 +446,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
       }
       leave();  // 3: beta rho Z's planes are there
       // what leaves for memory goes while the product runs
-      if (quad < 2) {
+      if (a.maps) {
+      } else if (quad < 2) {
         if (a.Zh) {
           float4* f = (float4*)(a.zf + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
 #pragma unroll
@@ -469,10 +477,20 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
       }
       leave();  // 4: the products are over, Z's image is there
       if (more) put_state();
-      const int end = !more ? 0 : (ch + 1) % TC_EDGE == 0 ? (ch + 1) / TC_EDGE : -1;
-      if (a.sf && end >= 0) keep_state(end);
+      const int end = ch + 1 == nch ? 0 : (ch + 1) % TC_EDGE == 0 ? (ch + 1) / TC_EDGE : -1;
+      if (a.sf && !a.maps && end >= 0) keep_state(end);
     }
-    if (a.last) {
+    if (a.maps) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 128 + quad * 32 + lane, j = v0 - a.nvt * BV;
+        float* s = ident ? a.Mt + (((size_t)bn * a.segs + seg) * KR + j) * KR + r
+                         : a.Ht + (((size_t)bn * a.segs + seg) * a.nvt * BV + v0) * KR + r;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (!ident || j + c < KR) s[(size_t)c * KR] = r < a.KP ? S[mt][c] : 0.0f;
+      }
+    } else if (a.last && seg == a.segs - 1) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const int r = mt * 128 + quad * 32 + lane;
@@ -485,21 +503,135 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
       }
     }
   }
+  // steps past the row's length
+  if (!a.maps && seg == a.segs - 1) tc_zero_tail<BV>((bf16*)a.o + vat, vstride, nch * TC_C, a.T, vt * BV, a.Dv);
   tm_fence_before();
   __syncthreads();
   if (warp == 0) tm_free<512>(tm);
 }
 
-template <int BV, int MT> cudaError_t chain(const DeltaTcArgs& a, cudaStream_t st) {
+// ---- join ----------------------------------------------------------------------------
+// The states between the segments, one after the other: forward S = M S + H from
+// state0, backward dS = M^T dS + H from dlast. A CTA has CW columns of v of a head,
+// S in shared memory, M by blocks of 64 KB, two of them; 4 x 4 values a thread.
+// Rows and columns of M past KP are not looked at.
+template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_join_kernel(DeltaTcArgs a, int cols_total) {
+  constexpr int CW = KR == 128 ? 32 : 16, LD = CW + 4, JB = 16384 / KR;  // rows of Mt in a block
+  extern __shared__ __align__(16) unsigned char sm_raw[];
+  float* M = (float*)sm_raw;  // [2][JB][KR]
+  float* S = M + 2 * JB * KR; // [KR][LD]
+  const int groups = cols_total / CW;
+  const int tid = threadIdx.x, bn = blockIdx.x / groups, v0 = (blockIdx.x % groups) * CW;
+  const int cg = tid % (CW / 4) * 4, rg = tid / (CW / 4) * 4;
+  const float* x0 = BACK ? a.dlast : a.s0;
+  for (int k = tid; k < KR * CW; k += 256) {
+    const int r = k / CW, c = k % CW;
+    S[r * LD + c] = x0 && r < a.Dk && v0 + c < a.Dv ? x0[((size_t)bn * a.Dk + r) * a.Dv + v0 + c] : 0.0f;
+  }
+  const int blocks = (a.segs - 1) * (KR / JB);
+  auto load = [&](int k) {  // block k of the matrices in the order of their use
+    const int s = BACK ? a.segs - 1 - k / (KR / JB) : k / (KR / JB);
+    const float* m = a.Mt + (((size_t)bn * a.segs + s) * KR + (k % (KR / JB)) * JB) * KR;
+    const uint32_t to = smem_u32(M + (k & 1) * JB * KR);
+    for (int i = tid; i < JB * KR / 4; i += 256) cp16(to + i * 16, m + i * 4, true);
+    cp_commit();
+  };
+  load(0);
+  float acc[4][4];
+  for (int k = 0; k < blocks; ++k) {
+    const int s = BACK ? a.segs - 1 - k / (KR / JB) : k / (KR / JB), part = k % (KR / JB);
+    if (k + 1 < blocks) load(k + 1);
+    else cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    if (part == 0)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = 0.0f;
+    const float* m = M + (k & 1) * JB * KR;
+    if constexpr (!BACK) {  // column j of M times row j of S
+#pragma unroll 4
+      for (int j = 0; j < min(JB, a.KP - part * JB); ++j) {
+        const float4 x = *(const float4*)(m + j * KR + rg), y = *(const float4*)(S + (part * JB + j) * LD + cg);
+        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(xs[r], ys[c], acc[r][c]);
+      }
+    } else if (rg >= part * JB && rg < (part + 1) * JB) {  // this thread's columns of M, summed over its rows
+#pragma unroll 2
+      for (int j = 0; j < a.KP; j += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = *(const float4*)(m + (rg - part * JB + r) * KR + j);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 y = *(const float4*)(S + (j + q) * LD + cg);
+          const float ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float xr = q == 0 ? x[r].x : q == 1 ? x[r].y : q == 2 ? x[r].z : x[r].w;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(xr, ys[c], acc[r][c]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (part == KR / JB - 1) {
+      const size_t from = (((size_t)bn * a.segs + s) * cols_total + v0 + cg) * KR + rg;
+      const size_t to = (((size_t)bn * a.segs + (BACK ? s - 1 : s + 1)) * cols_total + v0 + cg) * KR + rg;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 h = *(const float4*)(a.Ht + from + (size_t)c * KR);
+        const float4 x = make_float4(acc[0][c] + h.x, acc[1][c] + h.y, acc[2][c] + h.z, acc[3][c] + h.w);
+        *(float4*)(a.St + to + (size_t)c * KR) = x;
+        S[rg * LD + cg + c] = x.x;
+        S[(rg + 1) * LD + cg + c] = x.y;
+        S[(rg + 2) * LD + cg + c] = x.z;
+        S[(rg + 3) * LD + cg + c] = x.w;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <int KR, bool BACK> cudaError_t join_run(const DeltaTcArgs& a, int BV, cudaStream_t st) {
+  constexpr int CW = KR == 128 ? 32 : 16;
+  constexpr size_t sm = 2 * 65536 + (size_t)KR * (CW + 4) * 4;
+  cudaError_t e = set_smem_attr((const void*)delta_tc_join_kernel<KR, BACK>, sm);
+  if (e != cudaSuccess) return e;
+  const int cols = a.nvt * BV;
+  delta_tc_join_kernel<KR, BACK><<<(unsigned)(a.B * a.N * (cols / CW)), 256, sm, st>>>(a, cols);
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <int BV, int MT> cudaError_t chain(DeltaTcArgs a, cudaStream_t st) {
   constexpr int sm = TcChain<BV, MT>::BYTES;
   cudaError_t e = set_smem_attr((const void*)delta_tc_chain_kernel<BV, MT>, sm);
   if (e != cudaSuccess) return e;
-  delta_tc_chain_kernel<BV, MT><<<(unsigned)(a.B * a.N * a.nvt), 384, sm, st>>>(a);
+  const unsigned lanes = (unsigned)(a.B * a.N * a.segs);
+  if (a.segs > 1) {
+    a.maps = 1;
+    delta_tc_chain_kernel<BV, MT><<<lanes * (a.nvt + (a.KP + BV - 1) / BV), 384, sm, st>>>(a);
+    note_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = join_run<MT * 128, false>(a, BV, st)) != cudaSuccess) return e;
+    a.maps = 0;
+  }
+  delta_tc_chain_kernel<BV, MT><<<lanes * a.nvt, 384, sm, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t delta_tc_join_back(int BV, const DeltaTcArgs& a, cudaStream_t st) {
+  return a.KP > 128 ? join_run<256, true>(a, BV, st) : join_run<128, true>(a, BV, st);
+}
 
 cudaError_t delta_tc_fwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st) {
   const size_t sm = prep_smem(a.KP);

@@ -157,3 +157,16 @@ def test_step(dtype):
         close(o, ref_o, "o", 1, dtype if dtype == BF else F32)
         close(out, ref_pool, "pool", 1, F32)
         assert torch.equal(rn.gated_delta_step(*args, pool, slots.cuda()), o) and torch.equal(pool, out)
+
+
+# few heads and a long axis: the chunks run in segments whose states are joined
+# (keys up to 128 channels, and past them), with shorter rows among them
+@pytest.mark.parametrize("shape", [(1, 3001, 1, 1, 64, 96), (2, 2500, 1, 2, 144, 40), (1, 2070, 1, 2, 16, 8)],
+                         ids=lambda s: "B%dT%dNk%dN%dDk%dDv%d" % s)
+def test_segments(shape):
+    p = make(*shape, BF, seed=5)
+    check(p)
+    B, T = shape[:2]
+    lengths = torch.tensor([T // 2 + 3, 70][:B], dtype=torch.int32).cuda()
+    reset = (torch.rand(B, T, generator=torch.Generator().manual_seed(1)) < 0.002).cuda()
+    check(p, reset, lengths)
