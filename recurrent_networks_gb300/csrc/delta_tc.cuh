@@ -56,6 +56,7 @@ struct DeltaTcArgs {
   const unsigned char* reset;
   const int* lengths;
   float scale;
+  bool tma;
   void* o;
   float* last;
   unsigned* status;
@@ -75,6 +76,13 @@ struct DeltaTcArgs {
   void *dq, *dk, *dv;
   float *dg, *dbeta, *ds0;
   float *pq, *pk;
+};
+
+// Tensor maps of the rows' tensors [B, T, heads, D] where their rows are whole
+// 16-byte pieces (a.tma), boxes of 64 steps of a head: k and q by 64 columns, the
+// others by a tile's.
+struct TcMaps {
+  CUtensorMap k, q, v, o, dO, dv;
 };
 
 // ---- tensor memory -----------------------------------------------------------------
@@ -290,6 +298,10 @@ template <int N> __device__ __forceinline__ void store_row(bf16* p, const float 
   }
 }
 
+// Rows `live` .. 63 of an image (from row0 on) are zero; one warp.
+template <int RB> __device__ __forceinline__ void clear_rows(unsigned char* im, int row0, int live) {
+  for (int i = (threadIdx.x & 31) * 16; i < (64 - live) * RB; i += 512) *(uint4*)(im + (row0 + live) * RB + i) = make_uint4(0, 0, 0, 0);
+}
 // Rows from t0 to T of a tile's columns are zero; all threads of the CTA.
 template <int BV>
 __device__ __forceinline__ void tc_zero_tail(bf16* p, size_t stride, int t0, int T, int c0, int D) {
@@ -318,5 +330,8 @@ __device__ __forceinline__ int tc_chunks(const DeltaTcArgs& a, int b) {
   if (a.lengths) len = max(0, min(a.T, __ldg(a.lengths + b)));
   return (len + TC_C - 1) / TC_C;
 }
+
+// A tensor's map (host).
+cudaError_t tc_map(CUtensorMap* m, const void* base, const DeltaTcArgs& a, int heads, int D, int cols);
 
 }  // namespace rnn

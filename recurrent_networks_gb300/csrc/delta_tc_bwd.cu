@@ -27,7 +27,7 @@ template <int BV, int MT> struct TcBack {
 // accumulator come from whatever lies a panel further (inside this CTA's shared
 // memory) and are not looked at.
 template <int BV, int MT>
-__global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
+__global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, const __grid_constant__ TcMaps maps) {
   using L = TcBack<BV, MT>;
   constexpr int RB = L::RB, NC = BV / 2, KST = L::KST, P = MT * 16;
   static_assert(3 * L::SPLANE >= TC_PANEL, "what TP's last plane is read past");
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
   unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *GS = sm + L::AT_G, *OS = sm + L::AT_O, *VS = sm + L::AT_V;
   float* recs = (float*)(sm + L::AT_REC);  // [2][gam, br][64]
   uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
-  uint32_t* slot = (uint32_t*)(barp + 3);
+  uint32_t* slot = (uint32_t*)(barp + 5);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
   constexpr int KR = MT * 128;
   const int vt = blockIdx.x % a.nvt, seg = blockIdx.x / a.nvt % a.segs, bn = blockIdx.x / a.nvt / a.segs;
@@ -44,9 +44,9 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
   if (a.maps && seg == 0) return;  // nothing comes before it
   const int nch = tc_chunks(a, b), ch0 = min(nch, seg * a.seglen), ch1 = min(nch, ch0 + a.seglen);
   const size_t vstride = (size_t)a.N * a.Dv, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
-  const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16;
+  const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16, bar_in = bar + 24, bar_v = bar + 32;
   if (tid == 0) {
-    for (int k = 0; k < 3; ++k) mbar_init(bar + 8 * k, 1);
+    for (int k = 0; k < 5; ++k) mbar_init(bar + 8 * k, 1);
     fence_mbar_init_cluster();
   }
   if (warp == 0) tm_alloc<512>(slot);
@@ -63,20 +63,72 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
     if (warp == 8) {  // ---- products, bulk copies
       const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
       const bool one = lane == 0;
-      if (one && ch0 < ch1) load_bulk(TP, tp + (size_t)(ch1 - 1) * L::TP, L::TP, bar_tp);
+      // K, Q, dO and the steps' factors of a chunk, counted by bar_in; V by bar_v
+      const int panels = (a.KP + 63) >> 6;
+      const uint32_t bytes = panels * 16384 + (a.dO ? 64 * RB : 0) + 512;
+      auto load_kq = [&](int ch) {
+        unsigned char* d = sm + (ch % KST) * L::KQ;
+        if (KST == 2) mbar_arrive_expect_tx(bar_in, bytes);
+        for (int p = 0; p < panels; ++p) {
+          tma_load_5d(smem_u32(d + p * TC_PANEL), &maps.k, bar_in, p * 64, nk, ch * TC_C, b, 0);
+          tma_load_5d(smem_u32(d + p * TC_PANEL + 8192), &maps.q, bar_in, p * 64, nk, ch * TC_C, b, 0);
+        }
+      };
+      auto load_o = [&](int ch) {
+        if (KST == 1) mbar_arrive_expect_tx(bar_in, bytes);
+        if (a.dO) tma_load_5d(smem_u32(OS), &maps.dO, bar_in, vt * BV, n, ch * TC_C, b, 0);
+        const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
+        const uint32_t d = smem_u32(recs + (ch & 1) * 2 * TC_C);
+        bulk_load_global(d, r + REC_GAM * TC_C, 256, bar_in);
+        bulk_load_global(d + 256, r + REC_BR * TC_C, 256, bar_in);
+      };
+      if (a.tma && !a.dO) {
+        clear_rows<RB>(OS, 0, 0);
+        fence_proxy_async_smem();
+      }
+      if (one && ch0 < ch1) {
+        load_bulk(TP, tp + (size_t)(ch1 - 1) * L::TP, L::TP, bar_tp);
+        if (a.tma) {
+          if (KST == 2) load_kq(ch1 - 1);
+          load_o(ch1 - 1);
+          if (KST == 1) load_kq(ch1 - 1);
+        }
+      }
       const uint64_t td = tc_desc(smem_u32(TP), TC_PANEL), gd = tc_desc<RB>(smem_u32(GS), L::GPLANE), od = tc_desc<RB>(smem_u32(OS), 16);
       for (int ch = ch1 - 1; ch >= ch0; --ch) {
-        const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
+        unsigned char* kqs = sm + (ch % KST) * L::KQ;
+        const uint32_t kq = smem_u32(kqs);
         const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
+        const int live = tc_live(a, b, ch);
+        const bool cut = a.tma && live < TC_C && ch * TC_C + live < a.T;  // steps of the tensor past the row's length
+        if (a.tma) {
+          wait(bar_in, (ch1 - 1 - ch) & 1);
+          if (cut) {
+            for (int p = 0; p < panels; ++p) {
+              clear_rows<128>(kqs + p * TC_PANEL, 0, live);
+              clear_rows<128>(kqs + p * TC_PANEL, 64, live);
+            }
+            clear_rows<RB>(OS, 0, live);
+            fence_proxy_async_smem();
+          }
+        }
         __syncthreads();  // 1
         if (one && !failed) {
           tm_fence_after();
           tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
           tc_commit(bar);
-          if (!a.maps) {  // the gradient of the chunk's last state, rounded: its first plane
+          if (KST == 2 && a.tma && ch > ch0) load_kq(ch - 1);
+          if (!a.maps) {
+            // the gradient of the chunk's last state, rounded: its first plane
             store_bulk(a.dSh + tile * a.KP * BV, SS, a.KP * RB);
             bulk_commit_group();
+            if (a.tma) {
+              bulk_wait_group_read<1>();  // dY has left V's image
+              mbar_arrive_expect_tx(bar_v, 64 * RB);
+              tma_load_5d(smem_u32(VS), &maps.v, bar_v, vt * BV, n, ch * TC_C, b, 0);
+            }
           }
+          bulk_wait_group_read<0>();  // the state's planes may be written again
         }
         __syncthreads();  // 2
         if (one) {
@@ -92,7 +144,11 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
               }
             tc_commit(bar);
           }
-          bulk_wait_group_read<0>();  // the state's planes may be written again
+        }
+        __syncwarp();
+        if (a.tma && !a.maps) {
+          wait(bar_v, (ch1 - 1 - ch) & 1);
+          if (cut) clear_rows<RB>(VS, 0, live);
         }
         __syncthreads();  // 3
         if (one && !failed) {
@@ -104,23 +160,33 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a) {
               tc_mma(tm + D3 + 3 * mt * BV, tc_desc(kq + 2 * mt * TC_PANEL + k * 2048, TC_PANEL), gd + k * RB,
                      tc_idesc(3 * BV, true, true), k);
           tc_commit(bar);
-          if (ch > ch0) load_bulk(TP, tp + (size_t)(ch - 1) * L::TP, L::TP, bar_tp);  // the second products have read it
+          if (ch > ch0) {
+            load_bulk(TP, tp + (size_t)(ch - 1) * L::TP, L::TP, bar_tp);  // the second products have read it
+            if (a.tma) load_o(ch - 1);
+          }
         }
         __syncthreads();  // 4
+        if (one && !failed && a.tma) {
+          if (KST == 1 && ch > ch0) load_kq(ch - 1);
+          if (!a.maps) {
+            tma_store_5d(&maps.dv, smem_u32(VS), vt * BV, n, ch * TC_C, b, 0);
+            bulk_commit_group();
+          }
+        }
       }
       if (one) {
         bulk_wait_group_all();
         bool f = false;
         tc_commit(bar_end);
         mbar_wait_bounded<false>(bar_end, 0, a.wait_limit_ns, nullptr, f);
-        if (failed)  // a copy of TP that nobody waited for lands before the CTA ends
-          for (int p = 0; p < 2; ++p) {
+        if (failed)  // copies that nobody waited for land before the CTA ends
+          for (int p = 0; p < 6; ++p) {
             f = false;
-            mbar_wait_bounded<false>(bar_tp, p, a.wait_limit_ns, nullptr, f);
+            mbar_wait_bounded<false>(bar_tp + 8 * (p >> 1), p & 1, a.wait_limit_ns, nullptr, f);
           }
       }
-    } else {  // ---- rows
-      const int t = tid - 320;  // warps 10 and 11
+    } else {  // ---- rows that TMA cannot take
+      const int t = a.tma ? -1 : tid - 320;  // warps 10 and 11
       const size_t kstride = (size_t)a.Nk * a.Dk, kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk;
       auto load_kq = [&](int ch) {
         unsigned char* d = sm + (ch % KST) * L::KQ;
@@ -408,6 +474,11 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     rec[4 * TC_C + tid] = r[REC_BR * TC_C];
     rec[5 * TC_C + tid] = r[REC_BETA * TC_C];
   }
+  {  // K and Q, which come last, on their way to the L2
+    const bf16* s = (const bf16*)(tid < 128 ? a.k : a.q) + kat + (size_t)((tid & 127) >> 1) * kstride;
+    if ((tid & 127) >> 1 < live)
+      for (int c = (tid & 1) * 64; c < a.Dk; c += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(s + c));
+  }
   if (warp == 0) tm_alloc<L::COLS>(slot);
   cp_wait_all();
   fence_proxy_async_smem();
@@ -472,7 +543,7 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     for (int c = 0; c < 32; ++c) {
       const int j = j0 + c;
       const bool on = (quad < 2 ? i > j : i >= j) && si == __float_as_int(rec[2 * TC_C + j]);
-      nf[c] = on ? (quad < 2 ? -nf[c] : a.scale * nf[c]) * __expf((ci - rec[j]) + (li - rec[TC_C + j])) * beta[j] : 0.0f;
+      nf[c] = on ? (quad < 2 ? -nf[c] : a.scale * nf[c]) * exp2_fast((ci - rec[j]) + (li - rec[TC_C + j])) * beta[j] : 0.0f;
     }
   }
   if (tid == 0)
@@ -652,20 +723,20 @@ __global__ void __launch_bounds__(256) delta_tc_share_kernel(const float* pq, co
   }
 }
 
-template <int BV, int MT> cudaError_t back(DeltaTcArgs a, cudaStream_t st) {
+template <int BV, int MT> cudaError_t back(DeltaTcArgs a, const TcMaps& maps, cudaStream_t st) {
   constexpr int sm = TcBack<BV, MT>::BYTES;
   cudaError_t e = set_smem_attr((const void*)delta_tc_back_kernel<BV, MT>, sm);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(a.B * a.N * a.segs * a.nvt);
   if (a.segs > 1) {
     a.maps = 1;
-    delta_tc_back_kernel<BV, MT><<<grid, 384, sm, st>>>(a);
+    delta_tc_back_kernel<BV, MT><<<grid, 384, sm, st>>>(a, maps);
     note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = delta_tc_join_back(BV, a, st)) != cudaSuccess) return e;
     a.maps = 0;
   }
-  delta_tc_back_kernel<BV, MT><<<grid, 384, sm, st>>>(a);
+  delta_tc_back_kernel<BV, MT><<<grid, 384, sm, st>>>(a, maps);
   note_launch();
   return cudaGetLastError();
 }
@@ -681,7 +752,15 @@ template <int KT, int BV> cudaError_t grad(const DeltaTcArgs& a, cudaStream_t st
 }  // namespace
 
 cudaError_t delta_tc_bwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st) {
-  cudaError_t e = a.KP > 128 ? back<32, 2>(a, st) : BV == 64 ? back<64, 1>(a, st) : back<32, 1>(a, st);
+  TcMaps maps;
+  DeltaTcArgs x = a;
+  cudaError_t e;
+  x.tma = a.Dk % 8 == 0 && a.Dv % 8 == 0;
+  if (x.tma && ((e = tc_map(&maps.k, a.k, a, a.Nk, a.Dk, 64)) != cudaSuccess || (e = tc_map(&maps.q, a.q, a, a.Nk, a.Dk, 64)) != cudaSuccess ||
+                (e = tc_map(&maps.v, a.v, a, a.N, a.Dv, BV)) != cudaSuccess || (e = tc_map(&maps.dv, a.dv, a, a.N, a.Dv, BV)) != cudaSuccess ||
+                (a.dO && (e = tc_map(&maps.dO, a.dO, a, a.N, a.Dv, BV)) != cudaSuccess)))
+    return e;
+  e = a.KP > 128 ? back<32, 2>(x, maps, st) : BV == 64 ? back<64, 1>(x, maps, st) : back<32, 1>(x, maps, st);
   if (e != cudaSuccess) return e;
   if ((e = a.KP > 128 ? grad<256, 32>(a, st) : BV == 64 ? grad<128, 64>(a, st) : grad<128, 32>(a, st)) != cudaSuccess) return e;
   const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE;

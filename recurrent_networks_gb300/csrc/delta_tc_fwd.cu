@@ -10,26 +10,41 @@ namespace {
 
 // ---- prep --------------------------------------------------------------------------
 constexpr int PREP_LD = TC_C + 4;
-__host__ __device__ constexpr size_t prep_smem(int KP) {
-  const size_t kq = (size_t)2 * TC_C * (KP + 8) * 2, tf = (size_t)2 * TC_C * PREP_LD * 4;  // K and Q; then Tm and PT
-  return (kq > tf ? kq : tf) + tf + REC_N * TC_C * 4;
+// K and Q, then L (and PT in its place) and P; beside them Tm and the steps' factors
+__host__ __device__ constexpr size_t prep_kq(int KP) {
+  const size_t kq = (size_t)2 * TC_C * (KP + 8) * 2, lp = (size_t)2 * TC_C * PREP_LD * 4;
+  return kq > lp ? kq : lp;
+}
+__host__ __device__ constexpr size_t prep_smem(int KP) { return prep_kq(KP) + (size_t)TC_C * PREP_LD * 4 + REC_N * TC_C * 4; }
+
+// start + the dot product of N (a multiple of 4) values in shared memory and in
+// registers, by packed pairs
+template <int N> __device__ __forceinline__ float dot_pairs(const float* p, const float* x, float start) {
+  FV<2> s[2] = {{{start, 0.0f}}, {{0.0f, 0.0f}}};
+#pragma unroll
+  for (int k = 0; k < N; k += 4) {
+    const float4 l = *(const float4*)(p + k);
+    s[0] = fma(FV<2>{{l.x, l.y}}, FV<2>{{x[k], x[k + 1]}}, s[0]);
+    s[1] = fma(FV<2>{{l.z, l.w}}, FV<2>{{x[k + 2], x[k + 3]}}, s[1]);
+  }
+  return (s[0].v[0] + s[1].v[0]) + (s[0].v[1] + s[1].v[1]);
 }
 
-// K K^T and Q K^T by mma.sync, 16 rows a warp; the rest in fp32 on the plain
-// cores. Tm: its two diagonal blocks of 32 by forward substitution, a column to a
-// thread, then T21 = -T22 (L21 T11); PT a column and every other row to a thread.
-// Bound by instructions: about 2500 a warp.
-__global__ void __launch_bounds__(128) delta_tc_prep_kernel(DeltaTcArgs a) {
+// K K^T and Q K^T by mma.sync, 16 rows a warp and the columns up to its last row;
+// the rest in fp32 on the plain cores. Tm: its two diagonal blocks of 32 by forward
+// substitution, a column to a thread, then T21 = -T22 (L21 T11); PT a column and
+// every other row to a thread. Bound by instructions, about 3500 a warp; four CTAs
+// an SM (Dk <= 128).
+__global__ void __launch_bounds__(128, 4) delta_tc_prep_kernel(DeltaTcArgs a) {
   constexpr int C = TC_C, NT = C / 8, LD = PREP_LD, H = C / 2;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   const int LDK = a.KP + 8, kplane = C * LDK;
-  const size_t kq = (size_t)2 * kplane * 2, tf = (size_t)2 * C * LD * 4;
   bf16* Ks = (bf16*)sm_raw;
   bf16* Qs = Ks + kplane;
-  float* Tf = (float*)sm_raw;  // [2 C][LD]: Tm, then PT, over K and Q
-  float* Lf = (float*)(sm_raw + (kq > tf ? kq : tf));  // [C][LD]; L21's place takes L21 T11
-  float* Pf = Lf + C * LD;                             // [C][LD]
-  float* rec = Pf + C * LD;                            // [REC_N][C]
+  float* Lf = (float*)sm_raw;  // [C][LD]; L21's place takes L21 T11, then all of it PT
+  float* Pf = Lf + C * LD;     // [C][LD]
+  float* Tf = (float*)(sm_raw + prep_kq(a.KP));  // [C][LD]
+  float* rec = Tf + C * LD;                      // [REC_N][C]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long item = blockIdx.x;
   if (item == 0 && tid == 0) *a.status = 0;  // the kernels behind this one report there
@@ -41,10 +56,10 @@ __global__ void __launch_bounds__(128) delta_tc_prep_kernel(DeltaTcArgs a) {
   load_rows<bf16, C>(Ks, LDK, kplane, (const bf16*)a.k + at, stride, live, a.Dk, 0, a.KP);
   load_rows<bf16, C>(Qs, LDK, kplane, (const bf16*)a.q + at, stride, live, a.Dk, 0, a.KP);
   cp_commit();
-  if (warp == 0) {  // the running sum of g, in 64 bits, and the documents
+  if (warp == 0) {  // the running sum of g (to the base 2), in 64 bits, and the documents
     double run = 0.0, cs[2];
     int seg = 0, sg[2];
-    float chi[2], clo[2], be[2];
+    float be[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = h * 32 + lane;
@@ -60,7 +75,7 @@ __global__ void __launch_bounds__(128) delta_tc_prep_kernel(DeltaTcArgs a) {
         if (g < -104.0f) mark = true;  // exp(g) is 0
         if (mark) g = 0.0f;
       }
-      double c = (double)g;
+      double c = (double)g * 1.4426950408889634;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double v = __shfl_up_sync(0xffffffffu, c, o);
@@ -72,64 +87,89 @@ __global__ void __launch_bounds__(128) delta_tc_prep_kernel(DeltaTcArgs a) {
       sg[h] = seg + __popc(m & (0xffffffffu >> (31 - lane)));
       seg += __popc(m);
       cs[h] = c;
-      chi[h] = (float)c;
-      clo[h] = (float)(c - (double)chi[h]);
+      const float chi = (float)c;
+      rec[REC_CHI * C + i] = chi;
+      rec[REC_CLO * C + i] = (float)(c - (double)chi);
+      rec[REC_SEG * C + i] = __int_as_float(sg[h]);
+      rec[REC_GAM * C + i] = sg[h] == 0 ? exp2f((float)c) : 0.0f;
+      rec[REC_BETA * C + i] = be[h];
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = h * 32 + lane;
-      const float rho = sg[h] == seg ? expf((float)(run - cs[h])) : 0.0f;
-      rec[REC_CHI * C + i] = chi[h];
-      rec[REC_CLO * C + i] = clo[h];
-      rec[REC_SEG * C + i] = __int_as_float(sg[h]);
-      rec[REC_GAM * C + i] = sg[h] == 0 ? expf((float)cs[h]) : 0.0f;
+      const float rho = sg[h] == seg ? exp2f((float)(run - cs[h])) : 0.0f;
       rec[REC_RHO * C + i] = rho;
-      rec[REC_BETA * C + i] = be[h];
       rec[REC_BR * C + i] = be[h] * rho;
     }
   }
   cp_wait<0>();
   __syncthreads();
   for (int i = tid; i < REC_N * C; i += 128) a.rec[(size_t)item * REC_N * C + i] = rec[i];
-  const Opnd K = opnd(Ks, LDK, kplane), Q = opnd(Qs, LDK, kplane);
   const int m0 = warp * 16;
   float kk[NT][4], qk[NT][4];
   zero(kk);
   zero(qk);
-  mma_acc<NT, 1, 1, false, true>(kk, K, m0, K, 0, a.KP);
-  mma_acc<NT, 1, 1, false, true>(qk, Q, m0, K, 0, a.KP);
+  {
+    const int id = lane >> 3, r = lane & 7;
+    uint32_t ka = smem_u32(Ks) + 2u * ((m0 + (id & 1) * 8 + r) * LDK + (id >> 1) * 8), qa = ka + 2u * kplane;
+    uint32_t kb = smem_u32(Ks) + 2u * (((id >> 1) * 8 + r) * LDK + (id & 1) * 8);
+#pragma unroll 2
+    for (int k = 0; k < a.KP; k += 16, ka += 32, qa += 32, kb += 32) {
+      uint32_t x[4], y[4];
+      ldsm4<false>(ka, x);
+      ldsm4<false>(qa, y);
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j) {
+        if (j > warp) continue;
+        uint32_t w[4];
+        ldsm4<false>(kb + j * 32 * LDK, w);
+        mma_bf16_16816(kk[2 * j], x, w[0], w[1]);
+        mma_bf16_16816(kk[2 * j + 1], x, w[2], w[3]);
+        mma_bf16_16816(qk[2 * j], y, w[0], w[1]);
+        mma_bf16_16816(qk[2 * j + 1], y, w[2], w[3]);
+      }
+    }
+  }
+  __syncthreads();  // K and Q are read
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int i = m0 + (lane >> 2) + 8 * h;
     const float ci = rec[REC_CHI * C + i], li = rec[REC_CLO * C + i];
     const int si = __float_as_int(rec[REC_SEG * C + i]);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
+      if (t > 2 * warp + 1) continue;
+      float p[2], l[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = t * 8 + (lane & 3) * 2 + e;
         const bool on = i >= j && si == __float_as_int(rec[REC_SEG * C + j]);
-        const float gb = on ? expf((ci - rec[REC_CHI * C + j]) + (li - rec[REC_CLO * C + j])) * rec[REC_BETA * C + j] : 0.0f;
-        Pf[i * LD + j] = on ? a.scale * qk[t][2 * h + e] * gb : 0.0f;
-        Lf[i * LD + j] = on && i > j ? kk[t][2 * h + e] * gb : 0.0f;
+        const float gb = exp2_fast((ci - rec[REC_CHI * C + j]) + (li - rec[REC_CLO * C + j])) * rec[REC_BETA * C + j];
+        p[e] = on ? a.scale * qk[t][2 * h + e] * gb : 0.0f;
+        l[e] = on && i > j ? -kk[t][2 * h + e] * gb : 0.0f;
       }
+      *(float2*)(Pf + i * LD + t * 8 + (lane & 3) * 2) = make_float2(p[0], p[1]);
+      *(float2*)(Lf + i * LD + t * 8 + (lane & 3) * 2) = make_float2(l[0], l[1]);  // -L
+    }
   }
   __syncthreads();
   if (warp < 2) {  // T11 and T22
     const int o = warp * H;
     float x[H];
 #pragma unroll
+    for (int i = 0; i < H; ++i) x[i] = 0.0f;
+#pragma unroll
     for (int i = 0; i < H; ++i) {
-      float s[4] = {i == lane ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
+      const float* l = Lf + (o + i) * LD + o;  // zero from column o + i on, as x is
+      float s = i == lane ? 1.0f : 0.0f;
+      FV<2> s0 = {{s, 0.0f}}, s1 = {{0.0f, 0.0f}};
 #pragma unroll
       for (int k = 0; k < i; k += 4) {
-        const float4 l = *(const float4*)(Lf + (o + i) * LD + o + k);
-        s[0] -= l.x * x[k];
-        if (k + 1 < i) s[1] -= l.y * x[k + 1];
-        if (k + 2 < i) s[2] -= l.z * x[k + 2];
-        if (k + 3 < i) s[3] -= l.w * x[k + 3];
+        const float4 v = *(const float4*)(l + k);
+        s0 = fma(FV<2>{{v.x, v.y}}, FV<2>{{x[k], x[k + 1]}}, s0);
+        s1 = fma(FV<2>{{v.z, v.w}}, FV<2>{{x[k + 2], x[k + 3]}}, s1);
       }
-      x[i] = (s[0] + s[1]) + (s[2] + s[3]);
+      x[i] = (s0.v[0] + s1.v[0]) + (s0.v[1] + s1.v[1]);
     }
 #pragma unroll
     for (int i = 0; i < H; ++i) Tf[(o + i) * LD + o + lane] = x[i];
@@ -143,49 +183,37 @@ __global__ void __launch_bounds__(128) delta_tc_prep_kernel(DeltaTcArgs a) {
 #pragma unroll
     for (int k = 0; k < H; ++k) col[k] = B[k * LD + lane];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      float t[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int k = 0; k < H; k += 4) {
-        const float4 l = *(const float4*)(A + (warp * 8 + r) * LD + k);
-        t[0] = fmaf(l.x, col[k], t[0]);
-        t[1] = fmaf(l.y, col[k + 1], t[1]);
-        t[0] = fmaf(l.z, col[k + 2], t[0]);
-        t[1] = fmaf(l.w, col[k + 3], t[1]);
-      }
-      s[r] = t[0] + t[1];
-    }
+    for (int r = 0; r < 8; ++r) s[r] = dot_pairs<H>(A + (warp * 8 + r) * LD, col, 0.0f);
   };
   float s8[8];
-  small(Lf + H * LD, Tf, s8);
+  small(Lf + H * LD, Tf, s8);  // -L21 T11
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < 8; ++r) Lf[(H + warp * 8 + r) * LD + lane] = s8[r];
   __syncthreads();
   small(Tf + H * LD + H, Lf + H * LD, s8);
 #pragma unroll
-  for (int r = 0; r < 8; ++r) Tf[(H + warp * 8 + r) * LD + lane] = -s8[r];
+  for (int r = 0; r < 8; ++r) Tf[(H + warp * 8 + r) * LD + lane] = s8[r];
   __syncthreads();
-  {  // PT = P Tm
+  {  // PT = P Tm, in L's place; P's columns up to the next multiple of 4 are written (16 rows by 16 columns at once)
     const int j = tid & (C - 1), odd = tid >> 6;
     float x[C];
 #pragma unroll
     for (int k = 0; k < C; ++k) x[k] = Tf[k * LD + j];
 #pragma unroll
-    for (int i = 0; i < C; i += 2) {
-      const float* p = Pf + (i + odd) * LD;  // zero past column i + odd
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < C; i += 4) {
 #pragma unroll
-      for (int k = 0; k < i + 2; k += 4) {
-        const float4 l = *(const float4*)(p + k);
-        s[0] = fmaf(l.x, x[k], s[0]);
-        s[1] = fmaf(l.y, x[k + 1], s[1]);
-        if (k + 2 < i + 2) {
-          s[2] = fmaf(l.z, x[k + 2], s[2]);
-          s[3] = fmaf(l.w, x[k + 3], s[3]);
+      for (int r = 0; r < 4; r += 2) {
+        const float* p = Pf + (i + r + odd) * LD;
+        FV<2> s0 = {{0.0f, 0.0f}}, s1 = {{0.0f, 0.0f}};
+#pragma unroll
+        for (int k = 0; k < i + 4; k += 4) {
+          const float4 v = *(const float4*)(p + k);
+          s0 = fma(FV<2>{{v.x, v.y}}, FV<2>{{x[k], x[k + 1]}}, s0);
+          s1 = fma(FV<2>{{v.z, v.w}}, FV<2>{{x[k + 2], x[k + 3]}}, s1);
         }
+        Lf[(i + r + odd) * LD + j] = (s0.v[0] + s1.v[0]) + (s0.v[1] + s1.v[1]);
       }
-      Tf[(C + i + odd) * LD + j] = (s[0] + s[1]) + (s[2] + s[3]);
     }
   }
   __syncthreads();
@@ -193,9 +221,10 @@ __global__ void __launch_bounds__(128) delta_tc_prep_kernel(DeltaTcArgs a) {
 #pragma unroll 2
   for (int i = tid; i < 128 * 8; i += 128) {
     const int r = i >> 3, c = i & 7;
+    const float* from = (r < C ? Tf + r * LD : Lf + (r - C) * LD) + c * 8;
     float x[8];
-    *(float4*)x = *(const float4*)(Tf + r * LD + c * 8);
-    *(float4*)(x + 4) = *(const float4*)(Tf + r * LD + c * 8 + 4);
+    *(float4*)x = *(const float4*)from;
+    *(float4*)(x + 4) = *(const float4*)(from + 4);
     uint4 p[3];
     split8(x, p);
 #pragma unroll
@@ -216,13 +245,13 @@ template <int BV, int MT> struct TcChain {
 // the accumulators (rows 0 .. 63: K's steps, 64 .. 127: Q's; or rows of the state)
 // and half of the tile's columns. Thread 256 issues the products and the bulk
 // copies of images (an issuing thread waits while earlier products run: 150
-// cycles a product), warps 10 and 11 load and store the rows of tensors. The third
-// warpgroup gives registers to the other two: 256 * 200 + 128 * 104 = 384 * 168.
+// cycles a product) and of the tensors' rows; rows that are not whole 16-byte pieces
+// are loaded and stored by warps 10 and 11. The third warpgroup gives registers to the other two: 256 * 200 + 128 * 104 = 384 * 168.
 // MT: tiles of 128 state rows, whose fp32 values stay in registers. A chunk is
 // three dependent products (2000 cycles for BV = 64, Dk = 128) and their ways
 // through registers between barriers of the whole CTA.
 template <int BV, int MT>
-__global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
+__global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, const __grid_constant__ TcMaps maps) {
   using L = TcChain<BV, MT>;
   constexpr int RB = L::RB, NC = BV / 2, KST = L::KST, P = MT * 16;
   extern __shared__ unsigned char sm_raw[];
@@ -230,7 +259,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
   unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *YS = sm + L::AT_Y, *VS = sm + L::AT_V, *ZS = sm + L::AT_Z, *OS = sm + L::AT_O;
   float* recs = (float*)(sm + L::AT_REC);  // [2][gam, br][64]
   uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
-  uint32_t* slot = (uint32_t*)(barp + 3);
+  uint32_t* slot = (uint32_t*)(barp + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
   constexpr int KR = MT * 128;
   const int tiles = a.maps ? a.nvt + (a.KP + BV - 1) / BV : a.nvt;  // maps: and those of the identity
@@ -240,9 +269,9 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
   if (a.maps && seg == a.segs - 1 && !(ident && a.Sh)) return;  // nothing follows it; a backward wants its M
   const int nch = tc_chunks(a, b), ch0 = min(nch, seg * a.seglen), ch1 = min(nch, ch0 + a.seglen);
   const size_t vstride = (size_t)a.N * a.Dv, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
-  const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16;
+  const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_tp = bar + 16, bar_in = bar + 24;
   if (tid == 0) {
-    for (int k = 0; k < 3; ++k) mbar_init(bar + 8 * k, 1);
+    for (int k = 0; k < 4; ++k) mbar_init(bar + 8 * k, 1);
     fence_mbar_init_cluster();
   }
   if (warp == 0) tm_alloc<512>(slot);
@@ -260,21 +289,62 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
     if (warp == 8) {  // ---- products, bulk copies
       const unsigned char* tp = (const unsigned char*)a.tp + (size_t)bn * a.nc * L::TP;
       const bool one = lane == 0;
-      if (one && ch0 < ch1) load_bulk(TP, tp + (size_t)ch0 * L::TP, L::TP, bar_tp);
+      // K, Q, V and the steps' factors of a chunk, counted by bar_in
+      const int panels = (a.KP + 63) >> 6;
+      const uint32_t bytes = panels * 16384 + (ident ? 0 : L::YPLANE) + 512;
+      auto load_kq = [&](int ch) {
+        unsigned char* d = sm + (ch % KST) * L::KQ;
+        if (KST == 2) mbar_arrive_expect_tx(bar_in, bytes);
+        for (int p = 0; p < panels; ++p) {
+          tma_load_5d(smem_u32(d + p * TC_PANEL), &maps.k, bar_in, p * 64, nk, ch * TC_C, b, 0);
+          tma_load_5d(smem_u32(d + p * TC_PANEL + 8192), &maps.q, bar_in, p * 64, nk, ch * TC_C, b, 0);
+        }
+      };
+      auto load_v = [&](int ch) {
+        if (KST == 1) mbar_arrive_expect_tx(bar_in, bytes);
+        if (!ident) tma_load_5d(smem_u32(VS), &maps.v, bar_in, vt * BV, n, ch * TC_C, b, 0);
+        const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * TC_C;
+        const uint32_t d = smem_u32(recs + (ch & 1) * 2 * TC_C);
+        bulk_load_global(d, r + REC_GAM * TC_C, 256, bar_in);
+        bulk_load_global(d + 256, r + REC_BR * TC_C, 256, bar_in);
+      };
+      if (one && ch0 < ch1) {
+        load_bulk(TP, tp + (size_t)ch0 * L::TP, L::TP, bar_tp);
+        if (a.tma) {
+          if (KST == 2) load_kq(ch0);
+          load_v(ch0);
+          if (KST == 1) load_kq(ch0);
+        }
+      }
       const uint64_t td = tc_desc(smem_u32(TP), 16), yd = tc_desc<RB>(smem_u32(YS), L::YPLANE);
       for (int ch = ch0; ch < ch1; ++ch) {
-        const uint32_t kq = smem_u32(sm + (ch % KST) * L::KQ);
+        unsigned char* kqs = sm + (ch % KST) * L::KQ;
+        const uint32_t kq = smem_u32(kqs);
         const size_t tile = ((size_t)bn * a.nc + ch) * a.nvt + vt;
+        if (a.tma) {
+          wait(bar_in, (ch - ch0) & 1);
+          const int live = tc_live(a, b, ch);
+          if (live < TC_C && ch * TC_C + live < a.T) {  // steps of the tensor past the row's length
+            for (int p = 0; p < panels; ++p) {
+              clear_rows<128>(kqs + p * TC_PANEL, 0, live);
+              clear_rows<128>(kqs + p * TC_PANEL, 64, live);
+            }
+            clear_rows<RB>(VS, 0, live);
+            fence_proxy_async_smem();
+          }
+        }
         __syncthreads();  // 1
         if (one && !failed) {
           tm_fence_after();
           tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
           tc_commit(bar);
+          if (KST == 2 && a.tma && ch + 1 < ch1) load_kq(ch + 1);
           if (a.Sh && !a.maps) {  // the chunk's starting state, rounded: its first plane
             store_bulk(a.Sh + tile * a.KP * BV, SS, a.KP * RB);
             bulk_commit_group();
           }
         }
+        if (one) bulk_wait_group_read<0>();  // the state's planes and Z's and o's images may be written again
         __syncthreads();  // 2
         if (one) {
           wait(bar_tp, (ch - ch0) & 1);
@@ -286,8 +356,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
               for (int k = 0; k < 4; ++k)
                 tc_mma(tm + D2 + p * BV, td + p * (TC_PANEL >> 4) + 2 * k, yd + k * RB, tc_idesc((3 - p) * BV, false, true), p || k);
             tc_commit(bar);
+            if (a.tma && ch + 1 < ch1) load_v(ch + 1);
           }
-          bulk_wait_group_read<0>();  // the state's planes and Z's image may be written again
         }
         __syncthreads();  // 3
         if (one && !failed) {
@@ -302,9 +372,13 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
           if (ch + 1 < ch1) load_bulk(TP, tp + (size_t)(ch + 1) * L::TP, L::TP, bar_tp);  // the second products have read it
         }
         __syncthreads();  // 4
-        if (one && a.Zh && !a.maps && !failed) {
-          store_bulk(a.Zh + tile * 64 * BV, ZS, L::YPLANE);
-          bulk_commit_group();
+        if (one && !failed) {
+          if (KST == 1 && a.tma && ch + 1 < ch1) load_kq(ch + 1);
+          if (!a.maps) {
+            if (a.Zh) store_bulk(a.Zh + tile * 64 * BV, ZS, L::YPLANE);
+            if (a.tma) tma_store_5d(&maps.o, smem_u32(OS), vt * BV, n, ch * TC_C, b, 0);
+            bulk_commit_group();
+          }
         }
       }
       if (one) {
@@ -312,14 +386,14 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a) {
         bool f = false;
         tc_commit(bar_end);
         mbar_wait_bounded<false>(bar_end, 0, a.wait_limit_ns, nullptr, f);
-        if (failed)  // a copy of TP that nobody waited for lands before the CTA ends
-          for (int p = 0; p < 2; ++p) {
+        if (failed)  // copies that nobody waited for land before the CTA ends
+          for (int p = 0; p < 4; ++p) {
             f = false;
-            mbar_wait_bounded<false>(bar_tp, p, a.wait_limit_ns, nullptr, f);
+            mbar_wait_bounded<false>(p < 2 ? bar_tp : bar_in, p & 1, a.wait_limit_ns, nullptr, f);
           }
       }
-    } else {  // ---- rows
-      const int t = tid - 320;  // warps 10 and 11
+    } else {  // ---- rows that TMA cannot take
+      const int t = a.tma ? -1 : tid - 320;  // warps 10 and 11
       const size_t kstride = (size_t)a.Nk * a.Dk, kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk;
       auto load_kq = [&](int ch) {
         unsigned char* d = sm + (ch % KST) * L::KQ;
@@ -609,20 +683,20 @@ template <int KR, bool BACK> cudaError_t join_run(const DeltaTcArgs& a, int BV, 
   return cudaGetLastError();
 }
 
-template <int BV, int MT> cudaError_t chain(DeltaTcArgs a, cudaStream_t st) {
+template <int BV, int MT> cudaError_t chain(DeltaTcArgs a, const TcMaps& maps, cudaStream_t st) {
   constexpr int sm = TcChain<BV, MT>::BYTES;
   cudaError_t e = set_smem_attr((const void*)delta_tc_chain_kernel<BV, MT>, sm);
   if (e != cudaSuccess) return e;
   const unsigned lanes = (unsigned)(a.B * a.N * a.segs);
   if (a.segs > 1) {
     a.maps = 1;
-    delta_tc_chain_kernel<BV, MT><<<lanes * (a.nvt + (a.KP + BV - 1) / BV), 384, sm, st>>>(a);
+    delta_tc_chain_kernel<BV, MT><<<lanes * (a.nvt + (a.KP + BV - 1) / BV), 384, sm, st>>>(a, maps);
     note_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = join_run<MT * 128, false>(a, BV, st)) != cudaSuccess) return e;
     a.maps = 0;
   }
-  delta_tc_chain_kernel<BV, MT><<<lanes * a.nvt, 384, sm, st>>>(a);
+  delta_tc_chain_kernel<BV, MT><<<lanes * a.nvt, 384, sm, st>>>(a, maps);
   note_launch();
   return cudaGetLastError();
 }
@@ -633,6 +707,12 @@ cudaError_t delta_tc_join_back(int BV, const DeltaTcArgs& a, cudaStream_t st) {
   return a.KP > 128 ? join_run<256, true>(a, BV, st) : join_run<128, true>(a, BV, st);
 }
 
+cudaError_t tc_map(CUtensorMap* m, const void* base, const DeltaTcArgs& a, int heads, int D, int cols) {
+  const unsigned long long dims[5] = {(unsigned long long)D, (unsigned long long)heads, (unsigned long long)a.T, (unsigned long long)a.B, 1};
+  const unsigned int box[5] = {(unsigned)cols, 1, TC_C, 1, 1};
+  return encode_tensor_map_swizzled(m, base, 2, 5, dims, box, cols * 2);
+}
+
 cudaError_t delta_tc_fwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st) {
   const size_t sm = prep_smem(a.KP);
   cudaError_t e = set_smem_attr((const void*)delta_tc_prep_kernel, sm);
@@ -640,8 +720,14 @@ cudaError_t delta_tc_fwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st) {
   delta_tc_prep_kernel<<<(unsigned)((long long)a.B * a.N * a.nc), 128, sm, st>>>(a);
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.KP > 128) return chain<32, 2>(a, st);
-  return BV == 64 ? chain<64, 1>(a, st) : chain<32, 1>(a, st);
+  TcMaps maps;
+  DeltaTcArgs x = a;
+  x.tma = a.Dk % 8 == 0 && a.Dv % 8 == 0;
+  if (x.tma && ((e = tc_map(&maps.k, a.k, a, a.Nk, a.Dk, 64)) != cudaSuccess || (e = tc_map(&maps.q, a.q, a, a.Nk, a.Dk, 64)) != cudaSuccess ||
+                (e = tc_map(&maps.v, a.v, a, a.N, a.Dv, BV)) != cudaSuccess || (e = tc_map(&maps.o, a.o, a, a.N, a.Dv, BV)) != cudaSuccess))
+    return e;
+  if (a.KP > 128) return chain<32, 2>(x, maps, st);
+  return BV == 64 ? chain<64, 1>(x, maps, st) : chain<32, 1>(x, maps, st);
 }
 
 }  // namespace rnn
