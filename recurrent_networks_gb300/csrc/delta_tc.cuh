@@ -273,15 +273,24 @@ __device__ __forceinline__ void store_bulk(void* dst, const unsigned char* im, u
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(im)), "r"(bytes) : "memory");
 }
 
-// The products of one operand's K-major image (KP columns, panels of 128 rows)
-// with the MN-major planes at b (rows of RB bytes, PLANE bytes apart), n columns.
-template <int RB>
-__device__ __forceinline__ void tc_wide(uint32_t d, uint32_t a, uint32_t b, int plane, int KP, uint32_t id) {
-  uint64_t ad = tc_desc(a, 16), bd = tc_desc<RB>(b, plane);
-  for (int k = 0; k < KP; k += 64, ad += TC_PANEL >> 4, bd += 4 * RB)
+// The products of one operand's K-major image (panels of 64 columns, 128 rows) with
+// the MN-major planes at b (rows of RB bytes, `plane` bytes apart). Whole panels:
+// their columns past KP are zero, the states' rows past it finite.
+template <int RB, int PANELS>
+__device__ __forceinline__ void tc_panels(uint32_t d, uint32_t a, uint32_t b, int plane, uint32_t id) {
+  const uint64_t ad = tc_desc(a, 16), bd = tc_desc<RB>(b, plane);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (k + 16 * j < KP) tc_mma(d, ad + 2 * j, bd + j * RB, id, k || j);
+  for (int k = 0; k < 4 * PANELS; ++k) tc_mma(d, ad + (k >> 2) * (TC_PANEL >> 4) + (k & 3) * 2, bd + k * RB, id, k);
+}
+template <int RB, int MT>
+__device__ __forceinline__ void tc_wide(int panels, uint32_t d, uint32_t a, uint32_t b, int plane, uint32_t id) {
+  if (MT == 1) {
+    if (panels == 1) tc_panels<RB, 1>(d, a, b, plane, id);
+    else tc_panels<RB, 2>(d, a, b, plane, id);
+  } else {
+    if (panels == 3) tc_panels<RB, 3>(d, a, b, plane, id);
+    else tc_panels<RB, 4>(d, a, b, plane, id);
+  }
 }
 
 // N values of a row of a tensor whose rows have D - c valid columns from p on

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
         __syncthreads();  // 1
         if (one && !failed) {
           tm_fence_after();
-          tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
+          tc_wide<RB, MT>(panels, tm + D1, kq, smem_u32(SS), L::SPLANE, tc_idesc(3 * BV, false, true));
           tc_commit(bar);
           if (KST == 2 && a.tma && ch > ch0) load_kq(ch - 1);
           if (!a.maps) {
@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
         unsigned char* d = sm + (ch % KST) * L::KQ;
         const int live = tc_live(a, b, ch);
         const size_t at = kat + (size_t)ch * TC_C * kstride;
-        load_img<128, P, 64>(t, d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
-        load_img<128, P, 64>(t, d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+        load_img<128, P, 64>(t, d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, (a.KP + 63) & ~63, TC_PANEL);
+        load_img<128, P, 64>(t, d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, (a.KP + 63) & ~63, TC_PANEL);
       };
       auto load_o = [&](int ch) {
         load_img<RB, BV / 8, 64>(t, OS, 0, (const bf16*)(a.dO ? a.dO : a.v) + vat + (size_t)ch * TC_C * vstride, vstride,
@@ -555,8 +555,8 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     }
   take();
   // X and Z are done with
-  load_img<128, KT / 8, 256>(tid, KQ, 0, (const bf16*)a.k + kat, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
-  load_img<128, KT / 8, 256>(tid, KQ, 64, (const bf16*)a.q + kat, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+  load_img<128, KT / 8, 256>(tid, KQ, 0, (const bf16*)a.k + kat, kstride, live, a.Dk, 0, (a.KP + 63) & ~63, TC_PANEL);
+  load_img<128, KT / 8, 256>(tid, KQ, 64, (const bf16*)a.q + kat, kstride, live, a.Dk, 0, (a.KP + 63) & ~63, TC_PANEL);
   cp_commit();
   // [M + M^T, R^T; R, 0] over the buffers of S0 and dS1: two panels of 128 rows
   if (quad >= 2) {
@@ -755,6 +755,8 @@ cudaError_t delta_tc_bwd_launch(int BV, const DeltaTcArgs& a, cudaStream_t st) {
   TcMaps maps;
   DeltaTcArgs x = a;
   cudaError_t e;
+  int dev = 0;  // a thread of autograd's makes its first call here, perhaps: the maps' encoding wants a context
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess || (e = cudaSetDevice(dev)) != cudaSuccess) return e;
   x.tma = a.Dk % 8 == 0 && a.Dv % 8 == 0;
   if (x.tma && ((e = tc_map(&maps.k, a.k, a, a.Nk, a.Dk, 64)) != cudaSuccess || (e = tc_map(&maps.q, a.q, a, a.Nk, a.Dk, 64)) != cudaSuccess ||
                 (e = tc_map(&maps.v, a.v, a, a.N, a.Dv, BV)) != cudaSuccess || (e = tc_map(&maps.dv, a.dv, a, a.N, a.Dv, BV)) != cudaSuccess ||

@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
         __syncthreads();  // 1
         if (one && !failed) {
           tm_fence_after();
-          tc_wide<RB>(tm + D1, kq, smem_u32(SS), L::SPLANE, a.KP, tc_idesc(3 * BV, false, true));
+          tc_wide<RB, MT>(panels, tm + D1, kq, smem_u32(SS), L::SPLANE, tc_idesc(3 * BV, false, true));
           tc_commit(bar);
           if (KST == 2 && a.tma && ch + 1 < ch1) load_kq(ch + 1);
           if (a.Sh && !a.maps) {  // the chunk's starting state, rounded: its first plane
@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
         unsigned char* d = sm + (ch % KST) * L::KQ;
         const int live = tc_live(a, b, ch);
         const size_t at = kat + (size_t)ch * TC_C * kstride;
-        load_img<128, P, 64>(t, d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
-        load_img<128, P, 64>(t, d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, a.KP, TC_PANEL);
+        load_img<128, P, 64>(t, d, 0, (const bf16*)a.k + at, kstride, live, a.Dk, 0, (a.KP + 63) & ~63, TC_PANEL);
+        load_img<128, P, 64>(t, d, 64, (const bf16*)a.q + at, kstride, live, a.Dk, 0, (a.KP + 63) & ~63, TC_PANEL);
       };
       auto load_v = [&](int ch) {
         if (!ident)
