@@ -27,28 +27,59 @@ struct NormArgs {
   void *y, *dx, *dgate;
   float* part;  // [gridDim.x][2][C]: sums of dt n and dt over a CTA's rows, or null
   int lanes, gp, rp;  // threads of a group; groups and rows that a CTA takes at once
+  // channels that warp k of a group's several has
+  __device__ int share_of(int k, int vec, int nv) const {
+    int n = 0;
+    for (int v = 0; v < nv; ++v) n += max(0, min(32, (W + vec - 1) / vec - (k * 32 + v * lanes))) * vec;
+    return n;
+  }
 };
 
-// VEC values of T at p, 16 bytes at once where VEC > 1
-template <typename T, int VEC> __device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = to_f(p[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 x = *(const float4*)p;
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-  } else {
-    const uint4 x = *(const uint4*)p;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// VEC values of T as they are loaded: 16 bytes, a pair, or one value
+template <typename T, int VEC> struct Raw {
+  uint4 v;
+  __device__ void load(const T* p) { v = __ldcs((const uint4*)p); }
+  __device__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ void get(float (&x)[VEC]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
     }
   }
+};
+template <typename T> struct Raw<T, 2> {
+  alignas(2 * sizeof(T)) T v[2];
+  __device__ void load(const T* p) {
+    if constexpr (sizeof(T) == 4) *(float2*)v = *(const float2*)p;
+    else *(uint32_t*)v = *(const uint32_t*)p;
+  }
+  __device__ void zero() { v[0] = v[1] = from_f<T>(0.0f); }
+  __device__ void get(float (&x)[2]) const { x[0] = to_f(v[0]), x[1] = to_f(v[1]); }
+};
+template <typename T> struct Raw<T, 1> {
+  T v;
+  __device__ void load(const T* p) { v = *p; }
+  __device__ void zero() { v = from_f<T>(0.0f); }
+  __device__ void get(float (&x)[1]) const { x[0] = to_f(v); }
+};
+template <typename T, int VEC> __device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
+  Raw<T, VEC> r;
+  r.load(p);
+  r.get(v);
 }
 template <typename T, int VEC> __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
     p[0] = from_f<T>(v[0]);
+  } else if constexpr (VEC == 2) {
+    if constexpr (sizeof(T) == 4) *(float2*)p = make_float2(v[0], v[1]);
+    else *(__nv_bfloat162*)p = __floats2bfloat162_rn(v[0], v[1]);
   } else if constexpr (sizeof(T) == 4) {
     *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
   } else {
@@ -85,23 +116,16 @@ template <typename T> __device__ __forceinline__ void act_both(int act, float x,
   slope = act == RNN_ACT_SILU ? fmaf(x, c, s) : c;
 }
 
-// The sum over a group's threads: a power of two of a warp's lanes, or (MANY)
-// whole warps, whose sums pass through red [8]. A place of red is written again
-// three such sums later, with barriers between.
-template <bool MANY> __device__ __forceinline__ float lane_sum(float v, int lanes, float* red) {
-  if constexpr (!MANY) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  } else {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int warp = threadIdx.x >> 5, n = lanes >> 5, w0 = warp & ~(n - 1);
-    if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    v = 0.0f;
-    for (int i = 0; i < n; ++i) v += red[w0 + i];
-    return v;
-  }
+// The sum over `lanes` (a power of two up to 32) lanes of a warp.
+__device__ __forceinline__ float lane_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// What the warps of a group (MANY: of several whole warps) have, through red [8]:
+// one barrier; the place is written again only behind the next one.
+__device__ __forceinline__ void share(float2* red, float a, float b) {
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
 }
 
 // What both directions do with a value once the statistics are known.
@@ -120,20 +144,27 @@ __device__ __forceinline__ float backward_value(int act, float n, float w, float
   return GATE ? dy * a : dy * slope;
 }
 
-// Groups of up to 256 * NV vectors: `lanes` threads (a power of two; MANY: of
-// several warps) hold a group's channels in registers. A CTA takes gp groups of
-// rp rows at once, the same groups for all its rows, so that a thread's sums of
-// dw and db are over one set of columns. One pass over the data.
+// Groups of up to 256 * NV vectors (of VEC channels): `lanes` threads (a power of
+// two; MANY: of several warps) hold a group's channels in registers. A CTA takes
+// gp groups of rp rows at once, the same groups for all its rows, so that a
+// thread's sums of dw and db are over one set of columns. One pass over the data,
+// bound by DRAM: measured 69 us forward (floor 59) and 142 backward (floor 99) for
+// 16384 rows x 32 groups of 128, bf16, gated; 23 and 44 us (floors 10 and 15) for
+// 16384 rows of one group of 1024, where the two sums of a row that eight warps
+// share are waited for. Four CTAs an SM forward, with few spills, against one with
+// none: 34 us and 47 (30000 rows x 16 of 64, gated); backward they cost more (85 us
+// against 66), and it keeps its registers.
 template <typename T, int VEC, int NV, bool GATE, bool BWD, bool MANY>
-__global__ void __launch_bounds__(256) norm_kernel(NormArgs p) {
+__global__ void __launch_bounds__(256, BWD ? (VEC * NV > 8 ? 1 : 2) : (VEC * NV > 16 ? 2 : 4)) norm_kernel(NormArgs p) {
   extern __shared__ float sums[];  // [2][gp * W], BWD with p.part
-  __shared__ float red[4][8];
+  __shared__ float2 red[2][8];
   const int li = threadIdx.x % p.lanes, slot = threadIdx.x / p.lanes;
   const int gi = slot % p.gp, ri = slot / p.gp;
   const int g = blockIdx.y * p.gp + gi;
   const bool on = ri < p.rp && g < p.G;
   const long long C = (long long)p.G * p.W;
   const float inv = 1.0f / (float)p.W;
+  const int many = MANY ? p.lanes >> 5 : 1, lanes = MANY ? 32 : p.lanes, w0 = (threadIdx.x >> 5) & ~(many - 1);
   float w[NV][VEC], b[NV][VEC];
   bool have[NV];
 #pragma unroll
@@ -152,8 +183,35 @@ __global__ void __launch_bounds__(256) norm_kernel(NormArgs p) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) dw[v][e] = db[v][e] = 0.0f;
   }
-  // all threads of a warp stay in the loop: the sums are over the warp's lanes
-  for (long long r0 = (long long)blockIdx.x * p.rp; r0 < p.rows; r0 += (long long)gridDim.x * p.rp) {
+  __shared__ float part[8];  // channels of a group's warp
+  if constexpr (MANY) {
+    if (threadIdx.x < many) part[threadIdx.x] = (float)p.share_of(threadIdx.x, VEC, NV);
+    __syncthreads();
+  }
+  const float mine = MANY ? 1.0f / fmaxf(part[(threadIdx.x >> 5) - w0], 1.0f) : inv;
+  // A row's values are loaded while the one before is worked on. All threads of a
+  // warp stay in the loop: the sums are over the warp's lanes.
+  Raw<T, VEC> rx[NV], rz[GATE ? NV : 1], rd[BWD ? NV : 1];
+  auto load = [&](long long r) {
+    const bool live = on && r < p.rows;
+    const size_t at = (size_t)(live ? r : 0) * C + (size_t)(on ? g : 0) * p.W;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (li + v * p.lanes) * VEC;
+      if (live && have[v]) {
+        rx[v].load((const T*)p.x + at + c);
+        if constexpr (GATE) rz[v].load((const T*)p.gate + at + c);
+        if constexpr (BWD) rd[v].load((const T*)p.dy + at + c);
+      } else {
+        rx[v].zero();
+        if constexpr (GATE) rz[v].zero();
+        if constexpr (BWD) rd[v].zero();
+      }
+    }
+  };
+  const long long step = (long long)gridDim.x * p.rp;
+  load((long long)blockIdx.x * p.rp + ri);
+  for (long long r0 = (long long)blockIdx.x * p.rp; r0 < p.rows; r0 += step) {
     const long long r = r0 + ri;
     const bool live = on && r < p.rows;
     const size_t at = (size_t)(live ? r : 0) * C + (size_t)(on ? g : 0) * p.W;
@@ -161,32 +219,45 @@ __global__ void __launch_bounds__(256) norm_kernel(NormArgs p) {
     float s = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (li + v * p.lanes) * VEC;
-      if (live && have[v]) {
-        load_vec<T, VEC>((const T*)p.x + at + c, x[v]);
-        if constexpr (GATE) load_vec<T, VEC>((const T*)p.gate + at + c, z[v]);
-        if constexpr (BWD) load_vec<T, VEC>((const T*)p.dy + at + c, dy[v]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          x[v][e] = 0.0f;
-          if constexpr (GATE) z[v][e] = 0.0f;
-          if constexpr (BWD) dy[v][e] = 0.0f;
-        }
-      }
+      rx[v].get(x[v]);
+      if constexpr (GATE) rz[v].get(z[v]);
+      if constexpr (BWD) rd[v].get(dy[v]);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s += x[v][e];
     }
-    const float mean = p.centered ? lane_sum<MANY>(s, p.lanes, red[0]) * inv : 0.0f;
-    s = 0.0f;
+    if (r0 + step < p.rows) load(r + step);
+    // Mean and sum of squares around it; where a group has several warps, around
+    // each warp's own mean, joined by the distance of the means.
+    s = p.centered ? lane_sum(s, lanes) : 0.0f;
+    float mean = s * mine;
+    float q = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        x[v][e] = have[v] ? x[v][e] - mean : 0.0f;
-        s = fmaf(x[v][e], x[v][e], s);
+        const float d = have[v] ? x[v][e] - mean : 0.0f;
+        if constexpr (!MANY) x[v][e] = d;
+        q = fmaf(d, d, q);
       }
-    const float rstd = 1.0f / sqrtf(fmaf(lane_sum<MANY>(s, p.lanes, red[1]), inv, p.eps));
+    q = lane_sum(q, lanes);
+    if constexpr (MANY) {
+      share(red[0], s, q);
+      float tot = 0.0f;
+      for (int k = 0; k < many; ++k) tot += red[0][w0 + k].x;
+      mean = tot * inv;
+      q = 0.0f;
+      for (int k = 0; k < many; ++k) {
+        const float n = part[k];
+        const float2 r = red[0][w0 + k];
+        const float d = p.centered ? __fdividef(r.x, fmaxf(n, 1.0f)) - mean : 0.0f;
+        q += fmaf(n * d, d, r.y);
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[v][e] = have[v] ? x[v][e] - mean : 0.0f;
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(q, inv, p.eps));
     if constexpr (!BWD) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -217,8 +288,22 @@ __global__ void __launch_bounds__(256) norm_kernel(NormArgs p) {
           s1 += dn;
           s2 = fmaf(dn, n, s2);
         }
-      s1 = p.centered ? lane_sum<MANY>(s1, p.lanes, red[2]) * inv : 0.0f;
-      s2 = lane_sum<MANY>(s2, p.lanes, red[3]) * inv;
+      for (int o = lanes >> 1; o > 0; o >>= 1) {
+        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+      }
+      if constexpr (MANY) {
+        share(red[1], s1, s2);
+        s1 = s2 = 0.0f;
+        for (int k = 0; k < many; ++k) {
+          s1 += red[1][w0 + k].x;
+          s2 += red[1][w0 + k].y;
+        }
+      } else {
+        __syncwarp();
+      }
+      s1 = p.centered ? s1 * inv : 0.0f;
+      s2 *= inv;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         if (!live || !have[v]) continue;
@@ -384,19 +469,22 @@ struct NormPlan {
   int vec, nv, lanes, gp, rp;
   unsigned gx, gy;
 };
-NormPlan norm_plan(long long rows, int G, int W, int dtype) {
+NormPlan norm_plan(long long rows, int G, int W, int dtype, bool bwd) {
   NormPlan p{};
   const int full = dtype == RNN_BF16 ? 8 : 4;
-  p.vec = W % full == 0 ? full : 1;
+  p.vec = W % full == 0 ? full : W % 2 == 0 ? 2 : 1;
   const int n = (W + p.vec - 1) / p.vec;  // vectors of a group
-  const int most = p.vec == 1 ? 8 : 2;  // a thread's, so that the registers suffice
+  // Threads before vectors: a group of several warps is slower by its barrier and
+  // faster by its loads in flight. Backward, 4 KB rows at one vector a thread take
+  // 44 us and at two 64; forward two are as fast, and 8 KB rows gain (22 us, 27).
+  const int most = p.vec == 1 ? 8 : p.vec == 2 ? 4 : 2, some = p.vec == 1 ? 4 : p.vec == 2 || !bwd ? 2 : 1;  // vectors a thread: at most, and while threads are to be had
   if (n > 256 * most) {
     p.gp = p.rp = 1;
     p.gy = (unsigned)G;
   } else {
     p.lanes = 1;
     while (p.lanes < 32 && p.lanes < n) p.lanes *= 2;
-    while (p.lanes * most < n) p.lanes *= 2;
+    while (p.lanes < 256 && p.lanes * some < n) p.lanes *= 2;
     p.nv = 1;
     while (p.nv * p.lanes < n) p.nv *= 2;
     const int slots = 256 / p.lanes;
@@ -405,7 +493,7 @@ NormPlan norm_plan(long long rows, int G, int W, int dtype) {
     p.gy = (unsigned)((G + p.gp - 1) / p.gp);
   }
   const long long want = (rows + p.rp - 1) / p.rp;
-  long long most_ctas = (long long)device_sms() * (p.nv ? 6 : 2) / p.gy;
+  long long most_ctas = (long long)device_sms() * (p.nv && p.nv * p.vec <= (bwd ? 8 : 16) ? 4 : 2) / p.gy;  // about what an SM holds
   if (most_ctas < 1) most_ctas = 1;
   p.gx = (unsigned)(want < 1 ? 1 : want < most_ctas ? want : most_ctas);
   return p;
@@ -427,12 +515,15 @@ template <typename T, int VEC, int NV> cudaError_t narrow(const NormPlan& pl, co
 template <typename T, int VEC> cudaError_t launch_nv(const NormPlan& pl, const NormArgs& a, bool bwd, cudaStream_t st) {
   if (pl.nv == 1) return narrow<T, VEC, 1>(pl, a, bwd, st);
   if (pl.nv == 2) return narrow<T, VEC, 2>(pl, a, bwd, st);
-  if constexpr (VEC == 1) return pl.nv == 4 ? narrow<T, 1, 4>(pl, a, bwd, st) : narrow<T, 1, 8>(pl, a, bwd, st);
+  if constexpr (VEC <= 2) {
+    if (pl.nv == 4) return narrow<T, VEC, 4>(pl, a, bwd, st);
+  }
+  if constexpr (VEC == 1) return narrow<T, 1, 8>(pl, a, bwd, st);
   return cudaErrorInvalidValue;
 }
 template <typename T> cudaError_t launch(const NormPlan& pl, const NormArgs& a, bool bwd, cudaStream_t st) {
   constexpr int FULL = 16 / sizeof(T);
-  if (pl.nv) return pl.vec == 1 ? launch_nv<T, 1>(pl, a, bwd, st) : launch_nv<T, FULL>(pl, a, bwd, st);
+  if (pl.nv) return pl.vec == 1 ? launch_nv<T, 1>(pl, a, bwd, st) : pl.vec == 2 ? launch_nv<T, 2>(pl, a, bwd, st) : launch_nv<T, FULL>(pl, a, bwd, st);
   void (*k)(NormArgs) = bwd ? (a.gate ? norm_wide_kernel<T, true, true> : norm_wide_kernel<T, false, true>)
                             : (a.gate ? norm_wide_kernel<T, true, false> : norm_wide_kernel<T, false, false>);
   const size_t sm = (size_t)(bwd ? (a.part ? 4 : 2) : 1) * a.W * 4;
@@ -459,7 +550,7 @@ extern "C" {
 
 size_t rnn_group_norm_workspace_size(long long rows, int groups, int width, int dtype) {
   if (!norm_ok(rows, groups, width, dtype)) return 0;
-  return 256 + (size_t)norm_plan(rows, groups, width, dtype).gx * 2 * groups * width * sizeof(float);
+  return 256 + (size_t)norm_plan(rows, groups, width, dtype, true).gx * 2 * groups * width * sizeof(float);
 }
 
 int rnn_group_norm_fwd(long long rows, int groups, int width, int dtype, int act, int centered, float eps, const void* x,
@@ -470,7 +561,7 @@ int rnn_group_norm_fwd(long long rows, int groups, int width, int dtype, int act
   for (const void* p : ptrs)
     if (p && !al16(p)) return RNN_EINVAL;
   if (rows == 0) return RNN_OK;
-  const NormPlan pl = norm_plan(rows, groups, width, dtype);
+  const NormPlan pl = norm_plan(rows, groups, width, dtype, false);
   NormArgs a = norm_args(pl, rows, groups, width, act, centered, eps);
   a.x = x; a.w = w; a.b = b; a.gate = gate; a.y = y;
   cudaStream_t st = (cudaStream_t)stream;
@@ -491,7 +582,7 @@ int rnn_group_norm_bwd(long long rows, int groups, int width, int dtype, int act
     int rc = dw ? cuda_status(cudaMemsetAsync(dw, 0, C * e, st)) : RNN_OK;
     return rc || !db ? rc : cuda_status(cudaMemsetAsync(db, 0, C * e, st));
   }
-  const NormPlan pl = norm_plan(rows, groups, width, dtype);
+  const NormPlan pl = norm_plan(rows, groups, width, dtype, true);
   NormArgs a = norm_args(pl, rows, groups, width, act, centered, eps);
   a.x = x; a.w = w; a.b = b; a.gate = gate; a.dy = dy; a.dx = dx; a.dgate = dgate;
   if (dw || db) {

@@ -142,7 +142,9 @@ def flashrnn_stack(x, layers, function: str = "lstm", backend: str = "auto"):
     layer's h, [B, T, N*D], otherwise) with W_x [G*N*D, I_l] (+ bias_x) and
     runs the head-wise scan with R, b and initial states (or zeros).
     layers: sequence of dicts with keys W_x, bias_x (optional), R, b, states
-    (optional). Returns (h of the last layer [B, T, N*D], [(states, last) of
+    (optional) and norm (optional: a dict of group_norm's weight, bias,
+    activation, eps and centered, with which the layer's h leaves it, normalised
+    head by head). Returns (h of the last layer [B, T, N*D], [(states, last) of
     every layer]). Differentiable end to end (autograd chains the kernels'
     backward passes)."""
     B, T = x.shape[0], x.shape[1]
@@ -155,6 +157,8 @@ def flashrnn_stack(x, layers, function: str = "lstm", backend: str = "auto"):
         states, last = flashrnn(Wx, R, layer["b"], layer.get("states"), function, backend)
         outs.append((states, last))
         h = states[0].reshape(B, T, N * D)
+        if layer.get("norm") is not None:
+            h = group_norm(h, N, **layer["norm"])
     return h, outs
 
 
@@ -415,16 +419,20 @@ class _DeltaFn(torch.autograd.Function):
         return (_delta_bwd_once if torch.is_grad_enabled() else _delta_bwd)(ctx, do, dlast)
 
 
+def _delta_grads(q, v, state, plan):
+    """dq, dk, dv, dg, dbeta, dstate (or None) and the workspace."""
+    B, T, N, Dv = v.shape
+    dg, dbeta = (torch.empty((B, T, N), dtype=torch.float32, device=q.device) for _ in range(2))
+    ds = torch.empty((B, 1, N, q.shape[3], Dv), dtype=torch.float32, device=q.device) if state else None
+    return (q.new_empty(q.shape), q.new_empty(q.shape), q.new_empty(v.shape), dg, dbeta, ds,
+            torch.empty(plan[3], dtype=torch.uint8, device=q.device))
+
+
 def _delta_bwd(ctx, do, dlast):
     _first_order(do, dlast)
     q, k, v, lengths, tape = ctx.saved_tensors
-    dims, _, _, size = ctx.plan
-    B, T, N, Dv = v.shape
-    dq, dk, dv = q.new_empty(q.shape), q.new_empty(q.shape), q.new_empty(v.shape)
-    dg, dbeta = (torch.empty((B, T, N), dtype=torch.float32, device=q.device) for _ in range(2))
-    ds = torch.empty((B, 1, N, q.shape[3], Dv), dtype=torch.float32, device=q.device) if ctx.needs_input_grad[5] else None
-    ws = torch.empty(size, dtype=torch.uint8, device=q.device)
-    _lib.rnn_delta_bwd(dims, q, k, v, lengths, ctx.scale, tape, _dense(do), _dense(dlast), dq, dk, dv, dg, dbeta, ds, ws)
+    dq, dk, dv, dg, dbeta, ds, ws = _delta_grads(q, v, ctx.needs_input_grad[5], ctx.plan)
+    _lib.rnn_delta_bwd(ctx.plan[0], q, k, v, lengths, ctx.scale, tape, _dense(do), _dense(dlast), dq, dk, dv, dg, dbeta, ds, ws)
     _add_status(ctx.status, tape)
     return dq, dk, dv, dg, dbeta, ds, None, None, None, None
 
@@ -551,24 +559,28 @@ class _NormFn(torch.autograd.Function):
         return (_norm_bwd_once if torch.is_grad_enabled() else _norm_bwd)(ctx, dy)
 
 
+def _norm_grads(x, weight, bias, gate, groups, need):
+    """dx, dweight, dbias, dgate (or None) and the workspace (or None)."""
+    dx, dgate = x.new_empty(x.shape), None if gate is None else x.new_empty(x.shape)
+    dw = weight.new_empty(weight.shape) if need[1] else None
+    db = bias.new_empty(bias.shape) if need[2] else None
+    ws = None
+    if dw is not None or db is not None:
+        C = x.shape[-1]
+        size = _lib.rnn_group_norm_workspace_size(x.numel() // C, groups, C // groups, x.dtype, x.get_device())
+        ws = torch.empty(size, dtype=torch.uint8, device=x.device)
+    return dx, dw, db, dgate, ws
+
+
 def _norm_bwd(ctx, dy):
     _first_order(dy)
     x, weight, bias, gate = ctx.saved_tensors
     groups, activation, eps, centered = ctx.args
     need = ctx.needs_input_grad
+    dx, dw, db, dgate, ws = _norm_grads(x, weight, bias, gate, groups, need)
     C = x.shape[-1]
-    rows, width = x.numel() // C, C // groups
-    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
-    dx = new(x)
-    dgate = None if gate is None else new(gate)
-    dw = new(weight) if need[1] else None
-    db = new(bias) if need[2] else None
-    ws = None
-    if dw is not None or db is not None:
-        size = _lib.rnn_group_norm_workspace_size(rows, groups, width, x.dtype, x.get_device())
-        ws = torch.empty(size, dtype=torch.uint8, device=x.device)
-    _lib.rnn_group_norm_bwd(rows, groups, width, activation, centered, eps, x, weight, bias, gate, _dense(dy), dx, dgate,
-                            dw, db, ws)
+    _lib.rnn_group_norm_bwd(x.numel() // C, groups, C // groups, activation, centered, eps, x, weight, bias, gate,
+                            _dense(dy), dx, dgate, dw, db, ws)
     return dx if need[0] else None, dw, db, dgate if need[3] else None, None, None, None, None
 
 

@@ -70,7 +70,7 @@ def check(p, groups, act, gate=True, affine=True, centered=True, eps=1e-5):
 # several warps a group, with rows that are whole vectors and that are not; the
 # row in shared memory; the widest; more groups than a CTA takes
 SHAPES = [(1, 1, 1), (3, 5, 7), (7, 4, 16), (37, 5, 83), (9, 3, 256), (5, 2, 264), (130, 8, 128), (4, 1, 1000), (3, 2, 1001),
-          (5, 1, 2049), (3, 1, 4096), (2, 1, 8192), (2, 1, 14336), (2, 1, 14335), (6, 300, 8), (3, 70, 24), (5000, 3, 40)]
+          (5, 1, 2049), (9, 3, 382), (2, 1, 2050), (3, 1, 4096), (2, 1, 8192), (2, 1, 14336), (2, 1, 14335), (6, 300, 8), (3, 70, 24), (5000, 3, 40)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
