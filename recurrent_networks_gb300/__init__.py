@@ -2,7 +2,8 @@
 backward through time in hand-written sm_103a CUDA kernels behind a C ABI
 (include/rnn.h, librnn_gb300.so); beside it the operators of a recurrent
 language model around the scan: the gated linear scan and its single-token
-step, 8-bit activation checkpoints and the token embedding."""
+step, the gated delta rule (a matrix for a state) and its step, the group norm
+of a scan's heads, 8-bit activation checkpoints and the token embedding."""
 from .functional import (checkpoint_pack, checkpoint_unpack, embedding, flashrnn, gated_delta,  # noqa: F401
                          gated_delta_step, gated_scan, gated_scan_step, group_norm, input_projection)
 

@@ -160,13 +160,13 @@ bool delta_sizes(const rnn_delta_dims_t* d, bool keep, DeltaSizes* z) {
   if (!d || d->B < 1 || d->T < 0 || d->T > INT_MAX - 64 || !delta_heads_ok(d->Nk, d->N, d->Dk, d->Dv, d->dtype)) return false;
   *z = DeltaSizes{};
   z->bf = d->dtype == RNN_BF16;
-  z->C = z->bf ? TC_C : DeltaCfg<float>::C;
-  z->NP = 3;
+  z->C = z->bf ? TC_C : F32_C;
+  z->NP = F32_NP;
   z->KP = (d->Dk + 15) / 16 * 16;
   z->nc = ((long long)d->T + z->C - 1) / z->C;
   z->items = z->nc * d->B * d->N;
   if ((long long)d->B * d->N * 64 > INT_MAX || z->items > INT_MAX / 16) return false;  // counted in 32 bits with their tiles
-  DeltaLay lay{32, 1, 0};
+  DeltaLay lay{F32_BV, 1, 0};
   if (z->bf) lay = delta_lay((long long)d->B * d->N, d->Dv, z->KP, z->nc, device_sms(), keep);
   z->BV = lay.BV; z->segs = lay.segs; z->seglen = lay.seglen;
   z->nvt = (d->Dv + z->BV - 1) / z->BV;
@@ -175,8 +175,8 @@ bool delta_sizes(const rnn_delta_dims_t* d, bool keep, DeltaSizes* z) {
   if (z->bf) {
     z->ne = z->nc / TC_EDGE + 1;
     z->tri = up256(n * 3 * 128 * TC_C * 2);  // TP
-    z->S = up256(n * z->nvt * z->KP * z->BV * 2);
-    z->Z = up256(n * z->nvt * 64 * z->BV * 2);
+    z->S = up256(n * z->nvt * 2 * z->KP * z->BV * 2);
+    z->Z = up256(n * z->nvt * 64 * z->BV * 2);  // dY's second plane
     z->zf = up256(n * z->nvt * 64 * z->BV * 4);
     z->sf = up256(heads * z->ne * z->nvt * (z->KP > 128 ? 256 : 128) * z->BV * 4);
     if (z->segs > 1) {
@@ -185,10 +185,10 @@ bool delta_sizes(const rnn_delta_dims_t* d, bool keep, DeltaSizes* z) {
       z->H = up256(heads * z->segs * z->nvt * z->BV * KR * 4);
     }
     z->tape = z->rec + z->tri + z->M + 2 * z->H;
-    if (keep) z->tape += z->S + z->Z + 2 * z->zf + z->sf;
+    if (keep) z->tape += z->S + 2 * z->zf + z->sf;
     z->dots = up256(n * z->nvt * 6 * TC_C * 4);
     z->edge = up256(heads * z->ne * z->nvt * 8 * 4);
-    z->bwd = z->S + z->dots + z->edge + 2 * z->H;
+    z->bwd = z->S + z->Z + z->dots + z->edge + 2 * z->H;
   } else {
     z->tri = up256(n * z->NP * z->C * z->C * 2);  // each of Tm and P
     z->S = up256(n * z->nvt * z->NP * z->KP * z->BV * 2);
@@ -231,8 +231,7 @@ DeltaTcArgs delta_tc_args(const rnn_delta_dims_t* d, const DeltaSizes& z, void* 
   t += z.H;
   if (!keep) return a;
   a.Sh = (bf16*)t;
-  a.Zh = (bf16*)(t += z.S);
-  a.zf = (float*)(t += z.Z);
+  a.zf = (float*)(t += z.S);
   a.of = (float*)(t += z.zf);
   a.sf = (float*)(t += z.zf);
   return a;
@@ -319,10 +318,11 @@ int rnn_delta_bwd(const rnn_delta_dims_t* d, const void* q, const void* k, const
     DeltaTcArgs a = delta_tc_args(d, z, tape, true);
     fill(a);
     a.dSh = (bf16*)w;
-    a.dots = (float*)(w + z.S);
-    a.edge = (float*)(w + z.S + z.dots);
-    a.Ht = (float*)(w + z.S + z.dots + z.edge);
-    a.St = (float*)(w + z.S + z.dots + z.edge + z.H);
+    a.dYl = (bf16*)(w += z.S);
+    a.dots = (float*)(w += z.Z);
+    a.edge = (float*)(w += z.dots);
+    a.Ht = (float*)(w += z.edge);
+    a.St = (float*)(w += z.H);
     return cuda_status(delta_tc_bwd_launch(z.BV, a, st));
   }
   DeltaArgs a = delta_args(d, z, tape);

@@ -18,11 +18,14 @@
 //   E = F P + N L, dc_{C-1} += sum_j beta_j k_j.H_j + gam_{C-1} <S0, dS1>,
 //   dg_t = the sum of dc_i over the steps i >= t of t's document.
 //
-// The products run on mma.sync with operands in bf16 planes: a value computed
-// in fp32 (S, Y, Z, Tm, ...) is the sum of NP planes, each the rounding of what
-// the planes before it left, and a product takes the plane pairs (i, j) with
-// i + j < NP. Two planes (bf16 storage) hold 2^-16 of a value, three (fp32
-// storage) 2^-24; the inputs q, k, v, dO of bf16 storage are one exact plane.
+// This file has what the kernels of fp32 storage need (delta_fwd.cu, delta_bwd.cu);
+// those of bf16 storage are in delta_tc*.
+//
+// fp32: the products run on mma.sync with operands in NP = 3 bf16 planes: a value
+// is the sum of its planes, each the rounding of what the planes before it left
+// (2^-24 of the value remain), and a product takes the plane pairs (i, j) with
+// i + j < NP: six products instead of one. Three planes of every operand leave
+// shared memory for chunks of 32 steps and tiles of 32 columns of v.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,12 +38,7 @@ namespace rnn {
 
 typedef __nv_bfloat16 bf16;
 
-// Per storage type: planes of a computed value (NP) and of an input (NI), and
-// steps of a chunk (C). fp32: six products instead of one and three planes of
-// every operand, so half the chunk for the same shared memory.
-template <typename T> struct DeltaCfg;
-template <> struct DeltaCfg<bf16> { static constexpr int NP = 2, NI = 1, C = 64; };
-template <> struct DeltaCfg<float> { static constexpr int NP = 3, NI = 3, C = 32; };
+constexpr int F32_NP = 3, F32_C = 32, F32_BV = 32;  // planes, steps of a chunk, columns of a tile of v
 
 // per-step values of a chunk that delta_prep leaves for the other kernels
 enum { REC_CHI = 0, REC_CLO, REC_SEG, REC_GAM, REC_RHO, REC_BETA, REC_BR, REC_N };
@@ -96,14 +94,13 @@ __device__ __forceinline__ Opnd opnd(const bf16* p, int ld, int plane) { return 
 
 // acc[NT] (16 x 8 NT) += A(m0.., :) B(:, n0..) over K (a multiple of 16).
 // A(m, k) is stored [m][k] (AT: [k][m]); B(k, n) is stored [k][n] (BK: [n][k]).
-// PA, PB: planes; the pairs (i, j) with i + j < max(PA, PB) are summed. The
-// tensor cores cut an accumulator off at each addition, always towards zero
+// The tensor cores cut an accumulator off at each addition, always towards zero
 // (2^-23 of it), so the large products (0, 0) have an accumulator to themselves
 // and the sum so far joins by a rounded addition: 24 additions of six products
 // into the running state were 7e-6 off after a few chunks of fp32.
-template <int NT, int PA, int PB, bool AT, bool BK>
+template <int NT, bool AT, bool BK>
 __device__ __forceinline__ void mma_acc(float (&acc)[NT][4], const Opnd& A, int m0, const Opnd& B, int n0, int K) {
-  constexpr int PT = PA > PB ? PA : PB;
+  constexpr int NP = F32_NP;
   const int lane = threadIdx.x & 31, id = lane >> 3, r = lane & 7;
   const int arow = AT ? (id >> 1) * 8 + r : (id & 1) * 8 + r, acol = AT ? (id & 1) * 8 : (id >> 1) * 8;
   uint32_t aat = A.at + 2u * (uint32_t)(AT ? arow * A.ld + m0 + acol : (m0 + arow) * A.ld + acol);
@@ -111,51 +108,35 @@ __device__ __forceinline__ void mma_acc(float (&acc)[NT][4], const Opnd& A, int 
   const int kofs = (id & 1) * 8, nofs = (id >> 1) * 8;
   uint32_t bat = B.at + 2u * (uint32_t)(BK ? (n0 + nofs + r) * B.ld + kofs : (kofs + r) * B.ld + n0 + nofs);
   const uint32_t bstep = BK ? 32u : 32u * B.ld, bpair = BK ? 32u * B.ld : 32u;
-  float hi[NT][4], lo[PT > 1 ? NT : 1][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      hi[t][e] = 0.0f;
-      if constexpr (PT > 1) lo[t][e] = 0.0f;
-    }
+  float hi[NT][4] = {}, lo[NT][4] = {};
 #pragma unroll 2
   for (int k = 0; k < K; k += 16, aat += astep, bat += bstep) {
-    uint32_t a[PA][4];
+    uint32_t a[NP][4];
 #pragma unroll
-    for (int p = 0; p < PA; ++p) ldsm4<AT>(aat + 2u * p * A.plane, a[p]);
+    for (int p = 0; p < NP; ++p) ldsm4<AT>(aat + 2u * p * A.plane, a[p]);
 #pragma unroll
     for (int j = 0; j < (NT + 1) / 2; ++j) {
-      uint32_t b[PB][4];
+      uint32_t b[NP][4];
 #pragma unroll
-      for (int p = 0; p < PB; ++p) {
+      for (int p = 0; p < NP; ++p) {
         if (2 * j + 1 < NT) ldsm4<!BK>(bat + j * bpair + 2u * p * B.plane, b[p]);
         else ldsm2<!BK>(bat + j * bpair + 2u * p * B.plane, b[p]);
       }
       // the small products first
 #pragma unroll
-      for (int s = PT - 1; s >= 0; --s)
+      for (int s = NP - 1; s >= 0; --s)
 #pragma unroll
-        for (int pa = 0; pa < PA; ++pa) {
-          const int pb = s - pa;
-          if (pb < 0 || pb >= PB) continue;
-          if constexpr (PT > 1) {
-            mma_bf16_16816(s ? lo[2 * j] : hi[2 * j], a[pa], b[pb][0], b[pb][1]);
-            if (2 * j + 1 < NT) mma_bf16_16816(s ? lo[2 * j + 1] : hi[2 * j + 1], a[pa], b[pb][2], b[pb][3]);
-          } else {
-            mma_bf16_16816(hi[2 * j], a[pa], b[pb][0], b[pb][1]);
-            if (2 * j + 1 < NT) mma_bf16_16816(hi[2 * j + 1], a[pa], b[pb][2], b[pb][3]);
-          }
+        for (int pa = 0; pa <= s; ++pa) {
+          const uint32_t* w = b[s - pa];
+          mma_bf16_16816(s ? lo[2 * j] : hi[2 * j], a[pa], w[0], w[1]);
+          if (2 * j + 1 < NT) mma_bf16_16816(s ? lo[2 * j + 1] : hi[2 * j + 1], a[pa], w[2], w[3]);
         }
     }
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (PT > 1) acc[t][e] += hi[t][e] + lo[t][e];
-      else acc[t][e] += hi[t][e];
-    }
+    for (int e = 0; e < 4; ++e) acc[t][e] += hi[t][e] + lo[t][e];
 }
 template <int NT> __device__ __forceinline__ void zero(float (&acc)[NT][4]) {
 #pragma unroll
@@ -164,31 +145,31 @@ template <int NT> __device__ __forceinline__ void zero(float (&acc)[NT][4]) {
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 }
 
-// x0, x1 as NP planes, written to p (+ plane, ...) as pairs
-template <int NP> __device__ __forceinline__ void split_store(bf16* p, int plane, float x0, float x1) {
+// x0, x1 as planes, written to p (+ plane, ...) as pairs
+__device__ __forceinline__ void split_store(bf16* p, int plane, float x0, float x1) {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
+  for (int i = 0; i < F32_NP; ++i) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
     *(__nv_bfloat162*)(p + (size_t)i * plane) = h;
-    if (i + 1 < NP) {
+    if (i + 1 < F32_NP) {
       x0 -= __bfloat162float(h.x);
       x1 -= __bfloat162float(h.y);
     }
   }
 }
-// one value as NP planes
-template <int NP> __device__ __forceinline__ void split_store1(bf16* p, int plane, float x) {
+// one value as planes
+__device__ __forceinline__ void split_store1(bf16* p, int plane, float x) {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
+  for (int i = 0; i < F32_NP; ++i) {
     const bf16 h = __float2bfloat16_rn(x);
     p[(size_t)i * plane] = h;
     x -= __bfloat162float(h);
   }
 }
-template <int NP> __device__ __forceinline__ float2 planes_sum(const bf16* p, int plane) {
+__device__ __forceinline__ float2 planes_sum(const bf16* p, int plane) {
   float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int i = NP - 1; i >= 0; --i) {
+  for (int i = F32_NP - 1; i >= 0; --i) {
     const __nv_bfloat162 h = *(const __nv_bfloat162*)(p + (size_t)i * plane);
     s.x += __bfloat162float(h.x);
     s.y += __bfloat162float(h.y);
@@ -216,7 +197,7 @@ __device__ __forceinline__ void cp_tile(bf16* dst, int ld, const bf16* src, int 
 }
 
 // The C rows of a chunk of an input [.., D] (rows `stride` elements apart), the
-// columns c0 .. c0 + cols, into NI planes; rows from `live` on and columns past D
+// columns c0 .. c0 + cols, into planes (bf16: one); rows from `live` on and columns past D
 // are zero and not read. bf16 rows of whole 16-byte vectors arrive by
 // asynchronous copies, others and fp32 at once.
 template <typename T, int C>
@@ -254,7 +235,7 @@ __device__ __forceinline__ void load_rows(bf16* dst, int ld, int plane, const T*
         if (c0 + c < D) x0 = p[0];
         if (c0 + c + 1 < D) x1 = p[1];
       }
-      split_store<3>(dst + r * ld + c, plane, x0, x1);
+      split_store(dst + r * ld + c, plane, x0, x1);
     }
   }
 }

@@ -10,8 +10,9 @@ namespace rnn {
 // of v, and segments (delta_tc.cuh). A CTA an SM, so the time is the number of
 // rounds that the CTAs take times the chunks of a segment; segments cost the pass
 // of maps (the identity's tiles among them, forward) and the join. Microseconds a
-// chunk as measured: forward 4.3 (BV = 64) and 2.9 (32; 3.6 for keys past 128
-// channels), backward 5.9, 3.8 and 4.9; a join 2.6 a segment, 15 a further launch.
+// chunk as measured with all SMs taken: forward 4.8 (BV = 64) and 3.4 (32; 5.3 for
+// keys past 128 channels), backward 6.2, 4.3 and 6.3; a join 2.6 a segment, 15 a
+// further launch.
 struct DeltaLay {
   int BV, segs, seglen;
 };
@@ -20,7 +21,7 @@ inline DeltaLay delta_lay(long long heads, int Dv, int KP, long long nc, int sms
   double least = 1e300;
   for (int BV = 64; BV >= 32; BV -= 32) {
     if (BV == 64 && (KP > 128 || Dv <= 32)) continue;
-    const double f = BV == 64 ? 4.3 : KP > 128 ? 3.6 : 2.9, w = keep ? (BV == 64 ? 5.9 : KP > 128 ? 4.9 : 3.8) : 0.0;
+    const double f = BV == 64 ? 4.8 : KP > 128 ? 5.3 : 3.4, w = keep ? (BV == 64 ? 6.2 : KP > 128 ? 6.3 : 4.3) : 0.0;
     const long long nvt = (Dv + BV - 1) / BV, ki = (KP + BV - 1) / BV;
     auto rounds = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
     for (int segs = 1; segs <= 64; ++segs) {

@@ -11,29 +11,27 @@ namespace rnn {
 namespace {
 
 // ---- chain --------------------------------------------------------------------------
-template <typename T, int BV> struct BwdChainSmem {
-  static constexpr int C = DeltaCfg<T>::C, NP = DeltaCfg<T>::NP, NI = DeltaCfg<T>::NI;
-  static __host__ __device__ int kstages(int DKP) { return sizeof(T) == 2 && DKP <= 128 ? 2 : 1; }
+struct BwdChainSmem {
+  static constexpr int C = F32_C, NP = F32_NP, BV = F32_BV;
   static __host__ __device__ size_t bytes(int DKP) {
-    return 2 * ((size_t)(kstages(DKP) + 1) * NI * C * (DKP + 8) + (size_t)2 * NP * C * (C + 8) + (size_t)NI * C * (BV + 8) +
+    return 2 * ((size_t)2 * NP * C * (DKP + 8) + (size_t)2 * NP * C * (C + 8) + (size_t)NP * C * (BV + 8) +
                 (size_t)NP * DKP * (BV + 8) + (size_t)3 * NP * C * (BV + 8)) +
            2 * 2 * C * 4;
   }
 };
 
-template <typename T, int BV, int MT>
+template <int MT>
 __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
-  constexpr int C = DeltaCfg<T>::C, NP = DeltaCfg<T>::NP, NI = DeltaCfg<T>::NI;
+  constexpr int C = F32_C, NP = F32_NP, BV = F32_BV;
   constexpr int WM = C / 16, WN = 8 / WM, NT = BV / WN / 8, NS = BV / 8, LDV = BV + 8, LDC = C + 8;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   const int DKP = a.DKP, LDK = DKP + 8, kplane = C * LDK;
-  const int KST = BwdChainSmem<T, BV>::kstages(DKP);
   bf16* Ks = (bf16*)sm_raw;
-  bf16* Qs = Ks + KST * NI * kplane;
-  bf16* Ts = Qs + NI * kplane;
+  bf16* Qs = Ks + NP * kplane;
+  bf16* Ts = Qs + NP * kplane;
   bf16* Ps = Ts + NP * C * LDC;
   bf16* Os = Ps + NP * C * LDC;          // dO
-  bf16* Ss = Os + NI * C * LDV;          // dS1
+  bf16* Ss = Os + NP * C * LDV;          // dS1
   bf16* Zs = Ss + NP * DKP * LDV;        // dZ
   bf16* Ys = Zs + NP * C * LDV;          // -gam dY
   bf16* Gs = Ys + NP * C * LDV;          // gam scale dO
@@ -44,20 +42,20 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
   const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv;
   const size_t kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk, vat = (size_t)b * a.T * vstride + (size_t)n * a.Dv;
   auto load_k = [&](int ch) {
-    load_rows<T, C>(Ks + (ch % KST) * NI * kplane, LDK, kplane, (const T*)a.k + kat + (size_t)ch * C * kstride, kstride,
+    load_rows<float, C>(Ks, LDK, kplane, (const float*)a.k + kat + (size_t)ch * C * kstride, kstride,
                     live_steps(a, b, ch, C), a.Dk, 0, DKP);
   };
   auto load_q = [&](int ch) {
-    load_rows<T, C>(Qs, LDK, kplane, (const T*)a.q + kat + (size_t)ch * C * kstride, kstride, live_steps(a, b, ch, C),
+    load_rows<float, C>(Qs, LDK, kplane, (const float*)a.q + kat + (size_t)ch * C * kstride, kstride, live_steps(a, b, ch, C),
                     a.Dk, 0, DKP);
   };
   auto load_po = [&](int ch) {
     const size_t item = (size_t)bn * a.nc + ch;
     if (a.dO) {
-      load_rows<T, C>(Os, LDV, C * LDV, (const T*)a.dO + vat + (size_t)ch * C * vstride, vstride, live_steps(a, b, ch, C),
+      load_rows<float, C>(Os, LDV, C * LDV, (const float*)a.dO + vat + (size_t)ch * C * vstride, vstride, live_steps(a, b, ch, C),
                       a.Dv, vt * BV, BV);
     } else {
-      for (int i = tid; i < NI * C * LDV; i += 256) Os[i] = __float2bfloat16_rn(0.0f);
+      for (int i = tid; i < NP * C * LDV; i += 256) Os[i] = __float2bfloat16_rn(0.0f);
     }
     cp_tile(Ps, LDC, a.pm + item * NP * C * C, C, NP * C, C);
     const float* r = a.rec + item * REC_N * C;
@@ -85,7 +83,7 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
       for (int t = 0; t < NS; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          split_store<NP>(Ss + (r + (lane >> 2) + 8 * h) * LDV + t * 8 + (lane & 3) * 2, DKP * LDV, S[mt][t][2 * h],
+          split_store(Ss + (r + (lane >> 2) + 8 * h) * LDV + t * 8 + (lane & 3) * 2, DKP * LDV, S[mt][t][2 * h],
                           S[mt][t][2 * h + 1]);
     }
   };
@@ -106,15 +104,13 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
     const bool more = ch > 0;
     cp_wait<1>();  // all but q
     __syncthreads();
-    if (KST == 2 && more) load_k(ch - 1);
-    cp_commit();
-    const Opnd K = opnd(Ks + (ch % KST) * NI * kplane, LDK, kplane);
+    const Opnd K = opnd(Ks, LDK, kplane);
     const float *gam = recs + (ch & 1) * 2 * C, *br = gam + C;
     float acc[NT][4], acc2[NT][4];
     zero(acc);
     zero(acc2);
-    mma_acc<NT, NP, NI, true, false>(acc, P, m0, O, n0, C);
-    mma_acc<NT, NI, NP, false, false>(acc2, K, m0, So, n0, DKP);
+    mma_acc<NT, true, false>(acc, P, m0, O, n0, C);
+    mma_acc<NT, false, false>(acc2, K, m0, So, n0, DKP);
     {
       bf16* d = a.dS + tile * NP * DKP * BV;
       for (int i = tid; i < NP * DKP * (BV / 8); i += 256) {
@@ -134,19 +130,19 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
           x += bi * acc2[t][2 * h];
           y += bi * acc2[t][2 * h + 1];
         }
-        split_store<NP>(Zs + i * LDV + c, C * LDV, x, y);
-        const float2 d = planes_sum<NI>(Os + i * LDV + c, C * LDV);
-        split_store<NP>(Gs + i * LDV + c, C * LDV, gi * d.x, gi * d.y);
+        split_store(Zs + i * LDV + c, C * LDV, x, y);
+        const float2 d = planes_sum(Os + i * LDV + c, C * LDV);
+        split_store(Gs + i * LDV + c, C * LDV, gi * d.x, gi * d.y);
       }
     }
     __syncthreads();
     if (more) load_po(ch - 1);
     cp_commit();
     zero(acc);
-    mma_acc<NT, NP, NP, true, false>(acc, Tm, m0, Zo, n0, C);
+    mma_acc<NT, true, false>(acc, Tm, m0, Zo, n0, C);
     {
       bf16* y = a.dY + tile * NP * C * BV;
-      T* dv = a.dv ? (T*)a.dv + vat + (size_t)ch * C * vstride + vt * BV : nullptr;
+      float* dv = a.dv ? (float*)a.dv + vat + (size_t)ch * C * vstride + vt * BV : nullptr;
       const int steps = min(C, a.T - ch * C), cols = a.Dv - vt * BV;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -156,24 +152,21 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
         for (int t = 0; t < NT; ++t) {
           const int c = n0 + t * 8 + (lane & 3) * 2;
           const float x0 = acc[t][2 * h], x1 = acc[t][2 * h + 1];
-          split_store<NP>(y + i * BV + c, C * BV, x0, x1);
-          split_store<NP>(Ys + i * LDV + c, C * LDV, gi * x0, gi * x1);
+          split_store(y + i * BV + c, C * BV, x0, x1);
+          split_store(Ys + i * LDV + c, C * LDV, gi * x0, gi * x1);
           if (dv && i < steps) {
-            T* p = dv + (size_t)i * vstride + c;
+            float* p = dv + (size_t)i * vstride + c;
             if (a.Dv % 2 == 0) {
-              if (c < cols) {
-                if constexpr (sizeof(T) == 2) *(__nv_bfloat162*)p = __floats2bfloat162_rn(x0, x1);
-                else *(float2*)p = make_float2(x0, x1);
-              }
+              if (c < cols) *(float2*)p = make_float2(x0, x1);
             } else {
-              if (c < cols) p[0] = from_f<T>(x0);
-              if (c + 1 < cols) p[1] = from_f<T>(x1);
+              if (c < cols) p[0] = x0;
+              if (c + 1 < cols) p[1] = x1;
             }
           }
         }
       }
     }
-    cp_wait<2>();  // q
+    cp_wait<1>();  // q
     __syncthreads();
     if (more) load_t(ch - 1);
     cp_commit();
@@ -186,16 +179,14 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
       for (int t = 0; t < NS; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[mt][t][e] = gC != 0.0f ? gC * S[mt][t][e] : 0.0f;
-      mma_acc<NS, NI, NP, true, false>(S[mt], Q, r, Go, 0, C);
-      mma_acc<NS, NI, NP, true, false>(S[mt], K, r, Yo, 0, C);
+      mma_acc<NS, true, false>(S[mt], Q, r, Go, 0, C);
+      mma_acc<NS, true, false>(S[mt], K, r, Yo, 0, C);
     }
     if (more) {
       put_state();
       __syncthreads();  // q and k are done with
-      if (KST == 1) {
-        load_k(ch - 1);
-        cp_commit();
-      }
+      load_k(ch - 1);
+      cp_commit();
       load_q(ch - 1);
       cp_commit();
     }
@@ -216,26 +207,26 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
 // ---- grad ----------------------------------------------------------------------------
 constexpr int GRAD_BK = 64;  // columns of dQ and dK taken at once
 
-template <typename T, int BV> struct GradSmem {
-  static constexpr int C = DeltaCfg<T>::C, NP = DeltaCfg<T>::NP, NI = DeltaCfg<T>::NI;
+struct GradSmem {
+  static constexpr int C = F32_C, NP = F32_NP, BV = F32_BV;
   static __host__ __device__ size_t bytes(int DKP) {
-    return 2 * ((size_t)2 * NI * C * (DKP + 8) + (size_t)2 * NP * C * (C + 8) + (size_t)NI * C * (BV + 8) +
+    return 2 * ((size_t)2 * NP * C * (DKP + 8) + (size_t)2 * NP * C * (C + 8) + (size_t)NP * C * (BV + 8) +
                 (size_t)2 * NP * C * (BV + 8) + (size_t)2 * NP * GRAD_BK * (BV + 8)) +
            4 * (REC_N * C + 4 * C + 4 * C + 3 * 4 * C + 3 * C + 16);
   }
 };
 
-template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
-  constexpr int C = DeltaCfg<T>::C, NP = DeltaCfg<T>::NP, NI = DeltaCfg<T>::NI;
+__global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
+  constexpr int C = F32_C, NP = F32_NP, BV = F32_BV;
   constexpr int WM = C / 16, WN = 8 / WM, NT = C / WN / 8, NK = GRAD_BK / WN / 8, LDV = BV + 8, LDC = C + 8;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   const int DKP = a.DKP, LDK = DKP + 8, kplane = C * LDK;
   bf16* Ks = (bf16*)sm_raw;
-  bf16* Qs = Ks + NI * kplane;
-  bf16* Rs = Qs + NI * kplane;
+  bf16* Qs = Ks + NP * kplane;
+  bf16* Rs = Qs + NP * kplane;
   bf16* Ms = Rs + NP * C * LDC;  // M + M^T
   bf16* Os = Ms + NP * C * LDC;  // dO
-  bf16* Zs = Os + NI * C * LDV;
+  bf16* Zs = Os + NP * C * LDV;
   bf16* Ys = Zs + NP * C * LDV;  // dY
   bf16* Ss = Ys + NP * C * LDV;  // GRAD_BK rows of S0
   bf16* Ds = Ss + NP * GRAD_BK * LDV;  // of dS1
@@ -262,24 +253,24 @@ template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_gr
     for (int i = tid; i < steps * a.Dk; i += 256) {
       const int r = i / a.Dk, c = i % a.Dk;
       if (shared_heads) a.pq[pat + r * pstride + c] = a.pk[pat + r * pstride + c] = 0.0f;
-      else ((T*)a.dq)[kat + r * kstride + c] = ((T*)a.dk)[kat + r * kstride + c] = from_f<T>(0.0f);
+      else ((float*)a.dq)[kat + r * kstride + c] = ((float*)a.dk)[kat + r * kstride + c] = 0.0f;
     }
     for (int i = tid; i < steps * a.Dv; i += 256)
-      ((T*)a.dv)[vat + (size_t)(i / a.Dv) * vstride + i % a.Dv] = from_f<T>(0.0f);
+      ((float*)a.dv)[vat + (size_t)(i / a.Dv) * vstride + i % a.Dv] = 0.0f;
     return;
   }
   auto load_v = [&](int vt) {
     if (a.dO) {
-      load_rows<T, C>(Os, LDV, C * LDV, (const T*)a.dO + vat, vstride, live, a.Dv, vt * BV, BV);
+      load_rows<float, C>(Os, LDV, C * LDV, (const float*)a.dO + vat, vstride, live, a.Dv, vt * BV, BV);
     } else {
-      for (int i = tid; i < NI * C * LDV; i += 256) Os[i] = __float2bfloat16_rn(0.0f);
+      for (int i = tid; i < NP * C * LDV; i += 256) Os[i] = __float2bfloat16_rn(0.0f);
     }
     const size_t t = ((size_t)item * a.nvt + vt) * NP * C * BV;
     cp_tile(Zs, LDV, a.Z + t, BV, NP * C, BV);
     cp_tile(Ys, LDV, a.dY + t, BV, NP * C, BV);
   };
-  load_rows<T, C>(Ks, LDK, kplane, (const T*)a.k + kat, kstride, live, a.Dk, 0, DKP);
-  load_rows<T, C>(Qs, LDK, kplane, (const T*)a.q + kat, kstride, live, a.Dk, 0, DKP);
+  load_rows<float, C>(Ks, LDK, kplane, (const float*)a.k + kat, kstride, live, a.Dk, 0, DKP);
+  load_rows<float, C>(Qs, LDK, kplane, (const float*)a.q + kat, kstride, live, a.Dk, 0, DKP);
   for (int i = tid; i < REC_N * C / 4; i += 256) cp16(smem_u32(rec + i * 4), a.rec + (size_t)item * REC_N * C + i * 4, true);
   load_v(0);
   cp_commit();
@@ -296,8 +287,8 @@ template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_gr
     zero(qk);
     zero(f);
     zero(nn);
-    mma_acc<NT, NI, NI, false, true>(kk, K, m0, K, n0, DKP);
-    mma_acc<NT, NI, NI, false, true>(qk, Q, m0, K, n0, DKP);
+    mma_acc<NT, false, true>(kk, K, m0, K, n0, DKP);
+    mma_acc<NT, false, true>(qk, Q, m0, K, n0, DKP);
     for (int vt = 0; vt < a.nvt; ++vt) {
       if (vt) {
         __syncthreads();
@@ -306,8 +297,8 @@ template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_gr
         cp_wait<0>();
         __syncthreads();
       }
-      mma_acc<NT, NI, NP, false, true>(f, O, m0, Z, n0, BV);
-      mma_acc<NT, NP, NP, false, true>(nn, Y, m0, Z, n0, BV);
+      mma_acc<NT, false, true>(f, O, m0, Z, n0, BV);
+      mma_acc<NT, false, true>(nn, Y, m0, Z, n0, BV);
     }
     float rsum[2] = {0.0f, 0.0f}, csum[NT][2];
 #pragma unroll
@@ -332,13 +323,13 @@ template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_gr
           rsum[h] += bj * e0;
           csum[t][e] += e0;
           if (i > j) {
-            split_store1<NP>(Ms + i * LDC + j, C * LDC, nx * bj);
-            split_store1<NP>(Ms + j * LDC + i, C * LDC, nx * bj);
+            split_store1(Ms + i * LDC + j, C * LDC, nx * bj);
+            split_store1(Ms + j * LDC + i, C * LDC, nx * bj);
           } else if (i == j) {
-            split_store1<NP>(Ms + i * LDC + j, C * LDC, 0.0f);
+            split_store1(Ms + i * LDC + j, C * LDC, 0.0f);
           }
         }
-        split_store<NP>(Rs + i * LDC + n0 + t * 8 + (lane & 3) * 2, C * LDC, r[0], r[1]);
+        split_store(Rs + i * LDC + n0 + t * 8 + (lane & 3) * 2, C * LDC, r[0], r[1]);
       }
     }
 #pragma unroll
@@ -379,13 +370,13 @@ template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_gr
       cp_wait<0>();
       __syncthreads();
       if (nn0 < rows) {
-        mma_acc<NK, NI, NP, false, true>(aq, O, m0, S, nn0, BV);
-        mma_acc<NK, NP, NP, false, true>(ak, Y, m0, S, nn0, BV);
-        mma_acc<NK, NP, NP, false, true>(ah, Z, m0, D, nn0, BV);
+        mma_acc<NK, false, true>(aq, O, m0, S, nn0, BV);
+        mma_acc<NK, false, true>(ak, Y, m0, S, nn0, BV);
+        mma_acc<NK, false, true>(ah, Z, m0, D, nn0, BV);
       }
       for (int i = tid; i < rows * (BV / 2); i += 256) {
         const int at = (i / (BV / 2)) * LDV + (i % (BV / 2)) * 2;
-        const float2 x = planes_sum<NP>(Ss + at, GRAD_BK * LDV), y = planes_sum<NP>(Ds + at, GRAD_BK * LDV);
+        const float2 x = planes_sum(Ss + at, GRAD_BK * LDV), y = planes_sum(Ds + at, GRAD_BK * LDV);
         ss += x.x * y.x + x.y * y.y;
       }
     }
@@ -403,7 +394,7 @@ template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_gr
             for (int e = 0; e < 2; ++e) aq[t][2 * h + e] = dk[t][2 * h + e] = 0.0f;
             continue;
           }
-          const float2 q = planes_sum<NI>(Qs + i * LDK + c, kplane), k = planes_sum<NI>(Ks + i * LDK + c, kplane);
+          const float2 q = planes_sum(Qs + i * LDK + c, kplane), k = planes_sum(Ks + i * LDK + c, kplane);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float x = gi != 0.0f ? gi * a.scale * aq[t][2 * h + e] : 0.0f;
@@ -418,9 +409,9 @@ template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_gr
           }
         }
       }
-      mma_acc<NK, NP, NI, false, false>(aq, R, m0, K, k0 + nn0, C);
-      mma_acc<NK, NP, NI, false, false>(dk, M, m0, K, k0 + nn0, C);
-      mma_acc<NK, NP, NI, true, false>(dk, R, m0, Q, k0 + nn0, C);
+      mma_acc<NK, false, false>(aq, R, m0, K, k0 + nn0, C);
+      mma_acc<NK, false, false>(dk, M, m0, K, k0 + nn0, C);
+      mma_acc<NK, true, false>(dk, R, m0, Q, k0 + nn0, C);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = i0 + 8 * h;
@@ -436,15 +427,10 @@ template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_gr
             r[0] = y0;
             if (c + 1 < a.Dk) p[1] = x1, r[1] = y1;
           } else {
-            T *p = (T*)a.dq + kat + i * kstride + c, *r = (T*)a.dk + kat + i * kstride + c;
-            if (sizeof(T) == 2 && a.Dk % 2 == 0) {
-              *(__nv_bfloat162*)p = __floats2bfloat162_rn(x0, x1);
-              *(__nv_bfloat162*)r = __floats2bfloat162_rn(y0, y1);
-            } else {
-              p[0] = from_f<T>(x0);
-              r[0] = from_f<T>(y0);
-              if (c + 1 < a.Dk) p[1] = from_f<T>(x1), r[1] = from_f<T>(y1);
-            }
+            float *p = (float*)a.dq + kat + i * kstride + c, *r = (float*)a.dk + kat + i * kstride + c;
+            p[0] = x0;
+            r[0] = y0;
+            if (c + 1 < a.Dk) p[1] = x1, r[1] = y1;
           }
         }
       }
@@ -500,8 +486,7 @@ template <typename T, int BV> __global__ void __launch_bounds__(256, 1) delta_gr
 
 // ---- share ---------------------------------------------------------------------------
 // dq, dk [rows, Nk, Dk] = sums of pq, pk [rows, Nk, share, Dk], in the heads' order
-template <typename T>
-__global__ void __launch_bounds__(256) delta_share_kernel(const float* pq, const float* pk, T* dq, T* dk, long long n, int share,
+__global__ void __launch_bounds__(256) delta_share_kernel(const float* pq, const float* pk, float* dq, float* dk, long long n, int share,
                                                           int Dk) {
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
     const long long r = i / Dk;
@@ -511,26 +496,26 @@ __global__ void __launch_bounds__(256) delta_share_kernel(const float* pq, const
       x += pq[at + (size_t)s * Dk];
       y += pk[at + (size_t)s * Dk];
     }
-    dq[i] = from_f<T>(x);
-    dk[i] = from_f<T>(y);
+    dq[i] = x;
+    dk[i] = y;
   }
 }
 
-template <typename T, int BV> cudaError_t run(const DeltaArgs& a, cudaStream_t st) {
-  void (*chain)(DeltaArgs) = a.DKP <= 128 ? delta_bwd_chain_kernel<T, BV, 1> : delta_bwd_chain_kernel<T, BV, 2>;
-  size_t sm = BwdChainSmem<T, BV>::bytes(a.DKP);
+cudaError_t run(const DeltaArgs& a, cudaStream_t st) {
+  void (*chain)(DeltaArgs) = a.DKP <= 128 ? delta_bwd_chain_kernel<1> : delta_bwd_chain_kernel<2>;
+  size_t sm = BwdChainSmem::bytes(a.DKP);
   cudaError_t e = set_smem_attr((const void*)chain, sm);
   if (e != cudaSuccess) return e;
   chain<<<(unsigned)(a.B * a.N * a.nvt), 256, sm, st>>>(a);
   note_launch();
-  sm = GradSmem<T, BV>::bytes(a.DKP);
-  if ((e = set_smem_attr((const void*)delta_grad_kernel<T, BV>, sm)) != cudaSuccess) return e;
-  delta_grad_kernel<T, BV><<<(unsigned)((long long)a.B * a.N * a.nc), 256, sm, st>>>(a);
+  sm = GradSmem::bytes(a.DKP);
+  if ((e = set_smem_attr((const void*)delta_grad_kernel, sm)) != cudaSuccess) return e;
+  delta_grad_kernel<<<(unsigned)((long long)a.B * a.N * a.nc), 256, sm, st>>>(a);
   note_launch();
   if (a.pq) {
     const long long n = (long long)a.B * a.T * a.Nk * a.Dk;
     const long long blocks = (n + 255) / 256, most = 16LL * device_sms();
-    delta_share_kernel<T><<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(a.pq, a.pk, (T*)a.dq, (T*)a.dk, n,
+    delta_share_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(a.pq, a.pk, (float*)a.dq, (float*)a.dk, n,
                                                                                    a.N / a.Nk, a.Dk);
     note_launch();
   }
@@ -539,6 +524,6 @@ template <typename T, int BV> cudaError_t run(const DeltaArgs& a, cudaStream_t s
 
 }  // namespace
 
-cudaError_t delta_bwd_launch(const DeltaArgs& a, cudaStream_t st) { return run<float, 32>(a, st); }
+cudaError_t delta_bwd_launch(const DeltaArgs& a, cudaStream_t st) { return run(a, st); }
 
 }  // namespace rnn

@@ -10,23 +10,22 @@ namespace rnn {
 namespace {
 
 // ---- prep --------------------------------------------------------------------------
-template <typename T> struct PrepSmem {
-  static constexpr int C = DeltaCfg<T>::C, NI = DeltaCfg<T>::NI;
+struct PrepSmem {
+  static constexpr int C = F32_C, NP = F32_NP;
   static __host__ __device__ size_t bytes(int DKP) {
-    return (size_t)2 * NI * C * (DKP + 8) * 2 + (size_t)C * (C + 4) * 4 + REC_N * C * 4;
+    return (size_t)2 * NP * C * (DKP + 8) * 2 + (size_t)C * (C + 4) * 4 + REC_N * C * 4;
   }
 };
 
 // A warp takes 16 rows of K K^T and Q K^T; Tm by forward substitution, a column
 // to a thread with its values in registers.
-template <typename T>
-__global__ void __launch_bounds__(2 * DeltaCfg<T>::C) delta_prep_kernel(DeltaArgs a) {
-  constexpr int C = DeltaCfg<T>::C, NP = DeltaCfg<T>::NP, NI = DeltaCfg<T>::NI, NT = C / 8;
+__global__ void __launch_bounds__(2 * F32_C) delta_prep_kernel(DeltaArgs a) {
+  constexpr int C = F32_C, NP = F32_NP, NT = C / 8;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   const int LDK = a.DKP + 8, kplane = C * LDK;
   bf16* Ks = (bf16*)sm_raw;
-  bf16* Qs = Ks + NI * kplane;
-  float* Lf = (float*)(Qs + NI * kplane);  // [C][C + 4]
+  bf16* Qs = Ks + NP * kplane;
+  float* Lf = (float*)(Qs + NP * kplane);  // [C][C + 4]
   float* rec = Lf + C * (C + 4);           // [REC_N][C]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long item = blockIdx.x;
@@ -36,56 +35,38 @@ __global__ void __launch_bounds__(2 * DeltaCfg<T>::C) delta_prep_kernel(DeltaArg
   if (live == 0) return;
   const int nk = n / (a.N / a.Nk);
   const size_t stride = (size_t)a.Nk * a.Dk, at = ((size_t)b * a.T + (size_t)ch * C) * stride + (size_t)nk * a.Dk;
-  load_rows<T, C>(Ks, LDK, kplane, (const T*)a.k + at, stride, live, a.Dk, 0, a.DKP);
-  load_rows<T, C>(Qs, LDK, kplane, (const T*)a.q + at, stride, live, a.Dk, 0, a.DKP);
+  load_rows<float, C>(Ks, LDK, kplane, (const float*)a.k + at, stride, live, a.Dk, 0, a.DKP);
+  load_rows<float, C>(Qs, LDK, kplane, (const float*)a.q + at, stride, live, a.Dk, 0, a.DKP);
   cp_commit();
   if (warp == 0) {  // the running sum of g, in 64 bits, and the documents
-    double run = 0.0;
-    int seg = 0;
-    float chi[C / 32], clo[C / 32], be[C / 32];
-    int sg[C / 32];
-    double cs[C / 32];
-#pragma unroll
-    for (int h = 0; h < C / 32; ++h) {
-      const int i = h * 32 + lane;
-      float g = 0.0f;
-      bool mark = false;
-      be[h] = 0.0f;
-      if (i < live) {
-        const size_t s = ((size_t)b * a.T + (size_t)ch * C + i) * a.N + n;
-        g = a.g[s];
-        be[h] = a.beta[s];
-        mark = a.reset && a.reset[(size_t)b * a.T + (size_t)ch * C + i];
-        if (g < -104.0f) mark = true;  // exp(g) is 0
-        if (mark) g = 0.0f;
-      }
-      double c = (double)g;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, c, o);
-        if (lane >= o) c += v;
-      }
-      c += run;
-      run = __shfl_sync(0xffffffffu, c, 31);
-      const unsigned m = __ballot_sync(0xffffffffu, mark);
-      sg[h] = seg + __popc(m & (0xffffffffu >> (31 - lane)));
-      seg += __popc(m);
-      cs[h] = c;
-      chi[h] = (float)c;
-      clo[h] = (float)(c - (double)chi[h]);
+    static_assert(C == 32, "a lane a step");
+    float g = 0.0f, be = 0.0f;
+    bool mark = false;
+    if (lane < live) {
+      const size_t s = ((size_t)b * a.T + (size_t)ch * C + lane) * a.N + n;
+      g = a.g[s];
+      be = a.beta[s];
+      mark = a.reset && a.reset[(size_t)b * a.T + (size_t)ch * C + lane];
+      if (g < -104.0f) mark = true;  // exp(g) is 0
+      if (mark) g = 0.0f;
     }
+    double c = (double)g;
 #pragma unroll
-    for (int h = 0; h < C / 32; ++h) {
-      const int i = h * 32 + lane;
-      const float rho = sg[h] == seg ? expf((float)(run - cs[h])) : 0.0f;
-      rec[REC_CHI * C + i] = chi[h];
-      rec[REC_CLO * C + i] = clo[h];
-      rec[REC_SEG * C + i] = __int_as_float(sg[h]);
-      rec[REC_GAM * C + i] = sg[h] == 0 ? expf((float)cs[h]) : 0.0f;
-      rec[REC_RHO * C + i] = rho;
-      rec[REC_BETA * C + i] = be[h];
-      rec[REC_BR * C + i] = be[h] * rho;
+    for (int o = 1; o < 32; o <<= 1) {
+      const double v = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += v;
     }
+    const double all = __shfl_sync(0xffffffffu, c, 31);
+    const unsigned m = __ballot_sync(0xffffffffu, mark);
+    const int seg = __popc(m & (0xffffffffu >> (31 - lane)));
+    const float chi = (float)c, rho = seg == __popc(m) ? expf((float)(all - c)) : 0.0f;
+    rec[REC_CHI * C + lane] = chi;
+    rec[REC_CLO * C + lane] = (float)(c - (double)chi);
+    rec[REC_SEG * C + lane] = __int_as_float(seg);
+    rec[REC_GAM * C + lane] = seg == 0 ? expf(chi) : 0.0f;
+    rec[REC_RHO * C + lane] = rho;
+    rec[REC_BETA * C + lane] = be;
+    rec[REC_BR * C + lane] = be * rho;
   }
   cp_wait<0>();
   __syncthreads();
@@ -95,8 +76,8 @@ __global__ void __launch_bounds__(2 * DeltaCfg<T>::C) delta_prep_kernel(DeltaArg
   float kk[NT][4], qk[NT][4];
   zero(kk);
   zero(qk);
-  mma_acc<NT, NI, NI, false, true>(kk, K, m0, K, 0, a.DKP);
-  mma_acc<NT, NI, NI, false, true>(qk, Q, m0, K, 0, a.DKP);
+  mma_acc<NT, false, true>(kk, K, m0, K, 0, a.DKP);
+  mma_acc<NT, false, true>(qk, Q, m0, K, 0, a.DKP);
   bf16* pm = a.pm + (size_t)item * NP * C * C;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -114,7 +95,7 @@ __global__ void __launch_bounds__(2 * DeltaCfg<T>::C) delta_prep_kernel(DeltaArg
         p[e] = on ? qk[t][2 * h + e] * gb : 0.0f;
         Lf[i * (C + 4) + j] = on && i > j ? kk[t][2 * h + e] * gb : 0.0f;
       }
-      split_store<NP>(pm + i * C + t * 8 + (lane & 3) * 2, C * C, p[0], p[1]);
+      split_store(pm + i * C + t * 8 + (lane & 3) * 2, C * C, p[0], p[1]);
     }
   }
   __syncthreads();
@@ -135,33 +116,31 @@ __global__ void __launch_bounds__(2 * DeltaCfg<T>::C) delta_prep_kernel(DeltaArg
     }
     bf16* tm = a.tm + (size_t)item * NP * C * C;
 #pragma unroll
-    for (int i = 0; i < C; ++i) split_store1<NP>(tm + i * C + tid, C * C, x[i]);
+    for (int i = 0; i < C; ++i) split_store1(tm + i * C + tid, C * C, x[i]);
   }
 }
 
 // ---- chain --------------------------------------------------------------------------
-template <typename T, int BV> struct ChainSmem {
-  static constexpr int C = DeltaCfg<T>::C, NP = DeltaCfg<T>::NP, NI = DeltaCfg<T>::NI;
-  static __host__ __device__ int kstages(int DKP) { return sizeof(T) == 2 && DKP <= 128 ? 2 : 1; }
+struct ChainSmem {
+  static constexpr int C = F32_C, NP = F32_NP, BV = F32_BV;
   static __host__ __device__ size_t bytes(int DKP) {
-    return 2 * ((size_t)kstages(DKP) * NI * C * (DKP + 8) + (size_t)NP * C * (C + 8) + (size_t)NI * C * (BV + 8) +
+    return 2 * ((size_t)NP * C * (DKP + 8) + (size_t)NP * C * (C + 8) + (size_t)NP * C * (BV + 8) +
                 (size_t)NP * DKP * (BV + 8) + (size_t)2 * NP * C * (BV + 8)) +
            2 * 2 * C * 4;
   }
 };
 
 // MT: tiles of 16 state rows a warp (1 for Dk <= 128, else 2), in registers.
-template <typename T, int BV, int MT>
+template <int MT>
 __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
-  constexpr int C = DeltaCfg<T>::C, NP = DeltaCfg<T>::NP, NI = DeltaCfg<T>::NI;
+  constexpr int C = F32_C, NP = F32_NP, BV = F32_BV;
   constexpr int WM = C / 16, WN = 8 / WM, NT = BV / WN / 8, NS = BV / 8, LDV = BV + 8, LDC = C + 8;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   const int DKP = a.DKP, LDK = DKP + 8, kplane = C * LDK;
-  const int KST = ChainSmem<T, BV>::kstages(DKP);
   bf16* Ks = (bf16*)sm_raw;
-  bf16* Ts = Ks + KST * NI * kplane;
+  bf16* Ts = Ks + NP * kplane;
   bf16* Vs = Ts + NP * C * LDC;
-  bf16* Ss = Vs + NI * C * LDV;
+  bf16* Ss = Vs + NP * C * LDV;
   bf16* Ys = Ss + NP * DKP * LDV;
   bf16* Zs = Ys + NP * C * LDV;
   float* recs = (float*)(Zs + NP * C * LDV);  // [2][gam, br][C]
@@ -169,14 +148,14 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
   const int vt = blockIdx.x % a.nvt, bn = blockIdx.x / a.nvt, n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
   const int nch = live_chunks(a, b, C);
   const size_t kstride = (size_t)a.Nk * a.Dk, vstride = (size_t)a.N * a.Dv;
-  const T* kb = (const T*)a.k + (size_t)b * a.T * kstride + (size_t)nk * a.Dk;
-  const T* vb = (const T*)a.v + (size_t)b * a.T * vstride + (size_t)n * a.Dv;
+  const float* kb = (const float*)a.k + (size_t)b * a.T * kstride + (size_t)nk * a.Dk;
+  const float* vb = (const float*)a.v + (size_t)b * a.T * vstride + (size_t)n * a.Dv;
   auto load_k = [&](int ch) {
-    load_rows<T, C>(Ks + (ch % KST) * NI * kplane, LDK, kplane, kb + (size_t)ch * C * kstride, kstride,
+    load_rows<float, C>(Ks, LDK, kplane, kb + (size_t)ch * C * kstride, kstride,
                     live_steps(a, b, ch, C), a.Dk, 0, DKP);
   };
   auto load_v = [&](int ch) {
-    load_rows<T, C>(Vs, LDV, C * LDV, vb + (size_t)ch * C * vstride, vstride, live_steps(a, b, ch, C), a.Dv, vt * BV, BV);
+    load_rows<float, C>(Vs, LDV, C * LDV, vb + (size_t)ch * C * vstride, vstride, live_steps(a, b, ch, C), a.Dv, vt * BV, BV);
     const float* r = a.rec + ((size_t)bn * a.nc + ch) * REC_N * C;
     float* d = recs + (ch & 1) * 2 * C;
     if (tid < C / 4) cp16(smem_u32(d + tid * 4), r + REC_GAM * C + tid * 4, true);
@@ -205,7 +184,7 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
       for (int t = 0; t < NS; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          split_store<NP>(Ss + (r + (lane >> 2) + 8 * h) * LDV + t * 8 + (lane & 3) * 2, DKP * LDV, S[mt][t][2 * h],
+          split_store(Ss + (r + (lane >> 2) + 8 * h) * LDV + t * 8 + (lane & 3) * 2, DKP * LDV, S[mt][t][2 * h],
                           S[mt][t][2 * h + 1]);
     }
   };
@@ -223,13 +202,11 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
     const bool more = ch + 1 < nch;
     cp_wait<0>();
     __syncthreads();
-    if (KST == 2 && more) load_k(ch + 1);
-    cp_commit();
-    const Opnd K = opnd(Ks + (ch % KST) * NI * kplane, LDK, kplane);
+    const Opnd K = opnd(Ks, LDK, kplane);
     const float *gam = recs + (ch & 1) * 2 * C, *br = gam + C;
     float acc[NT][4];
     zero(acc);
-    mma_acc<NT, NI, NP, false, false>(acc, K, m0, So, n0, DKP);
+    mma_acc<NT, false, false>(acc, K, m0, So, n0, DKP);
     {  // the chunk's starting state, for the other kernels
       bf16* d = a.S + tile * NP * DKP * BV;
       for (int i = tid; i < NP * DKP * (BV / 8); i += 256) {
@@ -244,19 +221,19 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int c = n0 + t * 8 + (lane & 3) * 2;
-        float2 y = planes_sum<NI>(Vs + i * LDV + c, C * LDV);
+        float2 y = planes_sum(Vs + i * LDV + c, C * LDV);
         if (gi != 0.0f) {  // behind a reset the old state has no part, whatever it holds
           y.x -= gi * acc[t][2 * h];
           y.y -= gi * acc[t][2 * h + 1];
         }
-        split_store<NP>(Ys + i * LDV + c, C * LDV, y.x, y.y);
+        split_store(Ys + i * LDV + c, C * LDV, y.x, y.y);
       }
     }
     __syncthreads();
     if (more) load_v(ch + 1);
     cp_commit();
     zero(acc);
-    mma_acc<NT, NP, NP, false, false>(acc, Tm, m0, Yo, n0, C);
+    mma_acc<NT, false, false>(acc, Tm, m0, Yo, n0, C);
     {
       bf16* z = a.Z + tile * NP * C * BV;
 #pragma unroll
@@ -266,8 +243,8 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int c = n0 + t * 8 + (lane & 3) * 2;
-          split_store<NP>(z + i * BV + c, C * BV, acc[t][2 * h], acc[t][2 * h + 1]);
-          split_store<NP>(Zs + i * LDV + c, C * LDV, bi * acc[t][2 * h], bi * acc[t][2 * h + 1]);
+          split_store(z + i * BV + c, C * BV, acc[t][2 * h], acc[t][2 * h + 1]);
+          split_store(Zs + i * LDV + c, C * LDV, bi * acc[t][2 * h], bi * acc[t][2 * h + 1]);
         }
       }
     }
@@ -283,10 +260,10 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
       for (int t = 0; t < NS; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[mt][t][e] = gC != 0.0f ? gC * S[mt][t][e] : 0.0f;
-      mma_acc<NS, NI, NP, true, false>(S[mt], K, r, Zo, 0, C);
+      mma_acc<NS, true, false>(S[mt], K, r, Zo, 0, C);
     }
     if (more) put_state();
-    if (KST == 1 && more) {
+    if (more) {
       __syncthreads();
       load_k(ch + 1);
       cp_commit();
@@ -306,21 +283,21 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
 }
 
 // ---- out -----------------------------------------------------------------------------
-template <typename T, int BV> struct OutSmem {
-  static constexpr int C = DeltaCfg<T>::C, NP = DeltaCfg<T>::NP, NI = DeltaCfg<T>::NI;
+struct OutSmem {
+  static constexpr int C = F32_C, NP = F32_NP, BV = F32_BV;
   static __host__ __device__ size_t bytes(int DKP) {
-    return 2 * ((size_t)NI * C * (DKP + 8) + (size_t)NP * C * (C + 8) + (size_t)NP * DKP * (BV + 8) +
+    return 2 * ((size_t)NP * C * (DKP + 8) + (size_t)NP * C * (C + 8) + (size_t)NP * DKP * (BV + 8) +
                 (size_t)NP * C * (BV + 8)) + C * 4;
   }
 };
 
-template <typename T, int BV> __global__ void __launch_bounds__(256) delta_out_kernel(DeltaArgs a) {
-  constexpr int C = DeltaCfg<T>::C, NP = DeltaCfg<T>::NP, NI = DeltaCfg<T>::NI;
+__global__ void __launch_bounds__(256) delta_out_kernel(DeltaArgs a) {
+  constexpr int C = F32_C, NP = F32_NP, BV = F32_BV;
   constexpr int WM = C / 16, WN = 8 / WM, NT = BV / WN / 8, LDV = BV + 8, LDC = C + 8;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   const int DKP = a.DKP, LDK = DKP + 8;
   bf16* Qs = (bf16*)sm_raw;
-  bf16* Ps = Qs + NI * C * LDK;
+  bf16* Ps = Qs + NP * C * LDK;
   bf16* Ss = Ps + NP * C * LDC;
   bf16* Zs = Ss + NP * DKP * LDV;
   float* gam = (float*)(Zs + NP * C * LDV);
@@ -330,15 +307,15 @@ template <typename T, int BV> __global__ void __launch_bounds__(256) delta_out_k
   const int ch = (int)(item % a.nc), bn = (int)(item / a.nc), n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
   const int live = live_steps(a, b, ch, C);
   const size_t ostride = (size_t)a.N * a.Dv;
-  T* o = (T*)a.o + ((size_t)b * a.T + (size_t)ch * C) * ostride + (size_t)n * a.Dv + vt * BV;
+  float* o = (float*)a.o + ((size_t)b * a.T + (size_t)ch * C) * ostride + (size_t)n * a.Dv + vt * BV;
   const int steps = min(C, a.T - ch * C), cols = min(BV, a.Dv - vt * BV);
   if (live == 0) {
     for (int i = tid; i < steps * BV; i += 256)
-      if (i % BV < cols) o[(size_t)(i / BV) * ostride + i % BV] = from_f<T>(0.0f);
+      if (i % BV < cols) o[(size_t)(i / BV) * ostride + i % BV] = 0.0f;
     return;
   }
   const size_t qstride = (size_t)a.Nk * a.Dk;
-  load_rows<T, C>(Qs, LDK, C * LDK, (const T*)a.q + ((size_t)b * a.T + (size_t)ch * C) * qstride + (size_t)nk * a.Dk,
+  load_rows<float, C>(Qs, LDK, C * LDK, (const float*)a.q + ((size_t)b * a.T + (size_t)ch * C) * qstride + (size_t)nk * a.Dk,
                   qstride, live, a.Dk, 0, DKP);
   cp_tile(Ss, LDV, a.S + ((size_t)item * a.nvt + vt) * NP * DKP * BV, BV, NP * DKP, BV);
   if (tid < C / 4) cp16(smem_u32(gam + tid * 4), a.rec + ((size_t)item * REC_N + REC_GAM) * C + tid * 4, true);
@@ -351,7 +328,7 @@ template <typename T, int BV> __global__ void __launch_bounds__(256) delta_out_k
   const int m0 = (warp % WM) * 16, n0 = (warp / WM) * (BV / WN);
   float acc[NT][4];
   zero(acc);
-  mma_acc<NT, NI, NP, false, false>(acc, opnd(Qs, LDK, C * LDK), m0, opnd(Ss, LDV, DKP * LDV), n0, DKP);
+  mma_acc<NT, false, false>(acc, opnd(Qs, LDK, C * LDK), m0, opnd(Ss, LDV, DKP * LDV), n0, DKP);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const float gi = gam[m0 + (lane >> 2) + 8 * h];
@@ -362,7 +339,7 @@ template <typename T, int BV> __global__ void __launch_bounds__(256) delta_out_k
   }
   cp_wait<0>();
   __syncthreads();
-  mma_acc<NT, NP, NP, false, false>(acc, opnd(Ps, LDC, C * LDC), m0, opnd(Zs, LDV, C * LDV), n0, C);
+  mma_acc<NT, false, false>(acc, opnd(Ps, LDC, C * LDC), m0, opnd(Zs, LDV, C * LDV), n0, C);
   const bool pairs = a.Dv % 2 == 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -372,41 +349,38 @@ template <typename T, int BV> __global__ void __launch_bounds__(256) delta_out_k
     for (int t = 0; t < NT; ++t) {
       const int c = n0 + t * 8 + (lane & 3) * 2;
       const float x = i < live ? a.scale * acc[t][2 * h] : 0.0f, y = i < live ? a.scale * acc[t][2 * h + 1] : 0.0f;
-      T* p = o + (size_t)i * ostride + c;
+      float* p = o + (size_t)i * ostride + c;
       if (pairs) {
-        if (c < cols) {
-          if constexpr (sizeof(T) == 2) *(__nv_bfloat162*)p = __floats2bfloat162_rn(x, y);
-          else *(float2*)p = make_float2(x, y);
-        }
+        if (c < cols) *(float2*)p = make_float2(x, y);
       } else {
-        if (c < cols) p[0] = from_f<T>(x);
-        if (c + 1 < cols) p[1] = from_f<T>(y);
+        if (c < cols) p[0] = x;
+        if (c + 1 < cols) p[1] = y;
       }
     }
   }
 }
 
-template <typename T, int BV> cudaError_t run(const DeltaArgs& a, cudaStream_t st) {
+cudaError_t run(const DeltaArgs& a, cudaStream_t st) {
   const long long items = (long long)a.B * a.N * a.nc;
-  size_t sm = PrepSmem<T>::bytes(a.DKP);
-  cudaError_t e = set_smem_attr((const void*)delta_prep_kernel<T>, sm);
+  size_t sm = PrepSmem::bytes(a.DKP);
+  cudaError_t e = set_smem_attr((const void*)delta_prep_kernel, sm);
   if (e != cudaSuccess) return e;
-  delta_prep_kernel<T><<<(unsigned)items, 2 * DeltaCfg<T>::C, sm, st>>>(a);
+  delta_prep_kernel<<<(unsigned)items, 2 * F32_C, sm, st>>>(a);
   note_launch();
-  void (*chain)(DeltaArgs) = a.DKP <= 128 ? delta_chain_kernel<T, BV, 1> : delta_chain_kernel<T, BV, 2>;
-  sm = ChainSmem<T, BV>::bytes(a.DKP);
+  void (*chain)(DeltaArgs) = a.DKP <= 128 ? delta_chain_kernel<1> : delta_chain_kernel<2>;
+  sm = ChainSmem::bytes(a.DKP);
   if ((e = set_smem_attr((const void*)chain, sm)) != cudaSuccess) return e;
   chain<<<(unsigned)(a.B * a.N * a.nvt), 256, sm, st>>>(a);
   note_launch();
-  sm = OutSmem<T, BV>::bytes(a.DKP);
-  if ((e = set_smem_attr((const void*)delta_out_kernel<T, BV>, sm)) != cudaSuccess) return e;
-  delta_out_kernel<T, BV><<<(unsigned)(items * a.nvt), 256, sm, st>>>(a);
+  sm = OutSmem::bytes(a.DKP);
+  if ((e = set_smem_attr((const void*)delta_out_kernel, sm)) != cudaSuccess) return e;
+  delta_out_kernel<<<(unsigned)(items * a.nvt), 256, sm, st>>>(a);
   note_launch();
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t delta_fwd_launch(const DeltaArgs& a, cudaStream_t st) { return run<float, 32>(a, st); }
+cudaError_t delta_fwd_launch(const DeltaArgs& a, cudaStream_t st) { return run(a, st); }
 
 }  // namespace rnn

@@ -25,8 +25,11 @@
 // with i + j < 3 summed, those of equal i + j in an accumulator of their own
 // (delta.cuh says why). An operand's planes are one operand of three times the
 // columns: the other operand is read once for all three (a 128 x 64 x 16 product
-// reads 6 KB of shared memory in the time it multiplies 4 KB). dQ and dK, bf16 themselves, are taken from operands rounded to bf16
-// once (dY, Z, S0, dS1, M, R).
+// reads 6 KB of shared memory in the time it multiplies 4 KB). dQ and dK, bf16
+// themselves, are taken from operands in two planes (dY, Z, S0, dS1, M, R: 2^-18 of
+// a value remain), without the product of two second planes. One plane would put
+// four more roundings beside the result's own: 3e-3 to 4.4e-3 off (2-norm) instead
+// of 1.7e-3.
 //
 // Shared-memory images are rows of 128 bytes (64 columns; 64 bytes where a tile
 // of v has 32), 16-byte pieces swizzled as the tensor cores read them, panels of
@@ -64,13 +67,14 @@ struct DeltaTcArgs {
   float* rec;  // [items][REC_N][64]
   bf16* tp;    // [items][3][128 x 64 image]
   // what a backward needs besides (null: none comes)
-  bf16 *Sh, *Zh;       // [items][nvt][KP x BV image] of S0, [items][nvt][64 x BV image] of Z
-  float *zf, *of;      // [items][nvt][...] z and o in fp32, as the threads hold them
+  bf16* Sh;            // [items][nvt][2][KP x BV image] two planes of S0
+  float *zf, *of;      // [items][nvt][BV / 4][64][4] z and o in fp32, as the threads hold them
   float* sf;           // [B N][ne][nvt][...] S at the end (0) and at every TC_EDGE-th chunk's start
   // backward
   const void* dO;
   const float* dlast;
   bf16* dSh;           // as Sh, of dS1
+  bf16* dYl;           // [items][nvt][BV / 8][64][8] the second plane of dY (the first is dv)
   float* dots;         // [items][nvt][3][2][64]: z.dY, -v.dY, o.dO of half a tile's columns
   float* edge;         // [B N][ne][nvt][8]: <S, dS> there, by warp
   void *dq, *dk, *dv;
@@ -136,6 +140,14 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// the same, lanes 64 .. 127 of the accumulator left as they are
+__device__ __forceinline__ void tc_mma_upper(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %6, %6}, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(0u), "r"(0xffffffffu)
       : "memory");
 }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -290,20 +302,6 @@ __device__ __forceinline__ void tc_wide(int panels, uint32_t d, uint32_t a, uint
   } else {
     if (panels == 3) tc_panels<RB, 3>(d, a, b, plane, id);
     else tc_panels<RB, 4>(d, a, b, plane, id);
-  }
-}
-
-// N values of a row of a tensor whose rows have D - c valid columns from p on
-template <int N> __device__ __forceinline__ void store_row(bf16* p, const float (&x)[N], int valid, bool vec) {
-#pragma unroll
-  for (int c = 0; c < N; c += 8) {
-    if (vec) {
-      if (c < valid) *(uint4*)(p + c) = round8(x + c);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < valid) p[c + e] = __float2bfloat16_rn(x[c + e]);
-    }
   }
 }
 

@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
           tc_commit(bar);
           if (KST == 2 && a.tma && ch > ch0) load_kq(ch - 1);
           if (!a.maps) {
-            // the gradient of the chunk's last state, rounded: its first plane
-            store_bulk(a.dSh + tile * a.KP * BV, SS, a.KP * RB);
+            // the gradient of the chunk's last state: its first two planes
+            for (int k = 0; k < 2; ++k) store_bulk(a.dSh + (tile * 2 + k) * a.KP * BV, SS + k * L::SPLANE, a.KP * RB);
             bulk_commit_group();
             if (a.tma) {
               bulk_wait_group_read<1>();  // dY has left V's image
@@ -341,12 +341,16 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
       leave();  // 3: -gam dY's planes are there, dO is read, V is there
       if (quad < 2 && !a.maps) {  // what leaves for memory goes while the product runs
         float zy = 0.0f, vy = 0.0f;
+        uint4* low = (uint4*)(a.dYl + tile * 64 * BV) + (size_t)half * (NC / 8) * 64 + i;
 #pragma unroll
         for (int c = 0; c < NC; c += 8) {
           uint4* at = (uint4*)(VS + img<RB>(i, (c0 + c) >> 3));
+          uint4 p[3];
           float v[8];
           widen8(*at, v);
-          *at = round8(y + c);
+          split8(y + c, p);
+          *at = p[0];
+          low[(c / 8) * 64] = p[1];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             zy = fmaf(kept[c + e], y[c + e], zy);
@@ -400,30 +404,35 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
 // TMEM: two accumulators of KT columns; the second one's hold N and F before.
 template <int KT, int BV> struct TcGrad {  // KT: Dk rounded up to 128 or 256
   static constexpr int RB = 2 * BV;
-  static constexpr int KQ = KT / 64 * TC_PANEL, SB = KT * RB;  // bytes of KQ and of a tile of S0
-  static constexpr int XB = 128 * RB, XZ = XB + 64 * RB;       // a tile of X = [dY; dO], and of it and Z
-  static constexpr int STAGES = KT == 128 && BV == 64 ? 1 : 2;  // tiles of S0 and dS1 at once; one where two CTAs an SM fit then
+  static constexpr int KQ = KT / 64 * TC_PANEL, SB = KT * RB;  // bytes of KQ and of a plane of a tile of S0
+  // a tile of X = [dY; dO], of Z's two planes and of dY's second
+  static constexpr int AT_Z = 128 * RB, AT_L = AT_Z + 128 * RB, XZ = AT_L + 64 * RB;
+  // planes of tiles of S0 and dS1 at once; one where two CTAs an SM fit then
+  static constexpr int STAGES = KT == 128 && BV == 64 ? 1 : 2;
   static constexpr int SD = STAGES * 2 * SB > 2 * TC_PANEL ? STAGES * 2 * SB : 2 * TC_PANEL;
-  static __host__ __device__ int at_sd(int nvt) { return (nvt * XZ > KQ ? nvt * XZ : KQ) + 1023 & ~1023; }
-  static __host__ __device__ size_t bytes(int nvt) { return (size_t)at_sd(nvt) + SD + 6 * TC_C * 4 + 64 + 1024; }
+  static __host__ __device__ constexpr int at_sd(int nvt) { return nvt * XZ > KQ + 2 * TC_PANEL ? nvt * XZ : KQ + 2 * TC_PANEL; }
+  static __host__ __device__ constexpr size_t bytes(int nvt) { return (size_t)at_sd(nvt) + SD + 3 * TC_C * 4 + TC_C + 64; }
   static constexpr int COLS = KT == 128 ? 256 : 512;
 };
+static_assert(2 * (TcGrad<128, 64>::bytes(2) + 1024) <= 228 * 1024, "two CTAs an SM for heads of 128 channels");
+static_assert(TcGrad<128, 64>::bytes(4) <= 227 * 1024 && TcGrad<128, 32>::bytes(8) <= 227 * 1024 && TcGrad<256, 32>::bytes(8) <= 227 * 1024, "fits");
 
-// X and Z stay in shared memory, S0 and dS1 pass by tiles of BV columns of v. N
-// and F go to registers, M and R are made from them while the state's products
-// run, and multiply KQ from the buffers of S0 and dS1, KQ in X's and Z's. The
-// product of Z's 64 rows reads as many rows behind them, whose results are not
-// looked at.
+// X and Z stay in shared memory, S0 and dS1 pass by planes of tiles of BV columns
+// of v. N and F go to registers, M and R are made from them while the state's
+// products run, and multiply KQ: their first planes from the buffers of S0 and
+// dS1, their second from behind KQ, which has X's and Z's place. The products of
+// 64 rows (Z's, dY's second plane) read as many rows behind them: Z's results
+// there are not looked at, dY's are not written, since dO's stand there.
 template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delta_tc_grad_kernel(DeltaTcArgs a) {
   using L = TcGrad<KT, BV>;
   constexpr int RB = L::RB;
-  extern __shared__ unsigned char sm_raw[];
-  unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
-  unsigned char *X = sm, *KQ = sm, *SD = sm + L::at_sd(a.nvt);
-  float* rec = (float*)(SD + L::SD);  // chi, clo, seg, gam, br, beta
-  const float* beta = rec + 5 * TC_C;
-  uint64_t* barp = (uint64_t*)(rec + 6 * TC_C);
-  uint32_t* slot = (uint32_t*)(barp + 6);
+  extern __shared__ __align__(1024) unsigned char sm_grad[];
+  unsigned char *X = sm_grad, *KQ = sm_grad, *SD = sm_grad + L::at_sd(a.nvt), *ML = KQ + L::KQ;
+  float* rec = (float*)(SD + L::SD);  // chi, clo, beta
+  const float* beta = rec + 2 * TC_C;
+  unsigned char* segs = (unsigned char*)(rec + 3 * TC_C);
+  uint64_t* barp = (uint64_t*)(segs + TC_C);
+  uint32_t* slot = (uint32_t*)(barp + 5);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
   const long long item = blockIdx.x;
   const int ch = (int)(item % a.nc), bn = (int)(item / a.nc), n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
@@ -440,16 +449,13 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     }
     return;
   }
-  const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_z = bar + 16, bar_s = bar + 24, bar_m = bar + 40;  // bar_s: by stage
+  const uint32_t bar = smem_u32(barp), bar_end = bar + 8, bar_s = bar + 16, bar_m = bar + 32;  // bar_s: by stage
   if (tid == 0) {
-    for (int k = 0; k < 6; ++k) mbar_init(bar + 8 * k, 1);
+    for (int k = 0; k < 5; ++k) mbar_init(bar + 8 * k, 1);
     fence_mbar_init_cluster();
-    const bf16* z = a.Zh + (size_t)item * a.nvt * 64 * BV;
-    mbar_arrive_expect_tx(bar_z, a.nvt * 64 * RB);
-    for (int p = 0; p < a.nvt; ++p) bulk_load_global(smem_u32(X + p * L::XZ + L::XB), z + (size_t)p * 64 * BV, 64 * RB, bar_z);
   }
-  auto load_sd = [&](int p) {  // one thread
-    const size_t at = ((size_t)item * a.nvt + p) * a.KP * BV;
+  auto load_sd = [&](int p) {  // plane p % 2 of tile p / 2; one thread
+    const size_t at = ((size_t)item * a.nvt * 2 + p) * a.KP * BV;
     const uint32_t bytes = a.KP * RB, to = smem_u32(SD + (p % L::STAGES) * 2 * L::SB), br = bar_s + 8 * (p % L::STAGES);
     mbar_arrive_expect_tx(br, 2 * bytes);
     bulk_load_global(to, a.Sh + at, bytes, br);
@@ -457,22 +463,32 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
   };
   if (tid == 0) {
     load_sd(0);
-    if (L::STAGES == 2 && a.nvt > 1) load_sd(1);
+    if (L::STAGES == 2) load_sd(1);
   }
   for (int p = 0; p < a.nvt; ++p) {
     unsigned char* x = X + p * L::XZ;
     load_img<RB, BV / 8, 256>(tid, x, 0, (const bf16*)a.dv + vat, vstride, live, a.Dv, p * BV, BV, 0);
     load_img<RB, BV / 8, 256>(tid, x, 64, (const bf16*)(a.dO ? a.dO : a.dv) + vat, vstride, a.dO ? live : 0, a.Dv, p * BV, BV, 0);
+    const size_t tile = (size_t)item * a.nvt + p;
+    for (int k = tid; k < 64 * (BV / 8); k += 256) {  // 8 columns of a step
+      const int r = k & 63, c = k >> 6;
+      cp16(smem_u32(x + L::AT_L) + img<RB>(r, c), a.dYl + (tile * 64 * (BV / 8) + k) * 8, r < live);
+      const float4* z = (const float4*)(a.zf + tile * 64 * BV) + (size_t)c * 128 + r;
+      const float4 z0 = __ldcs(z), z1 = __ldcs(z + 64);
+      const float zs[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+      uint4 q[3];
+      split8(zs, q);
+      *(uint4*)(x + L::AT_Z + img<RB>(r, c)) = q[0];
+      *(uint4*)(x + L::AT_Z + 64 * RB + img<RB>(r, c)) = q[1];
+    }
   }
   cp_commit();
+  const float* own = a.rec + (size_t)item * REC_N * TC_C;
   if (tid < TC_C) {
-    const float* r = a.rec + (size_t)item * REC_N * TC_C + tid;
-    rec[tid] = r[REC_CHI * TC_C];
-    rec[TC_C + tid] = r[REC_CLO * TC_C];
-    rec[2 * TC_C + tid] = r[REC_SEG * TC_C];
-    rec[3 * TC_C + tid] = r[REC_GAM * TC_C];
-    rec[4 * TC_C + tid] = r[REC_BR * TC_C];
-    rec[5 * TC_C + tid] = r[REC_BETA * TC_C];
+    rec[tid] = own[REC_CHI * TC_C + tid];
+    rec[TC_C + tid] = own[REC_CLO * TC_C + tid];
+    rec[2 * TC_C + tid] = own[REC_BETA * TC_C + tid];
+    segs[tid] = (unsigned char)__float_as_int(own[REC_SEG * TC_C + tid]);  // 0 .. 64
   }
   {  // K and Q, which come last, on their way to the L2
     const bf16* s = (const bf16*)(tid < 128 ? a.k : a.q) + kat + (size_t)((tid & 127) >> 1) * kstride;
@@ -494,30 +510,38 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     parity ^= 1;
     tm_fence_after();
   };
-  // the state's products of tile p
+  constexpr uint64_t XZ = L::AT_Z >> 4, XL = L::AT_L >> 4, PZ = 64 * RB >> 4;  // in descriptors: Z, dY's second plane, from plane to plane of Z
+  // the state's products with plane p % 2 of tile p / 2
   auto state = [&](int p) {
     wait(bar_s + 8 * (p % L::STAGES), (p / L::STAGES) & 1);
     if (failed) return;
     const uint32_t id = tc_idesc(a.KP, false, false);
-    const uint64_t x = tc_desc<RB>(smem_u32(X) + p * L::XZ, 16), s = tc_desc<RB>(smem_u32(SD) + (p % L::STAGES) * 2 * L::SB, 16);
+    const uint64_t x = tc_desc<RB>(smem_u32(X) + (p >> 1) * L::XZ, 16), s = tc_desc<RB>(smem_u32(SD) + (p % L::STAGES) * 2 * L::SB, 16);
+    const uint64_t ds = s + (L::SB >> 4);
 #pragma unroll
     for (int k = 0; k < BV / 16; ++k) tc_mma(tm, x + 2 * k, s + 2 * k, id, p || k);  // [dY; dO] S0^T
 #pragma unroll
-    for (int k = 0; k < BV / 16; ++k)  // Z dS1^T (rows 0 .. 63)
-      tc_mma(tm + KT, x + (L::XB >> 4) + 2 * k, s + (L::SB >> 4) + 2 * k, id, p || k);
-    tc_commit(p + 1 < a.nvt ? bar_m : bar);  // the CTA waits for the last tile's alone
+    for (int k = 0; k < BV / 16; ++k) tc_mma(tm + KT, x + XZ + 2 * k, ds + 2 * k, id, p || k);  // Z dS1^T (rows 0 .. 63)
+    if (!(p & 1)) {
+#pragma unroll
+      for (int k = 0; k < BV / 16; ++k) tc_mma_upper(tm, x + XL + 2 * k, s + 2 * k, id, true);
+#pragma unroll
+      for (int k = 0; k < BV / 16; ++k) tc_mma(tm + KT, x + XZ + PZ + 2 * k, ds + 2 * k, id, true);
+    }
+    tc_commit(p + 1 < 2 * a.nvt ? bar_m : bar);  // the CTA waits for the last tile's alone
   };
   if (tid == 0) {  // [N; F] = X Z^T, in the second accumulator's columns
-    wait(bar_z, 0);
     constexpr uint32_t id = tc_idesc(64, false, false);
-    if (!failed) {
-      for (int p = 0; p < a.nvt; ++p) {
-        const uint64_t x = tc_desc<RB>(smem_u32(X) + p * L::XZ, 16);
+    for (int p = 0; p < a.nvt; ++p) {
+      const uint64_t x = tc_desc<RB>(smem_u32(X) + p * L::XZ, 16);
 #pragma unroll
-        for (int k = 0; k < BV / 16; ++k) tc_mma(tm + KT, x + 2 * k, x + (L::XB >> 4) + 2 * k, id, p || k);
-      }
-      tc_commit(bar);
+      for (int k = 0; k < BV / 16; ++k) tc_mma(tm + KT, x + 2 * k, x + XZ + 2 * k, id, p || k);
+#pragma unroll
+      for (int k = 0; k < BV / 16; ++k) tc_mma(tm + KT, x + 2 * k, x + XZ + PZ + 2 * k, id, true);
+#pragma unroll
+      for (int k = 0; k < BV / 16; ++k) tc_mma_upper(tm + KT, x + XL + 2 * k, x + XZ + 2 * k, id, true);
     }
+    tc_commit(bar);
   }
   const int i = (quad & 1) * 32 + lane, j0 = half * 32;
   take();
@@ -538,19 +562,19 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
   }
   {  // R_ij (Q's steps) or M_ij (K's), i the thread's step
     const float ci = rec[i], li = rec[TC_C + i];
-    const int si = __float_as_int(rec[2 * TC_C + i]);
+    const int si = segs[i];
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
       const int j = j0 + c;
-      const bool on = (quad < 2 ? i > j : i >= j) && si == __float_as_int(rec[2 * TC_C + j]);
+      const bool on = (quad < 2 ? i > j : i >= j) && si == segs[j];
       nf[c] = on ? (quad < 2 ? -nf[c] : a.scale * nf[c]) * exp2_fast((ci - rec[j]) + (li - rec[TC_C + j])) * beta[j] : 0.0f;
     }
   }
   if (tid == 0)
-    for (int p = 1; p < a.nvt && !failed; ++p) {
+    for (int p = 1; p < 2 * a.nvt && !failed; ++p) {
       wait(bar_m, (p - 1) & 1);  // before the next commit: the barrier's parity tells two phases apart
       if (L::STAGES == 1) load_sd(p);
-      else if (p + 1 < a.nvt) load_sd(p + 1);
+      else if (p + 1 < 2 * a.nvt) load_sd(p + 1);
       state(p);
     }
   take();
@@ -558,28 +582,37 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
   load_img<128, KT / 8, 256>(tid, KQ, 0, (const bf16*)a.k + kat, kstride, live, a.Dk, 0, (a.KP + 63) & ~63, TC_PANEL);
   load_img<128, KT / 8, 256>(tid, KQ, 64, (const bf16*)a.q + kat, kstride, live, a.Dk, 0, (a.KP + 63) & ~63, TC_PANEL);
   cp_commit();
-  // [M + M^T, R^T; R, 0] over the buffers of S0 and dS1: two panels of 128 rows
-  if (quad >= 2) {
+  // [M + M^T, R^T; R, 0], two panels of 128 rows: the first plane over the buffers
+  // of S0 and dS1, the second behind KQ
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-      *(uint4*)(SD + img<128>(64 + i, (j0 + c) >> 3)) = round8(nf + c);
-      *(uint4*)(SD + TC_PANEL + img<128>(64 + i, (j0 + c) >> 3)) = make_uint4(0, 0, 0, 0);
-    }
+  for (int k = 0; k < 2; ++k) {
+    unsigned char* to = k ? ML : SD;
+    if (quad >= 2) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-      *(bf16*)(SD + TC_PANEL + img<128>(j0 + c, i >> 3) + (i & 7) * 2) = __float2bfloat16_rn(nf[c]);
-  } else {
+      for (int c = 0; c < 32; c += 8) {
+        *(uint4*)(to + img<128>(64 + i, (j0 + c) >> 3)) = round8(nf + c);
+        *(uint4*)(to + TC_PANEL + img<128>(64 + i, (j0 + c) >> 3)) = make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const int j = j0 + c;
-      const bf16 m = __float2bfloat16_rn(nf[c]);
-      if (j <= i) *(bf16*)(SD + img<128>(i, j >> 3) + (j & 7) * 2) = m;
-      if (j < i) *(bf16*)(SD + img<128>(j, i >> 3) + (i & 7) * 2) = m;
+      for (int c = 0; c < 32; ++c) {
+        const bf16 m = __float2bfloat16_rn(nf[c]);
+        *(bf16*)(to + TC_PANEL + img<128>(j0 + c, i >> 3) + (i & 7) * 2) = m;
+        nf[c] -= __bfloat162float(m);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const int j = j0 + c;
+        const bf16 m = __float2bfloat16_rn(nf[c]);
+        if (j <= i) *(bf16*)(to + img<128>(i, j >> 3) + (j & 7) * 2) = m;
+        if (j < i) *(bf16*)(to + img<128>(j, i >> 3) + (i & 7) * 2) = m;
+        nf[c] -= __bfloat162float(m);
+      }
     }
   }
   // The state's parts, scaled by rows in fp32, back into the first accumulator
-  const float gi = rec[3 * TC_C + i];
-  const float f0 = quad < 2 ? -gi : a.scale * gi, f1 = quad < 2 ? rec[4 * TC_C + i] : 0.0f;
+  const float gi = own[REC_GAM * TC_C + i];
+  const float f0 = quad < 2 ? -gi : a.scale * gi, f1 = quad < 2 ? own[REC_BR * TC_C + i] : 0.0f;
   for (int c = half * 16; c < a.KP; c += 32) {
     uint32_t x[16], h[16];
     tm_ld16(x, row + c);
@@ -605,9 +638,11 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
   if (tid == 0 && !failed) {
     tm_fence_after();
     const uint32_t id = tc_idesc(a.KP, false, true);
-    const uint64_t m = tc_desc(smem_u32(SD), 16), k0 = tc_desc(smem_u32(KQ), TC_PANEL);
+    const uint64_t m = tc_desc(smem_u32(SD), 16), ml = tc_desc(smem_u32(ML), 16), k0 = tc_desc(smem_u32(KQ), TC_PANEL);
 #pragma unroll
     for (int k = 0; k < 8; ++k) tc_mma(tm, m + (k >> 2) * (TC_PANEL >> 4) + (k & 3) * 2, k0 + k * 128, id, true);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) tc_mma(tm, ml + (k >> 2) * (TC_PANEL >> 4) + (k & 3) * 2, k0 + k * 128, id, true);
     tc_commit(bar);
   }
   take();
@@ -643,10 +678,10 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     }
   }
   if (tid == 0 && failed) {  // copies that nobody waited for land before the CTA ends
-    for (int k = 0; k < 1 + L::STAGES; ++k)
+    for (int k = 0; k < L::STAGES; ++k)
       for (int q = 0; q < 2; ++q) {
         bool f = false;
-        mbar_wait_bounded<false>(bar_z + 8 * k, q, a.wait_limit_ns, nullptr, f);
+        mbar_wait_bounded<false>(bar_s + 8 * k, q, a.wait_limit_ns, nullptr, f);
       }
   }
   tc_finish(bar_end, a.wait_limit_ns);

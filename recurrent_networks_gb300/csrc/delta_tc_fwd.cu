@@ -2,6 +2,8 @@
 //   prep   every chunk by itself: TP and the per-step factors
 //   chain  per head and tile of BV columns of v, the chunks one after the other:
 //          o and the state, and what a backward needs
+#include <type_traits>
+
 #include "delta.h"
 #include "delta_tc.cuh"
 
@@ -237,7 +239,7 @@ template <int BV, int MT> struct TcChain {
   static constexpr int RB = 2 * BV, KST = MT == 1 ? 2 : 1;  // bytes of a tile's row; stages of KQ
   static constexpr int KQ = 2 * MT * TC_PANEL, TP = 3 * TC_PANEL, SPLANE = MT * 128 * RB, YPLANE = 64 * RB;
   static constexpr int AT_TP = KST * KQ, AT_S = AT_TP + TP, AT_Y = AT_S + 3 * SPLANE, AT_V = AT_Y + 3 * YPLANE;
-  static constexpr int AT_Z = AT_V + YPLANE, AT_O = AT_Z + YPLANE;  // rounded, on their way out
+  static constexpr int AT_O = AT_V + YPLANE;  // o, on its way out
   static constexpr int AT_REC = AT_O + YPLANE, BYTES = AT_REC + 2 * 2 * 64 * 4 + 64 + 1024;
 };
 
@@ -245,18 +247,22 @@ template <int BV, int MT> struct TcChain {
 // the accumulators (rows 0 .. 63: K's steps, 64 .. 127: Q's; or rows of the state)
 // and half of the tile's columns. Thread 256 issues the products and the bulk
 // copies of images (an issuing thread waits while earlier products run: 150
-// cycles a product) and of the tensors' rows; rows that are not whole 16-byte pieces
-// are loaded and stored by warps 10 and 11. The third warpgroup gives registers to the other two: 256 * 200 + 128 * 104 = 384 * 168.
+// cycles a product) and of the tensors' rows; rows that are not whole 16-byte
+// pieces are loaded and stored by warps 10 and 11. The third warpgroup gives
+// registers to the other two: 256 * 200 + 128 * 104 = 384 * 168.
 // MT: tiles of 128 state rows, whose fp32 values stay in registers. A chunk is
 // three dependent products (2000 cycles for BV = 64, Dk = 128) and their ways
-// through registers between barriers of the whole CTA.
+// through registers between barriers of the whole CTA, 4.5 us in all: 286 us for
+// the 64 chunks of B = 8, T = 4096, N = 8, Dk = Dv = 128, where 557 MB pass in a
+// training step (82 us). Tiles of 32 columns would double the CTAs and shorten a
+// chunk to two thirds: 1.3 times the time where all SMs are taken.
 template <int BV, int MT>
 __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, const __grid_constant__ TcMaps maps) {
   using L = TcChain<BV, MT>;
   constexpr int RB = L::RB, NC = BV / 2, KST = L::KST, P = MT * 16;
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)sm_raw + 1023) & ~(uintptr_t)1023);
-  unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *YS = sm + L::AT_Y, *VS = sm + L::AT_V, *ZS = sm + L::AT_Z, *OS = sm + L::AT_O;
+  unsigned char *TP = sm + L::AT_TP, *SS = sm + L::AT_S, *YS = sm + L::AT_Y, *VS = sm + L::AT_V, *OS = sm + L::AT_O;
   float* recs = (float*)(sm + L::AT_REC);  // [2][gam, br][64]
   uint64_t* barp = (uint64_t*)(recs + 2 * 2 * 64);
   uint32_t* slot = (uint32_t*)(barp + 4);
@@ -339,12 +345,12 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
           tc_wide<RB, MT>(panels, tm + D1, kq, smem_u32(SS), L::SPLANE, tc_idesc(3 * BV, false, true));
           tc_commit(bar);
           if (KST == 2 && a.tma && ch + 1 < ch1) load_kq(ch + 1);
-          if (a.Sh && !a.maps) {  // the chunk's starting state, rounded: its first plane
-            store_bulk(a.Sh + tile * a.KP * BV, SS, a.KP * RB);
+          if (a.Sh && !a.maps) {  // the chunk's starting state: its first two planes
+            for (int k = 0; k < 2; ++k) store_bulk(a.Sh + (tile * 2 + k) * a.KP * BV, SS + k * L::SPLANE, a.KP * RB);
             bulk_commit_group();
           }
         }
-        if (one) bulk_wait_group_read<0>();  // the state's planes and Z's and o's images may be written again
+        if (one) bulk_wait_group_read<0>();  // the state's planes and o's image may be written again
         __syncthreads();  // 2
         if (one) {
           wait(bar_tp, (ch - ch0) & 1);
@@ -374,9 +380,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
         __syncthreads();  // 4
         if (one && !failed) {
           if (KST == 1 && a.tma && ch + 1 < ch1) load_kq(ch + 1);
-          if (!a.maps) {
-            if (a.Zh) store_bulk(a.Zh + tile * 64 * BV, ZS, L::YPLANE);
-            if (a.tma) tma_store_5d(&maps.o, smem_u32(OS), vt * BV, n, ch * TC_C, b, 0);
+          if (!a.maps && a.tma) {
+            tma_store_5d(&maps.o, smem_u32(OS), vt * BV, n, ch * TC_C, b, 0);
             bulk_commit_group();
           }
         }
@@ -522,10 +527,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
       // what leaves for memory goes while the product runs
       if (a.maps) {
       } else if (quad < 2) {
-        if (a.Zh) {
+        if (a.zf) {
           float4* f = (float4*)(a.zf + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
-#pragma unroll
-          for (int c = 0; c < NC; c += 8) *(uint4*)(ZS + img<RB>(i, (c0 + c) >> 3)) = round8(z + c);
 #pragma unroll
           for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
         }
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
 #pragma unroll
         for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
       }
-      leave();  // 4: the products are over, Z's image is there
+      leave();  // 4: the products are over, o's image is there
       if (more) put_state();
       const int end = ch + 1 == nch ? 0 : (ch + 1) % TC_EDGE == 0 ? (ch + 1) / TC_EDGE : -1;
       if (a.sf && !a.maps && end >= 0) keep_state(end);
@@ -588,7 +591,9 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
 // The states between the segments, one after the other: forward S = M S + H from
 // state0, backward dS = M^T dS + H from dlast. A CTA has CW columns of v of a head,
 // S in shared memory, M by blocks of 64 KB, two of them; 4 x 4 values a thread.
-// Rows and columns of M past KP are not looked at.
+// Rows and columns of M past KP are not looked at. M is exactly zero where a reset
+// stands in its segment: then nothing of S may pass, an infinity or a NaN neither,
+// so the zeros of M are left out where S holds one.
 template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_join_kernel(DeltaTcArgs a, int cols_total) {
   constexpr int CW = KR == 128 ? 32 : 16, LD = CW + 4, JB = 16384 / KR;  // rows of Mt in a block
   extern __shared__ __align__(16) unsigned char sm_raw[];
@@ -598,10 +603,14 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
   const int tid = threadIdx.x, bn = blockIdx.x / groups, v0 = (blockIdx.x % groups) * CW;
   const int cg = tid % (CW / 4) * 4, rg = tid / (CW / 4) * 4;
   const float* x0 = BACK ? a.dlast : a.s0;
+  int odd = 0;
   for (int k = tid; k < KR * CW; k += 256) {
     const int r = k / CW, c = k % CW;
-    S[r * LD + c] = x0 && r < a.Dk && v0 + c < a.Dv ? x0[((size_t)bn * a.Dk + r) * a.Dv + v0 + c] : 0.0f;
+    const float x = x0 && r < a.Dk && v0 + c < a.Dv ? x0[((size_t)bn * a.Dk + r) * a.Dv + v0 + c] : 0.0f;
+    S[r * LD + c] = x;
+    odd |= !isfinite(x);
   }
+  odd = __syncthreads_or(odd);
   const int blocks = (a.segs - 1) * (KR / JB);
   auto load = [&](int k) {  // block k of the matrices in the order of their use
     const int s = BACK ? a.segs - 1 - k / (KR / JB) : k / (KR / JB);
@@ -624,37 +633,45 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[r][c] = 0.0f;
     const float* m = M + (k & 1) * JB * KR;
-    if constexpr (!BACK) {  // column j of M times row j of S
+    auto products = [&](auto guard) {
+      auto add = [&](float& acc, float x, float y) {
+        if (!decltype(guard)::value || x != 0.0f) acc = fmaf(x, y, acc);
+      };
+      if constexpr (!BACK) {  // column j of M times row j of S
 #pragma unroll 4
-      for (int j = 0; j < min(JB, a.KP - part * JB); ++j) {
-        const float4 x = *(const float4*)(m + j * KR + rg), y = *(const float4*)(S + (part * JB + j) * LD + cg);
-        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        for (int j = 0; j < min(JB, a.KP - part * JB); ++j) {
+          const float4 x = *(const float4*)(m + j * KR + rg), y = *(const float4*)(S + (part * JB + j) * LD + cg);
+          const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+          for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(xs[r], ys[c], acc[r][c]);
-      }
-    } else if (rg >= part * JB && rg < (part + 1) * JB) {  // this thread's columns of M, summed over its rows
+            for (int c = 0; c < 4; ++c) add(acc[r][c], xs[r], ys[c]);
+        }
+      } else if (rg >= part * JB && rg < (part + 1) * JB) {  // this thread's columns of M, summed over its rows
 #pragma unroll 2
-      for (int j = 0; j < a.KP; j += 4) {
-        float4 x[4];
+        for (int j = 0; j < a.KP; j += 4) {
+          float4 x[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = *(const float4*)(m + (rg - part * JB + r) * KR + j);
+          for (int r = 0; r < 4; ++r) x[r] = *(const float4*)(m + (rg - part * JB + r) * KR + j);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 y = *(const float4*)(S + (j + q) * LD + cg);
-          const float ys[4] = {y.x, y.y, y.z, y.w};
+          for (int q = 0; q < 4; ++q) {
+            const float4 y = *(const float4*)(S + (j + q) * LD + cg);
+            const float ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float xr = q == 0 ? x[r].x : q == 1 ? x[r].y : q == 2 ? x[r].z : x[r].w;
+            for (int r = 0; r < 4; ++r) {
+              const float xr = q == 0 ? x[r].x : q == 1 ? x[r].y : q == 2 ? x[r].z : x[r].w;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(xr, ys[c], acc[r][c]);
+              for (int c = 0; c < 4; ++c) add(acc[r][c], xr, ys[c]);
+            }
           }
         }
       }
-    }
+    };
+    if (odd) products(std::true_type{});
+    else products(std::false_type{});
     __syncthreads();
     if (part == KR / JB - 1) {
+      odd = 0;
       const size_t from = (((size_t)bn * a.segs + s) * cols_total + v0 + cg) * KR + rg;
       const size_t to = (((size_t)bn * a.segs + (BACK ? s - 1 : s + 1)) * cols_total + v0 + cg) * KR + rg;
 #pragma unroll
@@ -666,8 +683,9 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
         S[(rg + 1) * LD + cg + c] = x.y;
         S[(rg + 2) * LD + cg + c] = x.z;
         S[(rg + 3) * LD + cg + c] = x.w;
+        odd |= !isfinite(x.x) | !isfinite(x.y) | !isfinite(x.z) | !isfinite(x.w);
       }
-      __syncthreads();
+      odd = __syncthreads_or(odd);
     }
   }
 }

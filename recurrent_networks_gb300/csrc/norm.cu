@@ -122,9 +122,9 @@ __device__ __forceinline__ float lane_sum(float v, int lanes) {
   return v;
 }
 // What the warps of a group (MANY: of several whole warps) have, through red [8]:
-// one barrier; the place is written again only behind the next one.
-__device__ __forceinline__ void share(float2* red, float a, float b) {
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+// one barrier; red may be written again only behind the next one.
+template <typename V> __device__ __forceinline__ void share(V* red, V v) {
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
 }
 
@@ -157,7 +157,8 @@ __device__ __forceinline__ float backward_value(int act, float n, float w, float
 template <typename T, int VEC, int NV, bool GATE, bool BWD, bool MANY>
 __global__ void __launch_bounds__(256, BWD ? (VEC * NV > 8 ? 1 : 2) : (VEC * NV > 16 ? 2 : 4)) norm_kernel(NormArgs p) {
   extern __shared__ float sums[];  // [2][gp * W], BWD with p.part
-  __shared__ float2 red[2][8];
+  __shared__ float4 stats[2][8];  // in turn: forward, one barrier a row stands between a row's reads and the writes two rows on
+  __shared__ float2 red[8];
   const int li = threadIdx.x % p.lanes, slot = threadIdx.x / p.lanes;
   const int gi = slot % p.gp, ri = slot / p.gp;
   const int g = blockIdx.y * p.gp + gi;
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(256, BWD ? (VEC * NV > 8 ? 1 : 2) : (VEC * NV 
     }
   };
   const long long step = (long long)gridDim.x * p.rp;
+  int turn = 0;
   load((long long)blockIdx.x * p.rp + ri);
   for (long long r0 = (long long)blockIdx.x * p.rp; r0 < p.rows; r0 += step) {
     const long long r = r0 + ri;
@@ -226,37 +228,50 @@ __global__ void __launch_bounds__(256, BWD ? (VEC * NV > 8 ? 1 : 2) : (VEC * NV 
       for (int e = 0; e < VEC; ++e) s += x[v][e];
     }
     if (r0 + step < p.rows) load(r + step);
-    // Mean and sum of squares around it; where a group has several warps, around
-    // each warp's own mean, joined by the distance of the means.
+    // The mean, and around it the sums of d = x - mean and of its squares: the
+    // first is the mean's own rounding, which a mean far above the spread makes
+    // large beside d. Where a group has several warps each does so by itself, and
+    // the distances of their means to the first one's join them.
     s = p.centered ? lane_sum(s, lanes) : 0.0f;
     float mean = s * mine;
-    float q = 0.0f;
+    float q = 0.0f, e1 = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float d = have[v] ? x[v][e] - mean : 0.0f;
         if constexpr (!MANY) x[v][e] = d;
+        e1 += d;
         q = fmaf(d, d, q);
       }
-    q = lane_sum(q, lanes);
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+      e1 += __shfl_xor_sync(0xffffffffu, e1, o);
+    }
+    if (!p.centered) e1 = 0.0f;
     if constexpr (MANY) {
-      share(red[0], s, q);
-      float tot = 0.0f;
-      for (int k = 0; k < many; ++k) tot += red[0][w0 + k].x;
-      mean = tot * inv;
-      q = 0.0f;
+      const float4* st = stats[turn] + w0;
+      share(stats[turn], make_float4(mean, e1, q, 0.0f));
+      turn ^= 1;
+      mean = st[0].x;
+      q = e1 = 0.0f;
       for (int k = 0; k < many; ++k) {
-        const float n = part[k];
-        const float2 r = red[0][w0 + k];
-        const float d = p.centered ? __fdividef(r.x, fmaxf(n, 1.0f)) - mean : 0.0f;
-        q += fmaf(n * d, d, r.y);
+        const float4 r = st[k];
+        const float n = part[k], d = r.x - mean;
+        q += r.z + d * fmaf(n, d, 2.0f * r.y);
+        e1 += fmaf(n, d, r.y);
       }
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[v][e] = have[v] ? x[v][e] - mean : 0.0f;
+        for (int e = 0; e < VEC; ++e) x[v][e] = x[v][e] - mean;
     }
+    e1 *= inv;
+    q = fmaxf(fmaf(-e1 * e1, (float)p.W, q), 0.0f);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[v][e] = have[v] ? x[v][e] - e1 : 0.0f;
     const float rstd = 1.0f / sqrtf(fmaf(q, inv, p.eps));
     if constexpr (!BWD) {
 #pragma unroll
@@ -293,11 +308,11 @@ __global__ void __launch_bounds__(256, BWD ? (VEC * NV > 8 ? 1 : 2) : (VEC * NV 
         s2 += __shfl_xor_sync(0xffffffffu, s2, o);
       }
       if constexpr (MANY) {
-        share(red[1], s1, s2);
+        share(red, make_float2(s1, s2));
         s1 = s2 = 0.0f;
         for (int k = 0; k < many; ++k) {
-          s1 += red[1][w0 + k].x;
-          s2 += red[1][w0 + k].y;
+          s1 += red[w0 + k].x;
+          s2 += red[w0 + k].y;
         }
       } else {
         __syncwarp();
@@ -381,8 +396,15 @@ template <typename T, bool GATE, bool BWD> __global__ void __launch_bounds__(512
     }
     const float mean = p.centered ? block_sum(s, red) * inv : 0.0f;
     s = 0.0f;
+    float e1 = 0.0f;  // the mean's own rounding
     for (int c = threadIdx.x; c < W; c += 512) {
       const float v = xs[c] - mean;
+      xs[c] = v;
+      e1 += v;
+    }
+    e1 = p.centered ? block_sum(e1, red) * inv : 0.0f;
+    for (int c = threadIdx.x; c < W; c += 512) {
+      const float v = xs[c] - e1;
       xs[c] = v;
       s = fmaf(v, v, s);
     }
