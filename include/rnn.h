@@ -403,8 +403,9 @@ int rnn_gated_step(int rows, int slots, int N, int D, int function, int dtype, c
  * steps past a length are not looked at, o and the gradients are 0 there. An
  * infinity or a NaN in an input may reach every step of its row and head.
  * Chunks of 64 steps (bf16) or 32 (fp32) are taken at once by matrix products
- * whose computed operands are held to 2^-24; bf16 dq and dk are taken from
- * operands rounded to bf16 once.
+ * whose computed operands are held to 2^-24 (bf16 dq and dk: 2^-17). How the
+ * chunks are spread over the GPU follows from the sizes, the number of SMs and
+ * keep; it moves the last bits of fp32 results. No result depends on the run.
  */
 #define RNN_DELTA_MAX_D 256 /* the largest Dk and Dv */
 typedef struct {
@@ -413,7 +414,7 @@ typedef struct {
 } rnn_delta_dims_t;
 
 /* Bytes of the tape: what the forward works on and, with keep != 0, what the
- * backward needs (for bf16 and Dk = Dv = 128 about 2.5 KB a step and head,
+ * backward needs (for bf16 and Dk = Dv = 128 about 3 KB a step and head,
  * without a backward 0.8 KB), and of the backward's workspace; 0 for invalid
  * dims. The tape's first word is a status word (rnn_check_status): a device-side
  * wait of the forward or the backward that ran out. */
@@ -429,7 +430,8 @@ int rnn_delta_fwd(const rnn_delta_dims_t *dims, const void *q, const void *k, co
                   void *o, void *last, int keep, void *tape, size_t tape_bytes, void *stream);
 
 /* Backward: the gradient of sum(o*dO) + sum(last*dlast). q, k, v, lengths, scale
- * and the tape as in / from the forward (keep != 0); dO [B,T,N,Dv] and dlast
+ * and the tape as in / from the forward (keep != 0; the same device, with the
+ * same limits of rnn_plan_set_limits); dO [B,T,N,Dv] and dlast
  * [B,1,N,Dk,Dv] fp32 may be NULL (zero). Outputs dq, dk [B,T,Nk,Dk] (sums over
  * the heads that share them, in the heads' order), dv [B,T,N,Dv], dg, dbeta
  * [B,T,N] fp32, dstate0 [B,1,N,Dk,Dv] fp32 or NULL. Errors: as the forward. */

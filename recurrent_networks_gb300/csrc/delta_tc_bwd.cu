@@ -465,25 +465,37 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     load_sd(0);
     if (L::STAGES == 2) load_sd(1);
   }
+  constexpr int UN = 64 * (BV / 8) / 256;  // pieces of 8 columns of a step that a thread has of a tile
+  float4 z[UN][2];
+  auto fetch = [&](int p) {
+    const float4* f = (const float4*)(a.zf + ((size_t)item * a.nvt + p) * 64 * BV) + (tid >> 6) * 128 + (tid & 63);
+#pragma unroll
+    for (int u = 0; u < UN; ++u) z[u][0] = __ldcs(f + u * 512), z[u][1] = __ldcs(f + u * 512 + 64);
+  };
+  fetch(0);
+  const float* own = a.rec + (size_t)item * REC_N * TC_C;
+  const int i = (quad & 1) * 32 + lane, j0 = half * 32;  // this thread's step and columns of M and R
+  const float gi = own[REC_GAM * TC_C + i], bri = own[REC_BR * TC_C + i];
   for (int p = 0; p < a.nvt; ++p) {
     unsigned char* x = X + p * L::XZ;
     load_img<RB, BV / 8, 256>(tid, x, 0, (const bf16*)a.dv + vat, vstride, live, a.Dv, p * BV, BV, 0);
     load_img<RB, BV / 8, 256>(tid, x, 64, (const bf16*)(a.dO ? a.dO : a.dv) + vat, vstride, a.dO ? live : 0, a.Dv, p * BV, BV, 0);
-    const size_t tile = (size_t)item * a.nvt + p;
-    for (int k = tid; k < 64 * (BV / 8); k += 256) {  // 8 columns of a step
-      const int r = k & 63, c = k >> 6;
-      cp16(smem_u32(x + L::AT_L) + img<RB>(r, c), a.dYl + (tile * 64 * (BV / 8) + k) * 8, r < live);
-      const float4* z = (const float4*)(a.zf + tile * 64 * BV) + (size_t)c * 128 + r;
-      const float4 z0 = __ldcs(z), z1 = __ldcs(z + 64);
-      const float zs[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
-      uint4 q[3];
-      split8(zs, q);
-      *(uint4*)(x + L::AT_Z + img<RB>(r, c)) = q[0];
-      *(uint4*)(x + L::AT_Z + 64 * RB + img<RB>(r, c)) = q[1];
+    const bf16* low = a.dYl + (((size_t)item * a.nvt + p) * 64 * (BV / 8) + tid) * 8;
+#pragma unroll
+    for (int u = 0; u < UN; ++u) cp16(smem_u32(x + L::AT_L) + img<RB>(tid & 63, (tid >> 6) + 4 * u), low + u * 2048, (tid & 63) < live);
+    uint4 q[UN][3];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const float zs[8] = {z[u][0].x, z[u][0].y, z[u][0].z, z[u][0].w, z[u][1].x, z[u][1].y, z[u][1].z, z[u][1].w};
+      split8(zs, q[u]);
     }
+    if (p + 1 < a.nvt) fetch(p + 1);
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) *(uint4*)(x + L::AT_Z + k * 64 * RB + img<RB>(tid & 63, (tid >> 6) + 4 * u)) = q[u][k];
   }
   cp_commit();
-  const float* own = a.rec + (size_t)item * REC_N * TC_C;
   if (tid < TC_C) {
     rec[tid] = own[REC_CHI * TC_C + tid];
     rec[TC_C + tid] = own[REC_CLO * TC_C + tid];
@@ -543,7 +555,6 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     }
     tc_commit(bar);
   }
-  const int i = (quad & 1) * 32 + lane, j0 = half * 32;
   take();
   float nf[32];
   {
@@ -583,36 +594,33 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
   load_img<128, KT / 8, 256>(tid, KQ, 64, (const bf16*)a.q + kat, kstride, live, a.Dk, 0, (a.KP + 63) & ~63, TC_PANEL);
   cp_commit();
   // [M + M^T, R^T; R, 0], two panels of 128 rows: the first plane over the buffers
-  // of S0 and dS1, the second behind KQ
+  // of S0 and dS1, the second behind KQ. Rows first (M's hold zeros past the
+  // diagonal), then what is transposed: its 2-byte stores are of one row a warp.
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    unsigned char* to = k ? ML : SD;
-    if (quad >= 2) {
+  for (int c = 0; c < 32; c += 8) {
+    uint4 p[3];
+    split8(nf + c, p);
+    const uint32_t at = img<128>(quad * 32 + lane, (j0 + c) >> 3);
 #pragma unroll
-      for (int c = 0; c < 32; c += 8) {
-        *(uint4*)(to + img<128>(64 + i, (j0 + c) >> 3)) = round8(nf + c);
-        *(uint4*)(to + TC_PANEL + img<128>(64 + i, (j0 + c) >> 3)) = make_uint4(0, 0, 0, 0);
-      }
+    for (int k = 0; k < 2; ++k) {
+      unsigned char* to = k ? ML : SD;
+      *(uint4*)(to + at) = p[k];
+      if (quad >= 2) *(uint4*)(to + TC_PANEL + at) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  if (quad < 2) asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const bf16 m = __float2bfloat16_rn(nf[c]);
-        *(bf16*)(to + TC_PANEL + img<128>(j0 + c, i >> 3) + (i & 7) * 2) = m;
-        nf[c] -= __bfloat162float(m);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const int j = j0 + c;
-        const bf16 m = __float2bfloat16_rn(nf[c]);
-        if (j <= i) *(bf16*)(to + img<128>(i, j >> 3) + (j & 7) * 2) = m;
-        if (j < i) *(bf16*)(to + img<128>(j, i >> 3) + (i & 7) * 2) = m;
-        nf[c] -= __bfloat162float(m);
-      }
+  for (int c = 0; c < 32; ++c) {
+    const int j = j0 + c;
+    const uint32_t at = (quad < 2 ? 0 : TC_PANEL) + img<128>(j, i >> 3) + (i & 7) * 2;
+    const bf16 hi = __float2bfloat16_rn(nf[c]);
+    if (quad >= 2 || j < i) {
+      *(bf16*)(SD + at) = hi;
+      *(bf16*)(ML + at) = __float2bfloat16_rn(nf[c] - __bfloat162float(hi));
     }
   }
   // The state's parts, scaled by rows in fp32, back into the first accumulator
-  const float gi = own[REC_GAM * TC_C + i];
-  const float f0 = quad < 2 ? -gi : a.scale * gi, f1 = quad < 2 ? own[REC_BR * TC_C + i] : 0.0f;
+  const float f0 = quad < 2 ? -gi : a.scale * gi, f1 = quad < 2 ? bri : 0.0f;
   for (int c = half * 16; c < a.KP; c += 32) {
     uint32_t x[16], h[16];
     tm_ld16(x, row + c);

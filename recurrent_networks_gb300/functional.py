@@ -477,13 +477,14 @@ def gated_delta(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=No
     goes with q and k head n // (N // Nk); Dk and Dv up to 256), g and beta
     [B,T,N] (fp32 or q's dtype), state [B,1,N,Dk,Dv] or None (zeros), scale None =
     Dk ** -0.5. Keys are taken as they are: beta |k|^2 past 2 lets the state
-    grow.
+    grow (group_norm with centered=False and a weight of Dk ** -0.5 makes unit keys).
     reset [B,T] (bool or uint8): S_{t-1} counts as zero at the marked steps
     (packed documents), whatever it holds. lengths [B]: row b has lengths[b]
     steps; past them nothing is looked at, o is zero and the state is kept.
     Returns (o [B,T,N,Dv], last [B,1,N,Dk,Dv]: the state after the last step,
     fp32). Differentiable in q, k, v, g, beta and state; what is fp32 is fp32
-    throughout, bf16 gradients of q and k come from operands rounded to bf16 once.
+    throughout. The last bits of fp32 results follow from how the steps are spread
+    over the GPU: from the sizes, and from whether a gradient will be asked for.
     An infinity or a NaN in an input may reach every step of its row and head.
     status: an int32 CUDA tensor of one element, zeroed by the caller, in which
     the forward and the backward record a device-side wait that ran out (their
