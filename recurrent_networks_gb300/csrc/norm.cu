@@ -148,8 +148,8 @@ __device__ __forceinline__ float backward_value(int act, float n, float w, float
 // two; MANY: of several warps) hold a group's channels in registers. A CTA takes
 // gp groups of rp rows at once, the same groups for all its rows, so that a
 // thread's sums of dw and db are over one set of columns. One pass over the data,
-// bound by DRAM: measured 69 us forward (floor 59) and 142 backward (floor 99) for
-// 16384 rows x 32 groups of 128, bf16, gated; 23 and 44 us (floors 10 and 15) for
+// bound by DRAM: measured 74 us forward (floor 59) and 140 backward (floor 99) for
+// 65536 rows x 8 groups of 128, bf16, gated; 23 and 41 us (floors 10 and 15) for
 // 16384 rows of one group of 1024, where the two sums of a row that eight warps
 // share are waited for. Four CTAs an SM forward, with few spills, against one with
 // none: 34 us and 47 (30000 rows x 16 of 64, gated); backward they cost more (85 us
@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(256, BWD ? (VEC * NV > 8 ? 1 : 2) : (VEC * NV 
         for (int e = 0; e < VEC; ++e) x[v][e] = x[v][e] - mean;
     }
     e1 *= inv;
-    q = fmaxf(fmaf(-e1 * e1, (float)p.W, q), 0.0f);
+    q = fmaf(-e1 * e1, (float)p.W, q);
+    if (q < 0.0f) q = 0.0f;  // a NaN stays one
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -495,11 +496,12 @@ NormPlan norm_plan(long long rows, int G, int W, int dtype, bool bwd) {
   NormPlan p{};
   const int full = dtype == RNN_BF16 ? 8 : 4;
   p.vec = W % full == 0 ? full : W % 2 == 0 ? 2 : 1;
-  const int n = (W + p.vec - 1) / p.vec;  // vectors of a group
+  const int n = (W + p.vec - 1) / p.vec;  // vectors of a group; below, of a thread: at most, and while threads are to be had
   // Threads before vectors: a group of several warps is slower by its barrier and
-  // faster by its loads in flight. Backward, 4 KB rows at one vector a thread take
-  // 44 us and at two 64; forward two are as fast, and 8 KB rows gain (22 us, 27).
-  const int most = p.vec == 1 ? 8 : p.vec == 2 ? 4 : 2, some = p.vec == 1 ? 4 : p.vec == 2 || !bwd ? 2 : 1;  // vectors a thread: at most, and while threads are to be had
+  // faster by its loads in flight. Backward, 2 KB rows (1024 bf16) at one vector a
+  // thread take 44 us and at two 64; forward two are as fast, and 8 KB rows gain
+  // (22 us against 27).
+  const int most = p.vec == 1 ? 8 : p.vec == 2 ? 4 : 2, some = p.vec == 1 ? 4 : p.vec == 2 || !bwd ? 2 : 1;
   if (n > 256 * most) {
     p.gp = p.rp = 1;
     p.gy = (unsigned)G;

@@ -131,6 +131,8 @@ def test_a_row_keeps_to_itself():
         bad[4, 1] = bad[7, 0] = True
         bad = bad.repeat_interleave(width, 1)
         assert torch.equal(y[~bad], clean[~bad]) and not torch.isfinite(y[4, width:]).any()
+        y = rn.group_norm(x, 2, p["w"], p["b"], centered=False)  # the statistic of a group with a NaN is one
+        assert y[7, :width].isnan().all() and torch.isfinite(y[7, width:]).all()
 
 
 def test_leading_axes_strides_and_streams():
