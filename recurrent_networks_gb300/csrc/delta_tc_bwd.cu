@@ -698,27 +698,40 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
 
 // ---- gates ---------------------------------------------------------------------------
 // dg and dbeta of TC_EDGE chunks: a thread has a step, sums its document's dc to
-// the chunk's end, and what lies beyond comes from chunk to chunk after that.
+// the chunk's end, and what lies beyond comes from chunk to chunk after that. The
+// sums run in 64 bits: dc's signs change, and where memories are short a sum of
+// hundreds of them is small beside what it passes through.
 __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcArgs a) {
-  __shared__ float dc[TC_EDGE][TC_C], seg_sm[TC_EDGE][TC_C], from[TC_EDGE], after[TC_EDGE], es[32];
-  const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE, k = threadIdx.x / TC_C, i = threadIdx.x % TC_C;
+  __shared__ double tail[TC_EDGE][TC_C], from[TC_EDGE], after[TC_EDGE];
+  __shared__ float es[32];
+  __shared__ unsigned marks[TC_EDGE][2];
+  const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE, k = threadIdx.x / TC_C, i = threadIdx.x % TC_C, lane = threadIdx.x & 31;
   const int bn = blockIdx.x / groups, gr = blockIdx.x % groups, n = bn % a.N, b = bn / a.N;
-  const int nch = tc_chunks(a, b), lo = gr * TC_EDGE, ch = lo + k, t = ch * TC_C + i;
+  const int nch = tc_chunks(a, b), lo = gr * TC_EDGE, ch = lo + k;
   const int live = ch < a.nc ? tc_live(a, b, ch) : 0;
-  const size_t item = (size_t)bn * a.nc + ch, out = ((size_t)b * a.T + t) * a.N + n;
+  const size_t item = (size_t)bn * a.nc + ch;
   const float* rec = a.rec + item * REC_N * TC_C;
-  float zy = 0.0f, c = 0.0f, bt = 1.0f;
+  float zy = 0.0f, bt = 1.0f;
+  double c = 0.0;
+  bool mark = false;  // the first step of a document
   if (live > 0) {
 #pragma unroll 2
     for (int vt = 0; vt < a.nvt; ++vt) {
       const float* d = a.dots + (item * a.nvt + vt) * 6 * TC_C;
       zy += d[i] + d[TC_C + i];
-      c += (d[2 * TC_C + i] + d[3 * TC_C + i]) + (d[4 * TC_C + i] + d[5 * TC_C + i]);
+      c += ((double)d[2 * TC_C + i] + d[3 * TC_C + i]) + ((double)d[4 * TC_C + i] + d[5 * TC_C + i]);
     }
     bt = rec[REC_BETA * TC_C + i];
+    mark = __float_as_int(rec[REC_SEG * TC_C + i]) != (i ? __float_as_int(rec[REC_SEG * TC_C + i - 1]) : 0);
   }
-  dc[k][i] = c;
-  seg_sm[k][i] = live > 0 ? rec[REC_SEG * TC_C + i] : 0.0f;
+  const unsigned m = __ballot_sync(0xffffffffu, mark);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double x = __shfl_down_sync(0xffffffffu, c, o);
+    if (lane + o < 32) c += x;
+  }
+  tail[k][i] = c;  // of the step's half chunk
+  if (lane == 0) marks[k][i >> 5] = m;
   if (threadIdx.x < 32) {  // <S, dS> at the group's end: a lane has every 32nd part
     const int at = lo + TC_EDGE >= nch ? 0 : gr + 1;
     float e = 0.0f;
@@ -727,26 +740,25 @@ __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcA
     es[threadIdx.x] = e;
   }
   __syncthreads();
-  const int mine = __float_as_int(seg_sm[k][i]), last = __float_as_int(seg_sm[k][TC_C - 1]);
-  float s = 0.0f;
-  for (int j = TC_C - 1; j >= i; --j)
-    if (__float_as_int(seg_sm[k][j]) == mine) s += dc[k][j];
+  auto sum_from = [&](int j) { return j >= TC_C ? 0.0 : j < 32 ? tail[k][j] + tail[k][32] : tail[k][j]; };
+  const unsigned long long starts = (unsigned long long)marks[k][1] << 32 | marks[k][0], later = starts >> i >> 1;
+  double s = sum_from(i) - sum_from(later ? i + __ffsll(later) : TC_C);  // the document's steps from here on
   if (i == 0) from[k] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
-    float e = 0.0f;
+    double e = 0.0;
     for (int w = 0; w < 32; ++w) e += es[w];
     for (int q = min(TC_EDGE, nch - lo) - 1; q >= 0; --q) {
       after[q] = e;
-      const int first = __float_as_int(seg_sm[q][0]), end = __float_as_int(seg_sm[q][TC_C - 1]);
-      e = first == 0 ? from[q] + (end == 0 ? e : 0.0f) : 0.0f;  // a chunk that begins a document needs nothing before it
+      // a chunk that begins a document needs nothing before it
+      e = marks[q][0] & 1 ? 0.0 : from[q] + (marks[q][0] | marks[q][1] ? 0.0 : e);
     }
   }
   __syncthreads();
-  if (ch >= a.nc || t >= a.T) return;
-  const bool mark = mine != (i ? __float_as_int(seg_sm[k][i - 1]) : 0);
-  if (i < live && mine == last) s += after[k];
-  a.dg[out] = i < live && !mark ? s : 0.0f;
+  if (ch >= a.nc || ch * TC_C + i >= a.T) return;
+  const size_t out = ((size_t)b * a.T + (size_t)ch * TC_C + i) * a.N + n;
+  if (i < live && !later) s += after[k];
+  a.dg[out] = i < live && !mark ? (float)s : 0.0f;
   a.dbeta[out] = i < live ? zy / bt : 0.0f;
 }
 
