@@ -4,6 +4,8 @@
 //          first: dY (= dV) and the state's gradient, left for every chunk
 //   grad   every chunk by itself: dQ, dK, dg, dbeta
 //   share  sums dQ and dK over the heads that share q and k
+// Measured 83 + 49 + 3 us at B=3 T=515, 6 heads of 40 x 72 on 2 (54 CTAs walk 17
+// chunks of 5 us each).
 #include "delta.h"
 #include "kernels.cuh"
 

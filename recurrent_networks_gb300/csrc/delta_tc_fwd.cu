@@ -35,8 +35,9 @@ template <int N> __device__ __forceinline__ float dot_pairs(const float* p, cons
 // K K^T and Q K^T by mma.sync, 16 rows a warp and the columns up to its last row;
 // the rest in fp32 on the plain cores. Tm: its two diagonal blocks of 32 by forward
 // substitution, a column to a thread, then T21 = -T22 (L21 T11); PT a column and
-// every other row to a thread. Bound by instructions, about 3500 a warp; four CTAs
-// an SM (Dk <= 128).
+// every other row to a thread. Bound by instructions, about 3500 a warp (issue slots
+// 42 % busy, barriers between the parts); four CTAs an SM (Dk <= 128). 133 us for
+// the 4096 chunks of the chain's size below.
 __global__ void __launch_bounds__(128, 4) delta_tc_prep_kernel(DeltaTcArgs a) {
   constexpr int C = TC_C, NT = C / 8, LD = PREP_LD, H = C / 2;
   extern __shared__ __align__(16) unsigned char sm_raw[];
@@ -252,7 +253,7 @@ template <int BV, int MT> struct TcChain {
 // registers to the other two: 256 * 200 + 128 * 104 = 384 * 168.
 // MT: tiles of 128 state rows, whose fp32 values stay in registers. A chunk is
 // three dependent products (2000 cycles for BV = 64, Dk = 128) and their ways
-// through registers between barriers of the whole CTA, 4.5 us in all: 286 us for
+// through registers between barriers of the whole CTA, 4.7 us in all: 299 us for
 // the 64 chunks of B = 8, T = 4096, N = 8, Dk = Dv = 128, where 557 MB pass in a
 // training step (82 us). Tiles of 32 columns would double the CTAs and shorten a
 // chunk to two thirds: 1.3 times the time where all SMs are taken.
