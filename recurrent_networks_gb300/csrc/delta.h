@@ -26,7 +26,7 @@ inline DeltaLay delta_lay(long long heads, int Dv, int KP, long long nc, int sms
     auto rounds = [&](long long ctas) { return (double)((ctas + sms - 1) / sms); };
     for (int segs = 1; segs <= 64; ++segs) {
       const long long len = ((nc + segs - 1) / segs + 7) / 8 * 8;
-      if (segs > 1 && (len * (segs - 1) >= nc)) break;  // a segment would be empty
+      if (segs > 1 && len * (segs - 1) >= nc) continue;  // a segment would be empty
       const double own = rounds(heads * segs * nvt) * (segs > 1 ? len : nc);
       double cost = own * (f + w);
       if (segs > 1)
