@@ -11,8 +11,8 @@ namespace rnn {
 // rounds that the CTAs take times the chunks of a segment; segments cost the pass
 // of maps (the identity's tiles among them, forward) and the join. Microseconds a
 // chunk as measured with all SMs taken: forward 4.8 (BV = 64) and 3.4 (32; 5.3 for
-// keys past 128 channels), backward 6.2, 4.3 and 6.3; a join 2.6 a segment, 15 a
-// further launch.
+// keys past 128 channels), backward 6.2, 4.3 and 6.3; a join 4.2 a segment (11 for
+// keys past 128), 15 a further launch.
 struct DeltaLay {
   int BV, segs, seglen;
 };
@@ -30,7 +30,7 @@ inline DeltaLay delta_lay(long long heads, int Dv, int KP, long long nc, int sms
       const double own = rounds(heads * segs * nvt) * (segs > 1 ? len : nc);
       double cost = own * (f + w);
       if (segs > 1)
-        cost += rounds(heads * segs * (nvt + ki)) * len * f + own * w + (2.6 * segs + 30.0) * (keep ? 2 : 1);
+        cost += rounds(heads * segs * (nvt + ki)) * len * f + own * w + ((KP > 128 ? 11.0 : 4.2) * segs + 30.0) * (keep ? 2 : 1);
       if (cost < least * 0.97) {
         least = cost;
         best = DeltaLay{BV, segs, (int)(segs > 1 ? len : (nc > 0 ? nc : 1))};

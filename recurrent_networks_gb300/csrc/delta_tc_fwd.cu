@@ -591,18 +591,18 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
 // ---- join ----------------------------------------------------------------------------
 // The states between the segments, one after the other: forward S = M S + H from
 // state0, backward dS = M^T dS + H from dlast. A CTA has CW columns of v of a head,
-// S in shared memory, M by blocks of 64 KB, two of them; 4 x 4 values a thread.
+// S in shared memory, M by blocks of 64 KB, two of them; 4 x 2 values a thread.
 // Rows and columns of M past KP are not looked at. M is exactly zero where a reset
 // stands in its segment: then nothing of S may pass, an infinity or a NaN neither,
 // so the zeros of M are left out where S holds one.
 template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_join_kernel(DeltaTcArgs a, int cols_total) {
-  constexpr int CW = KR == 128 ? 32 : 16, LD = CW + 4, JB = 16384 / KR;  // rows of Mt in a block
+  constexpr int CW = KR == 128 ? 16 : 8, LD = CW + 4, JB = 16384 / KR;  // rows of Mt in a block
   extern __shared__ __align__(16) unsigned char sm_raw[];
   float* M = (float*)sm_raw;  // [2][JB][KR]
   float* S = M + 2 * JB * KR; // [KR][LD]
   const int groups = cols_total / CW;
   const int tid = threadIdx.x, bn = blockIdx.x / groups, v0 = (blockIdx.x % groups) * CW;
-  const int cg = tid % (CW / 4) * 4, rg = tid / (CW / 4) * 4;
+  const int cg = tid % (CW / 2) * 2, rg = tid / (CW / 2) * 4;
   const float* x0 = BACK ? a.dlast : a.s0;
   int odd = 0;
   for (int k = tid; k < KR * CW; k += 256) {
@@ -621,7 +621,7 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
     cp_commit();
   };
   load(0);
-  float acc[4][4];
+  float acc[4][2];
   for (int k = 0; k < blocks; ++k) {
     const int s = BACK ? a.segs - 1 - k / (KR / JB) : k / (KR / JB), part = k % (KR / JB);
     if (k + 1 < blocks) load(k + 1);
@@ -632,7 +632,7 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[r][c] = 0.0f;
+        for (int c = 0; c < 2; ++c) acc[r][c] = 0.0f;
     const float* m = M + (k & 1) * JB * KR;
     auto products = [&](auto guard) {
       auto add = [&](float& acc, float x, float y) {
@@ -641,12 +641,13 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
       if constexpr (!BACK) {  // column j of M times row j of S
 #pragma unroll 4
         for (int j = 0; j < min(JB, a.KP - part * JB); ++j) {
-          const float4 x = *(const float4*)(m + j * KR + rg), y = *(const float4*)(S + (part * JB + j) * LD + cg);
-          const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+          const float4 x = *(const float4*)(m + j * KR + rg);
+          const float2 y = *(const float2*)(S + (part * JB + j) * LD + cg);
+          const float xs[4] = {x.x, x.y, x.z, x.w}, ys[2] = {y.x, y.y};
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) add(acc[r][c], xs[r], ys[c]);
+            for (int c = 0; c < 2; ++c) add(acc[r][c], xs[r], ys[c]);
         }
       } else if (rg >= part * JB && rg < (part + 1) * JB) {  // this thread's columns of M, summed over its rows
 #pragma unroll 2
@@ -656,13 +657,13 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
           for (int r = 0; r < 4; ++r) x[r] = *(const float4*)(m + (rg - part * JB + r) * KR + j);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float4 y = *(const float4*)(S + (j + q) * LD + cg);
-            const float ys[4] = {y.x, y.y, y.z, y.w};
+            const float2 y = *(const float2*)(S + (j + q) * LD + cg);
+            const float ys[2] = {y.x, y.y};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float xr = q == 0 ? x[r].x : q == 1 ? x[r].y : q == 2 ? x[r].z : x[r].w;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) add(acc[r][c], xr, ys[c]);
+              for (int c = 0; c < 2; ++c) add(acc[r][c], xr, ys[c]);
             }
           }
         }
@@ -676,7 +677,7 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
       const size_t from = (((size_t)bn * a.segs + s) * cols_total + v0 + cg) * KR + rg;
       const size_t to = (((size_t)bn * a.segs + (BACK ? s - 1 : s + 1)) * cols_total + v0 + cg) * KR + rg;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         const float4 h = *(const float4*)(a.Ht + from + (size_t)c * KR);
         const float4 x = make_float4(acc[0][c] + h.x, acc[1][c] + h.y, acc[2][c] + h.z, acc[3][c] + h.w);
         *(float4*)(a.St + to + (size_t)c * KR) = x;
@@ -692,7 +693,7 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
 }
 
 template <int KR, bool BACK> cudaError_t join_run(const DeltaTcArgs& a, int BV, cudaStream_t st) {
-  constexpr int CW = KR == 128 ? 32 : 16;
+  constexpr int CW = KR == 128 ? 16 : 8;
   constexpr size_t sm = 2 * 65536 + (size_t)KR * (CW + 4) * 4;
   cudaError_t e = set_smem_attr((const void*)delta_tc_join_kernel<KR, BACK>, sm);
   if (e != cudaSuccess) return e;
