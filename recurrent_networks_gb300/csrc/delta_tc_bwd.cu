@@ -309,16 +309,16 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
       }
       if (quad >= 2) {
         const float f = gi * a.scale;
-        float d[NC], s = 0.0f;
+        float d[NC], s[4] = {};
 #pragma unroll
         for (int c = 0; c < NC; c += 8) widen8(*(const uint4*)(OS + img<RB>(i, (c0 + c) >> 3)), d + c);
         if (!a.maps)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) s = fmaf(d[c], kept[c], s);
+          for (int c = 0; c < NC; ++c) s[c & 3] = fmaf(d[c], kept[c], s[c & 3]);
 #pragma unroll
         for (int c = 0; c < NC; ++c) d[c] = gi != 0.0f ? f * d[c] : 0.0f;
         put_planes<RB, NC>(GS, L::GPLANE, 64 + i, c0, d);
-        if (!a.maps) a.dots[((tile * 3 + 2) * 2 + half) * TC_C + i] = i < tc_live(a, b, ch) ? s : 0.0f;
+        if (!a.maps) a.dots[((tile * 3 + 2) * 2 + half) * TC_C + i] = i < tc_live(a, b, ch) ? (s[0] + s[1]) + (s[2] + s[3]) : 0.0f;
       }
       take();
       if (quad < 2) {
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
       }
       leave();  // 3: -gam dY's planes are there, dO is read, V is there
       if (quad < 2 && !a.maps) {  // what leaves for memory goes while the product runs
-        float zy = 0.0f, vy = 0.0f;
+        float zy[4] = {}, vy[4] = {};
         uint4* low = (uint4*)(a.dYl + tile * 64 * BV) + (size_t)half * (NC / 8) * 64 + i;
 #pragma unroll
         for (int c = 0; c < NC; c += 8) {
@@ -353,12 +353,12 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
           low[(c / 8) * 64] = p[1];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            zy = fmaf(kept[c + e], y[c + e], zy);
-            vy = fmaf(v[e], y[c + e], vy);
+            zy[e & 3] = fmaf(kept[c + e], y[c + e], zy[e & 3]);
+            vy[e & 3] = fmaf(v[e], y[c + e], vy[e & 3]);
           }
         }
-        a.dots[((tile * 3 + 0) * 2 + half) * TC_C + i] = zy;
-        a.dots[((tile * 3 + 1) * 2 + half) * TC_C + i] = -vy;
+        a.dots[((tile * 3 + 0) * 2 + half) * TC_C + i] = (zy[0] + zy[1]) + (zy[2] + zy[3]);
+        a.dots[((tile * 3 + 1) * 2 + half) * TC_C + i] = -((vy[0] + vy[1]) + (vy[2] + vy[3]));
       }
       const float gC = gam[TC_C - 1];
       take();
