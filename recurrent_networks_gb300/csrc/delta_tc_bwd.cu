@@ -703,8 +703,8 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
 // dg and dbeta of TC_EDGE chunks: a thread has a step, sums its document's dc to
 // the chunk's end, and what lies beyond comes from chunk to chunk after that. The
 // sums run in 64 bits: dc's signs change, and where memories are short a sum of
-// hundreds of them is small beside what it passes through (2.2e-6 off in 32 bits,
-// 1.3e-6 here, at worst of 250 cases; 22 us at the chain's size, 12 in 32 bits).
+// hundreds of them is small beside what it passes through (2.2e-6 off in 32 bits
+// against 1.3e-6, at worst of 250 cases; 22 us at the chain's size, 12 in 32 bits).
 __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcArgs a) {
   __shared__ double tail[TC_EDGE][TC_C], from[TC_EDGE], after[TC_EDGE];
   __shared__ float es[32];
