@@ -592,7 +592,9 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
 // The states between the segments, one after the other: forward S = M S + H from
 // state0, backward dS = M^T dS + H from dlast. A CTA has CW columns of v of a head,
 // S in shared memory, M by blocks of 64 KB, two of them; 4 x 2 values a thread.
-// Rows and columns of M past KP are not looked at. M is exactly zero where a reset
+// Rows and columns of M past KP are not looked at (the maps' pass writes whole tiles
+// of columns, the rest of Mt is whatever the caller's memory held): the states are
+// zero there, which the chain's whole panels count on. M is exactly zero where a reset
 // stands in its segment: then nothing of S may pass, an infinity or a NaN neither,
 // so the zeros of M are left out where S holds one.
 template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_join_kernel(DeltaTcArgs a, int cols_total) {
@@ -649,7 +651,7 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
 #pragma unroll
             for (int c = 0; c < 2; ++c) add(acc[r][c], xs[r], ys[c]);
         }
-      } else if (rg >= part * JB && rg < (part + 1) * JB) {  // this thread's columns of M, summed over its rows
+      } else if (rg >= part * JB && rg < min((part + 1) * JB, a.KP)) {  // this thread's columns of M, summed over its rows
 #pragma unroll 2
         for (int j = 0; j < a.KP; j += 4) {
           float4 x[4];
