@@ -43,6 +43,13 @@ constexpr int F32_NP = 3, F32_C = 32, F32_BV = 32;  // planes, steps of a chunk,
 // per-step values of a chunk that delta_prep leaves for the other kernels
 enum { REC_CHI = 0, REC_CLO, REC_SEG, REC_GAM, REC_RHO, REC_BETA, REC_BR, REC_N };
 
+// gam is +0 for the steps behind a reset alone, and -0 where the decays' product is
+// below the smallest number: the state before the reset has no part in the former,
+// whatever it holds, and is multiplied by the latter as by any factor (an infinity
+// stays no number).
+__device__ __forceinline__ float keep_part(float f) { return f == 0.0f ? -0.0f : f; }
+__device__ __forceinline__ bool has_part(float f) { return __float_as_uint(f) != 0u; }
+
 struct DeltaArgs {
   int B, T, Nk, N, Dk, Dv;
   int DKP, nvt, nc;  // Dk rounded up to 16, tiles of BV columns of v, chunks

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
 #pragma unroll
       for (int t = 0; t < NS; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[mt][t][e] = gC != 0.0f ? gC * S[mt][t][e] : 0.0f;
+        for (int e = 0; e < 4; ++e) S[mt][t][e] = has_part(gC) ? gC * S[mt][t][e] : 0.0f;
       mma_acc<NS, true, false>(S[mt], Q, r, Go, 0, C);
       mma_acc<NS, true, false>(S[mt], K, r, Yo, 0, C);
     }
@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
           const float2 q = planes_sum(Qs + i * LDK + c, kplane), k = planes_sum(Ks + i * LDK + c, kplane);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float x = gi != 0.0f ? gi * a.scale * aq[t][2 * h + e] : 0.0f;
-            const float k1 = gi != 0.0f ? -gi * ak[t][2 * h + e] : 0.0f;
+            const float x = has_part(gi) ? gi * a.scale * aq[t][2 * h + e] : 0.0f;
+            const float k1 = has_part(gi) ? -gi * ak[t][2 * h + e] : 0.0f;
             const float hh = ri != 0.0f ? ri * ah[t][2 * h + e] : 0.0f;
             const float qe = e ? q.y : q.x, ke = e ? k.y : k.x;
             dot[0][h] += qe * x;
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
     }
     const float bt = beta[tid];
     fin[tid] = re - bt * cb + d[0] + d[1] - bt * d[2];
-    fin[C + tid] = cb + d[2];
+    fin[C + tid] = cb + d[2] + 0.0f * d[1];  // z is left finite where a reset follows a state that is not
     fin[2 * C + tid] = bt * d[2];
   }
   __syncthreads();
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
       float tot = 0.0f, w = 0.0f;
       for (int i = 0; i < C; ++i) tot += fin[2 * C + i];
       for (int i = 0; i < 8; ++i) w += wsum[i];
-      s = tot + (gam[C - 1] != 0.0f ? gam[C - 1] * w : 0.0f);
+      s = tot + (has_part(gam[C - 1]) ? gam[C - 1] * w : 0.0f);
     }
     for (int i = C - 1; i >= tid; --i)
       if (__float_as_int(seg[i]) == mine) s += fin[i];

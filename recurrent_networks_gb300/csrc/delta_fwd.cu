@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(2 * F32_C) delta_prep_kernel(DeltaArgs a) {
     rec[REC_CHI * C + lane] = chi;
     rec[REC_CLO * C + lane] = (float)(c - (double)chi);
     rec[REC_SEG * C + lane] = __int_as_float(seg);
-    rec[REC_GAM * C + lane] = seg == 0 ? expf(chi) : 0.0f;
+    rec[REC_GAM * C + lane] = seg == 0 ? keep_part(expf(chi)) : 0.0f;
     rec[REC_RHO * C + lane] = rho;
     rec[REC_BETA * C + lane] = be;
     rec[REC_BR * C + lane] = be * rho;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
     cp_wait<0>();
     __syncthreads();
     const Opnd K = opnd(Ks, LDK, kplane);
-    const float *gam = recs + (ch & 1) * 2 * C, *br = gam + C;
+    const float *gam = recs + (ch & 1) * 2 * C, *br = gam + C, gC = gam[C - 1];
     float acc[NT][4];
     zero(acc);
     mma_acc<NT, false, false>(acc, K, m0, So, n0, DKP);
@@ -224,9 +224,15 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
       for (int t = 0; t < NT; ++t) {
         const int c = n0 + t * 8 + (lane & 3) * 2;
         float2 y = planes_sum(Vs + i * LDV + c, C * LDV);
-        if (gi != 0.0f) {  // behind a reset the old state has no part, whatever it holds
+        if (has_part(gi)) {  // behind a reset the old state has no part, whatever it holds
           y.x -= gi * acc[t][2 * h];
           y.y -= gi * acc[t][2 * h + 1];
+          // The products with Tm and P reach over the reset by zeros, which an infinity
+          // would pass. o and the gradients have it from S0.
+          if (!has_part(gC)) {
+            if (!isfinite(acc[t][2 * h])) y.x = 0.0f;
+            if (!isfinite(acc[t][2 * h + 1])) y.y = 0.0f;
+          }
         }
         split_store(Ys + i * LDV + c, C * LDV, y.x, y.y);
       }
@@ -253,7 +259,6 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
     __syncthreads();
     if (more) load_t(ch + 1);
     cp_commit();
-    const float gC = gam[C - 1];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int r = (warp + 8 * mt) * 16;
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(256, 1) delta_chain_kernel(DeltaArgs a) {
 #pragma unroll
       for (int t = 0; t < NS; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[mt][t][e] = gC != 0.0f ? gC * S[mt][t][e] : 0.0f;
+        for (int e = 0; e < 4; ++e) S[mt][t][e] = has_part(gC) ? gC * S[mt][t][e] : 0.0f;
       mma_acc<NS, true, false>(S[mt], K, r, Zo, 0, C);
     }
     if (more) put_state();
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(256) delta_out_kernel(DeltaArgs a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) acc[t][2 * h + e] = gi != 0.0f ? gi * acc[t][2 * h + e] : 0.0f;
+      for (int e = 0; e < 2; ++e) acc[t][2 * h + e] = has_part(gi) ? gi * acc[t][2 * h + e] : 0.0f;
   }
   cp_wait<0>();
   __syncthreads();

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
         float d[NC];
         tm_sum<NC, BV>(d, row + D3 + 3 * mt * BV + c0);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
+        for (int c = 0; c < NC; ++c) S[mt][c] = has_part(gC) ? fmaf(gC, S[mt][c], d[c]) : d[c];
       }
       leave();  // 4: the products are over, dY's image is there
       if (more) put_state();
@@ -631,7 +631,7 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     tm_wait_ld();
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      float s = f0 != 0.0f ? f0 * __uint_as_float(x[e]) : 0.0f;
+      float s = has_part(gi) ? f0 * __uint_as_float(x[e]) : 0.0f;
       if (f1 != 0.0f) s = fmaf(f1, __uint_as_float(h[e]), s);
       x[e] = __float_as_uint(s);
     }

@@ -2,8 +2,6 @@
 //   prep   every chunk by itself: TP and the per-step factors
 //   chain  per head and tile of BV columns of v, the chunks one after the other:
 //          o and the state, and what a backward needs
-#include <type_traits>
-
 #include "delta.h"
 #include "delta_tc.cuh"
 
@@ -94,7 +92,7 @@ __global__ void __launch_bounds__(128, 4) delta_tc_prep_kernel(DeltaTcArgs a) {
       rec[REC_CHI * C + i] = chi;
       rec[REC_CLO * C + i] = (float)(c - (double)chi);
       rec[REC_SEG * C + i] = __int_as_float(sg[h]);
-      rec[REC_GAM * C + i] = sg[h] == 0 ? exp2f((float)c) : 0.0f;
+      rec[REC_GAM * C + i] = sg[h] == 0 ? keep_part(exp2f((float)c)) : 0.0f;
       rec[REC_BETA * C + i] = be[h];
     }
 #pragma unroll
@@ -492,7 +490,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
       const bool more = ch + 1 < ch1;
       leave();  // 1: KQ, V and S's planes are there
       const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
-      const float gi = gam[i];
+      const float gi = gam[i], gC = gam[TC_C - 1];
+      unsigned lost = 0;  // columns whose state is not finite, where it ends in this chunk
       float y[NC];
       if (ident)
 #pragma unroll
@@ -504,14 +503,22 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
       float x[NC];
       tm_sum<NC, BV>(x, row + D1 + c0);
       if (quad < 2) {
-        if (gi != 0.0f)  // behind a reset the old state has no part, whatever it holds
+        if (has_part(gi)) {  // behind a reset the old state has no part, whatever it holds
 #pragma unroll
           for (int c = 0; c < NC; ++c) y[c] = fmaf(-gi, x[c], y[c]);
+          if (!has_part(gC))  // the products with TP reach over the reset by zeros, which an infinity would pass
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (!isfinite(x[c])) {
+                y[c] = 0.0f;
+                lost |= 1u << c;
+              }
+        }
         put_planes<RB, NC>(YS, L::YPLANE, i, c0, y);
       } else {
         const float f = gi * a.scale;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) x[c] = gi != 0.0f ? f * x[c] : 0.0f;
+        for (int c = 0; c < NC; ++c) x[c] = has_part(gi) ? f * x[c] : 0.0f;
       }
       leave();  // 2: Y's planes are there, V is read
       const int live = tc_live(a, b, ch);
@@ -529,6 +536,10 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
       if (a.maps) {
       } else if (quad < 2) {
         if (a.zf) {
+          if (lost)  // its z are no numbers
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (lost >> c & 1) z[c] = nanf("");
           float4* f = (float4*)(a.zf + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
 #pragma unroll
           for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
@@ -544,14 +555,13 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
 #pragma unroll
         for (int c = 0; c < NC; c += 8) *(uint4*)(OS + img<RB>(i, (c0 + c) >> 3)) = round8(z + c);
       }
-      const float gC = gam[TC_C - 1];
       take();
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float d[NC];
         tm_sum<NC, BV>(d, row + D3 + 3 * mt * BV + c0);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) S[mt][c] = gC != 0.0f ? fmaf(gC, S[mt][c], d[c]) : d[c];
+        for (int c = 0; c < NC; ++c) S[mt][c] = has_part(gC) ? fmaf(gC, S[mt][c], d[c]) : d[c];
       }
       leave();  // 4: the products are over, o's image is there
       if (more) put_state();
@@ -596,14 +606,14 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
 // of columns, the rest of Mt is whatever the caller's memory held): the states are
 // zero there, which the chain's whole panels count on. M is exactly zero where a reset
 // stands in its segment: then nothing of S may pass, an infinity or a NaN neither,
-// so the zeros of M are left out where S holds one.
+// so where S holds one a reset is looked for and M left out.
 template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_join_kernel(DeltaTcArgs a, int cols_total) {
   constexpr int CW = KR == 128 ? 16 : 8, LD = CW + 4, JB = 16384 / KR;  // rows of Mt in a block
   extern __shared__ __align__(16) unsigned char sm_raw[];
   float* M = (float*)sm_raw;  // [2][JB][KR]
   float* S = M + 2 * JB * KR; // [KR][LD]
   const int groups = cols_total / CW;
-  const int tid = threadIdx.x, bn = blockIdx.x / groups, v0 = (blockIdx.x % groups) * CW;
+  const int tid = threadIdx.x, bn = blockIdx.x / groups, v0 = (blockIdx.x % groups) * CW, nch = tc_chunks(a, bn / a.N);
   const int cg = tid % (CW / 2) * 2, rg = tid / (CW / 2) * 4;
   const float* x0 = BACK ? a.dlast : a.s0;
   int odd = 0;
@@ -624,22 +634,27 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
   };
   load(0);
   float acc[4][2];
+  int cut = 0;
   for (int k = 0; k < blocks; ++k) {
     const int s = BACK ? a.segs - 1 - k / (KR / JB) : k / (KR / JB), part = k % (KR / JB);
     if (k + 1 < blocks) load(k + 1);
     else cp_commit();
     cp_wait<1>();
     __syncthreads();
-    if (part == 0)
+    if (part == 0) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int c = 0; c < 2; ++c) acc[r][c] = 0.0f;
+      cut = 0;
+      if (odd) {
+        for (int ch = s * a.seglen + tid; ch < min(nch, (s + 1) * a.seglen); ch += 256)
+          cut |= !has_part(a.rec[(((size_t)bn * a.nc + ch) * REC_N + REC_GAM) * TC_C + TC_C - 1]);
+        cut = __syncthreads_or(cut);
+      }
+    }
     const float* m = M + (k & 1) * JB * KR;
-    auto products = [&](auto guard) {
-      auto add = [&](float& acc, float x, float y) {
-        if (!decltype(guard)::value || x != 0.0f) acc = fmaf(x, y, acc);
-      };
+    if (!cut) {
       if constexpr (!BACK) {  // column j of M times row j of S
 #pragma unroll 4
         for (int j = 0; j < min(JB, a.KP - part * JB); ++j) {
@@ -649,7 +664,7 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) add(acc[r][c], xs[r], ys[c]);
+            for (int c = 0; c < 2; ++c) acc[r][c] = fmaf(xs[r], ys[c], acc[r][c]);
         }
       } else if (rg >= part * JB && rg < min((part + 1) * JB, a.KP)) {  // this thread's columns of M, summed over its rows
 #pragma unroll 2
@@ -665,14 +680,12 @@ template <int KR, bool BACK> __global__ void __launch_bounds__(256, 1) delta_tc_
             for (int r = 0; r < 4; ++r) {
               const float xr = q == 0 ? x[r].x : q == 1 ? x[r].y : q == 2 ? x[r].z : x[r].w;
 #pragma unroll
-              for (int c = 0; c < 2; ++c) add(acc[r][c], xr, ys[c]);
+              for (int c = 0; c < 2; ++c) acc[r][c] = fmaf(xr, ys[c], acc[r][c]);
             }
           }
         }
       }
-    };
-    if (odd) products(std::true_type{});
-    else products(std::false_type{});
+    }
     __syncthreads();
     if (part == KR / JB - 1) {
       odd = 0;

@@ -485,7 +485,8 @@ def gated_delta(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=No
     fp32). Differentiable in q, k, v, g, beta and state; what is fp32 is fp32
     throughout. The last bits of fp32 results follow from how the steps are spread
     over the GPU: from the sizes, and from whether a gradient will be asked for.
-    An infinity or a NaN in an input may reach every step of its row and head.
+    An infinity or a NaN in q, k, v, g or beta may reach every step of its row and
+    head; one in the state ends at the next reset.
     status: an int32 CUDA tensor of one element, zeroed by the caller, in which
     the forward and the backward record a device-side wait that ran out (their
     results are then not valid); _lib.rnn_check_status(status) raises for it."""
