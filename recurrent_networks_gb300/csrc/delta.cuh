@@ -46,7 +46,8 @@ enum { REC_CHI = 0, REC_CLO, REC_SEG, REC_GAM, REC_RHO, REC_BETA, REC_BR, REC_N 
 // gam is +0 for the steps behind a reset alone, and -0 where the decays' product is
 // below the smallest number: the state before the reset has no part in the former,
 // whatever it holds, and is multiplied by the latter as by any factor (an infinity
-// stays no number).
+// stays no number). So rho and br = beta rho, for the steps before a later reset and
+// the gradient of the state behind it.
 __device__ __forceinline__ float keep_part(float f) { return f == 0.0f ? -0.0f : f; }
 __device__ __forceinline__ bool has_part(float f) { return __float_as_uint(f) != 0u; }
 

@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
     cp_wait<1>();  // all but q
     __syncthreads();
     const Opnd K = opnd(Ks, LDK, kplane);
-    const float *gam = recs + (ch & 1) * 2 * C, *br = gam + C;
+    const float *gam = recs + (ch & 1) * 2 * C, *br = gam + C, gC = gam[C - 1];
+    bool lost[NT][4];  // where the state's gradient is not finite and ends in this chunk
     float acc[NT][4], acc2[NT][4];
     zero(acc);
     zero(acc2);
@@ -127,12 +128,17 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int c = n0 + t * 8 + (lane & 3) * 2;
-        float x = a.scale * acc[t][2 * h], y = a.scale * acc[t][2 * h + 1];
-        if (bi != 0.0f) {  // no part of the state's gradient before a later document
-          x += bi * acc2[t][2 * h];
-          y += bi * acc2[t][2 * h + 1];
+        float x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[e] = a.scale * acc[t][2 * h + e];
+          // no part of the state's gradient before a later document; the products reach
+          // there by zeros, which an infinity would pass
+          const float w = has_part(bi) ? bi * acc2[t][2 * h + e] : 0.0f;
+          lost[t][2 * h + e] = !has_part(gC) && !isfinite(w);
+          if (!lost[t][2 * h + e]) x[e] += w;
         }
-        split_store(Zs + i * LDV + c, C * LDV, x, y);
+        split_store(Zs + i * LDV + c, C * LDV, x[0], x[1]);
         const float2 d = planes_sum(Os + i * LDV + c, C * LDV);
         split_store(Gs + i * LDV + c, C * LDV, gi * d.x, gi * d.y);
       }
@@ -149,13 +155,13 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = m0 + (lane >> 2) + 8 * h;
-        const float gi = -gam[i];
+        const float gi = gam[i];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int c = n0 + t * 8 + (lane & 3) * 2;
-          const float x0 = acc[t][2 * h], x1 = acc[t][2 * h + 1];
+          const float x0 = lost[t][2 * h] ? nanf("") : acc[t][2 * h], x1 = lost[t][2 * h + 1] ? nanf("") : acc[t][2 * h + 1];
           split_store(y + i * BV + c, C * BV, x0, x1);
-          split_store(Ys + i * LDV + c, C * LDV, gi * x0, gi * x1);
+          split_store(Ys + i * LDV + c, C * LDV, has_part(gi) ? -gi * x0 : 0.0f, has_part(gi) ? -gi * x1 : 0.0f);
           if (dv && i < steps) {
             float* p = dv + (size_t)i * vstride + c;
             if (a.Dv % 2 == 0) {
@@ -172,7 +178,6 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
     __syncthreads();
     if (more) load_t(ch - 1);
     cp_commit();
-    const float gC = gam[C - 1];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int r = (warp + 8 * mt) * 16;
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
           for (int e = 0; e < 2; ++e) {
             const float x = has_part(gi) ? gi * a.scale * aq[t][2 * h + e] : 0.0f;
             const float k1 = has_part(gi) ? -gi * ak[t][2 * h + e] : 0.0f;
-            const float hh = ri != 0.0f ? ri * ah[t][2 * h + e] : 0.0f;
+            const float hh = has_part(ri) ? ri * ah[t][2 * h + e] : 0.0f;
             const float qe = e ? q.y : q.x, ke = e ? k.y : k.x;
             dot[0][h] += qe * x;
             dot[1][h] += ke * k1;

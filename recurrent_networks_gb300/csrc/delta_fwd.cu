@@ -61,14 +61,15 @@ __global__ void __launch_bounds__(2 * F32_C) delta_prep_kernel(DeltaArgs a) {
     const double all = __shfl_sync(0xffffffffu, c, 31);
     const unsigned m = __ballot_sync(0xffffffffu, mark);
     const int seg = __popc(m & (0xffffffffu >> (31 - lane)));
-    const float chi = (float)c, rho = seg == __popc(m) ? expf((float)(all - c)) : 0.0f;
+    const bool last = seg == __popc(m);
+    const float chi = (float)c, rho = last ? keep_part(expf((float)(all - c))) : 0.0f;
     rec[REC_CHI * C + lane] = chi;
     rec[REC_CLO * C + lane] = (float)(c - (double)chi);
     rec[REC_SEG * C + lane] = __int_as_float(seg);
     rec[REC_GAM * C + lane] = seg == 0 ? keep_part(expf(chi)) : 0.0f;
     rec[REC_RHO * C + lane] = rho;
     rec[REC_BETA * C + lane] = be;
-    rec[REC_BR * C + lane] = be * rho;
+    rec[REC_BR * C + lane] = last ? keep_part(be * rho) : 0.0f;
   }
   cp_wait<0>();
   __syncthreads();

@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
       const bool more = ch > ch0;
       leave();  // 1: KQ, dO and dS's planes are there
       const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
-      const float gi = gam[i], bi = br[i];
+      const float gi = gam[i], bi = br[i], gC = gam[TC_C - 1];
+      unsigned lost = 0;  // columns where the state's gradient is not finite and ends in this chunk
       float kept[NC];  // z (K's steps) or o (Q's), in fp32
       if (!a.maps) {
         const float4* f = (const float4*)((quad < 2 ? a.zf : a.of) + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
@@ -325,7 +326,14 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
         float x[NC];
         tm_sum<NC, BV>(x, row + D1 + c0);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) x[c] = bi != 0.0f ? bi * x[c] : 0.0f;  // no part of it before a later document
+        for (int c = 0; c < NC; ++c) x[c] = has_part(bi) ? bi * x[c] : 0.0f;  // no part of it before a later document
+        if (!has_part(gC))  // as the forward's Y
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if (!isfinite(x[c])) {
+              x[c] = 0.0f;
+              lost |= 1u << c;
+            }
         put_planes<RB, NC>(GS, L::GPLANE, i, c0, x);
       }
       leave();  // 2: W's planes are there
@@ -333,9 +341,13 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
       float y[NC];
       if (quad < 2) {
         tm_sum<NC, BV>(y, row + D2 + c0);
+        if (lost)  // its dY are no numbers
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if (lost >> c & 1) y[c] = nanf("");
         float g[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) g[c] = gi != 0.0f ? -gi * y[c] : 0.0f;
+        for (int c = 0; c < NC; ++c) g[c] = has_part(gi) ? -gi * y[c] : 0.0f;
         put_planes<RB, NC>(GS, L::GPLANE, i, c0, g);
       }
       leave();  // 3: -gam dY's planes are there, dO is read, V is there
@@ -360,7 +372,6 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
         a.dots[((tile * 3 + 0) * 2 + half) * TC_C + i] = (zy[0] + zy[1]) + (zy[2] + zy[3]);
         a.dots[((tile * 3 + 1) * 2 + half) * TC_C + i] = -((vy[0] + vy[1]) + (vy[2] + vy[3]));
       }
-      const float gC = gam[TC_C - 1];
       take();
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -632,7 +643,7 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       float s = has_part(gi) ? f0 * __uint_as_float(x[e]) : 0.0f;
-      if (f1 != 0.0f) s = fmaf(f1, __uint_as_float(h[e]), s);
+      if (has_part(f1)) s = fmaf(f1, __uint_as_float(h[e]), s);
       x[e] = __float_as_uint(s);
     }
     asm volatile(
@@ -701,12 +712,14 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
 
 // ---- gates ---------------------------------------------------------------------------
 // dg and dbeta of TC_EDGE chunks: a thread has a step, sums its document's dc to
-// the chunk's end, and what lies beyond comes from chunk to chunk after that. The
+// the chunk's end (and no other's, which may not be finite), and what lies beyond
+// comes from chunk to chunk after that. The
 // sums run in 64 bits: dc's signs change, and where memories are short a sum of
 // hundreds of them is small beside what it passes through (2.2e-6 off in 32 bits
 // against 1.3e-6, at worst of 250 cases; 22 us at the chain's size, 12 in 32 bits).
 __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcArgs a) {
-  __shared__ double tail[TC_EDGE][TC_C], from[TC_EDGE], after[TC_EDGE];
+  __shared__ double tail[TC_EDGE], from[TC_EDGE], after[TC_EDGE];
+  __shared__ int tseg[TC_EDGE];
   __shared__ float es[32];
   __shared__ unsigned marks[TC_EDGE][2];
   const int groups = (a.nc + TC_EDGE - 1) / TC_EDGE, k = threadIdx.x / TC_C, i = threadIdx.x % TC_C, lane = threadIdx.x & 31;
@@ -716,6 +729,7 @@ __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcA
   const size_t item = (size_t)bn * a.nc + ch;
   const float* rec = a.rec + item * REC_N * TC_C;
   float zy = 0.0f, bt = 1.0f;
+  int seg = 0;
   double c = 0.0;
   bool mark = false;  // the first step of a document
   if (live > 0) {
@@ -726,15 +740,17 @@ __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcA
       c += ((double)d[2 * TC_C + i] + d[3 * TC_C + i]) + ((double)d[4 * TC_C + i] + d[5 * TC_C + i]);
     }
     bt = rec[REC_BETA * TC_C + i];
-    mark = __float_as_int(rec[REC_SEG * TC_C + i]) != (i ? __float_as_int(rec[REC_SEG * TC_C + i - 1]) : 0);
+    seg = __float_as_int(rec[REC_SEG * TC_C + i]);
+    mark = seg != (i ? __float_as_int(rec[REC_SEG * TC_C + i - 1]) : 0);
   }
   const unsigned m = __ballot_sync(0xffffffffu, mark);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const double x = __shfl_down_sync(0xffffffffu, c, o);
-    if (lane + o < 32) c += x;
+    const int sx = __shfl_down_sync(0xffffffffu, seg, o);
+    if (lane + o < 32 && sx == seg) c += x;
   }
-  tail[k][i] = c;  // of the step's half chunk
+  if (i == 32) tail[k] = c, tseg[k] = seg;  // the second half's first document
   if (lane == 0) marks[k][i >> 5] = m;
   if (threadIdx.x < 32) {  // <S, dS> at the group's end: a lane has every 32nd part
     const int at = lo + TC_EDGE >= nch ? 0 : gr + 1;
@@ -744,9 +760,8 @@ __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcA
     es[threadIdx.x] = e;
   }
   __syncthreads();
-  auto sum_from = [&](int j) { return j >= TC_C ? 0.0 : j < 32 ? tail[k][j] + tail[k][32] : tail[k][j]; };
   const unsigned long long starts = (unsigned long long)marks[k][1] << 32 | marks[k][0], later = starts >> i >> 1;
-  double s = sum_from(i) - sum_from(later ? i + __ffsll(later) : TC_C);  // the document's steps from here on
+  double s = i < 32 && tseg[k] == seg ? c + tail[k] : c;  // the document's steps from here on
   if (i == 0) from[k] = s;
   __syncthreads();
   if (threadIdx.x == 0) {

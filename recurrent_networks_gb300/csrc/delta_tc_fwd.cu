@@ -98,9 +98,10 @@ __global__ void __launch_bounds__(128, 4) delta_tc_prep_kernel(DeltaTcArgs a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = h * 32 + lane;
-      const float rho = sg[h] == seg ? exp2f((float)(run - cs[h])) : 0.0f;
+      const bool last = sg[h] == seg;
+      const float rho = last ? keep_part(exp2f((float)(run - cs[h]))) : 0.0f;
       rec[REC_RHO * C + i] = rho;
-      rec[REC_BR * C + i] = be[h] * rho;
+      rec[REC_BR * C + i] = last ? keep_part(be[h] * rho) : 0.0f;
     }
   }
   cp_wait<0>();

@@ -1,7 +1,8 @@
 """A reset takes the state before it as zero, whatever it holds, wherever in a
 chunk or a segment it stands: the documents behind it give the bits that they give
-after a finite state, and the one before it is not made finite. Columns of v do
-not see one another's states."""
+after a finite state, and the one before it is not made finite. Backward, nothing
+of the last state's gradient comes to the documents before the last. Columns of v
+do not see one another's states."""
 import pytest
 import torch
 
@@ -70,3 +71,21 @@ def test_decays_that_end_in_zero(dtype):
     got = run(dict(p, state=torch.full_like(p["state"], float("inf"))), reset)
     assert not torch.isfinite(got[0][:, :20]).any()
     assert torch.equal(got[0][:, 20:], ref[0][:, 20:]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape,at", CASES, ids=lambda x: str(x) if isinstance(x, int) else "B%dT%dNk%dN%dDk%dDv%d" % x)
+def test_gradient_behind_a_reset(shape, at, dtype):
+    p = make(*shape, dtype, seed=24)
+    reset = marks(shape, max(at - 20, 0), at)
+    ref = dict(zip(NAMES, run(p, reset)))
+    for bad in BAD:
+        got = dict(zip(NAMES, run(dict(p, dlast=torch.full_like(p["dlast"], bad)), reset)))
+        for name in ("o", "last", "dstate", "dq"):
+            assert torch.equal(got[name], ref[name]), name
+        for name in ("dk", "dv", "dg", "dbeta"):
+            assert torch.equal(got[name][:, :at], ref[name][:, :at]), name
+        for name in ("dk", "dv", "dbeta"):
+            assert not torch.isfinite(got[name][:, at:]).any(), name
+        assert torch.isfinite(got["dg"][:, at]).all()  # a reset's own step has no decay
+        assert not torch.isfinite(got["dg"][:, at + 1:]).any()
