@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
     {
       bf16* y = a.dY + tile * NP * C * BV;
       float* dv = a.dv ? (float*)a.dv + vat + (size_t)ch * C * vstride + vt * BV : nullptr;
-      const int steps = min(C, a.T - ch * C), cols = a.Dv - vt * BV;
+      const int steps = min(C, a.T - ch * C), cols = a.Dv - vt * BV, live = live_steps(a, b, ch, C);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = m0 + (lane >> 2) + 8 * h;
@@ -164,11 +164,12 @@ __global__ void __launch_bounds__(256, 1) delta_bwd_chain_kernel(DeltaArgs a) {
           split_store(Ys + i * LDV + c, C * LDV, has_part(gi) ? -gi * x0 : 0.0f, has_part(gi) ? -gi * x1 : 0.0f);
           if (dv && i < steps) {
             float* p = dv + (size_t)i * vstride + c;
+            const float v0 = i < live ? x0 : 0.0f, v1 = i < live ? x1 : 0.0f;
             if (a.Dv % 2 == 0) {
-              if (c < cols) *(float2*)p = make_float2(x0, x1);
+              if (c < cols) *(float2*)p = make_float2(v0, v1);
             } else {
-              if (c < cols) p[0] = x0;
-              if (c + 1 < cols) p[1] = x1;
+              if (c < cols) p[0] = v0;
+              if (c + 1 < cols) p[1] = v1;
             }
           }
         }
@@ -427,7 +428,9 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
         for (int t = 0; t < NK; ++t) {
           const int c = k0 + nn0 + t * 8 + (lane & 3) * 2;
           if (c >= a.Dk) continue;
-          const float x0 = aq[t][2 * h], x1 = aq[t][2 * h + 1], y0 = dk[t][2 * h], y1 = dk[t][2 * h + 1];
+          const bool on = i < live;
+          const float x0 = on ? aq[t][2 * h] : 0.0f, x1 = on ? aq[t][2 * h + 1] : 0.0f;
+          const float y0 = on ? dk[t][2 * h] : 0.0f, y1 = on ? dk[t][2 * h + 1] : 0.0f;
           if (shared_heads) {
             float *p = a.pq + pat + i * pstride + c, *r = a.pk + pat + i * pstride + c;
             p[0] = x0;

@@ -353,6 +353,9 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
       leave();  // 3: -gam dY's planes are there, dO is read, V is there
       if (quad < 2 && !a.maps) {  // what leaves for memory goes while the product runs
         float zy[4] = {}, vy[4] = {};
+        if (i >= tc_live(a, b, ch))  // also where the state or its gradient is not finite
+#pragma unroll
+          for (int c = 0; c < NC; ++c) y[c] = 0.0f;
         uint4* low = (uint4*)(a.dYl + tile * 64 * BV) + (size_t)half * (NC / 8) * 64 + i;
 #pragma unroll
         for (int c = 0; c < NC; c += 8) {
@@ -677,7 +680,7 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
         float* p = (quad < 2 ? a.pk : a.pq) + pat + (size_t)i * pstride + c;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (e < a.Dk - c) p[e] = __uint_as_float(r[e]);
+          if (e < a.Dk - c) p[e] = i < live ? __uint_as_float(r[e]) : 0.0f;
       }
       __syncwarp();
     }
@@ -688,7 +691,7 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
       tm_wait_ld();
       float x[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]);
+      for (int e = 0; e < 16; ++e) x[e] = i < live ? __uint_as_float(r[e]) : 0.0f;
       unsigned char* d = KQ + (c >> 6) * TC_PANEL;
       *(uint4*)(d + img<128>(quad * 32 + lane, (c & 63) >> 3)) = round8(x);
       *(uint4*)(d + img<128>(quad * 32 + lane, ((c & 63) >> 3) + 1)) = round8(x + 8);

@@ -89,3 +89,17 @@ def test_gradient_behind_a_reset(shape, at, dtype):
             assert not torch.isfinite(got[name][:, at:]).any(), name
         assert torch.isfinite(got["dg"][:, at]).all()  # a reset's own step has no decay
         assert not torch.isfinite(got["dg"][:, at + 1:]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_steps_past_a_length(dtype):
+    """o and the gradients there are zero, whatever the state and its gradient hold."""
+    for T in (150, 2500):
+        p = make(2, T, 1, 1, 40, 48, dtype, seed=25)
+        lengths = torch.tensor([T - 13, 70], dtype=torch.int32, device="cuda")
+        for name in ("state", "dlast"):
+            for bad in BAD:
+                got = dict(zip(NAMES, run(dict(p, **{name: torch.full_like(p[name], bad)}), lengths=lengths)))
+                for out in ("o", "dq", "dk", "dv", "dg", "dbeta"):
+                    for i, n in enumerate(lengths.tolist()):
+                        assert (got[out][i, n:] == 0).all(), (name, out)
