@@ -403,6 +403,8 @@ int rnn_gated_step(int rows, int slots, int N, int D, int function, int dtype, c
  * steps past a length are not looked at, o and the gradients are 0 there. An
  * infinity or a NaN in q, k, v, g, beta or dO may reach every step of its row and
  * head; one in a state ends at the next reset, one in dlast at the last.
+ * bf16 with keep takes a |beta| below 2^-60 as 2^-60 with beta's sign: a shut gate
+ * then writes 1e-18 of its value, and its dbeta is the formula's.
  * Chunks of 64 steps (bf16) or 32 (fp32) are taken at once by matrix products
  * whose computed operands are held to 2^-24 (bf16 dq and dk: 2^-17). How the
  * chunks are spread over the GPU follows from the sizes, the number of SMs and

@@ -16,9 +16,9 @@
 //   dbeta_j = z_j.dY_j / beta_j,   dc_i = dO_i.o_i - dY_i.v_i,
 //   dg_t = the sum of dc_i over i >= t of t's document, to the chunk's end, +
 //          <S1, dS1> where the document goes on.
-// dY_j carries the factor beta_j throughout, so the quotient keeps its digits
-// for any beta_j but 0, which therefore counts as 2^-60 (far below a rounding
-// of anything it enters).
+// dY_j carries the factor beta_j throughout, so the quotient keeps its digits as
+// long as dY_j's planes do: where a backward comes, |beta_j| below 2^-60 counts as
+// 2^-60 (a shut gate, down to 0; far below a rounding of anything else it enters).
 //
 // The states, o, dY and all that fp32 outputs follow from are held to fp32: the
 // computed operands (S, Y, Z, TP, ...) in three bf16 planes, plane pairs (i, j)
@@ -44,6 +44,7 @@ namespace rnn {
 constexpr int TC_C = 64;        // steps of a chunk
 constexpr int TC_EDGE = 8;      // chunks between the states kept in fp32 for dg
 constexpr int TC_PANEL = 16384; // bytes of a panel of 128 rows
+constexpr float BETA_MIN = 0x1p-60f;
 
 struct DeltaTcArgs {
   int B, T, Nk, N, Dk, Dv;

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(128, 4) delta_tc_prep_kernel(DeltaTcArgs a) {
         const size_t row = (size_t)b * a.T + (size_t)ch * C + i;
         g = a.g[row * a.N + n];
         be[h] = a.beta[row * a.N + n];
-        if (be[h] == 0.0f) be[h] = 0x1p-60f;
+        if (a.Sh && fabsf(be[h]) < BETA_MIN) be[h] = copysignf(BETA_MIN, be[h]);  // a backward comes
         mark = a.reset && a.reset[row];
         if (g < -104.0f) mark = true;  // exp(g) is 0
         if (mark) g = 0.0f;

@@ -484,7 +484,8 @@ def gated_delta(q, k, v, g, beta, state=None, scale=None, reset=None, lengths=No
     Returns (o [B,T,N,Dv], last [B,1,N,Dk,Dv]: the state after the last step,
     fp32). Differentiable in q, k, v, g, beta and state; what is fp32 is fp32
     throughout. The last bits of fp32 results follow from how the steps are spread
-    over the GPU: from the sizes, and from whether a gradient will be asked for.
+    over the GPU: from the sizes, and from whether a gradient will be asked for;
+    where one will be, bf16 takes a |beta| below 2^-60 (a shut gate) as 2^-60.
     An infinity or a NaN in q, k, v, g or beta may reach every step of its row and
     head; one in the state ends at the next reset.
     status: an int32 CUDA tensor of one element, zeroed by the caller, in which
