@@ -111,7 +111,16 @@ template <typename T> __device__ __forceinline__ void act_both(int act, float x,
     slope = 1.0f;
     return;
   }
-  const float s = sigm<T>(x), c = s * (1.0f - s);
+  // s and s (1 - s) from e = exp(-|x|): 1 - s would be the rounding of s at an open gate
+  float e, r;
+  if constexpr (sizeof(T) == 2) {
+    e = exp2_fast(-1.4426950408889634f * fabsf(x));
+    r = rcp_fast(1.0f + e);
+  } else {
+    e = expf(-fabsf(x));
+    r = 1.0f / (1.0f + e);
+  }
+  const float s = x < 0.0f ? e * r : r, c = e * r * r;
   a = act == RNN_ACT_SILU ? x * s : s;
   slope = act == RNN_ACT_SILU ? fmaf(x, c, s) : c;
 }
