@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
       const bool more = ch > ch0;
       leave();  // 1: KQ, dO and dS's planes are there
       const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
-      const float gi = gam[i], bi = br[i], gC = gam[TC_C - 1];
+      const float gi = gam[i], bi = br[i];
       unsigned lost = 0;  // columns where the state's gradient is not finite and ends in this chunk
       float kept[NC];  // z (K's steps) or o (Q's), in fp32
       if (!a.maps) {
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
         tm_sum<NC, BV>(x, row + D1 + c0);
 #pragma unroll
         for (int c = 0; c < NC; ++c) x[c] = has_part(bi) ? bi * x[c] : 0.0f;  // no part of it before a later document
-        if (!has_part(gC))  // as the forward's Y
+        if (!has_part(gam[TC_C - 1]))  // as the forward's Y
 #pragma unroll
           for (int c = 0; c < NC; ++c)
             if (!isfinite(x[c])) {
@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
         a.dots[((tile * 3 + 0) * 2 + half) * TC_C + i] = (zy[0] + zy[1]) + (zy[2] + zy[3]);
         a.dots[((tile * 3 + 1) * 2 + half) * TC_C + i] = -((vy[0] + vy[1]) + (vy[2] + vy[3]));
       }
+      const float gC = gam[TC_C - 1];
       take();
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {

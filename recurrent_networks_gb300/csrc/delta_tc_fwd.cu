@@ -491,8 +491,8 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
       const bool more = ch + 1 < ch1;
       leave();  // 1: KQ, V and S's planes are there
       const float *gam = recs + (ch & 1) * 2 * TC_C, *br = gam + TC_C;
-      const float gi = gam[i], gC = gam[TC_C - 1];
-      unsigned lost = 0;  // columns whose state is not finite, where it ends in this chunk
+      const float gi = gam[i];
+      bool lost = false;  // whether a column's state is not finite and ends in this chunk
       float y[NC];
       if (ident)
 #pragma unroll
@@ -507,13 +507,10 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
         if (has_part(gi)) {  // behind a reset the old state has no part, whatever it holds
 #pragma unroll
           for (int c = 0; c < NC; ++c) y[c] = fmaf(-gi, x[c], y[c]);
-          if (!has_part(gC))  // the products with TP reach over the reset by zeros, which an infinity would pass
+          if (!has_part(gam[TC_C - 1]))  // the products with TP reach over the reset by zeros, which an infinity would pass
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-              if (!isfinite(x[c])) {
-                y[c] = 0.0f;
-                lost |= 1u << c;
-              }
+              if (!isfinite(x[c])) y[c] = 0.0f, lost = true;
         }
         put_planes<RB, NC>(YS, L::YPLANE, i, c0, y);
       } else {
@@ -537,10 +534,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
       if (a.maps) {
       } else if (quad < 2) {
         if (a.zf) {
-          if (lost)  // its z are no numbers
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (lost >> c & 1) z[c] = nanf("");
+          if (lost) z[0] = nanf("");  // for what is summed over z's columns: no more is made of this row's
           float4* f = (float4*)(a.zf + tile * 64 * BV) + (size_t)half * (NC / 4) * 64 + i;
 #pragma unroll
           for (int c = 0; c < NC; c += 4) f[(c / 4) * 64] = make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
@@ -556,6 +550,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_chain_kernel(DeltaTcArgs a, c
 #pragma unroll
         for (int c = 0; c < NC; c += 8) *(uint4*)(OS + img<RB>(i, (c0 + c) >> 3)) = round8(z + c);
       }
+      const float gC = gam[TC_C - 1];
       take();
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
