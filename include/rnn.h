@@ -383,7 +383,8 @@ int rnn_gated_bwd(const rnn_gated_dims_t *dims, const void *Wx, const void *b, c
  *     touched. No slot may appear twice. A slot >= slots counts as unused and
  *     sets RNN_ERANGE in `status`.
  *   pool [slots,N,D] fp32: read; pool_out: the new states are written here (pool
- *     itself, or another pool that keeps the old states valid)
+ *     itself, or another pool that keeps the old states valid and shares no memory
+ *     with it)
  *   status: a device word (4-byte aligned) that rnn_check_status reads, not
  *     cleared by this call, or NULL
  * Errors: RNN_EINVAL, RNN_ECUDA. */

@@ -342,6 +342,7 @@ int rnn_delta_step(int rows, int slots, int Nk, int N, int Dk, int Dv, int dtype
   for (const void* p : ptrs)
     if (p && !al16(p)) return RNN_EINVAL;
   if (!al4(slot) || !al4(status)) return RNN_EINVAL;
+  if (!pools_apart(pool, pool_out, (size_t)slots * N * Dk * Dv * sizeof(float))) return RNN_EINVAL;
   const int tiles = (Dv + 31) / 32;
   if ((long long)rows * N * tiles > INT_MAX) return RNN_EINVAL;
   if (rows == 0) return RNN_OK;

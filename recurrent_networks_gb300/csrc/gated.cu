@@ -1321,6 +1321,7 @@ int rnn_gated_step(int rows, int slots, int N, int D, int function, int dtype, c
   for (const void* p : ptrs)
     if (p && !al16(p)) return RNN_EINVAL;
   if (((uintptr_t)slot & 3u) || ((uintptr_t)status & 3u)) return RNN_EINVAL;
+  if (!pools_apart(pool, pool_out, (size_t)slots * N * D * sizeof(float))) return RNN_EINVAL;
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0) return RNN_OK;
   StepArgs a{rows, N * D, slots, Wx, b, slot, (const float*)pool, (float*)pool_out, h, (unsigned*)status};

@@ -195,6 +195,12 @@ int cluster_capacity_of(const void* func, const FusedShape& sh);
 int fused_capacity(int fn, bool bwd, const FusedShape& sh);
 // SM count of the current device; the GB300's 152 when no device can be asked.
 int device_sms();
+// A step's new states go where the old ones are, or apart from them: CTAs read and
+// write in any order.
+inline bool pools_apart(const void* pool, const void* out, size_t bytes) {
+  const uintptr_t a = (uintptr_t)pool, b = (uintptr_t)out;
+  return a == b || (a < b ? b - a : a - b) >= bytes;
+}
 cudaError_t fused_fwd_run(int fn, const FusedShape& sh, const FusedArgs& a, cudaStream_t st);
 cudaError_t grid_fwd_run(int fn, const FusedShape& sh, const FusedArgs& a, cudaStream_t st);
 struct UmmaMaps;

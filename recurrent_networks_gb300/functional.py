@@ -322,6 +322,8 @@ def _check_pool(pools, slots, M, shape, names, t, name):
         if not p.is_contiguous() or p.data_ptr() % 16 or p.get_device() != dev:
             raise ValueError(f"the pool must be contiguous, 16-byte aligned and on {name}'s device")
     P = pools[0].shape[0]
+    if len(pools) == 2 and 0 < abs(pools[0].data_ptr() - pools[1].data_ptr()) < 4 * pools[0].numel():
+        raise ValueError("pool_out must be the pool itself or share no memory with it")
     if slots is None:
         if M > P:
             raise ValueError(f"{M} rows need as many slots, the pool has {P}")
@@ -371,8 +373,8 @@ def gated_scan_step(Wx, b, pool, slots=None, function: str = "linear", pool_out=
     differentiable). Wx [M,G,N,D], b [G,N,D] or None, pool [P,N,D] fp32, slots
     [M] int32: each row's place in the pool, or None for the row's number; no
     slot twice; a negative slot marks an unused row (h = 0, no state touched).
-    The new states go to pool_out, by default the pool itself. Returns h
-    [M,N,D]. status: an int32 CUDA tensor of one element, zeroed by the caller,
+    The new states go to pool_out, by default the pool itself (another one shares
+    no memory with it). Returns h [M,N,D]. status: an int32 CUDA tensor of one element, zeroed by the caller,
     in which a slot past the pool is recorded (such a row counts as unused);
     _lib.rnn_check_status(status) raises for it."""
     _on_gpu(Wx, "gated_scan_step")
