@@ -22,6 +22,8 @@ CHECKPOINTS = {None: 0, "int8": 1}
 ACT_BLOCK = 32  # rows that share a scale in an 8-bit checkpoint
 ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
 NORM_MAX_WIDTH = 14336  # the group norm's widest group
+NORM_MAX_GROUPS = 65535
+NORM_MAX_CHANNELS = 1 << 28
 DELTA_MAX_D = 256  # the delta rule's largest Dk and Dv
 
 EXPORTS = ["rnn_num_gates", "rnn_num_states", "rnn_tape_size", "rnn_workspace_size", "rnn_fwd",

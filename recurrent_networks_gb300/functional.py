@@ -601,7 +601,7 @@ def group_norm(x, groups: int, weight=None, bias=None, gate=None, activation=Non
     t * act(gate). weight, bias [C] or None; activation None, "silu" or
     "sigmoid"; centered=False leaves the mean out (var is then the mean square).
     Differentiable in x, weight, bias and gate; the statistics and all sums are
-    fp32. Groups of up to 14336 channels."""
+    fp32. Up to 65535 groups of up to 14336 channels, 2^28 channels in all."""
     _on_gpu(x, "group_norm")
     if x.dtype not in _lib.DTYPES:
         raise TypeError(f"unsupported dtype {x.dtype}")
@@ -610,6 +610,8 @@ def group_norm(x, groups: int, weight=None, bias=None, gate=None, activation=Non
     C = x.shape[-1]
     if groups < 1 or C % groups:
         raise ValueError(f"{C} channels do not make {groups} groups")
+    if groups > _lib.NORM_MAX_GROUPS or C > _lib.NORM_MAX_CHANNELS:
+        raise ValueError(f"up to {_lib.NORM_MAX_GROUPS} groups and {_lib.NORM_MAX_CHANNELS} channels, got {groups} and {C}")
     if C // groups > _lib.NORM_MAX_WIDTH:
         raise ValueError(f"groups of up to {_lib.NORM_MAX_WIDTH} channels, got {C // groups}")
     if activation not in _lib.ACTIVATIONS:
