@@ -14,9 +14,11 @@
 //   dQ = gam dO' S0^T + R K,
 //   dK = -gam dY S0^T + beta H + (M + M^T) K + R^T Q,  H = rho Z dS1^T,
 //   dbeta_j = sum_i F_ij Gam_ij q_i.k_j + sum_i N_ij Gam_ij k_i.k_j + k_j.H_j,
-//   dc_i = sum_j E_ij - sum_j E_ji + q_i.(gam dO' S0^T)_i - k_i.(gam dY S0^T)_i - beta_i k_i.H_i,
-//   E = F P + N L, dc_{C-1} += sum_j beta_j k_j.H_j + gam_{C-1} <S0, dS1>,
-//   dg_t = the sum of dc_i over the steps i >= t of t's document.
+//   G_i = q_i.(gam dO' S0^T)_i - k_i.(gam dY S0^T)_i,  E = F P + N L,
+//   dg_t = what reaches over step t in its document:
+//          sum_{i >= t > j} E_ij + sum_{i >= t} G_i + sum_{j < t} beta_j k_j.H_j + gam_{C-1} <S0, dS1>.
+// (As a difference of sums of rows and columns of E, dg_t would have the error of
+// terms that do not reach over t and are not small with a_t.)
 //
 // This file has what the kernels of fp32 storage need (delta_fwd.cu, delta_bwd.cu);
 // those of bf16 storage are in delta_tc*.

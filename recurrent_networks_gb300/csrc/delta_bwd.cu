@@ -220,7 +220,7 @@ struct GradSmem {
   static __host__ __device__ size_t bytes(int DKP) {
     return 2 * ((size_t)2 * NP * C * (DKP + 8) + (size_t)2 * NP * C * (C + 8) + (size_t)NP * C * (BV + 8) +
                 (size_t)2 * NP * C * (BV + 8) + (size_t)2 * NP * GRAD_BK * (BV + 8)) +
-           4 * (REC_N * C + 4 * C + 4 * C + 3 * 4 * C + 3 * C + 16);
+           4 * (REC_N * C + C * (C + 1) + 4 * C + 3 * 4 * C + 2 * C + 16);
   }
 };
 
@@ -239,11 +239,11 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   bf16* Ss = Ys + NP * C * LDV;  // GRAD_BK rows of S0
   bf16* Ds = Ss + NP * GRAD_BK * LDV;  // of dS1
   float* rec = (float*)(Ds + NP * GRAD_BK * LDV);
-  float* rowE = rec + REC_N * C;  // [WN][C] partial sums
-  float* colB = rowE + 4 * C;     // [WM][C]
+  float* Es = rec + REC_N * C;    // [C][C + 1]: E below the diagonal
+  float* colB = Es + C * (C + 1); // [WM][C] partial sums
   float* dots = colB + 4 * C;     // [3][WN][C]: q.dq, k.dk1, k.H of the state's parts
-  float* fin = dots + 12 * C;     // [3][C]
-  float* wsum = fin + 3 * C;      // [8]
+  float* fin = dots + 12 * C;     // [2][C]
+  float* wsum = fin + 2 * C;      // [8]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long item = blockIdx.x;
   const int ch = (int)(item % a.nc), bn = (int)(item / a.nc), n = bn % a.N, b = bn / a.N, nk = n / (a.N / a.Nk);
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
       mma_acc<NT, false, true>(f, O, m0, Z, n0, BV);
       mma_acc<NT, false, true>(nn, Y, m0, Z, n0, BV);
     }
-    float rsum[2] = {0.0f, 0.0f}, csum[NT][2];
+    float csum[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) csum[t][0] = csum[t][1] = 0.0f;
 #pragma unroll
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
           const float nx = on && i > j ? -nn[t][2 * h + e] * ga : 0.0f;
           r[e] = fx * bj;
           const float e0 = on ? fx * qk[t][2 * h + e] + nx * kk[t][2 * h + e] : 0.0f;
-          rsum[h] += bj * e0;
+          Es[i * (C + 1) + j] = i > j ? bj * e0 : 0.0f;
           csum[t][e] += e0;
           if (i > j) {
             split_store1(Ms + i * LDC + j, C * LDC, nx * bj);
@@ -339,12 +339,6 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
         }
         split_store(Rs + i * LDC + n0 + t * 8 + (lane & 3) * 2, C * LDC, r[0], r[1]);
       }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      rsum[h] += __shfl_xor_sync(0xffffffffu, rsum[h], 1);
-      rsum[h] += __shfl_xor_sync(0xffffffffu, rsum[h], 2);
-      if ((lane & 3) == 0) rowE[wn * C + m0 + (lane >> 2) + 8 * h] = rsum[h];
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -460,37 +454,35 @@ __global__ void __launch_bounds__(256, 1) delta_grad_kernel(DeltaArgs a) {
   if (lane == 0) wsum[warp] = ss;
   __syncthreads();
   if (tid < C) {
-    float re = 0.0f, cb = 0.0f, d[3] = {};
+    float cb = 0.0f, d[3] = {};
 #pragma unroll
     for (int w = 0; w < WM; ++w) cb += colB[w * C + tid];
 #pragma unroll
-    for (int w = 0; w < WN; ++w) {
-      re += rowE[w * C + tid];
+    for (int w = 0; w < WN; ++w)
 #pragma unroll
       for (int k = 0; k < 3; ++k) d[k] += dots[(k * WN + w) * C + tid];
-    }
-    const float bt = beta[tid];
-    fin[tid] = re - bt * cb + d[0] + d[1] - bt * d[2];
-    fin[C + tid] = cb + d[2] + 0.0f * d[1];  // z is left finite where a reset follows a state that is not
-    fin[2 * C + tid] = bt * d[2];
+    fin[tid] = d[0] + d[1];
+    fin[C + tid] = beta[tid] * d[2];
+    // z is left finite where a reset follows a state that is not
+    if (tid < steps) a.dbeta[(row0 + tid) * a.N + n] = tid < live ? cb + d[2] + 0.0f * d[1] : 0.0f;
   }
   __syncthreads();
-  if (tid < steps) {
+  {  // dg: what reaches over a step, 8 threads a step
+    static_assert(C * 8 == 256, "all threads");
+    const int t = tid >> 3, k = tid & 7;
     const float* seg = rec + REC_SEG * C;
-    const int mine = __float_as_int(seg[tid]);
-    const bool mark = mine != (tid ? __float_as_int(seg[tid - 1]) : 0);
+    const bool mark = __float_as_int(seg[t]) != (t ? __float_as_int(seg[t - 1]) : 0);
     float s = 0.0f;
-    if (mine == __float_as_int(seg[C - 1])) {  // the end of the chunk
-      float tot = 0.0f, w = 0.0f;
-      for (int i = 0; i < C; ++i) tot += fin[2 * C + i];
-      for (int i = 0; i < 8; ++i) w += wsum[i];
-      s = tot + (has_part(gam[C - 1]) ? gam[C - 1] * w : 0.0f);
+    for (int i = t + k; i < C; i += 8) {
+      float r = fin[i];
+      for (int j = 0; j < t; ++j) r += Es[i * (C + 1) + j];
+      s += r;
     }
-    for (int i = C - 1; i >= tid; --i)
-      if (__float_as_int(seg[i]) == mine) s += fin[i];
-    const size_t at = (row0 + tid) * a.N + n;
-    a.dg[at] = tid < live && !mark ? s : 0.0f;
-    a.dbeta[at] = tid < live ? fin[C + tid] : 0.0f;
+    for (int j = k; j < t; j += 8) s += fin[C + j];
+    if (has_part(gam[C - 1])) s = fmaf(gam[C - 1], wsum[k], s);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (k == 0 && t < steps) a.dg[(row0 + t) * a.N + n] = t < live && !mark ? s : 0.0f;
   }
 }
 
