@@ -148,7 +148,7 @@ struct DeltaSizes {
   size_t rec, tri, S, Z, zf, sf;  // bytes
   size_t M, H;                    // of the segments' maps, of H and of the states between
   size_t tape;
-  size_t dots, edge, part, bwd;
+  size_t dots, edge, near, cross, part, bwd;
 };
 
 bool delta_heads_ok(int Nk, int N, int Dk, int Dv, int dtype) {
@@ -189,7 +189,9 @@ bool delta_sizes(const rnn_delta_dims_t* d, bool keep, DeltaSizes* z) {
     if (keep) z->tape += z->S + 2 * z->zf + z->sf;
     z->dots = up256(n * z->nvt * 6 * TC_C * 4);
     z->edge = up256(heads * z->ne * z->nvt * 8 * 4);
-    z->bwd = z->S + z->Z + z->dots + z->edge + 2 * z->H;
+    z->near = up256(n * TC_C * 4);
+    z->cross = up256(n * z->nvt * 3 * 4);
+    z->bwd = z->S + z->Z + z->dots + z->edge + z->near + z->cross + 2 * z->H;
   } else {
     z->tri = up256(n * z->NP * z->C * z->C * 2);  // each of Tm and P
     z->S = up256(n * z->nvt * z->NP * z->KP * z->BV * 2);
@@ -322,7 +324,9 @@ int rnn_delta_bwd(const rnn_delta_dims_t* d, const void* q, const void* k, const
     a.dYl = (bf16*)(w += z.S);
     a.dots = (float*)(w += z.Z);
     a.edge = (float*)(w += z.dots);
-    a.Ht = (float*)(w += z.edge);
+    a.near = (float*)(w += z.edge);
+    a.cross = (float*)(w += z.near);
+    a.Ht = (float*)(w += z.cross);
     a.St = (float*)(w += z.H);
     return cuda_status(delta_tc_bwd_launch(z.BV, a, st));
   }

@@ -16,6 +16,9 @@
 //   dbeta_j = z_j.dY_j / beta_j,   dc_i = dO_i.o_i - dY_i.v_i,
 //   dg_t = the sum of dc_i over i >= t of t's document, to the chunk's end, +
 //          <S1, dS1> where the document goes on.
+// That sum's terms do not become small with a_t. Where g_t is below GATE_NEAR, dg_t
+// is taken as what reaches over the step (delta.cuh), from the grad kernel's operands
+// in two planes.
 // dY_j carries the factor beta_j throughout, so the quotient keeps its digits as
 // long as dY_j's planes do: where a backward comes, |beta_j| below 2^-60 counts as
 // 2^-60 (a shut gate, down to 0; far below a rounding of anything else it enters).
@@ -45,6 +48,19 @@ constexpr int TC_C = 64;        // steps of a chunk
 constexpr int TC_EDGE = 8;      // chunks between the states kept in fp32 for dg
 constexpr int TC_PANEL = 16384; // bytes of a panel of 128 rows
 constexpr float BETA_MIN = 0x1p-60f;
+// Which of its two sums dg_t is taken from, the row products' or (below) what reaches
+// over the step. Off by (L2, T = 512, heads of 64, all steps with this g)
+//   g                       -0.01   -0.1    -0.5    -1      -5      -10     -20
+//   row products            8.0e-7  8.5e-7  4.8e-6  6.3e-6  1.6e-4  5.6e-2  1e3
+//   what reaches over       5.9e-6  3.6e-6  5.3e-6  2.9e-6  3.4e-6  3.4e-6  3.6e-6
+// The second costs a chunk of it 11 % of the back chain and 12 % of the grad kernel
+// (418 us for 377 and 306 for 273 at the chain's size with all chunks), and a chunk
+// without such a step nothing but the question.
+constexpr float GATE_NEAR = -0.75f;
+// What bf16 storage has in rho's place in rec (its kernels need beta rho alone): 2
+// for a step whose g is below GATE_NEAR, 1 for the others of a chunk with such a step,
+// 0 in a chunk without one.
+constexpr int REC_NEAR = REC_RHO;
 
 struct DeltaTcArgs {
   int B, T, Nk, N, Dk, Dv;
@@ -78,6 +94,8 @@ struct DeltaTcArgs {
   bf16* dYl;           // [items][nvt][BV / 8][64][8] the second plane of dY (the first is dv)
   float* dots;         // [items][nvt][3][2][64]: z.dY, -v.dY, o.dO of half a tile's columns
   float* edge;         // [B N][ne][nvt][8]: <S, dS> there, by warp
+  float* near;         // [items][64] dg without the next, of chunks with a step that wants it
+  float* cross;        // [items][nvt][3] <S0, dS1>, by warp
   void *dq, *dk, *dv;
   float *dg, *dbeta, *ds0;
   float *pq, *pk;

@@ -185,8 +185,87 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
             mbar_wait_bounded<false>(bar_tp + 8 * (p >> 1), p & 1, a.wait_limit_ns, nullptr, f);
           }
       }
+    } else if (a.tma || warp == 9) {  // ---- <S0, dS1>
+      // Of the chunks whose gates want it, from two planes of each, which are laid out
+      // alike: a third between each two barriers, the pieces of S0 loaded between the
+      // two before. A thread's pieces of both go to mma.sync as they are, in the same
+      // places of A and B; the diagonal of the 8 x 8 products is theirs.
+      const int cw = warp - 9, cws = a.tma ? 3 : 1;  // rows that TMA cannot take keep the other two warps busy
+      const int bytes = a.KP * RB;
+      constexpr int CU = 4;  // pieces of 16 bytes that a thread has of a third at once
+      uint4 sx[CU][2];
+      float dot[4];
+      unsigned wanted = 0;  // of the 32 chunks around
+      auto wants = [&](int ch) -> bool {
+        if (ch < ch0 || a.maps) return false;
+        if (ch == ch1 - 1 || (ch & 31) == 31) {
+          const int k = (ch & ~31) + lane;
+          wanted = __ballot_sync(0xffffffffu, k <= ch && a.rec[(((size_t)bn * a.nc + k) * REC_N + REC_NEAR) * TC_C] != 0.0f);
+        }
+        return wanted >> (ch & 31) & 1;
+      };
+      auto place = [&](int part, int u) { return (((u * 3 + part) * cws + cw) * 32 + lane) * 16; };
+      auto fetch = [&](int ch, int part, int u0) {
+        const unsigned char* s0 = (const unsigned char*)(a.Sh + (((size_t)bn * a.nc + ch) * a.nvt + vt) * 2 * a.KP * BV);
+#pragma unroll
+        for (int u = 0; u < CU; ++u) {
+          const int o = place(part, u0 + u);
+          sx[u][0] = sx[u][1] = make_uint4(0, 0, 0, 0);
+          if (o < bytes) {
+            sx[u][0] = __ldg((const uint4*)(s0 + o));
+            sx[u][1] = __ldg((const uint4*)(s0 + bytes + o));
+          }
+        }
+      };
+      auto add = [&](const uint4& p, const uint4& q) {
+        const uint32_t a0[4] = {p.x, 0, p.y, 0}, a1[4] = {p.z, 0, p.w, 0};
+        mma_bf16_16816(dot, a0, q.x, q.y);
+        mma_bf16_16816(dot, a1, q.z, q.w);
+      };
+      auto cross = [&](int ch, int part) {
+        for (int u0 = 0;; u0 += CU) {
+#pragma unroll
+          for (int u = 0; u < CU; ++u) {
+            const int o = place(part, u0 + u), at = o < bytes ? o : 0;  // past the end x is zero
+            const uint4 y = *(const uint4*)(SS + at), yl = *(const uint4*)(SS + L::SPLANE + at);
+            add(sx[u][1], y);
+            add(sx[u][0], yl);
+            add(sx[u][0], y);
+          }
+          if (place(part, u0 + CU) - lane * 16 >= bytes) break;
+          fetch(ch, part, u0 + CU);
+        }
+      };
+      bool want = wants(ch1 - 1);
+      if (want) fetch(ch1 - 1, 0, 0);
+      for (int ch = ch1 - 1; ch >= ch0; --ch) {
+        dot[0] = dot[1] = dot[2] = dot[3] = 0.0f;
+        __syncthreads();  // 1
+        if (want) {
+          cross(ch, 0);
+          fetch(ch, 1, 0);
+        }
+        __syncthreads();  // 2
+        if (want) {
+          cross(ch, 1);
+          fetch(ch, 2, 0);
+        }
+        __syncthreads();  // 3
+        if (want) {
+          cross(ch, 2);
+          // of rows lane / 4 and columns lane % 4 * 2 and one on
+          float d = lane >> 2 == (lane & 3) * 2 ? dot[0] : lane >> 2 == (lane & 3) * 2 + 1 ? dot[1] : 0.0f;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+          float* to = a.cross + (((size_t)bn * a.nc + ch) * a.nvt + vt) * 3;
+          if (lane < 3 && (lane == cw || cws == 1)) to[lane] = lane == cw ? d : 0.0f;
+        }
+        want = wants(ch - 1);
+        if (want) fetch(ch - 1, 0, 0);
+        __syncthreads();  // 4
+      }
     } else {  // ---- rows that TMA cannot take
-      const int t = a.tma ? -1 : tid - 320;  // warps 10 and 11
+      const int t = tid - 320;  // warps 10 and 11
       const size_t kstride = (size_t)a.Nk * a.Dk, kat = (size_t)b * a.T * kstride + (size_t)nk * a.Dk;
       auto load_kq = [&](int ch) {
         unsigned char* d = sm + (ch % KST) * L::KQ;
@@ -205,16 +284,16 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
       auto store_dv = [&](int ch) {
         store_img<RB, 64>(t, VS, (bf16*)a.dv + vat + (size_t)ch * TC_C * vstride, vstride, min(TC_C, a.T - ch * TC_C), a.Dv, vt * BV);
       };
-      if (t >= 0 && ch0 < ch1) {
+      if (ch0 < ch1) {
         load_kq(ch1 - 1);
         load_o(ch1 - 1);
         cp_wait_all();
         fence_proxy_async_smem();
       }
       for (int ch = ch1 - 1; ch >= ch0; --ch) {
-        const bool more = ch > ch0 && t >= 0;
+        const bool more = ch > ch0;
         __syncthreads();  // 1
-        if (t >= 0 && !a.maps) {
+        if (!a.maps) {
           if (ch + 1 < ch1) store_dv(ch + 1);
           asm volatile("bar.sync 1, 64;" ::: "memory");  // the rows are read: V's may follow
           load_img<RB, BV / 8, 64>(t, VS, 0, (const bf16*)a.v + vat + (size_t)ch * TC_C * vstride, vstride, tc_live(a, b, ch), a.Dv,
@@ -234,7 +313,7 @@ __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, co
           fence_proxy_async_smem();
         }
       }
-      if (t >= 0 && ch0 < ch1 && !a.maps) store_dv(ch0);
+      if (ch0 < ch1 && !a.maps) store_dv(ch0);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -425,7 +504,10 @@ template <int KT, int BV> struct TcGrad {  // KT: Dk rounded up to 128 or 256
   // planes of tiles of S0 and dS1 at once; one where two CTAs an SM fit then
   static constexpr int STAGES = KT == 128 && BV == 64 ? 1 : 2;
   static constexpr int SD = STAGES * 2 * SB > 2 * TC_PANEL ? STAGES * 2 * SB : 2 * TC_PANEL;
-  static __host__ __device__ constexpr int at_sd(int nvt) { return nvt * XZ > KQ + 2 * TC_PANEL ? nvt * XZ : KQ + 2 * TC_PANEL; }
+  // what reaches over a step: E's columns by warps' rows, G and H by halves, E's rows
+  static constexpr int NEAR_E = 0, NEAR_G = 4 * 64, NEAR_H = NEAR_G + 2 * 128, NEAR_T = NEAR_H + 2 * 64, NEAR = (NEAR_T + 2 * 32) * 4;
+  static constexpr int LATE = KQ + 2 * TC_PANEL + NEAR;  // what X's and Z's place holds when they are done with
+  static __host__ __device__ constexpr int at_sd(int nvt) { return nvt * XZ > LATE ? nvt * XZ : (LATE + 1023) & ~1023; }
   static __host__ __device__ constexpr size_t bytes(int nvt) { return (size_t)at_sd(nvt) + SD + 3 * TC_C * 4 + TC_C + 64; }
   static constexpr int COLS = KT == 128 ? 256 : 512;
 };
@@ -494,6 +576,7 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
   const float* own = a.rec + (size_t)item * REC_N * TC_C;
   const int i = (quad & 1) * 32 + lane, j0 = half * 32;  // this thread's step and columns of M and R
   const float gi = own[REC_GAM * TC_C + i], bri = own[REC_BR * TC_C + i];
+  const bool near = own[REC_NEAR * TC_C] != 0.0f;  // the chunk's gates want what reaches over a step
   for (int p = 0; p < a.nvt; ++p) {
     unsigned char* x = X + p * L::XZ;
     load_img<RB, BV / 8, 256>(tid, x, 0, (const bf16*)a.dv + vat, vstride, live, a.Dv, p * BV, BV, 0);
@@ -637,13 +720,32 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
       *(bf16*)(ML + at) = __float2bfloat16_rn(nf[c] - __bfloat162float(hi));
     }
   }
-  // The state's parts, scaled by rows in fp32, back into the first accumulator
+  if (near) {  // K's and Q's rows are looked at
+    cp_wait_all();
+    __syncthreads();
+  }
+  // The state's parts, scaled by rows in fp32, back into the first accumulator; with
+  // the row itself they make G and H
   const float f0 = quad < 2 ? -gi : a.scale * gi, f1 = quad < 2 ? bri : 0.0f;
+  float gsum = 0.0f, hsum = 0.0f;
   for (int c = half * 16; c < a.KP; c += 32) {
     uint32_t x[16], h[16];
     tm_ld16(x, row + c);
     tm_ld16(h, row + KT + c);
     tm_wait_ld();
+    if (near) {
+      const unsigned char* im = KQ + (c >> 6) * TC_PANEL;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float k[8];
+        widen8(*(const uint4*)(im + img<128>(quad * 32 + lane, ((c & 63) >> 3) + u)), k);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (has_part(gi)) gsum = fmaf(k[e], f0 * __uint_as_float(x[u * 8 + e]), gsum);
+          if (has_part(f1)) hsum = fmaf(k[e], f1 * __uint_as_float(h[u * 8 + e]), hsum);
+        }
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       float s = has_part(gi) ? f0 * __uint_as_float(x[e]) : 0.0f;
@@ -669,9 +771,89 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
     for (int k = 0; k < 8; ++k) tc_mma(tm, m + (k >> 2) * (TC_PANEL >> 4) + (k & 3) * 2, k0 + k * 128, id, true);
 #pragma unroll
     for (int k = 0; k < 8; ++k) tc_mma(tm, ml + (k >> 2) * (TC_PANEL >> 4) + (k & 3) * 2, k0 + k * 128, id, true);
+    if (near) {  // [K K^T; Q K^T], in the second accumulator's columns
+      const uint64_t kq = tc_desc(smem_u32(KQ), 16);
+      for (int k = 0; k < (a.KP + 63) >> 6 << 2; ++k) {
+        const uint64_t at = kq + (k >> 2) * (TC_PANEL >> 4) + (k & 3) * 2;
+        tc_mma(tm + KT, at, at, tc_idesc(64, false, false), k);
+      }
+    }
     tc_commit(bar);
   }
   take();
+  if (near) {
+    // E_ij = M_ij k_i.k_j + R_ij q_i.k_j, j < i, from M's and R's planes; a thread has
+    // 32 columns of a row. Summed along the row up to t - 1, then over the rows from t
+    // on, it reaches over t.
+    float* sums = (float*)(ML + 2 * TC_PANEL);
+    float e[32];
+    {
+      uint32_t r[32];
+      tm_ld16(r, row + KT + j0);
+      tm_ld16(r + 16, row + KT + j0 + 16);
+      tm_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) {
+        const uint32_t at = img<128>(quad * 32 + lane, (j0 + c) >> 3);
+        float hi[8], lo[8];
+        widen8(*(const uint4*)(SD + at), hi);
+        widen8(*(const uint4*)(ML + at), lo);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[c + k] = j0 + c + k < i ? (hi[k] + lo[k]) * __uint_as_float(r[c + k]) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int c = 1; c < 32; ++c) e[c] += e[c - 1];
+    float rest = e[31];  // of the row's first half: reaches over all of the second's steps up to i
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (j0 + c + 1 > i) e[c] = 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)  // the warp's rows: lane l keeps column l
+#pragma unroll
+      for (int c = 0; c < o; ++c) {
+        const bool up = lane & o;
+        const float keep = up ? e[c + o] : e[c], give = up ? e[c] : e[c + o];
+        e[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    sums[L::NEAR_E + quad * 64 + j0 + lane] = e[0];  // over t = j0 + lane + 1
+    if (half == 0 && (quad & 1)) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_down_sync(0xffffffffu, rest, o);
+        if (lane + o < 32) rest += x;
+      }
+      sums[L::NEAR_T + (quad >> 1) * 32 + lane] = rest;
+    }
+    sums[L::NEAR_G + half * 128 + quad * 32 + lane] = gsum;
+    if (quad < 2) sums[L::NEAR_H + half * 64 + i] = hsum;
+    __syncthreads();
+    if (warp == 0) {  // steps lane and 32 + lane
+      const float *E = sums + L::NEAR_E + lane, *G = sums + L::NEAR_G + lane, *H = sums + L::NEAR_H + lane, *T = sums + L::NEAR_T + lane;
+      float g[2], h[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        g[u] = (G[32 * u] + G[128 + 32 * u]) + (G[64 + 32 * u] + G[192 + 32 * u]);
+        h[u] = H[32 * u] + H[64 + 32 * u];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float x = __shfl_down_sync(0xffffffffu, g[u], o), y = __shfl_up_sync(0xffffffffu, h[u], o);
+          if (lane + o < 32) g[u] += x;
+          if (lane >= o) h[u] += y;
+        }
+      }
+      g[0] += __shfl_sync(0xffffffffu, g[1], 0);
+      const float h31 = __shfl_sync(0xffffffffu, h[0], 31);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {  // of the steps before
+        h[u] = __shfl_up_sync(0xffffffffu, h[u], 1);
+        if (lane == 0) h[u] = 0.0f;
+      }
+      float* to = a.near + (size_t)item * TC_C + lane;
+      to[0] = g[0] + h[0] + (lane ? (E[-1] + E[63]) + (E[127] + E[191]) : 0.0f);
+      to[32] = g[1] + (h[1] + h31) + ((E[31] + E[95]) + (E[159] + E[223])) + (lane ? T[0] + T[32] : 0.0f);
+    }
+  }
   if (shared_heads) {
     for (int c = half * 16; c < a.KP; c += 32) {
       uint32_t r[16];
@@ -733,6 +915,7 @@ __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcA
   const size_t item = (size_t)bn * a.nc + ch;
   const float* rec = a.rec + item * REC_N * TC_C;
   float zy = 0.0f, bt = 1.0f;
+  bool near = false;
   int seg = 0;
   double c = 0.0;
   bool mark = false;  // the first step of a document
@@ -744,6 +927,7 @@ __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcA
       c += ((double)d[2 * TC_C + i] + d[3 * TC_C + i]) + ((double)d[4 * TC_C + i] + d[5 * TC_C + i]);
     }
     bt = rec[REC_BETA * TC_C + i];
+    near = rec[REC_NEAR * TC_C + i] == 2.0f;
     seg = __float_as_int(rec[REC_SEG * TC_C + i]);
     mark = seg != (i ? __float_as_int(rec[REC_SEG * TC_C + i - 1]) : 0);
   }
@@ -781,6 +965,12 @@ __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcA
   if (ch >= a.nc || ch * TC_C + i >= a.T) return;
   const size_t out = ((size_t)b * a.T + (size_t)ch * TC_C + i) * a.N + n;
   if (i < live && !later) s += after[k];
+  if (near) {
+    s = a.near[item * TC_C + i];
+    const float gC = rec[REC_GAM * TC_C + TC_C - 1];
+    if (has_part(gC))
+      for (int w = 0; w < a.nvt * 3; ++w) s += gC * a.cross[item * a.nvt * 3 + w];
+  }
   a.dg[out] = i < live && !mark ? (float)s : 0.0f;
   a.dbeta[out] = i < live ? zy / bt : 0.0f;
 }

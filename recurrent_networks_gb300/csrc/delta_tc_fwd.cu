@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(128, 4) delta_tc_prep_kernel(DeltaTcArgs a) {
   if (warp == 0) {  // the running sum of g (to the base 2), in 64 bits, and the documents
     double run = 0.0, cs[2];
     int seg = 0, sg[2];
+    bool near[2];
     float be[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -76,6 +77,7 @@ __global__ void __launch_bounds__(128, 4) delta_tc_prep_kernel(DeltaTcArgs a) {
         if (g < -104.0f) mark = true;  // exp(g) is 0
         if (mark) g = 0.0f;
       }
+      near[h] = g < GATE_NEAR;
       double c = (double)g * 1.4426950408889634;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -95,13 +97,12 @@ __global__ void __launch_bounds__(128, 4) delta_tc_prep_kernel(DeltaTcArgs a) {
       rec[REC_GAM * C + i] = sg[h] == 0 ? keep_part(exp2f((float)c)) : 0.0f;
       rec[REC_BETA * C + i] = be[h];
     }
+    const bool some = __any_sync(0xffffffffu, near[0] || near[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = h * 32 + lane;
-      const bool last = sg[h] == seg;
-      const float rho = last ? keep_part(exp2f((float)(run - cs[h]))) : 0.0f;
-      rec[REC_RHO * C + i] = rho;
-      rec[REC_BR * C + i] = last ? keep_part(be[h] * rho) : 0.0f;
+      rec[REC_BR * C + i] = sg[h] == seg ? keep_part(be[h] * exp2f((float)(run - cs[h]))) : 0.0f;
+      rec[REC_NEAR * C + i] = near[h] ? 2.0f : some ? 1.0f : 0.0f;
     }
   }
   cp_wait<0>();

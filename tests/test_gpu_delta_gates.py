@@ -4,11 +4,13 @@ digits: the step's own part of o and of dY, which is not small, is not in it.
 
 Tolerances (L2, over steps of one decay). A sum of products of signed terms has the
 terms' relative error, taken as independent, at the sum's own size. fp32: as in
-test_gpu_delta.py, and 2^-24 |g| by the rounded exponent: 2^-24 (64 + T / 4 + 3 |g|)."""
+test_gpu_delta.py, and 2^-24 |g| by the rounded exponent: 2^-24 (64 + T / 4 + 3 |g|).
+bf16: operands in two bf16 planes, 2^-17 of a value at most (dY, Z, S0, dS1, M or R):
+five of them, below 2^-14."""
 import pytest
 import torch
 
-from test_gpu_delta import F32, make, oracle, run
+from test_gpu_delta import BF, F32, make, oracle, run
 
 pytestmark = pytest.mark.gpu
 
@@ -21,10 +23,10 @@ def off(got, ref):
 
 
 def limit(dtype, T, g):
-    return 2.0 ** -24 * (64 + T / 4 + 3 * abs(g))
+    return 2.0 ** -14 if dtype == BF else 2.0 ** -24 * (64 + T / 4 + 3 * abs(g))
 
 
-@pytest.mark.parametrize("dtype", [F32], ids=["f32"])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "B%dT%dNk%dN%dDk%dDv%d" % s)
 def test_one_decay(shape, dtype):
     p = make(*shape, dtype, seed=41)
@@ -34,7 +36,7 @@ def test_one_decay(shape, dtype):
         assert e <= limit(dtype, shape[1], g), f"g {g}: {e:.3g}"
 
 
-@pytest.mark.parametrize("dtype", [F32], ids=["f32"])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "B%dT%dNk%dN%dDk%dDv%d" % s)
 def test_decays_of_all_sizes(shape, dtype):
     """Long memories with a cut here and there, around the ends of chunks among them, and resets."""
