@@ -407,7 +407,8 @@ int rnn_gated_step(int rows, int slots, int N, int D, int function, int dtype, c
  * bf16 with keep takes a |beta| below 2^-60 as 2^-60 with beta's sign: a shut gate
  * then writes 1e-18 of its value, and its dbeta is the formula's.
  * Chunks of 64 steps (bf16) or 32 (fp32) are taken at once by matrix products
- * whose computed operands are held to 2^-24 (bf16 dq and dk: 2^-17). How the
+ * whose computed operands are held to 2^-24 (bf16 dq and dk: 2^-17, and dg where g
+ * is below -0.75). How the
  * chunks are spread over the GPU follows from the sizes, the number of SMs and
  * keep; it moves the last bits of fp32 results. No result depends on the run.
  */

@@ -23,9 +23,10 @@ template <int BV, int MT> struct TcBack {
 // until dY's products have read it, then -gam dY; rows 64 .. 127 scale gam dO,
 // written by the threads of Q's steps while the first product runs. dY goes out
 // through V's image, each value in the place of the v that its thread has read.
+// Warps 9 to 11 take <S0, dS1> of the chunks with a step below GATE_NEAR.
 // The products for dY take TP by columns, 64 of them; the other 64 rows of the
 // accumulator come from whatever lies a panel further (inside this CTA's shared
-// memory) and are not looked at. Bound as the forward's chain: 368 us at its size.
+// memory) and are not looked at. Bound as the forward's chain: 377 us at its size.
 template <int BV, int MT>
 __global__ void __launch_bounds__(384, 1) delta_tc_back_kernel(DeltaTcArgs a, const __grid_constant__ TcMaps maps) {
   using L = TcBack<BV, MT>;
@@ -520,7 +521,9 @@ static_assert(TcGrad<128, 64>::bytes(4) <= 227 * 1024 && TcGrad<128, 32>::bytes(
 // dS1, their second from behind KQ, which has X's and Z's place. The products of
 // 64 rows (Z's, dY's second plane) read as many rows behind them: Z's results
 // there are not looked at, dY's are not written, since dO's stand there.
-// Measured 269 us at the chain's size, where its 1.14 GB take 168: an item waits
+// Where a step is below GATE_NEAR, the rows of the state's parts times K's and Q's,
+// and K K^T and Q K^T times M and R, give what reaches over each step of the chunk.
+// Measured 273 us at the chain's size, where its 1.14 GB take 168: an item waits
 // for its loads, two CTAs an SM cover half of it. Single buffers for the planes,
 // two in flight, took 353 us (of 324 then: the issuing thread waits in turn).
 template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 : 1) delta_tc_grad_kernel(DeltaTcArgs a) {
@@ -899,10 +902,11 @@ template <int KT, int BV> __global__ void __launch_bounds__(256, KT == 128 ? 2 :
 // ---- gates ---------------------------------------------------------------------------
 // dg and dbeta of TC_EDGE chunks: a thread has a step, sums its document's dc to
 // the chunk's end (and no other's, which may not be finite), and what lies beyond
-// comes from chunk to chunk after that. The
-// sums run in 64 bits: dc's signs change, and where memories are short a sum of
-// hundreds of them is small beside what it passes through (2.2e-6 off in 32 bits
-// against 1.3e-6, at worst of 250 cases; 22 us at the chain's size, 12 in 32 bits).
+// comes from chunk to chunk after that. The sums run in 64 bits: dc's signs change,
+// and where memories are short a sum of hundreds of them is small beside what it
+// passes through (21 us at the chain's size, 12 in 32 bits, which are twice as far
+// off). How far dc's own rounding carries is at GATE_NEAR; steps below it have their
+// dg from the grad kernel and the back chain.
 __global__ void __launch_bounds__(TC_EDGE * TC_C) delta_tc_gates_kernel(DeltaTcArgs a) {
   __shared__ double tail[TC_EDGE], from[TC_EDGE], after[TC_EDGE];
   __shared__ int tseg[TC_EDGE];

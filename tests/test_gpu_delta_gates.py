@@ -55,3 +55,21 @@ def test_decays_of_all_sizes(shape, dtype):
         at = (pick == k) & ~reset[..., None]
         e = off(got[at.cuda()], ref[at])
         assert e <= limit(dtype, T, sizes[k].item()), f"g {sizes[k]}: {e:.3g}"
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_ragged_rows(dtype):
+    """Rows of several lengths, whatever stands past them, on a long axis too."""
+    for shape in ((4, 150, 1, 2, 40, 48), (2, 2500, 1, 1, 32, 32)):
+        p = make(*shape, dtype, seed=43)
+        B, T = shape[:2]
+        p["g"] = 12 * p["g"] - 2
+        lengths = torch.tensor([T - 13, 70, 0, 1][:B], dtype=torch.int32)
+        ref = torch.as_tensor(oracle(p, None, lengths)[5])
+        for i in range(B):
+            for name in ("q", "k", "v", "g", "beta", "do"):
+                p[name][i, int(lengths[i]):] = float("nan")
+        got = run(p, None, lengths.cuda())[5]
+        for i, n in enumerate(lengths.tolist()):
+            assert (got[i, n:] == 0).all()
+        assert off(got, ref) <= limit(dtype, T, -2.0)

@@ -49,7 +49,8 @@ def test_delta(shape, dtype):
     B, T = shape[:2]
     short = torch.tensor([T // 2 + 3, T, 0][:B], dtype=torch.int32, device="cuda")
     marks = (torch.rand(B, T, generator=torch.Generator().manual_seed(2)) < 0.004).cuda()
-    for lengths, reset in ((None, None), (short, marks)):
+    for lengths, reset, decay in ((None, None, 1), (short, marks, 1), (None, marks, 30)):  # the last: states soon forgotten
+        p["g"] = p["g"] * decay
         for keep in (True, False):
             clean, dirty = (run(p, fill, lengths, reset, keep) for fill in (0, 255))
             for name, a, b in zip(("o", "last", *LEAVES), clean, dirty):
