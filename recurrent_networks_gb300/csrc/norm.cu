@@ -157,7 +157,7 @@ __device__ __forceinline__ float backward_value(int act, float n, float w, float
 // two; MANY: of several warps) hold a group's channels in registers. A CTA takes
 // gp groups of rp rows at once, the same groups for all its rows, so that a
 // thread's sums of dw and db are over one set of columns. One pass over the data,
-// bound by DRAM: measured 74 us forward (floor 59) and 140 backward (floor 99) for
+// bound by DRAM: measured 75 us forward (floor 59) and 145 backward (floor 99) for
 // 65536 rows x 8 groups of 128, bf16, gated; 23 and 41 us (floors 10 and 15) for
 // 16384 rows of one group of 1024, where the two sums of a row that eight warps
 // share are waited for. Four CTAs an SM forward, with few spills, against one with
