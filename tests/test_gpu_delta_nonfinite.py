@@ -69,8 +69,11 @@ def test_decays_that_end_in_zero(dtype):
     reset = marks((1, 64), 20)
     ref = run(p, reset)
     got = run(dict(p, state=torch.full_like(p["state"], float("inf"))), reset)
-    assert not torch.isfinite(got[0][:, :20]).any()
-    assert torch.equal(got[0][:, 20:], ref[0][:, 20:]) and torch.equal(got[1], ref[1])
+    got, ref = dict(zip(NAMES, got)), dict(zip(NAMES, ref))
+    for name in ("o", "dq", "dk", "dg", "dbeta"):
+        assert not torch.isfinite(got[name][:, :20]).any(), name
+        assert torch.equal(got[name][:, 20:], ref[name][:, 20:]), name
+    assert torch.equal(got["last"], ref["last"])
 
 
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
